@@ -322,6 +322,125 @@ int spec_verify_get_plan_greedy(sv_ctx* ctx, int B, int K, int64_t V, int logits
 int spec_verify_plan_greedy_for(int num_sms, int max_cluster, int B, int K, int64_t V,
                                 int logits_dtype, int ovr_cluster, sv_plan* out);
 
+/* Settings of the sampling calls, for rows [B, rows_per_seq].  For a row l of V
+ * logits at temperature T > 0, w_v = exp((l_v - max l)/T) and S = sum w; v is
+ * kept when l_v > -inf and
+ *   top_k: fewer than top_k entries are larger than l_v (<= 0 turns it off);
+ *   top_p: the mass of the entries larger than l_v is below top_p * S (>= 1: off);
+ *   min_p: w_v >= min_p (<= 0: off).
+ * Every filter looks at the untruncated row and keeps or drops equal logits
+ * together, as spec_verify_run_truncated does, so their order does not matter.
+ * T = 0 is the greedy limit: the lowest token id among the largest logits is
+ * kept and nothing else, whatever the filters.
+ * Each setting is a number for the whole call or, where its pointer is not
+ * NULL, a device array [B] with one value per sequence; a sequence whose value
+ * is out of range (T negative, denormal, infinite or NaN; top_p <= 0 or NaN;
+ * min_p >= 1 or NaN) gets SV_ERR_INVALID_ARG in its rows' status. */
+typedef struct {
+    float temperature;
+    int32_t top_k;
+    double top_p;
+    double min_p;
+    const float* temperatures;
+    const int32_t* top_ks;
+    const float* top_ps;
+    const float* min_ps;
+} sv_sampling;
+
+/* Draws one token per row ([P1] "Speculative decoding: draft first, then
+ * verify": the drafter samples each draft token from its own softmax at its
+ * temperature; [P2] "Two things that follow from the math" names the sampler
+ * settings), and optionally writes the distribution it drew from, in the form
+ * the verify takes as q.
+ *
+ *   logits    R = B * rows_per_seq rows of V (dtype logits_dtype), row r at
+ *             r * logits_stride; row r belongs to sequence r / rows_per_seq
+ *   uniforms  float in [0, 1), row r's at r * uniforms_stride
+ *   tokens    out int32, row r's at r * tokens_stride
+ *   probs     optional out float, row r at r * probs_stride: w_v / E on the
+ *             kept entries (E their sum), 0 elsewhere
+ *   p_token   optional out float [R]: the drawn token's entry of probs
+ *   kept      optional out int32 [R]: entries kept
+ *   status    optional out int32 [R]
+ * Strides count elements, so a step of a draft loop can write position i of
+ * draft_tokens [B, K] (stride K) and q [B, K, V] (stride K * V) in place.
+ *
+ * The draw: the kept entries by descending logit and ascending id, the first
+ * whose running sum exceeds u * E.  (The verify's draws run by ascending id
+ * alone: the same law, another token for the same uniform.)  Weights are
+ * integers, good to 2^-39 of themselves and 2^-44 of the largest (for V up to
+ * 2^19; a bit less for each doubling beyond), so a draw or a cut does not depend
+ * on the order of any sum, and repeated calls give the same bits.
+ *
+ * An erroneous row (a bad setting; a uniform outside [0, 1): SV_ERR_UNIFORM_RANGE;
+ * a NaN or +inf, or only -inf: SV_ERR_NONFINITE) gets token -1, kept 0, NaN
+ * p_token and probs, so that a verify that reads its probs reports it too, and sets
+ * the context's error word.
+ * Asynchronous, no allocation, one launch on `stream`; safe to capture.
+ * Returns SV_OK, SV_ERR_INVALID_ARG (null or misaligned pointers, B or
+ * rows_per_seq - 1 or V beyond the context's limits, a stride below its row,
+ * R * logits_stride >= 2^40, a setting out of range), SV_ERR_UNSUPPORTED or
+ * SV_ERR_CUDA. */
+int spec_sample_run(sv_ctx* ctx, const void* logits, int logits_dtype, int64_t logits_stride,
+                    const float* uniforms, int64_t uniforms_stride, int B, int rows_per_seq,
+                    int64_t V, const sv_sampling* settings, int32_t* tokens, int64_t tokens_stride,
+                    float* probs, int64_t probs_stride, float* p_token, int32_t* kept,
+                    int32_t* status, void* stream);
+
+/* Truncates logits: out_logits holds l_v where v is kept under the settings and
+ * -inf elsewhere, so that softmax(out/T) is the truncated distribution and any
+ * verify entry that is then given out_logits verifies against it -- under
+ * top-k as well, per-sequence settings included (the verify itself must be
+ * called at the same temperature).
+ *
+ *   out_logits  R rows of V in the input's dtype, row r at r * out_stride; the
+ *               input itself (in place, same stride) or memory apart from it
+ *   kept        optional out int32 [R]: entries kept
+ *   mass        optional out float [R]: their share of the row, E / S
+ *   status      optional out int32 [R]
+ * An erroneous row is copied as it is (the verify that reads it reports it),
+ * with kept 0, mass NaN and its status.  Everything else as spec_sample_run. */
+int spec_filter_run(sv_ctx* ctx, const void* logits, int logits_dtype, int64_t logits_stride,
+                    int B, int rows_per_seq, int64_t V, const sv_sampling* settings,
+                    void* out_logits, int64_t out_stride, int32_t* kept, float* mass,
+                    int32_t* status, void* stream);
+
+/* The launch plan of the two calls above on the context's device, and their
+ * planner as a pure host function (no CUDA call): one cluster per row, the
+ * largest whose CTAs (two of 512 threads per SM) hold every row at once. */
+int spec_sample_get_plan(sv_ctx* ctx, int B, int rows_per_seq, int64_t V, int logits_dtype,
+                         sv_plan* out);
+int spec_sample_plan_for(int num_sms, int max_cluster, int B, int rows_per_seq, int64_t V,
+                         int logits_dtype, int ovr_cluster, sv_plan* out);
+
+/* Log-probabilities of the tokens a verify emitted.  For row i < accept_len[b]
+ * of sequence b and its token x = tokens[b, i]:
+ *   logprob [B, rows]          (l_x - max l)/T - ln sum_v exp((l_v - max l)/T)
+ *   rank    [B, rows] optional 1 + the number of entries larger than l_x
+ *   top_logprobs, top_tokens [B, rows, top_n] (0 <= top_n <= 32; not needed for
+ *           0): the top_n largest entries above -inf by descending logit and
+ *           ascending id; NaN and -1 behind the last
+ *   status  [B, rows] optional
+ * target_logits: row (b, i) at (b * rows_per_seq + i) * logits_stride; tokens
+ * [B, rows_per_seq] and accept_len [B] are the verify's outputs (out_tokens,
+ * accept_len; NULL: every row).  Rows from accept_len on are not read; their
+ * logprob is NaN, their rank 0.  The same goes for an erroneous row (a
+ * token outside [0, V): SV_ERR_TOKEN_RANGE; a NaN or +inf, or only -inf:
+ * SV_ERR_NONFINITE), which also sets the context's error word.
+ * T is positive, normal and finite.  Asynchronous, no allocation, one launch on
+ * `stream`; safe to capture.  Returns as spec_sample_run. */
+int spec_logprobs_run(sv_ctx* ctx, const void* target_logits, int logits_dtype,
+                      int64_t logits_stride, const int32_t* tokens, const int32_t* accept_len,
+                      int B, int rows_per_seq, int64_t V, float temperature, int top_n,
+                      float* logprob, int32_t* rank, float* top_logprobs, int32_t* top_tokens,
+                      int32_t* status, void* stream);
+
+/* Its launch plan, and its planner as a pure host function. */
+int spec_logprobs_get_plan(sv_ctx* ctx, int B, int rows_per_seq, int64_t V, int logits_dtype,
+                           sv_plan* out);
+int spec_logprobs_plan_for(int num_sms, int max_cluster, int B, int rows_per_seq, int64_t V,
+                           int logits_dtype, int ovr_cluster, sv_plan* out);
+
 /* Acceptance telemetry ([P1] "Production perspective": ship the acceptance
  * rate and the mean accepted length; its operational checklist: record
  * acceptance histograms).  With `accept_hist` set, every later verify on this

@@ -37,6 +37,13 @@ class sv_plan(ctypes.Structure):
         return {f: getattr(self, f) for f, _ in self._fields_}
 
 
+class sv_sampling(ctypes.Structure):
+    _fields_ = [("temperature", ctypes.c_float), ("top_k", ctypes.c_int32),
+                ("top_p", ctypes.c_double), ("min_p", ctypes.c_double),
+                ("temperatures", ctypes.c_void_p), ("top_ks", ctypes.c_void_p),
+                ("top_ps", ctypes.c_void_p), ("min_ps", ctypes.c_void_p)]
+
+
 class sv_adapt(ctypes.Structure):
     _fields_ = [("sequences", ctypes.c_uint64), ("errors", ctypes.c_uint64),
                 ("tested", ctypes.c_uint64), ("accepted", ctypes.c_uint64),
@@ -122,6 +129,25 @@ def library() -> ctypes.CDLL:
                                                            ctypes.c_int, ctypes.c_int,
                                                            ctypes.c_int64, ctypes.c_int,
                                                            ctypes.c_int, ctypes.POINTER(sv_plan)]),
+            "spec_sample_run": (ctypes.c_int, [P, P, ctypes.c_int, ctypes.c_int64, P,
+                                               ctypes.c_int64, ctypes.c_int, ctypes.c_int,
+                                               ctypes.c_int64, ctypes.POINTER(sv_sampling), P,
+                                               ctypes.c_int64, P, ctypes.c_int64, P, P, P, P]),
+            "spec_filter_run": (ctypes.c_int, [P, P, ctypes.c_int, ctypes.c_int64, ctypes.c_int,
+                                               ctypes.c_int, ctypes.c_int64,
+                                               ctypes.POINTER(sv_sampling), P, ctypes.c_int64, P,
+                                               P, P, P]),
+            "spec_logprobs_run": (ctypes.c_int, [P, P, ctypes.c_int, ctypes.c_int64, P, P,
+                                                 ctypes.c_int, ctypes.c_int, ctypes.c_int64,
+                                                 ctypes.c_float, ctypes.c_int, P, P, P, P, P, P]),
+            **{f"spec_{op}_get_plan": (ctypes.c_int, [P, ctypes.c_int, ctypes.c_int,
+                                                      ctypes.c_int64, ctypes.c_int,
+                                                      ctypes.POINTER(sv_plan)])
+               for op in ("sample", "logprobs")},
+            **{f"spec_{op}_plan_for": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                                      ctypes.c_int, ctypes.c_int64, ctypes.c_int,
+                                                      ctypes.c_int, ctypes.POINTER(sv_plan)])
+               for op in ("sample", "logprobs")},
             "spec_verify_set_telemetry": (ctypes.c_int, [P, P, ctypes.c_int]),
             "spec_verify_selftest_wait": (ctypes.c_int, [ctypes.c_int, ctypes.c_ulonglong,
                                                          ctypes.c_int,
@@ -288,6 +314,63 @@ def spec_verify_selftest_wait(device: int, limit_ns: int, arrive: bool):
     return rc, done.value, el.value
 
 
+def spec_sample_run(ctx, logits_ptr, dtype, logits_stride, uniforms_ptr, uniforms_stride, B,
+                    rows_per_seq, V, settings: sv_sampling, tokens_ptr, tokens_stride,
+                    probs_ptr=None, probs_stride=0, p_token_ptr=None, kept_ptr=None,
+                    status_ptr=None, stream=None) -> int:
+    return library().spec_sample_run(ctx, logits_ptr, dtype, logits_stride, uniforms_ptr,
+                                     uniforms_stride, B, rows_per_seq, V, settings, tokens_ptr,
+                                     tokens_stride, probs_ptr, probs_stride, p_token_ptr, kept_ptr,
+                                     status_ptr, stream)
+
+
+def spec_filter_run(ctx, logits_ptr, dtype, logits_stride, B, rows_per_seq, V,
+                    settings: sv_sampling, out_ptr, out_stride, kept_ptr=None, mass_ptr=None,
+                    status_ptr=None, stream=None) -> int:
+    return library().spec_filter_run(ctx, logits_ptr, dtype, logits_stride, B, rows_per_seq, V,
+                                     settings, out_ptr, out_stride, kept_ptr, mass_ptr, status_ptr,
+                                     stream)
+
+
+def spec_logprobs_run(ctx, logits_ptr, dtype, logits_stride, tokens_ptr, accept_len_ptr, B,
+                      rows_per_seq, V, T, top_n, logprob_ptr, rank_ptr=None, top_logprobs_ptr=None,
+                      top_tokens_ptr=None, status_ptr=None, stream=None) -> int:
+    return library().spec_logprobs_run(ctx, logits_ptr, dtype, logits_stride, tokens_ptr,
+                                       accept_len_ptr, B, rows_per_seq, V, float(T), int(top_n),
+                                       logprob_ptr, rank_ptr, top_logprobs_ptr, top_tokens_ptr,
+                                       status_ptr, stream)
+
+
+def spec_sample_get_plan(ctx, B, rows_per_seq, V, dtype) -> dict:
+    plan = sv_plan()
+    rc = library().spec_sample_get_plan(ctx, B, rows_per_seq, V, dtype, ctypes.byref(plan))
+    if rc != SV_OK:
+        raise SpecVerifyError(rc, "spec_sample_get_plan")
+    return plan.as_dict()
+
+
+def spec_sample_plan_for(num_sms, max_cluster, B, rows_per_seq, V, dtype, ovr_cluster=0):
+    plan = sv_plan()
+    rc = library().spec_sample_plan_for(num_sms, max_cluster, B, rows_per_seq, V, dtype,
+                                        ovr_cluster, ctypes.byref(plan))
+    return rc, plan.as_dict()
+
+
+def spec_logprobs_get_plan(ctx, B, rows_per_seq, V, dtype) -> dict:
+    plan = sv_plan()
+    rc = library().spec_logprobs_get_plan(ctx, B, rows_per_seq, V, dtype, ctypes.byref(plan))
+    if rc != SV_OK:
+        raise SpecVerifyError(rc, "spec_logprobs_get_plan")
+    return plan.as_dict()
+
+
+def spec_logprobs_plan_for(num_sms, max_cluster, B, rows_per_seq, V, dtype, ovr_cluster=0):
+    plan = sv_plan()
+    rc = library().spec_logprobs_plan_for(num_sms, max_cluster, B, rows_per_seq, V, dtype,
+                                          ovr_cluster, ctypes.byref(plan))
+    return rc, plan.as_dict()
+
+
 def spec_verify_set_telemetry(ctx, hist_ptr, bins) -> int:
     return library().spec_verify_set_telemetry(ctx, hist_ptr, int(bins))
 
@@ -340,6 +423,21 @@ def _dtype_code(t) -> int:
     if t.dtype == torch.bfloat16:
         return SV_BF16
     raise TypeError(f"logits must be float32 or bfloat16, got {t.dtype}")
+
+
+def _row_stride(t, name: str, rows: int, inner: int) -> int:
+    """Elements from one row of ``t`` to the next, its rows taken in order.
+    ``t`` is [B, ...] or [B, rows, ...] with ``inner`` (0: none) contiguous
+    entries per row; rows must be evenly spaced."""
+    B = t.shape[0]
+    three = t.dim() == (3 if inner else 2)
+    if inner > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    if rows == 1 or not three:
+        return t.stride(0) if B > 1 else max(inner, 1)
+    if B > 1 and t.stride(0) != rows * t.stride(1):
+        raise ValueError(f"{name}: rows must be evenly spaced in memory")
+    return t.stride(1)
 
 
 class Verifier:
@@ -581,6 +679,168 @@ class Verifier:
         if rc != SV_OK:
             raise SpecVerifyError(rc, "spec_verify_run_draft_logits")
         return out
+
+    def _rows_of(self, logits):
+        """(B, rows per sequence, V, dtype code, row stride) of logits [B, V] or [B, rows, V]."""
+        code = _dtype_code(logits)
+        if logits.dim() not in (2, 3):
+            raise ValueError("logits must be [B, V] or [B, rows, V]")
+        self._on_device(logits, "logits")
+        B, V = logits.shape[0], logits.shape[-1]
+        rows = logits.shape[1] if logits.dim() == 3 else 1
+        return B, rows, V, code, _row_stride(logits, "logits", rows, V)
+
+    def _on_device(self, t, name):
+        if not t.is_cuda or t.device.index != self.device:
+            raise ValueError(f"{name} must be a tensor on CUDA device {self.device}")
+
+    def _expect(self, t, name, shape, dtype):
+        """An input or output of a fixed shape and type."""
+        if t.dtype != dtype or t.shape != shape:
+            raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} of "
+                             f"shape {tuple(t.shape)}")
+        self._on_device(t, name)
+        return t
+
+    def _dense(self, t, name, shape, dtype):
+        if not self._expect(t, name, shape, dtype).is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return t.data_ptr()
+
+    def _settings(self, temperature, top_k, top_p, min_p, B) -> sv_sampling:
+        import torch
+        s = sv_sampling()
+        if torch.is_tensor(temperature):
+            s.temperatures = self._dense(temperature, "temperature", (B,), torch.float32)
+        else:
+            s.temperature = temperature
+        if torch.is_tensor(top_k):
+            s.top_ks = self._dense(top_k, "top_k", (B,), torch.int32)
+        else:
+            s.top_k = min(max(int(top_k), 0), 0x7fffffff)
+        if torch.is_tensor(top_p):
+            s.top_ps = self._dense(top_p, "top_p", (B,), torch.float32)
+        else:
+            s.top_p = top_p
+        if torch.is_tensor(min_p):
+            s.min_ps = self._dense(min_p, "min_p", (B,), torch.float32)
+        else:
+            s.min_p = min_p
+        return s
+
+    def sample(self, logits, uniforms, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0,
+               out: Optional[dict] = None, probs: bool = False, status: bool = True,
+               stream=None) -> dict:
+        """Draws one token per row of logits [B, V] or [B, rows, V] (float32 or
+        bfloat16; rows evenly spaced) from uniforms of logits' shape without V.
+        The settings are numbers, or CUDA tensors [B] (float32; top_k int32) with
+        one value per sequence; temperature 0 is greedy.  Returns tokens (int32),
+        p_token, kept, and optionally probs (the distribution drawn from, as the
+        verify's q) and status.  ``out``: the tensors to write instead, tokens
+        and probs with strides of their own (draft_tokens[:, i], q[:, i])."""
+        import torch
+        B, rows, V, code, stride = self._rows_of(logits)
+        shape = logits.shape[:-1]
+        settings = self._settings(temperature, top_k, top_p, min_p, B)
+        self._expect(uniforms, "uniforms", shape, torch.float32)
+        if out is None:
+            dev = logits.device
+            out = {"tokens": torch.empty(shape, dtype=torch.int32, device=dev),
+                   "p_token": torch.empty(shape, dtype=torch.float32, device=dev),
+                   "kept": torch.empty(shape, dtype=torch.int32, device=dev)}
+            if probs:
+                out["probs"] = torch.empty(logits.shape, dtype=torch.float32, device=dev)
+            if status:
+                out["status"] = torch.empty(shape, dtype=torch.int32, device=dev)
+        tokens = self._expect(out["tokens"], "tokens", shape, torch.int32)
+        q, p_token, kept, st = (out.get(k) for k in ("probs", "p_token", "kept", "status"))
+        rc = spec_sample_run(
+            self.ctx, logits.data_ptr(), code, stride, uniforms.data_ptr(),
+            _row_stride(uniforms, "uniforms", rows, 0), B, rows, V, settings, tokens.data_ptr(),
+            _row_stride(tokens, "tokens", rows, 0),
+            None if q is None else self._expect(q, "probs", logits.shape, torch.float32).data_ptr(),
+            0 if q is None else _row_stride(q, "probs", rows, V),
+            None if p_token is None else self._dense(p_token, "p_token", shape, torch.float32),
+            None if kept is None else self._dense(kept, "kept", shape, torch.int32),
+            None if st is None else self._dense(st, "status", shape, torch.int32),
+            stream if stream is not None else torch.cuda.current_stream(self.device).cuda_stream)
+        if rc != SV_OK:
+            raise SpecVerifyError(rc, "spec_sample_run")
+        return out
+
+    def filter_logits(self, logits, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0,
+                      out: Optional[dict] = None, status: bool = True, stream=None) -> dict:
+        """Truncates logits [B, V] or [B, rows, V]: kept entries as they are, the
+        others -inf, under settings as in ``sample``.  Returns logits, kept, mass
+        (the kept share of the row) and optionally status; with
+        ``out={"logits": logits, ...}`` in place.  The truncated rows are what any
+        of the verify calls may be given."""
+        import torch
+        B, rows, V, code, stride = self._rows_of(logits)
+        shape = logits.shape[:-1]
+        settings = self._settings(temperature, top_k, top_p, min_p, B)
+        if out is None:
+            dev = logits.device
+            out = {"logits": torch.empty(logits.shape, dtype=logits.dtype, device=dev),
+                   "kept": torch.empty(shape, dtype=torch.int32, device=dev),
+                   "mass": torch.empty(shape, dtype=torch.float32, device=dev)}
+            if status:
+                out["status"] = torch.empty(shape, dtype=torch.int32, device=dev)
+        o = self._expect(out["logits"], "out logits", logits.shape, logits.dtype)
+        kept, mass, st = (out.get(k) for k in ("kept", "mass", "status"))
+        rc = spec_filter_run(
+            self.ctx, logits.data_ptr(), code, stride, B, rows, V, settings, o.data_ptr(),
+            _row_stride(o, "out logits", rows, V),
+            None if kept is None else self._dense(kept, "kept", shape, torch.int32),
+            None if mass is None else self._dense(mass, "mass", shape, torch.float32),
+            None if st is None else self._dense(st, "status", shape, torch.int32),
+            stream if stream is not None else torch.cuda.current_stream(self.device).cuda_stream)
+        if rc != SV_OK:
+            raise SpecVerifyError(rc, "spec_filter_run")
+        return out
+
+    def logprobs(self, logits, tokens, accept_len=None, temperature: float = 1.0, top_n: int = 0,
+                 out: Optional[dict] = None, status: bool = True, stream=None) -> dict:
+        """Log-probabilities of the tokens [B, rows] (int32) a verify emitted from
+        logits [B, rows, V] (or [B] and [B, V]); rows from accept_len[b] on are
+        not read (None: every row).  Returns logprob, rank, and for top_n > 0
+        top_logprobs and top_tokens [B, rows, top_n], and optionally status."""
+        import torch
+        B, rows, V, code, stride = self._rows_of(logits)
+        shape = logits.shape[:-1]
+        if out is None:
+            dev = logits.device
+            out = {"logprob": torch.empty(shape, dtype=torch.float32, device=dev),
+                   "rank": torch.empty(shape, dtype=torch.int32, device=dev)}
+            if top_n > 0:
+                out["top_logprobs"] = torch.empty((*shape, top_n), dtype=torch.float32, device=dev)
+                out["top_tokens"] = torch.empty((*shape, top_n), dtype=torch.int32, device=dev)
+            if status:
+                out["status"] = torch.empty(shape, dtype=torch.int32, device=dev)
+        rank, st = out.get("rank"), out.get("status")
+        top = top_n > 0
+        rc = spec_logprobs_run(
+            self.ctx, logits.data_ptr(), code, stride,
+            self._dense(tokens, "tokens", shape, torch.int32),
+            None if accept_len is None else self._dense(accept_len, "accept_len", (B,), torch.int32),
+            B, rows, V, temperature, top_n,
+            self._dense(out["logprob"], "logprob", shape, torch.float32),
+            None if rank is None else self._dense(rank, "rank", shape, torch.int32),
+            self._dense(out["top_logprobs"], "top_logprobs", (*shape, top_n), torch.float32)
+            if top else None,
+            self._dense(out["top_tokens"], "top_tokens", (*shape, top_n), torch.int32)
+            if top else None,
+            None if st is None else self._dense(st, "status", shape, torch.int32),
+            stream if stream is not None else torch.cuda.current_stream(self.device).cuda_stream)
+        if rc != SV_OK:
+            raise SpecVerifyError(rc, "spec_logprobs_run")
+        return out
+
+    def plan_sample(self, B, rows_per_seq, V, dtype=SV_BF16) -> dict:
+        return spec_sample_get_plan(self.ctx, B, rows_per_seq, V, dtype)
+
+    def plan_logprobs(self, B, rows_per_seq, V, dtype=SV_BF16) -> dict:
+        return spec_logprobs_get_plan(self.ctx, B, rows_per_seq, V, dtype)
 
     def plan_draft_logits(self, B, K, V, dtype=SV_BF16, filters=0) -> dict:
         return spec_verify_get_plan_draft_logits(self.ctx, B, K, V, dtype, filters)

@@ -1,0 +1,399 @@
+// logprobs.cu -- log-probabilities of the tokens a verify emitted, their
+// ranks, and the largest entries of their rows.
+//
+// For a row l reached by the verify and its token x:
+//   logprob = (l_x - l_max)/T - ln sum exp((l - l_max)/T)
+//   rank    = 1 + #{l > l_x}
+//   top n   = the n largest entries by descending logit and ascending id
+//
+// Design: one cluster of C CTAs per row, a slice of the vocabulary per CTA;
+// rows from accept_len on are not read.  One pass takes the maximum, the sum
+// (rescaled when a thread's maximum grows), the count above l_x, and every
+// thread's largest entry.  The n-th largest of a CTA's thread maxima bounds
+// its n-th largest entry from below: only threads whose maximum reaches that
+// bound look at their entries again, and hand those that do to a short list.
+// Each CTA sends its n best to the first one, which orders them.
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "../../include/spec_verify.h"
+#include "sampling_common.cuh"
+#include "sv_context.h"
+
+namespace cg = cooperative_groups;
+
+namespace {
+
+using namespace sv;
+
+constexpr int kNT = 256;
+constexpr int kNW = kNT / 32;
+constexpr int kMaxC = 16;
+constexpr int kMaxTop = 32;
+constexpr int kList = 1024;
+
+struct Args {
+    const void* logits;
+    int64_t stride;
+    const int32_t* tokens;
+    const int32_t* accept_len;  // or NULL: every row
+    float* logprob;
+    int32_t* rank;
+    float* top_logprobs;
+    int32_t* top_tokens;
+    int32_t* status;
+    uint32_t* err_word;
+    int64_t V, slice;
+    int rows_per_seq, C, vec, top_n;
+    float T, ch, cl;
+};
+
+struct Shared {
+    unsigned long long list[kList];         // key << 32 | ~id
+    unsigned long long best[kMaxC][kMaxTop];  // first CTA: every CTA's n best, 0 behind the last
+    float part_max[kMaxC], part_sum[kMaxC];
+    uint32_t part_above[kMaxC];
+    float warp_max[kNW], warp_sum[kNW];
+    uint32_t warp_above[kNW];
+    uint32_t list_n;
+    unsigned long long warp_best[kNW];
+};
+
+__device__ __forceinline__ unsigned long long order_of(float l, int64_t id) {
+    return ((unsigned long long)logit_key(l) << 32) | (uint32_t)~(uint32_t)id;
+}
+
+template <int ES>
+__global__ void __launch_bounds__(kNT, 4) sv_logprobs_kernel(const __grid_constant__ Args a) {
+    __shared__ Shared sh;
+    cg::cluster_group cluster = cg::this_cluster();
+    constexpr int E = 16 / ES, D = 4;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int C = a.C, rank = (int)cluster.block_rank(), n = a.top_n;
+    const int64_t row = blockIdx.x / C, seq = row / a.rows_per_seq;
+    const float inf = __int_as_float(0x7f800000), nan = __int_as_float(0x7fffffff);
+
+    const auto leave = [&](int code) {  // a row with no answer
+        if (rank == 0) {
+            if (tid == 0) {
+                a.logprob[row] = nan;
+                if (a.rank)
+                    a.rank[row] = 0;
+                if (a.status)
+                    a.status[row] = code;
+                if (code)
+                    atomicOr(a.err_word, 1u << code);
+            }
+            if (tid < n) {
+                a.top_logprobs[row * n + tid] = nan;
+                a.top_tokens[row * n + tid] = -1;
+            }
+        }
+    };
+    if (a.accept_len && row - seq * a.rows_per_seq >= a.accept_len[seq]) {
+        leave(SV_OK);
+        return;
+    }
+    const int32_t x = a.tokens[row];
+    if (x < 0 || x >= a.V) {
+        leave(SV_ERR_TOKEN_RANGE);
+        return;
+    }
+    const unsigned char* base = static_cast<const unsigned char*>(a.logits) + row * a.stride * ES;
+    const float lx = scalar_entry<ES>(base, x);
+    const int64_t s0 = rank * a.slice < a.V ? rank * a.slice : a.V;
+    const int64_t s1 = s0 + a.slice < a.V ? s0 + a.slice : a.V;
+    const int64_t v1 = a.vec ? s1 / E : 0, tail = a.vec ? v1 * E : s0;
+    const uint4* vp = reinterpret_cast<const uint4*>(base);
+
+    cluster.barrier_arrive();
+
+    // the pass over the slice
+    float m = -inf, s = 0.0f;
+    uint32_t above = 0;
+    const auto take = [&](float l) {
+        above += l > lx;
+        if (!(l <= m)) {  // a new maximum, or a NaN, which stays
+            const float grown = max_nan(m, l);
+            s = m > -inf ? s * ex2_approx((m - grown) * a.ch) : 0.0f;
+            m = grown;
+        }
+        if (l > -inf)
+            s += ex2_approx((l - m) * a.ch);
+    };
+    if (a.vec)
+        for (int64_t v = s0 / E + tid; v < v1; v += D * kNT) {
+            uint4 w[D];
+#pragma unroll
+            for (int k = 0; k < D; ++k)
+                if (v + k * kNT < v1)
+                    w[k] = load_stream(vp + v + k * kNT);
+#pragma unroll
+            for (int k = 0; k < D; ++k)
+                if (v + k * kNT < v1) {
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        take(vector_entry<ES>(w[k], e));
+                }
+        }
+    for (int64_t i = tail + tid; i < s1; i += kNT)
+        take(scalar_entry<ES>(base, i));
+    const float mine = m;
+
+    // join the threads, then the CTAs
+    const auto merge = [&](float& m0, float& s0_, float m1, float s1_) {
+        const float mm = max_nan(m0, m1);
+        s0_ = (m0 > -inf ? s0_ * ex2_approx((m0 - mm) * a.ch) : 0.0f) +
+              (m1 > -inf ? s1_ * ex2_approx((m1 - mm) * a.ch) : 0.0f);
+        m0 = mm;
+    };
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        const float m1 = __shfl_xor_sync(kAllLanes, m, o), s1_ = __shfl_xor_sync(kAllLanes, s, o);
+        merge(m, s, m1, s1_);
+    }
+    above = __reduce_add_sync(kAllLanes, above);
+    if (lane == 0) {
+        sh.warp_max[warp] = m;
+        sh.warp_sum[warp] = s;
+        sh.warp_above[warp] = above;
+    }
+    if (tid == 0)
+        sh.list_n = 0;
+    __syncthreads();
+    cluster.barrier_wait();  // every CTA of the cluster runs: its memory may be written
+    if (tid == 0) {
+        for (int w = 1; w < kNW; ++w) {
+            merge(m, s, sh.warp_max[w], sh.warp_sum[w]);
+            above += sh.warp_above[w];
+        }
+        *cluster.map_shared_rank(&sh.part_max[rank], 0) = m;
+        *cluster.map_shared_rank(&sh.part_sum[rank], 0) = s;
+        *cluster.map_shared_rank(&sh.part_above[rank], 0) = above;
+    }
+
+    // the CTA's n largest
+    if (n) {
+        // bound: the largest key that n threads' maxima reach (bf16: its upper half says all)
+        const uint32_t key = logit_key(mine);
+        uint32_t bound = 0;
+        for (int bit = 31; bit >= (ES == 2 ? 16 : 0); --bit) {
+            const uint32_t t = bound | (1u << bit);
+            if (__syncthreads_count(key >= t) >= n)
+                bound = t;
+        }
+        if (bound <= kKeyMinusInf)
+            bound = kKeyMinusInf + 1;
+        if (key >= bound) {
+            const auto offer = [&](float l, int64_t id) {
+                if (logit_key(l) >= bound) {
+                    const uint32_t at = atomicAdd(&sh.list_n, 1u);
+                    if (at < (uint32_t)kList)
+                        sh.list[at] = order_of(l, id);
+                }
+            };
+            if (a.vec)
+                for (int64_t v = s0 / E + tid; v < v1; v += D * kNT) {
+                    uint4 w[D];
+#pragma unroll
+                    for (int k = 0; k < D; ++k)
+                        if (v + k * kNT < v1)
+                            w[k] = load_stream(vp + v + k * kNT);
+#pragma unroll
+                    for (int k = 0; k < D; ++k)
+                        if (v + k * kNT < v1) {
+#pragma unroll
+                            for (int e = 0; e < E; ++e)
+                                offer(vector_entry<ES>(w[k], e), (v + k * kNT) * E + e);
+                        }
+                }
+            for (int64_t i = tail + tid; i < s1; i += kNT)
+                offer(scalar_entry<ES>(base, i), i);
+        }
+        __syncthreads();
+        const uint32_t got = sh.list_n;
+        unsigned long long* best = cluster.map_shared_rank(sh.best[rank], 0);
+        if (got <= (uint32_t)kList) {
+            // an entry's place is the number of entries before it
+            for (uint32_t i = tid; i < got; i += kNT) {
+                const unsigned long long o = sh.list[i];
+                int place = 0;
+                for (uint32_t j = 0; j < got && place < n; ++j)
+                    place += sh.list[j] > o;
+                if (place < n)
+                    best[place] = o;
+            }
+            for (int i = (int)got + tid; i < n; i += kNT)
+                best[i] = 0;
+        } else {
+            // many equal logits at the bound: one entry after the other
+            unsigned long long last = ~0ull;
+            for (int r = 0; r < n; ++r) {
+                unsigned long long o = 0;
+                for (int64_t i = s0 + tid; i < s1; i += kNT) {
+                    const unsigned long long y = order_of(scalar_entry<ES>(base, i), i);
+                    if (y < last && y > o && (uint32_t)(y >> 32) > kKeyMinusInf)
+                        o = y;
+                }
+                for (int k = 16; k; k >>= 1) {
+                    const unsigned long long y = __shfl_xor_sync(kAllLanes, o, k);
+                    o = y > o ? y : o;
+                }
+                if (lane == 0)
+                    sh.warp_best[warp] = o;
+                __syncthreads();
+                for (int w = 0; w < kNW; ++w)
+                    o = sh.warp_best[w] > o ? sh.warp_best[w] : o;
+                if (tid == 0)
+                    best[r] = o;
+                last = o;
+                __syncthreads();
+            }
+        }
+    }
+    cluster.sync();
+    if (rank)
+        return;
+    m = sh.part_max[0];
+    s = sh.part_sum[0];
+    above = sh.part_above[0];
+    for (int r = 1; r < C; ++r) {
+        merge(m, s, sh.part_max[r], sh.part_sum[r]);
+        above += sh.part_above[r];
+    }
+    if (!(m > -inf && m < inf)) {
+        leave(SV_ERR_NONFINITE);
+        return;
+    }
+    const float ls = logf(s);
+    const auto value = [&](float l) {
+        const float d = l - m;
+        return fmaf(d, 1.0f / a.T, -ls);
+    };
+    if (tid == 0) {
+        a.logprob[row] = value(lx);
+        if (a.rank)
+            a.rank[row] = (int32_t)above + 1;
+        if (a.status)
+            a.status[row] = SV_OK;
+    }
+    // order the CTAs' best
+    int listed = 0;
+    for (int i0 = 0; i0 < C * n; i0 += kNT) {
+        const int i = i0 + tid;
+        const unsigned long long o = i < C * n ? sh.best[i / n][i % n] : 0;
+        listed += __syncthreads_count(o != 0);
+        if (!o)
+            continue;
+        int place = 0;
+        for (int r = 0; r < C; ++r)
+            for (int j = 0; j < n && sh.best[r][j] > o; ++j)
+                ++place;
+        if (place < n) {
+            a.top_logprobs[row * n + place] = value(key_logit((uint32_t)(o >> 32)));
+            a.top_tokens[row * n + place] = (int32_t)~(uint32_t)o;
+        }
+    }
+    if (tid >= listed && tid < n) {
+        a.top_logprobs[row * n + tid] = nan;
+        a.top_tokens[row * n + tid] = -1;
+    }
+}
+
+}  // namespace
+
+namespace sv {
+
+bool logprobs_setup() {
+    for (const void* fn : {(const void*)sv_logprobs_kernel<2>, (const void*)sv_logprobs_kernel<4>})
+        if (cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+            cudaSuccess) {
+            (void)cudaGetLastError();
+            return false;
+        }
+    return true;
+}
+
+}  // namespace sv
+
+extern "C" {
+
+int spec_logprobs_get_plan(sv_ctx* ctx, int B, int rows_per_seq, int64_t V, int logits_dtype,
+                           sv_plan* out) {
+    if (!ctx)
+        return SV_ERR_INVALID_ARG;
+    return spec_logprobs_plan_for(ctx->num_sms, ctx->sampling_max_cluster, B, rows_per_seq, V,
+                                  logits_dtype, ctx->ovr_cluster, out);
+}
+
+int spec_logprobs_run(sv_ctx* ctx, const void* target_logits, int logits_dtype,
+                      int64_t logits_stride, const int32_t* tokens, const int32_t* accept_len,
+                      int B, int rows_per_seq, int64_t V, float temperature, int top_n,
+                      float* logprob, int32_t* rank, float* top_logprobs, int32_t* top_tokens,
+                      int32_t* status, void* stream) {
+    if (!ctx || !target_logits || !tokens || !logprob ||
+        (logits_dtype != SV_F32 && logits_dtype != SV_BF16))
+        return SV_ERR_INVALID_ARG;
+    if (B < 1 || B > ctx->max_B || rows_per_seq < 1 || rows_per_seq > ctx->max_K + 1 || V < 1 ||
+        V > ctx->max_V || V > ((int64_t)1 << 31) || logits_stride < V ||
+        logits_stride > ((int64_t)1 << 40) ||
+        (double)B * (double)rows_per_seq * (double)logits_stride >= 1099511627776.0)  // 2^40
+        return SV_ERR_INVALID_ARG;
+    if (!(temperature >= 1.17549435e-38f) || !std::isfinite(temperature) || top_n < 0 ||
+        top_n > kMaxTop || (top_n && (!top_logprobs || !top_tokens)))
+        return SV_ERR_INVALID_ARG;
+    const int es = logits_dtype == SV_BF16 ? 2 : 4;
+    if (!aligned(target_logits, es) || !aligned(tokens, 4) || !aligned(accept_len, 4) ||
+        !aligned(logprob, 4) || !aligned(rank, 4) || !aligned(top_logprobs, 4) ||
+        !aligned(top_tokens, 4) || !aligned(status, 4))
+        return SV_ERR_INVALID_ARG;
+    sv_plan plan;
+    const int rc = spec_logprobs_get_plan(ctx, B, rows_per_seq, V, logits_dtype, &plan);
+    if (rc != SV_OK)
+        return rc;
+    Args a;
+    std::memset(&a, 0, sizeof a);
+    a.logits = target_logits;
+    a.stride = logits_stride;
+    a.tokens = tokens;
+    a.accept_len = accept_len;
+    a.logprob = logprob;
+    a.rank = rank;
+    a.top_logprobs = top_logprobs;
+    a.top_tokens = top_tokens;
+    a.status = status;
+    a.err_word = ctx->d_err;
+    a.V = V;
+    a.slice = plan.slice;
+    a.rows_per_seq = rows_per_seq;
+    a.C = plan.cluster;
+    a.vec = aligned(target_logits, 16) && (logits_stride * es) % 16 == 0 ? 1 : 0;
+    a.top_n = top_n;
+    a.T = temperature;
+    a.ch = (float)(1.4426950408889634074 / (double)temperature);
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof cfg);
+    cfg.gridDim = dim3((unsigned)plan.grid, 1, 1);
+    cfg.blockDim = dim3(kNT, 1, 1);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)plan.cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    DeviceGuard guard(ctx->device);
+    if (cudaLaunchKernelEx(&cfg, es == 2 ? sv_logprobs_kernel<2> : sv_logprobs_kernel<4>, a) !=
+        cudaSuccess) {
+        (void)cudaGetLastError();
+        return SV_ERR_CUDA;
+    }
+    return SV_OK;
+}
+
+}  // extern "C"

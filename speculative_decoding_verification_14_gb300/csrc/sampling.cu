@@ -1,0 +1,887 @@
+// sampling.cu -- drawing tokens, and truncating logits, under temperature,
+// top-k, top-p and min-p.
+//
+// For a row l of V logits and a temperature T > 0, w_v = exp((l_v - l_max)/T),
+// S = sum w.  Entry v is kept when l_v > -inf and
+//   top-k: fewer than k entries are larger than l_v;
+//   top-p: the mass of the entries larger than l_v is below top_p S;
+//   min-p: w_v >= min_p;
+// every filter looks at the untruncated row and keeps or drops equal logits
+// together, so the kept set is {l >= cut}.  With E the kept mass, the draw
+// lays the kept entries out by descending logit and ascending id and takes the
+// first whose running sum exceeds u E.  The kept set is a prefix of that
+// order, so the cut and the draw are one search: for the place where a count
+// or a mass is crossed.  T = 0 keeps the lowest id of the largest logits.
+//
+// Design: one cluster of C CTAs per row, a slice of the vocabulary per CTA.
+//  A. a pass for l_max;
+//  B. a pass that adds every entry's count and integer weight into 2048 bins
+//     over t = (l_max - l) c, 32 to the octave, in shared memory; the cluster
+//     adds its CTAs' bins up, each CTA a range of them, and finds the bin where
+//     the first filter ends (the cut) and then the one that u E falls into;
+//  C. the entries of such a bin go to a list in the first CTA, which sorts it
+//     and finds the exact place.  A bin with more entries than the list holds
+//     is split by the logits' keys, 2048 ways, until it fits or is one value.
+//  D. probabilities or truncated logits are written in a last pass.
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "../../include/spec_verify.h"
+#include "sampling_common.cuh"
+#include "sv_context.h"
+
+namespace cg = cooperative_groups;
+
+namespace {
+
+using namespace sv;
+
+constexpr int kNT = 512;
+constexpr int kNW = kNT / 32;
+constexpr int kBins = 2048;
+constexpr int kList = 1024;  // entries of the list (two per thread)
+constexpr int kMaxC = 16;
+constexpr float kBinsPerOctave = 32.0f;
+
+struct Args {
+    const void* logits;
+    int64_t stride;
+    const float* u;  // NULL: no draw
+    int64_t u_stride;
+    int32_t* tokens;
+    int64_t token_stride;
+    float* probs;  // or NULL
+    int64_t probs_stride;
+    float* p_token;
+    void* out;  // truncated logits, or NULL
+    int64_t out_stride;
+    float* mass;
+    int32_t* kept;
+    int32_t* status;
+    uint32_t* err_word;
+    sv_sampling set;
+    int64_t V, slice;
+    int rows_per_seq, C, fix;
+    int vec;      // rows may be read as 16-byte vectors
+    int out_vec;  // and the output written so
+};
+
+enum Cond { kByCount, kByMass, kByLimit, kConds };
+
+struct Found {
+    int bin;  // kBins: none
+    uint32_t count, above_count;
+    unsigned long long mass, above_mass;
+};
+
+struct Shared {
+    uint32_t lo[kBins], hi[kBins], cnt[kBins];
+    unsigned long long list[kList];  // key << 32 | ~id
+    float2 pow2[64];
+    unsigned long long part_mass[kMaxC];
+    uint32_t part_cnt[kMaxC];
+    uint32_t part_max[kMaxC];
+    uint32_t part_flag[kMaxC];
+    unsigned long long warp_mass[kNW];
+    uint32_t warp_cnt[kNW];
+    uint32_t warp_max[kNW];
+    Found found[kConds];
+    uint32_t list_n;
+    // what the first CTA (or the CTA that finds it) tells the others
+    uint32_t cut_key;
+    uint32_t kept;
+    unsigned long long kept_mass;
+    uint32_t token;
+    uint32_t token_key;
+};
+
+template <int ES>
+struct Kernel {
+    const Args& a;
+    cg::cluster_group cluster;
+    Shared& sh;
+    int tid, lane, warp, rank, C;
+    int64_t row;
+    const unsigned char* base;  // the row's first logit
+    int64_t s0, s1;             // this CTA's slice
+    RowScale scale;
+
+    __device__ Kernel(const Args& args, Shared& shared)
+        : a(args), cluster(cg::this_cluster()), sh(shared) {
+        tid = threadIdx.x;
+        lane = tid & 31;
+        warp = tid >> 5;
+        C = a.C;
+        rank = (int)cluster.block_rank();
+        row = blockIdx.x / C;
+        base = static_cast<const unsigned char*>(a.logits) + row * a.stride * ES;
+        s0 = rank * a.slice < a.V ? rank * a.slice : a.V;
+        s1 = s0 + a.slice < a.V ? s0 + a.slice : a.V;
+        scale.fix = a.fix;
+    }
+
+    // fn(l, id) for every entry of the slice
+    template <class F>
+    __device__ __forceinline__ void each(F&& fn) const {
+        constexpr int E = 16 / ES, D = 4;
+        int64_t i = s0;
+        if (a.vec) {
+            const int64_t v1 = s1 / E;
+            const uint4* p = reinterpret_cast<const uint4*>(base);
+            for (int64_t v = s0 / E + tid; v < v1; v += D * kNT) {
+                uint4 w[D];
+#pragma unroll
+                for (int k = 0; k < D; ++k)
+                    if (v + k * kNT < v1)
+                        w[k] = load_stream(p + v + k * kNT);
+#pragma unroll
+                for (int k = 0; k < D; ++k)
+                    if (v + k * kNT < v1) {
+#pragma unroll
+                        for (int e = 0; e < E; ++e)
+                            fn(vector_entry<ES>(w[k], e), (v + k * kNT) * E + e);
+                    }
+            }
+            i = v1 * E;
+        }
+        for (i += tid; i < s1; i += kNT)
+            fn(scalar_entry<ES>(base, i), i);
+    }
+
+    // the linear bin of a logit; larger logits, smaller bins
+    __device__ __forceinline__ int bin_of(float l) const {
+        const float t = (scale.lmax - l) * scale.ch * kBinsPerOctave;
+        return t < (float)(kBins - 1) ? (int)t : kBins - 1;
+    }
+
+    template <class Map>
+    __device__ void histogram(Map&& map) {
+        for (int b = tid; b < kBins; b += kNT)
+            sh.lo[b] = sh.hi[b] = sh.cnt[b] = 0;
+        if (tid < kConds)
+            sh.found[tid].bin = kBins;
+        if (tid == 0)
+            sh.list_n = 0;
+        __syncthreads();
+        each([&](float l, int64_t) {
+            const int b = map(l);
+            if (b < 0)
+                return;
+            const unsigned long long w = weight_fixed(scale, sh.pow2, l);
+            const uint32_t wl = (uint32_t)w;
+            const uint32_t old = atomicAdd(&sh.lo[b], wl);
+            const uint32_t h = (uint32_t)(w >> 32) + (old + wl < old);
+            if (h)
+                atomicAdd(&sh.hi[b], h);
+            atomicAdd(&sh.cnt[b], 1u);
+        });
+        cluster.sync();
+        // this CTA's range of the bins, added up over the cluster
+        const int per = (kBins + C - 1) / C, b0 = rank * per;
+        const int b1 = b0 + per < kBins ? b0 + per : kBins;
+        for (int b = b0 + tid; b < b1; b += kNT) {
+            unsigned long long m = 0;
+            uint32_t n = 0;
+            for (int r = 0; r < C; ++r) {
+                m += ((unsigned long long)cluster.map_shared_rank(sh.hi, r)[b] << 32) +
+                     cluster.map_shared_rank(sh.lo, r)[b];
+                n += cluster.map_shared_rank(sh.cnt, r)[b];
+            }
+            sh.lo[b] = (uint32_t)m;
+            sh.hi[b] = (uint32_t)(m >> 32);
+            sh.cnt[b] = n;
+        }
+        __syncthreads();
+    }
+
+    // exclusive prefixes over the CTA's threads of (mass, count); totals returned in m, n
+    __device__ void scan(unsigned long long& m, uint32_t& n, unsigned long long& before_m,
+                         uint32_t& before_n) {
+        unsigned long long im = m;
+        uint32_t in = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned long long pm = __shfl_up_sync(kAllLanes, im, o);
+            const uint32_t pn = __shfl_up_sync(kAllLanes, in, o);
+            if (lane >= o) {
+                im += pm;
+                in += pn;
+            }
+        }
+        __syncthreads();
+        if (lane == 31) {
+            sh.warp_mass[warp] = im;
+            sh.warp_cnt[warp] = in;
+        }
+        __syncthreads();
+        before_m = im - m;
+        before_n = in - n;
+        m = 0;
+        n = 0;
+        for (int w = 0; w < kNW; ++w) {
+            if (w < warp) {
+                before_m += sh.warp_mass[w];
+                before_n += sh.warp_cnt[w];
+            }
+            m += sh.warp_mass[w];
+            n += sh.warp_cnt[w];
+        }
+    }
+
+    struct Search {
+        unsigned long long above_mass;  // of the entries above the searched range
+        uint32_t above_count;
+        uint32_t k;            // count to reach, 0: none
+        double top_p;          // >= 1: none
+        unsigned long long p;  // mass to reach (from top_p when `whole`)
+        int limit_bin;         // bin of the min-p limit, kBins: none
+        bool draw;             // p is a mass to exceed: u E
+    };
+
+    // Finds, for each condition, the bin where it ends, in every CTA's `found`;
+    // returns the range's totals.
+    __device__ void search(Search& s, bool whole, unsigned long long& total, uint32_t& total_n) {
+        const int per = (kBins + C - 1) / C, b0 = rank * per;
+        const int b1 = b0 + per < kBins ? b0 + per : kBins;
+        const int q = (per + kNT - 1) / kNT;
+        const int t0 = b0 + tid * q, t1 = t0 + q < b1 ? t0 + q : b1;
+        unsigned long long m = 0, before_m;
+        uint32_t n = 0, before_n;
+        for (int b = t0; b < t1; ++b) {
+            m += ((unsigned long long)sh.hi[b] << 32) + sh.lo[b];
+            n += sh.cnt[b];
+        }
+        scan(m, n, before_m, before_n);
+        if (tid < C) {
+            *cluster.map_shared_rank(&sh.part_mass[rank], tid) = m;
+            *cluster.map_shared_rank(&sh.part_cnt[rank], tid) = n;
+        }
+        cluster.sync();
+        total = 0;
+        total_n = 0;
+        before_m += s.above_mass;
+        before_n += s.above_count;
+        for (int r = 0; r < C; ++r) {
+            if (r < rank) {
+                before_m += sh.part_mass[r];
+                before_n += sh.part_cnt[r];
+            }
+            total += sh.part_mass[r];
+            total_n += sh.part_cnt[r];
+        }
+        if (whole && s.top_p < 1.0)
+            s.p = ceil_scaled(s.top_p, total);
+        const bool by_mass = s.draw || s.top_p < 1.0;
+        for (int b = t0; b < t1; ++b) {
+            Found f;
+            f.bin = b;
+            f.count = sh.cnt[b];
+            f.mass = ((unsigned long long)sh.hi[b] << 32) + sh.lo[b];
+            f.above_count = before_n;
+            f.above_mass = before_m;
+            before_n += f.count;
+            before_m += f.mass;
+            if (s.k && f.above_count < s.k && before_n >= s.k)
+                tell(kByCount, f);
+            if (by_mass && (s.draw ? f.above_mass <= s.p && before_m > s.p
+                                   : f.above_mass < s.p && before_m >= s.p))
+                tell(kByMass, f);
+            if (b == s.limit_bin)
+                tell(kByLimit, f);
+        }
+        cluster.sync();
+    }
+
+    __device__ void tell(int cond, const Found& f) {
+        for (int r = 0; r < C; ++r)
+            *cluster.map_shared_rank(&sh.found[cond], r) = f;
+    }
+
+    // the condition that ends first
+    __device__ Found first() const {
+        Found f = sh.found[0];
+        for (int c = 1; c < kConds; ++c)
+            if (sh.found[c].bin < f.bin)
+                f = sh.found[c];
+        return f;
+    }
+
+    // the largest key with bin >= b (or the smallest with bin <= b): bins fall as keys grow
+    __device__ uint32_t key_at(int b, bool largest) const {
+        uint32_t lo = kKeyMinusInf + 1, hi = logit_key(scale.lmax);
+        while (lo < hi) {
+            if (largest) {
+                const uint32_t mid = lo + (hi - lo + 1) / 2;
+                if (bin_of(key_logit(mid)) >= b)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            } else {
+                const uint32_t mid = lo + (hi - lo) / 2;
+                if (bin_of(key_logit(mid)) <= b)
+                    hi = mid;
+                else
+                    lo = mid + 1;
+            }
+        }
+        return lo;
+    }
+
+    // Narrows the entries of found bin f to a key range [klo, khi] that fits
+    // the list, or is a single key.
+    __device__ void narrow(Search s, Found& f, uint32_t limit_key, uint32_t& klo, uint32_t& khi,
+                           bool& split) {
+        khi = key_at(f.bin, true);
+        klo = key_at(f.bin, false);
+        while (f.count > kList && klo != khi) {
+            split = true;
+            int sh_ = 0;
+            while (((khi - klo) >> sh_) >= (uint32_t)kBins)
+                ++sh_;
+            const uint32_t top = khi, bottom = klo;
+            cluster.sync();  // everyone has read `found`
+            histogram([&](float l) {
+                const uint32_t k = logit_key(l);
+                return k <= top && k >= bottom ? (int)((top - k) >> sh_) : -1;
+            });
+            s.above_mass = f.above_mass;
+            s.above_count = f.above_count;
+            s.limit_bin = kBins;
+            if (!s.draw && limit_key >= bottom && limit_key <= top)
+                s.limit_bin = (int)((top - limit_key) >> sh_);
+            unsigned long long m;
+            uint32_t n;
+            search(s, false, m, n);
+            const Found g = first();  // a condition that ends in a range ends in a part of it
+            f = g;
+            khi = top - ((uint32_t)g.bin << sh_);
+            const uint32_t low = sh_ ? khi - ((1u << sh_) - 1) : khi;
+            klo = low > bottom && low <= khi ? low : bottom;
+        }
+    }
+
+    // Entries with klo <= key <= khi into the first CTA's list, sorted there.
+    __device__ void gather(uint32_t klo, uint32_t khi) {
+        cluster.sync();  // everyone has read `found`; list_n is zero since the histogram
+        if (rank == 0 && tid == 0)
+            sh.list_n = 0;
+        cluster.sync();
+        uint32_t* n = cluster.map_shared_rank(&sh.list_n, 0);
+        unsigned long long* list = cluster.map_shared_rank(sh.list, 0);
+        each([&](float l, int64_t id) {
+            const uint32_t k = logit_key(l);
+            if (k >= klo && k <= khi) {
+                const uint32_t at = atomicAdd(n, 1u);
+                if (at < (uint32_t)kList)
+                    list[at] = ((unsigned long long)k << 32) | (uint32_t)~(uint32_t)id;
+            }
+        });
+        cluster.sync();
+        if (rank == 0) {
+            if (tid == 0 && sh.list_n > (uint32_t)kList)
+                sh.list_n = kList;
+            __syncthreads();
+            int size = 2;
+            while (size < (int)sh.list_n)
+                size <<= 1;
+            for (int i = (int)sh.list_n + tid; i < size; i += kNT)
+                sh.list[i] = 0;
+            __syncthreads();
+            for (int len = 2; len <= size; len <<= 1)
+                for (int gap = len >> 1; gap; gap >>= 1) {
+                    for (int i = tid; i < size / 2; i += kNT) {
+                        const int x = 2 * i - (i & (gap - 1)), y = x + gap;
+                        const unsigned long long vx = sh.list[x], vy = sh.list[y];
+                        if ((vx < vy) == ((x & len) == 0)) {  // descending runs first
+                            sh.list[x] = vy;
+                            sh.list[y] = vx;
+                        }
+                    }
+                    __syncthreads();
+                }
+        }
+    }
+
+    // weights of the list's two entries of this thread, and what lies before them
+    __device__ void list_scan(unsigned long long w[2], unsigned long long& before) {
+        unsigned long long m = 0, bm;
+        uint32_t n = 0, bn;
+        for (int j = 0; j < 2; ++j) {
+            const int i = 2 * tid + j;
+            w[j] = i < (int)sh.list_n
+                       ? weight_fixed(scale, sh.pow2, key_logit((uint32_t)(sh.list[i] >> 32)))
+                       : 0;
+            m += w[j];
+        }
+        scan(m, n, bm, bn);
+        before = bm;
+    }
+
+    // The last group of equal logits in the list that every filter keeps; the
+    // first CTA tells the cut, the kept mass and count.
+    __device__ void cut_in_list(const Search& s, const Found& f, uint32_t limit_key) {
+        if (rank == 0) {
+            const int n = (int)sh.list_n;
+            unsigned long long w[2], before;
+            list_scan(w, before);
+            unsigned long long at = f.above_mass + before;
+            int last = -1;
+            for (int j = 0; j < 2; ++j) {
+                const int i = 2 * tid + j;
+                if (i < n) {
+                    const uint32_t k = (uint32_t)(sh.list[i] >> 32);
+                    const bool start = i == 0 || (uint32_t)(sh.list[i - 1] >> 32) != k;
+                    if (start && k >= limit_key && (!s.k || f.above_count + i < s.k) &&
+                        (s.top_p >= 1.0 || at < s.p))
+                        last = i;
+                }
+                at += w[j];
+            }
+            // conditions fail for good once they fail: the last start over all threads
+            for (int o = 16; o; o >>= 1) {
+                const int x = __shfl_xor_sync(kAllLanes, last, o);
+                last = x > last ? x : last;
+            }
+            __syncthreads();
+            if (lane == 0)
+                sh.warp_max[warp] = (uint32_t)(last + 1);
+            __syncthreads();
+            int g = 0;
+            for (int i = 0; i < kNW; ++i)
+                g = (int)sh.warp_max[i] > g ? (int)sh.warp_max[i] : g;
+            --g;  // -1: nothing of the list is kept
+            const uint32_t key = g >= 0 ? (uint32_t)(sh.list[g] >> 32) : limit_key;
+            unsigned long long at2 = f.above_mass + before;
+            if (tid == 0 && (g < 0 || n == 0)) {
+                sh.cut_key = key;
+                sh.kept = f.above_count;
+                sh.kept_mass = f.above_mass;
+            }
+            for (int j = 0; j < 2; ++j) {
+                const int i = 2 * tid + j;
+                at2 += w[j];
+                if (g >= 0 && i < n && (uint32_t)(sh.list[i] >> 32) == key &&
+                    (i == n - 1 || (uint32_t)(sh.list[i + 1] >> 32) != key)) {
+                    sh.cut_key = key;
+                    sh.kept = f.above_count + i + 1;
+                    sh.kept_mass = at2;
+                }
+            }
+            __syncthreads();
+            if (tid > 0 && tid < C) {
+                *cluster.map_shared_rank(&sh.cut_key, tid) = sh.cut_key;
+                *cluster.map_shared_rank(&sh.kept, tid) = sh.kept;
+                *cluster.map_shared_rank(&sh.kept_mass, tid) = sh.kept_mass;
+            }
+        }
+        cluster.sync();
+    }
+
+    // The first entry of the list whose running sum exceeds `target`.
+    __device__ void draw_in_list(unsigned long long above_mass, unsigned long long target) {
+        if (rank == 0) {
+            const int n = (int)sh.list_n;
+            unsigned long long w[2], at;
+            list_scan(w, at);
+            at += above_mass;
+            for (int j = 0; j < 2; ++j) {
+                const int i = 2 * tid + j;
+                if (i < n && at <= target && at + w[j] > target) {
+                    sh.token = ~(uint32_t)sh.list[i];
+                    sh.token_key = (uint32_t)(sh.list[i] >> 32);
+                }
+                at += w[j];
+            }
+            __syncthreads();
+        }
+    }
+
+    // The entry number r, by ascending id, among those with this key.
+    __device__ void draw_among_equals(uint32_t key, unsigned long long r) {
+        const int64_t per = (s1 - s0 + kNT - 1) / kNT;
+        const int64_t e0 = s0 + tid * per, e1 = e0 + per < s1 ? e0 + per : s1;
+        uint32_t n = 0, before;
+        unsigned long long m = 0, bm;
+        for (int64_t e = e0; e < e1; ++e)
+            n += logit_key(scalar_entry<ES>(base, e)) == key;
+        const uint32_t mine = n;
+        scan(m, n, bm, before);
+        cluster.sync();
+        if (tid < C)
+            *cluster.map_shared_rank(&sh.part_cnt[rank], tid) = n;
+        cluster.sync();
+        for (int c = 0; c < rank; ++c)
+            before += sh.part_cnt[c];
+        if (r >= before && r < (unsigned long long)before + mine) {
+            uint32_t left = (uint32_t)(r - before);
+            for (int64_t e = e0; e < e1; ++e)
+                if (logit_key(scalar_entry<ES>(base, e)) == key && left-- == 0) {
+                    *cluster.map_shared_rank(&sh.token, 0) = (uint32_t)e;
+                    *cluster.map_shared_rank(&sh.token_key, 0) = key;
+                    break;
+                }
+        }
+        cluster.sync();
+    }
+
+    // probabilities (or a fill) and truncated logits; keep(l, id) says what stays
+    template <class Keep>
+    __device__ void write(Keep&& keep, float inv, bool bad) {
+        if (a.probs) {
+            float* p = a.probs + row * a.probs_stride;
+            each([&](float l, int64_t id) {
+                p[id] = bad ? __int_as_float(0x7fffffff)
+                            : keep(l, id) ? (inv > 0.0f ? weight_float(scale, l) * inv : 1.0f) : 0.0f;
+            });
+        }
+        if (a.out) {
+            unsigned char* o = static_cast<unsigned char*>(a.out) + row * a.out_stride * ES;
+            each([&](float l, int64_t id) {
+                const uint32_t b = bad || keep(l, id) ? __float_as_uint(l) : 0xff800000u;
+                if constexpr (ES == 4)
+                    reinterpret_cast<uint32_t*>(o)[id] = b;
+                else
+                    reinterpret_cast<unsigned short*>(o)[id] = (unsigned short)(b >> 16);
+            });
+        }
+    }
+
+    __device__ void finish(int code, uint32_t kept, float mass, float p) {
+        if (rank == 0 && tid == 0) {
+            if (a.tokens)
+                a.tokens[row * a.token_stride] = code ? -1 : (int32_t)sh.token;
+            const float nan = __int_as_float(0x7fffffff);
+            if (a.p_token)
+                a.p_token[row] = code ? nan : p;
+            if (a.mass)
+                a.mass[row] = code ? nan : mass;
+            if (a.kept)
+                a.kept[row] = code ? 0 : (int32_t)kept;
+            if (a.status)
+                a.status[row] = code;
+            if (code)
+                atomicOr(a.err_word, 1u << code);
+        }
+    }
+
+    __device__ void run() {
+        const int64_t seq = row / a.rows_per_seq;
+        const float T = a.set.temperatures ? a.set.temperatures[seq] : a.set.temperature;
+        const int32_t top_k = a.set.top_ks ? a.set.top_ks[seq] : a.set.top_k;
+        const double top_p = a.set.top_ps ? (double)a.set.top_ps[seq] : a.set.top_p;
+        const double min_p = a.set.min_ps ? (double)a.set.min_ps[seq] : a.set.min_p;
+        const float u = a.u ? a.u[row * a.u_stride] : 0.0f;
+        int code = SV_OK;
+        if (!(T == 0.0f || (T >= 1.17549435e-38f && T <= 3.402823466e38f)) || !(top_p > 0.0) ||
+            !(min_p < 1.0))
+            code = SV_ERR_INVALID_ARG;
+        else if (!(u >= 0.0f && u < 1.0f))
+            code = SV_ERR_UNIFORM_RANGE;
+        if (tid < 64)
+            sh.pow2[tid] = kPow2Steps[tid];
+
+        cluster.barrier_arrive();
+
+        // A. the largest logit (NaN if there is one), over the cluster
+        float m = __int_as_float(0xff800000);
+        each([&](float l, int64_t) { m = max_nan(m, l); });
+#pragma unroll
+        for (int o = 16; o; o >>= 1)
+            m = max_nan(m, __shfl_xor_sync(kAllLanes, m, o));
+        if (lane == 0)
+            sh.warp_max[warp] = __float_as_uint(m);
+        __syncthreads();
+        for (int w = 0; w < kNW; ++w)
+            m = max_nan(m, __uint_as_float(sh.warp_max[w]));
+        cluster.barrier_wait();  // every CTA of the cluster runs: its memory may be written
+        if (tid < C)
+            *cluster.map_shared_rank(&sh.part_max[rank], tid) = __float_as_uint(m);
+        cluster.sync();
+        for (int r = 0; r < C; ++r)
+            m = max_nan(m, __uint_as_float(sh.part_max[r]));
+        if (!code && !(m >= -3.402823466e38f && m <= 3.402823466e38f))
+            code = SV_ERR_NONFINITE;
+        scale.lmax = m;
+        if (code) {
+            write([](float, int64_t) { return false; }, 0.0f, true);
+            finish(code, 0, 0.0f, 0.0f);
+            cluster.sync();
+            return;
+        }
+        if (T == 0.0f) {
+            uint32_t id = 0xffffffffu;
+            each([&](float l, int64_t i) {
+                if (l == m)
+                    id = min(id, (uint32_t)i);
+            });
+            id = __reduce_min_sync(kAllLanes, id);
+            __syncthreads();
+            if (lane == 0)
+                sh.warp_cnt[warp] = id;
+            __syncthreads();
+            for (int w = 0; w < kNW; ++w)
+                id = min(id, sh.warp_cnt[w]);
+            if (tid < C)
+                *cluster.map_shared_rank(&sh.part_cnt[rank], tid) = id;
+            cluster.sync();
+            for (int r = 0; r < C; ++r)
+                id = min(id, sh.part_cnt[r]);
+            if (tid == 0)
+                sh.token = id;
+            write([=](float, int64_t i) { return (uint32_t)i == id; }, 0.0f, false);
+            finish(SV_OK, 1, 1.0f, 1.0f);
+            cluster.sync();
+            return;
+        }
+        split_scale(T, scale.ch, scale.cl);
+
+        // B. bins over the whole row
+        const auto linear = [&](float l) {
+            return logit_key(l) > kKeyMinusInf ? bin_of(l) : -1;
+        };
+        histogram(linear);
+        Search s;
+        s.above_mass = 0;
+        s.above_count = 0;
+        s.k = top_k > 0 ? (uint32_t)top_k : 0;
+        s.top_p = top_p;
+        s.p = 0;
+        s.draw = false;
+        s.limit_bin = kBins;
+        uint32_t limit_key = 0;
+        if (min_p > 0.0) {
+            // the smallest float l with l - l_max >= T ln(min_p)
+            const float limit = __double2float_ru((double)m + (double)T * log(min_p));
+            limit_key = logit_key(limit);
+            if (limit_key > kKeyMinusInf)
+                s.limit_bin = bin_of(limit);
+        }
+        unsigned long long whole, E;
+        uint32_t n, kept;
+        search(s, true, whole, n);
+        const Found f = first();
+        uint32_t cut_key = kKeyMinusInf + 1, klo = 1, khi = 0;
+        bool split = false;
+        Found g = f;
+        if (f.bin < kBins) {
+            narrow(s, g, limit_key, klo, khi, split);
+            if (g.count <= kList) {
+                gather(klo, khi);
+                cut_in_list(s, g, limit_key);
+                cut_key = sh.cut_key;
+                kept = sh.kept;
+                E = sh.kept_mass;
+            } else {  // one value: the conditions hold at its start, or the limit is above it
+                const bool in = klo >= limit_key;
+                cut_key = in ? klo : limit_key;
+                kept = g.above_count + (in ? g.count : 0);
+                E = g.above_mass + (in ? g.mass : 0);
+            }
+        } else {
+            kept = n;
+            E = whole;
+        }
+
+        // C. the draw
+        float p = 0.0f;
+        const float inv = (float)((double)(1ull << scale.fix) / (double)E);
+        if (a.u) {
+            const unsigned long long target = floor_scaled(u, E);
+            if (f.bin < kBins && g.count <= kList && target >= g.above_mass) {
+                draw_in_list(g.above_mass, target);  // the cut's list holds it
+            } else if (f.bin < kBins && g.count > kList && target >= g.above_mass) {
+                const unsigned long long w = weight_fixed(scale, sh.pow2, key_logit(klo));
+                draw_among_equals(klo, (target - g.above_mass) / w);
+            } else {
+                cluster.sync();
+                if (split)
+                    histogram(linear);
+                else if (tid < kConds)
+                    sh.found[tid].bin = kBins;
+                cluster.sync();
+                Search d;
+                d.above_mass = 0;
+                d.above_count = 0;
+                d.k = 0;
+                d.top_p = 1.0;
+                d.p = target;
+                d.limit_bin = kBins;
+                d.draw = true;
+                unsigned long long dm;
+                uint32_t dn;
+                search(d, true, dm, dn);
+                Found h = first();
+                narrow(d, h, 0, klo, khi, split);
+                if (h.count <= kList) {
+                    gather(klo, khi);
+                    draw_in_list(h.above_mass, target);
+                } else {
+                    const unsigned long long w = weight_fixed(scale, sh.pow2, key_logit(klo));
+                    draw_among_equals(klo, (target - h.above_mass) / w);
+                }
+            }
+            if (rank == 0 && tid == 0)
+                p = weight_float(scale, key_logit(sh.token_key)) * inv;
+        }
+        // D. rows out
+        write([&](float l, int64_t) { return logit_key(l) >= cut_key; }, inv, false);
+        finish(SV_OK, kept, (float)((double)E / (double)whole), p);
+        cluster.sync();  // no CTA leaves while another may still write into it
+    }
+};
+
+template <int ES>
+__global__ void __launch_bounds__(kNT, 2) sv_sample_kernel(const __grid_constant__ Args a) {
+    __shared__ Shared sh;
+    Kernel<ES> k(a, sh);
+    k.run();
+}
+
+int launch(sv_ctx* ctx, Args& a, int B, int rows, int64_t V, int dtype, cudaStream_t stream) {
+    sv_plan plan;
+    const int rc = spec_sample_get_plan(ctx, B, rows, V, dtype, &plan);
+    if (rc != SV_OK)
+        return rc;
+    const int es = dtype == SV_BF16 ? 2 : 4;
+    a.err_word = ctx->d_err;
+    a.V = V;
+    a.slice = plan.slice;
+    a.C = plan.cluster;
+    a.rows_per_seq = rows;
+    a.fix = weight_bits(V);
+    a.vec = aligned(a.logits, 16) && (a.stride * es) % 16 == 0 ? 1 : 0;
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof cfg);
+    cfg.gridDim = dim3((unsigned)plan.grid, 1, 1);
+    cfg.blockDim = dim3(kNT, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)plan.cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    DeviceGuard guard(ctx->device);
+    if (cudaLaunchKernelEx(&cfg, es == 2 ? sv_sample_kernel<2> : sv_sample_kernel<4>, a) !=
+        cudaSuccess) {
+        (void)cudaGetLastError();
+        return SV_ERR_CUDA;
+    }
+    return SV_OK;
+}
+
+// The checks that the draw and the filter share.
+int check(const sv_ctx* ctx, const void* logits, int dtype, int64_t stride, int B, int rows,
+          int64_t V, const sv_sampling* s) {
+    if (!ctx || !logits || !s || (dtype != SV_F32 && dtype != SV_BF16))
+        return SV_ERR_INVALID_ARG;
+    if (B < 1 || B > ctx->max_B || rows < 1 || rows > ctx->max_K + 1 || V < 1 || V > ctx->max_V ||
+        V > ((int64_t)1 << 31) || stride < V || stride > ((int64_t)1 << 40))
+        return SV_ERR_INVALID_ARG;
+    if ((double)B * (double)rows * (double)stride >= 1099511627776.0)  // 2^40
+        return SV_ERR_INVALID_ARG;
+    if (!aligned(logits, dtype == SV_BF16 ? 2 : 4) || !aligned(s->temperatures, 4) ||
+        !aligned(s->top_ks, 4) || !aligned(s->top_ps, 4) || !aligned(s->min_ps, 4))
+        return SV_ERR_INVALID_ARG;
+    if (!s->temperatures && !(s->temperature == 0.0f || (s->temperature >= 1.17549435e-38f &&
+                                                         std::isfinite(s->temperature))))
+        return SV_ERR_INVALID_ARG;
+    if ((!s->top_ps && !(s->top_p > 0.0)) || (!s->min_ps && !(s->min_p < 1.0)))
+        return SV_ERR_INVALID_ARG;
+    return SV_OK;
+}
+
+}  // namespace
+
+namespace sv {
+
+int sampling_setup() {
+    for (const void* fn : {(const void*)sv_sample_kernel<2>, (const void*)sv_sample_kernel<4>})
+        if (cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+            cudaSuccess) {
+            (void)cudaGetLastError();
+            return 8;
+        }
+    return logprobs_setup() ? 16 : 8;
+}
+
+}  // namespace sv
+
+extern "C" {
+
+int spec_sample_get_plan(sv_ctx* ctx, int B, int rows_per_seq, int64_t V, int logits_dtype,
+                         sv_plan* out) {
+    if (!ctx)
+        return SV_ERR_INVALID_ARG;
+    return spec_sample_plan_for(ctx->num_sms, ctx->sampling_max_cluster, B, rows_per_seq, V,
+                                logits_dtype, ctx->ovr_cluster, out);
+}
+
+int spec_sample_run(sv_ctx* ctx, const void* logits, int logits_dtype, int64_t logits_stride,
+                    const float* uniforms, int64_t uniforms_stride, int B, int rows_per_seq,
+                    int64_t V, const sv_sampling* settings, int32_t* tokens, int64_t tokens_stride,
+                    float* probs, int64_t probs_stride, float* p_token, int32_t* kept,
+                    int32_t* status, void* stream) {
+    const int rc = check(ctx, logits, logits_dtype, logits_stride, B, rows_per_seq, V, settings);
+    if (rc != SV_OK)
+        return rc;
+    const int64_t most = (int64_t)1 << 40;
+    if (!uniforms || !tokens || uniforms_stride < 1 || uniforms_stride > most ||
+        tokens_stride < 1 || tokens_stride > most || !aligned(uniforms, 4) || !aligned(tokens, 4) ||
+        !aligned(probs, 4) || !aligned(p_token, 4) || !aligned(kept, 4) || !aligned(status, 4) ||
+        (probs && (probs_stride < V || probs_stride > most)))
+        return SV_ERR_INVALID_ARG;
+    Args a;
+    std::memset(&a, 0, sizeof a);
+    a.logits = logits;
+    a.stride = logits_stride;
+    a.u = uniforms;
+    a.u_stride = uniforms_stride;
+    a.tokens = tokens;
+    a.token_stride = tokens_stride;
+    a.probs = probs;
+    a.probs_stride = probs_stride;
+    a.p_token = p_token;
+    a.kept = kept;
+    a.status = status;
+    a.set = *settings;
+    return launch(ctx, a, B, rows_per_seq, V, logits_dtype, static_cast<cudaStream_t>(stream));
+}
+
+int spec_filter_run(sv_ctx* ctx, const void* logits, int logits_dtype, int64_t logits_stride,
+                    int B, int rows_per_seq, int64_t V, const sv_sampling* settings,
+                    void* out_logits, int64_t out_stride, int32_t* kept, float* mass,
+                    int32_t* status, void* stream) {
+    const int rc = check(ctx, logits, logits_dtype, logits_stride, B, rows_per_seq, V, settings);
+    if (rc != SV_OK)
+        return rc;
+    const int es = logits_dtype == SV_BF16 ? 2 : 4;
+    if (!out_logits || !aligned(out_logits, es) || out_stride < V ||
+        out_stride > ((int64_t)1 << 40) || !aligned(kept, 4) || !aligned(mass, 4) ||
+        !aligned(status, 4))
+        return SV_ERR_INVALID_ARG;
+    // in place, or apart: rows that overlap others would be read after they were written
+    const int64_t last = (int64_t)B * rows_per_seq - 1;
+    const char *i0 = static_cast<const char*>(logits), *o0 = static_cast<char*>(out_logits);
+    const char *i1 = i0 + (last * logits_stride + V) * es, *o1 = o0 + (last * out_stride + V) * es;
+    if (o0 < i1 && i0 < o1 && !(i0 == o0 && (last == 0 || logits_stride == out_stride)))
+        return SV_ERR_INVALID_ARG;
+    Args a;
+    std::memset(&a, 0, sizeof a);
+    a.logits = logits;
+    a.stride = logits_stride;
+    a.out = out_logits;
+    a.out_stride = out_stride;
+    a.kept = kept;
+    a.mass = mass;
+    a.status = status;
+    a.set = *settings;
+    return launch(ctx, a, B, rows_per_seq, V, logits_dtype, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,59 @@
+// sampling_planner.cpp -- maps the rows of a sampling, filter or
+// log-probability call onto thread-block clusters: one cluster per row, a
+// slice of the vocabulary per CTA.
+#include "../../include/spec_verify.h"
+#include "sv_internal.h"
+
+namespace {
+
+// The largest power of two of CTAs per row that the GPU holds for every row
+// at once (ctas_per_sm of `threads` each) and that leaves a CTA at least
+// min_slice entries.
+int plan_rows(int num_sms, int max_cluster, int B, int rows_per_seq, int64_t V, int dtype,
+              int ovr_cluster, int threads, int ctas_per_sm, int64_t min_slice, sv_plan* out) {
+    using namespace sv;
+    if (!out || num_sms < 1 || max_cluster < 1 || B < 1 || rows_per_seq < 1 ||
+        rows_per_seq > kMaxRows || V < 1 || V > ((int64_t)1 << 31) ||
+        (dtype != SV_F32 && dtype != SV_BF16) || ovr_cluster < 0 || ovr_cluster > kMaxCluster)
+        return SV_ERR_INVALID_ARG;
+    if (ovr_cluster > max_cluster)
+        return SV_ERR_UNSUPPORTED;
+    const int64_t rows = (int64_t)B * rows_per_seq;
+    int C = 1;
+    if (ovr_cluster) {
+        C = ovr_cluster;
+    } else {
+        for (int c = max_cluster < kMaxCluster ? max_cluster : kMaxCluster; c > 1; c /= 2)
+            if (rows * c <= (int64_t)ctas_per_sm * num_sms && ceil_div(V, c) >= min_slice) {
+                C = c;
+                break;
+            }
+    }
+    if (rows * C > 0x7fffffff)
+        return SV_ERR_UNSUPPORTED;
+    out->cluster = C;
+    out->group = 1;
+    out->threads = threads;
+    out->smem_bytes = 0;
+    out->slice = round_up(ceil_div(V, C), kSliceAlign);
+    out->grid = rows * C;
+    out->bulk_copy = ((V * (dtype == SV_BF16 ? 2 : 4)) % 16) == 0 ? 1 : 0;
+    out->prefetch_next = 0;
+    out->stages = 0;
+    return SV_OK;
+}
+
+}  // namespace
+
+extern "C" int spec_sample_plan_for(int num_sms, int max_cluster, int B, int rows_per_seq,
+                                    int64_t V, int logits_dtype, int ovr_cluster, sv_plan* out) {
+    return plan_rows(num_sms, max_cluster, B, rows_per_seq, V, logits_dtype, ovr_cluster, 512, 2,
+                     2048, out);
+}
+
+extern "C" int spec_logprobs_plan_for(int num_sms, int max_cluster, int B, int rows_per_seq,
+                                      int64_t V, int logits_dtype, int ovr_cluster,
+                                      sv_plan* out) {
+    return plan_rows(num_sms, max_cluster, B, rows_per_seq, V, logits_dtype, ovr_cluster, 256, 4,
+                     2048, out);
+}

@@ -54,6 +54,7 @@
 #include <type_traits>
 
 #include "../../include/spec_verify.h"
+#include "sv_context.h"
 #include "sv_internal.h"
 
 namespace cg = cooperative_groups;
@@ -1920,40 +1921,12 @@ KernelFn pick_kernel(int es, int threads, int stages = sv::kStages, bool dl = fa
     return nullptr;
 }
 
-struct DeviceGuard {
-    int prev = -1;
-    bool switched = false;
-    explicit DeviceGuard(int dev) {
-        if (cudaGetDevice(&prev) == cudaSuccess && prev != dev) {
-            switched = cudaSetDevice(dev) == cudaSuccess;
-        }
-    }
-    ~DeviceGuard() {
-        if (switched)
-            cudaSetDevice(prev);
-    }
-};
+using sv::aligned;
+using sv::DeviceGuard;
 
 }  // namespace
 
-struct sv_ctx {
-    int device = 0;
-    int max_B = 0, max_K = 0;
-    int64_t max_V = 0;
-    int num_sms = 0, smem_optin = 0, max_cluster = 8;
-    int greedy_max_cluster = 8;
-    uint32_t* d_err = nullptr;
-    int ovr_cluster = 0, ovr_group = 0, ovr_threads = 0;  // spec_verify_set_plan_override
-    uint32_t* al_hist = nullptr;  // caller's accepted-length counters (device), or none
-    int al_bins = 0;
-    // staging for the host-buffer entry point
-    unsigned char* d_stage = nullptr;
-    size_t stage_bytes = 0;
-};
-
 namespace {
-
-bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 
 int validate(const sv_ctx* ctx, const void* logits, int dtype, const float* q, const int32_t* tokens,
              const float* uniforms, int B, int K, int64_t V, float T, const int32_t* accept_len,
@@ -2208,7 +2181,9 @@ int spec_verify_init(sv_ctx** out, int device, int max_B, int max_K, int64_t max
     ctx->max_K = max_K;
     ctx->max_V = max_V;
     apply_device_info(ctx, info);
-    if (cudaMalloc(&ctx->d_err, sizeof(uint32_t)) != cudaSuccess ||
+    const int sampling_max = sv::sampling_setup();
+    ctx->sampling_max_cluster = sampling_max < info.max_cluster ? sampling_max : info.max_cluster;
+    if (sampling_max < 1 || cudaMalloc(&ctx->d_err, sizeof(uint32_t)) != cudaSuccess ||
         cudaMemset(ctx->d_err, 0, sizeof(uint32_t)) != cudaSuccess) {
         (void)cudaGetLastError();
         if (ctx->d_err)
