@@ -407,7 +407,7 @@ int spec_filter_run(sv_ctx* ctx, const void* logits, int logits_dtype, int64_t l
 
 /* The launch plan of the two calls above on the context's device, and their
  * planner as a pure host function (no CUDA call): one cluster per row, the
- * largest whose CTAs (two of 512 threads per SM) hold every row at once. */
+ * largest whose CTAs (four of 256 threads per SM) hold every row at once. */
 int spec_sample_get_plan(sv_ctx* ctx, int B, int rows_per_seq, int64_t V, int logits_dtype,
                          sv_plan* out);
 int spec_sample_plan_for(int num_sms, int max_cluster, int B, int rows_per_seq, int64_t V,

@@ -40,10 +40,11 @@ namespace {
 
 using namespace sv;
 
-constexpr int kNT = 512;
+constexpr int kNT = 256;
 constexpr int kNW = kNT / 32;
 constexpr int kBins = 2048;
-constexpr int kList = 1024;  // entries of the list (two per thread)
+constexpr int kList = 1024;  // entries of the list
+constexpr int kOwn = kList / kNT;  // of them per thread
 constexpr int kMaxC = 16;
 constexpr float kBinsPerOctave = 32.0f;
 
@@ -78,10 +79,34 @@ struct Found {
     unsigned long long mass, above_mass;
 };
 
+// bfloat16 rows are counted value by value: a place for every magnitude from
+// 2^-25 up to 127 of either sign, and one each for what is smaller and larger.
+// A place i is 0 below the window, 1..kMags inside it and kMags + 1 above; its
+// signed index is i, or -1 - i for negative logits, so that it grows with the
+// logit.  Searches run by descending logit: D = kMags + 1 - index.
+constexpr int kMag0 = (127 - 25) << 7;
+constexpr int kMags = 4094;
+constexpr int kPlaces = 2 * (kMags + 2);
+constexpr int kChunks = kPlaces / 32;  // places a warp takes at once
+constexpr int kFirstTiny = kMags + 1;  // D of the two places below the window
+constexpr int kNoPlace = kPlaces;
+
 struct Shared {
-    uint32_t lo[kBins], hi[kBins], cnt[kBins];
-    unsigned long long list[kList];  // key << 32 | ~id
+    union {
+        struct {
+            uint32_t lo[kBins], hi[kBins], cnt[kBins];
+            unsigned long long list[kList];  // key << 32 | ~id
+        };
+        uint32_t count[kPlaces];
+    };
     float2 pow2[64];
+    unsigned long long chunk_mass[kChunks];
+    uint32_t chunk_cnt[kChunks];
+    struct {
+        int chunk;
+        uint32_t above_count;
+        unsigned long long above_mass;
+    } hit[kConds];
     unsigned long long part_mass[kMaxC];
     uint32_t part_cnt[kMaxC];
     uint32_t part_max[kMaxC];
@@ -406,12 +431,12 @@ struct Kernel {
         }
     }
 
-    // weights of the list's two entries of this thread, and what lies before them
-    __device__ void list_scan(unsigned long long w[2], unsigned long long& before) {
+    // weights of this thread's entries of the list, and what lies before them
+    __device__ void list_scan(unsigned long long w[kOwn], unsigned long long& before) {
         unsigned long long m = 0, bm;
         uint32_t n = 0, bn;
-        for (int j = 0; j < 2; ++j) {
-            const int i = 2 * tid + j;
+        for (int j = 0; j < kOwn; ++j) {
+            const int i = kOwn * tid + j;
             w[j] = i < (int)sh.list_n
                        ? weight_fixed(scale, sh.pow2, key_logit((uint32_t)(sh.list[i] >> 32)))
                        : 0;
@@ -426,12 +451,12 @@ struct Kernel {
     __device__ void cut_in_list(const Search& s, const Found& f, uint32_t limit_key) {
         if (rank == 0) {
             const int n = (int)sh.list_n;
-            unsigned long long w[2], before;
+            unsigned long long w[kOwn], before;
             list_scan(w, before);
             unsigned long long at = f.above_mass + before;
             int last = -1;
-            for (int j = 0; j < 2; ++j) {
-                const int i = 2 * tid + j;
+            for (int j = 0; j < kOwn; ++j) {
+                const int i = kOwn * tid + j;
                 if (i < n) {
                     const uint32_t k = (uint32_t)(sh.list[i] >> 32);
                     const bool start = i == 0 || (uint32_t)(sh.list[i - 1] >> 32) != k;
@@ -461,8 +486,8 @@ struct Kernel {
                 sh.kept = f.above_count;
                 sh.kept_mass = f.above_mass;
             }
-            for (int j = 0; j < 2; ++j) {
-                const int i = 2 * tid + j;
+            for (int j = 0; j < kOwn; ++j) {
+                const int i = kOwn * tid + j;
                 at2 += w[j];
                 if (g >= 0 && i < n && (uint32_t)(sh.list[i] >> 32) == key &&
                     (i == n - 1 || (uint32_t)(sh.list[i + 1] >> 32) != key)) {
@@ -485,11 +510,11 @@ struct Kernel {
     __device__ void draw_in_list(unsigned long long above_mass, unsigned long long target) {
         if (rank == 0) {
             const int n = (int)sh.list_n;
-            unsigned long long w[2], at;
+            unsigned long long w[kOwn], at;
             list_scan(w, at);
             at += above_mass;
-            for (int j = 0; j < 2; ++j) {
-                const int i = 2 * tid + j;
+            for (int j = 0; j < kOwn; ++j) {
+                const int i = kOwn * tid + j;
                 if (i < n && at <= target && at + w[j] > target) {
                     sh.token = ~(uint32_t)sh.list[i];
                     sh.token_key = (uint32_t)(sh.list[i] >> 32);
@@ -528,39 +553,481 @@ struct Kernel {
         cluster.sync();
     }
 
-    // probabilities (or a fill) and truncated logits; keep(l, id) says what stays
+    // Probabilities and truncated logits; keep(l, id) says what stays.  A vector
+    // none of whose logits reaches `cut` is written without looking further.
     template <class Keep>
-    __device__ void write(Keep&& keep, float inv, bool bad) {
-        if (a.probs) {
-            float* p = a.probs + row * a.probs_stride;
-            each([&](float l, int64_t id) {
-                p[id] = bad ? __int_as_float(0x7fffffff)
-                            : keep(l, id) ? (inv > 0.0f ? weight_float(scale, l) * inv : 1.0f) : 0.0f;
-            });
+    __device__ void write(Keep&& keep, float cut, float inv, bool bad) {
+        constexpr int E = 16 / ES;
+        const float nan = __int_as_float(0x7fffffff);
+        const auto prob = [&](float l, int64_t id) {
+            return bad ? nan : keep(l, id) ? (inv > 0.0f ? weight_float(scale, l) * inv : 1.0f) : 0.0f;
+        };
+        const auto logit = [&](float l, int64_t id) {
+            return bad || keep(l, id) ? __float_as_uint(l) : 0xff800000u;
+        };
+        float* p = a.probs ? a.probs + row * a.probs_stride : nullptr;
+        unsigned char* o = a.out ? static_cast<unsigned char*>(a.out) + row * a.out_stride * ES : nullptr;
+        if (!p && !o)
+            return;
+        int64_t i = s0;
+        if (a.vec && a.out_vec) {
+            const uint4* x = reinterpret_cast<const uint4*>(base);
+            const int64_t v1 = s1 / E;
+            constexpr int D = 2;
+            for (int64_t v = s0 / E + tid; v < v1; v += D * kNT) {
+                uint4 w[D];
+#pragma unroll
+                for (int k = 0; k < D; ++k)
+                    if (v + k * kNT < v1)
+                        w[k] = load_stream(x + v + k * kNT);
+#pragma unroll
+                for (int k = 0; k < D; ++k) {
+                    const int64_t u = v + k * kNT;
+                    if (u >= v1)
+                        continue;
+                    float m = vector_entry<ES>(w[k], 0);
+#pragma unroll
+                    for (int e = 1; e < E; ++e)
+                        m = fmaxf(m, vector_entry<ES>(w[k], e));
+                    const bool any = bad || m >= cut;
+                    if (p) {
+                        float f[E];
+#pragma unroll
+                        for (int e = 0; e < E; ++e)
+                            f[e] = any ? prob(vector_entry<ES>(w[k], e), u * E + e) : 0.0f;
+#pragma unroll
+                        for (int e = 0; e < E; e += 4)
+                            reinterpret_cast<float4*>(p)[(u * E + e) / 4] =
+                                make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+                    }
+                    if (o) {
+                        uint32_t h[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            if constexpr (ES == 4) {
+                                h[j] = any ? logit(vector_entry<ES>(w[k], j), u * E + j) : 0xff800000u;
+                            } else {
+                                h[j] = any ? (logit(vector_entry<ES>(w[k], 2 * j), u * E + 2 * j) >> 16) |
+                                                 (logit(vector_entry<ES>(w[k], 2 * j + 1), u * E + 2 * j + 1) &
+                                                  0xffff0000u)
+                                           : 0xff80ff80u;
+                            }
+                        }
+                        reinterpret_cast<uint4*>(o)[u] = make_uint4(h[0], h[1], h[2], h[3]);
+                    }
+                }
+            }
+            i = v1 * E;
         }
-        if (a.out) {
-            unsigned char* o = static_cast<unsigned char*>(a.out) + row * a.out_stride * ES;
-            each([&](float l, int64_t id) {
-                const uint32_t b = bad || keep(l, id) ? __float_as_uint(l) : 0xff800000u;
+        for (i += tid; i < s1; i += kNT) {
+            const float l = scalar_entry<ES>(base, i);
+            if (p)
+                p[i] = prob(l, i);
+            if (o) {
+                const uint32_t h = logit(l, i);
                 if constexpr (ES == 4)
-                    reinterpret_cast<uint32_t*>(o)[id] = b;
+                    reinterpret_cast<uint32_t*>(o)[i] = h;
                 else
-                    reinterpret_cast<unsigned short*>(o)[id] = (unsigned short)(b >> 16);
-            });
+                    reinterpret_cast<unsigned short*>(o)[i] = (unsigned short)(h >> 16);
+            }
         }
     }
 
-    __device__ void finish(int code, uint32_t kept, float mass, float p) {
+    // ------------------------------------------------ bfloat16 by value -----
+
+    __device__ __forceinline__ static float place_value(int D) {
+        const int s = kMags + 1 - D, i = s >= 0 ? s : -1 - s;
+        const uint32_t b = i ? (uint32_t)(kMag0 - 1 + i) : 0u;
+        return __uint_as_float((b | (s < 0 ? 0x8000u : 0u)) << 16);
+    }
+
+    // Counts two logits; `most` keeps the largest magnitudes seen.  Each place's
+    // byte offset is 4 i or 4 (-1 - i), both logits' in the halves of one word.
+    // Logits above -127 alone are counted: what is missing lies below.
+    __device__ __forceinline__ void count_pair(uint32_t x, uint32_t& most) {
+        constexpr uint32_t lo = (kMag0 - 1) * 0x10001u, hi = (kMag0 + kMags) * 0x10001u;
+        constexpr int far = 4 * (-1 - (kMags + 1));
+        uint32_t m = x & 0x7fff7fffu, sign, i;
+        asm("max.u16x2 %0, %1, %2;" : "=r"(most) : "r"(most), "r"(m));
+        asm("max.u16x2 %0, %1, %2;" : "=r"(i) : "r"(m), "r"(lo));
+        asm("min.u16x2 %0, %1, %2;" : "=r"(i) : "r"(i), "r"(hi));
+        asm("prmt.b32 %0, %1, %2, %3;" : "=r"(sign) : "r"(x), "r"(0u), "r"(0xbb99u));  // sign of each half
+        const uint32_t o = (((i - lo) << 2) ^ sign) & 0xfffcfffcu;
+        const int o0 = (int)(short)(o & 0xffffu), o1 = (int)o >> 16;
+        char* zero = reinterpret_cast<char*>(sh.count + kMags + 2);
+        if (o0 != far)
+            atomicAdd(reinterpret_cast<uint32_t*>(zero + o0), 1u);
+        if (o1 != far)
+            atomicAdd(reinterpret_cast<uint32_t*>(zero + o1), 1u);
+    }
+
+    // entries at place D, over the cluster
+    __device__ __forceinline__ uint32_t place_count(int D) const {
+        uint32_t n = 0;
+        for (int r = 0; r < C; ++r)
+            n += cluster.map_shared_rank(sh.count, r)[kPlaces - 1 - D];
+        return n;
+    }
+
+    struct Wanted {
+        uint32_t k;            // count to reach, 0: none
+        unsigned long long p;  // mass to reach, 0: none; with `draw` a mass to exceed
+        int limit;             // the last place min-p keeps, kNoPlace: none
+        bool draw;
+    };
+
+    // Finds the places where the conditions end, in every CTA's `found`.  The
+    // thread whose chunk of places holds one hands it to a warp, which goes through
+    // the chunk; m, n: the chunk's sums, before_m, before_n: what lies above it.
+    __device__ void search_places(const Wanted& s, int chunk, unsigned long long m, uint32_t n,
+                                  unsigned long long before_m, uint32_t before_n) {
+        __syncthreads();  // every thread has read `found`
+        if (tid < kConds) {
+            sh.hit[tid].chunk = -1;
+            sh.found[tid].bin = kNoPlace;
+        }
+        cluster.sync();
+        const auto hit = [&](int c) {
+            sh.hit[c].chunk = chunk;
+            sh.hit[c].above_mass = before_m;
+            sh.hit[c].above_count = before_n;
+        };
+        if (chunk >= 0) {
+            if (s.k && before_n < s.k && before_n + n >= s.k)
+                hit(kByCount);
+            if (s.draw ? before_m <= s.p && before_m + m > s.p
+                       : s.p && before_m < s.p && before_m + m >= s.p)
+                hit(kByMass);
+            if (s.limit / 32 == chunk)
+                hit(kByLimit);
+        }
+        __syncthreads();
+        if (warp < kConds && sh.hit[warp].chunk >= 0) {
+            const int D = sh.hit[warp].chunk * 32 + lane;
+            Found f;
+            f.bin = D;
+            f.count = place_count(D);
+            f.mass = f.count ? f.count * weight_fixed(scale, sh.pow2, place_value(D)) : 0;
+            unsigned long long im = f.mass;
+            uint32_t in = f.count;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned long long pm = __shfl_up_sync(kAllLanes, im, o);
+                const uint32_t pn = __shfl_up_sync(kAllLanes, in, o);
+                if (lane >= o) {
+                    im += pm;
+                    in += pn;
+                }
+            }
+            f.above_mass = sh.hit[warp].above_mass + im - f.mass;
+            f.above_count = sh.hit[warp].above_count + in - f.count;
+            const unsigned long long em = f.above_mass + f.mass;
+            const uint32_t en = f.above_count + f.count;
+            const bool here = warp == kByCount ? f.above_count < s.k && en >= s.k
+                              : warp == kByLimit ? D == s.limit
+                              : s.draw ? f.above_mass <= s.p && em > s.p
+                                       : f.above_mass < s.p && em >= s.p;
+            if (here)
+                tell(warp, f);
+        }
+        cluster.sync();
+    }
+
+    // which of the eight logits from group g of the slice equal the bits `two` holds twice
+    __device__ __forceinline__ uint32_t matches(int64_t g, uint32_t two) const {
+        const int64_t e = s0 + g * 8;
+        uint32_t mask = 0;
+        if (a.vec && e + 8 <= s1) {
+            const uint4 w = load_stream(reinterpret_cast<const uint4*>(base) + e / 8);
+            const uint32_t x[4] = {w.x ^ two, w.y ^ two, w.z ^ two, w.w ^ two};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                mask |= (((x[j] & 0xffffu) == 0) | ((x[j] >> 16) == 0) << 1) << (2 * j);
+        } else {
+            const unsigned short* q = reinterpret_cast<const unsigned short*>(base);
+            for (int j = 0; j < 8; ++j)
+                if (e + j < s1)
+                    mask |= (uint32_t)(q[e + j] == (two & 0xffffu)) << j;
+        }
+        return mask;
+    }
+
+    // The entry number r by ascending id at place D; the CTA that holds it returns
+    // its id in one thread, every other thread returns -1.
+    __device__ int64_t find(int D, unsigned long long r) {
+        uint32_t n = 0, in;
+        if (lane < C)
+            n = cluster.map_shared_rank(sh.count, lane)[kPlaces - 1 - D];
+        in = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t p = __shfl_up_sync(kAllLanes, in, o);
+            if (lane >= o)
+                in += p;
+        }
+        const uint32_t owners = __ballot_sync(kAllLanes, r >= in - n && r < in);
+        if (!owners || __ffs(owners) - 1 != rank)
+            return -1;
+        uint32_t left = (uint32_t)(r - __shfl_sync(kAllLanes, in - n, rank));
+        const uint32_t bits = __float_as_uint(place_value(D)) >> 16, two = bits * 0x10001u;
+        // a stretch of the slice per warp
+        const int64_t groups = (s1 - s0 + 7) / 8, per = (groups + kNW - 1) / kNW;
+        const int64_t g0 = warp * per, g1 = g0 + per < groups ? g0 + per : groups;
+        uint32_t mine = 0;
+        for (int64_t g = g0 + lane; g < g1; g += 32)
+            mine += __popc(matches(g, two));
+        mine = __reduce_add_sync(kAllLanes, mine);
+        __syncthreads();
+        if (lane == 0)
+            sh.warp_cnt[warp] = mine;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) {
+            if (left < sh.warp_cnt[w])
+                return -1;
+            left -= sh.warp_cnt[w];
+        }
+        if (left >= mine)
+            return -1;
+        for (int64_t g = g0; g < g1; g += 32) {
+            const uint32_t mask = g + lane < g1 ? matches(g + lane, two) : 0;
+            uint32_t c = __popc(mask), ic = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t p = __shfl_up_sync(kAllLanes, ic, o);
+                if (lane >= o)
+                    ic += p;
+            }
+            const uint32_t all = __shfl_sync(kAllLanes, ic, 31);
+            if (left < all) {
+                if (left >= ic - c && left < ic)
+                    return s0 + (g + lane) * 8 + __fns(mask, 0, left - (ic - c) + 1);
+                return -1;
+            }
+            left -= all;
+        }
+        return -1;
+    }
+
+    // The whole call for a bfloat16 row whose answer does not depend on logits
+    // outside the window; false (in every CTA) for the others.
+    __device__ bool by_value(float T, int32_t top_k, double top_p, double min_p, float u) {
+        for (int i = tid; i < kPlaces; i += kNT)
+            sh.count[i] = 0;
+        __syncthreads();
+        uint32_t most = 0;
+        {
+            int64_t i = s0;
+            constexpr int L = 4;
+            if (a.vec) {
+                const int64_t v1 = s1 / 8;
+                const uint4* p = reinterpret_cast<const uint4*>(base);
+                for (int64_t v = s0 / 8 + tid; v < v1; v += L * kNT) {
+                    uint4 w[L];
+#pragma unroll
+                    for (int k = 0; k < L; ++k)
+                        if (v + k * kNT < v1)
+                            w[k] = load_stream(p + v + k * kNT);
+#pragma unroll
+                    for (int k = 0; k < L; ++k)
+                        if (v + k * kNT < v1) {
+                            count_pair(w[k].x, most);
+                            count_pair(w[k].y, most);
+                            count_pair(w[k].z, most);
+                            count_pair(w[k].w, most);
+                        }
+                }
+                i = v1 * 8;
+            }
+            // a lone logit, paired with -inf, which is not counted
+            for (i += tid; i < s1; i += kNT) {
+                uint32_t m = 0;
+                count_pair(reinterpret_cast<const unsigned short*>(base)[i] | 0xff800000u, m);
+                m &= 0xffffu;
+                most = most > m ? most : m;
+            }
+        }
+        most = max(most & 0xffffu, most >> 16);
+        __syncthreads();
+        // the highest place taken here; kPlaces: a NaN
+        int top = -1;
+        for (int i = tid; i < kPlaces; i += kNT)
+            if (sh.count[i])
+                top = i;
+        if (most > 0x7f80u)
+            top = kPlaces;
+        top = __reduce_max_sync(kAllLanes, top);
+        if (lane == 0)
+            sh.warp_max[warp] = (uint32_t)(top + 1);
+        __syncthreads();
+        for (int w = 0; w < kNW; ++w)
+            top = max(top, (int)sh.warp_max[w] - 1);
+        meet();
+        if (tid < C)
+            *cluster.map_shared_rank(&sh.part_max[rank], tid) = (uint32_t)(top + 1);
+        cluster.sync();
+        for (int r = 0; r < C; ++r)
+            top = max(top, (int)sh.part_max[r] - 1);
+        const int D0 = kPlaces - 1 - top;  // by descending logit
+        if (top < 0 || D0 <= 0 || D0 == kFirstTiny || D0 == kFirstTiny + 1)
+            return false;
+        scale.lmax = place_value(D0);
+        if (T == 0.0f) {
+            const int64_t id = find(D0, 0);
+            if (id >= 0) {
+                a_token(id, 1.0f);
+                for (int r = 0; r < C; ++r)
+                    *cluster.map_shared_rank(&sh.token, r) = (uint32_t)id;
+            }
+            cluster.sync();
+            const uint32_t token = sh.token;
+            write([=](float, int64_t i) { return (uint32_t)i == token; }, scale.lmax, 0.0f, false);
+            finish(SV_OK, 1, 1.0f);
+            return true;
+        }
+        split_scale(T, scale.ch, scale.cl);
+        // logits from -127 down must weigh nothing
+        if (!((scale.lmax + 127.0f) * scale.ch >= 61.0f))
+            return false;
+
+        // sums of each chunk of places, a chunk per warp
+        const int per = (kChunks + C - 1) / C;
+        const int c0 = min(rank * per, kChunks), c1 = min(c0 + per, kChunks);
+        for (int c = c0 + warp; c < c1; c += kNW) {
+            const int D = c * 32 + lane;
+            uint32_t n = place_count(D);
+            unsigned long long m = 0;
+            if (__any_sync(kAllLanes, n)) {
+                if (n)
+                    m = n * weight_fixed(scale, sh.pow2, place_value(D));
+                n = __reduce_add_sync(kAllLanes, n);
+#pragma unroll
+                for (int o = 16; o; o >>= 1)
+                    m += __shfl_xor_sync(kAllLanes, m, o);
+            }
+            if (lane == 0) {
+                sh.chunk_mass[c - c0] = m;
+                sh.chunk_cnt[c - c0] = n;
+            }
+        }
+        __syncthreads();
+        static_assert(kChunks <= kNT, "a thread per chunk");
+        const bool has = tid < c1 - c0;
+        const unsigned long long m = has ? sh.chunk_mass[tid] : 0;
+        const uint32_t n = has ? sh.chunk_cnt[tid] : 0;
+        unsigned long long tm = m, before_m, whole = 0;
+        uint32_t tn = n, before_n, near = 0;
+        scan(tm, tn, before_m, before_n);
+        if (tid < C) {
+            *cluster.map_shared_rank(&sh.part_mass[rank], tid) = tm;
+            *cluster.map_shared_rank(&sh.part_cnt[rank], tid) = tn;
+        }
+        cluster.sync();
+        for (int r = 0; r < C; ++r) {
+            if (r < rank) {
+                before_m += sh.part_mass[r];
+                before_n += sh.part_cnt[r];
+            }
+            whole += sh.part_mass[r];
+            near += sh.part_cnt[r];
+        }
+        const int chunk = has ? c0 + tid : -1;
+
+        // the cut
+        Wanted s;
+        s.k = top_k > 0 ? (uint32_t)top_k : 0;
+        s.p = top_p < 1.0 ? ceil_scaled(top_p, whole) : 0;
+        s.limit = kNoPlace;
+        s.draw = false;
+        if (min_p > 0.0) {
+            // the smallest bfloat16 l with l - l_max >= T ln(min_p)
+            const float limit = __double2float_ru((double)scale.lmax + (double)T * log(min_p));
+            const uint32_t b = __float_as_uint(limit + 0.0f);
+            const int sign = b >> 31;
+            const int mag = (int)((b & 0x7fffffffu) >> 16) + (!sign && (b & 0xffffu));
+            if (mag < kMag0 || mag >= kMag0 + kMags)
+                return false;
+            const int i = mag - kMag0 + 1;
+            s.limit = kMags + 1 - (sign ? -1 - i : i);
+        }
+        Found f;
+        f.bin = kNoPlace;
+        if (s.k || s.p || s.limit < kNoPlace) {
+            search_places(s, chunk, m, n, before_m, before_n);
+            f = first();
+        }
+        unsigned long long E = whole;
+        int64_t kept = near;
+        float cut = -3.402823466e38f;
+        if (f.bin < kNoPlace) {
+            if (f.bin == kFirstTiny || f.bin == kFirstTiny + 1)
+                return false;
+            E = f.above_mass + f.mass;
+            kept = f.above_count + f.count;
+            cut = place_value(f.bin);
+        } else if ((uint64_t)near < (uint64_t)a.V) {
+            // everything is kept: those from -127 down that are not -inf as well
+            if (s.k)
+                return false;
+            uint32_t more = 0;
+            each([&](float l, int64_t) { more += l <= -127.0f && l > __int_as_float(0xff800000); });
+            more = __reduce_add_sync(kAllLanes, more);
+            __syncthreads();
+            if (lane == 0)
+                sh.warp_cnt[warp] = more;
+            __syncthreads();
+            more = 0;
+            for (int w = 0; w < kNW; ++w)
+                more += sh.warp_cnt[w];
+            cluster.sync();
+            if (tid < C)
+                *cluster.map_shared_rank(&sh.part_cnt[rank], tid) = more;
+            cluster.sync();
+            for (int r = 0; r < C; ++r)
+                kept += sh.part_cnt[r];
+        }
+
+        // the draw
+        const float inv = (float)((double)(1ull << scale.fix) / (double)E);
+        if (a.u) {
+            s.k = 0;
+            s.limit = kNoPlace;
+            s.draw = true;
+            s.p = floor_scaled(u, E);
+            search_places(s, chunk, m, n, before_m, before_n);
+            const Found d = first();
+            if (d.bin == kFirstTiny || d.bin == kFirstTiny + 1)
+                return false;
+            const float l = place_value(d.bin);
+            const int64_t id = find(d.bin, (s.p - d.above_mass) / weight_fixed(scale, sh.pow2, l));
+            if (id >= 0)
+                a_token(id, weight_float(scale, l) * inv);
+        }
+        write([&](float l, int64_t) { return l >= cut; }, cut, inv, false);
+        finish(SV_OK, (uint32_t)kept, (float)((double)E / (double)whole));
+        return true;
+    }
+
+    // the first use of another CTA's memory waits until every CTA runs
+    bool met = false;
+    __device__ void meet() {
+        if (!met)
+            cluster.barrier_wait();
+        met = true;
+    }
+
+    __device__ void a_token(int64_t id, float p) {
+        if (a.tokens)
+            a.tokens[row * a.token_stride] = (int32_t)id;
+        if (a.p_token)
+            a.p_token[row] = p;
+    }
+
+    __device__ void finish(int code, uint32_t kept, float mass) {
         if (rank == 0 && tid == 0) {
-            if (a.tokens)
-                a.tokens[row * a.token_stride] = code ? -1 : (int32_t)sh.token;
-            const float nan = __int_as_float(0x7fffffff);
-            if (a.p_token)
-                a.p_token[row] = code ? nan : p;
             if (a.mass)
-                a.mass[row] = code ? nan : mass;
+                a.mass[row] = mass;
             if (a.kept)
-                a.kept[row] = code ? 0 : (int32_t)kept;
+                a.kept[row] = (int32_t)kept;
             if (a.status)
                 a.status[row] = code;
             if (code)
@@ -585,6 +1052,11 @@ struct Kernel {
             sh.pow2[tid] = kPow2Steps[tid];
 
         cluster.barrier_arrive();
+        if constexpr (ES == 2)
+            if (!code && by_value(T, top_k, top_p, min_p, u)) {
+                cluster.sync();  // no CTA leaves while another may still read its memory
+                return;
+            }
 
         // A. the largest logit (NaN if there is one), over the cluster
         float m = __int_as_float(0xff800000);
@@ -597,7 +1069,7 @@ struct Kernel {
         __syncthreads();
         for (int w = 0; w < kNW; ++w)
             m = max_nan(m, __uint_as_float(sh.warp_max[w]));
-        cluster.barrier_wait();  // every CTA of the cluster runs: its memory may be written
+        meet();
         if (tid < C)
             *cluster.map_shared_rank(&sh.part_max[rank], tid) = __float_as_uint(m);
         cluster.sync();
@@ -607,8 +1079,11 @@ struct Kernel {
             code = SV_ERR_NONFINITE;
         scale.lmax = m;
         if (code) {
-            write([](float, int64_t) { return false; }, 0.0f, true);
-            finish(code, 0, 0.0f, 0.0f);
+            const float nan = __int_as_float(0x7fffffff);
+            write([](float, int64_t) { return false; }, 0.0f, 0.0f, true);
+            if (rank == 0 && tid == 0)
+                a_token(-1, nan);
+            finish(code, 0, nan);
             cluster.sync();
             return;
         }
@@ -630,10 +1105,10 @@ struct Kernel {
             cluster.sync();
             for (int r = 0; r < C; ++r)
                 id = min(id, sh.part_cnt[r]);
-            if (tid == 0)
-                sh.token = id;
-            write([=](float, int64_t i) { return (uint32_t)i == id; }, 0.0f, false);
-            finish(SV_OK, 1, 1.0f, 1.0f);
+            write([=](float, int64_t i) { return (uint32_t)i == id; }, m, 0.0f, false);
+            if (rank == 0 && tid == 0)
+                a_token(id, 1.0f);
+            finish(SV_OK, 1, 1.0f);
             cluster.sync();
             return;
         }
@@ -687,7 +1162,6 @@ struct Kernel {
         }
 
         // C. the draw
-        float p = 0.0f;
         const float inv = (float)((double)(1ull << scale.fix) / (double)E);
         if (a.u) {
             const unsigned long long target = floor_scaled(u, E);
@@ -725,17 +1199,18 @@ struct Kernel {
                 }
             }
             if (rank == 0 && tid == 0)
-                p = weight_float(scale, key_logit(sh.token_key)) * inv;
+                a_token(sh.token, weight_float(scale, key_logit(sh.token_key)) * inv);
         }
         // D. rows out
-        write([&](float l, int64_t) { return logit_key(l) >= cut_key; }, inv, false);
-        finish(SV_OK, kept, (float)((double)E / (double)whole), p);
+        const float cut = key_logit(cut_key);
+        write([&](float l, int64_t) { return l >= cut; }, cut, inv, false);
+        finish(SV_OK, kept, (float)((double)E / (double)whole));
         cluster.sync();  // no CTA leaves while another may still write into it
     }
 };
 
 template <int ES>
-__global__ void __launch_bounds__(kNT, 2) sv_sample_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kNT, 4) sv_sample_kernel(const __grid_constant__ Args a) {
     __shared__ Shared sh;
     Kernel<ES> k(a, sh);
     k.run();
@@ -754,6 +1229,10 @@ int launch(sv_ctx* ctx, Args& a, int B, int rows, int64_t V, int dtype, cudaStre
     a.rows_per_seq = rows;
     a.fix = weight_bits(V);
     a.vec = aligned(a.logits, 16) && (a.stride * es) % 16 == 0 ? 1 : 0;
+    a.out_vec = (!a.probs || (aligned(a.probs, 16) && a.probs_stride % 4 == 0)) &&
+                        (!a.out || (aligned(a.out, 16) && (a.out_stride * es) % 16 == 0))
+                    ? 1
+                    : 0;
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof cfg);
     cfg.gridDim = dim3((unsigned)plan.grid, 1, 1);

@@ -47,7 +47,7 @@ int plan_rows(int num_sms, int max_cluster, int B, int rows_per_seq, int64_t V, 
 
 extern "C" int spec_sample_plan_for(int num_sms, int max_cluster, int B, int rows_per_seq,
                                     int64_t V, int logits_dtype, int ovr_cluster, sv_plan* out) {
-    return plan_rows(num_sms, max_cluster, B, rows_per_seq, V, logits_dtype, ovr_cluster, 512, 2,
+    return plan_rows(num_sms, max_cluster, B, rows_per_seq, V, logits_dtype, ovr_cluster, 256, 4,
                      2048, out);
 }
 
