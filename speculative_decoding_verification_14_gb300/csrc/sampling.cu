@@ -79,7 +79,8 @@ struct Found {
     unsigned long long mass, above_mass;
 };
 
-// bfloat16 rows are counted value by value: a place for every magnitude from
+// Rows are counted by the upper 16 bits of their logits, which are a bfloat16
+// logit's value and a float32 logit's to 2^-8: a place for every magnitude from
 // 2^-25 up to 127 of either sign, and one each for what is smaller and larger.
 // A place i is 0 below the window, 1..kMags inside it and kMags + 1 above; its
 // signed index is i, or -1 - i for negative logits, so that it grows with the
@@ -110,12 +111,14 @@ struct Shared {
     unsigned long long part_mass[kMaxC];
     uint32_t part_cnt[kMaxC];
     uint32_t part_max[kMaxC];
-    uint32_t part_flag[kMaxC];
+    uint32_t part_key[kMaxC];
     unsigned long long warp_mass[kNW];
     uint32_t warp_cnt[kNW];
     uint32_t warp_max[kNW];
     Found found[kConds];
-    uint32_t list_n;
+    uint32_t list_n[2];
+    unsigned long long sums[3][kMaxC];
+    uint32_t ok;
     // what the first CTA (or the CTA that finds it) tells the others
     uint32_t cut_key;
     uint32_t kept;
@@ -190,7 +193,7 @@ struct Kernel {
         if (tid < kConds)
             sh.found[tid].bin = kBins;
         if (tid == 0)
-            sh.list_n = 0;
+            sh.list_n[0] = 0;
         __syncthreads();
         each([&](float l, int64_t) {
             const int b = map(l);
@@ -389,140 +392,161 @@ struct Kernel {
         }
     }
 
+    // The lists lie over the bins and places, which are done with when they are made.
+    __device__ __forceinline__ unsigned long long* list_at(int which) const {
+        return which ? reinterpret_cast<unsigned long long*>(sh.lo) : sh.list;
+    }
+
+    __device__ __forceinline__ void offer(uint32_t* n, unsigned long long* list, float l, int64_t id) const {
+        const uint32_t at = atomicAdd(n, 1u);
+        if (at < (uint32_t)kList)
+            list[at] = ((unsigned long long)logit_key(l) << 32) | (uint32_t)~(uint32_t)id;
+    }
+
+    // Sorts a list of this CTA: descending logits, ascending ids.
+    __device__ void sort(int which) {
+        unsigned long long* list = list_at(which);
+        if (tid == 0 && sh.list_n[which] > (uint32_t)kList)
+            sh.list_n[which] = kList;
+        __syncthreads();
+        const int n = (int)sh.list_n[which];
+        int size = 2;
+        while (size < n)
+            size <<= 1;
+        for (int i = n + tid; i < size; i += kNT)
+            list[i] = 0;
+        __syncthreads();
+        for (int len = 2; len <= size; len <<= 1)
+            for (int gap = len >> 1; gap; gap >>= 1) {
+                for (int i = tid; i < size / 2; i += kNT) {
+                    const int x = 2 * i - (i & (gap - 1)), y = x + gap;
+                    const unsigned long long vx = list[x], vy = list[y];
+                    if ((vx < vy) == ((x & len) == 0)) {  // descending runs first
+                        list[x] = vy;
+                        list[y] = vx;
+                    }
+                }
+                __syncthreads();
+            }
+    }
+
     // Entries with klo <= key <= khi into the first CTA's list, sorted there.
     __device__ void gather(uint32_t klo, uint32_t khi) {
-        cluster.sync();  // everyone has read `found`; list_n is zero since the histogram
+        cluster.sync();  // everyone has read `found`
         if (rank == 0 && tid == 0)
-            sh.list_n = 0;
+            sh.list_n[0] = 0;
         cluster.sync();
-        uint32_t* n = cluster.map_shared_rank(&sh.list_n, 0);
+        uint32_t* n = cluster.map_shared_rank(&sh.list_n[0], 0);
         unsigned long long* list = cluster.map_shared_rank(sh.list, 0);
         each([&](float l, int64_t id) {
             const uint32_t k = logit_key(l);
-            if (k >= klo && k <= khi) {
-                const uint32_t at = atomicAdd(n, 1u);
-                if (at < (uint32_t)kList)
-                    list[at] = ((unsigned long long)k << 32) | (uint32_t)~(uint32_t)id;
-            }
+            if (k >= klo && k <= khi)
+                offer(n, list, l, id);
         });
         cluster.sync();
-        if (rank == 0) {
-            if (tid == 0 && sh.list_n > (uint32_t)kList)
-                sh.list_n = kList;
-            __syncthreads();
-            int size = 2;
-            while (size < (int)sh.list_n)
-                size <<= 1;
-            for (int i = (int)sh.list_n + tid; i < size; i += kNT)
-                sh.list[i] = 0;
-            __syncthreads();
-            for (int len = 2; len <= size; len <<= 1)
-                for (int gap = len >> 1; gap; gap >>= 1) {
-                    for (int i = tid; i < size / 2; i += kNT) {
-                        const int x = 2 * i - (i & (gap - 1)), y = x + gap;
-                        const unsigned long long vx = sh.list[x], vy = sh.list[y];
-                        if ((vx < vy) == ((x & len) == 0)) {  // descending runs first
-                            sh.list[x] = vy;
-                            sh.list[y] = vx;
-                        }
-                    }
-                    __syncthreads();
-                }
-        }
+        if (rank == 0)
+            sort(0);
     }
 
-    // weights of this thread's entries of the list, and what lies before them
-    __device__ void list_scan(unsigned long long w[kOwn], unsigned long long& before) {
+    // weights of this thread's entries of a list, what lies before them and in all
+    __device__ void list_scan(int which, unsigned long long w[kOwn], unsigned long long& before,
+                              unsigned long long& total) {
         unsigned long long m = 0, bm;
         uint32_t n = 0, bn;
         for (int j = 0; j < kOwn; ++j) {
             const int i = kOwn * tid + j;
-            w[j] = i < (int)sh.list_n
-                       ? weight_fixed(scale, sh.pow2, key_logit((uint32_t)(sh.list[i] >> 32)))
+            w[j] = i < (int)sh.list_n[which]
+                       ? weight_fixed(scale, sh.pow2, key_logit((uint32_t)(list_at(which)[i] >> 32)))
                        : 0;
             m += w[j];
         }
         scan(m, n, bm, bn);
         before = bm;
+        total = m;
     }
 
-    // The last group of equal logits in the list that every filter keeps; the
-    // first CTA tells the cut, the kept mass and count.
-    __device__ void cut_in_list(const Search& s, const Found& f, uint32_t limit_key) {
-        if (rank == 0) {
-            const int n = (int)sh.list_n;
-            unsigned long long w[kOwn], before;
-            list_scan(w, before);
-            unsigned long long at = f.above_mass + before;
-            int last = -1;
-            for (int j = 0; j < kOwn; ++j) {
-                const int i = kOwn * tid + j;
-                if (i < n) {
-                    const uint32_t k = (uint32_t)(sh.list[i] >> 32);
-                    const bool start = i == 0 || (uint32_t)(sh.list[i - 1] >> 32) != k;
-                    if (start && k >= limit_key && (!s.k || f.above_count + i < s.k) &&
-                        (s.top_p >= 1.0 || at < s.p))
-                        last = i;
-                }
-                at += w[j];
+    // The last group of equal logits in the first list that every filter keeps
+    // (first CTA): the cut, the kept mass and count.  Returns whether the cut lies in
+    // the list: some filter ends with it, `low` being the lowest key it covers.
+    __device__ bool cut_in_list(const Search& s, const Found& f, uint32_t limit_key, uint32_t low) {
+        const int n = (int)sh.list_n[0];
+        unsigned long long w[kOwn], before, total;
+        list_scan(0, w, before, total);
+        unsigned long long at = f.above_mass + before;
+        int last = -1;
+        for (int j = 0; j < kOwn; ++j) {
+            const int i = kOwn * tid + j;
+            if (i < n) {
+                const uint32_t k = (uint32_t)(sh.list[i] >> 32);
+                const bool start = i == 0 || (uint32_t)(sh.list[i - 1] >> 32) != k;
+                if (start && k >= limit_key && (!s.k || f.above_count + i < s.k) &&
+                    (s.top_p >= 1.0 || at < s.p))
+                    last = i;
             }
-            // conditions fail for good once they fail: the last start over all threads
-            for (int o = 16; o; o >>= 1) {
-                const int x = __shfl_xor_sync(kAllLanes, last, o);
-                last = x > last ? x : last;
-            }
-            __syncthreads();
-            if (lane == 0)
-                sh.warp_max[warp] = (uint32_t)(last + 1);
-            __syncthreads();
-            int g = 0;
-            for (int i = 0; i < kNW; ++i)
-                g = (int)sh.warp_max[i] > g ? (int)sh.warp_max[i] : g;
-            --g;  // -1: nothing of the list is kept
-            const uint32_t key = g >= 0 ? (uint32_t)(sh.list[g] >> 32) : limit_key;
-            unsigned long long at2 = f.above_mass + before;
-            if (tid == 0 && (g < 0 || n == 0)) {
+            at += w[j];
+        }
+        // conditions fail for good once they fail: the last start over all threads
+        last = __reduce_max_sync(kAllLanes, last);
+        __syncthreads();
+        if (lane == 0)
+            sh.warp_max[warp] = (uint32_t)(last + 1);
+        __syncthreads();
+        int g = 0;
+        for (int i = 0; i < kNW; ++i)
+            g = (int)sh.warp_max[i] > g ? (int)sh.warp_max[i] : g;
+        --g;  // -1: nothing of the list is kept
+        const uint32_t key = g >= 0 ? (uint32_t)(sh.list[g] >> 32) : limit_key;
+        unsigned long long at2 = f.above_mass + before;
+        if (tid == 0 && g < 0) {
+            sh.cut_key = key;
+            sh.kept = f.above_count;
+            sh.kept_mass = f.above_mass;
+        }
+        for (int j = 0; j < kOwn; ++j) {
+            const int i = kOwn * tid + j;
+            at2 += w[j];
+            if (g >= 0 && i < n && (uint32_t)(sh.list[i] >> 32) == key &&
+                (i == n - 1 || (uint32_t)(sh.list[i + 1] >> 32) != key)) {
                 sh.cut_key = key;
-                sh.kept = f.above_count;
-                sh.kept_mass = f.above_mass;
+                sh.kept = f.above_count + i + 1;
+                sh.kept_mass = at2;
             }
-            for (int j = 0; j < kOwn; ++j) {
-                const int i = kOwn * tid + j;
-                at2 += w[j];
-                if (g >= 0 && i < n && (uint32_t)(sh.list[i] >> 32) == key &&
-                    (i == n - 1 || (uint32_t)(sh.list[i + 1] >> 32) != key)) {
-                    sh.cut_key = key;
-                    sh.kept = f.above_count + i + 1;
-                    sh.kept_mass = at2;
-                }
-            }
-            __syncthreads();
-            if (tid > 0 && tid < C) {
-                *cluster.map_shared_rank(&sh.cut_key, tid) = sh.cut_key;
-                *cluster.map_shared_rank(&sh.kept, tid) = sh.kept;
-                *cluster.map_shared_rank(&sh.kept_mass, tid) = sh.kept_mass;
-            }
+        }
+        __syncthreads();
+        if ((s.k && f.above_count >= s.k) || (s.top_p < 1.0 && f.above_mass >= s.p))
+            return false;
+        return limit_key >= low || (s.k && f.above_count + (uint32_t)n >= s.k) ||
+               (s.top_p < 1.0 && f.above_mass + total >= s.p);
+    }
+
+    // what the first CTA has found, to the others
+    __device__ void share_cut() {
+        if (rank == 0 && tid > 0 && tid < C) {
+            *cluster.map_shared_rank(&sh.cut_key, tid) = sh.cut_key;
+            *cluster.map_shared_rank(&sh.kept, tid) = sh.kept;
+            *cluster.map_shared_rank(&sh.kept_mass, tid) = sh.kept_mass;
+            *cluster.map_shared_rank(&sh.ok, tid) = sh.ok;
         }
         cluster.sync();
     }
 
-    // The first entry of the list whose running sum exceeds `target`.
-    __device__ void draw_in_list(unsigned long long above_mass, unsigned long long target) {
-        if (rank == 0) {
-            const int n = (int)sh.list_n;
-            unsigned long long w[kOwn], at;
-            list_scan(w, at);
-            at += above_mass;
-            for (int j = 0; j < kOwn; ++j) {
-                const int i = kOwn * tid + j;
-                if (i < n && at <= target && at + w[j] > target) {
-                    sh.token = ~(uint32_t)sh.list[i];
-                    sh.token_key = (uint32_t)(sh.list[i] >> 32);
-                }
-                at += w[j];
+    // The first entry of a list whose running sum exceeds `target` (first CTA);
+    // whether the list holds it.
+    __device__ bool draw_in_list(int which, unsigned long long above_mass, unsigned long long target) {
+        const int n = (int)sh.list_n[which];
+        unsigned long long w[kOwn], at, total;
+        list_scan(which, w, at, total);
+        at += above_mass;
+        for (int j = 0; j < kOwn; ++j) {
+            const int i = kOwn * tid + j;
+            if (i < n && at <= target && at + w[j] > target) {
+                sh.token = ~(uint32_t)list_at(which)[i];
+                sh.token_key = (uint32_t)(list_at(which)[i] >> 32);
             }
-            __syncthreads();
+            at += w[j];
         }
+        __syncthreads();
+        return above_mass <= target && above_mass + total > target;
     }
 
     // The entry number r, by ascending id, among those with this key.
@@ -633,12 +657,27 @@ struct Kernel {
         }
     }
 
-    // ------------------------------------------------ bfloat16 by value -----
+    // -------------------------------------------------------- by places -----
 
+    // the logit of least magnitude at place D (bfloat16: the only one)
     __device__ __forceinline__ static float place_value(int D) {
         const int s = kMags + 1 - D, i = s >= 0 ? s : -1 - s;
         const uint32_t b = i ? (uint32_t)(kMag0 - 1 + i) : 0u;
         return __uint_as_float((b | (s < 0 ? 0x8000u : 0u)) << 16);
+    }
+
+    // a float32 place's largest or smallest logit; inside the window
+    __device__ __forceinline__ static float place_end(int D, bool largest) {
+        const float l = place_value(D);
+        return largest == (l > 0.0f) ? __uint_as_float(__float_as_uint(l) | 0xffffu) : l;
+    }
+
+    // weight of the logits at place D: bfloat16 exactly, float32 by its middle
+    __device__ __forceinline__ unsigned long long place_weight(int D) const {
+        float l = place_value(D);
+        if constexpr (ES == 4)
+            l = fminf(__uint_as_float(__float_as_uint(l) | 0x8000u), scale.lmax);
+        return weight_fixed(scale, sh.pow2, l);
     }
 
     // Counts two logits; `most` keeps the largest magnitudes seen.  Each place's
@@ -707,7 +746,7 @@ struct Kernel {
             Found f;
             f.bin = D;
             f.count = place_count(D);
-            f.mass = f.count ? f.count * weight_fixed(scale, sh.pow2, place_value(D)) : 0;
+            f.mass = f.count ? f.count * place_weight(D) : 0;
             unsigned long long im = f.mass;
             uint32_t in = f.count;
 #pragma unroll
@@ -808,20 +847,91 @@ struct Kernel {
         return -1;
     }
 
-    // The whole call for a bfloat16 row whose answer does not depend on logits
-    // outside the window; false (in every CTA) for the others.
-    __device__ bool by_value(float T, int32_t top_k, double top_p, double min_p, float u) {
+    // A stretch of places around one of interest, as far as the list holds its
+    // entries: lane r looks at r places to either side.
+    struct Band {
+        bool on, from_top;
+        float lo, hi;          // its logits
+        uint32_t above_count;  // entries above it
+    };
+    __device__ Band band_around(const Found& f) const {
+        Band b;
+        const int D = f.bin - 16 + lane;
+        const uint32_t n = D >= 1 && D <= kPlaces - 2 ? place_count(D) : 0;
+        uint32_t in = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t p = __shfl_up_sync(kAllLanes, in, o);
+            if (lane >= o)
+                in += p;
+        }
+        const int r = lane & 15;
+        const uint32_t upto = __shfl_sync(kAllLanes, in, 16 + r);
+        const uint32_t over = __shfl_sync(kAllLanes, in - n, 16 - r);  // above the stretch, of these
+        const uint32_t mid = __shfl_sync(kAllLanes, in - n, 16);
+        const uint32_t whole = __ballot_sync(kAllLanes, f.above_count + (upto - mid) <= (uint32_t)kList) & 0xffffu;
+        const uint32_t part = __ballot_sync(kAllLanes, upto - over <= (uint32_t)kList) & 0xffffu;
+        b.from_top = whole != 0;
+        b.on = (whole | part) != 0;
+        if (!b.on)
+            return b;
+        const int reach = 31 - __clz(whole ? whole : part);
+        const int first = whole ? 1 : max(f.bin - reach, 1), last = min(f.bin + reach, kPlaces - 2);
+        b.above_count = whole ? 0 : f.above_count - (mid - __shfl_sync(kAllLanes, over, reach));
+        b.hi = whole ? scale.lmax : place_end(first, true);
+        b.lo = place_end(last, false);
+        // the two places below the window hold +0 and -0, which are one logit
+        if (first == kFirstTiny + 1 || first == kFirstTiny || last == kFirstTiny || last == kFirstTiny + 1)
+            b.on = false;
+        return b;
+    }
+
+    // sums over the cluster of three integers of every thread
+    __device__ void sum3(unsigned long long (&x)[3]) {
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+            unsigned long long v = x[j];
+            uint32_t n = 0, bn;
+            unsigned long long bv;
+            scan(v, n, bv, bn);
+            if (tid < C)
+                *cluster.map_shared_rank(&sh.sums[j][rank], tid) = v;
+        }
+        cluster.sync();
+#pragma unroll
+        for (int j = 0; j < 3; ++j) {
+            x[j] = 0;
+            for (int r = 0; r < C; ++r)
+                x[j] += sh.sums[j][r];
+        }
+    }
+
+    // The whole call for a row whose answer does not depend on logits outside the
+    // window of places; false (in every CTA) for the others.
+    //
+    // bfloat16: the places' sums are exact, and so are the cut and the draw.
+    // float32: they place the cut and the draw to within a few places.  A second
+    // pass takes the exact sums -- of the row and of what lies above the two
+    // stretches of places around them -- and lists the stretches' entries, among which
+    // the exact cut and draw are found; where a stretch turns out not to hold
+    // them, the row is left to the general way.  Few entries above the cut
+    // are listed whole, and need no sum.
+    __device__ bool by_place(float T, int32_t top_k, double top_p, double min_p, float u) {
+        constexpr int E = 16 / ES;
         for (int i = tid; i < kPlaces; i += kNT)
             sh.count[i] = 0;
+        if (tid < 2)
+            sh.list_n[tid] = 0;
         __syncthreads();
         uint32_t most = 0;
+        float lmax = __int_as_float(0xff800000);
         {
             int64_t i = s0;
             constexpr int L = 4;
             if (a.vec) {
-                const int64_t v1 = s1 / 8;
+                const int64_t v1 = s1 / E;
                 const uint4* p = reinterpret_cast<const uint4*>(base);
-                for (int64_t v = s0 / 8 + tid; v < v1; v += L * kNT) {
+                for (int64_t v = s0 / E + tid; v < v1; v += L * kNT) {
                     uint4 w[L];
 #pragma unroll
                     for (int k = 0; k < L; ++k)
@@ -830,48 +940,70 @@ struct Kernel {
 #pragma unroll
                     for (int k = 0; k < L; ++k)
                         if (v + k * kNT < v1) {
-                            count_pair(w[k].x, most);
-                            count_pair(w[k].y, most);
-                            count_pair(w[k].z, most);
-                            count_pair(w[k].w, most);
+                            if constexpr (ES == 2) {
+                                count_pair(w[k].x, most);
+                                count_pair(w[k].y, most);
+                                count_pair(w[k].z, most);
+                                count_pair(w[k].w, most);
+                            } else {
+                                count_pair(__byte_perm(w[k].x, w[k].y, 0x7632), most);
+                                count_pair(__byte_perm(w[k].z, w[k].w, 0x7632), most);
+                                lmax = max_nan(max_nan(lmax, __uint_as_float(w[k].x)),
+                                               __uint_as_float(w[k].y));
+                                lmax = max_nan(max_nan(lmax, __uint_as_float(w[k].z)),
+                                               __uint_as_float(w[k].w));
+                            }
                         }
                 }
-                i = v1 * 8;
+                i = v1 * E;
             }
             // a lone logit, paired with -inf, which is not counted
             for (i += tid; i < s1; i += kNT) {
+                const float l = scalar_entry<ES>(base, i);
                 uint32_t m = 0;
-                count_pair(reinterpret_cast<const unsigned short*>(base)[i] | 0xff800000u, m);
+                count_pair((__float_as_uint(l) >> 16) | 0xff800000u, m);
                 m &= 0xffffu;
                 most = most > m ? most : m;
+                lmax = max_nan(lmax, l);
             }
         }
         most = max(most & 0xffffu, most >> 16);
         __syncthreads();
-        // the highest place taken here; kPlaces: a NaN
+        // the highest place taken here (kPlaces: a NaN), and the largest key
         int top = -1;
         for (int i = tid; i < kPlaces; i += kNT)
             if (sh.count[i])
                 top = i;
-        if (most > 0x7f80u)
+        if (most > 0x7f80u || lmax != lmax)
             top = kPlaces;
         top = __reduce_max_sync(kAllLanes, top);
-        if (lane == 0)
+        uint32_t key = __reduce_max_sync(kAllLanes, logit_key(lmax));
+        if (lane == 0) {
             sh.warp_max[warp] = (uint32_t)(top + 1);
+            sh.warp_cnt[warp] = key;
+        }
         __syncthreads();
-        for (int w = 0; w < kNW; ++w)
+        for (int w = 0; w < kNW; ++w) {
             top = max(top, (int)sh.warp_max[w] - 1);
+            key = max(key, sh.warp_cnt[w]);
+        }
         meet();
-        if (tid < C)
+        if (tid < C) {
             *cluster.map_shared_rank(&sh.part_max[rank], tid) = (uint32_t)(top + 1);
+            *cluster.map_shared_rank(&sh.part_key[rank], tid) = key;
+        }
         cluster.sync();
-        for (int r = 0; r < C; ++r)
+        for (int r = 0; r < C; ++r) {
             top = max(top, (int)sh.part_max[r] - 1);
+            key = max(key, sh.part_key[r]);
+        }
         const int D0 = kPlaces - 1 - top;  // by descending logit
         if (top < 0 || D0 <= 0 || D0 == kFirstTiny || D0 == kFirstTiny + 1)
             return false;
-        scale.lmax = place_value(D0);
+        scale.lmax = ES == 2 ? place_value(D0) : key_logit(key);
         if (T == 0.0f) {
+            if constexpr (ES == 4)
+                return false;
             const int64_t id = find(D0, 0);
             if (id >= 0) {
                 a_token(id, 1.0f);
@@ -898,7 +1030,7 @@ struct Kernel {
             unsigned long long m = 0;
             if (__any_sync(kAllLanes, n)) {
                 if (n)
-                    m = n * weight_fixed(scale, sh.pow2, place_value(D));
+                    m = n * place_weight(D);
                 n = __reduce_add_sync(kAllLanes, n);
 #pragma unroll
                 for (int o = 16; o; o >>= 1)
@@ -938,12 +1070,14 @@ struct Kernel {
         s.p = top_p < 1.0 ? ceil_scaled(top_p, whole) : 0;
         s.limit = kNoPlace;
         s.draw = false;
+        uint32_t limit_key = 0;
         if (min_p > 0.0) {
-            // the smallest bfloat16 l with l - l_max >= T ln(min_p)
+            // the smallest float l with l - l_max >= T ln(min_p); bfloat16: the smallest of those
             const float limit = __double2float_ru((double)scale.lmax + (double)T * log(min_p));
+            limit_key = logit_key(limit);
             const uint32_t b = __float_as_uint(limit + 0.0f);
             const int sign = b >> 31;
-            const int mag = (int)((b & 0x7fffffffu) >> 16) + (!sign && (b & 0xffffu));
+            const int mag = (int)((b & 0x7fffffffu) >> 16) + (ES == 2 && !sign && (b & 0xffffu));
             if (mag < kMag0 || mag >= kMag0 + kMags)
                 return false;
             const int i = mag - kMag0 + 1;
@@ -955,15 +1089,17 @@ struct Kernel {
             search_places(s, chunk, m, n, before_m, before_n);
             f = first();
         }
-        unsigned long long E = whole;
+        unsigned long long mass = whole;  // kept
         int64_t kept = near;
         float cut = -3.402823466e38f;
         if (f.bin < kNoPlace) {
             if (f.bin == kFirstTiny || f.bin == kFirstTiny + 1)
                 return false;
-            E = f.above_mass + f.mass;
-            kept = f.above_count + f.count;
-            cut = place_value(f.bin);
+            mass = f.above_mass + f.mass;
+            if constexpr (ES == 2) {
+                kept = f.above_count + f.count;
+                cut = place_value(f.bin);
+            }
         } else if ((uint64_t)near < (uint64_t)a.V) {
             // everything is kept: those from -127 down that are not -inf as well
             if (s.k)
@@ -985,25 +1121,118 @@ struct Kernel {
             for (int r = 0; r < C; ++r)
                 kept += sh.part_cnt[r];
         }
+        const bool by_draw = a.u != nullptr;
 
-        // the draw
-        const float inv = (float)((double)(1ull << scale.fix) / (double)E);
-        if (a.u) {
-            s.k = 0;
-            s.limit = kNoPlace;
-            s.draw = true;
-            s.p = floor_scaled(u, E);
-            search_places(s, chunk, m, n, before_m, before_n);
-            const Found d = first();
-            if (d.bin == kFirstTiny || d.bin == kFirstTiny + 1)
+        if constexpr (ES == 4) {
+            Band c, d;
+            c.on = c.from_top = d.on = d.from_top = false;
+            if (f.bin < kNoPlace) {
+                c = band_around(f);
+                if (!c.on)
+                    return false;
+            }
+            Wanted w;
+            w.k = 0;
+            w.limit = kNoPlace;
+            w.draw = true;
+            if (by_draw && !c.from_top) {
+                w.p = floor_scaled(u, mass);
+                search_places(w, chunk, m, n, before_m, before_n);
+                const Found h = first();
+                if (!c.on || place_end(h.bin, true) > c.hi) {
+                    d = band_around(h);
+                    if (!d.on)
+                        return false;
+                }
+            }
+            cluster.sync();  // the lists lie over the places
+            unsigned long long sum[3] = {0, 0, 0};  // the row; above the cut's stretch; above the draw's
+            const bool sums = top_p < 1.0 || !c.on || a.mass || !c.from_top;
+            uint32_t *nc = cluster.map_shared_rank(&sh.list_n[0], 0), *nd = cluster.map_shared_rank(&sh.list_n[1], 0);
+            unsigned long long *lc = cluster.map_shared_rank(list_at(0), 0),
+                               *ld = cluster.map_shared_rank(list_at(1), 0);
+            const float inf = __int_as_float(0x7f800000);
+            const float clo = c.on ? c.lo : inf, chi = c.on ? c.hi : inf;
+            const float dlo = d.on ? d.lo : inf, dhi = d.on ? d.hi : inf;
+            if (sums)
+                each([&](float l, int64_t id) {
+                    const unsigned long long x = weight_fixed(scale, sh.pow2, l);
+                    sum[0] += x;
+                    sum[1] += l > chi ? x : 0;
+                    sum[2] += l > dhi ? x : 0;
+                    if (l >= clo && l <= chi)
+                        offer(nc, lc, l, id);
+                    if (l >= dlo && l <= dhi)
+                        offer(nd, ld, l, id);
+                });
+            else
+                each([&](float l, int64_t id) {
+                    if (l >= clo)
+                        offer(nc, lc, l, id);
+                });
+            sum3(sum);
+            whole = sum[0];
+            Search q;
+            q.k = s.k;
+            q.top_p = top_p;
+            q.p = top_p < 1.0 ? ceil_scaled(top_p, whole) : 0;
+            if (rank == 0) {
+                bool ok = true;
+                Found g;
+                g.above_mass = sum[1];
+                g.above_count = c.above_count;
+                if (c.on) {
+                    sort(0);
+                    ok = limit_key <= logit_key(c.hi) && cut_in_list(q, g, limit_key, logit_key(c.lo));
+                } else if (tid == 0) {
+                    sh.kept_mass = whole;
+                    sh.cut_key = kKeyMinusInf + 1;
+                    sh.kept = 0;
+                }
+                __syncthreads();
+                if (ok && by_draw) {
+                    const unsigned long long target = floor_scaled(u, sh.kept_mass);
+                    if (c.on && target >= sum[1]) {
+                        ok = draw_in_list(0, sum[1], target);
+                    } else {
+                        if (d.on)
+                            sort(1);
+                        ok = d.on && draw_in_list(1, sum[2], target);
+                    }
+                }
+                if (tid == 0)
+                    sh.ok = ok;
+                __syncthreads();
+            }
+            share_cut();
+            if (!sh.ok)
                 return false;
-            const float l = place_value(d.bin);
-            const int64_t id = find(d.bin, (s.p - d.above_mass) / weight_fixed(scale, sh.pow2, l));
-            if (id >= 0)
-                a_token(id, weight_float(scale, l) * inv);
+            mass = sh.kept_mass;
+            if (c.on)
+                kept = sh.kept;
+            cut = key_logit(sh.cut_key);
+        }
+        const float inv = (float)((double)(1ull << scale.fix) / (double)mass);
+        if (by_draw) {
+            if constexpr (ES == 2) {
+                s.k = 0;
+                s.limit = kNoPlace;
+                s.draw = true;
+                s.p = floor_scaled(u, mass);
+                search_places(s, chunk, m, n, before_m, before_n);
+                const Found d = first();
+                if (d.bin == kFirstTiny || d.bin == kFirstTiny + 1)
+                    return false;
+                const float l = place_value(d.bin);
+                const int64_t id = find(d.bin, (s.p - d.above_mass) / weight_fixed(scale, sh.pow2, l));
+                if (id >= 0)
+                    a_token(id, weight_float(scale, l) * inv);
+            } else if (rank == 0 && tid == 0) {
+                a_token(sh.token, weight_float(scale, key_logit(sh.token_key)) * inv);
+            }
         }
         write([&](float l, int64_t) { return l >= cut; }, cut, inv, false);
-        finish(SV_OK, (uint32_t)kept, (float)((double)E / (double)whole));
+        finish(SV_OK, (uint32_t)kept, (float)((double)mass / (double)whole));
         return true;
     }
 
@@ -1052,11 +1281,10 @@ struct Kernel {
             sh.pow2[tid] = kPow2Steps[tid];
 
         cluster.barrier_arrive();
-        if constexpr (ES == 2)
-            if (!code && by_value(T, top_k, top_p, min_p, u)) {
-                cluster.sync();  // no CTA leaves while another may still read its memory
-                return;
-            }
+        if (!code && by_place(T, top_k, top_p, min_p, u)) {
+            cluster.sync();  // no CTA leaves while another may still read its memory
+            return;
+        }
 
         // A. the largest logit (NaN if there is one), over the cluster
         float m = __int_as_float(0xff800000);
@@ -1146,7 +1374,9 @@ struct Kernel {
             narrow(s, g, limit_key, klo, khi, split);
             if (g.count <= kList) {
                 gather(klo, khi);
-                cut_in_list(s, g, limit_key);
+                if (rank == 0)
+                    cut_in_list(s, g, limit_key, klo);
+                share_cut();
                 cut_key = sh.cut_key;
                 kept = sh.kept;
                 E = sh.kept_mass;
@@ -1166,7 +1396,8 @@ struct Kernel {
         if (a.u) {
             const unsigned long long target = floor_scaled(u, E);
             if (f.bin < kBins && g.count <= kList && target >= g.above_mass) {
-                draw_in_list(g.above_mass, target);  // the cut's list holds it
+                if (rank == 0)
+                    draw_in_list(0, g.above_mass, target);  // the cut's list holds it
             } else if (f.bin < kBins && g.count > kList && target >= g.above_mass) {
                 const unsigned long long w = weight_fixed(scale, sh.pow2, key_logit(klo));
                 draw_among_equals(klo, (target - g.above_mass) / w);
@@ -1192,7 +1423,8 @@ struct Kernel {
                 narrow(d, h, 0, klo, khi, split);
                 if (h.count <= kList) {
                     gather(klo, khi);
-                    draw_in_list(h.above_mass, target);
+                    if (rank == 0)
+                        draw_in_list(0, h.above_mass, target);
                 } else {
                     const unsigned long long w = weight_fixed(scale, sh.pow2, key_logit(klo));
                     draw_among_equals(klo, (target - h.above_mass) / w);
