@@ -67,8 +67,6 @@ struct Args {
     sv_sampling set;
     int64_t V, slice;
     int rows_per_seq, C, fix;
-    int vec;      // rows may be read as 16-byte vectors
-    int out_vec;  // and the output written so
 };
 
 enum Cond { kByCount, kByMass, kByLimit, kConds };
@@ -92,7 +90,7 @@ constexpr int kChunks = kPlaces / 32;  // places a warp takes at once
 constexpr int kFirstTiny = kMags + 1;  // D of the two places below the window
 constexpr int kNoPlace = kPlaces;
 
-struct Shared {
+struct alignas(16) Shared {
     union {
         struct {
             uint32_t lo[kBins], hi[kBins], cnt[kBins];
@@ -107,11 +105,12 @@ struct Shared {
         int chunk;
         uint32_t above_count;
         unsigned long long above_mass;
-    } hit[kConds];
+    } hit[2][kConds];  // of the search for the cut and of that for the draw
+    Found place[2][kConds];
     unsigned long long part_mass[kMaxC];
     uint32_t part_cnt[kMaxC];
     uint32_t part_max[kMaxC];
-    uint32_t part_key[kMaxC];
+    uint32_t part_tiny[kMaxC];
     unsigned long long warp_mass[kNW];
     uint32_t warp_cnt[kNW];
     uint32_t warp_max[kNW];
@@ -135,8 +134,14 @@ struct Kernel {
     int tid, lane, warp, rank, C;
     int64_t row;
     const unsigned char* base;  // the row's first logit
-    int64_t s0, s1;             // this CTA's slice
+    uint32_t s0, s1;            // this CTA's slice, by ids
+    // The slice's 16-byte vectors: number k holds the ids from k E - off on, where off is the
+    // place of the row's first logit in its own vector.  What they leave at the
+    // slice's ends (the row's ends: slices meet between vectors) is taken one by one.
+    uint32_t off, k0, k1;
     RowScale scale;
+
+    static constexpr int E = 16 / ES;
 
     __device__ Kernel(const Args& args, Shared& shared)
         : a(args), cluster(cg::this_cluster()), sh(shared) {
@@ -147,37 +152,54 @@ struct Kernel {
         rank = (int)cluster.block_rank();
         row = blockIdx.x / C;
         base = static_cast<const unsigned char*>(a.logits) + row * a.stride * ES;
-        s0 = rank * a.slice < a.V ? rank * a.slice : a.V;
-        s1 = s0 + a.slice < a.V ? s0 + a.slice : a.V;
+        off = (uint32_t)(reinterpret_cast<uintptr_t>(base) & 15u) / ES;
+        const int64_t v0 = rank * a.slice - off, v1 = v0 + a.slice;
+        s0 = (uint32_t)(v0 < 0 ? 0 : v0 < a.V ? v0 : a.V);
+        s1 = (uint32_t)(v1 < a.V ? v1 : a.V);
+        k0 = (s0 + off + E - 1) / E;
+        k1 = (s1 + off) / E;
+        if (k1 < k0)
+            k1 = k0;
         scale.fix = a.fix;
+    }
+
+    __device__ __forceinline__ const uint4* vectors() const {
+        return reinterpret_cast<const uint4*>(base - (size_t)off * ES);
+    }
+    __device__ __forceinline__ uint32_t head_end() const { return min(k0 * E - off, s1); }
+    __device__ __forceinline__ uint32_t tail_start() const { return max(k1 * E - off, head_end()); }
+
+    // vec(w, id of its first logit) for every vector of the slice, one(id) for every other logit
+    template <int D, class Vec, class One>
+    __device__ __forceinline__ void walk(Vec&& vec, One&& one) const {
+        const uint4* p = vectors() + k0 + tid;
+        for (uint32_t k = k0 + tid; k < k1; k += D * kNT, p += D * kNT) {
+            uint4 w[D];
+#pragma unroll
+            for (int j = 0; j < D; ++j)
+                if (k + j * kNT < k1)
+                    w[j] = load_stream(p + j * kNT);
+#pragma unroll
+            for (int j = 0; j < D; ++j)
+                if (k + j * kNT < k1)
+                    vec(w[j], (k + j * kNT) * E - off);
+        }
+        for (uint32_t i = s0 + tid; i < head_end(); i += kNT)
+            one(i);
+        for (uint32_t i = tail_start() + tid; i < s1; i += kNT)
+            one(i);
     }
 
     // fn(l, id) for every entry of the slice
     template <class F>
     __device__ __forceinline__ void each(F&& fn) const {
-        constexpr int E = 16 / ES, D = 4;
-        int64_t i = s0;
-        if (a.vec) {
-            const int64_t v1 = s1 / E;
-            const uint4* p = reinterpret_cast<const uint4*>(base);
-            for (int64_t v = s0 / E + tid; v < v1; v += D * kNT) {
-                uint4 w[D];
+        walk<4>(
+            [&](const uint4& w, uint32_t id) {
 #pragma unroll
-                for (int k = 0; k < D; ++k)
-                    if (v + k * kNT < v1)
-                        w[k] = load_stream(p + v + k * kNT);
-#pragma unroll
-                for (int k = 0; k < D; ++k)
-                    if (v + k * kNT < v1) {
-#pragma unroll
-                        for (int e = 0; e < E; ++e)
-                            fn(vector_entry<ES>(w[k], e), (v + k * kNT) * E + e);
-                    }
-            }
-            i = v1 * E;
-        }
-        for (i += tid; i < s1; i += kNT)
-            fn(scalar_entry<ES>(base, i), i);
+                for (int e = 0; e < E; ++e)
+                    fn(vector_entry<ES>(w, e), id + e);
+            },
+            [&](uint32_t id) { fn(scalar_entry<ES>(base, id), id); });
     }
 
     // the linear bin of a logit; larger logits, smaller bins
@@ -195,7 +217,7 @@ struct Kernel {
         if (tid == 0)
             sh.list_n[0] = 0;
         __syncthreads();
-        each([&](float l, int64_t) {
+        each([&](float l, uint32_t) {
             const int b = map(l);
             if (b < 0)
                 return;
@@ -397,10 +419,10 @@ struct Kernel {
         return which ? reinterpret_cast<unsigned long long*>(sh.lo) : sh.list;
     }
 
-    __device__ __forceinline__ void offer(uint32_t* n, unsigned long long* list, float l, int64_t id) const {
+    __device__ __forceinline__ void offer(uint32_t* n, unsigned long long* list, float l, uint32_t id) const {
         const uint32_t at = atomicAdd(n, 1u);
         if (at < (uint32_t)kList)
-            list[at] = ((unsigned long long)logit_key(l) << 32) | (uint32_t)~(uint32_t)id;
+            list[at] = ((unsigned long long)logit_key(l) << 32) | ~id;
     }
 
     // Sorts a list of this CTA: descending logits, ascending ids.
@@ -438,7 +460,7 @@ struct Kernel {
         cluster.sync();
         uint32_t* n = cluster.map_shared_rank(&sh.list_n[0], 0);
         unsigned long long* list = cluster.map_shared_rank(sh.list, 0);
-        each([&](float l, int64_t id) {
+        each([&](float l, uint32_t id) {
             const uint32_t k = logit_key(l);
             if (k >= klo && k <= khi)
                 offer(n, list, l, id);
@@ -466,28 +488,34 @@ struct Kernel {
     }
 
     // The last group of equal logits in the first list that every filter keeps
-    // (first CTA): the cut, the kept mass and count.  Returns whether the cut lies in
-    // the list: some filter ends with it, `low` being the lowest key it covers.
-    __device__ bool cut_in_list(const Search& s, const Found& f, uint32_t limit_key, uint32_t low) {
+    // (first CTA): the cut, the kept mass and count.  Returns 1 when the cut lies in
+    // the list: some filter ends with it, `low` being the lowest key it covers; 0 when it
+    // does not; 2 when sums off by up to `slack` do not tell.
+    __device__ int cut_in_list(const Search& s, const Found& f, uint32_t limit_key, uint32_t low,
+                               unsigned long long slack) {
         const int n = (int)sh.list_n[0];
         unsigned long long w[kOwn], before, total;
         list_scan(0, w, before, total);
         unsigned long long at = f.above_mass + before;
         int last = -1;
+        bool near = false;
         for (int j = 0; j < kOwn; ++j) {
             const int i = kOwn * tid + j;
             if (i < n) {
                 const uint32_t k = (uint32_t)(sh.list[i] >> 32);
                 const bool start = i == 0 || (uint32_t)(sh.list[i - 1] >> 32) != k;
-                if (start && k >= limit_key && (!s.k || f.above_count + i < s.k) &&
-                    (s.top_p >= 1.0 || at < s.p))
-                    last = i;
+                if (start && k >= limit_key && (!s.k || f.above_count + i < s.k)) {
+                    if (s.top_p >= 1.0 || at < s.p)
+                        last = i;
+                    if (s.top_p < 1.0 && f.above_count + i > 0 && (at < s.p ? s.p - at : at - s.p) < slack)
+                        near = true;
+                }
             }
             at += w[j];
         }
         // conditions fail for good once they fail: the last start over all threads
         last = __reduce_max_sync(kAllLanes, last);
-        __syncthreads();
+        const bool any_near = __syncthreads_or(near);
         if (lane == 0)
             sh.warp_max[warp] = (uint32_t)(last + 1);
         __syncthreads();
@@ -513,10 +541,15 @@ struct Kernel {
             }
         }
         __syncthreads();
-        if ((s.k && f.above_count >= s.k) || (s.top_p < 1.0 && f.above_mass >= s.p))
-            return false;
-        return limit_key >= low || (s.k && f.above_count + (uint32_t)n >= s.k) ||
-               (s.top_p < 1.0 && f.above_mass + total >= s.p);
+        if (any_near)
+            return 2;
+        if ((s.k && f.above_count >= s.k) || (s.top_p < 1.0 && f.above_count && f.above_mass >= s.p))
+            return 0;
+        if (limit_key >= low || (s.k && f.above_count + (uint32_t)n >= s.k))
+            return 1;
+        if (s.top_p >= 1.0 || f.above_mass + total + slack < s.p)
+            return 0;
+        return f.above_mass + total >= s.p + slack ? 1 : 2;
     }
 
     // what the first CTA has found, to the others
@@ -551,11 +584,11 @@ struct Kernel {
 
     // The entry number r, by ascending id, among those with this key.
     __device__ void draw_among_equals(uint32_t key, unsigned long long r) {
-        const int64_t per = (s1 - s0 + kNT - 1) / kNT;
-        const int64_t e0 = s0 + tid * per, e1 = e0 + per < s1 ? e0 + per : s1;
+        const uint32_t per = (s1 - s0 + kNT - 1) / kNT;
+        const uint32_t e0 = min(s0 + tid * per, s1), e1 = min(e0 + per, s1);
         uint32_t n = 0, before;
         unsigned long long m = 0, bm;
-        for (int64_t e = e0; e < e1; ++e)
+        for (uint32_t e = e0; e < e1; ++e)
             n += logit_key(scalar_entry<ES>(base, e)) == key;
         const uint32_t mine = n;
         scan(m, n, bm, before);
@@ -567,9 +600,9 @@ struct Kernel {
             before += sh.part_cnt[c];
         if (r >= before && r < (unsigned long long)before + mine) {
             uint32_t left = (uint32_t)(r - before);
-            for (int64_t e = e0; e < e1; ++e)
+            for (uint32_t e = e0; e < e1; ++e)
                 if (logit_key(scalar_entry<ES>(base, e)) == key && left-- == 0) {
-                    *cluster.map_shared_rank(&sh.token, 0) = (uint32_t)e;
+                    *cluster.map_shared_rank(&sh.token, 0) = e;
                     *cluster.map_shared_rank(&sh.token_key, 0) = key;
                     break;
                 }
@@ -581,80 +614,74 @@ struct Kernel {
     // none of whose logits reaches `cut` is written without looking further.
     template <class Keep>
     __device__ void write(Keep&& keep, float cut, float inv, bool bad) {
-        constexpr int E = 16 / ES;
         const float nan = __int_as_float(0x7fffffff);
-        const auto prob = [&](float l, int64_t id) {
+        const auto prob = [&](float l, uint32_t id) {
             return bad ? nan : keep(l, id) ? (inv > 0.0f ? weight_float(scale, l) * inv : 1.0f) : 0.0f;
         };
-        const auto logit = [&](float l, int64_t id) {
+        const auto logit = [&](float l, uint32_t id) {
             return bad || keep(l, id) ? __float_as_uint(l) : 0xff800000u;
         };
         float* p = a.probs ? a.probs + row * a.probs_stride : nullptr;
         unsigned char* o = a.out ? static_cast<unsigned char*>(a.out) + row * a.out_stride * ES : nullptr;
         if (!p && !o)
             return;
-        int64_t i = s0;
-        if (a.vec && a.out_vec) {
-            const uint4* x = reinterpret_cast<const uint4*>(base);
-            const int64_t v1 = s1 / E;
-            constexpr int D = 2;
-            for (int64_t v = s0 / E + tid; v < v1; v += D * kNT) {
-                uint4 w[D];
+        const auto one = [&](uint32_t id) {
+            const float l = scalar_entry<ES>(base, id);
+            if (p)
+                p[id] = prob(l, id);
+            if (o) {
+                const uint32_t h = logit(l, id);
+                if constexpr (ES == 4)
+                    reinterpret_cast<uint32_t*>(o)[id] = h;
+                else
+                    reinterpret_cast<unsigned short*>(o)[id] = (unsigned short)(h >> 16);
+            }
+        };
+        // vectors of logits go to 16-byte places of both outputs, or are written one by one
+        const bool even = (!p || (reinterpret_cast<uintptr_t>(p - off) & 15u) == 0) &&
+                          (!o || (reinterpret_cast<uintptr_t>(o - off * ES) & 15u) == 0);
+        if (!even) {
+            for (uint32_t i = s0 + tid; i < s1; i += kNT)
+                one(i);
+            return;
+        }
+        walk<4>(
+            [&](const uint4& w, uint32_t id) {
+                float m = vector_entry<ES>(w, 0);
 #pragma unroll
-                for (int k = 0; k < D; ++k)
-                    if (v + k * kNT < v1)
-                        w[k] = load_stream(x + v + k * kNT);
+                for (int e = 1; e < E; ++e)
+                    m = fmaxf(m, vector_entry<ES>(w, e));
+                const bool any = bad || m >= cut;
+                if (p) {
+                    float4* q = reinterpret_cast<float4*>(p + id);
+                    if (!any) {
 #pragma unroll
-                for (int k = 0; k < D; ++k) {
-                    const int64_t u = v + k * kNT;
-                    if (u >= v1)
-                        continue;
-                    float m = vector_entry<ES>(w[k], 0);
+                        for (int e = 0; e < E / 4; ++e)
+                            q[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    } else {
 #pragma unroll
-                    for (int e = 1; e < E; ++e)
-                        m = fmaxf(m, vector_entry<ES>(w[k], e));
-                    const bool any = bad || m >= cut;
-                    if (p) {
-                        float f[E];
-#pragma unroll
-                        for (int e = 0; e < E; ++e)
-                            f[e] = any ? prob(vector_entry<ES>(w[k], e), u * E + e) : 0.0f;
-#pragma unroll
-                        for (int e = 0; e < E; e += 4)
-                            reinterpret_cast<float4*>(p)[(u * E + e) / 4] =
-                                make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
-                    }
-                    if (o) {
-                        uint32_t h[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            if constexpr (ES == 4) {
-                                h[j] = any ? logit(vector_entry<ES>(w[k], j), u * E + j) : 0xff800000u;
-                            } else {
-                                h[j] = any ? (logit(vector_entry<ES>(w[k], 2 * j), u * E + 2 * j) >> 16) |
-                                                 (logit(vector_entry<ES>(w[k], 2 * j + 1), u * E + 2 * j + 1) &
-                                                  0xffff0000u)
-                                           : 0xff80ff80u;
-                            }
-                        }
-                        reinterpret_cast<uint4*>(o)[u] = make_uint4(h[0], h[1], h[2], h[3]);
+                        for (int e = 0; e < E / 4; ++e)
+                            q[e] = make_float4(prob(vector_entry<ES>(w, 4 * e), id + 4 * e),
+                                               prob(vector_entry<ES>(w, 4 * e + 1), id + 4 * e + 1),
+                                               prob(vector_entry<ES>(w, 4 * e + 2), id + 4 * e + 2),
+                                               prob(vector_entry<ES>(w, 4 * e + 3), id + 4 * e + 3));
                     }
                 }
-            }
-            i = v1 * E;
-        }
-        for (i += tid; i < s1; i += kNT) {
-            const float l = scalar_entry<ES>(base, i);
-            if (p)
-                p[i] = prob(l, i);
-            if (o) {
-                const uint32_t h = logit(l, i);
-                if constexpr (ES == 4)
-                    reinterpret_cast<uint32_t*>(o)[i] = h;
-                else
-                    reinterpret_cast<unsigned short*>(o)[i] = (unsigned short)(h >> 16);
-            }
-        }
+                if (o) {
+                    uint32_t h[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if constexpr (ES == 4)
+                            h[j] = any ? logit(vector_entry<ES>(w, j), id + j) : 0xff800000u;
+                        else
+                            h[j] = any ? (logit(vector_entry<ES>(w, 2 * j), id + 2 * j) >> 16) |
+                                             (logit(vector_entry<ES>(w, 2 * j + 1), id + 2 * j + 1) & 0xffff0000u)
+                                       : 0xff80ff80u;
+                    }
+                    *reinterpret_cast<uint4*>(o + (size_t)id * ES) = make_uint4(h[0], h[1], h[2], h[3]);
+                }
+            },
+            one);
     }
 
     // -------------------------------------------------------- by places -----
@@ -664,6 +691,14 @@ struct Kernel {
         const int s = kMags + 1 - D, i = s >= 0 ? s : -1 - s;
         const uint32_t b = i ? (uint32_t)(kMag0 - 1 + i) : 0u;
         return __uint_as_float((b | (s < 0 ? 0x8000u : 0u)) << 16);
+    }
+
+    // the place of a logit
+    __device__ __forceinline__ static int place_of(float l) {
+        const uint32_t b = __float_as_uint(l);
+        const int m = (int)((b & 0x7fffffffu) >> 16);
+        const int i = min(max(m, kMag0 - 1), kMag0 + kMags) - (kMag0 - 1);
+        return kMags + 1 - ((b >> 31) ? -1 - i : i);
     }
 
     // a float32 place's largest or smallest logit; inside the window
@@ -680,14 +715,14 @@ struct Kernel {
         return weight_fixed(scale, sh.pow2, l);
     }
 
-    // Counts two logits; `most` keeps the largest magnitudes seen.  Each place's
-    // byte offset is 4 i or 4 (-1 - i), both logits' in the halves of one word.
+    // Counts the two logits whose upper 16 bits x holds.  Each place's byte
+    // offset is 4 i or 4 (-1 - i), both logits' in the halves of one word.
     // Logits above -127 alone are counted: what is missing lies below.
-    __device__ __forceinline__ void count_pair(uint32_t x, uint32_t& most) {
+    __device__ __forceinline__ void count_pair(uint32_t x) {
         constexpr uint32_t lo = (kMag0 - 1) * 0x10001u, hi = (kMag0 + kMags) * 0x10001u;
         constexpr int far = 4 * (-1 - (kMags + 1));
-        uint32_t m = x & 0x7fff7fffu, sign, i;
-        asm("max.u16x2 %0, %1, %2;" : "=r"(most) : "r"(most), "r"(m));
+        const uint32_t m = x & 0x7fff7fffu;
+        uint32_t sign, i;
         asm("max.u16x2 %0, %1, %2;" : "=r"(i) : "r"(m), "r"(lo));
         asm("min.u16x2 %0, %1, %2;" : "=r"(i) : "r"(i), "r"(hi));
         asm("prmt.b32 %0, %1, %2, %3;" : "=r"(sign) : "r"(x), "r"(0u), "r"(0xbb99u));  // sign of each half
@@ -700,12 +735,28 @@ struct Kernel {
             atomicAdd(reinterpret_cast<uint32_t*>(zero + o1), 1u);
     }
 
-    // entries at place D, over the cluster
+    // entries at N places, over the cluster
+    template <int N>
+    __device__ __forceinline__ void place_counts(const int (&D)[N], uint32_t (&n)[N]) const {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            n[j] = 0;
+        for (int r = 0; r < C; ++r) {
+            const uint32_t* count = cluster.map_shared_rank(sh.count, r);
+            uint32_t x[N];
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                x[j] = count[kPlaces - 1 - D[j]];
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                n[j] += x[j];
+        }
+    }
     __device__ __forceinline__ uint32_t place_count(int D) const {
-        uint32_t n = 0;
-        for (int r = 0; r < C; ++r)
-            n += cluster.map_shared_rank(sh.count, r)[kPlaces - 1 - D];
-        return n;
+        const int d[1] = {D};
+        uint32_t n[1];
+        place_counts<1>(d, n);
+        return n[0];
     }
 
     struct Wanted {
@@ -715,21 +766,16 @@ struct Kernel {
         bool draw;
     };
 
-    // Finds the places where the conditions end, in every CTA's `found`.  The
-    // thread whose chunk of places holds one hands it to a warp, which goes through
-    // the chunk; m, n: the chunk's sums, before_m, before_n: what lies above it.
-    __device__ void search_places(const Wanted& s, int chunk, unsigned long long m, uint32_t n,
-                                  unsigned long long before_m, uint32_t before_n) {
-        __syncthreads();  // every thread has read `found`
-        if (tid < kConds) {
-            sh.hit[tid].chunk = -1;
-            sh.found[tid].bin = kNoPlace;
-        }
-        cluster.sync();
+    // Finds the places where the conditions end, in every CTA's `place[set]`, and
+    // returns the first.  The thread whose chunk of places holds one hands it to a warp,
+    // which goes through the chunk; m, n: the chunk's sums, before_m, before_n: what
+    // lies above it.
+    __device__ Found search_places(int set, const Wanted& s, int chunk, unsigned long long m, uint32_t n,
+                                   unsigned long long before_m, uint32_t before_n) {
         const auto hit = [&](int c) {
-            sh.hit[c].chunk = chunk;
-            sh.hit[c].above_mass = before_m;
-            sh.hit[c].above_count = before_n;
+            sh.hit[set][c].chunk = chunk;
+            sh.hit[set][c].above_mass = before_m;
+            sh.hit[set][c].above_count = before_n;
         };
         if (chunk >= 0) {
             if (s.k && before_n < s.k && before_n + n >= s.k)
@@ -741,8 +787,8 @@ struct Kernel {
                 hit(kByLimit);
         }
         __syncthreads();
-        if (warp < kConds && sh.hit[warp].chunk >= 0) {
-            const int D = sh.hit[warp].chunk * 32 + lane;
+        if (warp < kConds && sh.hit[set][warp].chunk >= 0) {
+            const int D = sh.hit[set][warp].chunk * 32 + lane;
             Found f;
             f.bin = D;
             f.count = place_count(D);
@@ -758,8 +804,8 @@ struct Kernel {
                     in += pn;
                 }
             }
-            f.above_mass = sh.hit[warp].above_mass + im - f.mass;
-            f.above_count = sh.hit[warp].above_count + in - f.count;
+            f.above_mass = sh.hit[set][warp].above_mass + im - f.mass;
+            f.above_count = sh.hit[set][warp].above_count + in - f.count;
             const unsigned long long em = f.above_mass + f.mass;
             const uint32_t en = f.above_count + f.count;
             const bool here = warp == kByCount ? f.above_count < s.k && en >= s.k
@@ -767,32 +813,30 @@ struct Kernel {
                               : s.draw ? f.above_mass <= s.p && em > s.p
                                        : f.above_mass < s.p && em >= s.p;
             if (here)
-                tell(warp, f);
+                for (int r = 0; r < C; ++r)
+                    *cluster.map_shared_rank(&sh.place[set][warp], r) = f;
         }
         cluster.sync();
+        Found f = sh.place[set][0];
+        for (int c = 1; c < kConds; ++c)
+            if (sh.place[set][c].bin < f.bin)
+                f = sh.place[set][c];
+        return f;
     }
 
-    // which of the eight logits from group g of the slice equal the bits `two` holds twice
-    __device__ __forceinline__ uint32_t matches(int64_t g, uint32_t two) const {
-        const int64_t e = s0 + g * 8;
+    // which of a vector's eight logits equal the bits `two` holds twice
+    __device__ __forceinline__ static uint32_t matches(const uint4& w, uint32_t two) {
+        const uint32_t x[4] = {w.x ^ two, w.y ^ two, w.z ^ two, w.w ^ two};
         uint32_t mask = 0;
-        if (a.vec && e + 8 <= s1) {
-            const uint4 w = load_stream(reinterpret_cast<const uint4*>(base) + e / 8);
-            const uint32_t x[4] = {w.x ^ two, w.y ^ two, w.z ^ two, w.w ^ two};
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                mask |= (((x[j] & 0xffffu) == 0) | ((x[j] >> 16) == 0) << 1) << (2 * j);
-        } else {
-            const unsigned short* q = reinterpret_cast<const unsigned short*>(base);
-            for (int j = 0; j < 8; ++j)
-                if (e + j < s1)
-                    mask |= (uint32_t)(q[e + j] == (two & 0xffffu)) << j;
-        }
+        for (int j = 0; j < 4; ++j)
+            mask |= ((x[j] & 0xffffu) == 0 ? 1u << (2 * j) : 0u) | ((x[j] >> 16) == 0 ? 2u << (2 * j) : 0u);
         return mask;
     }
 
-    // The entry number r by ascending id at place D; the CTA that holds it returns
-    // its id in one thread, every other thread returns -1.
+    // The entry number r by ascending id at place D (bfloat16); the CTA that holds it
+    // returns its id in one thread, every other thread returns -1.  Each warp
+    // counts in a stretch of the slice, then the warp that holds the entry looks again.
     __device__ int64_t find(int D, unsigned long long r) {
         uint32_t n = 0, in;
         if (lane < C)
@@ -809,40 +853,77 @@ struct Kernel {
             return -1;
         uint32_t left = (uint32_t)(r - __shfl_sync(kAllLanes, in - n, rank));
         const uint32_t bits = __float_as_uint(place_value(D)) >> 16, two = bits * 0x10001u;
-        // a stretch of the slice per warp
-        const int64_t groups = (s1 - s0 + 7) / 8, per = (groups + kNW - 1) / kNW;
-        const int64_t g0 = warp * per, g1 = g0 + per < groups ? g0 + per : groups;
+        const unsigned short* q = reinterpret_cast<const unsigned short*>(base);
+        // what lies before the first vector: less than one
+        for (uint32_t i = s0; i < head_end(); ++i)
+            if (q[i] == bits && left-- == 0)
+                return tid == 0 ? (int64_t)i : -1;
+        constexpr int L = 8;
+        const uint4* p = vectors();
+        const uint32_t per = (k1 - k0 + kNW - 1) / kNW;
+        const uint32_t g0 = min(k0 + warp * per, k1), g1 = min(g0 + per, k1);
         uint32_t mine = 0;
-        for (int64_t g = g0 + lane; g < g1; g += 32)
-            mine += __popc(matches(g, two));
+        for (uint32_t g = g0 + lane; g < g1; g += 32 * L) {
+            uint4 w[L];
+#pragma unroll
+            for (int j = 0; j < L; ++j)
+                if (g + 32 * j < g1)
+                    w[j] = load_stream(p + g + 32 * j);
+#pragma unroll
+            for (int j = 0; j < L; ++j)
+                if (g + 32 * j < g1)
+                    mine += __popc(matches(w[j], two));
+        }
         mine = __reduce_add_sync(kAllLanes, mine);
         __syncthreads();
         if (lane == 0)
             sh.warp_cnt[warp] = mine;
         __syncthreads();
-        for (int w = 0; w < warp; ++w) {
-            if (left < sh.warp_cnt[w])
-                return -1;
+        int holder = -1;
+        for (int w = 0; w < kNW; ++w) {
+            if (left < sh.warp_cnt[w]) {
+                holder = w;
+                break;
+            }
             left -= sh.warp_cnt[w];
         }
-        if (left >= mine)
+        if (holder < 0) {
+            if (tid == 0)
+                for (uint32_t i = tail_start(); i < s1; ++i)
+                    if (q[i] == bits && left-- == 0)
+                        return i;
             return -1;
-        for (int64_t g = g0; g < g1; g += 32) {
-            const uint32_t mask = g + lane < g1 ? matches(g + lane, two) : 0;
-            uint32_t c = __popc(mask), ic = c;
+        }
+        if (holder != warp)
+            return -1;
+        for (uint32_t b = g0; b < g1; b += 32 * L) {
+            uint32_t mask[L];
+            uint4 w[L];
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t p = __shfl_up_sync(kAllLanes, ic, o);
-                if (lane >= o)
-                    ic += p;
-            }
-            const uint32_t all = __shfl_sync(kAllLanes, ic, 31);
-            if (left < all) {
+            for (int j = 0; j < L; ++j)
+                if (b + lane + 32 * j < g1)
+                    w[j] = load_stream(p + b + lane + 32 * j);
+#pragma unroll
+            for (int j = 0; j < L; ++j)
+                mask[j] = b + lane + 32 * j < g1 ? matches(w[j], two) : 0;
+#pragma unroll
+            for (int j = 0; j < L; ++j) {
+                const uint32_t c = __popc(mask[j]), all = __reduce_add_sync(kAllLanes, c);
+                if (left >= all) {
+                    left -= all;
+                    continue;
+                }
+                uint32_t ic = c;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const uint32_t x = __shfl_up_sync(kAllLanes, ic, o);
+                    if (lane >= o)
+                        ic += x;
+                }
                 if (left >= ic - c && left < ic)
-                    return s0 + (g + lane) * 8 + __fns(mask, 0, left - (ic - c) + 1);
+                    return (int64_t)(b + lane + 32 * j) * E - off + __fns(mask[j], 0, left - (ic - c) + 1);
                 return -1;
             }
-            left -= all;
         }
         return -1;
     }
@@ -857,7 +938,7 @@ struct Kernel {
     __device__ Band band_around(const Found& f) const {
         Band b;
         const int D = f.bin - 16 + lane;
-        const uint32_t n = D >= 1 && D <= kPlaces - 2 ? place_count(D) : 0;
+        const uint32_t n = place_count(D >= 1 && D <= kPlaces - 2 ? D : kPlaces - 1);  // the last: not counted, 0
         uint32_t in = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -911,96 +992,76 @@ struct Kernel {
     //
     // bfloat16: the places' sums are exact, and so are the cut and the draw.
     // float32: they place the cut and the draw to within a few places.  A second
-    // pass takes the exact sums -- of the row and of what lies above the two
-    // stretches of places around them -- and lists the stretches' entries, among which
-    // the exact cut and draw are found; where a stretch turns out not to hold
-    // them, the row is left to the general way.  Few entries above the cut
-    // are listed whole, and need no sum.
+    // pass takes the sums of the row and of what lies above the two stretches of
+    // places around them, and lists the stretches' entries, among which the exact cut and
+    // draw are found; where a stretch turns out not to hold them, the row is left to
+    // the general way.  Few entries above the cut are listed whole, and need no
+    // sum but the row's for top-p: it is taken in floats, to 2^-17, and where an entry
+    // lies nearer to top-p's border than that, once more in integers.
     __device__ bool by_place(float T, int32_t top_k, double top_p, double min_p, float u) {
-        constexpr int E = 16 / ES;
-        for (int i = tid; i < kPlaces; i += kNT)
-            sh.count[i] = 0;
-        if (tid < 2)
-            sh.list_n[tid] = 0;
-        __syncthreads();
-        uint32_t most = 0;
-        float lmax = __int_as_float(0xff800000);
         {
-            int64_t i = s0;
-            constexpr int L = 4;
-            if (a.vec) {
-                const int64_t v1 = s1 / E;
-                const uint4* p = reinterpret_cast<const uint4*>(base);
-                for (int64_t v = s0 / E + tid; v < v1; v += L * kNT) {
-                    uint4 w[L];
-#pragma unroll
-                    for (int k = 0; k < L; ++k)
-                        if (v + k * kNT < v1)
-                            w[k] = load_stream(p + v + k * kNT);
-#pragma unroll
-                    for (int k = 0; k < L; ++k)
-                        if (v + k * kNT < v1) {
-                            if constexpr (ES == 2) {
-                                count_pair(w[k].x, most);
-                                count_pair(w[k].y, most);
-                                count_pair(w[k].z, most);
-                                count_pair(w[k].w, most);
-                            } else {
-                                count_pair(__byte_perm(w[k].x, w[k].y, 0x7632), most);
-                                count_pair(__byte_perm(w[k].z, w[k].w, 0x7632), most);
-                                lmax = max_nan(max_nan(lmax, __uint_as_float(w[k].x)),
-                                               __uint_as_float(w[k].y));
-                                lmax = max_nan(max_nan(lmax, __uint_as_float(w[k].z)),
-                                               __uint_as_float(w[k].w));
-                            }
-                        }
+            uint4* z = reinterpret_cast<uint4*>(sh.count);
+            for (int i = tid; i < kPlaces / 4; i += kNT)
+                z[i] = make_uint4(0, 0, 0, 0);
+            if (tid < 2)
+                sh.list_n[tid] = 0;
+            if (tid < 2 * kConds) {
+                sh.hit[tid / kConds][tid % kConds].chunk = -1;
+                sh.place[tid / kConds][tid % kConds].bin = kNoPlace;
+            }
+        }
+        __syncthreads();
+        float lmax = __int_as_float(0xff800000);
+        uint32_t two = 0xff80ff80u;  // bfloat16: the largest of each half
+        walk<4>(
+            [&](const uint4& w, uint32_t) {
+                if constexpr (ES == 2) {
+                    count_pair(w.x);
+                    count_pair(w.y);
+                    count_pair(w.z);
+                    count_pair(w.w);
+                    uint32_t m, x;
+                    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(w.x), "r"(w.y));
+                    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(x) : "r"(w.z), "r"(w.w));
+                    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(x));
+                    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(two) : "r"(two), "r"(m));
+                } else {
+                    count_pair(__byte_perm(w.x, w.y, 0x7632));
+                    count_pair(__byte_perm(w.z, w.w, 0x7632));
+                    lmax = max_nan(max_nan(lmax, __uint_as_float(w.x)), __uint_as_float(w.y));
+                    lmax = max_nan(max_nan(lmax, __uint_as_float(w.z)), __uint_as_float(w.w));
                 }
-                i = v1 * E;
-            }
-            // a lone logit, paired with -inf, which is not counted
-            for (i += tid; i < s1; i += kNT) {
-                const float l = scalar_entry<ES>(base, i);
-                uint32_t m = 0;
-                count_pair((__float_as_uint(l) >> 16) | 0xff800000u, m);
-                m &= 0xffffu;
-                most = most > m ? most : m;
+            },
+            [&](uint32_t id) {  // a lone logit, paired with -inf, which is not counted
+                const float l = scalar_entry<ES>(base, id);
+                count_pair((__float_as_uint(l) >> 16) | 0xff800000u);
                 lmax = max_nan(lmax, l);
-            }
-        }
-        most = max(most & 0xffffu, most >> 16);
+            });
+        if constexpr (ES == 2)
+            lmax = max_nan(lmax, max_nan(__uint_as_float(two << 16), __uint_as_float(two & 0xffff0000u)));
+        // the largest key; above all of them: a NaN
+        uint32_t key = lmax == lmax ? logit_key(lmax) : 0xffffffffu;
+        key = __reduce_max_sync(kAllLanes, key);
+        if (lane == 0)
+            sh.warp_max[warp] = key;
         __syncthreads();
-        // the highest place taken here (kPlaces: a NaN), and the largest key
-        int top = -1;
-        for (int i = tid; i < kPlaces; i += kNT)
-            if (sh.count[i])
-                top = i;
-        if (most > 0x7f80u || lmax != lmax)
-            top = kPlaces;
-        top = __reduce_max_sync(kAllLanes, top);
-        uint32_t key = __reduce_max_sync(kAllLanes, logit_key(lmax));
-        if (lane == 0) {
-            sh.warp_max[warp] = (uint32_t)(top + 1);
-            sh.warp_cnt[warp] = key;
-        }
-        __syncthreads();
-        for (int w = 0; w < kNW; ++w) {
-            top = max(top, (int)sh.warp_max[w] - 1);
-            key = max(key, sh.warp_cnt[w]);
-        }
+        for (int w = 0; w < kNW; ++w)
+            key = max(key, sh.warp_max[w]);
         meet();
         if (tid < C) {
-            *cluster.map_shared_rank(&sh.part_max[rank], tid) = (uint32_t)(top + 1);
-            *cluster.map_shared_rank(&sh.part_key[rank], tid) = key;
+            *cluster.map_shared_rank(&sh.part_max[rank], tid) = key;
+            *cluster.map_shared_rank(&sh.part_tiny[rank], tid) = sh.count[kMags + 1] + sh.count[kMags + 2];
         }
         cluster.sync();
+        uint32_t tiny = 0;  // entries below the window
         for (int r = 0; r < C; ++r) {
-            top = max(top, (int)sh.part_max[r] - 1);
-            key = max(key, sh.part_key[r]);
+            key = max(key, sh.part_max[r]);
+            tiny += sh.part_tiny[r];
         }
-        const int D0 = kPlaces - 1 - top;  // by descending logit
-        if (top < 0 || D0 <= 0 || D0 == kFirstTiny || D0 == kFirstTiny + 1)
+        scale.lmax = key_logit(key);
+        const int D0 = place_of(scale.lmax);
+        if (key == 0xffffffffu || D0 < 1 || D0 > kPlaces - 2 || D0 == kFirstTiny || D0 == kFirstTiny + 1)
             return false;
-        scale.lmax = ES == 2 ? place_value(D0) : key_logit(key);
         if (T == 0.0f) {
             if constexpr (ES == 4)
                 return false;
@@ -1010,9 +1071,11 @@ struct Kernel {
                 for (int r = 0; r < C; ++r)
                     *cluster.map_shared_rank(&sh.token, r) = (uint32_t)id;
             }
-            cluster.sync();
-            const uint32_t token = sh.token;
-            write([=](float, int64_t i) { return (uint32_t)i == token; }, scale.lmax, 0.0f, false);
+            if (a.probs || a.out) {
+                cluster.sync();
+                const uint32_t token = sh.token;
+                write([=](float, uint32_t i) { return i == token; }, scale.lmax, 0.0f, false);
+            }
             finish(SV_OK, 1, 1.0f);
             return true;
         }
@@ -1020,25 +1083,52 @@ struct Kernel {
         // logits from -127 down must weigh nothing
         if (!((scale.lmax + 127.0f) * scale.ch >= 61.0f))
             return false;
+        // bfloat16 logits below the window are taken for 0: their weights are off by
+        // 2^-24/T of themselves, which must not show in the sum (>= 1 at l_max)
+        if (ES == 2 && tiny && (float)tiny * weight_float(scale, 0.0f) > T * 3.0517578e-5f) {  // 2^-39 / 2^-24
+            // unless they are zeros
+            bool other = false;
+            each([&](float l, uint32_t) { other = other || (l != 0.0f && fabsf(l) < 2.9802322e-8f); });
+            const uint32_t any = __syncthreads_or(other);
+            cluster.sync();  // everyone has read `part_tiny`
+            if (tid < C)
+                *cluster.map_shared_rank(&sh.part_tiny[rank], tid) = any;
+            cluster.sync();
+            for (int r = 0; r < C; ++r)
+                if (sh.part_tiny[r])
+                    return false;
+        }
 
         // sums of each chunk of places, a chunk per warp
         const int per = (kChunks + C - 1) / C;
         const int c0 = min(rank * per, kChunks), c1 = min(c0 + per, kChunks);
-        for (int c = c0 + warp; c < c1; c += kNW) {
-            const int D = c * 32 + lane;
-            uint32_t n = place_count(D);
-            unsigned long long m = 0;
-            if (__any_sync(kAllLanes, n)) {
-                if (n)
-                    m = n * place_weight(D);
-                n = __reduce_add_sync(kAllLanes, n);
+        constexpr int L = 4;
+        for (int c = c0 + warp; c < c1; c += L * kNW) {
+            int D[L];
+            uint32_t n[L];
 #pragma unroll
-                for (int o = 16; o; o >>= 1)
-                    m += __shfl_xor_sync(kAllLanes, m, o);
-            }
-            if (lane == 0) {
-                sh.chunk_mass[c - c0] = m;
-                sh.chunk_cnt[c - c0] = n;
+            for (int j = 0; j < L; ++j)
+                D[j] = min(c + j * kNW, kChunks - 1) * 32 + lane;
+            place_counts<L>(D, n);
+#pragma unroll
+            for (int j = 0; j < L; ++j) {
+                if (c + j * kNW >= c1)
+                    break;
+                unsigned long long m = 0;
+                uint32_t all = 0;
+                if (__any_sync(kAllLanes, n[j])) {
+                    if (n[j])
+                        m = n[j] * place_weight(D[j]);
+                    all = __reduce_add_sync(kAllLanes, n[j]);
+                    // 62 bits in three parts, so that the lanes' sums fit 32
+                    m = (unsigned long long)__reduce_add_sync(kAllLanes, (uint32_t)m & 0x1fffffu) +
+                        ((unsigned long long)__reduce_add_sync(kAllLanes, (uint32_t)(m >> 21) & 0x1fffffu) << 21) +
+                        ((unsigned long long)__reduce_add_sync(kAllLanes, (uint32_t)(m >> 42)) << 42);
+                }
+                if (lane == 0) {
+                    sh.chunk_mass[c + j * kNW - c0] = m;
+                    sh.chunk_cnt[c + j * kNW - c0] = all;
+                }
             }
         }
         __syncthreads();
@@ -1073,22 +1163,18 @@ struct Kernel {
         uint32_t limit_key = 0;
         if (min_p > 0.0) {
             // the smallest float l with l - l_max >= T ln(min_p); bfloat16: the smallest of those
-            const float limit = __double2float_ru((double)scale.lmax + (double)T * log(min_p));
+            float limit = __double2float_ru((double)scale.lmax + (double)T * log(min_p));
             limit_key = logit_key(limit);
-            const uint32_t b = __float_as_uint(limit + 0.0f);
-            const int sign = b >> 31;
-            const int mag = (int)((b & 0x7fffffffu) >> 16) + (ES == 2 && !sign && (b & 0xffffu));
-            if (mag < kMag0 || mag >= kMag0 + kMags)
+            if (ES == 2 && limit > 0.0f && (__float_as_uint(limit) & 0xffffu))
+                limit = __uint_as_float((__float_as_uint(limit) & 0xffff0000u) + 0x10000u);
+            s.limit = place_of(limit);
+            if (s.limit < 1 || s.limit > kPlaces - 2 || s.limit == kFirstTiny || s.limit == kFirstTiny + 1)
                 return false;
-            const int i = mag - kMag0 + 1;
-            s.limit = kMags + 1 - (sign ? -1 - i : i);
         }
         Found f;
         f.bin = kNoPlace;
-        if (s.k || s.p || s.limit < kNoPlace) {
-            search_places(s, chunk, m, n, before_m, before_n);
-            f = first();
-        }
+        if (s.k || s.p || s.limit < kNoPlace)
+            f = search_places(0, s, chunk, m, n, before_m, before_n);
         unsigned long long mass = whole;  // kept
         int64_t kept = near;
         float cut = -3.402823466e38f;
@@ -1105,7 +1191,7 @@ struct Kernel {
             if (s.k)
                 return false;
             uint32_t more = 0;
-            each([&](float l, int64_t) { more += l <= -127.0f && l > __int_as_float(0xff800000); });
+            each([&](float l, uint32_t) { more += place_of(l) == kPlaces - 1 && l > __int_as_float(0xff800000); });
             more = __reduce_add_sync(kAllLanes, more);
             __syncthreads();
             if (lane == 0)
@@ -1126,19 +1212,22 @@ struct Kernel {
         if constexpr (ES == 4) {
             Band c, d;
             c.on = c.from_top = d.on = d.from_top = false;
+            c.above_count = 0;
             if (f.bin < kNoPlace) {
                 c = band_around(f);
                 if (!c.on)
                     return false;
             }
-            Wanted w;
-            w.k = 0;
-            w.limit = kNoPlace;
-            w.draw = true;
+            // float sums will do to tell whether an entry listed whole lies above top-p's
+            // border; not where they become part of the answer, or entries weigh too little
+            bool fine = !c.from_top || a.mass || (s.p && place_weight(f.bin) < whole >> 15);
             if (by_draw && !c.from_top) {
+                Wanted w;
+                w.k = 0;
+                w.limit = kNoPlace;
+                w.draw = true;
                 w.p = floor_scaled(u, mass);
-                search_places(w, chunk, m, n, before_m, before_n);
-                const Found h = first();
+                const Found h = search_places(1, w, chunk, m, n, before_m, before_n);
                 if (!c.on || place_end(h.bin, true) > c.hi) {
                     d = band_around(h);
                     if (!d.on)
@@ -1146,7 +1235,6 @@ struct Kernel {
                 }
             }
             cluster.sync();  // the lists lie over the places
-            unsigned long long sum[3] = {0, 0, 0};  // the row; above the cut's stretch; above the draw's
             const bool sums = top_p < 1.0 || !c.on || a.mass || !c.from_top;
             uint32_t *nc = cluster.map_shared_rank(&sh.list_n[0], 0), *nd = cluster.map_shared_rank(&sh.list_n[1], 0);
             unsigned long long *lc = cluster.map_shared_rank(list_at(0), 0),
@@ -1154,59 +1242,102 @@ struct Kernel {
             const float inf = __int_as_float(0x7f800000);
             const float clo = c.on ? c.lo : inf, chi = c.on ? c.hi : inf;
             const float dlo = d.on ? d.lo : inf, dhi = d.on ? d.hi : inf;
-            if (sums)
-                each([&](float l, int64_t id) {
-                    const unsigned long long x = weight_fixed(scale, sh.pow2, l);
-                    sum[0] += x;
-                    sum[1] += l > chi ? x : 0;
-                    sum[2] += l > dhi ? x : 0;
-                    if (l >= clo && l <= chi)
-                        offer(nc, lc, l, id);
-                    if (l >= dlo && l <= dhi)
-                        offer(nd, ld, l, id);
-                });
-            else
-                each([&](float l, int64_t id) {
-                    if (l >= clo)
-                        offer(nc, lc, l, id);
-                });
-            sum3(sum);
-            whole = sum[0];
-            Search q;
-            q.k = s.k;
-            q.top_p = top_p;
-            q.p = top_p < 1.0 ? ceil_scaled(top_p, whole) : 0;
-            if (rank == 0) {
-                bool ok = true;
-                Found g;
-                g.above_mass = sum[1];
-                g.above_count = c.above_count;
-                if (c.on) {
-                    sort(0);
-                    ok = limit_key <= logit_key(c.hi) && cut_in_list(q, g, limit_key, logit_key(c.lo));
-                } else if (tid == 0) {
-                    sh.kept_mass = whole;
-                    sh.cut_key = kKeyMinusInf + 1;
-                    sh.kept = 0;
+            const float low = fminf(clo, dlo);
+            const auto list = [&](float l, uint32_t id) {
+                if (l >= clo && l <= chi)
+                    offer(nc, lc, l, id);
+                if (l >= dlo && l <= dhi)
+                    offer(nd, ld, l, id);
+            };
+            unsigned long long sum[3];  // the row; above the cut's stretch; above the draw's
+            unsigned long long slack = 0;
+            bool listed = false;
+            for (;;) {
+                sum[0] = sum[1] = sum[2] = 0;
+                if (sums && fine) {
+                    each([&](float l, uint32_t id) {
+                        const unsigned long long x = weight_fixed(scale, sh.pow2, l);
+                        sum[0] += x;
+                        sum[1] += l > chi ? x : 0;
+                        sum[2] += l > dhi ? x : 0;
+                        if (l >= low && !listed)
+                            list(l, id);
+                    });
+                } else if (sums) {
+                    const float one = (float)(1ull << scale.fix);
+                    const auto fast = [&](float l) { return ex2_approx((l - scale.lmax) * scale.ch); };
+                    walk<4>(
+                        [&](const uint4& w, uint32_t id) {
+                            float t = 0.0f, top = -inf;
+#pragma unroll
+                            for (int e = 0; e < E; ++e) {
+                                t += fast(vector_entry<ES>(w, e));
+                                top = fmaxf(top, vector_entry<ES>(w, e));
+                            }
+                            sum[0] += __float2ull_rn(t * one);
+                            if (top >= clo) {
+#pragma unroll
+                                for (int e = 0; e < E; ++e)
+                                    list(vector_entry<ES>(w, e), id + e);
+                            }
+                        },
+                        [&](uint32_t id) {
+                            const float l = scalar_entry<ES>(base, id);
+                            sum[0] += __float2ull_rn(fast(l) * one);
+                            list(l, id);
+                        });
+                } else {
+                    each([&](float l, uint32_t id) {
+                        if (l >= clo)
+                            offer(nc, lc, l, id);
+                    });
                 }
-                __syncthreads();
-                if (ok && by_draw) {
-                    const unsigned long long target = floor_scaled(u, sh.kept_mass);
-                    if (c.on && target >= sum[1]) {
-                        ok = draw_in_list(0, sum[1], target);
-                    } else {
-                        if (d.on)
-                            sort(1);
-                        ok = d.on && draw_in_list(1, sum[2], target);
+                sum3(sum);
+                whole = sum[0];
+                slack = sums && !fine ? whole >> 17 : 0;
+                if (rank == 0) {
+                    int ok = 1;  // 0: not in the lists, 2: too near a border for these sums
+                    Search q;
+                    q.k = s.k;
+                    q.top_p = top_p;
+                    q.p = top_p < 1.0 ? ceil_scaled(top_p, whole) : 0;
+                    Found g;
+                    g.above_mass = sum[1];
+                    g.above_count = c.above_count;
+                    if (c.on) {
+                        if (!listed)
+                            sort(0);
+                        ok = limit_key <= logit_key(c.hi) ? cut_in_list(q, g, limit_key, logit_key(c.lo), slack) : 0;
+                    } else if (tid == 0) {
+                        sh.kept_mass = whole;
+                        sh.cut_key = kKeyMinusInf + 1;
+                        sh.kept = 0;
                     }
+                    __syncthreads();
+                    if (ok == 1 && by_draw) {
+                        const unsigned long long target = floor_scaled(u, sh.kept_mass);
+                        if (c.on && target >= sum[1]) {
+                            ok = draw_in_list(0, sum[1], target);
+                        } else {
+                            if (d.on)
+                                sort(1);
+                            ok = d.on && draw_in_list(1, sum[2], target);
+                        }
+                    }
+                    if (tid == 0)
+                        sh.ok = ok;
+                    __syncthreads();
                 }
-                if (tid == 0)
-                    sh.ok = ok;
-                __syncthreads();
+                share_cut();
+                const uint32_t ok = sh.ok;
+                if (ok == 0)
+                    return false;
+                if (ok == 1)
+                    break;
+                fine = true;
+                listed = true;
+                cluster.sync();  // everyone has read `ok`
             }
-            share_cut();
-            if (!sh.ok)
-                return false;
             mass = sh.kept_mass;
             if (c.on)
                 kept = sh.kept;
@@ -1219,8 +1350,7 @@ struct Kernel {
                 s.limit = kNoPlace;
                 s.draw = true;
                 s.p = floor_scaled(u, mass);
-                search_places(s, chunk, m, n, before_m, before_n);
-                const Found d = first();
+                const Found d = search_places(1, s, chunk, m, n, before_m, before_n);
                 if (d.bin == kFirstTiny || d.bin == kFirstTiny + 1)
                     return false;
                 const float l = place_value(d.bin);
@@ -1231,7 +1361,7 @@ struct Kernel {
                 a_token(sh.token, weight_float(scale, key_logit(sh.token_key)) * inv);
             }
         }
-        write([&](float l, int64_t) { return l >= cut; }, cut, inv, false);
+        write([&](float l, uint32_t) { return l >= cut; }, cut, inv, false);
         finish(SV_OK, (uint32_t)kept, (float)((double)mass / (double)whole));
         return true;
     }
@@ -1285,10 +1415,16 @@ struct Kernel {
             cluster.sync();  // no CTA leaves while another may still read its memory
             return;
         }
+        if (met)
+            cluster.sync();  // every CTA is done with what it was told
+        general(code, T, top_k, top_p, min_p, u);
+    }
 
+    // The call for any row, and for an erroneous one.
+    __device__ __forceinline__ void general(int code, float T, int32_t top_k, double top_p, double min_p, float u) {
         // A. the largest logit (NaN if there is one), over the cluster
         float m = __int_as_float(0xff800000);
-        each([&](float l, int64_t) { m = max_nan(m, l); });
+        each([&](float l, uint32_t) { m = max_nan(m, l); });
 #pragma unroll
         for (int o = 16; o; o >>= 1)
             m = max_nan(m, __shfl_xor_sync(kAllLanes, m, o));
@@ -1308,7 +1444,7 @@ struct Kernel {
         scale.lmax = m;
         if (code) {
             const float nan = __int_as_float(0x7fffffff);
-            write([](float, int64_t) { return false; }, 0.0f, 0.0f, true);
+            write([](float, uint32_t) { return false; }, 0.0f, 0.0f, true);
             if (rank == 0 && tid == 0)
                 a_token(-1, nan);
             finish(code, 0, nan);
@@ -1317,9 +1453,9 @@ struct Kernel {
         }
         if (T == 0.0f) {
             uint32_t id = 0xffffffffu;
-            each([&](float l, int64_t i) {
+            each([&](float l, uint32_t i) {
                 if (l == m)
-                    id = min(id, (uint32_t)i);
+                    id = min(id, i);
             });
             id = __reduce_min_sync(kAllLanes, id);
             __syncthreads();
@@ -1333,7 +1469,7 @@ struct Kernel {
             cluster.sync();
             for (int r = 0; r < C; ++r)
                 id = min(id, sh.part_cnt[r]);
-            write([=](float, int64_t i) { return (uint32_t)i == id; }, m, 0.0f, false);
+            write([=](float, uint32_t i) { return i == id; }, m, 0.0f, false);
             if (rank == 0 && tid == 0)
                 a_token(id, 1.0f);
             finish(SV_OK, 1, 1.0f);
@@ -1375,7 +1511,7 @@ struct Kernel {
             if (g.count <= kList) {
                 gather(klo, khi);
                 if (rank == 0)
-                    cut_in_list(s, g, limit_key, klo);
+                    cut_in_list(s, g, limit_key, klo, 0);
                 share_cut();
                 cut_key = sh.cut_key;
                 kept = sh.kept;
@@ -1435,7 +1571,7 @@ struct Kernel {
         }
         // D. rows out
         const float cut = key_logit(cut_key);
-        write([&](float l, int64_t) { return l >= cut; }, cut, inv, false);
+        write([&](float l, uint32_t) { return l >= cut; }, cut, inv, false);
         finish(SV_OK, kept, (float)((double)E / (double)whole));
         cluster.sync();  // no CTA leaves while another may still write into it
     }
@@ -1460,11 +1596,6 @@ int launch(sv_ctx* ctx, Args& a, int B, int rows, int64_t V, int dtype, cudaStre
     a.C = plan.cluster;
     a.rows_per_seq = rows;
     a.fix = weight_bits(V);
-    a.vec = aligned(a.logits, 16) && (a.stride * es) % 16 == 0 ? 1 : 0;
-    a.out_vec = (!a.probs || (aligned(a.probs, 16) && a.probs_stride % 4 == 0)) &&
-                        (!a.out || (aligned(a.out, 16) && (a.out_stride * es) % 16 == 0))
-                    ? 1
-                    : 0;
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof cfg);
     cfg.gridDim = dim3((unsigned)plan.grid, 1, 1);

@@ -35,7 +35,8 @@ int plan_rows(int num_sms, int max_cluster, int B, int rows_per_seq, int64_t V, 
     out->group = 1;
     out->threads = threads;
     out->smem_bytes = 0;
-    out->slice = round_up(ceil_div(V, C), kSliceAlign);
+    // slices are cut between 16-byte vectors: a row may begin up to seven entries into one
+    out->slice = round_up(ceil_div(V + 7, C), kSliceAlign);
     out->grid = rows * C;
     out->bulk_copy = ((V * (dtype == SV_BF16 ? 2 : 4)) % 16) == 0 ? 1 : 0;
     out->prefetch_next = 0;
