@@ -146,9 +146,9 @@ __device__ __forceinline__ float weight_float(const RowScale& s, float l) {
 
 // c = log2(e)/T as the sum of two floats
 __device__ __forceinline__ void split_scale(float T, float& ch, float& cl) {
-    const double c = 1.4426950408889634074 / (double)T;
-    ch = (float)c;
-    cl = (float)(c - (double)ch);
+    constexpr float kLog2eh = 1.44269502162933349609375f, kLog2el = 1.9259629911266174e-8f;
+    ch = __fdiv_rn(kLog2eh, T);
+    cl = __fdiv_rn(fmaf(-ch, T, kLog2eh) + kLog2el, T);
 }
 
 // floor(u x) and ceil(p x) with no rounding before the last step.
