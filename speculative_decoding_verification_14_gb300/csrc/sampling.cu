@@ -134,9 +134,12 @@ __device__ __noinline__ uint32_t count_pass(Shared* sh) {
 __device__ __forceinline__ int chunks_per(int C) { return (kChunks + C - 1) / C; }
 __device__ __forceinline__ int first_chunk(int C, int rank) { return min(rank * chunks_per(C), kChunks); }
 
-// The cluster's counts at a CTA's range of places, which lie behind its shared
-// memory (a lone CTA's are its own).
-__device__ __forceinline__ uint32_t* merged(Shared* sh) { return reinterpret_cast<uint32_t*>(sh + 1); }
+// A CTA's chunks, and the cluster's counts at its range of places, which lie behind its
+// shared memory (a lone CTA's are its own).
+__device__ __forceinline__ Chunk* chunks(Shared* sh) { return reinterpret_cast<Chunk*>(sh + 1); }
+__device__ __forceinline__ uint32_t* merged(Shared* sh) {
+    return reinterpret_cast<uint32_t*>(chunks(sh) + chunks_per(sh->args.C));
+}
 
 // entries at place D of this CTA's range, which begins at place `first`; of any CTA's
 __device__ __forceinline__ uint32_t own_count(Shared* sh, int C, int first, int D) {
@@ -217,8 +220,8 @@ __device__ __noinline__ void weigh_places(Shared* sh) {
             m = warp_sum(m);
         }
         if (lane == 0) {
-            sh->chunk_mass[c - c0] = m;
-            sh->chunk_cnt[c - c0] = n;
+            chunks(sh)[c - c0].mass = m;
+            chunks(sh)[c - c0].cnt = n;
         }
     }
     if constexpr (ES == 4) {
@@ -234,17 +237,17 @@ __device__ __noinline__ void weigh_places(Shared* sh) {
         unsigned long long m = 0;
         uint32_t n = 0;
         for (int i = i0; i < i1; ++i) {
-            m += sh->chunk_mass[i];
-            n += sh->chunk_cnt[i];
+            m += chunks(sh)[i].mass;
+            n += chunks(sh)[i].cnt;
         }
         const Prefix x = warp_prefix(m, n);
         m = x.before_mass;
         n = x.before_count;
         for (int i = i0; i < i1; ++i) {
-            sh->chunk_above_mass[i] = m;
-            sh->chunk_above_cnt[i] = n;
-            m += sh->chunk_mass[i];
-            n += sh->chunk_cnt[i];
+            chunks(sh)[i].above_mass = m;
+            chunks(sh)[i].above_cnt = n;
+            m += chunks(sh)[i].mass;
+            n += chunks(sh)[i].cnt;
         }
         m = __shfl_sync(kAllLanes, x.mass, 31);
         n = __shfl_sync(kAllLanes, x.count, 31);
@@ -279,14 +282,14 @@ __device__ __noinline__ Found search_places(Shared* sh, int set, const Wanted s)
     const int c0 = first_chunk(C, rank), c1 = first_chunk(C, rank + 1);
     static_assert(kChunks <= kNT, "a thread per chunk");
     if (tid < c1 - c0) {
-        unsigned long long before_m = sh->chunk_above_mass[tid];
-        uint32_t before_n = sh->chunk_above_cnt[tid];
+        unsigned long long before_m = chunks(sh)[tid].above_mass;
+        uint32_t before_n = chunks(sh)[tid].above_cnt;
         for (int r = 0; r < rank; ++r) {
             before_m += sh->part_mass[r];
             before_n += sh->part_cnt[r];
         }
-        const unsigned long long after_m = before_m + sh->chunk_mass[tid];
-        const uint32_t after_n = before_n + sh->chunk_cnt[tid];
+        const unsigned long long after_m = before_m + chunks(sh)[tid].mass;
+        const uint32_t after_n = before_n + chunks(sh)[tid].cnt;
         const Hit h = {c0 + tid, before_n, before_m};
         if (s.k && before_n < s.k && after_n >= s.k)
             sh->hit[set][kByCount] = h;
@@ -573,10 +576,10 @@ __device__ __noinline__ void settle(Shared* sh, bool by_mass, bool exact, bool f
         sh->sums[tid][0] = x;
     }
     __syncthreads();
-    if (first) {
+    if (first && sh->band[0].on)
         pull_list(sh, 0);
+    if (first && sh->band[1].on)
         pull_list(sh, 1);
-    }
     int ok = 3;  // 3: the draw is not in this list
     if (sh->band[0].on) {
         if (tid == 0) {
@@ -729,7 +732,7 @@ __device__ __noinline__ bool count_places(Shared* sh) {
     if (tid == 0)
         sh->scale = scale;
     __syncthreads();
-    if (key == 0xffffffffu || !inside(place_of(scale.lmax)))
+    if (sh->code || key == 0xffffffffu || !inside(place_of(scale.lmax)))
         return false;
     if (T == 0.0f)
         return ES == 2;
@@ -903,54 +906,35 @@ __device__ __forceinline__ bool by_place(Shared* sh) {
 }
 
 template <int ES>
-__device__ __noinline__ void general_row(Shared* sh, int code, bool met) {
+__device__ __noinline__ void general_row(Shared* sh, int code) {
     sh = here();
     General<ES> g(sh);
-    g.run(code, met);
+    g.run(code);
 }
 
-// What the row's parts need to know, by the first thread and one of the second warp.
+// What the row's parts need to know: where it lies, by the first thread; its
+// settings, by one of the second warp, which nothing waits for before the counts are taken.
 template <int ES>
 __device__ __forceinline__ void set_up(Shared* sh, const Args& a) {
     const int tid = threadIdx.x;
+    const uint32_t row = blockIdx.x / a.C;
     if (tid == 0) {
-        const uint32_t row = blockIdx.x / a.C;
-        const int64_t seq = row / (uint32_t)a.rows_per_seq;
-        const float T = a.set.temperatures ? a.set.temperatures[seq] : a.set.temperature;
-        const int32_t k = a.set.top_ks ? a.set.top_ks[seq] : a.set.top_k;
-        const double top_p = a.set.top_ps ? (double)a.set.top_ps[seq] : a.set.top_p;
-        const double min_p = a.set.min_ps ? (double)a.set.min_ps[seq] : a.set.min_p;
-        const float u = a.u ? a.u[row * a.u_stride] : 0.0f;
         constexpr int E = View<ES>::E;
-        sh->args = a;
-        sh->row = row;
         const unsigned char* base = static_cast<const unsigned char*>(a.logits) + (int64_t)row * a.stride * ES;
         const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(base) & 15u) / ES;
         const int64_t v0 = cta_rank() * a.slice - off, v1 = v0 + a.slice;
         const uint32_t s0 = (uint32_t)(v0 < 0 ? 0 : v0 < a.V ? v0 : a.V), s1 = (uint32_t)(v1 < a.V ? v1 : a.V);
+        sh->args = a;
+        sh->row = row;
         sh->base = base;
         sh->s0 = s0;
         sh->s1 = s1;
         sh->off = off;
         sh->k0 = (s0 + off + E - 1) / E;
         sh->k1 = max((s1 + off) / E, sh->k0);
-        sh->T = T;
-        sh->u = u;
-        sh->k = k > 0 ? (uint32_t)k : 0;
-        sh->top_p = top_p;
-        sh->has_min = min_p > 0.0;
         sh->want_limit = 0;
-        sh->code = !(T == 0.0f || (T >= 1.17549435e-38f && T <= 3.402823466e38f)) || !(top_p > 0.0) || !(min_p < 1.0)
-                       ? SV_ERR_INVALID_ARG
-                   : !(u >= 0.0f && u < 1.0f) ? SV_ERR_UNIFORM_RANGE
-                                              : SV_OK;
         const float inf = __int_as_float(0x7f800000);
         sh->band[0] = sh->band[1] = {inf, inf, 0, false, false};
-    } else if (tid == 32) {
-        const int64_t seq = blockIdx.x / a.C / (uint32_t)a.rows_per_seq;
-        const double min_p = a.set.min_ps ? (double)a.set.min_ps[seq] : a.set.min_p;
-        if (min_p > 0.0)
-            sh->dmin = (double)(a.set.temperatures ? a.set.temperatures[seq] : a.set.temperature) * log(min_p);
     } else if (tid >= 64 && tid < 128) {
         sh->pow2[tid - 64] = kPow2Steps[tid - 64];
     } else if (tid >= 128 && tid < 128 + 2 * kConds) {
@@ -963,6 +947,25 @@ __device__ __forceinline__ void set_up(Shared* sh, const Args& a) {
     for (int i = tid; i < kPlaces / 4; i += kNT)
         z[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
+    if (tid == 32) {
+        const int64_t seq = row / (uint32_t)a.rows_per_seq;
+        const float T = a.set.temperatures ? a.set.temperatures[seq] : a.set.temperature;
+        const int32_t k = a.set.top_ks ? a.set.top_ks[seq] : a.set.top_k;
+        const double top_p = a.set.top_ps ? (double)a.set.top_ps[seq] : a.set.top_p;
+        const double min_p = a.set.min_ps ? (double)a.set.min_ps[seq] : a.set.min_p;
+        const float u = a.u ? a.u[row * a.u_stride] : 0.0f;
+        sh->T = T;
+        sh->u = u;
+        sh->k = k > 0 ? (uint32_t)k : 0;
+        sh->top_p = top_p;
+        sh->has_min = min_p > 0.0;
+        sh->code = !(T == 0.0f || (T >= 1.17549435e-38f && T <= 3.402823466e38f)) || !(top_p > 0.0) || !(min_p < 1.0)
+                       ? SV_ERR_INVALID_ARG
+                   : !(u >= 0.0f && u < 1.0f) ? SV_ERR_UNIFORM_RANGE
+                                              : SV_OK;
+        if (min_p > 0.0)
+            sh->dmin = (double)T * log(min_p);
+    }
 }
 
 template <int ES>
@@ -970,20 +973,20 @@ __global__ void __launch_bounds__(kNT, 4) sv_sample_kernel(const __grid_constant
     Shared* sh = here();
     the_cluster().barrier_arrive();
     set_up<ES>(sh, a);
-    const int code = sh->code;
-    if (!code && by_place<ES>(sh)) {
+    if (by_place<ES>(sh)) {
         the_cluster().sync();  // no CTA leaves while another may still read its memory
         return;
     }
-    if (!code)
-        the_cluster().sync();  // every CTA is done with what it was told
-    general_row<ES>(sh, code, !code);
+    the_cluster().sync();  // every CTA is done with what it was told
+    general_row<ES>(sh, sh->code);
 }
 
-// with the cluster's counts at a CTA's share of the places
+// with a CTA's chunks of places, and the cluster's counts at them
 size_t shared_size(int cluster) {
-    return sizeof(Shared) + (cluster > 1 ? (size_t)((kChunks + cluster - 1) / cluster) * 32 * sizeof(uint32_t) : 0);
+    const size_t chunks = (size_t)((kChunks + cluster - 1) / cluster);
+    return sizeof(Shared) + chunks * (sizeof(Chunk) + (cluster > 1 ? 32 * sizeof(uint32_t) : 0));
 }
+static_assert(4 * (sizeof(Shared) + kChunks / 2 * (sizeof(Chunk) + 128) + 1024) <= 233472, "four CTAs per SM");
 
 int launch(sv_ctx* ctx, Args& a, int B, int rows, int64_t V, int dtype, cudaStream_t stream) {
     sv_plan plan;

@@ -218,6 +218,21 @@ __device__ __forceinline__ float max_nan(float x, float y) {
     return d;
 }
 
+// The largest of a vector's logits.
+template <int ES>
+__device__ __forceinline__ float vector_max(const uint4& v) {
+    if constexpr (ES == 4) {
+        return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)),
+                     fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+    } else {
+        uint32_t m, x;
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(v.x), "r"(v.y));
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(x) : "r"(v.z), "r"(v.w));
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(x));
+        return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+    }
+}
+
 #endif  // __CUDACC__
 
 }  // namespace sv

@@ -259,7 +259,7 @@ struct General {
 
 
 
-    __device__ __forceinline__ void run(int code, bool met) {
+    __device__ __forceinline__ void run(int code) {
         const float T = sh->T;
         // A. the largest logit (NaN if there is one), over the cluster
         float m = __int_as_float(0xff800000);
@@ -272,8 +272,6 @@ struct General {
         __syncthreads();
         for (int w = 0; w < kNW; ++w)
             m = max_nan(m, __uint_as_float(sh->warp_max[w]));
-        if (!met)
-            the_cluster().barrier_wait();  // every CTA runs: its memory may be written
         if (tid < C)
             *peer(&sh->part_max[rank], tid) = __float_as_uint(m);
         the_cluster().sync();

@@ -80,6 +80,11 @@ struct Hit {  // the chunk of places that holds the end of a condition, and what
     unsigned long long above_mass;
 };
 
+struct Chunk {  // 32 places: their sums, and what lies above them in the CTA
+    unsigned long long mass, above_mass;
+    uint32_t cnt, above_cnt;
+};
+
 struct Band {  // a stretch of places that a list may hold
     float lo, hi;  // its logits; +inf: none
     uint32_t above_count;
@@ -94,8 +99,8 @@ struct Cut {
     unsigned long long p, above_mass, slack;
 };
 
-// A CTA's shared memory, followed by the cluster's counts at this CTA's range of
-// places when the cluster has more than one CTA.
+// A CTA's shared memory, followed by its chunks of places and, when the cluster has
+// more than one CTA, the cluster's counts at them.  Four CTAs share an SM's 227 KB.
 struct alignas(16) Shared {
     union {
         struct {
@@ -126,8 +131,6 @@ struct alignas(16) Shared {
     uint32_t near, kept_n;  // entries counted; kept
     float cut;
     Cut want;  // for the lists
-    unsigned long long chunk_mass[kChunks], chunk_above_mass[kChunks];
-    uint32_t chunk_cnt[kChunks], chunk_above_cnt[kChunks];
     Hit hit[2][kConds];  // of the search for the cut and of that for the draw
     Found place[2][kConds];
     Found found[kConds];
@@ -263,17 +266,28 @@ struct View {
     __device__ __forceinline__ uint32_t tail_start() const { return min(max(k1 * E - off, head_end()), s1); }
 
     // vec(w, id of its first logit) for every vector of the slice, one(id) for every
-    // other logit.  D loads are in flight; `Rolled` keeps one copy of vec's code.
+    // other logit.  The next D vectors are loaded before D are worked on; `Rolled` keeps
+    // one copy of vec's code.
     template <int D, bool Rolled, class Vec, class One>
     __device__ __forceinline__ void walk(Vec&& vec, One&& one) const {
         const int tid = threadIdx.x;
         const uint4* p = vectors() + k0 + tid;
-        for (uint32_t k = k0 + tid; k < k1; k += D * kNT, p += D * kNT) {
-            uint4 w[D];
+        uint4 next[D];
+        const auto load = [&](uint32_t k) {
 #pragma unroll
             for (int j = 0; j < D; ++j)
                 if (k + j * kNT < k1)
-                    w[j] = load_stream(p + j * kNT);
+                    next[j] = load_stream(p + j * kNT);
+            p += D * kNT;
+        };
+        load(k0 + tid);
+#pragma unroll 1
+        for (uint32_t k = k0 + tid; k < k1; k += D * kNT) {
+            uint4 w[D];
+#pragma unroll
+            for (int j = 0; j < D; ++j)
+                w[j] = next[j];
+            load(k + D * kNT);
             if constexpr (Rolled) {
 #pragma unroll 1
                 for (int j = 0; j < D && k + j * kNT < k1; ++j) {
@@ -578,11 +592,7 @@ __device__ __noinline__ void write_rows(Shared* sh, Keep how, float cut, float i
     }
     v.template walk<4, true>(
         [&](const uint4& w, uint32_t id) {
-            float m = vector_entry<ES>(w, 0);
-#pragma unroll
-            for (int e = 1; e < E; ++e)
-                m = fmaxf(m, vector_entry<ES>(w, e));
-            const bool any = bad || m >= cut;
+            const bool any = bad || vector_max<ES>(w) >= cut;
             if (p) {
                 float4* q = reinterpret_cast<float4*>(p + id);
                 if (!any) {
