@@ -48,8 +48,8 @@ struct Args {
     int32_t* status;
     uint32_t* err_word;
     int64_t V, slice;
-    int rows_per_seq, C, vec, top_n;
-    float T, ch, cl;
+    int rows_per_seq, C, top_n;
+    float T, ch;
 };
 
 struct Shared {
@@ -63,15 +63,50 @@ struct Shared {
     unsigned long long warp_best[kNW];
 };
 
-__device__ __forceinline__ unsigned long long order_of(float l, int64_t id) {
-    return ((unsigned long long)logit_key(l) << 32) | (uint32_t)~(uint32_t)id;
+__device__ __forceinline__ unsigned long long order_of(float l, uint32_t id) {
+    return ((unsigned long long)logit_key(l) << 32) | (uint32_t)~id;
+}
+
+// sum of 2^((l - m) c) over a vector's logits: differences (a bfloat16 operand is
+// widened inside the subtraction), products and sums two at a time
+template <int ES>
+__device__ __forceinline__ float exp_sum(const uint4& v, float m, float c) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    unsigned long long cc, sum = 0;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(cc) : "f"(c));
+#pragma unroll
+    for (int j = 0; j < 8 / ES; ++j) {
+        float lo, hi;
+        if constexpr (ES == 2) {
+            asm("{\n\t.reg .b16 l, h;\n\t"
+                "mov.b32 {l, h}, %2;\n\t"
+                "add.rn.f32.bf16 %0, l, %3;\n\t"
+                "add.rn.f32.bf16 %1, h, %3;\n\t}"
+                : "=f"(lo), "=f"(hi)
+                : "r"(w[j]), "f"(-m));
+        } else {
+            lo = __uint_as_float(w[2 * j]) - m;
+            hi = __uint_as_float(w[2 * j + 1]) - m;
+        }
+        unsigned long long t;
+        asm("{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\tmul.rn.f32x2 %0, d, %3;\n\t}" : "=l"(t) : "f"(lo), "f"(hi), "l"(cc));
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(t));
+        asm("mov.b64 %0, {%1, %2};" : "=l"(t) : "f"(ex2_approx(lo)), "f"(ex2_approx(hi)));
+        if (j)
+            asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum) : "l"(t));
+        else
+            sum = t;
+    }
+    float lo, hi;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(sum));
+    return lo + hi;
 }
 
 template <int ES>
 __global__ void __launch_bounds__(kNT, 4) sv_logprobs_kernel(const __grid_constant__ Args a) {
     __shared__ Shared sh;
     cg::cluster_group cluster = cg::this_cluster();
-    constexpr int E = 16 / ES, D = 4;
+    constexpr int E = 16 / ES;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int C = a.C, rank = (int)cluster.block_rank(), n = a.top_n;
     const int64_t row = blockIdx.x / C, seq = row / a.rows_per_seq;
@@ -105,43 +140,39 @@ __global__ void __launch_bounds__(kNT, 4) sv_logprobs_kernel(const __grid_consta
     }
     const unsigned char* base = static_cast<const unsigned char*>(a.logits) + row * a.stride * ES;
     const float lx = scalar_entry<ES>(base, x);
-    const int64_t s0 = rank * a.slice < a.V ? rank * a.slice : a.V;
-    const int64_t s1 = s0 + a.slice < a.V ? s0 + a.slice : a.V;
-    const int64_t v1 = a.vec ? s1 / E : 0, tail = a.vec ? v1 * E : s0;
-    const uint4* vp = reinterpret_cast<const uint4*>(base);
+    const Slice<ES, kNT> v(base, a.V, a.slice, rank);
 
     cluster.barrier_arrive();
 
     // the pass over the slice
     float m = -inf, s = 0.0f;
     uint32_t above = 0;
-    const auto take = [&](float l) {
-        above += l > lx;
-        if (!(l <= m)) {  // a new maximum, or a NaN, which stays
-            const float grown = max_nan(m, l);
-            s = m > -inf ? s * ex2_approx((m - grown) * a.ch) : 0.0f;
-            m = grown;
-        }
-        if (l > -inf)
-            s += ex2_approx((l - m) * a.ch);
+    const auto grow = [&](float top) {  // a new maximum, or a NaN, which stays
+        const float grown = max_nan(m, top);
+        s = m > -inf ? s * ex2_approx((m - grown) * a.ch) : 0.0f;
+        m = grown;
     };
-    if (a.vec)
-        for (int64_t v = s0 / E + tid; v < v1; v += D * kNT) {
-            uint4 w[D];
+    v.template walk<4, false>(
+        [&](const uint4& w, uint32_t) {
+            const float top = vector_max_nan<ES>(w);
+            if (!(top <= m))
+                grow(top);
+            if (top > lx) {
 #pragma unroll
-            for (int k = 0; k < D; ++k)
-                if (v + k * kNT < v1)
-                    w[k] = load_stream(vp + v + k * kNT);
-#pragma unroll
-            for (int k = 0; k < D; ++k)
-                if (v + k * kNT < v1) {
-#pragma unroll
-                    for (int e = 0; e < E; ++e)
-                        take(vector_entry<ES>(w[k], e));
-                }
-        }
-    for (int64_t i = tail + tid; i < s1; i += kNT)
-        take(scalar_entry<ES>(base, i));
+                for (int e = 0; e < E; ++e)
+                    above += vector_entry<ES>(w, e) > lx;
+            }
+            if (top > -inf)  // else m may be -inf too
+                s += exp_sum<ES>(w, m, a.ch);
+        },
+        [&](uint32_t id) {
+            const float l = scalar_entry<ES>(base, id);
+            above += l > lx;
+            if (!(l <= m))
+                grow(l);
+            if (l > -inf)
+                s += ex2_approx((l - m) * a.ch);
+        });
     const float mine = m;
 
     // join the threads, then the CTAs
@@ -189,30 +220,23 @@ __global__ void __launch_bounds__(kNT, 4) sv_logprobs_kernel(const __grid_consta
         if (bound <= kKeyMinusInf)
             bound = kKeyMinusInf + 1;
         if (key >= bound) {
-            const auto offer = [&](float l, int64_t id) {
+            const auto offer = [&](float l, uint32_t id) {
                 if (logit_key(l) >= bound) {
                     const uint32_t at = atomicAdd(&sh.list_n, 1u);
                     if (at < (uint32_t)kList)
                         sh.list[at] = order_of(l, id);
                 }
             };
-            if (a.vec)
-                for (int64_t v = s0 / E + tid; v < v1; v += D * kNT) {
-                    uint4 w[D];
+            const float least = key_logit(bound);
+            v.template walk<4, true>(
+                [&](const uint4& w, uint32_t id) {
+                    if (vector_max<ES>(w) >= least) {
 #pragma unroll
-                    for (int k = 0; k < D; ++k)
-                        if (v + k * kNT < v1)
-                            w[k] = load_stream(vp + v + k * kNT);
-#pragma unroll
-                    for (int k = 0; k < D; ++k)
-                        if (v + k * kNT < v1) {
-#pragma unroll
-                            for (int e = 0; e < E; ++e)
-                                offer(vector_entry<ES>(w[k], e), (v + k * kNT) * E + e);
-                        }
-                }
-            for (int64_t i = tail + tid; i < s1; i += kNT)
-                offer(scalar_entry<ES>(base, i), i);
+                        for (int e = 0; e < E; ++e)
+                            offer(vector_entry<ES>(w, e), id + e);
+                    }
+                },
+                [&](uint32_t id) { offer(scalar_entry<ES>(base, id), id); });
         }
         __syncthreads();
         const uint32_t got = sh.list_n;
@@ -234,7 +258,7 @@ __global__ void __launch_bounds__(kNT, 4) sv_logprobs_kernel(const __grid_consta
             unsigned long long last = ~0ull;
             for (int r = 0; r < n; ++r) {
                 unsigned long long o = 0;
-                for (int64_t i = s0 + tid; i < s1; i += kNT) {
+                for (uint32_t i = v.s0 + tid; i < v.s1; i += kNT) {
                     const unsigned long long y = order_of(scalar_entry<ES>(base, i), i);
                     if (y < last && y > o && (uint32_t)(y >> 32) > kKeyMinusInf)
                         o = y;
@@ -371,7 +395,6 @@ int spec_logprobs_run(sv_ctx* ctx, const void* target_logits, int logits_dtype,
     a.slice = plan.slice;
     a.rows_per_seq = rows_per_seq;
     a.C = plan.cluster;
-    a.vec = aligned(target_logits, 16) && (logits_stride * es) % 16 == 0 ? 1 : 0;
     a.top_n = top_n;
     a.T = temperature;
     a.ch = (float)(1.4426950408889634074 / (double)temperature);

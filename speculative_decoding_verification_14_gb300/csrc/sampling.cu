@@ -919,19 +919,16 @@ __device__ __forceinline__ void set_up(Shared* sh, const Args& a) {
     const int tid = threadIdx.x;
     const uint32_t row = blockIdx.x / a.C;
     if (tid == 0) {
-        constexpr int E = View<ES>::E;
-        const unsigned char* base = static_cast<const unsigned char*>(a.logits) + (int64_t)row * a.stride * ES;
-        const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(base) & 15u) / ES;
-        const int64_t v0 = cta_rank() * a.slice - off, v1 = v0 + a.slice;
-        const uint32_t s0 = (uint32_t)(v0 < 0 ? 0 : v0 < a.V ? v0 : a.V), s1 = (uint32_t)(v1 < a.V ? v1 : a.V);
+        const Slice<ES, kNT> v(static_cast<const unsigned char*>(a.logits) + (int64_t)row * a.stride * ES, a.V, a.slice,
+                              cta_rank());
         sh->args = a;
         sh->row = row;
-        sh->base = base;
-        sh->s0 = s0;
-        sh->s1 = s1;
-        sh->off = off;
-        sh->k0 = (s0 + off + E - 1) / E;
-        sh->k1 = max((s1 + off) / E, sh->k0);
+        sh->base = v.base;
+        sh->s0 = v.s0;
+        sh->s1 = v.s1;
+        sh->off = v.off;
+        sh->k0 = v.k0;
+        sh->k1 = v.k1;
         sh->want_limit = 0;
         const float inf = __int_as_float(0x7f800000);
         sh->band[0] = sh->band[1] = {inf, inf, 0, false, false};

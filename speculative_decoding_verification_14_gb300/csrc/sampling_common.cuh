@@ -218,7 +218,7 @@ __device__ __forceinline__ float max_nan(float x, float y) {
     return d;
 }
 
-// The largest of a vector's logits.
+// The largest of a vector's logits, whatever NaNs it holds; NaN if it holds one.
 template <int ES>
 __device__ __forceinline__ float vector_max(const uint4& v) {
     if constexpr (ES == 4) {
@@ -232,6 +232,103 @@ __device__ __forceinline__ float vector_max(const uint4& v) {
         return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
     }
 }
+template <int ES>
+__device__ __forceinline__ float vector_max_nan(const uint4& v) {
+    if constexpr (ES == 4) {
+        return max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)),
+                       max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
+    } else {
+        uint32_t m, x;
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(v.x), "r"(v.y));
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(x) : "r"(v.z), "r"(v.w));
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(x));
+        return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+    }
+}
+
+// One CTA's part of a row: ids s0..s1-1, and its 16-byte vectors.  Number k holds the
+// ids from k E - off on, where off is the place of the row's first logit in its own
+// vector.  What they leave at the part's ends (the row's ends: parts meet between
+// vectors) is taken one by one.  NT: threads of the CTA.
+template <int ES, int NT>
+struct Slice {
+    static constexpr int E = 16 / ES;
+    const unsigned char* base;  // the row's first logit
+    uint32_t s0, s1, off, k0, k1;
+
+    Slice() = default;
+    // part `rank` of parts of `slice` ids (a multiple of E, and together V + E - 1 at least)
+    __device__ __forceinline__ Slice(const unsigned char* row, int64_t V, int64_t slice, int rank) : base(row) {
+        off = (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15u) / ES;
+        const int64_t v0 = rank * slice - off, v1 = v0 + slice;
+        s0 = (uint32_t)(v0 < 0 ? 0 : v0 < V ? v0 : V);
+        s1 = (uint32_t)(v1 < V ? v1 : V);
+        k0 = (s0 + off + E - 1) / E;
+        k1 = max((s1 + off) / E, k0);
+    }
+
+    __device__ __forceinline__ const uint4* vectors() const {
+        return reinterpret_cast<const uint4*>(base - (size_t)off * ES);
+    }
+    __device__ __forceinline__ uint32_t head_end() const { return min(k0 * E - off, s1); }
+    __device__ __forceinline__ uint32_t tail_start() const { return min(max(k1 * E - off, head_end()), s1); }
+
+    // vec(w, id of its first logit) for every vector of the slice, one(id) for every
+    // other logit.  The next D vectors are loaded before D are worked on; `Rolled` keeps
+    // one copy of vec's code.
+    template <int D, bool Rolled, class Vec, class One>
+    __device__ __forceinline__ void walk(Vec&& vec, One&& one) const {
+        const int tid = threadIdx.x;
+        const uint4* p = vectors() + k0 + tid;
+        uint4 next[D];
+        const auto load = [&](uint32_t k) {
+#pragma unroll
+            for (int j = 0; j < D; ++j)
+                if (k + j * NT < k1)
+                    next[j] = load_stream(p + j * NT);
+            p += D * NT;
+        };
+        load(k0 + tid);
+#pragma unroll 1
+        for (uint32_t k = k0 + tid; k < k1; k += D * NT) {
+            uint4 w[D];
+#pragma unroll
+            for (int j = 0; j < D; ++j)
+                w[j] = next[j];
+            load(k + D * NT);
+            if constexpr (Rolled) {
+#pragma unroll 1
+                for (int j = 0; j < D && k + j * NT < k1; ++j) {
+                    vec(w[0], (k + j * NT) * E - off);
+#pragma unroll
+                    for (int i = 0; i + 1 < D; ++i)
+                        w[i] = w[i + 1];
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < D; ++j)
+                    if (k + j * NT < k1)
+                        vec(w[j], (k + j * NT) * E - off);
+            }
+        }
+        const uint32_t head = head_end() - s0, edge = head + (s1 - tail_start());
+#pragma unroll 1
+        for (uint32_t j = tid; j < edge; j += NT)
+            one(j < head ? s0 + j : tail_start() + (j - head));
+    }
+
+    // fn(l, id) for every entry of the slice
+    template <class F>
+    __device__ __forceinline__ void each(F&& fn) const {
+        walk<4, true>(
+            [&](const uint4& w, uint32_t id) {
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    fn(vector_entry<ES>(w, e), id + e);
+            },
+            [&](uint32_t id) { fn(scalar_entry<ES>(base, id), id); });
+    }
+};
 
 #endif  // __CUDACC__
 

@@ -111,10 +111,7 @@ struct alignas(16) Shared {
     };
     float2 pow2[64];
     Args args;
-    // The CTA's slice, ids s0..s1-1, and its 16-byte vectors: number k holds the ids from
-    // k E - off on, where off is the place of the row's first logit in its own vector.
-    // What they leave at the slice's ends (the row's ends: slices meet between
-    // vectors) is taken one by one.
+    // the CTA's slice of the row
     const unsigned char* base;  // the row's first logit
     uint32_t row, s0, s1, off, k0, k1;
     // the row's settings
@@ -251,74 +248,14 @@ __device__ __forceinline__ unsigned long long cta_sum(Shared* sh, unsigned long 
 // ------------------------------------------------------------- the slice -----
 
 template <int ES>
-struct View {
-    static constexpr int E = 16 / ES;
-    const unsigned char* base;
-    uint32_t s0, s1, off, k0, k1;
-
-    __device__ __forceinline__ explicit View(const Shared* sh)
-        : base(sh->base), s0(sh->s0), s1(sh->s1), off(sh->off), k0(sh->k0), k1(sh->k1) {}
-
-    __device__ __forceinline__ const uint4* vectors() const {
-        return reinterpret_cast<const uint4*>(base - (size_t)off * ES);
-    }
-    __device__ __forceinline__ uint32_t head_end() const { return min(k0 * E - off, s1); }
-    __device__ __forceinline__ uint32_t tail_start() const { return min(max(k1 * E - off, head_end()), s1); }
-
-    // vec(w, id of its first logit) for every vector of the slice, one(id) for every
-    // other logit.  The next D vectors are loaded before D are worked on; `Rolled` keeps
-    // one copy of vec's code.
-    template <int D, bool Rolled, class Vec, class One>
-    __device__ __forceinline__ void walk(Vec&& vec, One&& one) const {
-        const int tid = threadIdx.x;
-        const uint4* p = vectors() + k0 + tid;
-        uint4 next[D];
-        const auto load = [&](uint32_t k) {
-#pragma unroll
-            for (int j = 0; j < D; ++j)
-                if (k + j * kNT < k1)
-                    next[j] = load_stream(p + j * kNT);
-            p += D * kNT;
-        };
-        load(k0 + tid);
-#pragma unroll 1
-        for (uint32_t k = k0 + tid; k < k1; k += D * kNT) {
-            uint4 w[D];
-#pragma unroll
-            for (int j = 0; j < D; ++j)
-                w[j] = next[j];
-            load(k + D * kNT);
-            if constexpr (Rolled) {
-#pragma unroll 1
-                for (int j = 0; j < D && k + j * kNT < k1; ++j) {
-                    vec(w[0], (k + j * kNT) * E - off);
-#pragma unroll
-                    for (int i = 0; i + 1 < D; ++i)
-                        w[i] = w[i + 1];
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < D; ++j)
-                    if (k + j * kNT < k1)
-                        vec(w[j], (k + j * kNT) * E - off);
-            }
-        }
-        const uint32_t head = head_end() - s0, edge = head + (s1 - tail_start());
-#pragma unroll 1
-        for (uint32_t j = tid; j < edge; j += kNT)
-            one(j < head ? s0 + j : tail_start() + (j - head));
-    }
-
-    // fn(l, id) for every entry of the slice
-    template <class F>
-    __device__ __forceinline__ void each(F&& fn) const {
-        walk<4, true>(
-            [&](const uint4& w, uint32_t id) {
-#pragma unroll
-                for (int e = 0; e < E; ++e)
-                    fn(vector_entry<ES>(w, e), id + e);
-            },
-            [&](uint32_t id) { fn(scalar_entry<ES>(base, id), id); });
+struct View : Slice<ES, kNT> {
+    __device__ __forceinline__ explicit View(const Shared* sh) {
+        this->base = sh->base;
+        this->s0 = sh->s0;
+        this->s1 = sh->s1;
+        this->off = sh->off;
+        this->k0 = sh->k0;
+        this->k1 = sh->k1;
     }
 };
 
