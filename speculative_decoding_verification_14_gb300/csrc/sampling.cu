@@ -87,14 +87,21 @@ __device__ __forceinline__ void count_pair(Shared* sh, uint32_t x) {
         atomicAdd(reinterpret_cast<uint32_t*>(zero + o1), 1u);
 }
 
-// A.  The CTA's counts; returns its largest key, 0xffffffff for a NaN.
+// A.  The CTA's counts, and the codes of its steps; returns its largest key, 0xffffffff
+// for a NaN.
 template <int ES>
-__device__ __noinline__ uint32_t count_pass(Shared* sh) {
+__device__ __noinline__ uint32_t count_pass(Shared* sh, StepCodes* codes) {
     sh = here();
     const View<ES> v(sh);
+    const int shift = code_shift(v);
     float lmax = __int_as_float(0xff800000);
-    uint32_t two = 0xff80ff80u;  // bfloat16: the largest of each half
-    v.template walk<4, false>(
+    float step = lmax;           // float32: a step's largest
+    uint32_t two = 0xff80ff80u;  // bfloat16: of each half
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        codes->code[i] = 0;
+    v.template walk_steps<kDeep, false>(
+        [](uint32_t) { return true; },
         [&](const uint4& w, uint32_t) {
             if constexpr (ES == 2) {
                 count_pair(sh, w.x);
@@ -109,17 +116,26 @@ __device__ __noinline__ uint32_t count_pass(Shared* sh) {
             } else {
                 count_pair(sh, __byte_perm(w.x, w.y, 0x7632));
                 count_pair(sh, __byte_perm(w.z, w.w, 0x7632));
-                lmax = max_nan(max_nan(lmax, __uint_as_float(w.x)), __uint_as_float(w.y));
-                lmax = max_nan(max_nan(lmax, __uint_as_float(w.z)), __uint_as_float(w.w));
+                step = max_nan(step, vector_max_nan<4>(w));
             }
+        },
+        [](uint32_t) {},
+        [&](uint32_t s) {
+            if constexpr (ES == 2) {
+                step = max_nan(__uint_as_float(two << 16), __uint_as_float(two & 0xffff0000u));
+                two = 0xff80ff80u;
+            }
+            const uint8_t x = (uint8_t)step_code(step);
+            if (shift == 0 || x > codes->code[s >> shift])
+                codes->code[s >> shift] = x;
+            lmax = max_nan(lmax, step);
+            step = __int_as_float(0xff800000);
         },
         [&](uint32_t id) {  // a lone logit, paired with -inf, which is not counted
             const float l = scalar_entry<ES>(v.base, id);
             count_pair(sh, (__float_as_uint(l) >> 16) | 0xff800000u);
             lmax = max_nan(lmax, l);
         });
-    if constexpr (ES == 2)
-        lmax = max_nan(lmax, max_nan(__uint_as_float(two << 16), __uint_as_float(two & 0xffff0000u)));
     uint32_t key = lmax == lmax ? logit_key(lmax) : 0xffffffffu;
     key = __reduce_max_sync(kAllLanes, key);
     if ((threadIdx.x & 31) == 0)
@@ -134,56 +150,46 @@ __device__ __noinline__ uint32_t count_pass(Shared* sh) {
 __device__ __forceinline__ int chunks_per(int C) { return (kChunks + C - 1) / C; }
 __device__ __forceinline__ int first_chunk(int C, int rank) { return min(rank * chunks_per(C), kChunks); }
 
-// A CTA's chunks, and the cluster's counts at its range of places, which lie behind its
-// shared memory (a lone CTA's are its own).
+// A CTA's chunks lie behind its shared memory.
 __device__ __forceinline__ Chunk* chunks(Shared* sh) { return reinterpret_cast<Chunk*>(sh + 1); }
-__device__ __forceinline__ uint32_t* merged(Shared* sh) {
-    return reinterpret_cast<uint32_t*>(chunks(sh) + chunks_per(sh->args.C));
-}
 
-// entries at place D of this CTA's range, which begins at place `first`; of any CTA's
-__device__ __forceinline__ uint32_t own_count(Shared* sh, int C, int first, int D) {
-    return C == 1 ? sh->count[kPlaces - 1 - D] : merged(sh)[D - first];
-}
+// Entries at place D over the cluster, once they are merged: of a place of this CTA's
+// range, and of any.
+__device__ __forceinline__ uint32_t own_count(const Shared* sh, int D) { return sh->count[kPlaces - 1 - D]; }
 __device__ __forceinline__ uint32_t any_count(Shared* sh, int D) {
-    const int C = sh->args.C;
-    if (C == 1)
-        return sh->count[kPlaces - 1 - D];
-    const int per = chunks_per(C), r = D / 32 / per;
-    return peer(merged(sh), r)[D - r * per * 32];
+    const int r = D / 32 / chunks_per(sh->args.C);
+    return peer(sh->count, r)[kPlaces - 1 - D];
 }
 
-// All of a thread's reads of the other CTAs are independent of each other.
+// Adds the other CTAs' counts at this CTA's range of places to its own: nobody else
+// reads them there.  All of a thread's reads are independent of each other.
 __device__ __noinline__ void merge_counts(Shared* sh) {
     sh = here();
     const int C = sh->args.C, rank = cta_rank(), tid = threadIdx.x;
-    uint32_t* to = merged(sh);
     const int first = first_chunk(C, rank) * 32, span = chunks_per(C) * 32;
     const int places = first_chunk(C, rank + 1) * 32 - first;
-    for (int i = tid; i < places; i += kNT)
-        to[i] = 0;
-    __syncthreads();
+    uint32_t* last = sh->count + (kPlaces - 1 - first);  // the range's first place
     if ((C & (C - 1)) == 0) {
         const int lg = 31 - __clz(span);  // a power of two
         constexpr int L = 16;
-        for (int q = tid; q < span * C; q += L * kNT) {
+        for (int q = tid; q < span * (C - 1); q += L * kNT) {
             uint32_t x[L];
 #pragma unroll
             for (int j = 0; j < L; ++j) {
-                const int i = q + j * kNT, r = ((i >> lg) + rank) & (C - 1);
-                x[j] = peer(sh->count, r)[kPlaces - 1 - (first + (i & (span - 1)))];
+                const int i = q + j * kNT, r = (rank + 1 + (i >> lg)) & (C - 1);
+                x[j] = i < span * (C - 1) ? *(peer(last, r) - (i & (span - 1))) : 0;
             }
 #pragma unroll
             for (int j = 0; j < L; ++j)
                 if (x[j])
-                    atomicAdd(&to[(q + j * kNT) & (span - 1)], x[j]);
+                    atomicAdd(last - ((q + j * kNT) & (span - 1)), x[j]);
         }
     } else {
         for (int r = 0; r < C; ++r)
             for (int i = tid; i < places; i += kNT) {
-                const uint32_t x = peer(sh->count, r)[kPlaces - 1 - (first + i)];
+                const uint32_t x = r == rank ? 0 : *(peer(last, r) - i);
                 if (x)
-                    atomicAdd(&to[i], x);
+                    atomicAdd(last - i, x);
             }
     }
     __syncthreads();
@@ -202,7 +208,7 @@ __device__ __noinline__ void weigh_places(Shared* sh) {
 #pragma unroll 1
     for (int c = c0 + warp; c < c1; c += kNW) {
         const int D = c * 32 + lane;
-        uint32_t n = own_count(sh, C, c0 * 32, D);
+        uint32_t n = own_count(sh, D);
         unsigned long long m = 0;
         if (__any_sync(kAllLanes, n)) {
             if (n) {
@@ -303,7 +309,7 @@ __device__ __noinline__ Found search_places(Shared* sh, int set, const Wanted s)
         const Hit h = sh->hit[set][warp];
         Found f;
         f.bin = h.chunk * 32 + lane;
-        f.count = own_count(sh, C, c0 * 32, f.bin);
+        f.count = own_count(sh, f.bin);
         f.mass = f.count ? f.count * weight_call(sh->scale, sh->pow2, place_logit<ES>(sh->scale.lmax, f.bin)) : 0;
         const Prefix x = warp_prefix(f.mass, f.count);
         f.above_mass = h.above_mass + x.before_mass;
@@ -335,113 +341,96 @@ __device__ __noinline__ Found search_places(Shared* sh, int set, const Wanted s)
     return f;
 }
 
-// which of a vector's eight logits equal the bits `two` holds twice
-__device__ __forceinline__ uint32_t matches(const uint4& w, uint32_t two) {
-    const uint32_t x[4] = {w.x ^ two, w.y ^ two, w.z ^ two, w.w ^ two};
-    uint32_t mask = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        mask |= ((x[j] & 0xffffu) == 0 ? 1u << (2 * j) : 0u) | ((x[j] >> 16) == 0 ? 2u << (2 * j) : 0u);
-    return mask;
-}
-
 // The entry number r by ascending id at place D (bfloat16); the CTA that holds it
-// returns its id in one thread, every other thread returns -1.  Each warp counts in a
-// stretch of the slice, 32 steps of 32 vectors at a time; the warp that holds the entry
-// finds the step from what its lanes counted and reads that step again.
-__device__ __noinline__ int64_t find_entry(Shared* sh, int D, unsigned long long r) {
+// returns its id in one thread, every other thread returns -1.  Each CTA gathers
+// the ids of its entries there; in the one that holds it, the id with as many smaller ones
+// as are left is it.
+__device__ __noinline__ int64_t find_entry(Shared* sh, const StepCodes* codes, int D, unsigned long long r) {
     sh = here();
     const View<2> v(sh);
-    const int C = sh->args.C, rank = cta_rank(), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    uint32_t left;
-    {
-        const uint32_t n = lane < C ? peer(sh->count, lane)[kPlaces - 1 - D] : 0;
-        const Prefix x = warp_prefix(0, n);
-        const uint32_t owners = __ballot_sync(kAllLanes, r >= x.before_count && r < x.count);
-        if (!owners || __ffs(owners) - 1 != rank)
-            return -1;
-        left = (uint32_t)(r - __shfl_sync(kAllLanes, x.before_count, rank));
-    }
-    const uint32_t bits = __float_as_uint(place_value(D)) >> 16, two = bits * 0x10001u;
+    const int C = sh->args.C, rank = cta_rank(), tid = threadIdx.x;
+    const float l = place_value(D);
+    const uint32_t bits = __float_as_uint(l) >> 16, two = bits * 0x10001u;
     const unsigned short* q = reinterpret_cast<const unsigned short*>(v.base);
-    // what lies before the first vector: less than one
-    for (uint32_t i = v.s0; i < v.head_end(); ++i)
-        if (q[i] == bits && left-- == 0)
-            return tid == 0 ? (int64_t)i : -1;
-    constexpr int L = 8;
-    const uint4* p = v.vectors();
-    const uint32_t per = (v.k1 - v.k0 + kNW - 1) / kNW;
-    const uint32_t g0 = min(v.k0 + warp * per, v.k1), g1 = min(g0 + per, v.k1);
-    uint32_t seen[4];  // a lane's matches of each step of the last block, 4 bits each
-    const auto block = [&](uint32_t b) {
-        uint32_t sum = 0;
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-            uint4 w[L];
-#pragma unroll
-            for (int j = 0; j < L; ++j)
-                if (b + 32 * (L * h + j) + lane < g1)
-                    w[j] = load_stream(p + b + 32 * (L * h + j) + lane);
-            uint32_t s = 0;
-#pragma unroll
-            for (int j = 0; j < L; ++j)
-                if (b + 32 * (L * h + j) + lane < g1) {
-                    const uint32_t c = __popc(matches(w[j], two));
-                    s |= c << (4 * j);
-                    sum += c;
-                }
-            seen[h] = s;
-        }
-        return __reduce_add_sync(kAllLanes, sum);
+    const uint32_t least = step_code(l);
+    const int shift = code_shift(v);
+    constexpr uint32_t kIds = kPlaces;
+    uint32_t* ids = sh->count;  // the counts are done with
+    const auto found = [&](uint32_t id) {
+        const uint32_t at = atomicAdd(&sh->list_n[0], 1u);
+        if (at < kIds)
+            ids[at] = id;
     };
-    uint32_t mine = 0;
-    for (uint32_t b = g0; b < g1; b += 1024)
-        mine += block(b);
-    __syncthreads();
-    if (lane == 0)
-        sh->warp_cnt[warp] = mine;
-    __syncthreads();
-    int holder = -1;
-    for (int w = 0; w < kNW; ++w) {
-        if (left < sh->warp_cnt[w]) {
-            holder = w;
-            break;
-        }
-        left -= sh->warp_cnt[w];
-    }
-    if (holder < 0) {
-        if (tid == 0)
-            for (uint32_t i = v.tail_start(); i < v.s1; ++i)
-                if (q[i] == bits && left-- == 0)
-                    return i;
-        return -1;
-    }
-    if (holder != warp)
-        return -1;
-    for (uint32_t b = g0; b < g1; b += 1024) {
-        if (g1 - g0 > 1024) {
-            const uint32_t all = block(b);
-            if (left >= all) {
-                left -= all;
-                continue;
+    v.walk_steps<kDeep, true>(
+        [&](uint32_t s) { return codes->code[s >> shift] >= least; },
+        [&](const uint4& w, uint32_t id) {
+            uint32_t m;
+            const uint32_t x[4] = {w.x ^ two, w.y ^ two, w.z ^ two, w.w ^ two};
+            asm("min.u16x2 %0, %1, %2;" : "=r"(m) : "r"(x[0]), "r"(x[1]));
+            asm("min.u16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(x[2]));
+            asm("min.u16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(x[3]));
+            if ((m & 0xffffu) == 0 || (m >> 16) == 0) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if ((x[j] & 0xffffu) == 0)
+                        found(id + 2 * j);
+                    if ((x[j] >> 16) == 0)
+                        found(id + 2 * j + 1);
+                }
             }
-        }
-        for (int j = 0; j < 32; ++j) {
-            const uint32_t word = j < 8 ? seen[0] : j < 16 ? seen[1] : j < 24 ? seen[2] : seen[3];
-            const uint32_t c = word >> (4 * (j & 7)) & 15u, all = __reduce_add_sync(kAllLanes, c);
-            if (left >= all) {
-                left -= all;
-                continue;
-            }
-            const Prefix x = warp_prefix(0, c);
-            if (left < x.before_count || left >= x.count)
+        },
+        [](uint32_t) {}, [](uint32_t) {},
+        [&](uint32_t id) {
+            if (q[id] == bits)
+                found(id);
+        });
+    __syncthreads();
+    const uint32_t n = sh->list_n[0];
+    if (C > 1) {
+        if (tid < C)
+            *peer(&sh->part_list[0][rank], tid) = n;
+        the_cluster().sync();
+        for (int c = 0; c < rank; ++c) {
+            if (r < sh->part_list[0][c])
                 return -1;
-            const uint32_t g = b + 32 * j + lane;
-            const uint32_t mask = matches(load_stream(p + g), two);
-            return (int64_t)g * 8 - v.off + __fns(mask, 0, (int)(left - x.before_count) + 1);
+            r -= sh->part_list[0][c];
         }
     }
-    return -1;
+    if (r >= n)
+        return -1;
+    if (n > kIds) {
+        // a stretch of ids per thread: how many it holds, then which one
+        const uint32_t per = (v.s1 - v.s0 + kNT - 1) / kNT;
+        const uint32_t e0 = min(v.s0 + tid * per, v.s1), e1 = min(e0 + per, v.s1);
+        uint32_t mine = 0;
+        for (uint32_t e = e0; e < e1; ++e)
+            mine += q[e] == bits;
+        const Prefix x = cta_prefix(sh, 0, mine);
+        if (r < x.before_count || r >= x.before_count + mine)
+            return -1;
+        uint32_t left = (uint32_t)r - x.before_count, e = e0;
+        while (q[e] != bits || left-- != 0)
+            ++e;
+        return e;
+    }
+    if (n <= (uint32_t)kNT) {
+        const uint32_t id = tid < n ? ids[tid] : 0;
+        uint32_t before = 0;
+        for (uint32_t j = 0; j < n; ++j)
+            before += ids[j] < id;
+        return tid < n && before == r ? (int64_t)id : -1;
+    }
+    // the largest x with at most r ids below it
+    uint32_t x = 0;
+    for (int bit = 31 - __clz(v.s1); bit >= 0; --bit) {
+        const uint32_t t = x | 1u << bit;
+        uint32_t below = 0;
+        for (uint32_t i = tid; i < n; i += kNT)
+            below += ids[i] < t;
+        if (cta_sum(sh, below) <= r)
+            x = t;
+    }
+    return tid == 0 ? (int64_t)x : -1;
 }
 
 // A stretch of places around one of interest: lane r looks at r places to either
@@ -508,37 +497,142 @@ __device__ __noinline__ void pull_list(Shared* sh, int which) {
 struct Sums {
     unsigned long long x[3];
 };
+
+// A weight for sums, in half the instructions of weight_fixed: 2^(p - M), p = l c,
+// M = l_max c, without the difference l_max - l.
+//   M = Mk/128 + Mr, |Mr| <= 1/256;  p = k/128 + r + Mr, |r| <= 1/256, p - k/128 exact;
+//   2^(p - M) = 2^floor((k - Mk)/128) T[(k - Mk) mod 128] (1 + y),  y = e^z - 1 in one float.
+// y rounds at 2^-33 to either side, which a sum of many entries does not show (the
+// lists' entries, few, take weight_fixed).  T in two floats, a copy for each of 16 lanes,
+// so that lanes' reads do not meet in a bank.  For |M| < 128.
+struct SumScale {
+    float ch, cl, floor_l, mh, ml;  // mh + ml: Mr
+    int k0;                         // Mk
+    const float2* steps;
+};
+__device__ __forceinline__ SumScale sum_scale(Shared* sh, const RowScale& s) {
+    SumScale t;
+    t.ch = s.ch;
+    t.cl = s.cl;
+    t.floor_l = s.lmax - 70.0f / s.ch;
+    const float m = s.lmax * s.ch, ml = fmaf(s.lmax, s.ch, -m) + s.lmax * s.cl, k = rintf(m * 128.0f);
+    const float rest = fmaf(k, -0.0078125f, m);  // exact
+    t.mh = rest + ml;
+    t.ml = ml - (t.mh - rest);
+    t.k0 = (int)k;
+    float2* steps = reinterpret_cast<float2*>(sh->hi);  // behind the second list: 16 KB
+    constexpr float kHalfh = 1.00542986392974853515625f, kHalfl = 3.7183054286195135e-8f;  // 2^(1/128)
+    for (int i = threadIdx.x; i < 128 * 16; i += kNT) {
+        const int j = i >> 4;
+        float2 p = sh->pow2[j >> 1];
+        if (j & 1) {
+            const float h = p.x * kHalfh, l = fmaf(p.x, kHalfh, -h) + fmaf(p.x, kHalfl, p.y * kHalfh);
+            p.x = h + l;
+            p.y = l - (p.x - h);
+        }
+        steps[i] = p;
+    }
+    t.steps = steps + (threadIdx.x & 15);
+    __syncthreads();
+    return t;
+}
+// the weight as hi + lo, hi with 24 bits
+__device__ __forceinline__ float2 sum_weight(const SumScale& s, float l) {
+    constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
+    l = fmaxf(l, s.floor_l);
+    const float p = l * s.ch;
+    const float pl = fmaf(l, s.cl, -s.ml) + fmaf(l, s.ch, -p);
+    const float m = fmaf(p - s.mh, 128.0f, kMagic);
+    const int k = __float_as_int(m) - __float_as_int(kMagic) - s.k0;
+    const float r = (fmaf(m - kMagic, -0.0078125f, p) - s.mh) + pl;
+    const float y = r * fmaf(r, fmaf(r, fmaf(r, 0.00961812911f, 0.0555041087f), 0.240226507f), 0.693147181f);
+    const float2 t = s.steps[(k & 127) << 4];
+    const float two = __int_as_float(((k & ~127) << 16) + (127 << 23));  // 2^floor(k/128)
+    return make_float2(t.x * two, fmaf(t.x, y, t.y) * two);
+}
+// Adds up to four weights: what a float of 2^-20 units takes of them, and the rest.
+struct FourSum {
+    static constexpr float kBase = 12.0f;
+    float hi = kBase, lo = 0.0f;
+    __device__ __forceinline__ void add(float2 w) {
+        const float s = hi + w.x, taken = s - hi;
+        lo += w.y + (w.x - taken);
+        hi = s;
+    }
+    __device__ __forceinline__ unsigned long long fixed(float one) const {
+        return __float2ull_rn((hi - kBase) * one) + (unsigned long long)__float2ll_rn(lo * one);
+    }
+};
+
 __device__ __noinline__ Sums sum_exact(Shared* sh, bool list) {
     sh = here();
     const RowScale scale = sh->scale;
     const View<4> v(sh);
     const float clo = sh->band[0].lo, chi = sh->band[0].hi, dlo = sh->band[1].lo, dhi = sh->band[1].hi;
+    const bool c = sh->band[0].on && !sh->band[0].from_top, d = sh->band[1].on;
     const float low = list ? fminf(clo, dlo) : __int_as_float(0x7f800000);
     Sums s = {{0, 0, 0}};
-    v.each([&](float l, uint32_t id) {
-        const unsigned long long x = weight_fixed(scale, sh->pow2, l);
-        s.x[0] += x;
-        s.x[1] += l > chi ? x : 0;
-        s.x[2] += l > dhi ? x : 0;
+    const auto take = [&](float l, uint32_t id) {
         if (l >= low) {
             if (l >= clo && l <= chi)
                 offer(&sh->list_n[0], list_at(sh, 0), l, id);
             if (l >= dlo && l <= dhi)
                 offer(&sh->list_n[1], list_at(sh, 1), l, id);
         }
-    });
+    };
+    const auto one_exact = [&](float l, uint32_t id) {
+        const unsigned long long x = weight_fixed(scale, sh->pow2, l);
+        s.x[0] += x;
+        s.x[1] += l > chi ? x : 0;
+        s.x[2] += l > dhi ? x : 0;
+        take(l, id);
+    };
+    if (!(fabsf(scale.lmax * scale.ch) < 128.0f)) {
+        v.each(one_exact);
+        return s;
+    }
+    const SumScale t = sum_scale(sh, scale);
+    const float one = (float)(1ull << scale.fix);
+    v.walk<2, true>(
+        [&](const uint4& w, uint32_t id) {
+            const float l[4] = {__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w)};
+            FourSum all, over_c, over_d;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 x = sum_weight(t, l[e]);
+                all.add(x);
+                if (c && l[e] > chi)
+                    over_c.add(x);
+                if (d && l[e] > dhi)
+                    over_d.add(x);
+            }
+            s.x[0] += all.fixed(one);
+            if (c)
+                s.x[1] += over_c.fixed(one);
+            if (d)
+                s.x[2] += over_d.fixed(one);
+            if (vector_max<4>(w) >= low) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    take(l[e], id + e);
+            }
+        },
+        [&](uint32_t id) { one_exact(scalar_entry<4>(v.base, id), id); });
     return s;
 }
 // The row's sum in floats, to 2^-17 of itself (where `sum`), and the cut's entries.  A
 // weight is off by (l_max - l)/T * 2.5 * 2^-24 + 2^-22, below 2^-19 where it
 // counts (V < 2^20), and four of them are added before they become integers.
-__device__ __noinline__ unsigned long long sum_fast(Shared* sh, bool sum) {
+__device__ __noinline__ unsigned long long sum_fast(Shared* sh, const StepCodes* codes, bool sum) {
     sh = here();
     const RowScale scale = sh->scale;
     const View<4> v(sh);
     const float low = sh->band[0].lo, one = sum ? (float)(1ull << scale.fix) : 0.0f;
     unsigned long long s = 0;
-    v.walk<4, true>(
+    const uint32_t least = sum ? 0u : step_code(low);
+    const int shift = code_shift(v);
+    v.walk_steps<kDeep, true>(
+        [&](uint32_t s) { return codes->code[s >> shift] >= least; },
         [&](const uint4& w, uint32_t id) {
             const float l[4] = {__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w)};
             float t = 0.0f;
@@ -553,6 +647,7 @@ __device__ __noinline__ unsigned long long sum_fast(Shared* sh, bool sum) {
                         offer(&sh->list_n[0], list_at(sh, 0), l[e], id + e);
             }
         },
+        [](uint32_t) {}, [](uint32_t) {},
         [&](uint32_t id) {
             const float l = scalar_entry<4>(v.base, id);
             s += __float2ull_rn(ex2_approx((l - scale.lmax) * scale.ch) * one);
@@ -627,7 +722,7 @@ __device__ __noinline__ void settle(Shared* sh, bool by_mass, bool exact, bool f
 // C, float32.  Leaves the cut, what is kept, the row's sum in the first CTA's
 // sums[0][0], and the drawn entry there; false when the stretches do not hold them.
 // `fine`: integer sums at once.
-__device__ __noinline__ bool exact_pass(Shared* sh, bool by_mass, bool fine) {
+__device__ __noinline__ bool exact_pass(Shared* sh, const StepCodes* codes, bool by_mass, bool fine) {
     sh = here();
     const int rank = cta_rank(), tid = threadIdx.x;
     for (bool first = true;; first = false, fine = true) {
@@ -636,7 +731,7 @@ __device__ __noinline__ bool exact_pass(Shared* sh, bool by_mass, bool fine) {
         if (sums && fine)
             s = sum_exact(sh, first);
         else
-            s.x[0] = sum_fast(sh, sums);
+            s.x[0] = sum_fast(sh, codes, sums);
 #pragma unroll
         for (int j = 0; j < 3; ++j) {
             const unsigned long long x = warp_sum(s.x[j]);
@@ -709,10 +804,10 @@ __device__ __forceinline__ uint32_t cluster_sum(Shared* sh, uint32_t x) {
 
 // The counts and the scale of the weights.
 template <int ES>
-__device__ __noinline__ bool count_places(Shared* sh) {
+__device__ __noinline__ bool count_places(Shared* sh, StepCodes* codes) {
     sh = here();
     const int tid = threadIdx.x, C = sh->args.C, rank = cta_rank();
-    uint32_t key = count_pass<ES>(sh);
+    uint32_t key = count_pass<ES>(sh, codes);
     the_cluster().barrier_wait();  // every CTA runs: its memory may be written
     if (tid < C) {
         *peer(&sh->part_max[rank], tid) = key;
@@ -746,9 +841,9 @@ __device__ __noinline__ bool count_places(Shared* sh) {
 }
 
 // T = 0 (bfloat16): the first entry at the largest value's place.
-__device__ __noinline__ void take_largest(Shared* sh) {
+__device__ __noinline__ void take_largest(Shared* sh, const StepCodes* codes) {
     sh = here();
-    const int64_t id = find_entry(sh, place_of(sh->scale.lmax), 0);
+    const int64_t id = find_entry(sh, codes, place_of(sh->scale.lmax), 0);
     if (id >= 0) {
         put_token(sh, (int32_t)id, 1.0f);
         for (int r = 0; r < sh->args.C; ++r)
@@ -756,7 +851,7 @@ __device__ __noinline__ void take_largest(Shared* sh) {
     }
     if (writes_rows(sh)) {
         the_cluster().sync();
-        write_rows<2>(sh, kKeepToken, sh->scale.lmax, 0.0f, sh->token);
+        write_rows<2>(sh, codes, kKeepToken, sh->scale.lmax, 0.0f, sh->token);
     }
     put_rest(sh, SV_OK, 1, 1, 1);
 }
@@ -820,7 +915,7 @@ __device__ __noinline__ bool find_cut(Shared* sh) {
 }
 
 // bfloat16: the drawn place, and which of its entries it is.
-__device__ __noinline__ bool draw_value(Shared* sh) {
+__device__ __noinline__ bool draw_value(Shared* sh, const StepCodes* codes) {
     sh = here();
     const Wanted w = {0, floor_scaled(sh->u, sh->mass), kNoPlace, true};
     const Found d = search_places<2>(sh, 1, w);
@@ -828,14 +923,14 @@ __device__ __noinline__ bool draw_value(Shared* sh) {
         return false;
     const float l = place_value(d.bin);
     const int64_t id =
-        find_entry(sh, d.bin, (w.p - d.above_mass) / weight_call(sh->scale, sh->pow2, l));
+        find_entry(sh, codes, d.bin, (w.p - d.above_mass) / weight_call(sh->scale, sh->pow2, l));
     if (id >= 0)
         put_token(sh, (int32_t)id, weight_float(sh->scale, l) * inverse_mass(sh->scale, sh->mass));
     return true;
 }
 
 // float32: the stretches around the cut and the draw, and the second pass.
-__device__ __noinline__ bool settle_exactly(Shared* sh) {
+__device__ __noinline__ bool settle_exactly(Shared* sh, const StepCodes* codes) {
     sh = here();
     const int tid = threadIdx.x;
     const bool by_mass = sh->top_p < 1.0, draw = sh->args.u != nullptr;
@@ -863,7 +958,7 @@ __device__ __noinline__ bool settle_exactly(Shared* sh) {
     const bool fine =
         !sh->band[0].from_top || sh->args.mass ||
         (by_mass && weight_call(sh->scale, sh->pow2, place_logit<4>(sh->scale.lmax, sh->cut_at.bin)) < sh->whole >> 15);
-    if (!exact_pass(sh, by_mass, fine))
+    if (!exact_pass(sh, codes, by_mass, fine))
         return false;
     if (tid == 0) {
         sh->whole = sh->sums[0][0];
@@ -882,25 +977,26 @@ __device__ __noinline__ bool settle_exactly(Shared* sh) {
 // The whole call, or false.
 template <int ES>
 __device__ __forceinline__ bool by_place(Shared* sh) {
-    if (!count_places<ES>(sh))
+    StepCodes codes;
+    if (!count_places<ES>(sh, &codes))
         return false;
     if constexpr (ES == 2) {
         if (sh->T == 0.0f) {
-            take_largest(sh);
+            take_largest(sh, &codes);
             return true;
         }
     }
     if (!find_cut<ES>(sh))
         return false;
     if constexpr (ES == 2) {
-        if (sh->args.u && !draw_value(sh))
+        if (sh->args.u && !draw_value(sh, &codes))
             return false;
     } else {
-        if (!settle_exactly(sh))
+        if (!settle_exactly(sh, &codes))
             return false;
     }
     if (writes_rows(sh))
-        write_rows<ES>(sh, kKeepFrom, sh->cut, inverse_mass(sh->scale, sh->mass), 0);
+        write_rows<ES>(sh, &codes, kKeepFrom, sh->cut, inverse_mass(sh->scale, sh->mass), 0);
     put_rest(sh, SV_OK, sh->kept_n, sh->mass, sh->whole);
     return true;
 }
@@ -978,12 +1074,11 @@ __global__ void __launch_bounds__(kNT, 4) sv_sample_kernel(const __grid_constant
     general_row<ES>(sh, sh->code);
 }
 
-// with a CTA's chunks of places, and the cluster's counts at them
+// with a CTA's chunks of places
 size_t shared_size(int cluster) {
-    const size_t chunks = (size_t)((kChunks + cluster - 1) / cluster);
-    return sizeof(Shared) + chunks * (sizeof(Chunk) + (cluster > 1 ? 32 * sizeof(uint32_t) : 0));
+    return sizeof(Shared) + (size_t)((kChunks + cluster - 1) / cluster) * sizeof(Chunk);
 }
-static_assert(4 * (sizeof(Shared) + kChunks / 2 * (sizeof(Chunk) + 128) + 1024) <= 233472, "four CTAs per SM");
+static_assert(4 * (sizeof(Shared) + kChunks * sizeof(Chunk) + 1024) <= 233472, "four CTAs per SM");
 
 int launch(sv_ctx* ctx, Args& a, int B, int rows, int64_t V, int dtype, cudaStream_t stream) {
     sv_plan plan;
@@ -1046,7 +1141,7 @@ namespace sv {
 
 int sampling_setup() {
     for (const void* fn : {(const void*)sv_sample_kernel<2>, (const void*)sv_sample_kernel<4>}) {
-        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared_size(2)) !=
+        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared_size(1)) !=
             cudaSuccess) {
             (void)cudaGetLastError();
             return 0;

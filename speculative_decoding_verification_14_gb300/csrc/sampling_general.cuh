@@ -282,7 +282,7 @@ struct General {
         scale.lmax = m;
         if (code) {
             if (writes_rows(sh))
-                write_rows<ES>(sh, kBadRow, 0.0f, 0.0f, 0);
+                write_rows<ES>(sh, nullptr, kBadRow, 0.0f, 0.0f, 0);
             if (rank == 0 && tid == 0)
                 put_token(sh, -1, __int_as_float(0x7fffffff));
             put_rest(sh, code, 0, 0, 1);
@@ -308,7 +308,7 @@ struct General {
             for (int r = 0; r < C; ++r)
                 id = min(id, sh->part_cnt[r]);
             if (writes_rows(sh))
-                write_rows<ES>(sh, kKeepToken, m, 0.0f, id);
+                write_rows<ES>(sh, nullptr, kKeepToken, m, 0.0f, id);
             if (rank == 0 && tid == 0)
                 put_token(sh, (int32_t)id, 1.0f);
             put_rest(sh, SV_OK, 1, 1, 1);
@@ -416,7 +416,7 @@ struct General {
         }
         // D. rows out
         if (writes_rows(sh))
-            write_rows<ES>(sh, kKeepFrom, key_logit(cut_key), inv, 0);
+            write_rows<ES>(sh, nullptr, kKeepFrom, key_logit(cut_key), inv, 0);
         put_rest(sh, SV_OK, kept, E, whole);
         the_cluster().sync();  // no CTA leaves while another may still write into it
     }

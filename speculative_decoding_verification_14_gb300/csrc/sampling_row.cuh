@@ -99,8 +99,8 @@ struct Cut {
     unsigned long long p, above_mass, slack;
 };
 
-// A CTA's shared memory, followed by its chunks of places and, when the cluster has
-// more than one CTA, the cluster's counts at them.  Four CTAs share an SM's 227 KB.
+// A CTA's shared memory, followed by its chunks of places.  Four CTAs share an SM, and
+// leave a good part of it to the first-level cache, where the threads' saved registers are.
 struct alignas(16) Shared {
     union {
         struct {
@@ -258,6 +258,24 @@ struct View : Slice<ES, kNT> {
         this->k1 = sh->k1;
     }
 };
+
+// The largest logit of each of a thread's steps through the slice (the first pass goes
+// kDeep vectors a step, and so do later ones), to quarters and in eight bits: later
+// passes leave out the steps that hold nothing for them.  Long slices' steps share the
+// 16 codes.
+constexpr int kDeep = 4;
+struct StepCodes {
+    uint8_t code[16];
+};
+__device__ __forceinline__ uint32_t step_code(float l) {  // grows with l; NaN: the largest
+    const float x = fmaf(l, 4.0f, 64.0f);
+    return x < 0.0f ? 0u : x < 255.0f ? (uint32_t)x : 255u;
+}
+template <class V>
+__device__ __forceinline__ int code_shift(const V& v) {
+    const uint32_t steps = (v.k1 - v.k0 + kDeep * kNT - 1) / (kDeep * kNT);
+    return steps <= 16 ? 0 : 28 - __clz(steps - 1);
+}
 
 // --------------------------------------------------------------- lists -----
 
@@ -485,10 +503,12 @@ __device__ __forceinline__ void share_cut(Shared* sh) {
 
 enum Keep { kKeepFrom, kKeepToken, kBadRow };  // logits from `cut` on; one id; a row without an answer
 
-// Probabilities and truncated logits.  A vector none of whose logits reaches `cut`
-// is written without looking further.  inv: 2^F over the kept mass.
+// Probabilities and truncated logits.  Steps (see StepCodes; NULL: all are looked at) and
+// vectors none of whose logits reaches `cut` are written without looking further.  inv:
+// 2^F over the kept mass.
 template <int ES>
-__device__ __noinline__ void write_rows(Shared* sh, Keep how, float cut, float inv, uint32_t token) {
+__device__ __noinline__ void write_rows(Shared* sh, const StepCodes* codes, Keep how, float cut, float inv,
+                                        uint32_t token) {
     sh = here();
     const RowScale scale = sh->scale;
     const Args& a = sh->args;
@@ -527,39 +547,50 @@ __device__ __noinline__ void write_rows(Shared* sh, Keep how, float cut, float i
             one(i);
         return;
     }
-    v.template walk<4, true>(
+    const uint32_t least = codes && !bad ? step_code(cut) : 0u;
+    const int shift = code_shift(v);
+    const auto nothing = [&](uint32_t id) {
+        if (p) {
+            float4* q = reinterpret_cast<float4*>(p + id);
+#pragma unroll
+            for (int e = 0; e < E / 4; ++e)
+                q[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+        if (o) {
+            const uint32_t x = ES == 4 ? 0xff800000u : 0xff80ff80u;
+            *reinterpret_cast<uint4*>(o + (size_t)id * ES) = make_uint4(x, x, x, x);
+        }
+    };
+    v.template walk_steps<kDeep, true>(
+        [&](uint32_t s) { return least == 0 || codes->code[s >> shift] >= least; },
         [&](const uint4& w, uint32_t id) {
-            const bool any = bad || vector_max<ES>(w) >= cut;
+            if (!bad && !(vector_max<ES>(w) >= cut)) {
+                nothing(id);
+                return;
+            }
             if (p) {
                 float4* q = reinterpret_cast<float4*>(p + id);
-                if (!any) {
 #pragma unroll
-                    for (int e = 0; e < E / 4; ++e)
-                        q[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < E / 4; ++e)
-                        q[e] = make_float4(prob(vector_entry<ES>(w, 4 * e), id + 4 * e),
-                                           prob(vector_entry<ES>(w, 4 * e + 1), id + 4 * e + 1),
-                                           prob(vector_entry<ES>(w, 4 * e + 2), id + 4 * e + 2),
-                                           prob(vector_entry<ES>(w, 4 * e + 3), id + 4 * e + 3));
-                }
+                for (int e = 0; e < E / 4; ++e)
+                    q[e] = make_float4(prob(vector_entry<ES>(w, 4 * e), id + 4 * e),
+                                       prob(vector_entry<ES>(w, 4 * e + 1), id + 4 * e + 1),
+                                       prob(vector_entry<ES>(w, 4 * e + 2), id + 4 * e + 2),
+                                       prob(vector_entry<ES>(w, 4 * e + 3), id + 4 * e + 3));
             }
             if (o) {
                 uint32_t h[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     if constexpr (ES == 4)
-                        h[j] = any ? logit(vector_entry<ES>(w, j), id + j) : 0xff800000u;
+                        h[j] = logit(vector_entry<ES>(w, j), id + j);
                     else
-                        h[j] = any ? (logit(vector_entry<ES>(w, 2 * j), id + 2 * j) >> 16) |
-                                         (logit(vector_entry<ES>(w, 2 * j + 1), id + 2 * j + 1) & 0xffff0000u)
-                                   : 0xff80ff80u;
+                        h[j] = (logit(vector_entry<ES>(w, 2 * j), id + 2 * j) >> 16) |
+                               (logit(vector_entry<ES>(w, 2 * j + 1), id + 2 * j + 1) & 0xffff0000u);
                 }
                 *reinterpret_cast<uint4*>(o + (size_t)id * ES) = make_uint4(h[0], h[1], h[2], h[3]);
             }
         },
-        one);
+        nothing, [](uint32_t) {}, one);
 }
 
 __device__ __forceinline__ bool writes_rows(const Shared* sh) { return sh->args.probs || sh->args.out; }
