@@ -67,41 +67,6 @@ __device__ __forceinline__ unsigned long long order_of(float l, uint32_t id) {
     return ((unsigned long long)logit_key(l) << 32) | (uint32_t)~id;
 }
 
-// sum of 2^((l - m) c) over a vector's logits: differences (a bfloat16 operand is
-// widened inside the subtraction), products and sums two at a time
-template <int ES>
-__device__ __forceinline__ float exp_sum(const uint4& v, float m, float c) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    unsigned long long cc, sum = 0;
-    asm("mov.b64 %0, {%1, %1};" : "=l"(cc) : "f"(c));
-#pragma unroll
-    for (int j = 0; j < 8 / ES; ++j) {
-        float lo, hi;
-        if constexpr (ES == 2) {
-            asm("{\n\t.reg .b16 l, h;\n\t"
-                "mov.b32 {l, h}, %2;\n\t"
-                "add.rn.f32.bf16 %0, l, %3;\n\t"
-                "add.rn.f32.bf16 %1, h, %3;\n\t}"
-                : "=f"(lo), "=f"(hi)
-                : "r"(w[j]), "f"(-m));
-        } else {
-            lo = __uint_as_float(w[2 * j]) - m;
-            hi = __uint_as_float(w[2 * j + 1]) - m;
-        }
-        unsigned long long t;
-        asm("{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\tmul.rn.f32x2 %0, d, %3;\n\t}" : "=l"(t) : "f"(lo), "f"(hi), "l"(cc));
-        asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(t));
-        asm("mov.b64 %0, {%1, %2};" : "=l"(t) : "f"(ex2_approx(lo)), "f"(ex2_approx(hi)));
-        if (j)
-            asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum) : "l"(t));
-        else
-            sum = t;
-    }
-    float lo, hi;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(sum));
-    return lo + hi;
-}
-
 template <int ES>
 __global__ void __launch_bounds__(kNT, 4) sv_logprobs_kernel(const __grid_constant__ Args a) {
     __shared__ Shared sh;
@@ -147,11 +112,7 @@ __global__ void __launch_bounds__(kNT, 4) sv_logprobs_kernel(const __grid_consta
     // the pass over the slice
     float m = -inf, s = 0.0f;
     uint32_t above = 0;
-    const auto grow = [&](float top) {  // a new maximum, or a NaN, which stays
-        const float grown = max_nan(m, top);
-        s = m > -inf ? s * ex2_approx((m - grown) * a.ch) : 0.0f;
-        m = grown;
-    };
+    const auto grow = [&](float top) { join_sums(m, s, top, 0.0f, a.ch); };
     v.template walk<4, false>(
         [&](const uint4& w, uint32_t) {
             const float top = vector_max_nan<ES>(w);
@@ -176,12 +137,7 @@ __global__ void __launch_bounds__(kNT, 4) sv_logprobs_kernel(const __grid_consta
     const float mine = m;
 
     // join the threads, then the CTAs
-    const auto merge = [&](float& m0, float& s0_, float m1, float s1_) {
-        const float mm = max_nan(m0, m1);
-        s0_ = (m0 > -inf ? s0_ * ex2_approx((m0 - mm) * a.ch) : 0.0f) +
-              (m1 > -inf ? s1_ * ex2_approx((m1 - mm) * a.ch) : 0.0f);
-        m0 = mm;
-    };
+    const auto merge = [&](float& m0, float& s0, float m1, float s1) { join_sums(m0, s0, m1, s1, a.ch); };
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
         const float m1 = __shfl_xor_sync(kAllLanes, m, o), s1_ = __shfl_xor_sync(kAllLanes, s, o);

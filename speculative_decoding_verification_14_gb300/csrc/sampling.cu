@@ -67,6 +67,17 @@ __device__ __forceinline__ float place_logit(float lmax, int D) {
     return l;
 }
 
+// mass of n entries at place D: bfloat16 exactly, float32 by the middle one's float weight
+template <int ES>
+__device__ __forceinline__ unsigned long long place_mass(const RowScale& s, const float2* pow2, int D, uint32_t n) {
+    if (n == 0)
+        return 0;
+    const float l = place_logit<ES>(s.lmax, D);
+    if constexpr (ES == 2)
+        return n * weight_fixed(s, pow2, l);
+    return __float2ull_rn((float)n * (ex2_approx((l - s.lmax) * s.ch) * (float)(1ull << s.fix)));
+}
+
 // Counts the two logits whose upper 16 bits x holds.  Each place's byte
 // offset is 4 i or 4 (-1 - i), both logits' in the halves of one word.
 // Logits above -127 alone are counted: what is missing lies below.
@@ -96,6 +107,10 @@ __device__ __noinline__ uint32_t count_pass(Shared* sh, StepCodes* codes) {
     const int shift = code_shift(v);
     float lmax = __int_as_float(0xff800000);
     float step = lmax;           // float32: a step's largest
+    // float32 under top-p: the row's sum, too, in floats
+    const bool sum = ES == 4 && sh->top_p < 1.0 && sh->T > 0.0f;
+    const float ch = __fdiv_rn(1.44269502162933349609375f, sum ? sh->T : 1.0f);
+    float m = lmax, t = 0.0f;
     uint32_t two = 0xff80ff80u;  // bfloat16: of each half
 #pragma unroll
     for (int i = 0; i < 16; ++i)
@@ -116,7 +131,14 @@ __device__ __noinline__ uint32_t count_pass(Shared* sh, StepCodes* codes) {
             } else {
                 count_pair(sh, __byte_perm(w.x, w.y, 0x7632));
                 count_pair(sh, __byte_perm(w.z, w.w, 0x7632));
-                step = max_nan(step, vector_max_nan<4>(w));
+                const float top = vector_max_nan<4>(w);
+                step = max_nan(step, top);
+                if (sum) {
+                    if (!(top <= m))
+                        join_sums(m, t, top, 0.0f, ch);
+                    if (top > __int_as_float(0xff800000))
+                        t += exp_sum<4>(w, m, ch);
+                }
             }
         },
         [](uint32_t) {},
@@ -135,7 +157,20 @@ __device__ __noinline__ uint32_t count_pass(Shared* sh, StepCodes* codes) {
             const float l = scalar_entry<ES>(v.base, id);
             count_pair(sh, (__float_as_uint(l) >> 16) | 0xff800000u);
             lmax = max_nan(lmax, l);
+            if (sum)
+                join_sums(m, t, l, 1.0f, ch);
         });
+    if (sum) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            const float m1 = __shfl_xor_sync(kAllLanes, m, o), t1 = __shfl_xor_sync(kAllLanes, t, o);
+            join_sums(m, t, m1, t1, ch);
+        }
+        if ((threadIdx.x & 31) == 0) {
+            sh->warp_top[threadIdx.x >> 5] = m;
+            sh->warp_noise[threadIdx.x >> 5] = t;
+        }
+    }
     uint32_t key = lmax == lmax ? logit_key(lmax) : 0xffffffffu;
     key = __reduce_max_sync(kAllLanes, key);
     if ((threadIdx.x & 31) == 0)
@@ -211,16 +246,12 @@ __device__ __noinline__ void weigh_places(Shared* sh) {
         uint32_t n = own_count(sh, D);
         unsigned long long m = 0;
         if (__any_sync(kAllLanes, n)) {
-            if (n) {
-                const float l = place_logit<ES>(scale.lmax, D);
-                const unsigned long long w = weight_fixed(scale, sh->pow2, l);
-                m = n * w;
-                if constexpr (ES == 4) {
-                    // width 2^-7 of the place's power of two; 1 / sqrt(12)
-                    const float e = (float)w * (__uint_as_float((__float_as_uint(l) & 0x7f800000u) - (7u << 23)) *
-                                                0.28867513f * scale.ch);
-                    noise += (float)n * e * e;
-                }
+            m = place_mass<ES>(scale, sh->pow2, D, n);
+            if (ES == 4 && n) {
+                // width 2^-7 of the place's power of two; 1 / sqrt(12)
+                const uint32_t b = __float_as_uint(place_logit<ES>(scale.lmax, D)) & 0x7f800000u;
+                const float e = (float)m * (__uint_as_float(b - (7u << 23)) * 0.28867513f * scale.ch);
+                noise += e * e / (float)n;
             }
             n = __reduce_add_sync(kAllLanes, n);
             m = warp_sum(m);
@@ -310,7 +341,7 @@ __device__ __noinline__ Found search_places(Shared* sh, int set, const Wanted s)
         Found f;
         f.bin = h.chunk * 32 + lane;
         f.count = own_count(sh, f.bin);
-        f.mass = f.count ? f.count * weight_call(sh->scale, sh->pow2, place_logit<ES>(sh->scale.lmax, f.bin)) : 0;
+        f.mass = place_mass<ES>(sh->scale, sh->pow2, f.bin, f.count);
         const Prefix x = warp_prefix(f.mass, f.count);
         f.above_mass = h.above_mass + x.before_mass;
         f.above_count = h.above_count + x.before_count;
@@ -441,8 +472,7 @@ __device__ __noinline__ void band_around(Shared* sh, int which, const Found f, u
     sh = here();
     const int lane = threadIdx.x & 31, D = f.bin - 16 + lane;
     const uint32_t n = D >= 1 && D <= kPlaces - 2 ? any_count(sh, D) : 0;
-    const Prefix x =
-        warp_prefix(n ? n * weight_call(sh->scale, sh->pow2, place_logit<4>(sh->scale.lmax, D)) : 0, n);
+    const Prefix x = warp_prefix(place_mass<4>(sh->scale, sh->pow2, D, n), n);
     const int r = lane & 15;
     // the middle place is lane 16
     const uint32_t mid = __shfl_sync(kAllLanes, x.before_count, 16);
@@ -620,47 +650,44 @@ __device__ __noinline__ Sums sum_exact(Shared* sh, bool list) {
         [&](uint32_t id) { one_exact(scalar_entry<4>(v.base, id), id); });
     return s;
 }
-// The row's sum in floats, to 2^-17 of itself (where `sum`), and the cut's entries.  A
-// weight is off by (l_max - l)/T * 2.5 * 2^-24 + 2^-22, below 2^-19 where it
-// counts (V < 2^20), and four of them are added before they become integers.
-__device__ __noinline__ unsigned long long sum_fast(Shared* sh, const StepCodes* codes, bool sum) {
+// The cut's entries alone.
+__device__ __noinline__ void list_entries(Shared* sh, const StepCodes* codes) {
     sh = here();
-    const RowScale scale = sh->scale;
     const View<4> v(sh);
-    const float low = sh->band[0].lo, one = sum ? (float)(1ull << scale.fix) : 0.0f;
-    unsigned long long s = 0;
-    const uint32_t least = sum ? 0u : step_code(low);
+    const float low = sh->band[0].lo;
+    const uint32_t least = step_code(low);
     const int shift = code_shift(v);
+    const auto take = [&](float l, uint32_t id) {
+        if (l >= low)
+            offer(&sh->list_n[0], list_at(sh, 0), l, id);
+    };
     v.walk_steps<kDeep, true>(
         [&](uint32_t s) { return codes->code[s >> shift] >= least; },
         [&](const uint4& w, uint32_t id) {
-            const float l[4] = {__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w)};
-            float t = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                t += ex2_approx((l[e] - scale.lmax) * scale.ch);
-            s += __float2ull_rn(t * one);
-            if (fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])) >= low) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (l[e] >= low)
-                        offer(&sh->list_n[0], list_at(sh, 0), l[e], id + e);
+            if (vector_max<4>(w) >= low) {
+                take(__uint_as_float(w.x), id);
+                take(__uint_as_float(w.y), id + 1);
+                take(__uint_as_float(w.z), id + 2);
+                take(__uint_as_float(w.w), id + 3);
             }
         },
-        [](uint32_t) {}, [](uint32_t) {},
-        [&](uint32_t id) {
-            const float l = scalar_entry<4>(v.base, id);
-            s += __float2ull_rn(ex2_approx((l - scale.lmax) * scale.ch) * one);
-            if (l >= low)
-                offer(&sh->list_n[0], list_at(sh, 0), l, id);
-        });
-    return s;
+        [](uint32_t) {}, [](uint32_t) {}, [&](uint32_t id) { take(scalar_entry<4>(v.base, id), id); });
+}
+
+// How far the first pass's float sum may be off, as a share of itself: 2^-n.  A weight
+// is off by (l_max - l)/T * 2.5 * 2^-24 + 2^-22, which keeps below 2^-17 of the sum for
+// any V.  Each of a thread's vectors may raise its maximum, which rescales its sum by a
+// power good to 2^-22 with two roundings of 2^-24 beside it: 2^-14 holds for 64 vectors
+// a thread and the joins of threads and CTAs.
+__device__ __forceinline__ int fast_bits(const Shared* sh) {
+    const uint32_t vectors = (sh->args.slice / 4 + kNT) / kNT;
+    return vectors <= 64 ? 14 : max(14 - (26 - __clz(vectors - 1)), 0);
 }
 
 // The lists of the second pass in the first CTA, and what they say of the cut and the
 // draw; leaves in sh->ok 1: found, 0: not in the lists, 2: too near a border for
 // these sums.  `first`: the lists are new.
-__device__ __noinline__ void settle(Shared* sh, bool by_mass, bool exact, bool first) {
+__device__ __noinline__ void settle(Shared* sh, bool by_mass, bool summed, bool first) {
     sh = here();
     const int tid = threadIdx.x, C = sh->args.C;
     const bool draw = sh->args.u != nullptr;
@@ -678,9 +705,12 @@ __device__ __noinline__ void settle(Shared* sh, bool by_mass, bool exact, bool f
     int ok = 3;  // 3: the draw is not in this list
     if (sh->band[0].on) {
         if (tid == 0) {
+            if (!summed)
+                sh->sums[0][0] = by_mass ? __float2ull_rn(sh->fast_sum * (float)(1ull << sh->scale.fix)) : 0;
             const unsigned long long whole = sh->sums[0][0];
             sh->want = {sh->k, sh->want_limit, sh->band[0].above_count, logit_key(sh->band[0].lo),
-                        by_mass ? ceil_scaled(sh->top_p, whole) : 0, sh->sums[1][0], exact ? 0 : whole >> 17};
+                        by_mass ? ceil_scaled(sh->top_p, whole) : 0, sh->sums[1][0],
+                        summed ? 0 : whole >> fast_bits(sh)};
         }
         __syncthreads();
         if (sh->want_limit > logit_key(sh->band[0].hi)) {
@@ -726,12 +756,11 @@ __device__ __noinline__ bool exact_pass(Shared* sh, const StepCodes* codes, bool
     sh = here();
     const int rank = cta_rank(), tid = threadIdx.x;
     for (bool first = true;; first = false, fine = true) {
-        const bool sums = by_mass || !sh->band[0].from_top || sh->args.mass;
         Sums s = {{0, 0, 0}};
-        if (sums && fine)
+        if (fine)
             s = sum_exact(sh, first);
         else
-            s.x[0] = sum_fast(sh, codes, sums);
+            list_entries(sh, codes);
 #pragma unroll
         for (int j = 0; j < 3; ++j) {
             const unsigned long long x = warp_sum(s.x[j]);
@@ -749,7 +778,7 @@ __device__ __noinline__ bool exact_pass(Shared* sh, const StepCodes* codes, bool
         }
         the_cluster().sync();
         if (rank == 0)
-            settle(sh, by_mass, fine || !sums, first);
+            settle(sh, by_mass, fine, first);
         share_cut(sh);
         const uint32_t ok = sh->ok;
         if (ok != 2)
@@ -799,8 +828,8 @@ __device__ __forceinline__ uint32_t cluster_sum(Shared* sh, uint32_t x) {
 // places around them, and lists the stretches' entries, among which the exact cut and
 // draw are found; where a stretch turns out not to hold them, the row is left to
 // the general way.  Few entries above the cut are listed whole, and need no
-// sum but the row's for top-p: it is taken in floats, to 2^-17, and where an entry
-// lies nearer to top-p's border than that, once more in integers.
+// sum but the row's for top-p: the first pass has it in floats, to 2^-14, and where an
+// entry lies nearer to top-p's border than that, a pass takes it in integers.
 
 // The counts and the scale of the weights.
 template <int ES>
@@ -812,6 +841,14 @@ __device__ __noinline__ bool count_places(Shared* sh, StepCodes* codes) {
     if (tid < C) {
         *peer(&sh->part_max[rank], tid) = key;
         *peer(&sh->part_tiny[rank], tid) = sh->count[kMags + 1] + sh->count[kMags + 2];
+        if (ES == 4 && sh->top_p < 1.0) {
+            float m = sh->warp_top[0], t = sh->warp_noise[0];
+            const float ch = __fdiv_rn(1.44269502162933349609375f, sh->T);
+            for (int w = 1; w < kNW; ++w)
+                join_sums(m, t, sh->warp_top[w], sh->warp_noise[w], ch);
+            *peer(&sh->part_top[rank], tid) = m;
+            *peer(&sh->part_sum[rank], tid) = t;
+        }
     }
     the_cluster().sync();
     uint32_t tiny = 0;  // entries below the window
@@ -824,8 +861,15 @@ __device__ __noinline__ bool count_places(Shared* sh, StepCodes* codes) {
     scale.lmax = key_logit(key);
     const float T = sh->T;
     split_scale(T > 0.0f ? T : 1.0f, scale.ch, scale.cl);
-    if (tid == 0)
+    if (tid == 0) {
         sh->scale = scale;
+        if (ES == 4 && sh->top_p < 1.0) {
+            float m = sh->part_top[0], t = sh->part_sum[0];
+            for (int r = 1; r < C; ++r)
+                join_sums(m, t, sh->part_top[r], sh->part_sum[r], scale.ch);
+            sh->fast_sum = t;
+        }
+    }
     __syncthreads();
     if (sh->code || key == 0xffffffffu || !inside(place_of(scale.lmax)))
         return false;
@@ -953,11 +997,11 @@ __device__ __noinline__ bool settle_exactly(Shared* sh, const StepCodes* codes) 
                 return false;
         }
     }
-    // float sums will do to tell whether an entry listed whole lies above top-p's
-    // border; not where they become part of the answer, or entries weigh too little
+    // a float sum will do to tell whether an entry listed whole lies above top-p's
+    // border; not where it becomes part of the answer, or entries weigh too little
     const bool fine =
         !sh->band[0].from_top || sh->args.mass ||
-        (by_mass && weight_call(sh->scale, sh->pow2, place_logit<4>(sh->scale.lmax, sh->cut_at.bin)) < sh->whole >> 15);
+        (by_mass && sh->cut_at.bin < kNoPlace && place_mass<4>(sh->scale, sh->pow2, sh->cut_at.bin, 1) < sh->whole >> 15);
     if (!exact_pass(sh, codes, by_mass, fine))
         return false;
     if (tid == 0) {
@@ -1008,8 +1052,8 @@ __device__ __noinline__ void general_row(Shared* sh, int code) {
     g.run(code);
 }
 
-// What the row's parts need to know: where it lies, by the first thread; its
-// settings, by one of the second warp, which nothing waits for before the counts are taken.
+// What the row's parts need to know: where it lies, and its settings; what only the
+// later parts need, by a thread that nothing waits for before the counts are taken.
 template <int ES>
 __device__ __forceinline__ void set_up(Shared* sh, const Args& a) {
     const int tid = threadIdx.x;
@@ -1028,6 +1072,12 @@ __device__ __forceinline__ void set_up(Shared* sh, const Args& a) {
         sh->want_limit = 0;
         const float inf = __int_as_float(0x7f800000);
         sh->band[0] = sh->band[1] = {inf, inf, 0, false, false};
+    } else if (tid == 32) {
+        const int64_t seq = row / (uint32_t)a.rows_per_seq;
+        const int32_t k = a.set.top_ks ? a.set.top_ks[seq] : a.set.top_k;
+        sh->T = a.set.temperatures ? a.set.temperatures[seq] : a.set.temperature;
+        sh->k = k > 0 ? (uint32_t)k : 0;
+        sh->top_p = a.set.top_ps ? (double)a.set.top_ps[seq] : a.set.top_p;
     } else if (tid >= 64 && tid < 128) {
         sh->pow2[tid - 64] = kPow2Steps[tid - 64];
     } else if (tid >= 128 && tid < 128 + 2 * kConds) {
@@ -1042,17 +1092,11 @@ __device__ __forceinline__ void set_up(Shared* sh, const Args& a) {
     __syncthreads();
     if (tid == 32) {
         const int64_t seq = row / (uint32_t)a.rows_per_seq;
-        const float T = a.set.temperatures ? a.set.temperatures[seq] : a.set.temperature;
-        const int32_t k = a.set.top_ks ? a.set.top_ks[seq] : a.set.top_k;
-        const double top_p = a.set.top_ps ? (double)a.set.top_ps[seq] : a.set.top_p;
         const double min_p = a.set.min_ps ? (double)a.set.min_ps[seq] : a.set.min_p;
-        const float u = a.u ? a.u[row * a.u_stride] : 0.0f;
-        sh->T = T;
+        const float T = sh->T, u = a.u ? a.u[row * a.u_stride] : 0.0f;
         sh->u = u;
-        sh->k = k > 0 ? (uint32_t)k : 0;
-        sh->top_p = top_p;
         sh->has_min = min_p > 0.0;
-        sh->code = !(T == 0.0f || (T >= 1.17549435e-38f && T <= 3.402823466e38f)) || !(top_p > 0.0) || !(min_p < 1.0)
+        sh->code = !(T == 0.0f || (T >= 1.17549435e-38f && T <= 3.402823466e38f)) || !(sh->top_p > 0.0) || !(min_p < 1.0)
                        ? SV_ERR_INVALID_ARG
                    : !(u >= 0.0f && u < 1.0f) ? SV_ERR_UNIFORM_RANGE
                                               : SV_OK;

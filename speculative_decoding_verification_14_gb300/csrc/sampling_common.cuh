@@ -246,6 +246,49 @@ __device__ __forceinline__ float vector_max_nan(const uint4& v) {
     }
 }
 
+// Sums of 2^((l - m) c) against two maxima, joined into the first: a new maximum, or a
+// NaN, which stays.
+__device__ __forceinline__ void join_sums(float& m, float& s, float m1, float s1, float c) {
+    const float grown = max_nan(m, m1), inf = __int_as_float(0x7f800000);
+    s = (m > -inf ? s * ex2_approx((m - grown) * c) : 0.0f) + (m1 > -inf ? s1 * ex2_approx((m1 - grown) * c) : 0.0f);
+    m = grown;
+}
+
+// sum of 2^((l - m) c) over a vector's logits: differences (a bfloat16 operand is
+// widened inside the subtraction), products and sums two at a time
+template <int ES>
+__device__ __forceinline__ float exp_sum(const uint4& v, float m, float c) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    unsigned long long cc, sum = 0;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(cc) : "f"(c));
+#pragma unroll
+    for (int j = 0; j < 8 / ES; ++j) {
+        float lo, hi;
+        if constexpr (ES == 2) {
+            asm("{\n\t.reg .b16 l, h;\n\t"
+                "mov.b32 {l, h}, %2;\n\t"
+                "add.rn.f32.bf16 %0, l, %3;\n\t"
+                "add.rn.f32.bf16 %1, h, %3;\n\t}"
+                : "=f"(lo), "=f"(hi)
+                : "r"(w[j]), "f"(-m));
+        } else {
+            lo = __uint_as_float(w[2 * j]) - m;
+            hi = __uint_as_float(w[2 * j + 1]) - m;
+        }
+        unsigned long long t;
+        asm("{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\tmul.rn.f32x2 %0, d, %3;\n\t}" : "=l"(t) : "f"(lo), "f"(hi), "l"(cc));
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(t));
+        asm("mov.b64 %0, {%1, %2};" : "=l"(t) : "f"(ex2_approx(lo)), "f"(ex2_approx(hi)));
+        if (j)
+            asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum) : "l"(t));
+        else
+            sum = t;
+    }
+    float lo, hi;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(sum));
+    return lo + hi;
+}
+
 // One CTA's part of a row: ids s0..s1-1, and its 16-byte vectors.  Number k holds the
 // ids from k E - off on, where off is the place of the row's first logit in its own
 // vector.  What they leave at the part's ends (the row's ends: parts meet between

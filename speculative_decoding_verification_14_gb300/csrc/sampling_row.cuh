@@ -133,11 +133,12 @@ struct alignas(16) Shared {
     Found found[kConds];
     unsigned long long part_mass[kMaxC];
     uint32_t part_cnt[kMaxC], part_max[kMaxC], part_tiny[kMaxC], part_list[2][kMaxC];
-    float part_noise[kMaxC];
+    float part_noise[kMaxC], part_top[kMaxC], part_sum[kMaxC];
+    float fast_sum;  // of the row, against its maximum (float32 under top-p)
     unsigned long long sums[3][kMaxC];
     unsigned long long warp_mass[3][kNW];
     uint32_t warp_cnt[kNW], warp_max[kNW];
-    float warp_noise[kNW];
+    float warp_noise[kNW], warp_top[kNW];
     unsigned long long few[kFew];  // weights of a short list
     uint32_t list_n[2];
     Band band[2];  // of the cut and of the draw
