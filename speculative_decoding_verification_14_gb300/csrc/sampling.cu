@@ -176,6 +176,7 @@ __device__ __noinline__ uint32_t count_pass(Shared* sh, StepCodes* codes) {
     if ((threadIdx.x & 31) == 0)
         sh->warp_max[threadIdx.x >> 5] = key;
     __syncthreads();
+#pragma unroll 1
     for (int w = 0; w < kNW; ++w)
         key = max(key, sh->warp_max[w]);
     return key;
@@ -220,6 +221,7 @@ __device__ __noinline__ void merge_counts(Shared* sh) {
                     atomicAdd(last - ((q + j * kNT) & (span - 1)), x[j]);
         }
     } else {
+#pragma unroll 1
         for (int r = 0; r < C; ++r)
             for (int i = tid; i < places; i += kNT) {
                 const uint32_t x = r == rank ? 0 : *(peer(last, r) - i);
@@ -273,6 +275,7 @@ __device__ __noinline__ void weigh_places(Shared* sh) {
         const int q = (c1 - c0 + 31) / 32, i0 = min(lane * q, c1 - c0), i1 = min(i0 + q, c1 - c0);
         unsigned long long m = 0;
         uint32_t n = 0;
+#pragma unroll 1
         for (int i = i0; i < i1; ++i) {
             m += chunks(sh)[i].mass;
             n += chunks(sh)[i].cnt;
@@ -280,6 +283,7 @@ __device__ __noinline__ void weigh_places(Shared* sh) {
         const Prefix x = warp_prefix(m, n);
         m = x.before_mass;
         n = x.before_count;
+#pragma unroll 1
         for (int i = i0; i < i1; ++i) {
             chunks(sh)[i].above_mass = m;
             chunks(sh)[i].above_cnt = n;
@@ -293,6 +297,7 @@ __device__ __noinline__ void weigh_places(Shared* sh) {
             *peer(&sh->part_cnt[rank], lane) = n;
             if constexpr (ES == 4) {
                 noise = 0.0f;
+#pragma unroll 1
                 for (int w = 0; w < kNW; ++w)
                     noise += sh->warp_noise[w];
                 *peer(&sh->part_noise[rank], lane) = noise;
@@ -321,6 +326,7 @@ __device__ __noinline__ Found search_places(Shared* sh, int set, const Wanted s)
     if (tid < c1 - c0) {
         unsigned long long before_m = chunks(sh)[tid].above_mass;
         uint32_t before_n = chunks(sh)[tid].above_cnt;
+#pragma unroll 1
         for (int r = 0; r < rank; ++r) {
             before_m += sh->part_mass[r];
             before_n += sh->part_cnt[r];
@@ -421,6 +427,7 @@ __device__ __noinline__ int64_t find_entry(Shared* sh, const StepCodes* codes, i
         if (tid < C)
             *peer(&sh->part_list[0][rank], tid) = n;
         the_cluster().sync();
+#pragma unroll 1
         for (int c = 0; c < rank; ++c) {
             if (r < sh->part_list[0][c])
                 return -1;
@@ -508,6 +515,7 @@ __device__ __noinline__ void pull_list(Shared* sh, int which) {
     unsigned long long* to = list_at(sh, which);
     const int C = sh->args.C;
     uint32_t n = 0;
+#pragma unroll 1
     for (int r = 0; r < C; ++r)
         n += sh->part_list[which][r];
     for (uint32_t i = sh->part_list[which][0] + threadIdx.x; i < n && i < (uint32_t)kList; i += kNT) {
@@ -566,7 +574,7 @@ __device__ __forceinline__ SumScale sum_scale(Shared* sh, const RowScale& s) {
     __syncthreads();
     return t;
 }
-// the weight as hi + lo, hi with 24 bits
+// the weight as the table's part and the rest
 __device__ __forceinline__ float2 sum_weight(const SumScale& s, float l) {
     constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
     l = fmaxf(l, s.floor_l);
@@ -580,76 +588,120 @@ __device__ __forceinline__ float2 sum_weight(const SumScale& s, float l) {
     const float two = __int_as_float(((k & ~127) << 16) + (127 << 23));  // 2^floor(k/128)
     return make_float2(t.x * two, fmaf(t.x, y, t.y) * two);
 }
-// Adds up to four weights: what a float of 2^-20 units takes of them, and the rest.
+// What FourSum's floats are worth in units of 2^-F.
+struct Units {
+    float one;         // 2^n, n = min(F, 37)
+    uint32_t hi, low;  // 2^(F - 20), 2^(F - n)
+    __device__ __forceinline__ explicit Units(int F)
+        : one((float)(1ull << min(F, 37))), hi(1u << (F - 20)), low(1u << (F - min(F, 37))) {}
+};
+// Adds up to four weights' first parts in a float of 2^-20 units, whose bits count them,
+// and what that and the second parts (|e^z - 1| < 2^-8.5) leave in one below 2^-6.5,
+// which an integer of 2^-37 units holds.
 struct FourSum {
-    static constexpr float kBase = 12.0f;
+    static constexpr float kBase = 8.0f;
     float hi = kBase, lo = 0.0f;
     __device__ __forceinline__ void add(float2 w) {
         const float s = hi + w.x, taken = s - hi;
         lo += w.y + (w.x - taken);
         hi = s;
     }
-    __device__ __forceinline__ unsigned long long fixed(float one) const {
-        return __float2ull_rn((hi - kBase) * one) + (unsigned long long)__float2ll_rn(lo * one);
+    __device__ __forceinline__ void into(unsigned long long& x, const Units& u) const {
+        x += (unsigned long long)(__float_as_uint(hi) - __float_as_uint(kBase)) * u.hi;
+        x += (long long)__float2int_rn(lo * u.one) * (int)u.low;
     }
 };
+
+// What a pass adds to: all, and of each stretch that is no list from the largest on what
+// lies above it.  With what goes to the lists; a stretch that is off, or whose entries the
+// list has, reaches from infinity on.
+struct Above {
+    float chi, clo, dhi, dlo;
+    __device__ __forceinline__ Above(const Shared* sh, bool list) {
+        const float inf = __int_as_float(0x7f800000);
+        chi = sh->band[0].hi;
+        dhi = sh->band[1].hi;
+        clo = list ? sh->band[0].lo : inf;
+        dlo = list ? sh->band[1].lo : inf;
+    }
+    __device__ __forceinline__ void take(Shared* sh, float l, uint32_t id) const {
+        if (l >= clo && l <= chi)
+            offer(&sh->list_n[0], list_at(sh, 0), l, id);
+        if (l >= dlo && l <= dhi)
+            offer(&sh->list_n[1], list_at(sh, 1), l, id);
+    }
+};
+
+// by weight_fixed, of the whole slice or its entries beside the vectors
+__device__ __noinline__ Sums sum_each(Shared* sh, bool list, bool edges) {
+    sh = here();
+    View<4> v(sh);
+    const Above a(sh, list);
+    Sums s = {{0, 0, 0}};
+    const auto one = [&](float l, uint32_t id) {
+        const unsigned long long x = weight_fixed(sh->scale, sh->pow2, l);
+        s.x[0] += x;
+        s.x[1] += l > a.chi ? x : 0;
+        s.x[2] += l > a.dhi ? x : 0;
+        a.take(sh, l, id);
+    };
+    const uint32_t head = edges ? v.head_end() : v.s1, tail = edges ? v.tail_start() : v.s1;
+    const uint32_t n = head - v.s0 + (v.s1 - tail);
+#pragma unroll 1
+    for (uint32_t j = threadIdx.x; j < n; j += kNT) {
+        const uint32_t id = j < head - v.s0 ? v.s0 + j : tail + (j - (head - v.s0));
+        one(scalar_entry<4>(v.base, id), id);
+    }
+    return s;
+}
 
 __device__ __noinline__ Sums sum_exact(Shared* sh, bool list) {
     sh = here();
     const RowScale scale = sh->scale;
-    const View<4> v(sh);
-    const float clo = sh->band[0].lo, chi = sh->band[0].hi, dlo = sh->band[1].lo, dhi = sh->band[1].hi;
-    const bool c = sh->band[0].on && !sh->band[0].from_top, d = sh->band[1].on;
-    const float low = list ? fminf(clo, dlo) : __int_as_float(0x7f800000);
-    Sums s = {{0, 0, 0}};
-    const auto take = [&](float l, uint32_t id) {
-        if (l >= low) {
-            if (l >= clo && l <= chi)
-                offer(&sh->list_n[0], list_at(sh, 0), l, id);
-            if (l >= dlo && l <= dhi)
-                offer(&sh->list_n[1], list_at(sh, 1), l, id);
-        }
-    };
-    const auto one_exact = [&](float l, uint32_t id) {
-        const unsigned long long x = weight_fixed(scale, sh->pow2, l);
-        s.x[0] += x;
-        s.x[1] += l > chi ? x : 0;
-        s.x[2] += l > dhi ? x : 0;
-        take(l, id);
-    };
-    if (!(fabsf(scale.lmax * scale.ch) < 128.0f)) {
-        v.each(one_exact);
+    const bool fits = fabsf(scale.lmax * scale.ch) < 128.0f;
+    Sums s = sum_each(sh, list, fits);
+    if (!fits)
         return s;
-    }
+    const View<4> v(sh);
+    const Above a(sh, list);
     const SumScale t = sum_scale(sh, scale);
-    const float one = (float)(1ull << scale.fix);
-    v.walk<2, true>(
+    const Units units(scale.fix);
+    v.walk<1, true>(
         [&](const uint4& w, uint32_t id) {
             const float l[4] = {__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w)};
             FourSum all, over_c, over_d;
+            bool listed = false;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const float2 x = sum_weight(t, l[e]);
                 all.add(x);
-                if (c && l[e] > chi)
+                if (l[e] > a.chi)
                     over_c.add(x);
-                if (d && l[e] > dhi)
+                else
+                    listed |= l[e] >= a.clo;
+                if (l[e] > a.dhi)
                     over_d.add(x);
+                else
+                    listed |= l[e] >= a.dlo;
             }
-            s.x[0] += all.fixed(one);
-            if (c)
-                s.x[1] += over_c.fixed(one);
-            if (d)
-                s.x[2] += over_d.fixed(one);
-            if (vector_max<4>(w) >= low) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    take(l[e], id + e);
+            all.into(s.x[0], units);
+            if (a.chi < __int_as_float(0x7f800000))
+                over_c.into(s.x[1], units);
+            if (a.dhi < __int_as_float(0x7f800000))
+                over_d.into(s.x[2], units);
+            if (listed) {
+                uint4 x = w;
+#pragma unroll 1
+                for (int e = 0; e < 4; ++e) {
+                    a.take(sh, __uint_as_float(x.x), id + e);
+                    x = make_uint4(x.y, x.z, x.w, 0);
+                }
             }
         },
-        [&](uint32_t id) { one_exact(scalar_entry<4>(v.base, id), id); });
+        [](uint32_t) {});
     return s;
 }
+
 // The cut's entries alone.
 __device__ __noinline__ void list_entries(Shared* sh, const StepCodes* codes) {
     sh = here();
@@ -693,6 +745,7 @@ __device__ __noinline__ void settle(Shared* sh, bool by_mass, bool summed, bool 
     const bool draw = sh->args.u != nullptr;
     if (tid < 3) {
         unsigned long long x = 0;
+#pragma unroll 1
         for (int r = 0; r < C; ++r)
             x += sh->sums[tid][r];
         sh->sums[tid][0] = x;
@@ -770,6 +823,7 @@ __device__ __noinline__ bool exact_pass(Shared* sh, const StepCodes* codes, bool
         __syncthreads();
         if (tid < 3) {
             unsigned long long x = 0;
+#pragma unroll 1
             for (int w = 0; w < kNW; ++w)
                 x += sh->warp_mass[tid][w];
             *peer(&sh->sums[tid][rank], 0) = x;
@@ -814,6 +868,7 @@ __device__ __forceinline__ uint32_t cluster_sum(Shared* sh, uint32_t x) {
         *peer(&sh->part_tiny[cta_rank()], threadIdx.x) = x;
     the_cluster().sync();
     x = 0;
+#pragma unroll 1
     for (int r = 0; r < C; ++r)
         x += sh->part_tiny[r];
     return x;
@@ -844,6 +899,7 @@ __device__ __noinline__ bool count_places(Shared* sh, StepCodes* codes) {
         if (ES == 4 && sh->top_p < 1.0) {
             float m = sh->warp_top[0], t = sh->warp_noise[0];
             const float ch = __fdiv_rn(1.44269502162933349609375f, sh->T);
+#pragma unroll 1
             for (int w = 1; w < kNW; ++w)
                 join_sums(m, t, sh->warp_top[w], sh->warp_noise[w], ch);
             *peer(&sh->part_top[rank], tid) = m;
@@ -852,6 +908,7 @@ __device__ __noinline__ bool count_places(Shared* sh, StepCodes* codes) {
     }
     the_cluster().sync();
     uint32_t tiny = 0;  // entries below the window
+#pragma unroll 1
     for (int r = 0; r < C; ++r) {
         key = max(key, sh->part_max[r]);
         tiny += sh->part_tiny[r];
@@ -865,6 +922,7 @@ __device__ __noinline__ bool count_places(Shared* sh, StepCodes* codes) {
         sh->scale = scale;
         if (ES == 4 && sh->top_p < 1.0) {
             float m = sh->part_top[0], t = sh->part_sum[0];
+#pragma unroll 1
             for (int r = 1; r < C; ++r)
                 join_sums(m, t, sh->part_top[r], sh->part_sum[r], scale.ch);
             sh->fast_sum = t;
@@ -890,6 +948,7 @@ __device__ __noinline__ void take_largest(Shared* sh, const StepCodes* codes) {
     const int64_t id = find_entry(sh, codes, place_of(sh->scale.lmax), 0);
     if (id >= 0) {
         put_token(sh, (int32_t)id, 1.0f);
+#pragma unroll 1
         for (int r = 0; r < sh->args.C; ++r)
             *peer(&sh->token, r) = (uint32_t)id;
     }
@@ -910,6 +969,7 @@ __device__ __noinline__ bool find_cut(Shared* sh) {
     weigh_places<ES>(sh);
     unsigned long long whole = 0;
     uint32_t near = 0;
+#pragma unroll 1
     for (int r = 0; r < C; ++r) {
         whole += sh->part_mass[r];
         near += sh->part_cnt[r];
@@ -980,6 +1040,7 @@ __device__ __noinline__ bool settle_exactly(Shared* sh, const StepCodes* codes) 
     const bool by_mass = sh->top_p < 1.0, draw = sh->args.u != nullptr;
     // four standard deviations of the places' sum, and what their middles miss
     float noise = 0.0f;
+#pragma unroll 1
     for (int r = 0; r < sh->args.C; ++r)
         noise += sh->part_noise[r];
     const unsigned long long margin = __float2ull_rn(4.0f * sqrtf(noise)) + (sh->whole >> 12);

@@ -211,6 +211,7 @@ __device__ __noinline__ Prefix cta_prefix(Shared* sh, unsigned long long m, uint
     __syncthreads();
     p.mass = 0;
     p.count = 0;
+#pragma unroll 1
     for (int w = 0; w < kNW; ++w) {
         if (w < warp) {
             p.before_mass += sh->warp_mass[0][w];
@@ -230,6 +231,7 @@ __device__ __forceinline__ uint32_t cta_sum(Shared* sh, uint32_t x) {
         sh->warp_cnt[threadIdx.x >> 5] = x;
     __syncthreads();
     x = 0;
+#pragma unroll 1
     for (int w = 0; w < kNW; ++w)
         x += sh->warp_cnt[w];
     return x;
@@ -241,6 +243,7 @@ __device__ __forceinline__ unsigned long long cta_sum(Shared* sh, unsigned long 
         sh->warp_mass[0][threadIdx.x >> 5] = x;
     __syncthreads();
     x = 0;
+#pragma unroll 1
     for (int w = 0; w < kNW; ++w)
         x += sh->warp_mass[0][w];
     return x;
@@ -328,6 +331,7 @@ __device__ __noinline__ Prefix list_prefix(Shared* sh, int which) {
     const int n = (int)sh->list_n[which], own = (n + kNT - 1) / kNT;
     const int i0 = min(own * (int)threadIdx.x, n), i1 = min(i0 + own, n);
     unsigned long long m = 0;
+#pragma unroll 1
     for (int i = i0; i < i1; ++i)
         m += weight_call(sh->scale, sh->pow2, key_logit((uint32_t)(list[i] >> 32)));
     return cta_prefix(sh, m, 0);
@@ -357,6 +361,7 @@ __device__ __noinline__ int cut_in_sorted(Shared* sh) {
     unsigned long long at = c.above_mass + x.before_mass;
     int last = -1;
     bool near = false;
+#pragma unroll 1
     for (int i = i0; i < i1; ++i) {
         const uint32_t key = (uint32_t)(sh->list[i] >> 32);
         const bool start = i == 0 || (uint32_t)(sh->list[i - 1] >> 32) != key;
@@ -375,6 +380,7 @@ __device__ __noinline__ int cut_in_sorted(Shared* sh) {
         sh->warp_max[warp] = (uint32_t)(last + 1);
     __syncthreads();
     int g = 0;
+#pragma unroll 1
     for (int i = 0; i < kNW; ++i)
         g = max(g, (int)sh->warp_max[i]);
     --g;  // -1: nothing of the list is kept
@@ -408,6 +414,7 @@ __device__ __noinline__ bool draw_in_sorted(Shared* sh, int which, unsigned long
     const int i0 = min(own * (int)threadIdx.x, n), i1 = min(i0 + own, n);
     const Prefix x = list_prefix(sh, which);
     unsigned long long at = above_mass + x.before_mass;
+#pragma unroll 1
     for (int i = i0; i < i1; ++i) {
         const uint32_t key = (uint32_t)(list[i] >> 32);
         const unsigned long long w = weight_call(sh->scale, sh->pow2, key_logit(key));
@@ -467,6 +474,7 @@ __device__ __noinline__ int resolve_few(Shared* sh, int which, bool cut, bool dr
         __syncthreads();
         if (tid == 0) {
             uint32_t x = 0xffffffffu;
+#pragma unroll 1
             for (int i = 0; i < kNW; ++i)
                 x = min(x, sh->warp_max[i]);
             sh->cut_key = number ? x : c.limit_key;
