@@ -140,6 +140,7 @@ struct alignas(16) Shared {
     uint32_t warp_cnt[kNW], warp_max[kNW];
     float warp_noise[kNW], warp_top[kNW];
     unsigned long long few[kFew];  // weights of a short list
+    unsigned long long list_mass;  // in all
     uint32_t list_n[2];
     Band band[2];  // of the cut and of the draw
     uint32_t want_limit;  // the least key min-p keeps
@@ -184,7 +185,7 @@ __device__ __noinline__ Prefix warp_prefix(unsigned long long m, uint32_t n) {
     Prefix p;
     p.mass = m;
     p.count = n;
-#pragma unroll
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
         const unsigned long long pm = __shfl_up_sync(kAllLanes, p.mass, o);
         const uint32_t pn = __shfl_up_sync(kAllLanes, p.count, o);
@@ -428,26 +429,28 @@ __device__ __noinline__ bool draw_in_sorted(Shared* sh, int which, unsigned long
     return above_mass <= target && above_mass + x.mass > target;
 }
 
-// The same for a list of at most kFew entries in any order, each thread comparing
-// its entry with all: what is larger than it, and what comes before it.  `cut`: find the
-// cut (else all of the list counts as kept); `draw`: then the draw at u E, the kept mass E
+// The same for a list of at most kFew entries in any order, a few threads comparing an
+// entry with all: what is larger than it, and what comes before it.  `cut`: find the cut
+// (else all of the list counts as kept); `draw`: then the draw at u E, the kept mass E
 // being the cut's or, without one, sh->kept_mass.
 __device__ __noinline__ int resolve_few(Shared* sh, int which, bool cut, bool draw) {
     sh = here();
     const Cut& c = sh->want;
-    const int tid = threadIdx.x, n = (int)sh->list_n[which];
+    const int tid = threadIdx.x, warp = tid >> 5, n = (int)sh->list_n[which];
     const unsigned long long* list = list_at(sh, which);
-    const bool has = tid < n;
-    const unsigned long long mine = has ? list[tid] : 0;
-    const uint32_t key = (uint32_t)(mine >> 32);
-    const unsigned long long w = has ? weight_call(sh->scale, sh->pow2, key_logit(key)) : 0;
-    if (has)
-        sh->few[tid] = w;
+    if (tid < n)
+        sh->few[tid] = weight_call(sh->scale, sh->pow2, key_logit((uint32_t)(list[tid] >> 32)));
     __syncthreads();
-    unsigned long long larger = c.above_mass, before = c.above_mass;
-    uint32_t count = c.above_count;
-    if (has)
-        for (int j = 0; j < n; ++j) {
+    // 2, 4 or 8 threads to an entry
+    const int lg = n > 64 ? 1 : n > 32 ? 2 : 3, at = tid >> lg;
+    static_assert(kFew << 1 == kNT);
+    const unsigned long long mine = at < n ? list[at] : 0;
+    const uint32_t key = (uint32_t)(mine >> 32);
+    unsigned long long larger = 0, before = 0;
+    uint32_t count = 0;
+    if (at < n) {
+#pragma unroll 2
+        for (int j = tid & ((1 << lg) - 1); j < n; j += 1 << lg) {
             const unsigned long long o = list[j], x = sh->few[j];
             if (o > mine)
                 before += x;
@@ -456,6 +459,18 @@ __device__ __noinline__ int resolve_few(Shared* sh, int which, bool cut, bool dr
                 ++count;
             }
         }
+    }
+#pragma unroll 1
+    for (int o = 1 << lg >> 1; o; o >>= 1) {
+        larger += __shfl_xor_sync(kAllLanes, larger, o);
+        before += __shfl_xor_sync(kAllLanes, before, o);
+        count += __shfl_xor_sync(kAllLanes, count, o);
+    }
+    larger += c.above_mass;
+    before += c.above_mass;
+    count += c.above_count;
+    const bool has = at < n && (tid & ((1 << lg) - 1)) == 0;
+    const unsigned long long w = has ? sh->few[at] : 0;
     bool kept = has;
     int ok = 1;
     if (cut) {
@@ -465,24 +480,34 @@ __device__ __noinline__ int resolve_few(Shared* sh, int which, bool cut, bool dr
             near = count > 0 && (larger < c.p ? c.p - larger : larger - c.p) < c.slack;
             kept = larger < c.p;
         }
-        const bool any_near = __syncthreads_or(near);
-        const unsigned long long all = cta_sum(sh, w), mass = cta_sum(sh, kept ? w : 0ull);
-        const uint32_t number = (uint32_t)__syncthreads_count(kept);
+        // the least key kept, how many, their mass, and the list's
         const uint32_t least = __reduce_min_sync(kAllLanes, kept ? key : 0xffffffffu);
-        if ((tid & 31) == 0)
-            sh->warp_max[tid >> 5] = least;
-        __syncthreads();
+        const unsigned long long list_mass = warp_sum(w), kept_mass = warp_sum(kept ? w : 0ull);
+        const uint32_t number = __popc(__ballot_sync(kAllLanes, kept));
+        if ((tid & 31) == 0) {
+            sh->warp_max[warp] = least;
+            sh->warp_mass[0][warp] = list_mass;
+            sh->warp_mass[1][warp] = kept_mass;
+            sh->warp_cnt[warp] = number;
+        }
+        const bool any_near = __syncthreads_or(near);
         if (tid == 0) {
-            uint32_t x = 0xffffffffu;
+            uint32_t x = 0xffffffffu, sum = 0;
+            unsigned long long all = 0, mass = 0;
 #pragma unroll 1
-            for (int i = 0; i < kNW; ++i)
+            for (int i = 0; i < kNW; ++i) {
                 x = min(x, sh->warp_max[i]);
-            sh->cut_key = number ? x : c.limit_key;
-            sh->kept = c.above_count + number;
+                all += sh->warp_mass[0][i];
+                mass += sh->warp_mass[1][i];
+                sum += sh->warp_cnt[i];
+            }
+            sh->cut_key = sum ? x : c.limit_key;
+            sh->kept = c.above_count + sum;
             sh->kept_mass = c.above_mass + mass;
+            sh->list_mass = all;
         }
         __syncthreads();
-        ok = any_near ? 2 : cut_inside(c, n, all);
+        ok = any_near ? 2 : cut_inside(c, n, sh->list_mass);
     }
     if (ok == 1 && draw) {
         const unsigned long long target = floor_scaled(sh->u, sh->kept_mass);
