@@ -588,17 +588,18 @@ __device__ __forceinline__ float2 sum_weight(const SumScale& s, float l) {
     const float two = __int_as_float(((k & ~127) << 16) + (127 << 23));  // 2^floor(k/128)
     return make_float2(t.x * two, fmaf(t.x, y, t.y) * two);
 }
-// What FourSum's floats are worth in units of 2^-F.
+// What WeightSum's parts are worth in units of 2^-F.
 struct Units {
-    float one;         // 2^n, n = min(F, 37)
+    float one, back;   // 2^n, n = min(F, 37), and 2^-n
     uint32_t hi, low;  // 2^(F - 20), 2^(F - n)
     __device__ __forceinline__ explicit Units(int F)
-        : one((float)(1ull << min(F, 37))), hi(1u << (F - 20)), low(1u << (F - min(F, 37))) {}
+        : one((float)(1ull << min(F, 37))), back(1.0f / one), hi(1u << (F - 20)), low(1u << (F - min(F, 37))) {}
 };
-// Adds up to four weights' first parts in a float of 2^-20 units, whose bits count them,
-// and what that and the second parts (|e^z - 1| < 2^-8.5) leave in one below 2^-6.5,
-// which an integer of 2^-37 units holds.
-struct FourSum {
+// A sum of weights.  Of four at a time, the table's parts go to a float of 2^-20 units,
+// whose bits count them, and what that and the rests (|e^z - 1| < 2^-8.5) leave to one
+// below 2^-6.5.  An integer takes its 2^-37 units, and what is less stays for the next four:
+// a row's many small weights are not rounded away one by one.
+struct WeightSum {
     static constexpr float kBase = 8.0f;
     float hi = kBase, lo = 0.0f;
     __device__ __forceinline__ void add(float2 w) {
@@ -606,10 +607,14 @@ struct FourSum {
         lo += w.y + (w.x - taken);
         hi = s;
     }
-    __device__ __forceinline__ void into(unsigned long long& x, const Units& u) const {
+    __device__ __forceinline__ void into(unsigned long long& x, const Units& u) {
+        const int units = __float2int_rn(lo * u.one);
         x += (unsigned long long)(__float_as_uint(hi) - __float_as_uint(kBase)) * u.hi;
-        x += (long long)__float2int_rn(lo * u.one) * (int)u.low;
+        x += (long long)units * (int)u.low;
+        lo = fmaf((float)units, -u.back, lo);
+        hi = kBase;
     }
+    __device__ __forceinline__ long long rest(int F) const { return __float2ll_rn(lo * (float)(1ull << F)); }
 };
 
 // What a pass adds to: all, and of each stretch that is no list from the largest on what
@@ -666,10 +671,10 @@ __device__ __noinline__ Sums sum_exact(Shared* sh, bool list) {
     const Above a(sh, list);
     const SumScale t = sum_scale(sh, scale);
     const Units units(scale.fix);
+    WeightSum all, over_c, over_d;
     v.walk<1, true>(
         [&](const uint4& w, uint32_t id) {
             const float l[4] = {__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w)};
-            FourSum all, over_c, over_d;
             bool listed = false;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -699,6 +704,9 @@ __device__ __noinline__ Sums sum_exact(Shared* sh, bool list) {
             }
         },
         [](uint32_t) {});
+    s.x[0] += all.rest(scale.fix);
+    s.x[1] += over_c.rest(scale.fix);
+    s.x[2] += over_d.rest(scale.fix);
     return s;
 }
 
