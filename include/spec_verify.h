@@ -358,7 +358,7 @@ typedef struct {
  *   uniforms  float in [0, 1), row r's at r * uniforms_stride
  *   tokens    out int32, row r's at r * tokens_stride
  *   probs     optional out float, row r at r * probs_stride: w_v / E on the
- *             kept entries (E their sum), 0 elsewhere
+ *             kept entries (E their sum), 0 elsewhere; memory apart from logits
  *   p_token   optional out float [R]: the drawn token's entry of probs
  *   kept      optional out int32 [R]: entries kept
  *   status    optional out int32 [R]
@@ -369,8 +369,8 @@ typedef struct {
  * whose running sum exceeds u * E.  (The verify's draws run by ascending id
  * alone: the same law, another token for the same uniform.)  Weights are
  * integers, good to 2^-39 of themselves and 2^-44 of the largest (for V up to
- * 2^19; a bit less for each doubling beyond), so a draw or a cut does not depend
- * on the order of any sum, and repeated calls give the same bits.
+ * 2^19; a bit less for each doubling beyond); a float32 row's sums are good to
+ * 2^-31 of themselves.  Repeated calls give the same bits.
  *
  * An erroneous row (a bad setting; a uniform outside [0, 1): SV_ERR_UNIFORM_RANGE;
  * a NaN or +inf, or only -inf: SV_ERR_NONFINITE) gets token -1, kept 0, NaN
@@ -379,8 +379,8 @@ typedef struct {
  * Asynchronous, no allocation, one launch on `stream`; safe to capture.
  * Returns SV_OK, SV_ERR_INVALID_ARG (null or misaligned pointers, B or
  * rows_per_seq - 1 or V beyond the context's limits, a stride below its row,
- * R * logits_stride >= 2^40, a setting out of range), SV_ERR_UNSUPPORTED or
- * SV_ERR_CUDA. */
+ * R * logits_stride >= 2^40, outputs where the logits lie, a setting out of
+ * range), SV_ERR_UNSUPPORTED or SV_ERR_CUDA. */
 int spec_sample_run(sv_ctx* ctx, const void* logits, int logits_dtype, int64_t logits_stride,
                     const float* uniforms, int64_t uniforms_stride, int B, int rows_per_seq,
                     int64_t V, const sv_sampling* settings, int32_t* tokens, int64_t tokens_stride,
@@ -407,7 +407,8 @@ int spec_filter_run(sv_ctx* ctx, const void* logits, int logits_dtype, int64_t l
 
 /* The launch plan of the two calls above on the context's device, and their
  * planner as a pure host function (no CUDA call): one cluster per row, the
- * largest whose CTAs (four of 256 threads per SM) hold every row at once. */
+ * largest whose CTAs (four of 256 threads per SM) hold every row at once and
+ * leave each CTA enough of it. */
 int spec_sample_get_plan(sv_ctx* ctx, int B, int rows_per_seq, int64_t V, int logits_dtype,
                          sv_plan* out);
 int spec_sample_plan_for(int num_sms, int max_cluster, int B, int rows_per_seq, int64_t V,

@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kNT, 4) sv_logprobs_kernel(const __grid_consta
     if (tid == 0) {
         a.logprob[row] = value(lx);
         if (a.rank)
-            a.rank[row] = (int32_t)above + 1;
+            a.rank[row] = (int32_t)min(above + 1, 0x7fffffffu);
         if (a.status)
             a.status[row] = SV_OK;
     }

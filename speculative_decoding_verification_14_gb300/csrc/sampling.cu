@@ -1248,6 +1248,13 @@ int check(const sv_ctx* ctx, const void* logits, int dtype, int64_t stride, int 
     return SV_OK;
 }
 
+// Whether n rows of x_bytes from x on lie among n rows of y_bytes from y on.
+bool meet(const void* x, int64_t x_stride, const void* y, int64_t y_stride, int64_t n, int64_t x_bytes,
+          int64_t y_bytes) {
+    const char *x0 = static_cast<const char*>(x), *y0 = static_cast<const char*>(y);
+    return y0 < x0 + (n - 1) * x_stride + x_bytes && x0 < y0 + (n - 1) * y_stride + y_bytes;
+}
+
 }  // namespace
 
 namespace sv {
@@ -1294,6 +1301,9 @@ int spec_sample_run(sv_ctx* ctx, const void* logits, int logits_dtype, int64_t l
         !aligned(probs, 4) || !aligned(p_token, 4) || !aligned(kept, 4) || !aligned(status, 4) ||
         (probs && (probs_stride < V || probs_stride > most)))
         return SV_ERR_INVALID_ARG;
+    if (probs && meet(logits, logits_stride * (logits_dtype == SV_BF16 ? 2 : 4), probs, probs_stride * 4,
+                      (int64_t)B * rows_per_seq, V * (logits_dtype == SV_BF16 ? 2 : 4), V * 4))
+        return SV_ERR_INVALID_ARG;
     Args a;
     std::memset(&a, 0, sizeof a);
     a.logits = logits;
@@ -1324,10 +1334,9 @@ int spec_filter_run(sv_ctx* ctx, const void* logits, int logits_dtype, int64_t l
         !aligned(status, 4))
         return SV_ERR_INVALID_ARG;
     // in place, or apart: rows that overlap others would be read after they were written
-    const int64_t last = (int64_t)B * rows_per_seq - 1;
-    const char *i0 = static_cast<const char*>(logits), *o0 = static_cast<char*>(out_logits);
-    const char *i1 = i0 + (last * logits_stride + V) * es, *o1 = o0 + (last * out_stride + V) * es;
-    if (o0 < i1 && i0 < o1 && !(i0 == o0 && (last == 0 || logits_stride == out_stride)))
+    const int64_t n = (int64_t)B * rows_per_seq;
+    if (meet(logits, logits_stride * es, out_logits, out_stride * es, n, V * es, V * es) &&
+        !(logits == out_logits && (n == 1 || logits_stride == out_stride)))
         return SV_ERR_INVALID_ARG;
     Args a;
     std::memset(&a, 0, sizeof a);

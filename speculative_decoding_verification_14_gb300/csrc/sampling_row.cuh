@@ -645,7 +645,7 @@ __device__ __forceinline__ void put_rest(const Shared* sh, int code, uint32_t ke
         if (a.mass)
             a.mass[sh->row] = code ? __int_as_float(0x7fffffff) : (float)((double)mass / (double)whole);
         if (a.kept)
-            a.kept[sh->row] = (int32_t)kept;
+            a.kept[sh->row] = (int32_t)min(kept, 0x7fffffffu);
         if (a.status)
             a.status[sh->row] = code;
         if (code)

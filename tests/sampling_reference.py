@@ -1,10 +1,11 @@
 """The sampling operators in 64 bits, row by row, from their definitions: what the GPU tests compare
 with.  Besides each answer the functions say how far it is from another one (margin): the distance
 of the nearest filter border, or of the uniform from the nearest step of the running sum, as a share
-of the mass it is measured against.  Kernels hold weights as integers
-good to 2^-39 of themselves and 2^-44 of the largest: sums of V of them are off by 2^-39 of themselves
-and, with V <= 2^18 roundings that are as good as independent, by 2^-44 * 2^9 of the largest weight.
-Both are below 1e-10, so answers with a larger margin than MARGIN have to be equal."""
+of the mass it is measured against.  Kernels hold weights as integers good to 2^-39 of themselves and
+2^-44 of the largest: sums of V of them are off by 2^-39 of themselves and, with V <= 2^18 roundings
+that are as good as independent, by 2^-44 * 2^9 of the largest weight: both below 1e-10.  A float32
+row's sums take weights with y = e^z - 1, |z| < 2^-8.5, in one float: four roundings of 2^-33 of the
+weight, 4.7e-10 if all of them agree.  Answers with a larger margin than MARGIN have to be equal."""
 import numpy as np
 
 MARGIN = 1e-9

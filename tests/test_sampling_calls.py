@@ -115,7 +115,8 @@ def test_refusals_launch_nothing(sv):
         for bad in shared + bad_settings + [
                 dict(uniforms_ptr=None), dict(uniforms_ptr=u.data_ptr() + 1), dict(uniforms_stride=0),
                 dict(tokens_ptr=None), dict(tokens_stride=0), dict(tokens_ptr=tok.data_ptr() + 1),
-                dict(probs_stride=V - 1), dict(probs_ptr=out.data_ptr() + 1), dict(kept_ptr=ints.data_ptr() + 1),
+                dict(probs_stride=V - 1), dict(probs_ptr=out.data_ptr() + 1), dict(probs_ptr=lg.data_ptr()),
+                dict(probs_ptr=lg.data_ptr() + 4 * V), dict(kept_ptr=ints.data_ptr() + 1),
                 dict(p_token_ptr=fl.data_ptr() + 1)]:
             assert sv.spec_sample_run(**{**sample, **bad}) == sv.SV_ERR_INVALID_ARG, bad
         filt = {k: sample[k] for k in ("ctx", "logits_ptr", "dtype", "logits_stride", "B", "rows_per_seq", "V",
