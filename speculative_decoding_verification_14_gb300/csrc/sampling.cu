@@ -251,9 +251,11 @@ __device__ __noinline__ void weigh_places(Shared* sh) {
             m = place_mass<ES>(scale, sh->pow2, D, n);
             if (ES == 4 && n) {
                 // width 2^-7 of the place's power of two; 1 / sqrt(12)
-                const uint32_t b = __float_as_uint(place_logit<ES>(scale.lmax, D)) & 0x7f800000u;
-                const float e = (float)m * (__uint_as_float(b - (7u << 23)) * 0.28867513f * scale.ch);
-                noise += e * e / (float)n;
+                const float l = place_logit<ES>(scale.lmax, D);
+                const uint32_t b = __float_as_uint(l) & 0x7f800000u;
+                const float e = ex2_approx((l - scale.lmax) * scale.ch) *
+                                (__uint_as_float(b - (7u << 23)) * 0.28867513f * scale.ch);
+                noise = fmaf(e * e, (float)n, noise);
             }
             n = __reduce_add_sync(kAllLanes, n);
             m = warp_sum(m);
@@ -1051,7 +1053,7 @@ __device__ __noinline__ bool settle_exactly(Shared* sh, const StepCodes* codes) 
 #pragma unroll 1
     for (int r = 0; r < sh->args.C; ++r)
         noise += sh->part_noise[r];
-    const unsigned long long margin = __float2ull_rn(4.0f * sqrtf(noise)) + (sh->whole >> 12);
+    const unsigned long long margin = __float2ull_rn(4.0f * sqrtf(noise) * (float)(1ull << sh->scale.fix)) + (sh->whole >> 12);
     if (sh->cut_at.bin < kNoPlace) {
         band_around(sh, 0, sh->cut_at, margin);
         if (!sh->band[0].on)
