@@ -113,9 +113,19 @@ __global__ void __launch_bounds__(kNT, 4) sv_logprobs_kernel(const __grid_consta
     float m = -inf, s = 0.0f;
     uint32_t above = 0;
     const auto grow = [&](float top) { join_sums(m, s, top, 0.0f, a.ch); };
-    v.template walk<4, false>(
+    StepCodes codes;
+    const int shift = v.code_shift();
+    if (shift) {  // else every step has a code of its own
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            codes.code[i] = 0;
+    }
+    float step = -inf;  // the step's largest
+    v.template walk_steps<kDeep, false>(
+        [](uint32_t) { return true; },
         [&](const uint4& w, uint32_t) {
             const float top = vector_max_nan<ES>(w);
+            step = max_nan(step, top);
             if (!(top <= m))
                 grow(top);
             if (top > lx) {
@@ -125,6 +135,13 @@ __global__ void __launch_bounds__(kNT, 4) sv_logprobs_kernel(const __grid_consta
             }
             if (top > -inf)  // else m may be -inf too
                 s += exp_sum<ES>(w, m, a.ch);
+        },
+        [](uint32_t) {},
+        [&](uint32_t i) {
+            const uint8_t x = (uint8_t)step_code(step);
+            if (shift == 0 || x > codes.code[i >> shift])
+                codes.code[i >> shift] = x;
+            step = -inf;
         },
         [&](uint32_t id) {
             const float l = scalar_entry<ES>(base, id);
@@ -184,7 +201,9 @@ __global__ void __launch_bounds__(kNT, 4) sv_logprobs_kernel(const __grid_consta
                 }
             };
             const float least = key_logit(bound);
-            v.template walk<4, true>(
+            const uint32_t code = step_code(least);
+            v.template walk_steps<kDeep, true>(
+                [&](uint32_t i) { return codes.code[i >> shift] >= code; },
                 [&](const uint4& w, uint32_t id) {
                     if (vector_max<ES>(w) >= least) {
 #pragma unroll
@@ -192,6 +211,7 @@ __global__ void __launch_bounds__(kNT, 4) sv_logprobs_kernel(const __grid_consta
                             offer(vector_entry<ES>(w, e), id + e);
                     }
                 },
+                [](uint32_t) {}, [](uint32_t) {},
                 [&](uint32_t id) { offer(scalar_entry<ES>(base, id), id); });
         }
         __syncthreads();

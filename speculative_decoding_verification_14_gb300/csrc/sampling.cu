@@ -104,7 +104,7 @@ template <int ES>
 __device__ __noinline__ uint32_t count_pass(Shared* sh, StepCodes* codes) {
     sh = here();
     const View<ES> v(sh);
-    const int shift = code_shift(v);
+    const int shift = v.code_shift();
     float lmax = __int_as_float(0xff800000);
     float step = lmax;           // float32: a step's largest
     // float32 under top-p: the row's sum, too, in floats
@@ -392,7 +392,7 @@ __device__ __noinline__ int64_t find_entry(Shared* sh, const StepCodes* codes, i
     const uint32_t bits = __float_as_uint(l) >> 16, two = bits * 0x10001u;
     const unsigned short* q = reinterpret_cast<const unsigned short*>(v.base);
     const uint32_t least = step_code(l);
-    const int shift = code_shift(v);
+    const int shift = v.code_shift();
     constexpr uint32_t kIds = kPlaces;
     uint32_t* ids = sh->count;  // the counts are done with
     const auto found = [&](uint32_t id) {
@@ -718,7 +718,7 @@ __device__ __noinline__ void list_entries(Shared* sh, const StepCodes* codes) {
     const View<4> v(sh);
     const float low = sh->band[0].lo;
     const uint32_t least = step_code(low);
-    const int shift = code_shift(v);
+    const int shift = v.code_shift();
     const auto take = [&](float l, uint32_t id) {
         if (l >= low)
             offer(&sh->list_n[0], list_at(sh, 0), l, id);

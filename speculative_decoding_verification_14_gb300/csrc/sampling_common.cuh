@@ -289,6 +289,18 @@ __device__ __forceinline__ float exp_sum(const uint4& v, float m, float c) {
     return lo + hi;
 }
 
+// The largest logit of each of a thread's steps through the slice (the first pass goes
+// kDeep vectors a step, and so do later ones), to quarters and in eight bits: later
+// passes leave out the steps that hold nothing for them.  Long slices' steps share the
+// 16 codes.
+constexpr int kDeep = 4;
+struct StepCodes {
+    uint8_t code[16];
+};
+__device__ __forceinline__ uint32_t step_code(float l) {  // grows with l; NaN: the largest
+    const float x = fmaf(l, 4.0f, 64.0f);
+    return x < 0.0f ? 0u : x < 255.0f ? (uint32_t)x : 255u;
+}
 // One CTA's part of a row: ids s0..s1-1, and its 16-byte vectors.  Number k holds the
 // ids from k E - off on, where off is the place of the row's first logit in its own
 // vector.  What they leave at the part's ends (the row's ends: parts meet between
@@ -315,6 +327,12 @@ struct Slice {
     }
     __device__ __forceinline__ uint32_t head_end() const { return min(k0 * E - off, s1); }
     __device__ __forceinline__ uint32_t tail_start() const { return min(max(k1 * E - off, head_end()), s1); }
+
+    // which of the 16 codes is step s's: s >> code_shift()
+    __device__ __forceinline__ int code_shift() const {
+        const uint32_t steps = (k1 - k0 + kDeep * NT - 1) / (kDeep * NT);
+        return steps <= 16 ? 0 : 28 - __clz(steps - 1);
+    }
 
     // vec(w, id of its first logit) for every vector of the slice, one(id) for every
     // other logit.  The next D vectors are loaded before D are worked on; `Rolled` keeps

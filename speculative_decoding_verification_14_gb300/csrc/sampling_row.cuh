@@ -264,24 +264,6 @@ struct View : Slice<ES, kNT> {
     }
 };
 
-// The largest logit of each of a thread's steps through the slice (the first pass goes
-// kDeep vectors a step, and so do later ones), to quarters and in eight bits: later
-// passes leave out the steps that hold nothing for them.  Long slices' steps share the
-// 16 codes.
-constexpr int kDeep = 4;
-struct StepCodes {
-    uint8_t code[16];
-};
-__device__ __forceinline__ uint32_t step_code(float l) {  // grows with l; NaN: the largest
-    const float x = fmaf(l, 4.0f, 64.0f);
-    return x < 0.0f ? 0u : x < 255.0f ? (uint32_t)x : 255u;
-}
-template <class V>
-__device__ __forceinline__ int code_shift(const V& v) {
-    const uint32_t steps = (v.k1 - v.k0 + kDeep * kNT - 1) / (kDeep * kNT);
-    return steps <= 16 ? 0 : 28 - __clz(steps - 1);
-}
-
 // --------------------------------------------------------------- lists -----
 
 // The lists lie over the bins and places, which are done with when they are made.
@@ -582,7 +564,7 @@ __device__ __noinline__ void write_rows(Shared* sh, const StepCodes* codes, Keep
         return;
     }
     const uint32_t least = codes && !bad ? step_code(cut) : 0u;
-    const int shift = code_shift(v);
+    const int shift = v.code_shift();
     const auto nothing = [&](uint32_t id) {
         if (p) {
             float4* q = reinterpret_cast<float4*>(p + id);
