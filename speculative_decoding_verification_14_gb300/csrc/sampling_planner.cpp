@@ -49,8 +49,10 @@ int plan_rows(int num_sms, int max_cluster, int B, int rows_per_seq, int64_t V, 
 }  // namespace
 
 // A sampling row's work beside its passes grows with the CTAs, more for float32: 64
-// rows of 151936 bfloat16 take 40 us with eight CTAs a row and 43 with four, 150 rows
-// of 50257 float32 77 us with two and 94 with four.
+// rows of 151936 bfloat16 take 41 us with eight CTAs a row and 43 with four, 256 of
+// 128256 59 us with two and 68 with four; 150 rows of 50257 float32 69 us with two
+// and 84 with four.  A log-probability row's does less: 37 x 3 rows of 50257 float32
+// take 15 us with four and 16 with two.
 extern "C" int spec_sample_plan_for(int num_sms, int max_cluster, int B, int rows_per_seq,
                                     int64_t V, int logits_dtype, int ovr_cluster, sv_plan* out) {
     return plan_rows(num_sms, max_cluster, B, rows_per_seq, V, logits_dtype, ovr_cluster, 256, 4,
