@@ -1081,11 +1081,13 @@ __device__ __noinline__ bool settle_exactly(Shared* sh, const StepCodes* codes) 
                 return false;
         }
     }
+    the_cluster().barrier_arrive();
     // a float sum will do to tell whether an entry listed whole lies above top-p's
     // border; not where it becomes part of the answer, or entries weigh too little
     const bool fine =
         !sh->band[0].from_top || sh->args.mass ||
         (by_mass && sh->cut_at.bin < kNoPlace && place_mass<4>(sh->scale, sh->pow2, sh->cut_at.bin, 1) < sh->whole >> 15);
+    the_cluster().barrier_wait();  // every CTA has read the places around: lists may lie over them
     if (!exact_pass(sh, codes, by_mass, fine))
         return false;
     if (tid == 0) {
