@@ -211,35 +211,34 @@ __device__ __forceinline__ uint32_t any_count(Shared* sh, int D) {
 }
 
 // Adds the other CTAs' counts at this CTA's range of places to its own: nobody else
-// reads them there.  All of a thread's reads are independent of each other.
+// reads them there.  A thread takes four places at a time, of every CTA.
 __device__ __noinline__ void merge_counts(Shared* sh) {
     sh = here();
-    const int C = sh->args.C, rank = cta_rank(), tid = threadIdx.x;
-    const int first = first_chunk(C, rank) * 32, span = chunks_per(C) * 32;
-    const int places = first_chunk(C, rank + 1) * 32 - first;
-    uint32_t* last = sh->count + (kPlaces - 1 - first);  // the range's first place
-    if ((C & (C - 1)) == 0) {
-        const int lg = 31 - __clz(span);  // a power of two
-        constexpr int L = 16;
-        for (int q = tid; q < span * (C - 1); q += L * kNT) {
-            uint32_t x[L];
-#pragma unroll
-            for (int j = 0; j < L; ++j) {
-                const int i = q + j * kNT, r = (rank + 1 + (i >> lg)) & (C - 1);
-                x[j] = i < span * (C - 1) ? *(peer(last, r) - (i & (span - 1))) : 0;
-            }
-#pragma unroll
-            for (int j = 0; j < L; ++j)
-                if (x[j])
-                    atomicAdd(last - ((q + j * kNT) & (span - 1)), x[j]);
-        }
-    } else {
+    const int C = sh->args.C, rank = cta_rank(), first = first_chunk(C, rank) * 32;
+    const int n = first_chunk(C, rank + 1) * 8 - first / 4, per = (n + kNT - 1) / kNT;
+    uint4* own = reinterpret_cast<uint4*>(sh->count + kPlaces - first) - n;
+    int i = 0, g = 0, r = rank;
 #pragma unroll 1
-        for (int r = 0; r < C; ++r)
-            for (int i = tid; i < places; i += kNT) {
-                const uint32_t x = r == rank ? 0 : *(peer(last, r) - i);
-                if (x)
-                    atomicAdd(last - i, x);
+    for (int t = 0; t < per * (C - 1); t += 4) {
+        uint4 x[4];
+        int at[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (i == 0) {
+                g = threadIdx.x;
+                r = r + 1 < C ? r + 1 : 0;
+            }
+            i = i + 1 < per ? i + 1 : 0;
+            at[j] = t + j < per * (C - 1) && g < n ? g : -1;
+            if (at[j] >= 0)
+                x[j] = *peer(own + g, r);
+            g += kNT;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (at[j] >= 0) {
+                const uint4 s = own[at[j]];
+                own[at[j]] = make_uint4(s.x + x[j].x, s.y + x[j].y, s.z + x[j].z, s.w + x[j].w);
             }
     }
     __syncthreads();
