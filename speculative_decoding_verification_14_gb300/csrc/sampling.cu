@@ -1137,12 +1137,20 @@ __device__ __noinline__ void general_row(Shared* sh, int code) {
     g.run(code);
 }
 
+__device__ __forceinline__ void prefetch(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // What the row's parts need to know: where it lies, and its settings; what only the
 // later parts need, by a thread that nothing waits for before the counts are taken.
 template <int ES>
 __device__ __forceinline__ void set_up(Shared* sh, const Args& a) {
     const int tid = threadIdx.x;
     const uint32_t row = blockIdx.x / a.C;
+    {
+        // the part's first 32 KB are on their way while the counts are zeroed
+        const int64_t first = cta_rank() * a.slice, n = min(a.V - first, a.slice) * ES;
+        if (tid * 128 < n)
+            prefetch(static_cast<const unsigned char*>(a.logits) + ((int64_t)row * a.stride + first) * ES + tid * 128);
+    }
     if (tid == 0) {
         const Slice<ES, kNT> v(static_cast<const unsigned char*>(a.logits) + (int64_t)row * a.stride * ES, a.V, a.slice,
                               cta_rank());
