@@ -101,11 +101,11 @@ __global__ void __launch_bounds__(kNT, 4) sv_logprobs_kernel(const __grid_consta
             }
         }
     };
+    const int32_t x = a.tokens[row];  // both loads at once
     if (a.accept_len && row - seq * a.rows_per_seq >= a.accept_len[seq]) {
         leave(SV_OK);
         return;
     }
-    const int32_t x = a.tokens[row];
     if (x < 0 || x >= a.V) {
         leave(SV_ERR_TOKEN_RANGE);
         return;

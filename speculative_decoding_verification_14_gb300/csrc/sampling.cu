@@ -529,7 +529,7 @@ __device__ __noinline__ void pull_list(Shared* sh, int which) {
     unsigned long long* to = list_at(sh, which);
     const int C = sh->args.C;
     uint32_t n = 0;
-#pragma unroll 1
+#pragma unroll 4
     for (int r = 0; r < C; ++r)
         n += sh->part_list[which][r];
     for (uint32_t i = sh->part_list[which][0] + threadIdx.x; i < n && i < (uint32_t)kList; i += kNT) {
@@ -765,29 +765,31 @@ __device__ __noinline__ void settle(Shared* sh, bool by_mass, bool summed, bool 
     sh = here();
     const int tid = threadIdx.x, C = sh->args.C;
     const bool draw = sh->args.u != nullptr;
-    if (tid < 3) {
-        unsigned long long x = 0;
-#pragma unroll 1
-        for (int r = 0; r < C; ++r)
-            x += sh->sums[tid][r];
-        sh->sums[tid][0] = x;
+    if (summed) {
+        if (tid < 3) {
+            unsigned long long x = 0;
+#pragma unroll 4
+            for (int r = 0; r < C; ++r)
+                x += sh->sums[tid][r];
+            sh->sums[tid][0] = x;
+        }
+        __syncthreads();
     }
-    __syncthreads();
+    if (sh->band[0].on && tid == kNT - 1) {  // a thread that has nothing to pull, mostly
+        if (!summed)
+            sh->sums[0][0] = by_mass ? __float2ull_rn(sh->fast_sum * (float)(1ull << sh->scale.fix)) : 0;
+        const unsigned long long whole = sh->sums[0][0];
+        sh->want = {sh->k, sh->want_limit, sh->band[0].above_count, logit_key(sh->band[0].lo),
+                    by_mass ? ceil_scaled(sh->top_p, whole) : 0, sh->sums[1][0],
+                    summed ? 0 : whole >> fast_bits(sh)};
+    }
     if (first && sh->band[0].on)
         pull_list(sh, 0);
     if (first && sh->band[1].on)
         pull_list(sh, 1);
+    __syncthreads();
     int ok = 3;  // 3: the draw is not in this list
     if (sh->band[0].on) {
-        if (tid == 0) {
-            if (!summed)
-                sh->sums[0][0] = by_mass ? __float2ull_rn(sh->fast_sum * (float)(1ull << sh->scale.fix)) : 0;
-            const unsigned long long whole = sh->sums[0][0];
-            sh->want = {sh->k, sh->want_limit, sh->band[0].above_count, logit_key(sh->band[0].lo),
-                        by_mass ? ceil_scaled(sh->top_p, whole) : 0, sh->sums[1][0],
-                        summed ? 0 : whole >> fast_bits(sh)};
-        }
-        __syncthreads();
         if (sh->want_limit > logit_key(sh->band[0].hi)) {
             ok = 0;
         } else if (sh->list_n[0] <= (uint32_t)kFew) {

@@ -431,7 +431,7 @@ __device__ __noinline__ int resolve_few(Shared* sh, int which, bool cut, bool dr
     unsigned long long larger = 0, before = 0;
     uint32_t count = 0;
     if (at < n) {
-#pragma unroll 2
+#pragma unroll 4
         for (int j = tid & ((1 << lg) - 1); j < n; j += 1 << lg) {
             const unsigned long long o = list[j], x = sh->few[j];
             if (o > mine)
@@ -473,20 +473,18 @@ __device__ __noinline__ int resolve_few(Shared* sh, int which, bool cut, bool dr
             sh->warp_cnt[warp] = number;
         }
         const bool any_near = __syncthreads_or(near);
-        if (tid == 0) {
-            uint32_t x = 0xffffffffu, sum = 0;
-            unsigned long long all = 0, mass = 0;
-#pragma unroll 1
-            for (int i = 0; i < kNW; ++i) {
-                x = min(x, sh->warp_max[i]);
-                all += sh->warp_mass[0][i];
-                mass += sh->warp_mass[1][i];
-                sum += sh->warp_cnt[i];
+        if (warp == 0) {
+            const bool in = tid < kNW;
+            const uint32_t x = __reduce_min_sync(kAllLanes, in ? sh->warp_max[tid] : 0xffffffffu);
+            const uint32_t sum = __reduce_add_sync(kAllLanes, in ? sh->warp_cnt[tid] : 0u);
+            const unsigned long long all = warp_sum(in ? sh->warp_mass[0][tid] : 0ull);
+            const unsigned long long mass = warp_sum(in ? sh->warp_mass[1][tid] : 0ull);
+            if (tid == 0) {
+                sh->cut_key = sum ? x : c.limit_key;
+                sh->kept = c.above_count + sum;
+                sh->kept_mass = c.above_mass + mass;
+                sh->list_mass = all;
             }
-            sh->cut_key = sum ? x : c.limit_key;
-            sh->kept = c.above_count + sum;
-            sh->kept_mass = c.above_mass + mass;
-            sh->list_mass = all;
         }
         __syncthreads();
         ok = any_near ? 2 : cut_inside(c, n, sh->list_mass);
