@@ -174,11 +174,7 @@ __device__ __noinline__ uint32_t count_pass(Shared* sh, StepCodes* codes) {
                 join_sums(m, t, l, 1.0f, ch);
         });
     if (sum) {
-#pragma unroll
-        for (int o = 16; o; o >>= 1) {
-            const float m1 = __shfl_xor_sync(kAllLanes, m, o), t1 = __shfl_xor_sync(kAllLanes, t, o);
-            join_sums(m, t, m1, t1, ch);
-        }
+        join_lanes<32>(m, t, ch);
         if ((threadIdx.x & 31) == 0) {
             sh->warp_top[threadIdx.x >> 5] = m;
             sh->warp_noise[threadIdx.x >> 5] = t;
@@ -189,10 +185,7 @@ __device__ __noinline__ uint32_t count_pass(Shared* sh, StepCodes* codes) {
     if ((threadIdx.x & 31) == 0)
         sh->warp_max[threadIdx.x >> 5] = key;
     __syncthreads();
-#pragma unroll 1
-    for (int w = 0; w < kNW; ++w)
-        key = max(key, sh->warp_max[w]);
-    return key;
+    return __reduce_max_sync(kAllLanes, sh->warp_max[threadIdx.x & (kNW - 1)]);
 }
 
 // Chunks of places per CTA, and this CTA's first and last.
@@ -309,13 +302,14 @@ __device__ __noinline__ void weigh_places(Shared* sh) {
         if (lane < C) {
             *peer(&sh->part_mass[rank], lane) = m;
             *peer(&sh->part_cnt[rank], lane) = n;
-            if constexpr (ES == 4) {
-                noise = 0.0f;
-#pragma unroll 1
-                for (int w = 0; w < kNW; ++w)
-                    noise += sh->warp_noise[w];
+        }
+        if constexpr (ES == 4) {
+            noise = sh->warp_noise[lane & (kNW - 1)];
+#pragma unroll
+            for (int o = kNW / 2; o; o >>= 1)
+                noise += __shfl_xor_sync(kAllLanes, noise, o);
+            if (lane < C)
                 *peer(&sh->part_noise[rank], lane) = noise;
-            }
         }
     }
     the_cluster().sync();
@@ -337,14 +331,11 @@ __device__ __noinline__ Found search_places(Shared* sh, int set, const Wanted s)
     const int C = sh->args.C, rank = cta_rank(), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int c0 = first_chunk(C, rank), c1 = first_chunk(C, rank + 1);
     static_assert(kChunks <= kNT, "a thread per chunk");
+    const unsigned long long above_m = warp_sum(lane < rank ? sh->part_mass[lane] : 0ull);
+    const uint32_t above_n = __reduce_add_sync(kAllLanes, lane < rank ? sh->part_cnt[lane] : 0u);
     if (tid < c1 - c0) {
-        unsigned long long before_m = chunks(sh)[tid].above_mass;
-        uint32_t before_n = chunks(sh)[tid].above_cnt;
-#pragma unroll 1
-        for (int r = 0; r < rank; ++r) {
-            before_m += sh->part_mass[r];
-            before_n += sh->part_cnt[r];
-        }
+        const unsigned long long before_m = above_m + chunks(sh)[tid].above_mass;
+        const uint32_t before_n = above_n + chunks(sh)[tid].above_cnt;
         const unsigned long long after_m = before_m + chunks(sh)[tid].mass;
         const uint32_t after_n = before_n + chunks(sh)[tid].cnt;
         const Hit h = {c0 + tid, before_n, before_m};
@@ -528,10 +519,8 @@ __device__ __noinline__ void pull_list(Shared* sh, int which) {
     sh = here();
     unsigned long long* to = list_at(sh, which);
     const int C = sh->args.C;
-    uint32_t n = 0;
-#pragma unroll 4
-    for (int r = 0; r < C; ++r)
-        n += sh->part_list[which][r];
+    const int lane = threadIdx.x & 31;
+    const uint32_t n = __reduce_add_sync(kAllLanes, lane < C ? sh->part_list[which][lane] : 0u);
     for (uint32_t i = sh->part_list[which][0] + threadIdx.x; i < n && i < (uint32_t)kList; i += kNT) {
         int r = 0;
         uint32_t j = i;
@@ -766,12 +755,11 @@ __device__ __noinline__ void settle(Shared* sh, bool by_mass, bool summed, bool 
     const int tid = threadIdx.x, C = sh->args.C;
     const bool draw = sh->args.u != nullptr;
     if (summed) {
-        if (tid < 3) {
-            unsigned long long x = 0;
-#pragma unroll 4
-            for (int r = 0; r < C; ++r)
-                x += sh->sums[tid][r];
-            sh->sums[tid][0] = x;
+        const int warp = tid >> 5, lane = tid & 31;
+        if (warp < 3) {
+            const unsigned long long x = warp_sum(lane < C ? sh->sums[warp][lane] : 0ull);
+            if (lane == 0)
+                sh->sums[warp][0] = x;
         }
         __syncthreads();
     }
@@ -845,14 +833,13 @@ __device__ __noinline__ bool exact_pass(Shared* sh, const StepCodes* codes, bool
                 sh->warp_mass[j][tid >> 5] = x;
         }
         __syncthreads();
-        if (tid < 3) {
-            unsigned long long x = 0;
-#pragma unroll 1
-            for (int w = 0; w < kNW; ++w)
-                x += sh->warp_mass[tid][w];
-            *peer(&sh->sums[tid][rank], 0) = x;
-        } else if (tid < 5) {
-            *peer(&sh->part_list[tid - 3][rank], 0) = sh->list_n[tid - 3];
+        const int warp = tid >> 5, lane = tid & 31;
+        if (warp < 3) {
+            const unsigned long long x = warp_sum(lane < kNW ? sh->warp_mass[warp][lane] : 0ull);
+            if (lane == 0)
+                *peer(&sh->sums[warp][rank], 0) = x;
+        } else if (warp < 5 && lane == 0) {
+            *peer(&sh->part_list[warp - 3][rank], 0) = sh->list_n[warp - 3];
         }
         the_cluster().sync();
         if (rank == 0)
@@ -920,37 +907,32 @@ __device__ __noinline__ bool count_places(Shared* sh, StepCodes* codes) {
     if (tid < C) {
         *peer(&sh->part_max[rank], tid) = key;
         *peer(&sh->part_tiny[rank], tid) = sh->count[kMags + 1] + sh->count[kMags + 2];
-        if (ES == 4 && sh->top_p < 1.0) {
-            float m = sh->warp_top[0], t = sh->warp_noise[0];
-            const float ch = __fdiv_rn(1.44269502162933349609375f, sh->T);
-#pragma unroll 1
-            for (int w = 1; w < kNW; ++w)
-                join_sums(m, t, sh->warp_top[w], sh->warp_noise[w], ch);
+    }
+    if (ES == 4 && tid < 32 && sh->top_p < 1.0) {
+        float m = sh->warp_top[tid & (kNW - 1)], t = sh->warp_noise[tid & (kNW - 1)];
+        join_lanes<kNW>(m, t, __fdiv_rn(1.44269502162933349609375f, sh->T));
+        if (tid < C) {
             *peer(&sh->part_top[rank], tid) = m;
             *peer(&sh->part_sum[rank], tid) = t;
         }
     }
     the_cluster().sync();
-    uint32_t tiny = 0;  // entries below the window
-#pragma unroll 1
-    for (int r = 0; r < C; ++r) {
-        key = max(key, sh->part_max[r]);
-        tiny += sh->part_tiny[r];
-    }
+    const int lane = tid & 31;
+    key = __reduce_max_sync(kAllLanes, lane < C ? sh->part_max[lane] : 0u);
+    const uint32_t tiny = __reduce_add_sync(kAllLanes, lane < C ? sh->part_tiny[lane] : 0u);  // below the window
     RowScale scale;
     scale.fix = sh->args.fix;
     scale.lmax = key_logit(key);
     const float T = sh->T;
     split_scale(T > 0.0f ? T : 1.0f, scale.ch, scale.cl);
-    if (tid == 0) {
+    if (tid == 0)
         sh->scale = scale;
-        if (ES == 4 && sh->top_p < 1.0) {
-            float m = sh->part_top[0], t = sh->part_sum[0];
-#pragma unroll 1
-            for (int r = 1; r < C; ++r)
-                join_sums(m, t, sh->part_top[r], sh->part_sum[r], scale.ch);
+    if (ES == 4 && tid < 32 && sh->top_p < 1.0) {
+        const bool in = lane < C;
+        float m = in ? sh->part_top[lane] : __int_as_float(0xff800000), t = in ? sh->part_sum[lane] : 0.0f;
+        join_lanes<kMaxC>(m, t, scale.ch);
+        if (tid == 0)
             sh->fast_sum = t;
-        }
     }
     __syncthreads();
     if (sh->code || key == 0xffffffffu || !inside(place_of(scale.lmax)))
@@ -991,13 +973,9 @@ __device__ __noinline__ bool find_cut(Shared* sh) {
     if (C > 1)
         merge_counts(sh);
     weigh_places<ES>(sh);
-    unsigned long long whole = 0;
-    uint32_t near = 0;
-#pragma unroll 1
-    for (int r = 0; r < C; ++r) {
-        whole += sh->part_mass[r];
-        near += sh->part_cnt[r];
-    }
+    const int lane = tid & 31;
+    const unsigned long long whole = warp_sum(lane < C ? sh->part_mass[lane] : 0ull);
+    const uint32_t near = __reduce_add_sync(kAllLanes, lane < C ? sh->part_cnt[lane] : 0u);
     Wanted s = {sh->k, sh->top_p < 1.0 ? ceil_scaled(sh->top_p, whole) : 0, kNoPlace, false};
     if (sh->has_min) {
         // the smallest float l with l - l_max >= T ln(min_p); bfloat16: the smallest of those
@@ -1063,10 +1041,10 @@ __device__ __noinline__ bool settle_exactly(Shared* sh, const StepCodes* codes) 
     const int tid = threadIdx.x;
     const bool by_mass = sh->top_p < 1.0, draw = sh->args.u != nullptr;
     // four standard deviations of the places' sum, and what their middles miss
-    float noise = 0.0f;
-#pragma unroll 1
-    for (int r = 0; r < sh->args.C; ++r)
-        noise += sh->part_noise[r];
+    float noise = (tid & 15) < sh->args.C ? sh->part_noise[tid & 15] : 0.0f;
+#pragma unroll
+    for (int o = kMaxC / 2; o; o >>= 1)
+        noise += __shfl_xor_sync(kAllLanes, noise, o);
     const unsigned long long margin = __float2ull_rn(4.0f * sqrtf(noise) * (float)(1ull << sh->scale.fix)) + (sh->whole >> 12);
     if (sh->cut_at.bin < kNoPlace) {
         band_around(sh, 0, sh->cut_at, margin);

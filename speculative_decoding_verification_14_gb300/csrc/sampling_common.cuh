@@ -254,6 +254,16 @@ __device__ __forceinline__ void join_sums(float& m, float& s, float m1, float s1
     m = grown;
 }
 
+// the same over groups of N lanes
+template <int N>
+__device__ __forceinline__ void join_lanes(float& m, float& s, float c) {
+#pragma unroll
+    for (int o = N / 2; o; o >>= 1) {
+        const float m1 = __shfl_xor_sync(kAllLanes, m, o), s1 = __shfl_xor_sync(kAllLanes, s, o);
+        join_sums(m, s, m1, s1, c);
+    }
+}
+
 // sum of 2^((l - m) c) over a vector's logits: differences (a bfloat16 operand is
 // widened inside the subtraction), products and sums two at a time
 template <int ES>
