@@ -208,9 +208,8 @@ __global__ void __launch_bounds__(kNT, 4) sv_logprobs_kernel(const __grid_consta
                 }
             };
             const float least = key_logit(bound);
-            const uint32_t code = step_code(least);
-            v.template walk_steps<kDeep, true>(
-                [&](uint32_t i) { return codes.code[i >> shift] >= code; },
+            v.template walk_marked<kDeep>(
+                &codes, step_code(least),
                 [&](const uint4& w, uint32_t id) {
                     if (vector_max<ES>(w) >= least) {
 #pragma unroll
@@ -218,7 +217,6 @@ __global__ void __launch_bounds__(kNT, 4) sv_logprobs_kernel(const __grid_consta
                             offer(vector_entry<ES>(w, e), id + e);
                     }
                 },
-                [](uint32_t) {}, [](uint32_t) {},
                 [&](uint32_t id) { offer(scalar_entry<ES>(base, id), id); });
         }
         __syncthreads();

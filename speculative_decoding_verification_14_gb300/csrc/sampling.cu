@@ -395,7 +395,6 @@ __device__ __noinline__ int64_t find_entry(Shared* sh, const StepCodes* codes, i
     const uint32_t bits = __float_as_uint(l) >> 16, two = bits * 0x10001u;
     const unsigned short* q = reinterpret_cast<const unsigned short*>(v.base);
     const uint32_t least = step_code(l);
-    const int shift = v.code_shift();
     constexpr uint32_t kIds = kPlaces;
     uint32_t* ids = sh->count;  // the counts are done with
     const auto found = [&](uint32_t id) {
@@ -403,8 +402,8 @@ __device__ __noinline__ int64_t find_entry(Shared* sh, const StepCodes* codes, i
         if (at < kIds)
             ids[at] = id;
     };
-    v.walk_steps<kDeep, true>(
-        [&](uint32_t s) { return codes->code[s >> shift] >= least; },
+    v.walk_marked<kDeep>(
+        codes, least,
         [&](const uint4& w, uint32_t id) {
             uint32_t m;
             const uint32_t x[4] = {w.x ^ two, w.y ^ two, w.z ^ two, w.w ^ two};
@@ -421,7 +420,6 @@ __device__ __noinline__ int64_t find_entry(Shared* sh, const StepCodes* codes, i
                 }
             }
         },
-        [](uint32_t) {}, [](uint32_t) {},
         [&](uint32_t id) {
             if (q[id] == bits)
                 found(id);
@@ -719,13 +717,12 @@ __device__ __noinline__ void list_entries(Shared* sh, const StepCodes* codes) {
     const View<4> v(sh);
     const float low = sh->band[0].lo;
     const uint32_t least = step_code(low);
-    const int shift = v.code_shift();
     const auto take = [&](float l, uint32_t id) {
         if (l >= low)
             offer(&sh->list_n[0], list_at(sh, 0), l, id);
     };
-    v.walk_steps<kDeep, true>(
-        [&](uint32_t s) { return codes->code[s >> shift] >= least; },
+    v.walk_marked<kDeep>(
+        codes, least,
         [&](const uint4& w, uint32_t id) {
             if (vector_max<4>(w) >= low) {
                 take(__uint_as_float(w.x), id);
@@ -734,7 +731,7 @@ __device__ __noinline__ void list_entries(Shared* sh, const StepCodes* codes) {
                 take(__uint_as_float(w.w), id + 3);
             }
         },
-        [](uint32_t) {}, [](uint32_t) {}, [&](uint32_t id) { take(scalar_entry<4>(v.base, id), id); });
+        [&](uint32_t id) { take(scalar_entry<4>(v.base, id), id); });
 }
 
 // How far the first pass's float sum may be off, as a share of itself: 2^-n.  A weight

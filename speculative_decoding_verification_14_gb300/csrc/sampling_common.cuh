@@ -399,10 +399,61 @@ struct Slice {
             }
             done(s);
         }
+        edges(one);
+    }
+
+    // one(id) for the entries beside the vectors
+    template <class One>
+    __device__ __forceinline__ void edges(One&& one) const {
         const uint32_t head = head_end() - s0, edge = head + (s1 - tail_start());
 #pragma unroll 1
-        for (uint32_t j = tid; j < edge; j += NT)
+        for (uint32_t j = threadIdx.x; j < edge; j += NT)
             one(j < head ? s0 + j : tail_start() + (j - head));
+    }
+
+    // walk(), but of the steps whose code is at least `least` alone.  Each thread goes from one
+    // such step to its next: a warp waits for as many loads as its busiest lane has.
+    template <int D, class Vec, class One>
+    __device__ __forceinline__ void walk_marked(const StepCodes* codes, uint32_t least, Vec&& vec, One&& one) const {
+        const int tid = threadIdx.x, shift = code_shift();
+        uint32_t marks = 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            marks |= (uint32_t)(codes->code[i] >= least) << i;
+        const uint32_t mine = k1 - k0 > tid ? k1 - k0 - tid : 0, steps = (mine + D * NT - 1) / (D * NT);
+        const uint4* p = vectors() + k0 + tid;
+        const auto following = [&](uint32_t s) {
+            while (s < steps && !((marks >> (s >> shift)) & 1))
+                ++s;
+            return s;
+        };
+        uint4 next[D];
+        const auto load = [&](uint32_t s) {
+#pragma unroll
+            for (int j = 0; j < D; ++j)
+                if ((s * D + j) * NT < mine)
+                    next[j] = load_stream(p + (s * D + j) * NT);
+        };
+        uint32_t s = following(0);
+        load(s);
+#pragma unroll 1
+        while (s < steps) {
+            uint4 w[D];
+#pragma unroll
+            for (int j = 0; j < D; ++j)
+                w[j] = next[j];
+            const uint32_t at = s;
+            s = following(s + 1);
+            load(s);
+#pragma unroll 1
+            for (int j = 0; j < D && (at * D + j) * NT < mine; ++j) {
+                vec(w[0], (k0 + tid + (at * D + j) * NT) * E - off);
+#pragma unroll
+                for (int i = 0; i + 1 < D; ++i)
+                    w[i] = w[i + 1];
+            }
+        }
+        edges(one);
     }
 
     // fn(l, id) for every entry of the slice
