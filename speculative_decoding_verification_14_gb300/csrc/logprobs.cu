@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kNT, 4) sv_logprobs_kernel(const __grid_consta
             };
             const float least = key_logit(bound);
             v.template walk_marked<kDeep>(
-                &codes, step_code(least),
+                v.marks(&codes, step_code(least)),
                 [&](const uint4& w, uint32_t id) {
                     if (vector_max<ES>(w) >= least) {
 #pragma unroll

@@ -403,7 +403,7 @@ __device__ __noinline__ int64_t find_entry(Shared* sh, const StepCodes* codes, i
             ids[at] = id;
     };
     v.walk_marked<kDeep>(
-        codes, least,
+        v.marks(codes, least),
         [&](const uint4& w, uint32_t id) {
             uint32_t m;
             const uint32_t x[4] = {w.x ^ two, w.y ^ two, w.z ^ two, w.w ^ two};
@@ -722,7 +722,7 @@ __device__ __noinline__ void list_entries(Shared* sh, const StepCodes* codes) {
             offer(&sh->list_n[0], list_at(sh, 0), l, id);
     };
     v.walk_marked<kDeep>(
-        codes, least,
+        v.marks(codes, least),
         [&](const uint4& w, uint32_t id) {
             if (vector_max<4>(w) >= low) {
                 take(__uint_as_float(w.x), id);

@@ -411,15 +411,19 @@ struct Slice {
             one(j < head ? s0 + j : tail_start() + (j - head));
     }
 
-    // walk(), but of the steps whose code is at least `least` alone.  Each thread goes from one
-    // such step to its next: a warp waits for as many loads as its busiest lane has.
-    template <int D, class Vec, class One>
-    __device__ __forceinline__ void walk_marked(const StepCodes* codes, uint32_t least, Vec&& vec, One&& one) const {
-        const int tid = threadIdx.x, shift = code_shift();
-        uint32_t marks = 0;
+    // the codes that are at least `least`: a bit each
+    __device__ __forceinline__ static uint32_t marks(const StepCodes* codes, uint32_t least) {
+        uint32_t m = 0;
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-            marks |= (uint32_t)(codes->code[i] >= least) << i;
+            m |= (uint32_t)(codes->code[i] >= least) << i;
+        return m;
+    }
+    // walk(), but of the marked steps alone.  Each thread goes from one such step to its
+    // next: a warp waits for as many loads as its busiest lane has.
+    template <int D, class Vec, class One>
+    __device__ __forceinline__ void walk_marked(uint32_t marks, Vec&& vec, One&& one) const {
+        const int tid = threadIdx.x, shift = code_shift();
         const uint32_t mine = k1 - k0 > tid ? k1 - k0 - tid : 0, steps = (mine + D * NT - 1) / (D * NT);
         const uint4* p = vectors() + k0 + tid;
         const auto following = [&](uint32_t s) {
@@ -454,6 +458,21 @@ struct Slice {
             }
         }
         edges(one);
+    }
+
+    // skip(id of its first logit) for the vectors of the other steps
+    template <int D, class Skip>
+    __device__ __forceinline__ void pass_unmarked(uint32_t marks, Skip&& skip) const {
+        const int shift = code_shift();
+        uint32_t s = 0;
+#pragma unroll 1
+        for (uint32_t k = k0 + threadIdx.x; k < k1; k += D * NT, ++s)
+            if (!((marks >> (s >> shift)) & 1)) {
+#pragma unroll
+                for (int j = 0; j < D; ++j)
+                    if (k + j * NT < k1)
+                        skip((k + j * NT) * E - off);
+            }
     }
 
     // fn(l, id) for every entry of the slice

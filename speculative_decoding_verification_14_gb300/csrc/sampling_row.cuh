@@ -561,8 +561,7 @@ __device__ __noinline__ void write_rows(Shared* sh, const StepCodes* codes, Keep
             one(i);
         return;
     }
-    const uint32_t least = codes && !bad ? step_code(cut) : 0u;
-    const int shift = v.code_shift();
+    const uint32_t marks = codes && !bad ? v.marks(codes, step_code(cut)) : 0xffffu;
     const auto nothing = [&](uint32_t id) {
         if (p) {
             float4* q = reinterpret_cast<float4*>(p + id);
@@ -575,8 +574,9 @@ __device__ __noinline__ void write_rows(Shared* sh, const StepCodes* codes, Keep
             *reinterpret_cast<uint4*>(o + (size_t)id * ES) = make_uint4(x, x, x, x);
         }
     };
-    v.template walk_steps<kDeep, true>(
-        [&](uint32_t s) { return least == 0 || codes->code[s >> shift] >= least; },
+    v.template pass_unmarked<kDeep>(marks, nothing);
+    v.template walk_marked<kDeep>(
+        marks,
         [&](const uint4& w, uint32_t id) {
             if (!bad && !(vector_max<ES>(w) >= cut)) {
                 nothing(id);
@@ -604,7 +604,7 @@ __device__ __noinline__ void write_rows(Shared* sh, const StepCodes* codes, Keep
                 *reinterpret_cast<uint4*>(o + (size_t)id * ES) = make_uint4(h[0], h[1], h[2], h[3]);
             }
         },
-        nothing, [](uint32_t) {}, one);
+        one);
 }
 
 __device__ __forceinline__ bool writes_rows(const Shared* sh) { return sh->args.probs || sh->args.out; }
