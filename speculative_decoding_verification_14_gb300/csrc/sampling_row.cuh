@@ -574,7 +574,6 @@ __device__ __noinline__ void write_rows(Shared* sh, const StepCodes* codes, Keep
             *reinterpret_cast<uint4*>(o + (size_t)id * ES) = make_uint4(x, x, x, x);
         }
     };
-    v.template pass_unmarked<kDeep>(marks, nothing);
     v.template walk_marked<kDeep>(
         marks,
         [&](const uint4& w, uint32_t id) {
@@ -605,6 +604,7 @@ __device__ __noinline__ void write_rows(Shared* sh, const StepCodes* codes, Keep
             }
         },
         one);
+    v.template pass_unmarked<kDeep>(marks, nothing);
 }
 
 __device__ __forceinline__ bool writes_rows(const Shared* sh) { return sh->args.probs || sh->args.out; }
