@@ -48,20 +48,21 @@ int plan_rows(int num_sms, int max_cluster, int B, int rows_per_seq, int64_t V, 
 
 }  // namespace
 
-// A sampling row's work beside its passes grows with the CTAs, more for float32: 64
-// rows of 151936 bfloat16 take 41 us with eight CTAs a row and 43 with four, 256 of
-// 128256 59 us with two and 68 with four; 150 rows of 50257 float32 69 us with two
-// and 84 with four.  A log-probability row's does less: 37 x 3 rows of 50257 float32
-// take 15 us with four and 16 with two.
+// A sampling row's work beside its passes grows with the CTAs: 64 rows of 151936
+// bfloat16 take 38.9 us with eight CTAs a row and 38.3 with four, 256 of 128256 64 us
+// with four and 56 with two; 150 rows of 50257 float32 82 us with four and 68 with two.
 extern "C" int spec_sample_plan_for(int num_sms, int max_cluster, int B, int rows_per_seq,
                                     int64_t V, int logits_dtype, int ovr_cluster, sv_plan* out) {
     return plan_rows(num_sms, max_cluster, B, rows_per_seq, V, logits_dtype, ovr_cluster, 256, 4,
-                     2048, logits_dtype == SV_BF16 ? 16384 : 24576, out);
+                     2048, 24576, out);
 }
 
+// A log-probability row's does less: 37 x 3 rows of 50257 float32 take 14.2 us with
+// four CTAs a row and 16.7 with one; 8 x 5 of 32000 bfloat16 10.7 us with eight and 9.3
+// with four.
 extern "C" int spec_logprobs_plan_for(int num_sms, int max_cluster, int B, int rows_per_seq,
                                       int64_t V, int logits_dtype, int ovr_cluster,
                                       sv_plan* out) {
     return plan_rows(num_sms, max_cluster, B, rows_per_seq, V, logits_dtype, ovr_cluster, 256, 4,
-                     2048, 2048, out);
+                     2048, 4096, out);
 }
