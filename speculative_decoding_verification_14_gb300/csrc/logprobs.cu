@@ -129,7 +129,6 @@ __global__ void __launch_bounds__(kNT, 4) sv_logprobs_kernel(const __grid_consta
     }
     float step = -inf;  // the step's largest
     v.template walk_steps<kDeep, false>(
-        [](uint32_t) { return true; },
         [&](const uint4& w, uint32_t) {
             const float top = vector_max_nan<ES>(w);
             step = max_nan(step, top);
@@ -143,7 +142,6 @@ __global__ void __launch_bounds__(kNT, 4) sv_logprobs_kernel(const __grid_consta
             if (top > -inf)  // else m may be -inf too
                 s += exp_sum<ES>(w, m, a.ch);
         },
-        [](uint32_t) {},
         [&](uint32_t i) {
             const uint8_t x = (uint8_t)step_code(step);
             if (shift == 0 || x > codes.code[i >> shift])

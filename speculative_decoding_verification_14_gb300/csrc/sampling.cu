@@ -129,7 +129,6 @@ __device__ __noinline__ uint32_t count_pass(Shared* sh, StepCodes* codes) {
     for (int i = 0; i < 16; ++i)
         codes->code[i] = 0;
     v.template walk_steps<kDeep, false>(
-        [](uint32_t) { return true; },
         [&](const uint4& w, uint32_t) {
             if constexpr (ES == 2) {
                 count_pair(sh, w.x);
@@ -154,7 +153,6 @@ __device__ __noinline__ uint32_t count_pass(Shared* sh, StepCodes* codes) {
                 }
             }
         },
-        [](uint32_t) {},
         [&](uint32_t s) {
             if constexpr (ES == 2) {
                 step = max_nan(__uint_as_float(two << 16), __uint_as_float(two & 0xffff0000u));
@@ -955,9 +953,9 @@ __device__ __noinline__ void take_largest(Shared* sh, const StepCodes* codes) {
         for (int r = 0; r < sh->args.C; ++r)
             *peer(&sh->token, r) = (uint32_t)id;
     }
-    if (writes_rows(sh)) {
+    if (sh->args.probs || sh->args.out) {
         the_cluster().sync();
-        write_rows<2>(sh, codes, kKeepToken, sh->scale.lmax, 0.0f, sh->token);
+        write_out<2>(sh, codes, kKeepToken, sh->scale.lmax, 0.0f, sh->token);
     }
     put_rest(sh, SV_OK, 1, 1, 1);
 }
@@ -1101,8 +1099,7 @@ __device__ __forceinline__ bool by_place(Shared* sh) {
         if (!settle_exactly(sh, &codes))
             return false;
     }
-    if (writes_rows(sh))
-        write_rows<ES>(sh, &codes, kKeepFrom, sh->cut, inverse_mass(sh->scale, sh->mass), 0);
+    write_out<ES>(sh, &codes, kKeepFrom, sh->cut, inverse_mass(sh->scale, sh->mass), 0);
     put_rest(sh, SV_OK, sh->kept_n, sh->mass, sh->whole);
     return true;
 }

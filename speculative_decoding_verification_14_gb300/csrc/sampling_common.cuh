@@ -349,26 +349,22 @@ struct Slice {
     // one copy of vec's code.
     template <int D, bool Rolled, class Vec, class One>
     __device__ __forceinline__ void walk(Vec&& vec, One&& one) const {
-        walk_steps<D, Rolled>([](uint32_t) { return true; }, vec, [](uint32_t) {}, [](uint32_t) {}, one);
+        walk_steps<D, Rolled>(vec, [](uint32_t) {}, one);
     }
-    // The same step by step: a thread's step s is D of its vectors.  Steps for which want(s)
-    // is false are not loaded; their vectors' first ids go to skip(id).  done(s) follows
-    // each step that was.
-    template <int D, bool Rolled, class Want, class Vec, class Skip, class Done, class One>
-    __device__ __forceinline__ void walk_steps(Want&& want, Vec&& vec, Skip&& skip, Done&& done, One&& one) const {
+    // The same step by step: a thread's step s is D of its vectors, and done(s) follows it.
+    template <int D, bool Rolled, class Vec, class Done, class One>
+    __device__ __forceinline__ void walk_steps(Vec&& vec, Done&& done, One&& one) const {
         const int tid = threadIdx.x;
         const uint4* p = vectors() + k0 + tid;
         uint4 next[D];
-        const auto load = [&](uint32_t k, uint32_t s) {
-            if (k < k1 && want(s)) {
+        const auto load = [&](uint32_t k) {
 #pragma unroll
-                for (int j = 0; j < D; ++j)
-                    if (k + j * NT < k1)
-                        next[j] = load_stream(p + j * NT);
-            }
+            for (int j = 0; j < D; ++j)
+                if (k + j * NT < k1)
+                    next[j] = load_stream(p + j * NT);
             p += D * NT;
         };
-        load(k0 + tid, 0);
+        load(k0 + tid);
         uint32_t s = 0;
 #pragma unroll 1
         for (uint32_t k = k0 + tid; k < k1; k += D * NT, ++s) {
@@ -376,13 +372,7 @@ struct Slice {
 #pragma unroll
             for (int j = 0; j < D; ++j)
                 w[j] = next[j];
-            load(k + D * NT, s + 1);
-            if (!want(s)) {
-#pragma unroll 1
-                for (int j = 0; j < D && k + j * NT < k1; ++j)
-                    skip((k + j * NT) * E - off);
-                continue;
-            }
+            load(k + D * NT);
             if constexpr (Rolled) {
 #pragma unroll 1
                 for (int j = 0; j < D && k + j * NT < k1; ++j) {

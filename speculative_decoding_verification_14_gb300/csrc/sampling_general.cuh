@@ -281,8 +281,7 @@ struct General {
             code = SV_ERR_NONFINITE;
         scale.lmax = m;
         if (code) {
-            if (writes_rows(sh))
-                write_rows<ES>(sh, nullptr, kBadRow, 0.0f, 0.0f, 0);
+            write_out<ES>(sh, nullptr, kBadRow, 0.0f, 0.0f, 0);
             if (rank == 0 && tid == 0)
                 put_token(sh, -1, __int_as_float(0x7fffffff));
             put_rest(sh, code, 0, 0, 1);
@@ -307,8 +306,7 @@ struct General {
             the_cluster().sync();
             for (int r = 0; r < C; ++r)
                 id = min(id, sh->part_cnt[r]);
-            if (writes_rows(sh))
-                write_rows<ES>(sh, nullptr, kKeepToken, m, 0.0f, id);
+            write_out<ES>(sh, nullptr, kKeepToken, m, 0.0f, id);
             if (rank == 0 && tid == 0)
                 put_token(sh, (int32_t)id, 1.0f);
             put_rest(sh, SV_OK, 1, 1, 1);
@@ -415,8 +413,7 @@ struct General {
                 put_token(sh, (int32_t)sh->token, weight_float(scale, key_logit(sh->token_key)) * inv);
         }
         // D. rows out
-        if (writes_rows(sh))
-            write_rows<ES>(sh, nullptr, kKeepFrom, key_logit(cut_key), inv, 0);
+        write_out<ES>(sh, nullptr, kKeepFrom, key_logit(cut_key), inv, 0);
         put_rest(sh, SV_OK, kept, E, whole);
         the_cluster().sync();  // no CTA leaves while another may still write into it
     }

@@ -237,18 +237,6 @@ __device__ __forceinline__ uint32_t cta_sum(Shared* sh, uint32_t x) {
         x += sh->warp_cnt[w];
     return x;
 }
-__device__ __forceinline__ unsigned long long cta_sum(Shared* sh, unsigned long long x) {
-    x = warp_sum(x);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0)
-        sh->warp_mass[0][threadIdx.x >> 5] = x;
-    __syncthreads();
-    x = 0;
-#pragma unroll 1
-    for (int w = 0; w < kNW; ++w)
-        x += sh->warp_mass[0][w];
-    return x;
-}
 
 // ------------------------------------------------------------- the slice -----
 
@@ -517,10 +505,10 @@ __device__ __forceinline__ void share_cut(Shared* sh) {
 
 enum Keep { kKeepFrom, kKeepToken, kBadRow };  // logits from `cut` on; one id; a row without an answer
 
-// Probabilities and truncated logits.  Steps (see StepCodes; NULL: all are looked at) and
+// Probabilities (`Probs`) or truncated logits.  Steps (see StepCodes; NULL: all are looked at) and
 // vectors none of whose logits reaches `cut` are written without looking further.  inv:
 // 2^F over the kept mass.
-template <int ES>
+template <int ES, bool Probs>
 __device__ __noinline__ void write_rows(Shared* sh, const StepCodes* codes, Keep how, float cut, float inv,
                                         uint32_t token) {
     sh = here();
@@ -529,8 +517,8 @@ __device__ __noinline__ void write_rows(Shared* sh, const StepCodes* codes, Keep
     const View<ES> v(sh);
     constexpr int E = View<ES>::E;
     const int64_t row = sh->row;
-    float* p = a.probs ? a.probs + row * a.probs_stride : nullptr;
-    unsigned char* o = a.out ? static_cast<unsigned char*>(a.out) + row * a.out_stride * ES : nullptr;
+    float* p = a.probs + row * a.probs_stride;
+    unsigned char* o = static_cast<unsigned char*>(a.out) + row * a.out_stride * ES;
     const bool bad = how == kBadRow;
     const auto keep = [&](float l, uint32_t id) { return how == kKeepFrom ? l >= cut : id == token; };
     const auto prob = [&](float l, uint32_t id) {
@@ -542,9 +530,9 @@ __device__ __noinline__ void write_rows(Shared* sh, const StepCodes* codes, Keep
     };
     const auto one = [&](uint32_t id) {
         const float l = scalar_entry<ES>(v.base, id);
-        if (p)
+        if constexpr (Probs) {
             p[id] = prob(l, id);
-        if (o) {
+        } else {
             const uint32_t h = logit(l, id);
             if constexpr (ES == 4)
                 reinterpret_cast<uint32_t*>(o)[id] = h;
@@ -552,10 +540,9 @@ __device__ __noinline__ void write_rows(Shared* sh, const StepCodes* codes, Keep
                 reinterpret_cast<unsigned short*>(o)[id] = (unsigned short)(h >> 16);
         }
     };
-    // vectors of logits go to 16-byte places of both outputs, or are written one by one
-    const bool even = (!p || (reinterpret_cast<uintptr_t>(p - v.off) & 15u) == 0) &&
-                      (!o || (reinterpret_cast<uintptr_t>(o - v.off * ES) & 15u) == 0);
-    if (!even) {
+    // vectors of logits go to 16-byte places, or are written one by one
+    const uintptr_t start = Probs ? reinterpret_cast<uintptr_t>(p - v.off) : reinterpret_cast<uintptr_t>(o - v.off * ES);
+    if (start & 15u) {
 #pragma unroll 1
         for (uint32_t i = v.s0 + threadIdx.x; i < v.s1; i += kNT)
             one(i);
@@ -563,13 +550,12 @@ __device__ __noinline__ void write_rows(Shared* sh, const StepCodes* codes, Keep
     }
     const uint32_t marks = codes && !bad ? v.marks(codes, step_code(cut)) : 0xffffu;
     const auto nothing = [&](uint32_t id) {
-        if (p) {
+        if constexpr (Probs) {
             float4* q = reinterpret_cast<float4*>(p + id);
 #pragma unroll
             for (int e = 0; e < E / 4; ++e)
                 q[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        }
-        if (o) {
+        } else {
             const uint32_t x = ES == 4 ? 0xff800000u : 0xff80ff80u;
             *reinterpret_cast<uint4*>(o + (size_t)id * ES) = make_uint4(x, x, x, x);
         }
@@ -581,7 +567,7 @@ __device__ __noinline__ void write_rows(Shared* sh, const StepCodes* codes, Keep
                 nothing(id);
                 return;
             }
-            if (p) {
+            if constexpr (Probs) {
                 float4* q = reinterpret_cast<float4*>(p + id);
 #pragma unroll
                 for (int e = 0; e < E / 4; ++e)
@@ -589,8 +575,7 @@ __device__ __noinline__ void write_rows(Shared* sh, const StepCodes* codes, Keep
                                        prob(vector_entry<ES>(w, 4 * e + 1), id + 4 * e + 1),
                                        prob(vector_entry<ES>(w, 4 * e + 2), id + 4 * e + 2),
                                        prob(vector_entry<ES>(w, 4 * e + 3), id + 4 * e + 3));
-            }
-            if (o) {
+            } else {
                 uint32_t h[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -607,7 +592,15 @@ __device__ __noinline__ void write_rows(Shared* sh, const StepCodes* codes, Keep
     v.template pass_unmarked<kDeep>(marks, nothing);
 }
 
-__device__ __forceinline__ bool writes_rows(const Shared* sh) { return sh->args.probs || sh->args.out; }
+// whichever the call wants
+template <int ES>
+__device__ __forceinline__ void write_out(Shared* sh, const StepCodes* codes, Keep how, float cut, float inv,
+                                          uint32_t token) {
+    if (sh->args.probs)
+        write_rows<ES, true>(sh, codes, how, cut, inv, token);
+    else if (sh->args.out)
+        write_rows<ES, false>(sh, codes, how, cut, inv, token);
+}
 
 __device__ __forceinline__ void put_token(const Shared* sh, int32_t id, float p) {
     const Args& a = sh->args;
