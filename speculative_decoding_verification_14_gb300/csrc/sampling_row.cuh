@@ -505,11 +505,12 @@ __device__ __forceinline__ void share_cut(Shared* sh) {
 
 enum Keep { kKeepFrom, kKeepToken, kBadRow };  // logits from `cut` on; one id; a row without an answer
 
-// Probabilities (`Probs`) or truncated logits.  Steps (see StepCodes; NULL: all are looked at) and
+// Probabilities (`Probs`) or truncated logits, of the entries from `cut` on (`From`), of one
+// token, or of a row without an answer (`bad`).  Steps (see StepCodes; NULL: all are looked at) and
 // vectors none of whose logits reaches `cut` are written without looking further.  inv:
 // 2^F over the kept mass.
-template <int ES, bool Probs>
-__device__ __noinline__ void write_rows(Shared* sh, const StepCodes* codes, Keep how, float cut, float inv,
+template <int ES, bool Probs, bool From>
+__device__ __noinline__ void write_rows(Shared* sh, const StepCodes* codes, bool bad, float cut, float inv,
                                         uint32_t token) {
     sh = here();
     const RowScale scale = sh->scale;
@@ -519,11 +520,11 @@ __device__ __noinline__ void write_rows(Shared* sh, const StepCodes* codes, Keep
     const int64_t row = sh->row;
     float* p = a.probs + row * a.probs_stride;
     unsigned char* o = static_cast<unsigned char*>(a.out) + row * a.out_stride * ES;
-    const bool bad = how == kBadRow;
-    const auto keep = [&](float l, uint32_t id) { return how == kKeepFrom ? l >= cut : id == token; };
+    bad = !From && bad;
+    const auto keep = [&](float l, uint32_t id) { return From ? l >= cut : id == token; };
     const auto prob = [&](float l, uint32_t id) {
         return bad ? __int_as_float(0x7fffffff)
-                   : keep(l, id) ? (how == kKeepFrom ? weight_float(scale, l) * inv : 1.0f) : 0.0f;
+                   : keep(l, id) ? (From ? weight_float(scale, l) * inv : 1.0f) : 0.0f;
     };
     const auto logit = [&](float l, uint32_t id) {
         return bad || keep(l, id) ? __float_as_uint(l) : 0xff800000u;
@@ -596,10 +597,13 @@ __device__ __noinline__ void write_rows(Shared* sh, const StepCodes* codes, Keep
 template <int ES>
 __device__ __forceinline__ void write_out(Shared* sh, const StepCodes* codes, Keep how, float cut, float inv,
                                           uint32_t token) {
+    const bool from = how == kKeepFrom, bad = how == kBadRow;
     if (sh->args.probs)
-        write_rows<ES, true>(sh, codes, how, cut, inv, token);
+        from ? write_rows<ES, true, true>(sh, codes, bad, cut, inv, token)
+             : write_rows<ES, true, false>(sh, codes, bad, cut, inv, token);
     else if (sh->args.out)
-        write_rows<ES, false>(sh, codes, how, cut, inv, token);
+        from ? write_rows<ES, false, true>(sh, codes, bad, cut, inv, token)
+             : write_rows<ES, false, false>(sh, codes, bad, cut, inv, token);
 }
 
 __device__ __forceinline__ void put_token(const Shared* sh, int32_t id, float p) {
