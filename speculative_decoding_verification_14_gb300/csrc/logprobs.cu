@@ -12,13 +12,13 @@
 // thread's largest entry, and of each step of four vectors in eight bits.  The n-th
 // largest of a CTA's thread maxima bounds its n-th largest entry from below: only threads
 // whose maximum reaches that bound look at their entries again, in those steps that
-// may hold one (without the eight bits, at all of them: 90 instead of 75 us below), and
+// may hold one (without the eight bits, at all of them: 90 instead of 71 us below), and
 // hand them to a short list.  Each CTA sends its n best to the first one, which orders them.
 //
 // What bounds it: the pass's instructions (a difference, a product and an addition for
 // two entries at a time, an ex2.approx each) next to the reads, and the chain after it:
-// 256 x 8 rows of 128256 bfloat16, 56% of them live, top 20: 75 us for 296 MB, 3.9 TB/s;
-// 37 x 3 rows of 50257 float32 15 us; 8 x 5 rows of 32000 bfloat16 10 us, a launch and
+// 256 x 8 rows of 128256 bfloat16, 56% of them live, top 20: 71 us for 296 MB, 4.2 TB/s;
+// 37 x 3 rows of 50257 float32 14 us; 8 x 5 rows of 32000 bfloat16 9 us, a launch and
 // sixteen barriers for the bound.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>

@@ -27,18 +27,19 @@
 // Rows with logits outside the window of places that matter, or crowded where the
 // list should hold them, go the general way (sampling_general.cuh).
 //
-// What bounds it: instructions and waits, not bytes.  A CTA of 64128 bfloat16 entries (256
-// rows of 128256, two CTAs a row, 3.4 CTAs on an SM) spends 37 of its 75 thousand
-// cycles counting (about seven instructions an entry and a shared-memory add), 3 on
-// its start, 4 on merging, 7 on weighing, 8 on two searches and 10 on finding the drawn
-// entry.  Four CTAs of 256 threads fit an SM (43 KB, 64 registers).  Parts of a fixed size
+// What bounds it: instructions, shared-memory adds and waits, not bytes.  A CTA of 64128
+// bfloat16 entries (256 rows of 128256, two CTAs a row, 3.4 CTAs on an SM) spends 36 of its
+// 72 thousand cycles counting (about seven instructions an entry, and an add that
+// takes some 3.5 turns for 32 lanes whose places fall on the banks as they come), 3 on its
+// start, 5 on the exchange, 7 on weighing, 8 on two searches and 8 on finding the drawn entry.
+// Four CTAs of 256 threads fit an SM (43 KB, 64 registers).  Parts of a fixed size
 // are why rows are cut no finer than the planner does.  A row alone is a chain
-// of some twenty barriers through code fetched for the first time: 45 thousand cycles
+// of some twenty barriers through code fetched for the first time: 47 thousand cycles
 // for 32000 float32 entries, which is why most loops here are not unrolled.
 // Per launch on one GB300 (replayed back to back, inputs larger than L2): 256 rows of
-// 128256 bfloat16 under top-p 59 us (65.7 MB, 1.1 TB/s); 2048 of them truncated
-// 266 us (1.05 GB in and out, 3.95 TB/s); 256 rows of 128256 float32 under every filter
-// with their probabilities 115 us (263 MB, 2.3 TB/s); 32000 float32 23 us.
+// 128256 bfloat16 under top-p 56 us (65.7 MB, 1.2 TB/s); 2048 of them truncated
+// 240 us (1.05 GB in and out, 4.4 TB/s); 256 rows of 128256 float32 under every filter
+// with their probabilities 97 us (263 MB, 2.7 TB/s); one of 32000 float32 22 us.
 #include "sampling_row.cuh"
 
 #include "sampling_general.cuh"
