@@ -88,7 +88,7 @@ __device__ __forceinline__ unsigned long long place_mass(const RowScale& s, cons
         return 0;
     const float l = place_logit<ES>(s.lmax, D);
     if constexpr (ES == 2)
-        return n * weight_fixed(s, pow2, l);
+        return mass_fixed(s, pow2, l, n);
     return __float2ull_rn((float)n * (ex2_approx((l - s.lmax) * s.ch) * (float)(1ull << s.fix)));
 }
 
@@ -1024,8 +1024,10 @@ __device__ __noinline__ bool draw_value(Shared* sh, const StepCodes* codes) {
     if (is_tiny(d.bin))
         return false;
     const float l = place_value(d.bin);
-    const int64_t id =
-        find_entry(sh, codes, d.bin, (w.p - d.above_mass) / weight_call(sh->scale, sh->pow2, l));
+    // of the place's entries, each with the same share of its mass; products below 2^62
+    const int cut = max(34 - __clzll(d.mass) - __clz(d.count), 0);
+    const unsigned long long at = ((w.p - d.above_mass) >> cut) * d.count / (d.mass >> cut);
+    const int64_t id = find_entry(sh, codes, d.bin, min((uint32_t)at, d.count - 1));
     if (id >= 0)
         put_token(sh, (int32_t)id, weight_float(sh->scale, l) * inverse_mass(sh->scale, sh->mass));
     return true;

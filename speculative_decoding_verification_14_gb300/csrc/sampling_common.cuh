@@ -91,14 +91,15 @@ __device__ __forceinline__ void exponent_of(const RowScale& s, float l, float& t
     tl = fmaf(dl, s.ch, tl);
 }
 
-// round(2^F 2^-t), within 2^-39 of the weight plus half a unit; 0 from t = 60 on.
+// 2^-t as u 2^(-43 - down), 2^43 <= u < 2^44, within 2^-39 of itself; down = 64 from t = 60 on.
 //   -t = k/64 + r,  |r| <= 1/128:  2^-t = 2^floor(k/64) * 2^((k mod 64)/64) * (1 + y),
 //   y = e^z - 1 for z = r ln 2 as z + z^2/2 + z^3/6 + z^4/24, |z| < 2^-7.5, its first
 // term in two floats; the terms behind it are below 2^-16 and take one (2^-40).
-__device__ __forceinline__ unsigned long long weight_fixed(const RowScale& s, const float2* pow2,
-                                                           float l) {
+__device__ __forceinline__ unsigned long long weight_parts(const RowScale& s, const float2* pow2, float l,
+                                                           int& down) {
     float th, tl;
     exponent_of(s, l, th, tl);
+    down = 64;
     if (!(th < 60.0f))
         return 0;
     constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: adding it rounds to an integer
@@ -125,13 +126,28 @@ __device__ __forceinline__ unsigned long long weight_fixed(const RowScale& s, co
     const float left = e + (v - (v4 - 4.0f));
     constexpr float kMagicLow = 1.430511474609375e-6f;  // 1.5 * 2^-20
     const int low = __float_as_int(left + kMagicLow) - __float_as_int(kMagicLow);
-    const unsigned long long u =
-        ((unsigned long long)(uint32_t)(__float_as_int(v4) - __float_as_int(4.0f)) << 22) +
-        (long long)low;
-    const int sh = kMaxFix - s.fix - (k >> 6);  // >= 0
-    if (sh > 46)
-        return 0;
-    return sh ? (u + (1ull << (sh - 1))) >> sh : u;
+    down = -(k >> 6);  // >= 0
+    return ((unsigned long long)(uint32_t)(__float_as_int(v4) - __float_as_int(4.0f)) << 22) + (long long)low;
+}
+
+__device__ __forceinline__ unsigned long long rounded_shift(unsigned long long x, int n) {
+    return n > 62 ? 0 : n ? (x + (1ull << (n - 1))) >> n : x;
+}
+
+// round(2^F 2^-t)
+__device__ __forceinline__ unsigned long long weight_fixed(const RowScale& s, const float2* pow2, float l) {
+    int down;
+    const unsigned long long u = weight_parts(s, pow2, l, down);
+    return rounded_shift(u, down + kMaxFix - s.fix);
+}
+
+// round(2^F n 2^-t) for n <= V entries with one logit: many small ones are not rounded
+// away one by one (n u < 2^63 in units of 2^-F)
+__device__ __forceinline__ unsigned long long mass_fixed(const RowScale& s, const float2* pow2, float l,
+                                                         uint32_t n) {
+    int down;
+    const unsigned long long u = weight_parts(s, pow2, l, down);
+    return rounded_shift(rounded_shift(u, kMaxFix - s.fix) * n, down);
 }
 
 // 2^-t as a float (2^-22 of itself): what probabilities are written from.

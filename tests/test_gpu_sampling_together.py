@@ -188,6 +188,23 @@ def test_a_long_tail_of_small_weights(dtype):
     assert 0 <= j < V - 1 and abs(j - first) <= 2.0 ** -8 * V + 2
 
 
+@pytest.mark.parametrize("V,far", [(100003, 25.0), (250000, 25.0)])
+def test_a_bfloat16_tail_is_weighed_as_one(V, far):
+    """Equal entries in a place of their own: their mass is rounded once, not V times."""
+    x = np.full((1, 1, V), 2.0 - far)
+    x[0, 0, 1234] = 2.0
+    lg = _tensor(x, "bf16")
+    w = np.exp(-far)
+    E = 1.0 + (V - 1) * w
+    for part in (0.2, 0.7, 0.95):
+        u = np.float32((1.0 + part * (V - 1) * w) / E)
+        j = int(gh.verifier().sample(lg, _tensor([[u]], "f32"))["tokens"])
+        j = j if j < 1234 else j - 1
+        # the tail to 2^-39 of itself; E and u E to half a unit and a unit of 2^-43
+        off = (V - 1) * 2.0 ** -39 + 2 * 2.0 ** -43 / w + 1
+        assert abs(j - (float(u) * E - 1.0) / w) <= off
+
+
 def test_streams_and_threads():
     """Calls on streams of their own, at once, from two threads with one context."""
     torch = _torch()
