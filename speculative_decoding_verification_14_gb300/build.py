@@ -17,7 +17,7 @@ BUILD_DIR = os.path.join(PKG, "_build")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CUDA_SOURCES = ("spec_verify.cu", "greedy.cu", "truncated.cu", "sampling.cu", "logprobs.cu")
 HOST_SOURCES = ("planner.cpp", "adapt.cpp", "sampling_planner.cpp")
-HEADERS = ("sv_internal.h", "sv_context.h", "sampling_common.cuh",
+HEADERS = ("sv_internal.h", "sv_context.h", "sampling_common.cuh", "sampling_weights.cuh",
            "sampling_row.cuh", "sampling_general.cuh")
 SOURCES = [os.path.join(CSRC, f) for f in (*CUDA_SOURCES, *HEADERS, *HOST_SOURCES)] + [
     os.path.join(INCLUDE, "spec_verify.h")]

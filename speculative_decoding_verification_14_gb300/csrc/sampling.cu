@@ -536,18 +536,6 @@ struct Sums {
     unsigned long long x[3];
 };
 
-// A weight for sums, in half the instructions of weight_fixed: 2^(p - M), p = l c,
-// M = l_max c, without the difference l_max - l.
-//   M = Mk/128 + Mr, |Mr| <= 1/256;  p = k/128 + r + Mr, |r| <= 1/256, p - k/128 exact;
-//   2^(p - M) = 2^floor((k - Mk)/128) T[(k - Mk) mod 128] (1 + y),  y = e^z - 1 in one float.
-// y rounds at 2^-33 to either side, which a sum of many entries does not show (the
-// lists' entries, few, take weight_fixed).  T in two floats, a copy for each of 16 lanes,
-// so that lanes' reads do not meet in a bank.  For |M| < 128.
-struct SumScale {
-    float ch, cl, floor_l, mh, ml;  // mh + ml: Mr
-    int k0;                         // Mk
-    const float2* steps;
-};
 __device__ __forceinline__ SumScale sum_scale(Shared* sh, const RowScale& s) {
     SumScale t;
     t.ch = s.ch;
@@ -574,49 +562,6 @@ __device__ __forceinline__ SumScale sum_scale(Shared* sh, const RowScale& s) {
     __syncthreads();
     return t;
 }
-// the weight as the table's part and the rest
-__device__ __forceinline__ float2 sum_weight(const SumScale& s, float l) {
-    constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
-    l = fmaxf(l, s.floor_l);
-    const float p = l * s.ch;
-    const float pl = fmaf(l, s.cl, -s.ml) + fmaf(l, s.ch, -p);
-    const float m = fmaf(p - s.mh, 128.0f, kMagic);
-    const int k = __float_as_int(m) - __float_as_int(kMagic) - s.k0;
-    const float r = (fmaf(m - kMagic, -0.0078125f, p) - s.mh) + pl;
-    const float y = r * fmaf(r, fmaf(r, fmaf(r, 0.00961812911f, 0.0555041087f), 0.240226507f), 0.693147181f);
-    const float2 t = s.steps[(k & 127) << 4];
-    const float two = __int_as_float(((k & ~127) << 16) + (127 << 23));  // 2^floor(k/128)
-    return make_float2(t.x * two, fmaf(t.x, y, t.y) * two);
-}
-// What WeightSum's parts are worth in units of 2^-F.
-struct Units {
-    float one, back;   // 2^n, n = min(F, 37), and 2^-n
-    uint32_t hi, low;  // 2^(F - 20), 2^(F - n)
-    __device__ __forceinline__ explicit Units(int F)
-        : one((float)(1ull << min(F, 37))), back(1.0f / one), hi(1u << (F - 20)), low(1u << (F - min(F, 37))) {}
-};
-// A sum of weights.  Of four at a time, the table's parts go to a float of 2^-20 units,
-// whose bits count them, and what that and the rests (|e^z - 1| < 2^-8.5) leave to one
-// below 2^-6.5.  An integer takes its 2^-37 units, and what is less stays for the next four:
-// a row's many small weights are not rounded away one by one.
-struct WeightSum {
-    static constexpr float kBase = 8.0f;
-    float hi = kBase, lo = 0.0f;
-    __device__ __forceinline__ void add(float2 w) {
-        const float s = hi + w.x, taken = s - hi;
-        lo += w.y + (w.x - taken);
-        hi = s;
-    }
-    __device__ __forceinline__ void into(unsigned long long& x, const Units& u) {
-        const int units = __float2int_rn(lo * u.one);
-        x += (unsigned long long)(__float_as_uint(hi) - __float_as_uint(kBase)) * u.hi;
-        x += (long long)units * (int)u.low;
-        lo = fmaf((float)units, -u.back, lo);
-        hi = kBase;
-    }
-    __device__ __forceinline__ long long rest(int F) const { return __float2ll_rn(lo * (float)(1ull << F)); }
-};
-
 // What a pass adds to: all, and of each stretch that is no list from the largest on what
 // lies above it.  With what goes to the lists; a stretch that is off, or whose entries the
 // list has, reaches from infinity on.
