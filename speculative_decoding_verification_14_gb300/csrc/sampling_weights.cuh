@@ -158,7 +158,7 @@ __device__ __forceinline__ unsigned long long scaled(uint64_t mant, int sh, unsi
     return q + (up && rest ? 1 : 0);
 }
 __device__ __forceinline__ unsigned long long floor_scaled(float u, unsigned long long x) {
-    const uint32_t b = __float_as_uint(u);  // 0 <= u < 1
+    const uint32_t b = __float_as_uint(u) & 0x7fffffffu;  // 0 <= u < 1; -0 is 0
     const int ex = (int)(b >> 23);
     const uint32_t m = ex ? (b & 0x7fffffu) | 0x800000u : b & 0x7fffffu;
     return scaled(m, 150 - (ex ? ex : 1), x, false);

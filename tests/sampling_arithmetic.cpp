@@ -1,0 +1,84 @@
+// The sampling kernels' arithmetic on weights (sampling_weights.cuh), run on the host and
+// measured against long doubles: 64 bits and more, good to 2^-60 here.  Built without
+// contraction, as the header writes its fused operations out.  Prints a line "name value"
+// for each figure the tests ask about.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstdio>
+#include <cstring>
+#include <random>
+
+using std::max;
+using std::min;
+#define __CUDACC__
+#define __device__
+#define __forceinline__ inline
+struct float2 {
+    float x, y;
+};
+static inline float2 make_float2(float x, float y) { return {x, y}; }
+static inline uint32_t __float_as_uint(float f) {
+    uint32_t u;
+    std::memcpy(&u, &f, 4);
+    return u;
+}
+static inline int __float_as_int(float f) { return (int)__float_as_uint(f); }
+static inline float __uint_as_float(uint32_t u) {
+    float f;
+    std::memcpy(&f, &u, 4);
+    return f;
+}
+static inline float __int_as_float(int i) { return __uint_as_float((uint32_t)i); }
+static inline long long __double_as_longlong(double d) {
+    long long i;
+    std::memcpy(&i, &d, 8);
+    return i;
+}
+static inline unsigned long long __umul64hi(unsigned long long a, unsigned long long b) {
+    return (unsigned long long)(((unsigned __int128)a * b) >> 64);
+}
+static inline float __fdiv_rn(float a, float b) { return a / b; }
+static inline int __float2int_rn(float f) { return (int)lrintf(f); }
+static inline long long __float2ll_rn(float f) { return llrintf(f); }
+#include "../speculative_decoding_verification_14_gb300/csrc/sampling_weights.cuh"
+#undef __CUDACC__
+
+using namespace sv;
+
+static std::mt19937_64 gen(7);
+
+// floor(u x) and ceil(p x) against 128-bit products; the largest difference
+static void shares() {
+    const float us[] = {0.0f, -0.0f, 0x1p-149f, 0x1.8p-130f, 0x1p-24f, 0.3f, 0.5f, 0x1.fffffep-1f};
+    uint64_t off = 0, zero = 0;
+    for (int i = 0; i < 2000; ++i) {
+        const uint64_t x = gen() >> (2 + gen() % 60);
+        for (float u : us) {
+            int e;
+            const uint64_t m = (uint64_t)std::ldexp(std::frexp(std::fabs(u), &e), 24);
+            const unsigned __int128 y = (unsigned __int128)m * x;
+            const int sh = 24 - e;
+            const uint64_t want = sh >= 128 ? 0 : (uint64_t)(y >> sh), got = floor_scaled(u, x);
+            off = max(off, want > got ? want - got : got - want);
+            if (u == 0.0f)
+                zero = max<uint64_t>(zero, got);
+        }
+        const double p = (double)(gen() >> 11) * 0x1p-53;
+        if (p > 0.0) {
+            int e;
+            const uint64_t m = (uint64_t)std::ldexp(std::frexp(p, &e), 53);
+            const int sh = 53 - e;
+            const unsigned __int128 y = (unsigned __int128)m * x;
+            const uint64_t want = (uint64_t)(y >> sh) + ((y & (((unsigned __int128)1 << sh) - 1)) != 0);
+            const uint64_t got = ceil_scaled(p, x);
+            off = max(off, want > got ? want - got : got - want);
+        }
+    }
+    std::printf("shares_off %llu\nzero_share %llu\n", (unsigned long long)off, (unsigned long long)zero);
+}
+
+int main() {
+    shares();
+    return 0;
+}

@@ -1,0 +1,23 @@
+"""The sampling kernels' arithmetic on weights, compiled for the host from the header the kernels
+use (sampling_arithmetic.cpp), against wider arithmetic."""
+import os
+import subprocess
+
+import pytest
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+
+
+@pytest.fixture(scope="module")
+def figures(tmp_path_factory):
+    exe = str(tmp_path_factory.mktemp("arithmetic") / "run")
+    subprocess.run(["g++", "-O2", "-std=c++17", "-ffp-contract=off", "-o", exe,
+                    os.path.join(HERE, "sampling_arithmetic.cpp")], check=True)
+    out = subprocess.run([exe], check=True, capture_output=True, text=True).stdout
+    return {k: float(v) for k, v in (line.split() for line in out.splitlines())}
+
+
+def test_shares_of_a_mass_are_exact(figures):
+    """floor(u x) and ceil(p x) have no rounding before the last step; a uniform of -0 is 0."""
+    assert figures["zero_share"] == 0
+    assert figures["shares_off"] == 0
