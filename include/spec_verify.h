@@ -414,6 +414,16 @@ int spec_sample_get_plan(sv_ctx* ctx, int B, int rows_per_seq, int64_t V, int lo
 int spec_sample_plan_for(int num_sms, int max_cluster, int B, int rows_per_seq, int64_t V,
                          int logits_dtype, int ovr_cluster, sv_plan* out);
 
+/* Counts slow rows of the two calls above.  Most rows are settled by counting
+ * their entries by value; the others -- erroneous ones, float32 ones at T = 0, rows
+ * with logits of magnitude 127 and more that weigh something or fewer logits above
+ * -inf than top-k, and float32 rows with thousands of entries next to the cut or the
+ * draw -- go a general way with the same answers, which takes several passes more.  With `general_rows` set, every later call on this
+ * context adds 1 to it for each of them.  It is one DEVICE uint32 owned by the
+ * caller, who zeroes it and keeps it alive while set; NULL turns the counting off.
+ * Returns SV_OK or SV_ERR_INVALID_ARG (no context, misaligned). */
+int spec_sample_set_telemetry(sv_ctx* ctx, uint32_t* general_rows);
+
 /* Log-probabilities of the tokens a verify emitted.  For row i < accept_len[b]
  * of sequence b and its token x = tokens[b, i]:
  *   logprob [B, rows]          (l_x - max l)/T - ln sum_v exp((l_v - max l)/T)

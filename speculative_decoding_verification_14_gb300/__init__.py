@@ -149,6 +149,7 @@ def library() -> ctypes.CDLL:
                                                       ctypes.c_int, ctypes.POINTER(sv_plan)])
                for op in ("sample", "logprobs")},
             "spec_verify_set_telemetry": (ctypes.c_int, [P, P, ctypes.c_int]),
+            "spec_sample_set_telemetry": (ctypes.c_int, [P, P]),
             "spec_verify_selftest_wait": (ctypes.c_int, [ctypes.c_int, ctypes.c_ulonglong,
                                                          ctypes.c_int,
                                                          ctypes.POINTER(ctypes.c_int),
@@ -375,6 +376,10 @@ def spec_verify_set_telemetry(ctx, hist_ptr, bins) -> int:
     return library().spec_verify_set_telemetry(ctx, hist_ptr, int(bins))
 
 
+def spec_sample_set_telemetry(ctx, general_rows_ptr) -> int:
+    return library().spec_sample_set_telemetry(ctx, general_rows_ptr)
+
+
 def spec_adapt(hist, K: int, K_max: int, K_floor: int = 1, threshold: float = 0.35,
                min_tested: int = 0) -> dict:
     """`hist`: host sequence of accepted-length counts (bin 0 = errors) taken
@@ -500,6 +505,25 @@ class Verifier:
         if rc != SV_OK:
             raise SpecVerifyError(rc, "spec_verify_set_telemetry")
         self._telemetry = hist
+
+    def set_sample_telemetry(self, general_rows) -> None:
+        """Count the rows of every later sample and filter_logits call that went the
+        general, slower way into `general_rows`, a uint32 CUDA tensor of one element
+        (zeroed by the caller); None stops counting.  The tensor must stay alive
+        while it is set."""
+        if general_rows is not None:
+            import torch
+            if general_rows.dtype != torch.int32 and \
+                    general_rows.dtype != getattr(torch, "uint32", None):
+                raise TypeError("telemetry counters must be a 32-bit integer tensor")
+            if general_rows.numel() != 1:
+                raise ValueError("the counter of general rows must have one element")
+            self._on_device(general_rows, "the counter of general rows")
+        rc = spec_sample_set_telemetry(
+            self.ctx, None if general_rows is None else general_rows.data_ptr())
+        if rc != SV_OK:
+            raise SpecVerifyError(rc, "spec_sample_set_telemetry")
+        self._sample_telemetry = general_rows
 
     def run(self, logits, q, tokens, uniforms, temperature: float, out: Optional[dict] = None,
             stats: bool = False, status: bool = True, stream=None) -> dict:

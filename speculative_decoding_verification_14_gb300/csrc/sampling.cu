@@ -1130,6 +1130,8 @@ __global__ void __launch_bounds__(kNT, 4) sv_sample_kernel(const __grid_constant
         return;
     }
     the_cluster().sync();  // every CTA is done with what it was told
+    if (sh->args.general_rows && cta_rank() == 0 && threadIdx.x == 0)
+        atomicAdd(sh->args.general_rows, 1u);
     general_row<ES>(sh, sh->code);
 }
 
@@ -1146,6 +1148,7 @@ int launch(sv_ctx* ctx, Args& a, int B, int rows, int64_t V, int dtype, cudaStre
         return rc;
     const int es = dtype == SV_BF16 ? 2 : 4;
     a.err_word = ctx->d_err;
+    a.general_rows = ctx->general_rows;
     a.V = V;
     a.slice = plan.slice;
     a.C = plan.cluster;
@@ -1231,6 +1234,13 @@ int spec_sample_get_plan(sv_ctx* ctx, int B, int rows_per_seq, int64_t V, int lo
         return SV_ERR_INVALID_ARG;
     return spec_sample_plan_for(ctx->num_sms, ctx->sampling_max_cluster, B, rows_per_seq, V,
                                 logits_dtype, ctx->ovr_cluster, out);
+}
+
+int spec_sample_set_telemetry(sv_ctx* ctx, uint32_t* general_rows) {
+    if (!ctx || !aligned(general_rows, 4))
+        return SV_ERR_INVALID_ARG;
+    ctx->general_rows = general_rows;
+    return SV_OK;
 }
 
 int spec_sample_run(sv_ctx* ctx, const void* logits, int logits_dtype, int64_t logits_stride,

@@ -48,6 +48,7 @@ struct Args {
     int32_t* kept;
     int32_t* status;
     uint32_t* err_word;
+    uint32_t* general_rows;  // counter of rows that go the general way, or NULL
     sv_sampling set;
     int64_t V, slice;
     int rows_per_seq, C, fix;

@@ -18,6 +18,7 @@ struct sv_ctx {
     int ovr_cluster = 0, ovr_group = 0, ovr_threads = 0;  // spec_verify_set_plan_override
     uint32_t* al_hist = nullptr;  // caller's accepted-length counters (device), or none
     int al_bins = 0;
+    uint32_t* general_rows = nullptr;  // caller's counter of slow sampling rows (device), or none
     // staging for the host-buffer entry point
     unsigned char* d_stage = nullptr;
     size_t stage_bytes = 0;

@@ -24,3 +24,72 @@ def test_a_uniform_of_minus_zero_is_zero(dtype):
         got = gh.verifier().sample(lg, -u, **s, probs=True)
         assert all(torch.equal(got[k], want[k]) for k in want)
         check_rows(lg, s, (-u).cpu().numpy(), {k: t.cpu().numpy() for k, t in got.items()})
+
+
+def general_rows(lg, settings, u=None):
+    """How many rows of a draw, and of a filter, go the general way; their answers are checked."""
+    import torch
+    v = gh.verifier()
+    n = torch.zeros(2, dtype=torch.int32, device="cuda")
+    u = torch.rand(lg.shape[:-1], device="cuda", generator=torch.Generator(device="cuda").manual_seed(6)) \
+        if u is None else u
+    try:
+        v.set_sample_telemetry(n[0])
+        got = v.sample(lg, u, **settings, probs=True)
+        v.set_sample_telemetry(n[1])
+        fil = v.filter_logits(lg, **settings)
+    finally:
+        v.set_sample_telemetry(None)
+    v.sample(lg, u, **settings)  # not counted
+    check_rows(lg, settings, u.cpu().numpy(), {k: t.cpu().numpy() for k, t in got.items()},
+               {k: t.double().cpu().numpy() if t.is_floating_point() else t.cpu().numpy() for k, t in fil.items()})
+    return n.tolist()
+
+
+def shaped(kind, B, V, seed):
+    x = rows_of(B, 1, V, seed, 1.0)
+    if kind == "normal":
+        return 2.5 * x
+    if kind == "peaked":
+        return 3.0 * x + 8.0 * (np.random.default_rng(seed).random(x.shape) < 0.01)
+    if kind == "zipf":
+        return 2.0 * x - 1.1 * np.log(np.arange(1, V + 1))
+    if kind == "masked":
+        return np.where(np.random.default_rng(seed).random(x.shape) < 0.9, -np.inf, 2.5 * x)
+    lowest = -3.3895313892515355e38  # bfloat16's
+    return np.where(np.random.default_rng(seed).random(x.shape) < 0.9, lowest, 2.5 * x)
+
+
+QUICK = [OFF, {**OFF, "top_k": 50, "top_p": 0.95}, {**OFF, "temperature": 0.6, "top_p": 0.95, "min_p": 0.05}]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kind", ["normal", "peaked", "zipf", "masked", "lowest"])
+def test_ordinary_rows_are_settled_by_counting(kind, dtype):
+    B, V = 8, 20011
+    lg = _tensor(shaped(kind, B, V, 3), dtype)
+    for s in QUICK:
+        assert general_rows(lg, s) == [0, 0], s
+
+
+def test_rows_that_go_the_general_way():
+    B, V = 4, 4000
+    x = shaped("normal", B, V, 3)
+    assert general_rows(_tensor(x + 200.0, "bf16"), OFF) == [B, B]
+    assert general_rows(_tensor(x + 200.0, "f32"), OFF) == [B, B]
+    assert general_rows(_tensor(x, "f32"), {**OFF, "temperature": 0.0}) == [B, B]
+    assert general_rows(_tensor(x, "bf16"), {**OFF, "temperature": 0.0}) == [0, 0]
+    assert general_rows(_tensor(1.0 + 1e-3 * x, "f32"), {**OFF, "top_p": 0.5}) == [B, B]
+    x[2, 0, 7] = np.nan
+    assert general_rows(_tensor(x, "f32"), OFF) == [1, 1]
+    gh.verifier().error()
+
+
+def test_telemetry_refusals():
+    import torch
+    import speculative_decoding_verification_14_gb300 as sv
+    v = gh.verifier()
+    assert sv.spec_sample_set_telemetry(v.ctx, 2) == sv.SV_ERR_INVALID_ARG
+    for bad in (torch.zeros(1), torch.zeros(2, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32)):
+        with pytest.raises((TypeError, ValueError)):
+            v.set_sample_telemetry(bad)
