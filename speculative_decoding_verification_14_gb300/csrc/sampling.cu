@@ -81,7 +81,9 @@ __device__ __forceinline__ float place_logit(float lmax, int D) {
     return l;
 }
 
-// mass of n entries at place D: bfloat16 exactly, float32 by the middle one's float weight
+// mass of n entries at place D: bfloat16 exactly, float32 by the middle one's float weight;
+// one of those at l_max's place is l_max, which weighs 1: at low temperatures the middle weighs
+// nothing, and a row's mass is never 0
 template <int ES>
 __device__ __forceinline__ unsigned long long place_mass(const RowScale& s, const float2* pow2, int D, uint32_t n) {
     if (n == 0)
@@ -89,7 +91,9 @@ __device__ __forceinline__ unsigned long long place_mass(const RowScale& s, cons
     const float l = place_logit<ES>(s.lmax, D);
     if constexpr (ES == 2)
         return mass_fixed(s, pow2, l, n);
-    return __float2ull_rn((float)n * (ex2_approx((l - s.lmax) * s.ch) * (float)(1ull << s.fix)));
+    const float w = ex2_approx((l - s.lmax) * s.ch), one = (float)(1ull << s.fix);
+    const bool top = ((__float_as_uint(l) ^ __float_as_uint(s.lmax)) >> 16) == 0;
+    return __float2ull_rn(top ? one + (float)(n - 1) * (w * one) : (float)n * (w * one));
 }
 
 // Counts the two logits whose upper 16 bits x holds.  Each place's byte

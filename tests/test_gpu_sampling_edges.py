@@ -93,3 +93,16 @@ def test_telemetry_refusals():
     for bad in (torch.zeros(1), torch.zeros(2, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32)):
         with pytest.raises((TypeError, ValueError)):
             v.set_sample_telemetry(bad)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1.2e-38, 1e-30, 1e-10, 1e-5, 1e-4, 3e-4, 1e-3, 3e-3, 0.01, 0.03, 0.1])
+def test_low_temperatures(T, dtype):
+    """A row's mass is that of its largest few entries, however little a logit half a place below weighs."""
+    import torch
+    x = rows_of(16, 1, 3000, 5)
+    x[8:] *= 0.1
+    lg = _tensor(x, dtype)
+    for s in ({"top_p": 0.9}, {"top_p": 0.3}, {"top_p": 0.999, "top_k": 40}, {"top_p": 0.5, "min_p": 0.2}, {}):
+        s = {**OFF, "temperature": T, **s}
+        general_rows(lg, s, torch.rand(16, 1, device="cuda", generator=torch.Generator(device="cuda").manual_seed(2)))
