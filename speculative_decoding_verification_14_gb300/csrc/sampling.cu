@@ -258,11 +258,11 @@ __device__ __noinline__ void weigh_places(Shared* sh) {
         if (__any_sync(kAllLanes, n)) {
             m = place_mass<ES>(scale, sh->pow2, D, n);
             if (ES == 4 && n) {
-                // width 2^-7 of the place's power of two; 1 / sqrt(12)
+                // width 2^-7 of the place's power of two, 2^-25 below the window; 1 / sqrt(12)
                 const float l = place_logit<ES>(scale.lmax, D);
                 const uint32_t b = __float_as_uint(l) & 0x7f800000u;
-                const float e = ex2_approx((l - scale.lmax) * scale.ch) *
-                                (__uint_as_float(b - (7u << 23)) * 0.28867513f * scale.ch);
+                const float width = is_tiny(D) ? 0x1p-25f : __uint_as_float(b - (7u << 23));
+                const float e = ex2_approx((l - scale.lmax) * scale.ch) * (width * 0.28867513f * scale.ch);
                 noise = fmaf(e * e, (float)n, noise);
             }
             n = __reduce_add_sync(kAllLanes, n);
@@ -992,7 +992,8 @@ __device__ __noinline__ bool settle_exactly(Shared* sh, const StepCodes* codes) 
 #pragma unroll
     for (int o = kMaxC / 2; o; o >>= 1)
         noise += __shfl_xor_sync(kAllLanes, noise, o);
-    const unsigned long long margin = __float2ull_rn(4.0f * sqrtf(noise) * (float)(1ull << sh->scale.fix)) + (sh->whole >> 12);
+    const float deviations = 4.0f * sqrtf(noise) * (float)(1ull << sh->scale.fix);  // may be infinite
+    const unsigned long long margin = __float2ull_rn(fminf(deviations, (float)sh->whole)) + (sh->whole >> 12);
     if (sh->cut_at.bin < kNoPlace) {
         band_around(sh, 0, sh->cut_at, margin);
         if (!sh->band[0].on)

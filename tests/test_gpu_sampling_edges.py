@@ -106,3 +106,27 @@ def test_low_temperatures(T, dtype):
     for s in ({"top_p": 0.9}, {"top_p": 0.3}, {"top_p": 0.999, "top_k": 40}, {"top_p": 0.5, "min_p": 0.2}, {}):
         s = {**OFF, "temperature": T, **s}
         general_rows(lg, s, torch.rand(16, 1, device="cuda", generator=torch.Generator(device="cuda").manual_seed(2)))
+
+
+@pytest.mark.parametrize("zeros", [0, 4])
+def test_a_few_zeros_do_not_narrow_the_stretches(zeros):
+    """Half of each row's mass in two entries, one of them at its place's lower end: the places' sums are
+    off by up to 0.8 % of the row (2^-5 of a quarter), within four deviations (4 * 2^-4 / sqrt(12) of
+    the quarter), and the entries around the cut weigh a few 2^-14 each.  A few logits below the counted
+    magnitudes, as a padded vocabulary's, change nothing."""
+    import torch
+    B, V = 32, 4096
+    rng = np.random.default_rng(8)
+    x = rng.standard_normal((B, 1, V))
+    x[:, :, 11], x[:, :, 12] = 8.0, 8.07
+    if zeros:
+        x[:, :, -zeros:] = 0.0
+    lg = _tensor(x, "f32")
+    p = torch.tensor(rng.uniform(0.6, 0.9, B).astype(np.float32), device="cuda")
+    assert general_rows(lg, {**OFF, "top_p": p}) == [0, 0]
+
+
+def test_deviations_beyond_what_a_float_holds():
+    """At T = 1e-30 the square of a place's width over T is no float."""
+    lg = _tensor(rows_of(4, 1, 3000, 5), "f32")
+    assert general_rows(lg, {**OFF, "temperature": 1e-30, "top_p": 0.9}) == [0, 0]
