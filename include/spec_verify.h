@@ -370,7 +370,7 @@ typedef struct {
  * alone: the same law, another token for the same uniform.)  Weights are
  * integers, good to 2^-39 of themselves and 2^-44 of the largest (for V up to
  * 2^19; a bit less for each doubling beyond); a float32 row's sums are good to
- * 2^-31 of themselves.  Repeated calls give the same bits.
+ * 2^-30 of themselves.  Repeated calls give the same bits.
  *
  * An erroneous row (a bad setting; a uniform outside [0, 1): SV_ERR_UNIFORM_RANGE;
  * a NaN or +inf, or only -inf: SV_ERR_NONFINITE) gets token -1, kept 0, NaN

@@ -541,27 +541,10 @@ struct Sums {
 };
 
 __device__ __forceinline__ SumScale sum_scale(Shared* sh, const RowScale& s) {
-    SumScale t;
-    t.ch = s.ch;
-    t.cl = s.cl;
-    t.floor_l = s.lmax - 70.0f / s.ch;
-    const float m = s.lmax * s.ch, ml = fmaf(s.lmax, s.ch, -m) + s.lmax * s.cl, k = rintf(m * 128.0f);
-    const float rest = fmaf(k, -0.0078125f, m);  // exact
-    t.mh = rest + ml;
-    t.ml = ml - (t.mh - rest);
-    t.k0 = (int)k;
+    SumScale t(s);
     float2* steps = reinterpret_cast<float2*>(sh->hi);  // behind the second list: 16 KB
-    constexpr float kHalfh = 1.00542986392974853515625f, kHalfl = 3.7183054286195135e-8f;  // 2^(1/128)
-    for (int i = threadIdx.x; i < 128 * 16; i += kNT) {
-        const int j = i >> 4;
-        float2 p = sh->pow2[j >> 1];
-        if (j & 1) {
-            const float h = p.x * kHalfh, l = fmaf(p.x, kHalfh, -h) + fmaf(p.x, kHalfl, p.y * kHalfh);
-            p.x = h + l;
-            p.y = l - (p.x - h);
-        }
-        steps[i] = p;
-    }
+    for (int i = threadIdx.x; i < kSteps * 16; i += kNT)
+        steps[i] = sh->pow2[i >> 4];
     t.steps = steps + (threadIdx.x & 15);
     __syncthreads();
     return t;
@@ -1098,13 +1081,13 @@ __device__ __forceinline__ void set_up(Shared* sh, const Args& a) {
         sh->T = a.set.temperatures ? a.set.temperatures[seq] : a.set.temperature;
         sh->k = k > 0 ? (uint32_t)k : 0;
         sh->top_p = a.set.top_ps ? (double)a.set.top_ps[seq] : a.set.top_p;
-    } else if (tid >= 64 && tid < 128) {
-        sh->pow2[tid - 64] = kPow2Steps[tid - 64];
-    } else if (tid >= 128 && tid < 128 + 2 * kConds) {
-        sh->hit[(tid - 128) / kConds][(tid - 128) % kConds].chunk = -1;
-        sh->place[(tid - 128) / kConds][(tid - 128) % kConds].bin = kNoPlace;
-    } else if (tid >= 160 && tid < 162) {
-        sh->list_n[tid - 160] = 0;
+    } else if (tid >= 64 && tid < 64 + 2 * kConds) {
+        sh->hit[(tid - 64) / kConds][(tid - 64) % kConds].chunk = -1;
+        sh->place[(tid - 64) / kConds][(tid - 64) % kConds].bin = kNoPlace;
+    } else if (tid >= 96 && tid < 98) {
+        sh->list_n[tid - 96] = 0;
+    } else if (tid >= kNT - kSteps) {
+        sh->pow2[tid - (kNT - kSteps)] = kPow2Steps[tid - (kNT - kSteps)];
     }
     uint4* z = reinterpret_cast<uint4*>(sh->count);
     for (int i = tid; i < kPlaces / 4; i += kNT)

@@ -110,7 +110,7 @@ struct alignas(16) Shared {
         };
         uint32_t count[kPlaces];
     };
-    float2 pow2[64];
+    float2 pow2[kSteps];
     Args args;
     // the CTA's slice of the row
     const unsigned char* base;  // the row's first logit

@@ -26,30 +26,52 @@ inline int weight_bits(int64_t V) {
 
 #ifdef __CUDACC__
 
-// 2^(j/64) as the sum of two floats, j = 0..63.
-__device__ const float2 kPow2Steps[64] = {
-    {0x1.000000p+0f, 0x0p+0f}, {0x1.02c9a4p+0f, -0x1.887fa0p-28f}, {0x1.059b0ep+0f, -0x1.9d4f52p-25f},
-    {0x1.087452p+0f, -0x1.e2990ep-26f}, {0x1.0b5586p+0f, 0x1.9f3122p-25f}, {0x1.0e3ec4p+0f, -0x1.a585ccp-25f},
-    {0x1.11301ep+0f, -0x1.fdb496p-25f}, {0x1.1429aap+0f, 0x1.d525bcp-25f}, {0x1.172b84p+0f, -0x1.c15742p-27f},
-    {0x1.1a35bep+0f, 0x1.6df96ep-25f}, {0x1.1d4874p+0f, -0x1.d2e8cap-25f}, {0x1.2063b8p+0f, 0x1.0c519ap-25f},
-    {0x1.2387a6p+0f, 0x1.ceac48p-25f}, {0x1.26b456p+0f, 0x1.789f38p-26f}, {0x1.29e9e0p+0f, -0x1.5c0424p-25f},
-    {0x1.2d285ap+0f, 0x1.b900c2p-26f}, {0x1.306fe0p+0f, 0x1.4636e2p-25f}, {0x1.33c08cp+0f, -0x1.b37d20p-25f},
-    {0x1.371a74p+0f, -0x1.18aac6p-25f}, {0x1.3a7db4p+0f, -0x1.634c02p-25f}, {0x1.3dea64p+0f, 0x1.824684p-25f},
-    {0x1.4160a2p+0f, 0x1.f72e2ap-28f}, {0x1.44e086p+0f, 0x1.8624b4p-30f}, {0x1.486a2cp+0f, -0x1.47d866p-25f},
-    {0x1.4bfdaep+0f, -0x1.593abcp-25f}, {0x1.4f9b28p+0f, -0x1.2c5a6cp-25f}, {0x1.5342b6p+0f, -0x1.2c5610p-25f},
-    {0x1.56f474p+0f, -0x1.295b04p-25f}, {0x1.5ab07ep+0f, -0x1.5bd5ecp-27f}, {0x1.5e76f2p+0f, -0x1.4a5bd6p-25f},
-    {0x1.6247ecp+0f, -0x1.f8b550p-25f}, {0x1.662388p+0f, 0x1.2a9112p-27f}, {0x1.6a09e6p+0f, 0x1.9fcef4p-26f},
-    {0x1.6dfb24p+0f, -0x1.cd72e8p-27f}, {0x1.71f75ep+0f, 0x1.1d8beep-25f}, {0x1.75feb6p+0f, -0x1.37b306p-25f},
-    {0x1.7a1148p+0f, -0x1.829fd0p-25f}, {0x1.7e2f34p+0f, -0x1.261634p-25f}, {0x1.82589ap+0f, -0x1.accc7cp-26f},
-    {0x1.868d9ap+0f, -0x1.2edb44p-26f}, {0x1.8ace54p+0f, 0x1.15506ep-27f}, {0x1.8f1aeap+0f, -0x1.baa232p-26f},
-    {0x1.93737cp+0f, -0x1.e64744p-25f}, {0x1.97d82ap+0f, -0x1.0d8d84p-31f}, {0x1.9c4918p+0f, 0x1.51f848p-27f},
-    {0x1.a0c668p+0f, -0x1.2886a6p-26f}, {0x1.a5503cp+0f, -0x1.b83b54p-25f}, {0x1.a9e6b6p+0f, -0x1.50c048p-25f},
-    {0x1.ae89fap+0f, -0x1.a94b14p-26f}, {0x1.b33a2cp+0f, -0x1.ec3a82p-26f}, {0x1.b7f770p+0f, -0x1.a09438p-25f},
-    {0x1.bcc1eap+0f, -0x1.f687c6p-25f}, {0x1.c199bep+0f, -0x1.3d56b2p-27f}, {0x1.c67f12p+0f, 0x1.cafa2ap-25f},
-    {0x1.cb720ep+0f, -0x1.8837ccp-27f}, {0x1.d072d4p+0f, 0x1.40f130p-25f}, {0x1.d5818ep+0f, -0x1.822dbcp-27f},
-    {0x1.da9e60p+0f, 0x1.ed9942p-27f}, {0x1.dfc974p+0f, -0x1.908c94p-25f}, {0x1.e502eep+0f, 0x1.e2cffep-26f},
-    {0x1.ea4afap+0f, 0x1.52486cp-27f}, {0x1.efa1bep+0f, 0x1.cc2b44p-25f}, {0x1.f50766p+0f, -0x1.246eb0p-26f},
-    {0x1.fa7c18p+0f, 0x1.9e90d8p-28f}};
+// 2^(j/128) as the sum of two floats, to 2^-49.
+constexpr int kSteps = 128;
+__device__ const float2 kPow2Steps[kSteps] = {
+    {0x1.000000p+0f, 0x0p+0f}, {0x1.0163dap+0f, 0x1.3f6666p-25f}, {0x1.02c9a4p+0f, -0x1.887fa0p-28f},
+    {0x1.04315ep+0f, 0x1.0dcff0p-25f}, {0x1.059b0ep+0f, -0x1.9d4f52p-25f}, {0x1.0706b2p+0f, 0x1.3bbedcp-25f},
+    {0x1.087452p+0f, -0x1.e2990ep-26f}, {0x1.09e3ecp+0f, 0x1.58de70p-25f}, {0x1.0b5586p+0f, 0x1.9f3122p-25f},
+    {0x1.0cc922p+0f, 0x1.6e48fep-25f}, {0x1.0e3ec4p+0f, -0x1.a585ccp-25f}, {0x1.0fb66ap+0f, 0x1.ffda64p-25f},
+    {0x1.11301ep+0f, -0x1.fdb496p-25f}, {0x1.12abdcp+0f, 0x1.b0c730p-30f}, {0x1.1429aap+0f, 0x1.d525bcp-25f},
+    {0x1.15a98cp+0f, 0x1.14b1cap-25f}, {0x1.172b84p+0f, -0x1.c15742p-27f}, {0x1.18af94p+0f, -0x1.dcdc86p-26f},
+    {0x1.1a35bep+0f, 0x1.6df96ep-25f}, {0x1.1bbe08p+0f, 0x1.011734p-26f}, {0x1.1d4874p+0f, -0x1.d2e8cap-25f},
+    {0x1.1ed502p+0f, 0x1.7e6c8ep-27f}, {0x1.2063b8p+0f, 0x1.0c519ap-25f}, {0x1.21f49ap+0f, -0x1.d0446ep-25f},
+    {0x1.2387a6p+0f, 0x1.ceac48p-25f}, {0x1.251ce4p+0f, 0x1.f654c8p-25f}, {0x1.26b456p+0f, 0x1.789f38p-26f},
+    {0x1.284dfep+0f, 0x1.f56380p-28f}, {0x1.29e9e0p+0f, -0x1.5c0424p-25f}, {0x1.2b87fep+0f, -0x1.e4a4cep-25f},
+    {0x1.2d285ap+0f, 0x1.b900c2p-26f}, {0x1.2ecafap+0f, 0x1.27c5eap-25f}, {0x1.306fe0p+0f, 0x1.4636e2p-25f},
+    {0x1.321710p+0f, -0x1.d993e8p-27f}, {0x1.33c08cp+0f, -0x1.b37d20p-25f}, {0x1.356c56p+0f, -0x1.b5803cp-30f},
+    {0x1.371a74p+0f, -0x1.18aac6p-25f}, {0x1.38cae6p+0f, 0x1.a0bb0cp-25f}, {0x1.3a7db4p+0f, -0x1.634c02p-25f},
+    {0x1.3c32dcp+0f, 0x1.89d472p-27f}, {0x1.3dea64p+0f, 0x1.824684p-25f}, {0x1.3fa450p+0f, 0x1.2b2006p-26f},
+    {0x1.4160a2p+0f, 0x1.f72e2ap-28f}, {0x1.431f5ep+0f, -0x1.abd5dap-26f}, {0x1.44e086p+0f, 0x1.8624b4p-30f},
+    {0x1.46a41ep+0f, 0x1.a3a00ap-25f}, {0x1.486a2cp+0f, -0x1.47d866p-25f}, {0x1.4a32b0p+0f, -0x1.e50584p-25f},
+    {0x1.4bfdaep+0f, -0x1.593abcp-25f}, {0x1.4dcb2ap+0f, -0x1.8088bcp-26f}, {0x1.4f9b28p+0f, -0x1.2c5a6cp-25f},
+    {0x1.516daap+0f, 0x1.67b320p-27f}, {0x1.5342b6p+0f, -0x1.2c5610p-25f}, {0x1.551a4cp+0f, 0x1.4bb242p-25f},
+    {0x1.56f474p+0f, -0x1.295b04p-25f}, {0x1.58d12ep+0f, -0x1.6d0700p-25f}, {0x1.5ab07ep+0f, -0x1.5bd5ecp-27f},
+    {0x1.5c9268p+0f, 0x1.4b28d6p-25f}, {0x1.5e76f2p+0f, -0x1.4a5bd6p-25f}, {0x1.605e1cp+0f, -0x1.a248fep-26f},
+    {0x1.6247ecp+0f, -0x1.f8b550p-25f}, {0x1.643464p+0f, -0x1.66679cp-25f}, {0x1.662388p+0f, 0x1.2a9112p-27f},
+    {0x1.68155ep+0f, -0x1.766ad2p-25f}, {0x1.6a09e6p+0f, 0x1.9fcef4p-26f}, {0x1.6c0128p+0f, -0x1.5e84a8p-25f},
+    {0x1.6dfb24p+0f, -0x1.cd72e8p-27f}, {0x1.6ff7e0p+0f, -0x1.ab9ae0p-26f}, {0x1.71f75ep+0f, 0x1.1d8beep-25f},
+    {0x1.73f9a4p+0f, 0x1.14b02ep-25f}, {0x1.75feb6p+0f, -0x1.37b306p-25f}, {0x1.780694p+0f, 0x1.fbcba8p-25f},
+    {0x1.7a1148p+0f, -0x1.829fd0p-25f}, {0x1.7c1ed0p+0f, 0x1.30c132p-28f}, {0x1.7e2f34p+0f, -0x1.261634p-25f},
+    {0x1.804276p+0f, -0x1.783cbep-25f}, {0x1.82589ap+0f, -0x1.accc7cp-26f}, {0x1.8471a4p+0f, 0x1.88f1ecp-26f},
+    {0x1.868d9ap+0f, -0x1.2edb44p-26f}, {0x1.88ac7ep+0f, -0x1.9d665ap-26f}, {0x1.8ace54p+0f, 0x1.15506ep-27f},
+    {0x1.8cf322p+0f, -0x1.29576ep-25f}, {0x1.8f1aeap+0f, -0x1.baa232p-26f}, {0x1.9145b0p+0f, 0x1.723ff8p-25f},
+    {0x1.93737cp+0f, -0x1.e64744p-25f}, {0x1.95a44cp+0f, 0x1.790a42p-25f}, {0x1.97d82ap+0f, -0x1.0d8d84p-31f},
+    {0x1.9a0f18p+0f, -0x1.e6bf08p-25f}, {0x1.9c4918p+0f, 0x1.51f848p-27f}, {0x1.9e8632p+0f, -0x1.873738p-26f},
+    {0x1.a0c668p+0f, -0x1.2886a6p-26f}, {0x1.a309bep+0f, 0x1.8945a6p-25f}, {0x1.a5503cp+0f, -0x1.b83b54p-25f},
+    {0x1.a799e2p+0f, -0x1.99e994p-25f}, {0x1.a9e6b6p+0f, -0x1.50c048p-25f}, {0x1.ac36bcp+0f, -0x1.606432p-31f},
+    {0x1.ae89fap+0f, -0x1.a94b14p-26f}, {0x1.b0e072p+0f, 0x1.31b6ccp-25f}, {0x1.b33a2cp+0f, -0x1.ec3a82p-26f},
+    {0x1.b59728p+0f, 0x1.bcab28p-25f}, {0x1.b7f770p+0f, -0x1.a09438p-25f}, {0x1.ba5b04p+0f, -0x1.ebdf36p-25f},
+    {0x1.bcc1eap+0f, -0x1.f687c6p-25f}, {0x1.bf2c26p+0f, -0x1.0a387ep-26f}, {0x1.c199bep+0f, -0x1.3d56b2p-27f},
+    {0x1.c40ab6p+0f, -0x1.7c2c98p-39f}, {0x1.c67f12p+0f, 0x1.cafa2ap-25f}, {0x1.c8f6dap+0f, -0x1.7f230ap-25f},
+    {0x1.cb720ep+0f, -0x1.8837ccp-27f}, {0x1.cdf0b6p+0f, -0x1.544780p-25f}, {0x1.d072d4p+0f, 0x1.40f130p-25f},
+    {0x1.d2f870p+0f, 0x1.01b13ep-25f}, {0x1.d5818ep+0f, -0x1.822dbcp-27f}, {0x1.d80e32p+0f, -0x1.26cf8ep-25f},
+    {0x1.da9e60p+0f, 0x1.ed9942p-27f}, {0x1.dd3220p+0f, -0x1.9fc974p-25f}, {0x1.dfc974p+0f, -0x1.908c94p-25f},
+    {0x1.e26462p+0f, -0x1.614bdap-25f}, {0x1.e502eep+0f, 0x1.e2cffep-26f}, {0x1.e7a520p+0f, -0x1.0e2ce0p-26f},
+    {0x1.ea4afap+0f, 0x1.52486cp-27f}, {0x1.ecf482p+0f, 0x1.b1ccfep-25f}, {0x1.efa1bep+0f, 0x1.cc2b44p-25f},
+    {0x1.f252b4p+0f, -0x1.1288aep-25f}, {0x1.f50766p+0f, -0x1.246eb0p-26f}, {0x1.f7bfdap+0f, 0x1.b397c2p-25f},
+    {0x1.fa7c18p+0f, 0x1.9e90d8p-28f}, {0x1.fd3c22p+0f, 0x1.71ee3ep-25f}};
 
 // What turns a row's logits into weights: t = (l_max - l) c, c = log2(e)/T.
 struct RowScale {
@@ -70,10 +92,17 @@ __device__ __forceinline__ void exponent_of(const RowScale& s, float l, float& t
     tl = fmaf(dl, s.ch, tl);
 }
 
-// 2^-t as u 2^(-43 - down), 2^43 <= u < 2^44, within 2^-39 of itself; down = 64 from t = 60 on.
-//   -t = k/64 + r,  |r| <= 1/128:  2^-t = 2^floor(k/64) * 2^((k mod 64)/64) * (1 + y),
-//   y = e^z - 1 for z = r ln 2 as z + z^2/2 + z^3/6 + z^4/24, |z| < 2^-7.5, its first
-// term in two floats; the terms behind it are below 2^-16 and take one (2^-40).
+// 2^-t as u 2^(-43 - down), 0.997 * 2^43 <= u < 2^44, within 2^-39 of itself up to t = 32 (of
+// what lies beyond, rounding to 2^-43 leaves eleven bits at most); down = 64 from t = 60 on.  A
+// table and a polynomial, after P. T. P. Tang, "Table-driven implementation of the exponential
+// function in IEEE floating-point arithmetic", ACM TOMS 15 (1989):
+//   -t = k/128 + r,  |r| <= 1/256:  2^-t = 2^floor(k/128) * 2^((k mod 128)/128) * e^z,
+//   z = r ln 2 = zh + zl, |zh| < 2^-8.5, |zl| < 2^-19 up to t = 32,
+//   e^z - 1 = zh + q + zl (1 + zh + q + zl/2),  q = zh^2/2 + zh^3/6 + zh^4/24 < 2^-18.
+// What rounds, in units of 2^-42 of the weight: q twice 0.5; what is added to it 1, and its factor 0.9;
+// their product with the table's value 1.4, and the sum with what zh's leaves 1.4; t's lower part 0.9,
+// zl's 0.25, the last bit 0.25: 7.1 in all, 8 being 2^-39.  (With 64 steps the parts behind zh are four
+// times as large: 2^-37.4 at worst.)  The worst of 300 million is 2^-39.9.
 __device__ __forceinline__ unsigned long long weight_parts(const RowScale& s, const float2* pow2, float l,
                                                            int& down) {
     float th, tl;
@@ -83,20 +112,20 @@ __device__ __forceinline__ unsigned long long weight_parts(const RowScale& s, co
         return 0;
     constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: adding it rounds to an integer
     constexpr float kLn2h = 0.693147182464599609375f, kLn2l = -1.9046542121259336e-9f;
-    const float m = fmaf(th, -64.0f, kMagic);
+    const float m = fmaf(th, -128.0f, kMagic);
     const int k = __float_as_int(m) - __float_as_int(kMagic);
-    const float r = fmaf(m - kMagic, -0.015625f, -th);  // exact
+    const float r = fmaf(m - kMagic, -0.0078125f, -th);  // exact
     const float zh = r * kLn2h;
     float zl = fmaf(r, kLn2h, -zh);
     zl = fmaf(r, kLn2l, zl);
     zl = fmaf(tl, -kLn2h, zl);
-    const float z = zh + zl;
-    const float q = z * z * fmaf(z, fmaf(z, 1.0f / 24.0f, 1.0f / 6.0f), 0.5f);
-    const float2 p = pow2[k & 63];
+    const float half = zh * (0.5f * zh);
+    const float q = fmaf(half, zh * fmaf(zh, 1.0f / 12.0f, 1.0f / 3.0f), half);
+    const float2 p = pow2[k & (kSteps - 1)];
     const float ah = p.x * zh;
-    float b = fmaf(p.x, zh, -ah);
-    b = fmaf(p.x, zl + q, b);
-    b = fmaf(p.y, zh, b) + p.y;
+    const float small = fmaf(p.x, zh, -ah) + fmaf(p.y, zh, p.y);  // below 2^-24
+    const float slope = (1.0f + zh) + fmaf(0.5f, zl, q);
+    const float b = fmaf(p.x, fmaf(zl, slope, q), small);
     const float v = p.x + ah;               // p.x >= 1 > |ah|
     const float e = (ah - (v - p.x)) + b;
     // v + e in units of 2^-43: the multiple of 2^-21 from the bits of v + 4, what is left
@@ -105,7 +134,7 @@ __device__ __forceinline__ unsigned long long weight_parts(const RowScale& s, co
     const float left = e + (v - (v4 - 4.0f));
     constexpr float kMagicLow = 1.430511474609375e-6f;  // 1.5 * 2^-20
     const int low = __float_as_int(left + kMagicLow) - __float_as_int(kMagicLow);
-    down = -(k >> 6);  // >= 0
+    down = -(k >> 7);  // >= 0
     return ((unsigned long long)(uint32_t)(__float_as_int(v4) - __float_as_int(4.0f)) << 22) + (long long)low;
 }
 
@@ -176,13 +205,21 @@ __device__ __forceinline__ unsigned long long ceil_scaled(double p, unsigned lon
 // M = l_max c, without the difference l_max - l.
 //   M = Mk/128 + Mr, |Mr| <= 1/256;  p = k/128 + r + Mr, |r| <= 1/256, p - k/128 exact;
 //   2^(p - M) = 2^floor((k - Mk)/128) T[(k - Mk) mod 128] (1 + y),  y = e^z - 1 in one float.
-// y rounds at 2^-33 to either side, which a sum of many entries does not show (the
-// lists' entries, few, take weight_fixed).  T in two floats, a copy for each of 16 lanes,
+// y rounds at 2^-33 to either side, three times, and with ln 2 a weight is 2^-30.6 off at most:
+// a sum of many entries does not show it (the lists' entries, few, take weight_fixed).  T in two floats, a copy for each of 16 lanes,
 // so that lanes' reads do not meet in a bank.  For |M| < 128.
 struct SumScale {
     float ch, cl, floor_l, mh, ml;  // mh + ml: Mr
     int k0;                         // Mk
     const float2* steps;
+
+    __device__ __forceinline__ explicit SumScale(const RowScale& s) : ch(s.ch), cl(s.cl), floor_l(s.lmax - 70.0f / s.ch) {
+        const float m = s.lmax * s.ch, l = fmaf(s.lmax, s.ch, -m) + s.lmax * s.cl, k = rintf(m * 128.0f);
+        const float rest = fmaf(k, -0.0078125f, m);  // exact
+        mh = rest + l;
+        ml = l - (mh - rest);
+        k0 = (int)k;
+    }
 };
 // the weight as the table's part and the rest
 __device__ __forceinline__ float2 sum_weight(const SumScale& s, float l) {

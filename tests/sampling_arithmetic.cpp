@@ -78,7 +78,65 @@ static void shares() {
     std::printf("shares_off %llu\nzero_share %llu\n", (unsigned long long)off, (unsigned long long)zero);
 }
 
+// a row's scale at an ordinary temperature, a logit of it, and the logit's weight
+struct Sample {
+    RowScale s;
+    float l;
+    long double w;
+    Sample() {
+        std::normal_distribution<double> normal;
+        const float T = (float)(0.2 + 1.4 * (double)(gen() >> 11) * 0x1p-53);
+        s.lmax = (float)(10.0 + 3.0 * normal(gen));
+        s.fix = kMaxFix;
+        split_scale(T, s.ch, s.cl);
+        l = s.lmax - (float)std::fabs(normal(gen)) * 9.0f * T;
+        w = std::exp(((long double)l - (long double)s.lmax) / (long double)T);
+    }
+};
+
+// how far a weight is off, as a share of itself, and the range of its 44 bits
+static void weights() {
+    long double worst = 0, least = 2, most = 0;
+    for (int i = 0; i < 4000000; ++i) {
+        const Sample x;
+        int down;
+        const unsigned long long u = weight_parts(x.s, kPow2Steps, x.l, down);
+        if (down > kMaxFix)
+            continue;
+        worst = max(worst, std::fabs(std::ldexp((long double)u, -kMaxFix - down) / x.w - 1));
+        least = min(least, std::ldexp((long double)u, -kMaxFix));
+        most = max(most, std::ldexp((long double)u, -kMaxFix));
+    }
+    std::printf("weight_off %.9Lg\nleast_parts %.9Lg\nmost_parts %.9Lg\n", worst, least, most);
+}
+
+// how far a sum of four equal weights is off, as a share of itself: all errors agree
+static void sums() {
+    static float2 steps[kSteps * 16];
+    long double worst = 0;
+    const Units units(kMaxFix);
+    for (int j = 0; j < kSteps * 16; ++j)
+        steps[j] = kPow2Steps[j >> 4];
+    for (int i = 0; i < 4000000; ++i) {
+        const Sample x;
+        if (!(std::fabs(x.s.lmax * x.s.ch) < 128.0f) || x.w < 0x1p-10L)  // small ones' share is their units'
+            continue;
+        SumScale t(x.s);
+        t.steps = steps + (i & 15);
+        WeightSum sum;
+        unsigned long long n = 0;
+        for (int j = 0; j < 4; ++j)
+            sum.add(sum_weight(t, x.l));
+        sum.into(n, units);
+        n += sum.rest(kMaxFix);
+        worst = max(worst, std::fabs(std::ldexp((long double)n, -kMaxFix - 2) / x.w - 1));
+    }
+    std::printf("sum_off %.9Lg\n", worst);
+}
+
 int main() {
+    weights();
+    sums();
     shares();
     return 0;
 }

@@ -21,3 +21,14 @@ def test_shares_of_a_mass_are_exact(figures):
     """floor(u x) and ceil(p x) have no rounding before the last step; a uniform of -0 is 0."""
     assert figures["zero_share"] == 0
     assert figures["shares_off"] == 0
+
+
+def test_weights_keep_their_bound(figures):
+    """A weight is off by 2^-39 of itself and half a unit of 2^-43, which is not in `weight_off`."""
+    assert figures["weight_off"] <= 2.0 ** -39
+    assert 0.997 <= figures["least_parts"] and figures["most_parts"] < 2
+
+
+def test_sums_of_weights_keep_their_bound(figures):
+    """2^-30 of themselves, where a table's part and three roundings of 2^-33 all agree."""
+    assert figures["sum_off"] <= 2.0 ** -30
