@@ -74,7 +74,15 @@ __device__ __forceinline__ unsigned long long order_of(float l, uint32_t id) {
     return ((unsigned long long)logit_key(l) << 32) | (uint32_t)~id;
 }
 
-template <int ES>
+// x - y, or at temperatures from kFarT on (x - y) kShrink
+template <bool Far>
+__device__ __forceinline__ float apart(float x, float y) {
+    return Far ? x * kShrink - y * kShrink : x - y;
+}
+
+// `Far`: T from kFarT on, where logits may lie further apart than a float holds.  a.T and a.ch
+// are those of the smaller logits then.
+template <int ES, bool Far>
 __global__ void __launch_bounds__(kNT, 4) sv_logprobs_kernel(const __grid_constant__ Args a) {
     __shared__ Shared sh;
     cg::cluster_group cluster = cg::this_cluster();
@@ -119,7 +127,17 @@ __global__ void __launch_bounds__(kNT, 4) sv_logprobs_kernel(const __grid_consta
     // the pass over the slice
     float m = -inf, s = 0.0f;
     uint32_t above = 0;
-    const auto grow = [&](float top) { join_sums(m, s, top, 0.0f, a.ch); };
+    const auto merge = [&](float& m0, float& s0, float m1, float s1) {
+        if constexpr (Far) {
+            const float grown = max_nan(m0, m1);
+            s0 = (m0 > -inf ? s0 * ex2_approx(apart<true>(m0, grown) * a.ch) : 0.0f) +
+                 (m1 > -inf ? s1 * ex2_approx(apart<true>(m1, grown) * a.ch) : 0.0f);
+            m0 = grown;
+        } else {
+            join_sums(m0, s0, m1, s1, a.ch);
+        }
+    };
+    const auto grow = [&](float top) { merge(m, s, top, 0.0f); };
     StepCodes codes;
     const int shift = v.code_shift();
     if (shift) {  // else every step has a code of its own
@@ -139,8 +157,15 @@ __global__ void __launch_bounds__(kNT, 4) sv_logprobs_kernel(const __grid_consta
                 for (int e = 0; e < E; ++e)
                     above += vector_entry<ES>(w, e) > lx;
             }
-            if (top > -inf)  // else m may be -inf too
-                s += exp_sum<ES>(w, m, a.ch);
+            if (top > -inf) {  // else m may be -inf too
+                if constexpr (Far) {
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        s += ex2_approx(apart<true>(vector_entry<ES>(w, e), m) * a.ch);
+                } else {
+                    s += exp_sum<ES>(w, m, a.ch);
+                }
+            }
         },
         [&](uint32_t i) {
             const uint8_t x = (uint8_t)step_code(step);
@@ -154,12 +179,11 @@ __global__ void __launch_bounds__(kNT, 4) sv_logprobs_kernel(const __grid_consta
             if (!(l <= m))
                 grow(l);
             if (l > -inf)
-                s += ex2_approx((l - m) * a.ch);
+                s += ex2_approx(apart<Far>(l, m) * a.ch);
         });
     const float mine = m;
 
     // join the threads, then the CTAs
-    const auto merge = [&](float& m0, float& s0, float m1, float s1) { join_sums(m0, s0, m1, s1, a.ch); };
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
         const float m1 = __shfl_xor_sync(kAllLanes, m, o), s1_ = __shfl_xor_sync(kAllLanes, s, o);
@@ -274,8 +298,8 @@ __global__ void __launch_bounds__(kNT, 4) sv_logprobs_kernel(const __grid_consta
     }
     const float ls = logf(s);
     const auto value = [&](float l) {
-        const float d = l - m;
-        return fmaf(d, 1.0f / a.T, -ls);
+        // by halves: l - m may be no float where (l - m) / T is one
+        return Far ? fmaf(apart<true>(l, m), 1.0f / a.T, -ls) : fmaf(0.5f * l - 0.5f * m, 2.0f / a.T, -ls);
     };
     if (tid == 0) {
         a.logprob[row] = value(lx);
@@ -312,7 +336,8 @@ __global__ void __launch_bounds__(kNT, 4) sv_logprobs_kernel(const __grid_consta
 namespace sv {
 
 bool logprobs_setup() {
-    for (const void* fn : {(const void*)sv_logprobs_kernel<2>, (const void*)sv_logprobs_kernel<4>})
+    for (const void* fn : {(const void*)sv_logprobs_kernel<2, false>, (const void*)sv_logprobs_kernel<4, false>,
+                           (const void*)sv_logprobs_kernel<2, true>, (const void*)sv_logprobs_kernel<4, true>})
         if (cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
             cudaSuccess) {
             (void)cudaGetLastError();
@@ -375,8 +400,9 @@ int spec_logprobs_run(sv_ctx* ctx, const void* target_logits, int logits_dtype,
     a.rows_per_seq = rows_per_seq;
     a.C = plan.cluster;
     a.top_n = top_n;
-    a.T = temperature;
-    a.ch = (float)(1.4426950408889634074 / (double)temperature);
+    const bool far = temperature >= kFarT;
+    a.T = far ? temperature * kShrink : temperature;
+    a.ch = (float)(1.4426950408889634074 / (double)a.T);
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof cfg);
     cfg.gridDim = dim3((unsigned)plan.grid, 1, 1);
@@ -390,8 +416,9 @@ int spec_logprobs_run(sv_ctx* ctx, const void* target_logits, int logits_dtype,
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     DeviceGuard guard(ctx->device);
-    if (cudaLaunchKernelEx(&cfg, es == 2 ? sv_logprobs_kernel<2> : sv_logprobs_kernel<4>, a) !=
-        cudaSuccess) {
+    const auto kernel = far ? (es == 2 ? sv_logprobs_kernel<2, true> : sv_logprobs_kernel<4, true>)
+                            : (es == 2 ? sv_logprobs_kernel<2, false> : sv_logprobs_kernel<4, false>);
+    if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) {
         (void)cudaGetLastError();
         return SV_ERR_CUDA;
     }

@@ -852,7 +852,7 @@ __device__ __noinline__ bool count_places(Shared* sh, StepCodes* codes) {
     scale.fix = sh->args.fix;
     scale.lmax = key_logit(key);
     const float T = sh->T;
-    split_scale(T > 0.0f ? T : 1.0f, scale.ch, scale.cl);
+    set_temperature(scale, T > 0.0f ? T : 1.0f);
     if (tid == 0)
         sh->scale = scale;
     if (ES == 4 && tid < 32 && sh->top_p < 1.0) {
@@ -868,7 +868,7 @@ __device__ __noinline__ bool count_places(Shared* sh, StepCodes* codes) {
     if (T == 0.0f)
         return ES == 2;
     // logits from -127 down must weigh nothing
-    if (!((scale.lmax + 127.0f) * scale.ch >= 61.0f))
+    if (scale.g != 1.0f || !((scale.lmax + 127.0f) * scale.ch >= 61.0f))
         return false;
     // bfloat16 logits below the window are taken for 0: their weights are off by
     // 2^-24/T of themselves, which must not show in the sum (>= 1 at l_max) at 2^-39

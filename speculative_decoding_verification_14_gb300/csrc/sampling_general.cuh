@@ -24,11 +24,12 @@ struct General {
     __device__ __forceinline__ explicit General(Shared* s)
         : sh(s), v(s), tid(threadIdx.x), lane(tid & 31), warp(tid >> 5), rank(cta_rank()), C(s->args.C) {
         scale.fix = s->args.fix;
+        scale.g = 1.0f;
     }
 
     // the linear bin of a logit; larger logits, smaller bins
     __device__ __forceinline__ int bin_of(float l) const {
-        const float t = (scale.lmax - l) * scale.ch * kBinsPerOctave;
+        const float t = (scale.lmax * scale.g - l * scale.g) * scale.ch * kBinsPerOctave;
         return t < (float)(kBins - 1) ? (int)t : kBins - 1;
     }
 
@@ -313,7 +314,7 @@ struct General {
             the_cluster().sync();
             return;
         }
-        split_scale(T, scale.ch, scale.cl);
+        set_temperature(scale, T);
         if (tid == 0)
             sh->scale = scale;  // read behind the next barrier
 

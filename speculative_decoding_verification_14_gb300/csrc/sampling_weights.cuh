@@ -73,19 +73,26 @@ __device__ const float2 kPow2Steps[kSteps] = {
     {0x1.f252b4p+0f, -0x1.1288aep-25f}, {0x1.f50766p+0f, -0x1.246eb0p-26f}, {0x1.f7bfdap+0f, 0x1.b397c2p-25f},
     {0x1.fa7c18p+0f, 0x1.9e90d8p-28f}, {0x1.fd3c22p+0f, 0x1.71ee3ep-25f}};
 
-// What turns a row's logits into weights: t = (l_max - l) c, c = log2(e)/T.
+// What turns a row's logits into weights: t = (l_max g - l g) c, c = log2(e)/(T g).
 struct RowScale {
     float lmax;
     float ch, cl;  // c as the sum of two floats
+    float g;       // 1; kShrink from T = kFarT on
     int fix;       // F
 };
+
+// At temperatures that weigh differences of 2^127 and more, logits and T are both taken smaller: the
+// difference is a float then, and c a normal one.  What a logit below 2^-62 loses is nothing over such a T.
+constexpr float kFarT = 0x1p100f, kShrink = 0x1p-64f;
 
 // t as the sum of two floats; t >= 0, +inf for l = -inf.  The difference
 // l_max - l is taken with its rounding error, so t is good to 2^-45 of itself.
 __device__ __forceinline__ void exponent_of(const RowScale& s, float l, float& th, float& tl) {
-    const float d = s.lmax - l;
-    const float bv = d - s.lmax;
-    const float dl = (s.lmax - (d - bv)) - (l + bv);
+    const float m = s.lmax * s.g;
+    l *= s.g;
+    const float d = m - l;
+    const float bv = d - m;
+    const float dl = (m - (d - bv)) - (l + bv);
     th = d * s.ch;
     tl = fmaf(d, s.ch, -th);
     tl = fmaf(d, s.cl, tl);
@@ -158,11 +165,13 @@ __device__ __forceinline__ unsigned long long mass_fixed(const RowScale& s, cons
     return rounded_shift(rounded_shift(u, kMaxFix - s.fix) * n, down);
 }
 
-// c = log2(e)/T as the sum of two floats
-__device__ __forceinline__ void split_scale(float T, float& ch, float& cl) {
+// g and c of a temperature
+__device__ __forceinline__ void set_temperature(RowScale& s, float T) {
     constexpr float kLog2eh = 1.44269502162933349609375f, kLog2el = 1.9259629911266174e-8f;
-    ch = __fdiv_rn(kLog2eh, T);
-    cl = __fdiv_rn(fmaf(-ch, T, kLog2eh) + kLog2el, T);
+    s.g = T < kFarT ? 1.0f : kShrink;
+    T *= s.g;
+    s.ch = __fdiv_rn(kLog2eh, T);
+    s.cl = __fdiv_rn(fmaf(-s.ch, T, kLog2eh) + kLog2el, T);
 }
 
 // floor(u x) and ceil(p x) with no rounding before the last step.
@@ -201,7 +210,7 @@ __device__ __forceinline__ unsigned long long ceil_scaled(double p, unsigned lon
 
 // ---------------------------------------------------- sums of weights -----
 
-// A weight for sums, in half the instructions of weight_fixed: 2^(p - M), p = l c,
+// A weight for sums, in half the instructions of weight_fixed, below kFarT: 2^(p - M), p = l c,
 // M = l_max c, without the difference l_max - l.
 //   M = Mk/128 + Mr, |Mr| <= 1/256;  p = k/128 + r + Mr, |r| <= 1/256, p - k/128 exact;
 //   2^(p - M) = 2^floor((k - Mk)/128) T[(k - Mk) mod 128] (1 + y),  y = e^z - 1 in one float.

@@ -88,7 +88,7 @@ struct Sample {
         const float T = (float)(0.2 + 1.4 * (double)(gen() >> 11) * 0x1p-53);
         s.lmax = (float)(10.0 + 3.0 * normal(gen));
         s.fix = kMaxFix;
-        split_scale(T, s.ch, s.cl);
+        set_temperature(s, T);
         l = s.lmax - (float)std::fabs(normal(gen)) * 9.0f * T;
         w = std::exp(((long double)l - (long double)s.lmax) / (long double)T);
     }

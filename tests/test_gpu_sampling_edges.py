@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 
 from tests import gpu_helpers as gh
-from tests.test_gpu_sampling import OFF, SETTINGS, _tensor, check_rows, rows_of
+from tests.test_gpu_sampling import OFF, SETTINGS, _tensor, check_logprobs, check_rows, rows_of
 
 pytestmark = pytest.mark.gpu
 
@@ -26,7 +26,7 @@ def test_a_uniform_of_minus_zero_is_zero(dtype):
         check_rows(lg, s, (-u).cpu().numpy(), {k: t.cpu().numpy() for k, t in got.items()})
 
 
-def general_rows(lg, settings, u=None):
+def general_rows(lg, settings, u=None, limit=0.02):
     """How many rows of a draw, and of a filter, go the general way; their answers are checked."""
     import torch
     v = gh.verifier()
@@ -42,7 +42,7 @@ def general_rows(lg, settings, u=None):
         v.set_sample_telemetry(None)
     v.sample(lg, u, **settings)  # not counted
     check_rows(lg, settings, u.cpu().numpy(), {k: t.cpu().numpy() for k, t in got.items()},
-               {k: t.double().cpu().numpy() if t.is_floating_point() else t.cpu().numpy() for k, t in fil.items()})
+               {k: t.double().cpu().numpy() if t.is_floating_point() else t.cpu().numpy() for k, t in fil.items()}, limit)
     return n.tolist()
 
 
@@ -130,3 +130,22 @@ def test_deviations_beyond_what_a_float_holds():
     """At T = 1e-30 the square of a place's width over T is no float."""
     lg = _tensor(rows_of(4, 1, 3000, 5), "f32")
     assert general_rows(lg, {**OFF, "temperature": 1e-30, "top_p": 0.9}) == [0, 0]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1e29, 3e36, 1e38, 3.4e38])
+def test_logits_further_apart_than_a_float_holds(T, dtype):
+    """Finite logits whose difference is none, at temperatures that weigh it.  The weights of row 3's
+    ordinary logits are all 1 there, and 0.7 of 2000 end with an entry: of the 12 rows its two are at a
+    border, which is the limit."""
+    import torch
+    rng = np.random.default_rng(4)
+    x = 3.3e38 * rng.uniform(-1, 1, (6, 2, 2000))
+    x[2] = np.where(rng.random((2, 2000)) < 0.5, 3.3e38, -3.3e38)
+    x[3] = rows_of(1, 2, 2000, 3)[0]
+    x[4, :, 5] = -np.inf
+    lg = _tensor(x, dtype)
+    for s in ({}, {"top_p": 0.7}, {"min_p": 0.4}, {"top_k": 30}, {"top_k": 700, "top_p": 0.5, "min_p": 0.2}):
+        general_rows(lg, {**OFF, "temperature": T, **s}, torch.rand(6, 2, device="cuda"), 2 / 12)
+    t = torch.randint(0, 2000, (6, 2), device="cuda", dtype=torch.int32)
+    check_logprobs(lg, t, None, T, 5, gh.verifier().logprobs(lg, t, temperature=T, top_n=5))
