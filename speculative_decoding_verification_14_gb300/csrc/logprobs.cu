@@ -110,12 +110,15 @@ __global__ void __launch_bounds__(kNT, 4) sv_logprobs_kernel(const __grid_consta
         }
     };
     const int32_t x = a.tokens[row];  // both loads at once
-    if (a.accept_len && row - seq * a.rows_per_seq >= a.accept_len[seq]) {
-        leave(SV_OK);
-        return;
-    }
-    if (x < 0 || x >= a.V) {
-        leave(SV_ERR_TOKEN_RANGE);
+    const bool dead = a.accept_len && row - seq * a.rows_per_seq >= a.accept_len[seq];
+    if (dead || x < 0 || x >= a.V) {
+        leave(dead ? SV_OK : SV_ERR_TOKEN_RANGE);
+        // where a program changes these under the call, CTAs of a row may differ: none leaves while
+        // another may still write into it
+        if (C > 1) {
+            cluster.sync();
+            cluster.sync();
+        }
         return;
     }
     const unsigned char* base = static_cast<const unsigned char*>(a.logits) + row * a.stride * ES;

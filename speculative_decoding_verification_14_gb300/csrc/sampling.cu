@@ -126,8 +126,8 @@ __device__ __noinline__ uint32_t count_pass(Shared* sh, StepCodes* codes) {
     float lmax = __int_as_float(0xff800000);
     float step = lmax;           // float32: a step's largest
     // float32 under top-p: the row's sum, too, in floats
-    const bool sum = ES == 4 && sh->top_p < 1.0 && sh->T > 0.0f;
-    const float ch = __fdiv_rn(1.44269502162933349609375f, sum ? sh->T : 1.0f);
+    const bool sum = ES == 4 && sh->sum_T > 0.0f;
+    const float ch = __fdiv_rn(1.44269502162933349609375f, sum ? sh->sum_T : 1.0f);
     float m = lmax, t = 0.0f;
     uint32_t two = 0xff80ff80u;  // bfloat16: of each half
 #pragma unroll
@@ -453,9 +453,9 @@ __device__ __noinline__ int64_t find_entry(Shared* sh, const StepCodes* codes, i
         if (r < x.before_count || r >= x.before_count + mine)
             return -1;
         uint32_t left = (uint32_t)r - x.before_count, e = e0;
-        while (q[e] != bits || left-- != 0)
+        while (e < e1 && (q[e] != bits || left-- != 0))
             ++e;
-        return e;
+        return e < e1 ? (int64_t)e : -1;
     }
     if (n <= (uint32_t)kNT) {
         const uint32_t id = tid < n ? ids[tid] : 0;
@@ -695,8 +695,8 @@ __device__ __noinline__ void settle(Shared* sh, bool by_mass, bool summed, bool 
         if (!summed)
             sh->sums[0][0] = by_mass ? __float2ull_rn(sh->fast_sum * (float)(1ull << sh->scale.fix)) : 0;
         const unsigned long long whole = sh->sums[0][0];
-        sh->want = {sh->k, sh->want_limit, sh->band[0].above_count, logit_key(sh->band[0].lo),
-                    by_mass ? ceil_scaled(sh->top_p, whole) : 0, sh->sums[1][0],
+        sh->want = {sh->set.k, sh->want_limit, sh->band[0].above_count, logit_key(sh->band[0].lo),
+                    by_mass ? ceil_scaled(sh->set.top_p, whole) : 0, sh->sums[1][0],
                     summed ? 0 : whole >> fast_bits(sh)};
     }
     if (first && sh->band[0].on)
@@ -715,7 +715,7 @@ __device__ __noinline__ void settle(Shared* sh, bool by_mass, bool summed, bool 
                 sort_list(sh, 0);
             ok = cut_in_sorted(sh);
             if (ok == 1 && draw)
-                ok = draw_in_sorted(sh, 0, sh->want.above_mass, floor_scaled(sh->u, sh->kept_mass)) ? 1 : 3;
+                ok = draw_in_sorted(sh, 0, sh->want.above_mass, floor_scaled(sh->set.u, sh->kept_mass)) ? 1 : 3;
         }
     } else if (tid == 0) {
         sh->kept_mass = sh->sums[0][0];
@@ -733,7 +733,7 @@ __device__ __noinline__ void settle(Shared* sh, bool by_mass, bool summed, bool 
             ok = resolve_few(sh, 1, false, true);
         } else {
             sort_list(sh, 1);
-            ok = draw_in_sorted(sh, 1, sh->sums[2][0], floor_scaled(sh->u, sh->kept_mass)) ? 1 : 0;
+            ok = draw_in_sorted(sh, 1, sh->sums[2][0], floor_scaled(sh->set.u, sh->kept_mass)) ? 1 : 0;
         }
         ok = ok == 3 ? 0 : ok;
     }
@@ -836,9 +836,11 @@ __device__ __noinline__ bool count_places(Shared* sh, StepCodes* codes) {
         *peer(&sh->part_max[rank], tid) = key;
         *peer(&sh->part_tiny[rank], tid) = sh->count[kMags + 1] + sh->count[kMags + 2];
     }
-    if (ES == 4 && tid < 32 && sh->top_p < 1.0) {
+    if (rank == 0 && tid > 64 && tid < 64 + C)  // a warp that has nothing else to do
+        *peer(&sh->set, tid - 64) = sh->set;
+    if (ES == 4 && tid < 32 && sh->sum_T > 0.0f) {
         float m = sh->warp_top[tid & (kNW - 1)], t = sh->warp_noise[tid & (kNW - 1)];
-        join_lanes<kNW>(m, t, __fdiv_rn(1.44269502162933349609375f, sh->T));
+        join_lanes<kNW>(m, t, __fdiv_rn(1.44269502162933349609375f, sh->sum_T));
         if (tid < C) {
             *peer(&sh->part_top[rank], tid) = m;
             *peer(&sh->part_sum[rank], tid) = t;
@@ -851,11 +853,11 @@ __device__ __noinline__ bool count_places(Shared* sh, StepCodes* codes) {
     RowScale scale;
     scale.fix = sh->args.fix;
     scale.lmax = key_logit(key);
-    const float T = sh->T;
+    const float T = sh->set.T;
     set_temperature(scale, T > 0.0f ? T : 1.0f);
     if (tid == 0)
         sh->scale = scale;
-    if (ES == 4 && tid < 32 && sh->top_p < 1.0) {
+    if (ES == 4 && tid < 32 && sh->set.top_p < 1.0) {
         const bool in = lane < C;
         float m = in ? sh->part_top[lane] : __int_as_float(0xff800000), t = in ? sh->part_sum[lane] : 0.0f;
         join_lanes<kMaxC>(m, t, scale.ch);
@@ -863,7 +865,7 @@ __device__ __noinline__ bool count_places(Shared* sh, StepCodes* codes) {
             sh->fast_sum = t;
     }
     __syncthreads();
-    if (sh->code || key == 0xffffffffu || !inside(place_of(scale.lmax)))
+    if (sh->set.code || key == 0xffffffffu || !inside(place_of(scale.lmax)))
         return false;
     if (T == 0.0f)
         return ES == 2;
@@ -904,10 +906,10 @@ __device__ __noinline__ bool find_cut(Shared* sh) {
     const int lane = tid & 31;
     const unsigned long long whole = warp_sum(lane < C ? sh->part_mass[lane] : 0ull);
     const uint32_t near = __reduce_add_sync(kAllLanes, lane < C ? sh->part_cnt[lane] : 0u);
-    Wanted s = {sh->k, sh->top_p < 1.0 ? ceil_scaled(sh->top_p, whole) : 0, kNoPlace, false};
-    if (sh->has_min) {
+    Wanted s = {sh->set.k, sh->set.top_p < 1.0 ? ceil_scaled(sh->set.top_p, whole) : 0, kNoPlace, false};
+    if (sh->set.has_min) {
         // the smallest float l with l - l_max >= T ln(min_p); bfloat16: the smallest of those
-        float limit = __double2float_ru((double)sh->scale.lmax + sh->dmin);
+        float limit = __double2float_ru((double)sh->scale.lmax + sh->set.dmin);
         if (tid == 0)
             sh->want_limit = logit_key(limit);
         if (ES == 2 && limit > 0.0f && (__float_as_uint(limit) & 0xffffu))
@@ -938,7 +940,7 @@ __device__ __noinline__ bool find_cut(Shared* sh) {
     __syncthreads();
     if (sh->cut_at.bin == kNoPlace && (int64_t)sh->near < sh->args.V) {
         // everything is kept: those from -127 down that are not -inf as well
-        if (sh->k)
+        if (sh->set.k)
             return false;
         const uint32_t far = cluster_sum(sh, count_far<ES>(sh));
         if (tid == 0)
@@ -951,14 +953,14 @@ __device__ __noinline__ bool find_cut(Shared* sh) {
 // bfloat16: the drawn place, and which of its entries it is.
 __device__ __noinline__ bool draw_value(Shared* sh, const StepCodes* codes) {
     sh = here();
-    const Wanted w = {0, floor_scaled(sh->u, sh->mass), kNoPlace, true};
+    const Wanted w = {0, floor_scaled(sh->set.u, sh->mass), kNoPlace, true};
     const Found d = search_places<2>(sh, 1, w);
     if (is_tiny(d.bin))
         return false;
     const float l = place_value(d.bin);
     // of the place's entries, each with the same share of its mass; products below 2^62
     const int cut = max(34 - __clzll(d.mass) - __clz(d.count), 0);
-    const unsigned long long at = ((w.p - d.above_mass) >> cut) * d.count / (d.mass >> cut);
+    const unsigned long long at = ((w.p - d.above_mass) >> cut) * d.count / max(d.mass >> cut, 1ull);
     const int64_t id = find_entry(sh, codes, d.bin, min((uint32_t)at, d.count - 1));
     if (id >= 0)
         put_token(sh, (int32_t)id, weight_float(sh->scale, l) * inverse_mass(sh->scale, sh->mass));
@@ -969,7 +971,7 @@ __device__ __noinline__ bool draw_value(Shared* sh, const StepCodes* codes) {
 __device__ __noinline__ bool settle_exactly(Shared* sh, const StepCodes* codes) {
     sh = here();
     const int tid = threadIdx.x;
-    const bool by_mass = sh->top_p < 1.0, draw = sh->args.u != nullptr;
+    const bool by_mass = sh->set.top_p < 1.0, draw = sh->args.u != nullptr;
     // four standard deviations of the places' sum, and what their middles miss
     float noise = (tid & 15) < sh->args.C ? sh->part_noise[tid & 15] : 0.0f;
 #pragma unroll
@@ -983,7 +985,7 @@ __device__ __noinline__ bool settle_exactly(Shared* sh, const StepCodes* codes) 
             return false;
     }
     if (draw && !sh->band[0].from_top) {
-        const Wanted w = {0, floor_scaled(sh->u, sh->mass), kNoPlace, true};
+        const Wanted w = {0, floor_scaled(sh->set.u, sh->mass), kNoPlace, true};
         const Found h = search_places<4>(sh, 1, w);
         if (!sh->band[0].on || place_end(h.bin, true) > sh->band[0].hi) {
             band_around(sh, 1, h, margin);
@@ -1021,7 +1023,7 @@ __device__ __forceinline__ bool by_place(Shared* sh) {
     if (!count_places<ES>(sh, &codes))
         return false;
     if constexpr (ES == 2) {
-        if (sh->T == 0.0f) {
+        if (sh->set.T == 0.0f) {
             take_largest(sh, &codes);
             return true;
         }
@@ -1077,10 +1079,15 @@ __device__ __forceinline__ void set_up(Shared* sh, const Args& a) {
         sh->band[0] = sh->band[1] = {inf, inf, 0, false, false};
     } else if (tid == 32) {
         const int64_t seq = row / (uint32_t)a.rows_per_seq;
-        const int32_t k = a.set.top_ks ? a.set.top_ks[seq] : a.set.top_k;
-        sh->T = a.set.temperatures ? a.set.temperatures[seq] : a.set.temperature;
-        sh->k = k > 0 ? (uint32_t)k : 0;
-        sh->top_p = a.set.top_ps ? (double)a.set.top_ps[seq] : a.set.top_p;
+        const float T = a.set.temperatures ? a.set.temperatures[seq] : a.set.temperature;
+        const double top_p = a.set.top_ps ? (double)a.set.top_ps[seq] : a.set.top_p;
+        sh->sum_T = top_p < 1.0 ? T : 0.0f;
+        if (cta_rank() == 0) {
+            const int32_t k = a.set.top_ks ? a.set.top_ks[seq] : a.set.top_k;
+            sh->set.T = T;
+            sh->set.k = k > 0 ? (uint32_t)k : 0;
+            sh->set.top_p = top_p;
+        }
     } else if (tid >= 64 && tid < 64 + 2 * kConds) {
         sh->hit[(tid - 64) / kConds][(tid - 64) % kConds].chunk = -1;
         sh->place[(tid - 64) / kConds][(tid - 64) % kConds].bin = kNoPlace;
@@ -1093,18 +1100,18 @@ __device__ __forceinline__ void set_up(Shared* sh, const Args& a) {
     for (int i = tid; i < kPlaces / 4; i += kNT)
         z[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
-    if (tid == 32) {
+    if (tid == 32 && cta_rank() == 0) {
         const int64_t seq = row / (uint32_t)a.rows_per_seq;
         const double min_p = a.set.min_ps ? (double)a.set.min_ps[seq] : a.set.min_p;
-        const float T = sh->T, u = a.u ? a.u[row * a.u_stride] : 0.0f;
-        sh->u = u;
-        sh->has_min = min_p > 0.0;
-        sh->code = !(T == 0.0f || (T >= 1.17549435e-38f && T <= 3.402823466e38f)) || !(sh->top_p > 0.0) || !(min_p < 1.0)
+        const float T = sh->set.T, u = a.u ? a.u[row * a.u_stride] : 0.0f;
+        sh->set.u = u;
+        sh->set.has_min = min_p > 0.0;
+        sh->set.code = !(T == 0.0f || (T >= 1.17549435e-38f && T <= 3.402823466e38f)) || !(sh->set.top_p > 0.0) || !(min_p < 1.0)
                        ? SV_ERR_INVALID_ARG
                    : !(u >= 0.0f && u < 1.0f) ? SV_ERR_UNIFORM_RANGE
                                               : SV_OK;
         if (min_p > 0.0)
-            sh->dmin = (double)T * log(min_p);
+            sh->set.dmin = (double)T * log(min_p);
     }
 }
 
@@ -1120,7 +1127,7 @@ __global__ void __launch_bounds__(kNT, 4) sv_sample_kernel(const __grid_constant
     the_cluster().sync();  // every CTA is done with what it was told
     if (sh->args.general_rows && cta_rank() == 0 && threadIdx.x == 0)
         atomicAdd(sh->args.general_rows, 1u);
-    general_row<ES>(sh, sh->code);
+    general_row<ES>(sh, sh->set.code);
 }
 
 // with a CTA's chunks of places

@@ -178,41 +178,35 @@ struct General {
         return lo;
     }
 
-    // Narrows the entries of found bin f to a key range [klo, khi] that fits
-    // the list, or is a single key.
-    __device__ __forceinline__ void narrow(Search s, Found& f, uint32_t limit_key, uint32_t& klo, uint32_t& khi,
-                           bool& split) {
-        khi = key_at(f.bin, true);
-        klo = key_at(f.bin, false);
-        while (f.count > kList && klo != khi) {
+    // Narrows the entries of found bin f to keys that fit the list, or to a single key.
+    __device__ __forceinline__ KeyRange narrow(Search s, Found& f, uint32_t limit_key, bool& split) {
+        KeyRange keys;
+        keys.lo = key_at(f.bin, false);
+        keys.hi = max(key_at(f.bin, true), keys.lo);
+        while (f.count > kList && keys.lo != keys.hi) {
             split = true;
-            int sh_ = 0;
-            while (((khi - klo) >> sh_) >= (uint32_t)kBins)
-                ++sh_;
-            const uint32_t top = khi, bottom = klo;
+            const int n = keys.shift(kBins);
             the_cluster().sync();  // everyone has read `found`
             histogram([&](float l) {
                 const uint32_t k = logit_key(l);
-                return k <= top && k >= bottom ? (int)((top - k) >> sh_) : -1;
+                return k <= keys.hi && k >= keys.lo ? (int)((keys.hi - k) >> n) : -1;
             });
             s.above_mass = f.above_mass;
             s.above_count = f.above_count;
             s.limit_bin = kBins;
-            if (!s.draw && limit_key >= bottom && limit_key <= top)
-                s.limit_bin = (int)((top - limit_key) >> sh_);
+            if (!s.draw && limit_key >= keys.lo && limit_key <= keys.hi)
+                s.limit_bin = (int)((keys.hi - limit_key) >> n);
             unsigned long long m;
-            uint32_t n;
-            search(s, false, m, n);
-            const Found g = first();  // a condition that ends in a range ends in a part of it
-            f = g;
-            khi = top - ((uint32_t)g.bin << sh_);
-            const uint32_t low = sh_ ? khi - ((1u << sh_) - 1) : khi;
-            klo = low > bottom && low <= khi ? low : bottom;
+            uint32_t count;
+            search(s, false, m, count);
+            f = first();  // a condition that ends in a range ends in a part of it
+            keys = keys.part((uint32_t)f.bin, n);
         }
+        return keys;
     }
 
-    // Entries with klo <= key <= khi into the first CTA's list, sorted there.
-    __device__ __forceinline__ void gather(uint32_t klo, uint32_t khi) {
+    // Entries with such keys into the first CTA's list, sorted there.
+    __device__ __forceinline__ void gather(KeyRange keys) {
         the_cluster().sync();  // everyone has read `found`
         if (rank == 0 && tid == 0)
             sh->list_n[0] = 0;
@@ -221,7 +215,7 @@ struct General {
         unsigned long long* list = peer(sh->list, 0);
         v.each([&](float l, uint32_t id) {
             const uint32_t k = logit_key(l);
-            if (k >= klo && k <= khi)
+            if (k >= keys.lo && k <= keys.hi)
                 offer(n, list, l, id);
         });
         the_cluster().sync();
@@ -258,10 +252,8 @@ struct General {
         the_cluster().sync();
     }
 
-
-
     __device__ __forceinline__ void run(int code) {
-        const float T = sh->T;
+        const float T = sh->set.T;
         // A. the largest logit (NaN if there is one), over the cluster
         float m = __int_as_float(0xff800000);
         v.each([&](float l, uint32_t) { m = max_nan(m, l); });
@@ -326,15 +318,15 @@ struct General {
         Search s;
         s.above_mass = 0;
         s.above_count = 0;
-        s.k = sh->k;
-        s.top_p = sh->top_p;
+        s.k = sh->set.k;
+        s.top_p = sh->set.top_p;
         s.p = 0;
         s.draw = false;
         s.limit_bin = kBins;
         uint32_t limit_key = 0;
-        if (sh->has_min) {
+        if (sh->set.has_min) {
             // the smallest float l with l - l_max >= T ln(min_p)
-            const float limit = __double2float_ru((double)m + sh->dmin);
+            const float limit = __double2float_ru((double)m + sh->set.dmin);
             limit_key = logit_key(limit);
             if (limit_key > kKeyMinusInf)
                 s.limit_bin = bin_of(limit);
@@ -343,13 +335,14 @@ struct General {
         uint32_t n, kept;
         search(s, true, whole, n);
         const Found f = first();
-        uint32_t cut_key = kKeyMinusInf + 1, klo = 1, khi = 0;
+        uint32_t cut_key = kKeyMinusInf + 1, klo = 0;
         bool split = false;
         Found g = f;
         if (f.bin < kBins) {
-            narrow(s, g, limit_key, klo, khi, split);
+            const KeyRange keys = narrow(s, g, limit_key, split);
+            klo = keys.lo;
             if (g.count <= kList) {
-                gather(klo, khi);
+                gather(keys);
                 if (rank == 0) {
                     if (tid == 0)
                         sh->want = {s.k, limit_key, g.above_count, klo, s.top_p < 1.0 ? s.p : 0, g.above_mass, 0};
@@ -374,13 +367,13 @@ struct General {
         // C. the draw
         const float inv = inverse_mass(scale, E);
         if (sh->args.u) {
-            const unsigned long long target = floor_scaled(sh->u, E);
+            const unsigned long long target = floor_scaled(sh->set.u, E);
             if (f.bin < kBins && g.count <= kList && target >= g.above_mass) {
                 if (rank == 0)
                     draw_in_sorted(sh, 0, g.above_mass, target);  // the cut's list holds it
             } else if (f.bin < kBins && g.count > kList && target >= g.above_mass) {
                 const unsigned long long w = weight_call(scale, sh->pow2, key_logit(klo));
-                draw_among_equals(klo, (target - g.above_mass) / w);
+                draw_among_equals(klo, (target - g.above_mass) / max(w, 1ull));
             } else {
                 the_cluster().sync();
                 if (split)
@@ -400,14 +393,14 @@ struct General {
                 uint32_t dn;
                 search(d, true, dm, dn);
                 Found h = first();
-                narrow(d, h, 0, klo, khi, split);
+                const KeyRange keys = narrow(d, h, 0, split);
                 if (h.count <= kList) {
-                    gather(klo, khi);
+                    gather(keys);
                     if (rank == 0)
                         draw_in_sorted(sh, 0, h.above_mass, target);
                 } else {
-                    const unsigned long long w = weight_call(scale, sh->pow2, key_logit(klo));
-                    draw_among_equals(klo, (target - h.above_mass) / w);
+                    const unsigned long long w = weight_call(scale, sh->pow2, key_logit(keys.lo));
+                    draw_among_equals(keys.lo, (target - h.above_mass) / max(w, 1ull));
                 }
             }
             if (rank == 0 && tid == 0)

@@ -100,6 +100,17 @@ struct Cut {
     unsigned long long p, above_mass, slack;
 };
 
+// A row's settings, as the first CTA of the cluster has read them: all CTAs take the same turns,
+// also where a program changes a setting or a uniform under the call.
+struct alignas(16) Settings {
+    float T, u;
+    uint32_t k;     // top-k, 0: off
+    int code;
+    double top_p;   // >= 1: off
+    double dmin;    // T ln(min_p)
+    bool has_min;
+};
+
 // A CTA's shared memory, followed by its chunks of places.  Four CTAs share an SM, and
 // leave a good part of it to the first-level cache, where the threads' saved registers are.
 struct alignas(16) Shared {
@@ -115,13 +126,8 @@ struct alignas(16) Shared {
     // the CTA's slice of the row
     const unsigned char* base;  // the row's first logit
     uint32_t row, s0, s1, off, k0, k1;
-    // the row's settings
-    float T, u;
-    uint32_t k;     // top-k, 0: off
-    double top_p;   // >= 1: off
-    double dmin;    // T ln(min_p)
-    bool has_min;
-    int code;
+    Settings set;
+    float sum_T;    // as this CTA has read them: T where float32's first pass takes the float sum, else 0
     // what its parts have found
     RowScale scale;
     Found cut_at;   // the place where the cut lies
@@ -479,7 +485,7 @@ __device__ __noinline__ int resolve_few(Shared* sh, int which, bool cut, bool dr
         ok = any_near ? 2 : cut_inside(c, n, sh->list_mass);
     }
     if (ok == 1 && draw) {
-        const unsigned long long target = floor_scaled(sh->u, sh->kept_mass);
+        const unsigned long long target = floor_scaled(sh->set.u, sh->kept_mass);
         const bool it = kept && before <= target && before + w > target;
         if (it) {
             sh->token = ~(uint32_t)mine;

@@ -208,6 +208,24 @@ __device__ __forceinline__ unsigned long long ceil_scaled(double p, unsigned lon
     return scaled(ex ? f | 0x10000000000000ull : f, 1075 - (ex ? ex : 1), x, true);
 }
 
+// Keys lo..hi, and the parts that a search splits them into, counted from hi down: 2^shift
+// keys each, `parts` of them at most.  Whatever part a search names, it is less than the whole and inside
+// it: what goes on until one key is left ends after three of 2048 parts, also where the row changes under it.
+struct KeyRange {
+    uint32_t lo, hi;
+
+    __device__ __forceinline__ int shift(uint32_t parts) const {
+        int n = 0;
+        while (((hi - lo) >> n) >= parts)
+            ++n;
+        return n;
+    }
+    __device__ __forceinline__ KeyRange part(uint32_t i, int n) const {
+        const uint32_t top = hi - (min(i, (hi - lo) >> n) << n), width = (1u << n) - 1;
+        return {top - lo > width ? top - width : lo, top};
+    }
+};
+
 // ---------------------------------------------------- sums of weights -----
 
 // A weight for sums, in half the instructions of weight_fixed, below kFarT: 2^(p - M), p = l c,

@@ -134,7 +134,34 @@ static void sums() {
     std::printf("sum_off %.9Lg\n", worst);
 }
 
+// how many parts a search takes to one key, and how often a part was not a smaller one inside the whole,
+// whatever part the search names (2048 is what it names when it finds none)
+static void key_ranges() {
+    int most = 0, outside = 0;
+    for (int i = 0; i < 200000; ++i) {
+        KeyRange r;
+        r.lo = (uint32_t)gen() >> gen() % 32;
+        r.hi = max(r.lo, (uint32_t)gen() >> gen() % 32);
+        if (i == 0)
+            r = {0, 0xffffffffu};
+        int n = 0;
+        for (; r.lo != r.hi && n < 40; ++n) {
+            const int shift = r.shift(2048);
+            const uint32_t choice[4] = {(uint32_t)(gen() % 2048), 2048u, 0xffffffffu, 0u};
+            const uint32_t last = (r.hi - r.lo) >> shift, at = choice[gen() % 4];
+            const KeyRange p = r.part(at, shift);
+            outside += last >= 2048 || p.lo > p.hi || p.lo < r.lo || p.hi > r.hi || p.hi - p.lo >= r.hi - r.lo;
+            // the keys that count as that part are those in it
+            outside += at <= last && ((r.hi - p.hi) >> shift != at || (r.hi - p.lo) >> shift != at);
+            r = p;
+        }
+        most = max(most, n);
+    }
+    std::printf("key_range_rounds %d\nkey_ranges_outside %d\n", most, outside);
+}
+
 int main() {
+    key_ranges();
     weights();
     sums();
     shares();

@@ -32,3 +32,9 @@ def test_weights_keep_their_bound(figures):
 def test_sums_of_weights_keep_their_bound(figures):
     """2^-30 of themselves, where a table's part and three roundings of 2^-33 all agree."""
     assert figures["sum_off"] <= 2.0 ** -30
+
+
+def test_splitting_keys_ends(figures):
+    """After three parts of 2048, also where a search finds no part: of a row that changes under it."""
+    assert figures["key_ranges_outside"] == 0
+    assert figures["key_range_rounds"] <= 3
