@@ -738,6 +738,8 @@ class Verifier:
             s.temperatures = self._dense(temperature, "temperature", (B,), torch.float32)
         else:
             s.temperature = temperature
+            if s.temperature == 0 and temperature != 0:
+                s.temperature = float("nan")  # below any float32: refused as subnormal ones are
         if torch.is_tensor(top_k):
             s.top_ks = self._dense(top_k, "top_k", (B,), torch.int32)
         else:
