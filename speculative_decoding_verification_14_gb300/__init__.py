@@ -743,6 +743,8 @@ class Verifier:
         if torch.is_tensor(top_k):
             s.top_ks = self._dense(top_k, "top_k", (B,), torch.int32)
         else:
+            if int(top_k) != top_k:
+                raise ValueError(f"top_k must be a whole number, got {top_k}")
             s.top_k = min(max(int(top_k), 0), 0x7fffffff)
         if torch.is_tensor(top_p):
             s.top_ps = self._dense(top_p, "top_p", (B,), torch.float32)

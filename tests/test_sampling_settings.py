@@ -17,3 +17,12 @@ def test_a_temperature_below_any_float_is_not_greedy():
         assert math.isnan(settings(temperature=t).temperature), t
     for t in (0, 0.0, -0.0, 1e-40, 1.2e-38, 0.7, 1, np.float32(0.3)):
         assert settings(temperature=t).temperature == np.float32(t), t
+
+
+def test_top_k_is_a_whole_number():
+    """0.5 rounded down would turn the filter off."""
+    for k in (0.5, 1.5, -0.5, float("nan")):
+        with pytest.raises(ValueError):
+            settings(top_k=k)
+    for k, want in ((0, 0), (-3, 0), (50, 50), (50.0, 50), (np.int64(7), 7), (1 << 40, 0x7fffffff)):
+        assert settings(top_k=k).top_k == want
