@@ -358,7 +358,7 @@ typedef struct {
  *   uniforms  float in [0, 1), row r's at r * uniforms_stride
  *   tokens    out int32, row r's at r * tokens_stride
  *   probs     optional out float, row r at r * probs_stride: w_v / E on the
- *             kept entries (E their sum), 0 elsewhere; memory apart from logits
+ *             kept entries (E their sum), 0 elsewhere; rows apart from logits'
  *   p_token   optional out float [R]: the drawn token's entry of probs
  *   kept      optional out int32 [R]: entries kept
  *   status    optional out int32 [R]
@@ -379,8 +379,8 @@ typedef struct {
  * Asynchronous, no allocation, one launch on `stream`; safe to capture.
  * Returns SV_OK, SV_ERR_INVALID_ARG (null or misaligned pointers, B or
  * rows_per_seq - 1 or V beyond the context's limits, a stride below its row,
- * R * logits_stride >= 2^40, outputs where the logits lie, a setting out of
- * range), SV_ERR_UNSUPPORTED or SV_ERR_CUDA. */
+ * R * logits_stride >= 2^40, a row of probs where one of logits lies, a setting out
+ * of range), SV_ERR_UNSUPPORTED or SV_ERR_CUDA. */
 int spec_sample_run(sv_ctx* ctx, const void* logits, int logits_dtype, int64_t logits_stride,
                     const float* uniforms, int64_t uniforms_stride, int B, int rows_per_seq,
                     int64_t V, const sv_sampling* settings, int32_t* tokens, int64_t tokens_stride,
@@ -394,7 +394,7 @@ int spec_sample_run(sv_ctx* ctx, const void* logits, int logits_dtype, int64_t l
  * called at the same temperature).
  *
  *   out_logits  R rows of V in the input's dtype, row r at r * out_stride; the
- *               input itself (in place, same stride) or memory apart from it
+ *               input itself (in place, same stride) or rows apart from its rows
  *   kept        optional out int32 [R]: entries kept
  *   mass        optional out float [R]: their share of the row, E / S
  *   status      optional out int32 [R]

@@ -1192,11 +1192,20 @@ int check(const sv_ctx* ctx, const void* logits, int dtype, int64_t stride, int 
     return SV_OK;
 }
 
-// Whether n rows of x_bytes from x on lie among n rows of y_bytes from y on.
+// Whether one of n rows of x_bytes shares memory with one of n rows of y_bytes.  Rows of a kind do
+// not overlap, so that where neither end of two rows meets, the lower one meets no later one.
 bool meet(const void* x, int64_t x_stride, const void* y, int64_t y_stride, int64_t n, int64_t x_bytes,
           int64_t y_bytes) {
     const char *x0 = static_cast<const char*>(x), *y0 = static_cast<const char*>(y);
-    return y0 < x0 + (n - 1) * x_stride + x_bytes && x0 < y0 + (n - 1) * y_stride + y_bytes;
+    if (y0 >= x0 + (n - 1) * x_stride + x_bytes || x0 >= y0 + (n - 1) * y_stride + y_bytes)
+        return false;
+    for (int64_t i = 0, j = 0; i < n && j < n;) {
+        const char *a = x0 + i * x_stride, *b = y0 + j * y_stride;
+        if (a < b + y_bytes && b < a + x_bytes)
+            return true;
+        ++(a < b ? i : j);
+    }
+    return false;
 }
 
 }  // namespace
@@ -1286,8 +1295,8 @@ int spec_filter_run(sv_ctx* ctx, const void* logits, int logits_dtype, int64_t l
         return SV_ERR_INVALID_ARG;
     // in place, or apart: rows that overlap others would be read after they were written
     const int64_t n = (int64_t)B * rows_per_seq;
-    if (meet(logits, logits_stride * es, out_logits, out_stride * es, n, V * es, V * es) &&
-        !(logits == out_logits && (n == 1 || logits_stride == out_stride)))
+    if (!(logits == out_logits && (n == 1 || logits_stride == out_stride)) &&
+        meet(logits, logits_stride * es, out_logits, out_stride * es, n, V * es, V * es))
         return SV_ERR_INVALID_ARG;
     Args a;
     std::memset(&a, 0, sizeof a);

@@ -149,3 +149,29 @@ def test_logits_further_apart_than_a_float_holds(T, dtype):
         general_rows(lg, {**OFF, "temperature": T, **s}, torch.rand(6, 2, device="cuda"), 2 / 12)
     t = torch.randint(0, 2000, (6, 2), device="cuda", dtype=torch.int32)
     check_logprobs(lg, t, None, T, 5, gh.verifier().logprobs(lg, t, temperature=T, top_n=5))
+
+
+def test_rows_out_between_the_rows_in():
+    """Logits, truncated logits and probabilities side by side in one buffer: apart, though the stretches they
+    lie in are not.  One entry less apart is refused."""
+    import torch
+    import speculative_decoding_verification_14_gb300 as sv
+    B, rows, V, wide = 5, 3, 700, 2200
+    buf = torch.full((B, rows, wide), -3.0, device="cuda")
+    lg, cut, q = buf[:, :, :V], buf[:, :, V:2 * V], buf[:, :, 2 * V:3 * V]
+    lg.copy_(_tensor(rows_of(B, rows, V, 4), "f32"))
+    l, s = lg.clone(), {**OFF, "top_p": 0.9}
+    u = torch.rand(B, rows, device="cuda")
+    v = gh.verifier()
+    want, cut_want = v.sample(l, u, **s, probs=True), v.filter_logits(l, **s)
+    tokens = torch.empty(B, rows, dtype=torch.int32, device="cuda")
+    v.sample(lg, u, **s, out={"tokens": tokens, "probs": q})
+    v.filter_logits(lg, **s, out={"logits": cut})
+    assert torch.equal(q, want["probs"]) and torch.equal(tokens, want["tokens"]) and torch.equal(cut, cut_want["logits"])
+    assert torch.equal(lg, l) and (buf[:, :, 3 * V:] == -3.0).all()
+    for off in (V - 1, wide - V + 1):  # the end of its own row, the start of the next
+        near = buf.as_strided((B - 1, rows, V), (rows * wide, wide, 1), off)
+        for call in (lambda: v.sample(lg[:-1], u[:-1], **s, out={"tokens": tokens[:-1], "probs": near}),
+                     lambda: v.filter_logits(lg[:-1], **s, out={"logits": near})):
+            with pytest.raises(sv.SpecVerifyError):
+                call()
