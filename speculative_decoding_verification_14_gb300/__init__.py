@@ -760,7 +760,8 @@ class Verifier:
                out: Optional[dict] = None, probs: bool = False, status: bool = True,
                stream=None) -> dict:
         """Draws one token per row of logits [B, V] or [B, rows, V] (float32 or
-        bfloat16; rows evenly spaced) from uniforms of logits' shape without V.
+        bfloat16; rows evenly spaced, so that a part of [B, K + 1, V] along its second
+        dimension goes row by row or as a copy) from uniforms of logits' shape without V.
         The settings are numbers, or CUDA tensors [B] (float32; top_k int32) with
         one value per sequence; temperature 0 is greedy.  Returns tokens (int32),
         p_token, kept, and optionally probs (the distribution drawn from, as the
@@ -800,9 +801,11 @@ class Verifier:
                       out: Optional[dict] = None, status: bool = True, stream=None) -> dict:
         """Truncates logits [B, V] or [B, rows, V]: kept entries as they are, the
         others -inf, under settings as in ``sample``.  Returns logits, kept, mass
-        (the kept share of the row) and optionally status; with
-        ``out={"logits": logits, ...}`` in place.  The truncated rows are what any
-        of the verify calls may be given."""
+        (the kept share of the row; float32 rows are summed a second time for it) and
+        optionally status; with ``out={"logits": logits, ...}`` in place.  Any of the
+        verify calls may be given the truncated rows, at the same temperature: a verify
+        takes one for all sequences, so those of a batch with temperatures of their own
+        are verified in groups (rows cut at temperature 0 keep one token, and go with any)."""
         import torch
         B, rows, V, code, stride = self._rows_of(logits)
         shape = logits.shape[:-1]

@@ -34,12 +34,16 @@
 // start, 5 on the exchange, 7 on weighing, 8 on two searches and 8 on finding the drawn entry.
 // Four CTAs of 256 threads fit an SM (43 KB, 64 registers).  Parts of a fixed size
 // are why rows are cut no finer than the planner does.  A row alone is a chain
-// of some twenty barriers through code fetched for the first time: 47 thousand cycles
+// of some twenty barriers through code fetched for the first time: 46 thousand cycles
 // for 32000 float32 entries, which is why most loops here are not unrolled.
 // Per launch on one GB300 (replayed back to back, inputs larger than L2): 256 rows of
-// 128256 bfloat16 under top-p 56 us (65.7 MB, 1.2 TB/s); 2048 of them truncated
-// 240 us (1.05 GB in and out, 4.4 TB/s); 256 rows of 128256 float32 under every filter
-// with their probabilities 97 us (263 MB, 2.7 TB/s); one of 32000 float32 22 us.
+// 128256 bfloat16 under top-p 54 us (65.7 MB, 1.2 TB/s); 2048 of them truncated
+// 241 us (1.05 GB in and out, 4.4 TB/s); 256 rows of 128256 float32 under every filter
+// with their probabilities 94 us (263 MB, 2.8 TB/s); one of 32000 float32 21 us.
+// What rows beside these cost: beyond the counted magnitudes 256 rows of 128256 bfloat16 take
+// 660 us instead of 58, 150 of 50257 float32 84 instead of 67; float32 rows at T = 0, counted and then
+// walked twice more, 71 us for 256 of 128256 (bfloat16 34); a float32 row in a batch of 150 whose
+// stretches miss the cut or hold too many entries, less than one in a hundred, adds up to 300 us to its launch.
 #include "sampling_row.cuh"
 
 #include "sampling_general.cuh"
@@ -569,7 +573,8 @@ struct Above {
     }
 };
 
-// by weight_fixed, of the whole slice or its entries beside the vectors
+// by weight_fixed, of the whole slice (|l_max c| from 128 on: l_max 17.7 at T = 0.2; the open draw of
+// 150 rows of 50257 takes 99 us there and 78 at T = 1) or its entries beside the vectors
 __device__ __noinline__ Sums sum_each(Shared* sh, bool list, bool edges) {
     sh = here();
     View<4> v(sh);
@@ -995,7 +1000,8 @@ __device__ __noinline__ bool settle_exactly(Shared* sh, const StepCodes* codes) 
     }
     the_cluster().barrier_arrive();
     // a float sum will do to tell whether an entry listed whole lies above top-p's
-    // border; not where it becomes part of the answer, or entries weigh too little
+    // border; not where it becomes part of the answer, or entries weigh too little (a filter's
+    // `mass`: 256 rows of 128256 float32 under top-k 200 and top-p take 188 us with it, 104 without)
     const bool fine =
         !sh->band[0].from_top || sh->args.mass ||
         (by_mass && sh->cut_at.bin < kNoPlace && place_mass<4>(sh->scale, sh->pow2, sh->cut_at.bin, 1) < sh->whole >> 15);

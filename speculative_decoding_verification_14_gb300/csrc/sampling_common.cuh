@@ -159,7 +159,9 @@ __device__ __forceinline__ float exp_sum(const uint4& v, float m, float c) {
 // The largest logit of each of a thread's steps through the slice (the first pass goes
 // kDeep vectors a step, and so do later ones), to quarters and in eight bits: later
 // passes leave out the steps that hold nothing for them.  Long slices' steps share the
-// 16 codes.
+// 16 codes.  Codes tell logits from -16 to 47.75 apart; rows beyond, or of small scale, get one code and
+// are looked at whole (256 rows of 151936 bfloat16 with l_max about 60: draw under top-p 85 us
+// instead of 69, filter 61 instead of 57).
 constexpr int kDeep = 4;
 struct StepCodes {
     uint8_t code[16];

@@ -51,6 +51,10 @@ int plan_rows(int num_sms, int max_cluster, int B, int rows_per_seq, int64_t V, 
 // A sampling row's work beside its passes grows with the CTAs: 64 rows of 151936
 // bfloat16 take 38.9 us with eight CTAs a row and 38.3 with four, 256 of 128256 64 us
 // with four and 56 with two; 150 rows of 50257 float32 82 us with four and 68 with two.
+// Between those sizes it is not always the best: of 8 to 153 rows of 32000 to 151936 under top-k and
+// top-p, 67 of 104 are within 5 % of the best count.  The others: 77 to 152 rows of 32000, 25.5 us with
+// one CTA a row and 21.2 to 22.5 with two; 20 to 39 rows, up to 14 % better with twice as many; 152
+// rows of 128256 float32 or 151936, whose four CTAs a row do not all fit at once, 73 us and 49 with two.
 extern "C" int spec_sample_plan_for(int num_sms, int max_cluster, int B, int rows_per_seq,
                                     int64_t V, int logits_dtype, int ovr_cluster, sv_plan* out) {
     return plan_rows(num_sms, max_cluster, B, rows_per_seq, V, logits_dtype, ovr_cluster, 256, 4,
@@ -59,7 +63,8 @@ extern "C" int spec_sample_plan_for(int num_sms, int max_cluster, int B, int row
 
 // A log-probability row's does less: 37 x 3 rows of 50257 float32 take 14.2 us with
 // four CTAs a row and 16.7 with one; 8 x 5 of 32000 bfloat16 10.7 us with eight and 9.3
-// with four.
+// with four.  Where rows times CTAs come to all that the SMs hold (38 rows of sixteen, 76 of eight, 152
+// of four), clusters do not all fit at once: 152 rows of 32000 bfloat16 take 15.9 us and 10.8 with two.
 extern "C" int spec_logprobs_plan_for(int num_sms, int max_cluster, int B, int rows_per_seq,
                                       int64_t V, int logits_dtype, int ovr_cluster,
                                       sv_plan* out) {
