@@ -112,14 +112,19 @@ def measured_peak():
 
 
 _CSRC = "speculative_decoding_verification_14_gb300/csrc/"
-# the sources each mode's kernel and launch path are built from (every entry
-# point's host side lives in spec_verify.cu)
+# the sources each mode's kernel and launch path are built from (every verify
+# entry point's host side lives in spec_verify.cu), and those of the sampling
+# and log-probability kernels, which profiles/ covers too
 KERNEL_SOURCES = {
-    "sampled": ("spec_verify.cu", "sv_internal.h", "planner.cpp"),
-    "ragged": ("spec_verify.cu", "sv_internal.h", "planner.cpp"),
-    "greedy": ("greedy.cu", "spec_verify.cu", "sv_internal.h", "planner.cpp"),
-    "truncated": ("truncated.cu", "spec_verify.cu", "sv_internal.h", "planner.cpp"),
-    "draft_logits": ("spec_verify.cu", "sv_internal.h", "planner.cpp"),
+    "sampled": ("spec_verify.cu", "sv_internal.h", "sv_context.h", "planner.cpp"),
+    "ragged": ("spec_verify.cu", "sv_internal.h", "sv_context.h", "planner.cpp"),
+    "greedy": ("greedy.cu", "spec_verify.cu", "sv_internal.h", "sv_context.h", "planner.cpp"),
+    "truncated": ("truncated.cu", "spec_verify.cu", "sv_internal.h", "sv_context.h", "planner.cpp"),
+    "draft_logits": ("spec_verify.cu", "sv_internal.h", "sv_context.h", "planner.cpp"),
+    "sampling": ("sampling.cu", "sampling_row.cuh", "sampling_general.cuh", "sampling_common.cuh",
+                 "sampling_weights.cuh", "sampling_planner.cpp", "sv_context.h"),
+    "logprobs": ("logprobs.cu", "sampling_common.cuh", "sampling_weights.cuh", "sampling_planner.cpp",
+                 "sv_context.h"),
 }
 
 

@@ -420,7 +420,8 @@ int spec_sample_plan_for(int num_sms, int max_cluster, int B, int rows_per_seq, 
  * -inf than top-k, and float32 rows with thousands of entries next to the cut or the
  * draw -- go a general way with the same answers, which takes several passes more.  With `general_rows` set, every later call on this
  * context adds 1 to it for each of them.  It is one DEVICE uint32 owned by the
- * caller, who zeroes it and keeps it alive while set; NULL turns the counting off.
+ * caller, who zeroes it and keeps it alive while set, and while graphs captured then are
+ * replayed; NULL turns the counting off.
  * Returns SV_OK or SV_ERR_INVALID_ARG (no context, misaligned). */
 int spec_sample_set_telemetry(sv_ctx* ctx, uint32_t* general_rows);
 

@@ -16,7 +16,7 @@
 // hand them to a short list.  Each CTA sends its n best to the first one, which orders them.
 //
 // What bounds it: waiting for the pass's loads (four vectors a thread, one step ahead, four CTAs
-// an SM: 3.5 warps wait for each one that issues, and no pipe is above 30 %), and the chain after it:
+// an SM: nearly four warps wait for each one that issues, and no pipe is above 30 %), and the chain after it:
 // 256 x 8 rows of 128256 bfloat16, 56% of them live, top 20: 67 us for 296 MB, 4.4 TB/s;
 // 37 x 3 rows of 50257 float32 14 us; 8 x 5 rows of 32000 bfloat16 9 us, a launch and
 // sixteen barriers for the bound.  Where fewer tokens than n are left beside a finite mask, the mask's
