@@ -43,7 +43,7 @@
 // What rows beside these cost: beyond the counted magnitudes 256 rows of 128256 bfloat16 take
 // 660 us instead of 58, 150 of 50257 float32 84 instead of 67; float32 rows at T = 0, counted and then
 // walked twice more, 71 us for 256 of 128256 (bfloat16 34); a float32 row in a batch of 150 whose
-// stretches miss the cut or hold too many entries, less than one in a hundred, adds up to 300 us to its launch.
+// stretches miss the cut or hold too many entries, less than one in a hundred, adds some 240 us to its launch.
 #include "sampling_row.cuh"
 
 #include "sampling_general.cuh"
