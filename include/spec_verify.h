@@ -453,6 +453,61 @@ int spec_logprobs_get_plan(sv_ctx* ctx, int B, int rows_per_seq, int64_t V, int 
 int spec_logprobs_plan_for(int num_sms, int max_cluster, int B, int rows_per_seq, int64_t V,
                            int logits_dtype, int ovr_cluster, sv_plan* out);
 
+/* Distillation of the drafter from the target's top log-probabilities: what a
+ * drafter that keeps learning from its verifies is trained with.  (The pages
+ * measure acceptance as the sum of min(p, q) -- [P2] "Two things that follow from
+ * the math" -- which a closer q raises.)  For a row z of V draft logits,
+ * q = softmax(z / T), and the teacher's list of tokens x_k with log-probabilities
+ * a_k, t_k = exp(a_k):
+ *   tail 0: t_k is divided by the list's sum, and
+ *           loss = sum_k t_k (ln t_k - ln q(x_k)),
+ *           d loss / d z_v = (q_v - t_v) / T             (t_v = 0 off the list);
+ *           a_k may be logits, or log-probabilities less any constant
+ *   tail 1: what the list leaves, r = max(0, 1 - sum t_k), is one more outcome, of
+ *           draft mass q_rest = sum of q off the list, and
+ *           loss = sum_k t_k (a_k - ln q(x_k)) + r (ln r - ln q_rest),
+ *           d loss / d z_v = ((sum t_k + r) q_v - t_v) / T       on the list,
+ *                            ((sum t_k + r) q_v - r q_v / q_rest) / T   off it
+ *
+ *   draft_logits  R = B * rows_per_seq rows of V (dtype logits_dtype), row r at
+ *                 r * logits_stride; row r belongs to sequence r / rows_per_seq
+ *   top_logprobs, top_tokens  [B, rows, n] (1 <= n <= 128) float and int32, in any
+ *                 order; a token of -1 is no entry, whatever its log-probability:
+ *                 spec_logprobs_run's outputs of the target's rows are such lists
+ *   accept_len    [B] or NULL (every row): rows from accept_len on are not read
+ *   temperature   T of the draft rows, 2^-100 <= T <= 2^100
+ *   grad_loss     [B, rows] float or NULL (1): d objective / d loss of each row
+ *   loss          optional out float [B, rows]
+ *   grad_logits   optional out (not both NULL): grad_loss * d loss / d z, R rows of V
+ *                 in the logits' type, row r at r * grad_stride; the logits
+ *                 themselves (in place, same stride) or rows apart from theirs
+ *   status        optional out int32 [B, rows]
+ * A row is read once and its gradient written once, with or without the loss, so
+ * that the gradient for a grad_loss known only later is a second call without
+ * loss.  Rows from accept_len on and rows without an entry have loss 0 and a
+ * gradient of zeros.  A listed logit of -inf that the teacher gives mass has loss
+ * +inf (and its gradient); a list that leaves at most 2^-20 where the draft has no
+ * mass off the list leaves nothing.  An erroneous row (a token outside
+ * [-1, V) or listed twice: SV_ERR_TOKEN_RANGE; a listed log-probability that is
+ * NaN or +inf, or only -inf under tail 0; logits with a NaN or +inf or only -inf:
+ * SV_ERR_NONFINITE) gets a NaN loss and NaN gradients, and sets the context's
+ * error word.
+ * Repeated calls give the same bits.  Asynchronous, no allocation, one launch on
+ * `stream`; safe to capture.  Rows that 16 CTAs' shared memory holds (V up to
+ * 884733 float, 1769465 bfloat16) are taken: SV_ERR_UNSUPPORTED beyond.  Otherwise
+ * returns as spec_sample_run. */
+int spec_distill_run(sv_ctx* ctx, const void* draft_logits, int logits_dtype,
+                     int64_t logits_stride, const float* top_logprobs, const int32_t* top_tokens,
+                     int n, const int32_t* accept_len, int B, int rows_per_seq, int64_t V,
+                     float temperature, int tail, const float* grad_loss, float* loss,
+                     void* grad_logits, int64_t grad_stride, int32_t* status, void* stream);
+
+/* Its launch plan, and its planner as a pure host function. */
+int spec_distill_get_plan(sv_ctx* ctx, int B, int rows_per_seq, int64_t V, int logits_dtype,
+                          sv_plan* out);
+int spec_distill_plan_for(int num_sms, int max_cluster, int B, int rows_per_seq, int64_t V,
+                          int logits_dtype, int ovr_cluster, sv_plan* out);
+
 /* Acceptance telemetry ([P1] "Production perspective": ship the acceptance
  * rate and the mean accepted length; its operational checklist: record
  * acceptance histograms).  With `accept_hist` set, every later verify on this

@@ -143,11 +143,15 @@ def library() -> ctypes.CDLL:
             **{f"spec_{op}_get_plan": (ctypes.c_int, [P, ctypes.c_int, ctypes.c_int,
                                                       ctypes.c_int64, ctypes.c_int,
                                                       ctypes.POINTER(sv_plan)])
-               for op in ("sample", "logprobs")},
+               for op in ("sample", "logprobs", "distill")},
             **{f"spec_{op}_plan_for": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                                       ctypes.c_int, ctypes.c_int64, ctypes.c_int,
                                                       ctypes.c_int, ctypes.POINTER(sv_plan)])
-               for op in ("sample", "logprobs")},
+               for op in ("sample", "logprobs", "distill")},
+            "spec_distill_run": (ctypes.c_int, [P, P, ctypes.c_int, ctypes.c_int64, P, P,
+                                                ctypes.c_int, P, ctypes.c_int, ctypes.c_int,
+                                                ctypes.c_int64, ctypes.c_float, ctypes.c_int, P, P,
+                                                P, ctypes.c_int64, P, P]),
             "spec_verify_set_telemetry": (ctypes.c_int, [P, P, ctypes.c_int]),
             "spec_sample_set_telemetry": (ctypes.c_int, [P, P]),
             "spec_verify_selftest_wait": (ctypes.c_int, [ctypes.c_int, ctypes.c_ulonglong,
@@ -369,6 +373,31 @@ def spec_logprobs_plan_for(num_sms, max_cluster, B, rows_per_seq, V, dtype, ovr_
     plan = sv_plan()
     rc = library().spec_logprobs_plan_for(num_sms, max_cluster, B, rows_per_seq, V, dtype,
                                           ovr_cluster, ctypes.byref(plan))
+    return rc, plan.as_dict()
+
+
+def spec_distill_run(ctx, logits_ptr, dtype, logits_stride, top_logprobs_ptr, top_tokens_ptr, n,
+                     accept_len_ptr, B, rows_per_seq, V, T, tail, grad_loss_ptr=None,
+                     loss_ptr=None, grad_logits_ptr=None, grad_stride=0, status_ptr=None,
+                     stream=None) -> int:
+    return library().spec_distill_run(ctx, logits_ptr, dtype, logits_stride, top_logprobs_ptr,
+                                      top_tokens_ptr, int(n), accept_len_ptr, B, rows_per_seq, V,
+                                      float(T), int(tail), grad_loss_ptr, loss_ptr,
+                                      grad_logits_ptr, grad_stride, status_ptr, stream)
+
+
+def spec_distill_get_plan(ctx, B, rows_per_seq, V, dtype) -> dict:
+    plan = sv_plan()
+    rc = library().spec_distill_get_plan(ctx, B, rows_per_seq, V, dtype, ctypes.byref(plan))
+    if rc != SV_OK:
+        raise SpecVerifyError(rc, "spec_distill_get_plan")
+    return plan.as_dict()
+
+
+def spec_distill_plan_for(num_sms, max_cluster, B, rows_per_seq, V, dtype, ovr_cluster=0):
+    plan = sv_plan()
+    rc = library().spec_distill_plan_for(num_sms, max_cluster, B, rows_per_seq, V, dtype,
+                                         ovr_cluster, ctypes.byref(plan))
     return rc, plan.as_dict()
 
 
@@ -866,6 +895,53 @@ class Verifier:
         if rc != SV_OK:
             raise SpecVerifyError(rc, "spec_logprobs_run")
         return out
+
+    def distill(self, logits, top_logprobs, top_tokens, accept_len=None, temperature: float = 1.0,
+                tail: bool = False, grad_loss=None, loss: bool = True, grad: bool = True,
+                out: Optional[dict] = None, status: bool = True, stream=None) -> dict:
+        """Distillation of the drafter's logits [B, rows, V] (or [B, V]) from a teacher's lists
+        top_logprobs and top_tokens [B, rows, n] (float32, int32; -1: no entry), such as
+        ``logprobs`` gives of the target's rows: renormalised over the list, or with what the
+        list leaves as one more outcome (tail).  Rows from accept_len[b] on are not read (None:
+        every row).  grad_loss [B, rows] float32: the objective's derivative by each row's loss
+        (None: 1).  Returns loss and, for grad, grad_logits in the logits' type, and optionally
+        status; ``out={"grad_logits": logits, ...}`` writes in place.  A gradient asked for
+        later, once grad_loss is known, is a second call with loss=False."""
+        import torch
+        B, rows, V, code, stride = self._rows_of(logits)
+        shape = logits.shape[:-1]
+        if top_tokens.dim() != logits.dim():
+            raise ValueError("top_tokens must be logits' shape with n in place of V")
+        n = top_tokens.shape[-1]
+        if out is None:
+            dev = logits.device
+            out = {}
+            if loss:
+                out["loss"] = torch.empty(shape, dtype=torch.float32, device=dev)
+            if grad:
+                out["grad_logits"] = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+            if status:
+                out["status"] = torch.empty(shape, dtype=torch.int32, device=dev)
+        ls, g, st = (out.get(k) for k in ("loss", "grad_logits", "status"))
+        rc = spec_distill_run(
+            self.ctx, logits.data_ptr(), code, stride,
+            self._dense(top_logprobs, "top_logprobs", (*shape, n), torch.float32),
+            self._dense(top_tokens, "top_tokens", (*shape, n), torch.int32), n,
+            None if accept_len is None else self._dense(accept_len, "accept_len", (B,), torch.int32),
+            B, rows, V, temperature, bool(tail),
+            None if grad_loss is None else self._dense(grad_loss, "grad_loss", shape, torch.float32),
+            None if ls is None else self._dense(ls, "loss", shape, torch.float32),
+            None if g is None else
+            self._expect(g, "grad_logits", logits.shape, logits.dtype).data_ptr(),
+            0 if g is None else _row_stride(g, "grad_logits", rows, V),
+            None if st is None else self._dense(st, "status", shape, torch.int32),
+            stream if stream is not None else torch.cuda.current_stream(self.device).cuda_stream)
+        if rc != SV_OK:
+            raise SpecVerifyError(rc, "spec_distill_run")
+        return out
+
+    def plan_distill(self, B, rows_per_seq, V, dtype=SV_BF16) -> dict:
+        return spec_distill_get_plan(self.ctx, B, rows_per_seq, V, dtype)
 
     def plan_sample(self, B, rows_per_seq, V, dtype=SV_BF16) -> dict:
         return spec_sample_get_plan(self.ctx, B, rows_per_seq, V, dtype)

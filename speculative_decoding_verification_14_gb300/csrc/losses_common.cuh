@@ -1,0 +1,65 @@
+// losses_common.cuh -- shared by the kernels of the drafter's losses: barriers for copies that the
+// copy engine makes, and waits that end.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "sv_internal.h"
+
+namespace sv {
+
+__device__ __forceinline__ uint32_t shared_addr(const void* p) {
+    return (uint32_t)__cvta_generic_to_shared(p);
+}
+__device__ __forceinline__ void barrier_init(uint64_t* bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(shared_addr(bar)), "r"(count) : "memory");
+}
+// initialised barriers become visible to the copy engine and to other CTAs of the cluster
+__device__ __forceinline__ void barrier_init_fence() {
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ void barrier_expect(uint64_t* bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(shared_addr(bar)), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ bool barrier_try(uint64_t* bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(shared_addr(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+__device__ __forceinline__ unsigned long long global_ns() {
+    unsigned long long t;
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+    return t;
+}
+// Whether the barrier's phase came to its end within `limit` ns.
+static __device__ __noinline__ bool barrier_wait_slow(uint64_t* bar, uint32_t parity, unsigned long long limit) {
+    const unsigned long long t0 = global_ns();
+    do {
+        for (int i = 0; i < 64; ++i)
+            if (barrier_try(bar, parity))
+                return true;
+    } while (global_ns() - t0 < limit);
+    return false;
+}
+__device__ __forceinline__ bool barrier_wait(uint64_t* bar, uint32_t parity, unsigned long long limit) {
+    return barrier_try(bar, parity) || barrier_wait_slow(bar, parity, limit);
+}
+// global to this CTA's shared memory, both ends on 16 bytes, a multiple of 16 bytes
+__device__ __forceinline__ void copy_bulk(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     shared_addr(dst)),
+                 "l"(src), "r"(bytes), "r"(shared_addr(bar))
+                 : "memory");
+}
+
+}  // namespace sv
