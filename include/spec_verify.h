@@ -508,6 +508,66 @@ int spec_distill_get_plan(sv_ctx* ctx, int B, int rows_per_seq, int64_t V, int l
 int spec_distill_plan_for(int num_sms, int max_cluster, int B, int rows_per_seq, int64_t V,
                           int logits_dtype, int ovr_cluster, sv_plan* out);
 
+/* Softmax cross entropy of a vocabulary head over rows of hidden states, without
+ * keeping the logits: what a drafter learns from the tokens its verifies emitted.
+ * For a row h [D] with label y and the head's weight W [V, D], z_v = h . W_v:
+ *   lse = ln sum_v exp z_v,   loss = lse - z_y
+ * and spec_cross_entropy_grad, for the objective's derivative g by each loss:
+ *   d_v = g (exp(z_v - lse) - [v = y]),
+ *   grad_hidden = sum_v d_v W_v,   grad_weight_v = sum over rows of d_v h
+ *
+ *   hidden   R = B * rows_per_seq rows of D, row r at r * hidden_stride, in any
+ *            alignment; row r belongs to sequence r / rows_per_seq
+ *   weight   V rows of D, row v at v * weight_stride: 16-byte aligned, the stride a
+ *            multiple of 8
+ *   dtype    of hidden, weight and their gradients: SV_BF16 (SV_F32 returns
+ *            SV_ERR_UNSUPPORTED); products are summed in float
+ *   labels, accept_len  [B, rows] int32 and [B] or NULL (every row): a verify's
+ *            out_tokens and accept_len; rows from accept_len on and rows of label -1
+ *            do not count, whatever their hidden states hold
+ *   loss, lse  out float [B, rows]; 0 for rows that do not count
+ *   status   optional out int32 [B, rows]
+ *   grad_loss  [B, rows] float or NULL (1)
+ *   grad_hidden, grad_weight  optional out (not both NULL), R and V rows of D at
+ *            their strides, written as a whole: zeros where no row counts.  A
+ *            head that is not trained costs neither its product nor its bytes
+ *   workspace  device memory of spec_cross_entropy_workspace's bytes, 256-byte
+ *            aligned, written as the call likes: calls that can overlap on the GPU need
+ *            one each, and so do graphs that can.  grad 0: enough for
+ *            spec_cross_entropy_run; 1: for either call
+ * Each d_v is rounded to bfloat16 before the products that sum it, and each
+ * gradient once after.  A row's work is not done where it does not count.
+ * 1 <= D <= 2^20, R <= 2^24.  No output may lie where an input or another output does.
+ * An erroneous row (a label outside [-1, V): SV_ERR_TOKEN_RANGE; logits with a
+ * NaN or +inf or only -inf, in the gradients' call an lse that is not finite:
+ * SV_ERR_NONFINITE) gets a NaN loss and lse and a NaN grad_hidden, adds nothing to
+ * grad_weight, and sets the context's error word; a wait inside the kernels that
+ * runs out sets SV_ERR_TIMEOUT there.  Repeated calls give the same bits.
+ * Asynchronous, no allocation; a few launches on `stream` (three per piece of the
+ * vocabulary for both gradients); safe to capture.  Returns SV_OK,
+ * SV_ERR_INVALID_ARG (null or misaligned pointers, sizes beyond the context's
+ * limits, a stride below its row, too small a workspace), SV_ERR_UNSUPPORTED or
+ * SV_ERR_CUDA. */
+int spec_cross_entropy_run(sv_ctx* ctx, const void* hidden, int dtype, int64_t hidden_stride,
+                           const void* weight, int64_t weight_stride, const int32_t* labels,
+                           const int32_t* accept_len, int B, int rows_per_seq, int64_t V,
+                           int64_t D, float* loss, float* lse, int32_t* status, void* workspace,
+                           size_t workspace_bytes, void* stream);
+int spec_cross_entropy_grad(sv_ctx* ctx, const void* hidden, int dtype, int64_t hidden_stride,
+                            const void* weight, int64_t weight_stride, const int32_t* labels,
+                            const int32_t* accept_len, const float* lse, const float* grad_loss,
+                            int B, int rows_per_seq, int64_t V, int64_t D, void* grad_hidden,
+                            int64_t grad_hidden_stride, void* grad_weight,
+                            int64_t grad_weight_stride, int32_t* status, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace a call needs on the context's device, and the same as a pure host
+ * function of the device's SMs. */
+int spec_cross_entropy_workspace(sv_ctx* ctx, int B, int rows_per_seq, int64_t V, int64_t D,
+                                 int grad, size_t* bytes);
+int spec_cross_entropy_workspace_for(int num_sms, int B, int rows_per_seq, int64_t V, int64_t D,
+                                     int grad, size_t* bytes);
+
 /* Acceptance telemetry ([P1] "Production perspective": ship the acceptance
  * rate and the mean accepted length; its operational checklist: record
  * acceptance histograms).  With `accept_hist` set, every later verify on this

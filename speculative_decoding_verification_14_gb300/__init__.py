@@ -152,6 +152,23 @@ def library() -> ctypes.CDLL:
                                                 ctypes.c_int, P, ctypes.c_int, ctypes.c_int,
                                                 ctypes.c_int64, ctypes.c_float, ctypes.c_int, P, P,
                                                 P, ctypes.c_int64, P, P]),
+            "spec_cross_entropy_run": (ctypes.c_int, [P, P, ctypes.c_int, ctypes.c_int64, P,
+                                                      ctypes.c_int64, P, P, ctypes.c_int,
+                                                      ctypes.c_int, ctypes.c_int64, ctypes.c_int64,
+                                                      P, P, P, P, ctypes.c_size_t, P]),
+            "spec_cross_entropy_grad": (ctypes.c_int, [P, P, ctypes.c_int, ctypes.c_int64, P,
+                                                       ctypes.c_int64, P, P, P, P, ctypes.c_int,
+                                                       ctypes.c_int, ctypes.c_int64,
+                                                       ctypes.c_int64, P, ctypes.c_int64, P,
+                                                       ctypes.c_int64, P, P, ctypes.c_size_t, P]),
+            "spec_cross_entropy_workspace": (ctypes.c_int, [P, ctypes.c_int, ctypes.c_int,
+                                                            ctypes.c_int64, ctypes.c_int64,
+                                                            ctypes.c_int,
+                                                            ctypes.POINTER(ctypes.c_size_t)]),
+            "spec_cross_entropy_workspace_for": (ctypes.c_int, [ctypes.c_int, ctypes.c_int,
+                                                                ctypes.c_int, ctypes.c_int64,
+                                                                ctypes.c_int64, ctypes.c_int,
+                                                                ctypes.POINTER(ctypes.c_size_t)]),
             "spec_verify_set_telemetry": (ctypes.c_int, [P, P, ctypes.c_int]),
             "spec_sample_set_telemetry": (ctypes.c_int, [P, P]),
             "spec_verify_selftest_wait": (ctypes.c_int, [ctypes.c_int, ctypes.c_ulonglong,
@@ -399,6 +416,45 @@ def spec_distill_plan_for(num_sms, max_cluster, B, rows_per_seq, V, dtype, ovr_c
     rc = library().spec_distill_plan_for(num_sms, max_cluster, B, rows_per_seq, V, dtype,
                                          ovr_cluster, ctypes.byref(plan))
     return rc, plan.as_dict()
+
+
+def spec_cross_entropy_run(ctx, hidden_ptr, dtype, hidden_stride, weight_ptr, weight_stride,
+                           labels_ptr, accept_len_ptr, B, rows_per_seq, V, D, loss_ptr, lse_ptr,
+                           status_ptr=None, workspace_ptr=None, workspace_bytes=0,
+                           stream=None) -> int:
+    return library().spec_cross_entropy_run(ctx, hidden_ptr, dtype, hidden_stride, weight_ptr,
+                                            weight_stride, labels_ptr, accept_len_ptr, B,
+                                            rows_per_seq, V, D, loss_ptr, lse_ptr, status_ptr,
+                                            workspace_ptr, workspace_bytes, stream)
+
+
+def spec_cross_entropy_grad(ctx, hidden_ptr, dtype, hidden_stride, weight_ptr, weight_stride,
+                            labels_ptr, accept_len_ptr, lse_ptr, grad_loss_ptr, B, rows_per_seq, V,
+                            D, grad_hidden_ptr=None, grad_hidden_stride=0, grad_weight_ptr=None,
+                            grad_weight_stride=0, status_ptr=None, workspace_ptr=None,
+                            workspace_bytes=0, stream=None) -> int:
+    return library().spec_cross_entropy_grad(ctx, hidden_ptr, dtype, hidden_stride, weight_ptr,
+                                             weight_stride, labels_ptr, accept_len_ptr, lse_ptr,
+                                             grad_loss_ptr, B, rows_per_seq, V, D,
+                                             grad_hidden_ptr, grad_hidden_stride, grad_weight_ptr,
+                                             grad_weight_stride, status_ptr, workspace_ptr,
+                                             workspace_bytes, stream)
+
+
+def spec_cross_entropy_workspace(ctx, B, rows_per_seq, V, D, grad) -> int:
+    n = ctypes.c_size_t(0)
+    rc = library().spec_cross_entropy_workspace(ctx, B, rows_per_seq, V, D, int(grad),
+                                                ctypes.byref(n))
+    if rc != SV_OK:
+        raise SpecVerifyError(rc, "spec_cross_entropy_workspace")
+    return n.value
+
+
+def spec_cross_entropy_workspace_for(num_sms, B, rows_per_seq, V, D, grad):
+    n = ctypes.c_size_t(0)
+    rc = library().spec_cross_entropy_workspace_for(num_sms, B, rows_per_seq, V, D, int(grad),
+                                                    ctypes.byref(n))
+    return rc, n.value
 
 
 def spec_verify_set_telemetry(ctx, hist_ptr, bins) -> int:
@@ -938,6 +994,102 @@ class Verifier:
             stream if stream is not None else torch.cuda.current_stream(self.device).cuda_stream)
         if rc != SV_OK:
             raise SpecVerifyError(rc, "spec_distill_run")
+        return out
+
+    def cross_entropy_workspace(self, B, rows_per_seq, V, D, grad=True):
+        """Memory for ``cross_entropy`` calls of these sizes, and for ``cross_entropy_grad`` if
+        grad: a CUDA tensor to keep from call to call.  Calls that can overlap on the GPU (streams
+        not ordered with each other, graphs replayed side by side) need one each."""
+        import torch
+        n = spec_cross_entropy_workspace(self.ctx, B, rows_per_seq, V, D, grad)
+        return torch.empty(n, dtype=torch.uint8, device=f"cuda:{self.device}")
+
+    def _head_of(self, hidden, weight, labels, accept_len, workspace, grad, stream):
+        """What both cross-entropy calls take first, and their workspace."""
+        import torch
+        if hidden.dtype != torch.bfloat16 or weight.dtype != torch.bfloat16:
+            raise TypeError(f"hidden and weight must be bfloat16, got {hidden.dtype} and {weight.dtype}")
+        if hidden.dim() not in (2, 3) or weight.dim() != 2 or weight.shape[1] != hidden.shape[-1]:
+            raise ValueError("hidden must be [B, D] or [B, rows, D] and weight [V, D]")
+        self._on_device(hidden, "hidden")
+        self._on_device(weight, "weight")
+        B, D, V = hidden.shape[0], hidden.shape[-1], weight.shape[0]
+        rows = hidden.shape[1] if hidden.dim() == 3 else 1
+        if workspace is None:
+            workspace = self.cross_entropy_workspace(B, rows, V, D, grad)
+            if stream is not None:  # torch may hand it on once that stream is through with it
+                workspace.record_stream(torch.cuda.ExternalStream(stream, device=workspace.device))
+        elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+            raise ValueError("the workspace must be a contiguous uint8 tensor")
+        self._on_device(workspace, "workspace")
+        head = (hidden.data_ptr(), SV_BF16, _row_stride(hidden, "hidden", rows, D),
+                weight.data_ptr(), _row_stride(weight, "weight", 1, D),
+                self._dense(labels, "labels", hidden.shape[:-1], torch.int32),
+                None if accept_len is None else self._dense(accept_len, "accept_len", (B,), torch.int32))
+        return head, (B, rows, V, D), hidden.shape[:-1], workspace
+
+    def cross_entropy(self, hidden, weight, labels, accept_len=None, workspace=None,
+                      out: Optional[dict] = None, status: bool = True, stream=None) -> dict:
+        """Softmax cross entropy of labels [B, rows] (int32; -1: does not count) under the head
+        weight [V, D] over hidden states [B, rows, D] (or [B] and [B, D]), both bfloat16, without
+        keeping the logits: a verify's out_tokens and accept_len are such labels.  Returns loss and
+        lse [B, rows] (float32; 0 for rows that do not count) and optionally status.  weight's rows
+        have to lie on 16 bytes.  workspace: from ``cross_entropy_workspace`` (None: taken from
+        torch for this call)."""
+        import torch
+        head, (B, rows, V, D), shape, ws = self._head_of(hidden, weight, labels, accept_len,
+                                                         workspace, False, stream)
+        if out is None:
+            dev = hidden.device
+            out = {"loss": torch.empty(shape, dtype=torch.float32, device=dev),
+                   "lse": torch.empty(shape, dtype=torch.float32, device=dev)}
+            if status:
+                out["status"] = torch.empty(shape, dtype=torch.int32, device=dev)
+        st = out.get("status")
+        rc = spec_cross_entropy_run(
+            self.ctx, *head, B, rows, V, D, self._dense(out["loss"], "loss", shape, torch.float32),
+            self._dense(out["lse"], "lse", shape, torch.float32),
+            None if st is None else self._dense(st, "status", shape, torch.int32), ws.data_ptr(),
+            ws.numel(),
+            stream if stream is not None else torch.cuda.current_stream(self.device).cuda_stream)
+        if rc != SV_OK:
+            raise SpecVerifyError(rc, "spec_cross_entropy_run")
+        return out
+
+    def cross_entropy_grad(self, hidden, weight, labels, lse, accept_len=None, grad_loss=None,
+                           hidden_grad: bool = True, weight_grad: bool = True, workspace=None,
+                           out: Optional[dict] = None, status: bool = False, stream=None) -> dict:
+        """The gradients of the sum of grad_loss (float32 [B, rows]; None: 1) times ``cross_entropy``'s
+        losses, given its lse: grad_hidden and grad_weight in bfloat16, each only if it is asked for
+        (a head that is not trained costs neither its product nor its bytes)."""
+        import torch
+        head, (B, rows, V, D), shape, ws = self._head_of(hidden, weight, labels, accept_len,
+                                                         workspace, True, stream)
+        if out is None:
+            dev = hidden.device
+            out = {}
+            if hidden_grad:
+                out["grad_hidden"] = torch.empty(hidden.shape, dtype=hidden.dtype, device=dev)
+            if weight_grad:
+                out["grad_weight"] = torch.empty(weight.shape, dtype=weight.dtype, device=dev)
+            if status:
+                out["status"] = torch.empty(shape, dtype=torch.int32, device=dev)
+        gh, gw, st = (out.get(k) for k in ("grad_hidden", "grad_weight", "status"))
+        rc = spec_cross_entropy_grad(
+            self.ctx, *head, self._dense(lse, "lse", shape, torch.float32),
+            None if grad_loss is None else self._dense(grad_loss, "grad_loss", shape, torch.float32),
+            B, rows, V, D,
+            None if gh is None else
+            self._expect(gh, "grad_hidden", hidden.shape, torch.bfloat16).data_ptr(),
+            0 if gh is None else _row_stride(gh, "grad_hidden", rows, D),
+            None if gw is None else
+            self._expect(gw, "grad_weight", weight.shape, torch.bfloat16).data_ptr(),
+            0 if gw is None else _row_stride(gw, "grad_weight", 1, D),
+            None if st is None else self._dense(st, "status", shape, torch.int32), ws.data_ptr(),
+            ws.numel(),
+            stream if stream is not None else torch.cuda.current_stream(self.device).cuda_stream)
+        if rc != SV_OK:
+            raise SpecVerifyError(rc, "spec_cross_entropy_grad")
         return out
 
     def plan_distill(self, B, rows_per_seq, V, dtype=SV_BF16) -> dict:

@@ -1,4 +1,4 @@
-"""Builds libspecverify.so in-tree for sm_103a (nvcc + g++, ten translation
+"""Builds libspecverify.so in-tree for sm_103a (nvcc + g++, twelve translation
 units compiled in parallel, no cmake).  Run as ``python -m
 speculative_decoding_verification_14_gb300.build`` or through ``build()``."""
 from __future__ import annotations
@@ -16,10 +16,12 @@ BUILD_DIR = os.path.join(PKG, "_build")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CUDA_SOURCES = ("spec_verify.cu", "greedy.cu", "truncated.cu", "sampling.cu", "logprobs.cu",
-                "distill.cu")
-HOST_SOURCES = ("planner.cpp", "adapt.cpp", "sampling_planner.cpp", "distill_planner.cpp")
+                "distill.cu", "cross_entropy.cu")
+HOST_SOURCES = ("planner.cpp", "adapt.cpp", "sampling_planner.cpp", "distill_planner.cpp",
+                "cross_entropy_planner.cpp")
 HEADERS = ("sv_internal.h", "sv_context.h", "sampling_common.cuh", "sampling_weights.cuh",
-           "sampling_row.cuh", "sampling_general.cuh", "losses_common.cuh", "distill_plan.h")
+           "sampling_row.cuh", "sampling_general.cuh", "losses_common.cuh", "distill_plan.h",
+           "matrix_product.cuh", "cross_entropy.h")
 SOURCES = [os.path.join(CSRC, f) for f in (*CUDA_SOURCES, *HEADERS, *HOST_SOURCES)] + [
     os.path.join(INCLUDE, "spec_verify.h")]
 

@@ -1,0 +1,686 @@
+// cross_entropy.cu -- softmax cross entropy of a vocabulary head z = h W^T over rows of hidden states,
+// without keeping the logits, and its gradients.
+//
+//   loss = lse - z_y,  lse = ln sum_v exp z_v
+//   d_v = g (exp(z_v - lse) - [v = y]),  grad_h = sum_v d_v W_v,  grad_W_v = sum over rows of d_v h
+//
+// Rows that count are packed first (those below accept_len with a label), so that the products' work is
+// theirs alone and nothing that a padded row holds reaches the head's gradient.
+// Loss: one product whose tiles leave (maximum, sum) of each row's 256 logits, and a join of those.
+// Gradients: piece by piece of the vocabulary, the logits once more, now written as bfloat16 d
+// (a piece's d stays within 256 MB); then d W into float32 sums of the hidden states' gradient, and
+// d^T h, which is that piece's rows of the head's gradient.  d is rounded to bfloat16 (2^-8 of itself at most) since the
+// tensor cores take it so; its errors are independent from entry to entry, and both gradients sum many.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "../../include/spec_verify.h"
+#include "cross_entropy.h"
+#include "matrix_product.cuh"
+#include "sv_context.h"
+
+namespace {
+
+using namespace sv;
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// ---------------------------------------------------------------- rows that count
+
+struct Rows {
+    const __nv_bfloat16* hidden;
+    int64_t stride;
+    const int32_t* labels;
+    const int32_t* accept_len;  // or NULL
+    const float* lse;           // backward: rows whose lse is not finite have no gradient
+    const float* grad_loss;     // or NULL
+    int64_t R, V, D, depth;
+    int rows_per_seq;
+    // packed
+    int32_t* index;
+    int32_t* count;
+    int32_t* label;
+    float* packed_lse;
+    float* scale;
+    __nv_bfloat16* packed;
+    // of rows that do not count
+    float* loss;
+    float* lse_out;
+    int32_t* status;
+    uint32_t* err_word;
+    __nv_bfloat16* grad_hidden;
+    int64_t grad_stride;
+};
+
+constexpr int kRowsPerBlock = 8;
+
+// 0: counts; 1: does not; otherwise an error's code
+__device__ __forceinline__ int row_kind(const Rows& a, int64_t row) {
+    const int64_t seq = row / a.rows_per_seq;
+    if (a.accept_len && row - seq * a.rows_per_seq >= a.accept_len[seq])
+        return 1;
+    const int32_t y = a.labels[row];
+    if (y == -1)
+        return 1;
+    if (y < 0 || y >= a.V)
+        return SV_ERR_TOKEN_RANGE;
+    if (a.lse && !(fabsf(a.lse[row]) <= 3.4028235e38f))
+        return SV_ERR_NONFINITE;
+    return 0;
+}
+
+// Eight rows a block.  A block counts the rows before its own: no scan in between, and few rows
+// beside what the products take.  Blocks behind the last row clear the packed rows that fill up the
+// last block of depth.
+__global__ void __launch_bounds__(256) sv_ce_rows_kernel(const __grid_constant__ Rows a) {
+    __shared__ int before;
+    __shared__ int kinds[kRowsPerBlock];
+    const int tid = threadIdx.x;
+    const int64_t r0 = (int64_t)blockIdx.x * kRowsPerBlock, end = r0 < a.R ? r0 : a.R;
+    if (tid == 0)
+        before = 0;
+    __syncthreads();
+    int n = 0;
+    for (int64_t r = tid; r < end; r += blockDim.x)
+        n += row_kind(a, r) == 0;
+    n = __reduce_add_sync(0xffffffffu, n);
+    if ((tid & 31) == 0 && n)
+        atomicAdd(&before, n);
+    if (tid < kRowsPerBlock)
+        kinds[tid] = r0 + tid < a.R ? row_kind(a, r0 + tid) : 1;
+    __syncthreads();
+    if (r0 >= a.R) {  // one row of filling per block
+        const int64_t at = before + (int64_t)blockIdx.x - (a.R + kRowsPerBlock - 1) / kRowsPerBlock;
+        if (at < (before + kBlockK - 1) / kBlockK * (int64_t)kBlockK)
+            for (int64_t d = tid; d < a.depth; d += blockDim.x)
+                a.packed[at * a.depth + d] = __float2bfloat16_rn(0.0f);
+        return;
+    }
+    int64_t at = before;
+    for (int i = 0; i < kRowsPerBlock && r0 + i < a.R; ++i) {
+        const int64_t row = r0 + i;
+        const int kind = kinds[i];
+        if (kind == 0) {
+            const __nv_bfloat16* src = a.hidden + row * a.stride;
+            __nv_bfloat16* dst = a.packed + at * a.depth;
+            if ((reinterpret_cast<uintptr_t>(src) & 15u) == 0) {
+                for (int64_t d = tid; d < a.D / 8; d += blockDim.x)
+                    reinterpret_cast<uint4*>(dst)[d] = reinterpret_cast<const uint4*>(src)[d];
+                for (int64_t d = a.D / 8 * 8 + tid; d < a.D; d += blockDim.x)
+                    dst[d] = src[d];
+            } else {
+                for (int64_t d = tid; d < a.D; d += blockDim.x)
+                    dst[d] = src[d];
+            }
+            if (tid == 0) {
+                a.index[at] = (int32_t)row;
+                a.label[at] = a.labels[row];
+                if (a.packed_lse) {
+                    if (a.status)
+                        a.status[row] = SV_OK;
+                    a.packed_lse[at] = a.lse[row];
+                    a.scale[at] = a.grad_loss ? a.grad_loss[row] : 1.0f;
+                }
+            }
+            ++at;
+            continue;
+        }
+        const float nan = __int_as_float(0x7fffffff), x = kind == 1 ? 0.0f : nan;
+        if (tid == 0) {
+            if (a.loss)
+                a.loss[row] = x;
+            if (a.lse_out)
+                a.lse_out[row] = x;
+            if (a.status)
+                a.status[row] = kind == 1 ? SV_OK : kind;
+            if (kind != 1)
+                atomicOr(a.err_word, 1u << kind);
+        }
+        if (a.grad_hidden)
+            for (int64_t d = tid; d < a.D; d += blockDim.x)
+                a.grad_hidden[row * a.grad_stride + d] = __float2bfloat16_rn(x);
+    }
+    if (tid == 0 && r0 + kRowsPerBlock >= a.R)
+        *a.count = (int32_t)at;
+}
+
+// ---------------------------------------------------------------- tiles
+
+struct Tiles {
+    CUtensorMap a, b;
+    const int32_t* count;
+    const int32_t* label;
+    uint32_t* err_word;
+    int64_t V, D;
+    int64_t first_tile, tiles;  // vocabulary tiles of this launch
+    int64_t rows;               // of the workspace
+    // loss
+    float2* stats;
+    float* label_logit;
+    // gradients
+    const float* lse;
+    const float* scale;
+    __nv_bfloat16* probs;
+    int64_t probs_stride;
+    float* sums;
+    int64_t depth;
+    int splits, add;
+    __nv_bfloat16* out;
+    int64_t out_stride;
+    int out_vectors;  // rows of out lie on 16 bytes
+};
+
+__device__ __forceinline__ int64_t packed_rows(const Tiles& p) { return *p.count; }
+// the row of a tile that this thread has in tensor memory
+__device__ __forceinline__ int64_t tile_row(int64_t tile) {
+    uint32_t rank;
+    asm("mov.u32 %0, %cluster_ctarank;" : "=r"(rank));
+    return tile * kTile + rank * kHalf + (threadIdx.x & 127);
+}
+
+// (maximum, sum of exponentials) of each row's logits in each tile of the vocabulary
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsMm, 1)
+    sv_ce_stats_kernel(const __grid_constant__ Tiles p) {
+    const int64_t n = packed_rows(p);
+    const MatrixShape shape{(n + kTile - 1) / kTile, p.tiles, (p.D + kBlockK - 1) / kBlockK, 1};
+    run_tiles<false, false>(&p.a, &p.b, shape, 0, 0, p.err_word, 1u << SV_ERR_TIMEOUT,
+                            [&](int64_t rt, int64_t ct, int, auto load) {
+        const int64_t row = tile_row(rt), c0 = ct * kTile;
+        const bool there = row < n;
+        const int64_t y = there ? p.label[row] - c0 : -1;
+        float m = -__int_as_float(0x7f800000), s = 0.0f, zy = 0.0f;
+        for (int c = 0; c < kTile; c += 32) {
+            float v[32];
+            load(c, v);
+            const int left = (int)(p.V - c0 - c < 32 ? p.V - c0 - c : 32);  // columns of the vocabulary
+            if (left <= 0)
+                break;
+            float top = m;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+                if (e >= left)
+                    v[e] = -__int_as_float(0x7f800000);
+                // a NaN has to reach the sum
+                asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(v[e]));
+            }
+            if (y >= c && y < c + 32) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    if (y == c + e)
+                        zy = v[e];
+            }
+            const float base = top > -__int_as_float(0x7f800000) ? top : 0.0f;
+            float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                part[e & 3] += ex2((v[e] - base) * kLog2e);
+            s = s * ex2((m - base) * kLog2e) + ((part[0] + part[1]) + (part[2] + part[3]));
+            m = top;
+            if (!(top == top))
+                s = top;
+        }
+        if (there) {
+            p.stats[ct * p.rows + row] = make_float2(m, s);
+            if (y >= 0 && y < kTile)
+                p.label_logit[row] = zy;
+        }
+    });
+}
+
+// d of a piece of the vocabulary, bfloat16; zeros in rows and columns that only fill up tiles
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsMm, 1)
+    sv_ce_probs_kernel(const __grid_constant__ Tiles p) {
+    const int64_t n = packed_rows(p);
+    const MatrixShape shape{(n + kTile - 1) / kTile, p.tiles, (p.D + kBlockK - 1) / kBlockK, 1};
+    run_tiles<false, false>(&p.a, &p.b, shape, p.first_tile * kTile, 0, p.err_word, 1u << SV_ERR_TIMEOUT,
+                            [&](int64_t rt, int64_t ct, int, auto load) {
+        const int64_t row = tile_row(rt), c0 = (p.first_tile + ct) * kTile;
+        const bool there = row < n;
+        const int64_t y = there ? p.label[row] - c0 : -1;
+        const float lse = there ? p.lse[row] : 0.0f, g = there ? p.scale[row] : 0.0f;
+        __nv_bfloat16* out = p.probs + row * p.probs_stride + ct * kTile;
+        for (int c = 0; c < kTile; c += 32) {
+            float v[32];
+            load(c, v);
+            const int left = there ? (int)(p.V - c0 - c < 32 ? p.V - c0 - c : 32) : 0;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+                float d = ex2((v[e] - lse) * kLog2e);
+                if (y == c + e)
+                    d -= 1.0f;
+                v[e] = e < left ? d * g : 0.0f;
+            }
+            uint4* to = reinterpret_cast<uint4*>(out + c);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[e]) : "f"(v[q * 8 + 2 * e + 1]), "f"(v[q * 8 + 2 * e]));
+                to[q] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+    });
+}
+
+// a piece's part of the hidden states' gradient: float32 sums, those of a split apart
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsMm, 1)
+    sv_ce_hidden_kernel(const __grid_constant__ Tiles p) {
+    const int64_t n = packed_rows(p);
+    const MatrixShape shape{(n + kTile - 1) / kTile, (p.D + kTile - 1) / kTile, p.tiles * (kTile / kBlockK), p.splits};
+    run_tiles<false, true>(&p.a, &p.b, shape, 0, p.first_tile * kTile, p.err_word, 1u << SV_ERR_TIMEOUT,
+                           [&](int64_t rt, int64_t ct, int split, auto load) {
+        const int64_t row = tile_row(rt), c0 = ct * kTile;
+        float* out = p.sums + ((int64_t)split * p.rows + row) * p.depth + c0;
+        for (int c = 0; c < kTile && c0 + c < p.D; c += 32) {
+            float v[32];
+            load(c, v);
+            if (row >= n)
+                continue;
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (c0 + c + 4 * q < p.depth) {
+                    float4* to = reinterpret_cast<float4*>(out + c) + q;
+                    float4 x = p.add ? *to : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    x.x += v[4 * q], x.y += v[4 * q + 1], x.z += v[4 * q + 2], x.w += v[4 * q + 3];
+                    *to = x;
+                }
+        }
+    });
+}
+
+// a piece's rows of the head's gradient
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsMm, 1)
+    sv_ce_weight_kernel(const __grid_constant__ Tiles p) {
+    const int64_t n = packed_rows(p);
+    const MatrixShape shape{p.tiles, (p.D + kTile - 1) / kTile, (n + kBlockK - 1) / kBlockK, 1};
+    run_tiles<true, true>(&p.a, &p.b, shape, 0, 0, p.err_word, 1u << SV_ERR_TIMEOUT,
+                          [&](int64_t rt, int64_t ct, int, auto load) {
+        const int64_t v_id = p.first_tile * kTile + tile_row(rt), c0 = ct * kTile;
+        __nv_bfloat16* out = p.out + v_id * p.out_stride + c0;
+        for (int c = 0; c < kTile && c0 + c < p.D; c += 32) {
+            float v[32];
+            load(c, v);
+            if (v_id >= p.V)
+                continue;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if (p.out_vectors && c0 + c + 8 * q + 8 <= p.D) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
+                            : "=r"(w[e])
+                            : "f"(v[q * 8 + 2 * e + 1]), "f"(v[q * 8 + 2 * e]));
+                    reinterpret_cast<uint4*>(out + c)[q] = make_uint4(w[0], w[1], w[2], w[3]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (c0 + c + 8 * q + e < p.D)
+                            out[c + 8 * q + e] = __float2bfloat16_rn(v[8 * q + e]);
+                }
+            }
+        }
+    });
+}
+
+// ---------------------------------------------------------------- joins
+
+struct Join {
+    const int32_t* count;
+    const int32_t* index;
+    int64_t rows, tiles, D, depth;
+    const float2* stats;
+    const float* label_logit;
+    float* loss;
+    float* lse;
+    int32_t* status;
+    uint32_t* err_word;
+    const float* sums;
+    int splits;
+    __nv_bfloat16* grad_hidden;
+    int64_t grad_stride;
+};
+
+// 32 rows a block, their tiles over 8 threads each
+__global__ void __launch_bounds__(256) sv_ce_join_kernel(const __grid_constant__ Join a) {
+    __shared__ float2 part[8][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t row = (int64_t)blockIdx.x * 32 + lane;
+    const int64_t n = *a.count;
+    if ((int64_t)blockIdx.x * 32 >= n)
+        return;
+    const float inf = __int_as_float(0x7f800000);
+    float m = -inf, s = 0.0f;
+    const auto join = [&](float m1, float s1) {
+        float top = m;
+        asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(m1));
+        s = (m > -inf ? s * ex2((m - top) * kLog2e) : 0.0f) + (m1 > -inf ? s1 * ex2((m1 - top) * kLog2e) : 0.0f);
+        m = top;
+    };
+    if (row < n)
+        for (int64_t t = warp; t < a.tiles; t += 8) {
+            const float2 x = a.stats[t * a.rows + row];
+            join(x.x, x.y);
+        }
+    part[warp][lane] = make_float2(m, s);
+    __syncthreads();
+    if (warp || row >= n)
+        return;
+    for (int w = 1; w < 8; ++w)
+        join(part[w][lane].x, part[w][lane].y);
+    const int64_t to = a.index[row];
+    const bool good = m > -inf && m < inf;
+    const float ls = logf(s), nan = __int_as_float(0x7fffffff);
+    a.loss[to] = good ? (m - a.label_logit[row]) + ls : nan;
+    a.lse[to] = good ? m + ls : nan;
+    if (a.status)
+        a.status[to] = good ? SV_OK : SV_ERR_NONFINITE;
+    if (!good)
+        atomicOr(a.err_word, 1u << SV_ERR_NONFINITE);
+}
+
+// a row a block: the splits' sums, rounded once
+__global__ void __launch_bounds__(256) sv_ce_hidden_join_kernel(const __grid_constant__ Join a) {
+    const int64_t row = blockIdx.x;
+    if (row >= *a.count)
+        return;
+    __nv_bfloat16* out = a.grad_hidden + (int64_t)a.index[row] * a.grad_stride;
+    for (int64_t d = threadIdx.x; d < a.D; d += blockDim.x) {
+        float x = 0.0f;
+        for (int s = 0; s < a.splits; ++s)
+            x += a.sums[((int64_t)s * a.rows + row) * a.depth + d];
+        out[d] = __float2bfloat16_rn(x);
+    }
+}
+
+// ---------------------------------------------------------------- host
+
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encoder() {
+    static std::atomic<void*> fn{nullptr};
+    void* f = fn.load(std::memory_order_acquire);
+    if (!f) {
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) !=
+                cudaSuccess ||
+            found != cudaDriverEntryPointSuccess) {
+            (void)cudaGetLastError();
+            return nullptr;
+        }
+        fn.store(f, std::memory_order_release);
+    }
+    return reinterpret_cast<EncodeFn>(f);
+}
+
+// A bfloat16 matrix [rows, columns] as boxes of 64 columns and `box` rows; what lies beyond is zeros.
+bool tensor_map(CUtensorMap* map, const void* base, int64_t rows, int64_t columns, int64_t stride, int box) {
+    const EncodeFn encode = encoder();
+    if (!encode)
+        return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)columns, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)stride * 2};
+    const cuuint32_t boxes[2] = {64, (cuuint32_t)box}, steps[2] = {1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, boxes, steps,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+typedef void (*TilesFn)(const Tiles);
+
+// Attributes of the kernels on a device, and how many pairs run at once.
+int matrix_pairs(int device) {
+    static std::atomic<int> pairs[64];
+    if (device < 0 || device >= 64)
+        return 0;
+    int n = pairs[device].load(std::memory_order_acquire);
+    if (n)
+        return n;
+    int least = 1 << 30;
+    for (TilesFn fn : {sv_ce_stats_kernel, sv_ce_probs_kernel, sv_ce_hidden_kernel, sv_ce_weight_kernel}) {
+        if (cudaFuncSetAttribute((const void*)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMm) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return 0;
+        }
+        cudaLaunchConfig_t cfg;
+        std::memset(&cfg, 0, sizeof cfg);
+        cfg.gridDim = dim3(2, 1, 1);
+        cfg.blockDim = dim3(kThreadsMm, 1, 1);
+        cfg.dynamicSmemBytes = kSmemMm;
+        int clusters = 0;
+        if (cudaOccupancyMaxActiveClusters(&clusters, (const void*)fn, &cfg) != cudaSuccess || clusters < 1) {
+            (void)cudaGetLastError();
+            return 0;
+        }
+        least = clusters < least ? clusters : least;
+    }
+    pairs[device].store(least, std::memory_order_release);
+    return least;
+}
+
+bool launch_tiles(TilesFn fn, const Tiles& p, int64_t most, int pairs, cudaStream_t stream) {
+    const int64_t n = most < pairs ? most : pairs;
+    fn<<<dim3((unsigned)(2 * (n < 1 ? 1 : n))), kThreadsMm, kSmemMm, stream>>>(p);
+    return cudaGetLastError() == cudaSuccess;
+}
+
+int check(const sv_ctx* ctx, const void* hidden, int dtype, int64_t hidden_stride, const void* weight,
+          int64_t weight_stride, const int32_t* labels, const int32_t* accept_len, int B, int rows_per_seq, int64_t V,
+          int64_t D, const void* workspace, size_t workspace_bytes, bool grad, CrossEntropyPlan* plan) {
+    if (!ctx || !hidden || !weight || !labels || !workspace || (dtype != SV_F32 && dtype != SV_BF16))
+        return SV_ERR_INVALID_ARG;
+    const int64_t most = (int64_t)1 << 40;
+    if (B < 1 || B > ctx->max_B || rows_per_seq < 1 || rows_per_seq > ctx->max_K + 1 || V < 1 || V > ctx->max_V ||
+        V > ((int64_t)1 << 31) - 1 || D < 1 || D > ((int64_t)1 << 20) || (int64_t)B * rows_per_seq > (1 << 24) ||
+        hidden_stride < D || hidden_stride > most || weight_stride < D || weight_stride > ((int64_t)1 << 32) ||
+        (double)B * rows_per_seq * (double)hidden_stride >= 1099511627776.0 ||  // 2^40
+        (double)V * (double)weight_stride >= 1099511627776.0)
+        return SV_ERR_INVALID_ARG;
+    if (dtype != SV_BF16)
+        return SV_ERR_UNSUPPORTED;
+    // the copy engine takes the weight's rows on 16 bytes
+    if (!aligned(hidden, 2) || !aligned(weight, 16) || weight_stride % 8 || !aligned(labels, 4) ||
+        !aligned(accept_len, 4) || !aligned(workspace, 256))
+        return SV_ERR_INVALID_ARG;
+    *plan = cross_entropy_plan(ctx->num_sms, (int64_t)B * rows_per_seq, V, D, grad);
+    return workspace_bytes < plan->total ? SV_ERR_INVALID_ARG : SV_OK;
+}
+
+Rows pack_args(const CrossEntropyPlan& plan, unsigned char* ws, const void* hidden, int64_t stride,
+               const int32_t* labels, const int32_t* accept_len, int B, int rows_per_seq, int64_t V, int64_t D,
+               uint32_t* err_word) {
+    Rows r;
+    std::memset(&r, 0, sizeof r);
+    r.hidden = static_cast<const __nv_bfloat16*>(hidden);
+    r.stride = stride;
+    r.labels = labels;
+    r.accept_len = accept_len;
+    r.R = (int64_t)B * rows_per_seq;
+    r.V = V;
+    r.D = D;
+    r.depth = plan.depth;
+    r.rows_per_seq = rows_per_seq;
+    r.index = reinterpret_cast<int32_t*>(ws + plan.index);
+    r.count = r.index + plan.rows;
+    r.label = reinterpret_cast<int32_t*>(ws + plan.label);
+    r.packed = reinterpret_cast<__nv_bfloat16*>(ws + plan.hidden);
+    r.err_word = err_word;
+    return r;
+}
+
+}  // namespace
+
+extern "C" {
+
+int spec_cross_entropy_workspace(sv_ctx* ctx, int B, int rows_per_seq, int64_t V, int64_t D, int grad, size_t* bytes) {
+    if (!ctx)
+        return SV_ERR_INVALID_ARG;
+    return spec_cross_entropy_workspace_for(ctx->num_sms, B, rows_per_seq, V, D, grad, bytes);
+}
+
+int spec_cross_entropy_run(sv_ctx* ctx, const void* hidden, int dtype, int64_t hidden_stride, const void* weight,
+                           int64_t weight_stride, const int32_t* labels, const int32_t* accept_len, int B,
+                           int rows_per_seq, int64_t V, int64_t D, float* loss, float* lse, int32_t* status,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+    CrossEntropyPlan plan;
+    const int rc = check(ctx, hidden, dtype, hidden_stride, weight, weight_stride, labels, accept_len, B, rows_per_seq,
+                         V, D, workspace, workspace_bytes, false, &plan);
+    if (rc != SV_OK)
+        return rc;
+    if (!loss || !lse || !aligned(loss, 4) || !aligned(lse, 4) || !aligned(status, 4))
+        return SV_ERR_INVALID_ARG;
+    DeviceGuard guard(ctx->device);
+    const int pairs = matrix_pairs(ctx->device);
+    if (!pairs)
+        return SV_ERR_CUDA;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    Rows r = pack_args(plan, ws, hidden, hidden_stride, labels, accept_len, B, rows_per_seq, V, D, ctx->d_err);
+    r.loss = loss;
+    r.lse_out = lse;
+    r.status = status;
+    Tiles p;
+    std::memset(&p, 0, sizeof p);
+    if (!tensor_map(&p.a, r.packed, plan.rows, D, plan.depth, kHalf) ||
+        !tensor_map(&p.b, weight, V, D, weight_stride, kHalf))
+        return SV_ERR_CUDA;
+    p.count = r.count;
+    p.label = r.label;
+    p.err_word = ctx->d_err;
+    p.V = V;
+    p.D = D;
+    p.tiles = plan.vocab_tiles;
+    p.rows = plan.rows;
+    p.stats = reinterpret_cast<float2*>(ws + plan.stats);
+    p.label_logit = reinterpret_cast<float*>(ws + plan.label_logit);
+    Join j;
+    std::memset(&j, 0, sizeof j);
+    j.count = r.count;
+    j.index = r.index;
+    j.rows = plan.rows;
+    j.tiles = plan.vocab_tiles;
+    j.stats = p.stats;
+    j.label_logit = p.label_logit;
+    j.loss = loss;
+    j.lse = lse;
+    j.status = status;
+    j.err_word = ctx->d_err;
+    sv_ce_rows_kernel<<<(unsigned)((r.R + kRowsPerBlock - 1) / kRowsPerBlock), 256, 0, st>>>(r);
+    if (cudaGetLastError() != cudaSuccess ||
+        !launch_tiles(sv_ce_stats_kernel, p, plan.rows / kTile * plan.vocab_tiles, pairs, st))
+        return SV_ERR_CUDA;
+    sv_ce_join_kernel<<<(unsigned)((r.R + 31) / 32), 256, 0, st>>>(j);
+    return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}
+
+int spec_cross_entropy_grad(sv_ctx* ctx, const void* hidden, int dtype, int64_t hidden_stride, const void* weight,
+                            int64_t weight_stride, const int32_t* labels, const int32_t* accept_len, const float* lse,
+                            const float* grad_loss, int B, int rows_per_seq, int64_t V, int64_t D, void* grad_hidden,
+                            int64_t grad_hidden_stride, void* grad_weight, int64_t grad_weight_stride, int32_t* status,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+    CrossEntropyPlan plan;
+    const int rc = check(ctx, hidden, dtype, hidden_stride, weight, weight_stride, labels, accept_len, B, rows_per_seq,
+                         V, D, workspace, workspace_bytes, true, &plan);
+    if (rc != SV_OK)
+        return rc;
+    const int64_t R = (int64_t)B * rows_per_seq, most = (int64_t)1 << 40;
+    if (!lse || (!grad_hidden && !grad_weight) || !aligned(lse, 4) || !aligned(grad_loss, 4) ||
+        !aligned(grad_hidden, 2) || !aligned(grad_weight, 2) || !aligned(status, 4) ||
+        (grad_hidden && (grad_hidden_stride < D || grad_hidden_stride > most ||
+                         (double)R * (double)grad_hidden_stride >= 1099511627776.0)) ||
+        (grad_weight && (grad_weight_stride < D || grad_weight_stride > most ||
+                         (double)V * (double)grad_weight_stride >= 1099511627776.0)))
+        return SV_ERR_INVALID_ARG;
+    DeviceGuard guard(ctx->device);
+    const int pairs = matrix_pairs(ctx->device);
+    if (!pairs)
+        return SV_ERR_CUDA;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    Rows r = pack_args(plan, ws, hidden, hidden_stride, labels, accept_len, B, rows_per_seq, V, D, ctx->d_err);
+    r.lse = lse;
+    r.grad_loss = grad_loss;
+    r.packed_lse = reinterpret_cast<float*>(ws + plan.lse);
+    r.scale = reinterpret_cast<float*>(ws + plan.scale);
+    r.status = status;
+    r.grad_hidden = static_cast<__nv_bfloat16*>(grad_hidden);
+    r.grad_stride = grad_hidden_stride;
+    __nv_bfloat16* probs = reinterpret_cast<__nv_bfloat16*>(ws + plan.probs);
+    const int64_t width = plan.piece_tiles * kTile;
+    Tiles logits, hid, wgt;
+    std::memset(&logits, 0, sizeof logits);
+    logits.count = r.count;
+    logits.label = r.label;
+    logits.err_word = ctx->d_err;
+    logits.V = V;
+    logits.D = D;
+    logits.rows = plan.rows;
+    logits.lse = r.packed_lse;
+    logits.scale = r.scale;
+    logits.probs = probs;
+    logits.probs_stride = width;
+    logits.sums = reinterpret_cast<float*>(ws + plan.sums);
+    logits.depth = plan.depth;
+    logits.splits = plan.splits;
+    logits.out = static_cast<__nv_bfloat16*>(grad_weight);
+    logits.out_stride = grad_weight_stride;
+    logits.out_vectors = aligned(grad_weight, 16) && grad_weight_stride % 8 == 0;
+    hid = wgt = logits;
+    if (!tensor_map(&logits.a, r.packed, plan.rows, D, plan.depth, kHalf) ||
+        !tensor_map(&logits.b, weight, V, D, weight_stride, kHalf) ||
+        !tensor_map(&hid.a, probs, plan.rows, width, width, kHalf) ||
+        !tensor_map(&hid.b, weight, V, D, weight_stride, kBlockK) ||
+        !tensor_map(&wgt.a, probs, plan.rows, width, width, kBlockK) ||
+        !tensor_map(&wgt.b, r.packed, plan.rows, D, plan.depth, kBlockK))
+        return SV_ERR_CUDA;
+    sv_ce_rows_kernel<<<(unsigned)((R + kRowsPerBlock - 1) / kRowsPerBlock + kBlockK), 256, 0, st>>>(r);
+    if (cudaGetLastError() != cudaSuccess)
+        return SV_ERR_CUDA;
+    const int64_t row_tiles = plan.rows / kTile, depth_tiles = (D + kTile - 1) / kTile;
+    for (int64_t piece = 0; piece < plan.pieces; ++piece) {
+        const int64_t first = piece * plan.piece_tiles;
+        const int64_t tiles = plan.vocab_tiles - first < plan.piece_tiles ? plan.vocab_tiles - first : plan.piece_tiles;
+        for (Tiles* t : {&logits, &hid, &wgt}) {
+            t->first_tile = first;
+            t->tiles = tiles;
+            t->add = piece > 0;
+        }
+        if (!launch_tiles(sv_ce_probs_kernel, logits, row_tiles * tiles, pairs, st) ||
+            (grad_hidden && !launch_tiles(sv_ce_hidden_kernel, hid, row_tiles * depth_tiles * plan.splits, pairs, st)) ||
+            (grad_weight && !launch_tiles(sv_ce_weight_kernel, wgt, tiles * depth_tiles, pairs, st)))
+            return SV_ERR_CUDA;
+    }
+    if (grad_hidden) {
+        Join j;
+        std::memset(&j, 0, sizeof j);
+        j.count = r.count;
+        j.index = r.index;
+        j.rows = plan.rows;
+        j.D = D;
+        j.depth = plan.depth;
+        j.sums = logits.sums;
+        j.splits = plan.splits;
+        j.grad_hidden = r.grad_hidden;
+        j.grad_stride = grad_hidden_stride;
+        sv_ce_hidden_join_kernel<<<(unsigned)R, 256, 0, st>>>(j);
+        if (cudaGetLastError() != cudaSuccess)
+            return SV_ERR_CUDA;
+    }
+    return SV_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,34 @@
+// cross_entropy.h -- sizes and workspace of the cross-entropy calls, shared by their planner and their
+// kernels.  Not part of the public ABI.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+namespace sv {
+
+constexpr int kTile = 256;             // rows and columns of a CTA pair's tile
+constexpr int kHalf = kTile / 2;       // of one CTA's operands
+constexpr int kBlockK = 64;            // depth of a stage: 128 bytes, one swizzle atom
+constexpr int64_t kPieceBytes = (int64_t)1 << 28;  // draft of a piece's probabilities
+constexpr int kMaxSplits = 16;
+
+// What a call keeps in its workspace: offsets in bytes.
+struct CrossEntropyPlan {
+    int64_t rows;        // R rounded up to a tile
+    int64_t depth;       // D rounded up to 16 bytes: the packed rows' stride
+    int64_t vocab_tiles;
+    int64_t piece_tiles; // of one piece of the vocabulary
+    int64_t pieces;
+    int splits;          // of a piece's depth in the hidden states' gradient
+    size_t index, label, lse, scale;    // [rows]: source row, label, lse, grad_loss
+    size_t hidden;                      // bf16 [rows, depth]
+    size_t stats, label_logit;          // float2 [vocab_tiles, rows], float [rows]
+    size_t probs;                       // bf16 [rows, piece_tiles * kTile]
+    size_t sums;                        // float [splits, rows, depth]
+    size_t total;
+};
+
+CrossEntropyPlan cross_entropy_plan(int num_sms, int64_t R, int64_t V, int64_t D, bool grad);
+
+}  // namespace sv

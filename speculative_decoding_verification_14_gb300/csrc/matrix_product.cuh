@@ -1,0 +1,320 @@
+// matrix_product.cuh -- tiles of a bfloat16 matrix product on the tensor cores, for kernels that do
+// something with each tile instead of writing it.
+//
+// A pair of CTAs (a cluster of two) computes a tile of 256 x 256: each holds 128 rows of A and 128 rows
+// of B per stage, in 64 elements of depth, and the products of all of them go to the tensor memory of
+// the CTA that holds the rows of A (tcgen05.mma, cta_group::2).  Pairs are persistent and take tiles in
+// turn.  One thread of each CTA issues the copies (cp.async.bulk.tensor, 128-byte swizzle) that fill its
+// ring of stages, one thread of the first CTA the products, and four warps of each CTA take the finished
+// tile out of tensor memory, where two tiles have room: the next one's products run meanwhile.
+// An operand lies in memory with its depth contiguous, or with its rows contiguous ("turned": the
+// probabilities as [v, r] and the weight as [d, v] are read from [r, v] and [v, d] as they lie).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "cross_entropy.h"
+#include "losses_common.cuh"
+
+namespace sv {
+
+constexpr int kStagesMm = 6;
+constexpr int kOperandBytes = kHalf * kBlockK * 2;  // one operand of one stage: 16 KB
+constexpr int kStageBytes = 2 * kOperandBytes;
+constexpr int kThreadsMm = 256;  // warps: copies, products, tensor memory, none, four for tiles
+constexpr int kTmemColumns = 512;
+constexpr int kSmemMm = kStagesMm * kStageBytes + 1024;  // and the distance to a multiple of 1024
+
+struct MatrixBarriers {
+    uint64_t full[kStagesMm], empty[kStagesMm], tile_full[2], tile_empty[2];
+    uint32_t tmem, failed;
+};
+
+__device__ __forceinline__ uint32_t first_cta(uint32_t addr) {  // the same place in the pair's first CTA
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+    return r;
+}
+__device__ __forceinline__ void barrier_arrive_cluster(uint32_t addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+__device__ __forceinline__ bool barrier_try_cluster(uint64_t* bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(shared_addr(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+// Waits for a phase, at most kWaitNs; whoever gives up says so to the CTA's other warps, which then give up too.
+static __device__ __noinline__ bool matrix_wait_slow(uint64_t* bar, uint32_t parity, volatile uint32_t* failed) {
+    const unsigned long long t0 = global_ns();
+    while (!*failed) {
+        for (int i = 0; i < 64; ++i)
+            if (barrier_try_cluster(bar, parity))
+                return true;
+        if (global_ns() - t0 > kWaitNs)
+            *failed = 1;
+    }
+    return false;
+}
+__device__ __forceinline__ bool matrix_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* failed) {
+    return barrier_try_cluster(bar, parity) || matrix_wait_slow(bar, parity, failed);
+}
+
+__device__ __forceinline__ void copy_tile(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+            dst),
+        "l"(map), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+}
+
+// Shared-memory descriptor of an operand: 128-byte swizzle.  Depth contiguous: rows of 128 bytes, groups of
+// eight rows 1024 apart.  Turned: 64 rows of the operand side by side in 128 bytes, groups of eight
+// depths 1024 apart, the next 64 rows 8192 on.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool turned) {
+    uint64_t d = (uint64_t)((addr & 0x3ffffu) >> 4);
+    d |= (uint64_t)((turned ? 8192u : 16u) >> 4) << 16;
+    d |= (uint64_t)(1024u >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+// bf16 x bf16 -> f32, 256 x 256
+__host__ __device__ constexpr uint32_t product_desc(bool turned_a, bool turned_b) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((turned_a ? 1u : 0u) << 15) | ((turned_b ? 1u : 0u) << 16) |
+           ((uint32_t)(kTile >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
+}
+__device__ __forceinline__ void product(uint32_t tmem, uint64_t a, uint64_t b, uint32_t desc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem),
+        "l"(a), "l"(b), "r"(desc), "r"((uint32_t)add)
+        : "memory");
+}
+// the products issued so far arrive on this barrier of both CTAs when they are done
+__device__ __forceinline__ void products_arrive(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            shared_addr(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+// 32 columns of this warp's 32 rows
+__device__ __forceinline__ void load_columns(uint32_t addr, float (&v)[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr)
+        : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        v[i] = __uint_as_float(r[i]);
+}
+
+// What a pair computes: `rows` x `columns` tiles, each over blocks k0 .. k1 - 1 of its split of the depth.
+struct MatrixShape {
+    int64_t row_tiles, column_tiles, blocks;
+    int splits;
+    __device__ __forceinline__ int64_t tiles() const { return row_tiles * column_tiles * splits; }
+    // Pairs that run at the same time share operands in L2: eight row tiles at a time, columns within them.
+    __device__ __forceinline__ void tile(int64_t i, int64_t& row, int64_t& column, int& split) const {
+        const int64_t one = row_tiles * column_tiles;
+        split = (int)(i / one);
+        i -= split * one;
+        const int64_t group = i / (8 * column_tiles), first = group * 8, in = i - first * column_tiles;
+        const int64_t height = row_tiles - first < 8 ? row_tiles - first : 8;
+        row = first + in % height;
+        column = in / height;
+    }
+    __device__ __forceinline__ void depth(int split, int64_t& k0, int64_t& k1) const {
+        k0 = blocks * split / splits;
+        k1 = blocks * (split + 1) / splits;
+    }
+};
+
+// Runs the pair's tiles.  a0, b0: rows (columns for a turned operand) at which the operands begin in their maps,
+// ka, kb: depths likewise.  finish(row tile, column tile, split, load) is called by the four tile warps of each CTA
+// for each tile; load(c, v) gives columns c .. c + 31 of the thread's row, and has to be called by whole warps;
+// without a single block of depth the tile is all zeros and load gives them.
+template <bool TurnedA, bool TurnedB, typename Finish>
+__device__ __forceinline__ void run_tiles(const CUtensorMap* map_a, const CUtensorMap* map_b, const MatrixShape& shape,
+                                          int64_t b0, int64_t kb, uint32_t* err_word, uint32_t timeout_bit,
+                                          Finish finish) {
+    extern __shared__ unsigned char dynamic[];
+    __shared__ MatrixBarriers bars;
+    const uint32_t stage0 = (shared_addr(dynamic) + 1023u) & ~1023u;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t rank;
+    asm("mov.u32 %0, %cluster_ctarank;" : "=r"(rank));
+    const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    volatile uint32_t* failed = &bars.failed;
+
+    if (warp == 0 && lane == 0) {
+        for (int s = 0; s < kStagesMm; ++s) {
+            barrier_init(&bars.full[s], 1);
+            barrier_init(&bars.empty[s], 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            barrier_init(&bars.tile_full[t], 1);
+            barrier_init(&bars.tile_empty[t], 8);  // four warps of two CTAs
+        }
+        bars.failed = 0;
+        barrier_init_fence();
+    }
+    if (warp == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(shared_addr(&bars.tmem)),
+                     "r"(kTmemColumns)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    const uint32_t tmem = *(volatile uint32_t*)&bars.tmem;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            bool go = true;
+            for (int64_t i = pair; go && i < shape.tiles(); i += pairs) {
+                int64_t row, column, k0, k1;
+                int split;
+                shape.tile(i, row, column, split);
+                shape.depth(split, k0, k1);
+                const int ra = (int)(row * kTile + rank * kHalf), rb = (int)(b0 + column * kTile + rank * kHalf);
+                for (int64_t k = k0; k < k1; ++k) {
+                    if (!matrix_wait(&bars.empty[stage], phase ^ 1u, failed)) {
+                        go = false;
+                        break;
+                    }
+                    // both CTAs' copies arrive on the first one's barrier
+                    const uint32_t bar = first_cta(shared_addr(&bars.full[stage]));
+                    if (rank == 0)
+                        barrier_expect(&bars.full[stage], 2 * kStageBytes);
+                    const uint32_t at = stage0 + stage * kStageBytes, bt = at + kOperandBytes;
+                    const int da = (int)(k * kBlockK), db = (int)(kb + k * kBlockK);
+                    if constexpr (TurnedA) {
+                        copy_tile(at, map_a, ra, da, bar);
+                        copy_tile(at + kOperandBytes / 2, map_a, ra + 64, da, bar);
+                    } else {
+                        copy_tile(at, map_a, da, ra, bar);
+                    }
+                    if constexpr (TurnedB) {
+                        copy_tile(bt, map_b, rb, db, bar);
+                        copy_tile(bt + kOperandBytes / 2, map_b, rb + 64, db, bar);
+                    } else {
+                        copy_tile(bt, map_b, db, rb, bar);
+                    }
+                    if (++stage == kStagesMm)
+                        stage = 0, phase ^= 1u;
+                }
+            }
+            // until every stage was read: the last arrivals on this CTA's barriers are in
+            for (int s = 0; go && s < kStagesMm; ++s) {
+                go = matrix_wait(&bars.empty[stage], phase ^ 1u, failed);
+                if (++stage == kStagesMm)
+                    stage = 0, phase ^= 1u;
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (rank == 0 && lane == 0) {
+            int stage = 0, t = 0;
+            uint32_t phase = 0, tphase = 0;
+            bool go = true;
+            for (int64_t i = pair; go && i < shape.tiles(); i += pairs) {
+                int64_t row, column, k0, k1;
+                int split;
+                shape.tile(i, row, column, split);
+                shape.depth(split, k0, k1);
+                if (k0 == k1)
+                    continue;
+                if (!matrix_wait(&bars.tile_empty[t], tphase ^ 1u, failed))
+                    break;
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                const uint32_t d = tmem + t * kTile;
+                for (int64_t k = k0; k < k1; ++k) {
+                    if (!matrix_wait(&bars.full[stage], phase, failed)) {
+                        go = false;
+                        break;
+                    }
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    const uint32_t at = stage0 + stage * kStageBytes;
+                    const uint64_t a = operand_desc(at, TurnedA), b = operand_desc(at + kOperandBytes, TurnedB);
+#pragma unroll
+                    for (int j = 0; j < kBlockK / 16; ++j)  // 16 of depth: 32 bytes, or two groups of eight
+                        product(d, a + j * (TurnedA ? 2048 >> 4 : 32 >> 4), b + j * (TurnedB ? 2048 >> 4 : 32 >> 4),
+                                product_desc(TurnedA, TurnedB), k > k0 || j > 0);
+                    products_arrive(&bars.empty[stage]);
+                    if (++stage == kStagesMm)
+                        stage = 0, phase ^= 1u;
+                }
+                if (!go)
+                    break;
+                products_arrive(&bars.tile_full[t]);
+                if (++t == 2)
+                    t = 0, tphase ^= 1u;
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        int t = 0;
+        uint32_t tphase = 0;
+        for (int64_t i = pair; i < shape.tiles(); i += pairs) {
+            int64_t row, column, k0, k1;
+            int split;
+            shape.tile(i, row, column, split);
+            shape.depth(split, k0, k1);
+            if (k0 == k1) {
+                finish(row, column, split, [](int, float(&v)[32]) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        v[e] = 0.0f;
+                });
+                continue;
+            }
+            const bool there = matrix_wait(&bars.tile_full[t], tphase, failed);
+            if (!__all_sync(0xffffffffu, there))
+                break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint32_t at = tmem + t * kTile + ((uint32_t)((warp & 3) * 32) << 16);
+            finish(row, column, split, [at](int c, float(&v)[32]) { load_columns(at + c, v); });
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            __syncwarp();
+            if (lane == 0)
+                barrier_arrive_cluster(first_cta(shared_addr(&bars.tile_empty[t])));
+            if (++t == 2)
+                t = 0, tphase ^= 1u;
+        }
+    }
+    // neither CTA leaves while the other may still write into it; after a wait that ran out (seconds), copies have
+    // long landed
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    if (threadIdx.x == 0 && *failed)
+        atomicOr(err_word, timeout_bit);
+    if (warp == 2)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemColumns) : "memory");
+}
+
+}  // namespace sv

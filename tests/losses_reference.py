@@ -71,3 +71,39 @@ def distill_truth(z, a, x, T=1.0, tail=False, g=1.0):
     g = float(np.float32(g))
     return {"status": 0, "loss": loss, "grad": g * grad / T, "loss_tol": loss_tol,
             "grad_tol": abs(g) / T * (grad_tol + 2.0 ** -22 * np.abs(grad))}
+
+
+def cross_entropy_truth(h, W, y, g=None):
+    """Rows h [R, D], weight W [V, D] (64-bit tensors of the stored values), labels y [R] all in [0, V), g [R]:
+    everything the two calls give, and bounds before the last rounding of each.
+
+    A logit's products are exact in float32; the tensor cores add them 16 at a time and may cut instead of round:
+    (D / 16 + 16) 2^-23 of sum |h| |w|, and the same for the sums of d W and d^T h.  d = g (p - [v = y]):
+    p is off by two logits' errors (its own and lse's) and by the power (2^-22 and 3 roundings of |z - lse| log2 e), and d is
+    rounded to bfloat16, 2^-8 of itself."""
+    import torch
+    g = torch.ones(len(h), dtype=torch.float64, device=h.device) if g is None else g.double()
+    D, V = h.shape[1], W.shape[0]
+    z = h @ W.T
+    add = lambda n: (n / 16 + 16) * 2.0 ** -23
+    dz = add(D) * (h.abs() @ W.abs().T)
+    dz_max = dz.amax(-1)
+    lse = torch.logsumexp(z, -1)
+    zy = z.gather(-1, y[:, None])[:, 0]
+    lse_tol = dz_max + SUM + 2.0 ** -22 + 2.0 ** -24 * lse.abs()
+    out = {"lse": lse, "lse_tol": lse_tol, "loss": lse - zy,
+           "loss_tol": lse_tol + dz.gather(-1, y[:, None])[:, 0] + 2.0 ** -24 * zy.abs()}
+    lp = z - lse[:, None]
+    p = lp.exp()
+    d = p.clone()
+    d[torch.arange(len(h), device=h.device), y] -= 1.0
+    rel = torch.expm1(dz + lse_tol[:, None]) + 2.0 ** -22 + 3 * lp.abs() * 2.0 ** -24
+    off = p * rel + 2.0 ** -24 * d.abs()
+    d, off = d * g[:, None], off * g.abs()[:, None]
+    off = off + 2.0 ** -8 * (d.abs() + off) + 2.0 ** -126
+    out["grad_hidden"], out["grad_weight"] = d @ W, d.T @ h
+    a = d.abs() + off
+    # parts of the sums (16 splits, 64 pieces at most) are joined in float32
+    out["grad_hidden_tol"] = off @ W.abs() + (add(V) + 80 * 2.0 ** -24) * (a @ W.abs())
+    out["grad_weight_tol"] = off.T @ h.abs() + add(len(h)) * (a.T @ h.abs())
+    return out
