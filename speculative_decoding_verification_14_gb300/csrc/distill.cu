@@ -15,9 +15,8 @@
 // list, without the cancellation of S - sum of listed weights, and against the maximum off the list, so
 // that q_v / q_rest is right where the whole tail underflows next to a listed entry.  The CTAs
 // exchange (maximum, sum) of both parts through distributed shared memory; r and the loss, where
-// float32 would lose what 1 - sum t_k or a small loss leaves, are taken in 64 bits by the first CTA
+// float32 would lose what 1 - sum t_k or a small loss leaves, are taken in two floats by the first CTA
 // from a few numbers per row.
-#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -25,14 +24,14 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <mutex>
 
 #include "../../include/spec_verify.h"
 #include "distill_plan.h"
 #include "losses_common.cuh"
 #include "sampling_common.cuh"
 #include "sv_context.h"
-
-namespace cg = cooperative_groups;
+#include "two_floats.cuh"
 
 namespace {
 
@@ -43,6 +42,9 @@ constexpr int kNW = kNT / 32;
 constexpr int kMaxC = 16;
 constexpr int kMaxList = kDistillMaxList;
 constexpr uint32_t kCopyPiece = 16384;
+// ex2.approx gives 5.0e-8 of itself too little in the mean over a period of its argument (measured, 2^22 arguments;
+// 4 to 7e-8 in each sixty-fourth of it): a sum of many is corrected by it where two floats are kept
+constexpr float kPowerBias = 5.0e-8f;
 
 struct Args {
     const void* logits;
@@ -56,54 +58,103 @@ struct Args {
     int64_t grad_stride;
     int32_t* status;
     uint32_t* err_word;
-    int64_t V;
+    int64_t V, rows;
     int rows_per_seq, C, n, tail;
     uint32_t vectors;  // per CTA
-    float T, ch;       // log2(e) / T
+    float iT, iTl, ch, cl;  // 1 / T and log2(e) / T in two parts each, the latter's both above 0
+};
+
+// what a CTA's slice gives off the list: a sum of weights, 2^-38 a unit in two halves, and what they are against
+struct CtaPart {
+    float hi, lo, m;
+};
+
+// what a row's gradients are written from: k 2^((z - m) c) off the list, g (total q - t) on it
+struct Answer {
+    float m, k, M, iS, total, g;
+    float mu, su;
+    int kind;      // an SV_ code, or -1: no teacher
+    bool nothing;  // r is what rounding left
 };
 
 struct Shared {
-    double t[kMaxList];  // first CTA: the list's shares
+    unsigned long long warp_sum[kNW];
+    uint64_t bar, exchange[2];
+    CtaPart part[2][kMaxC];
+    Answer answer;
     float a[kMaxList];
     int32_t token[kMaxList];
-    float z[kMaxList];  // first CTA: the draft logits of the list
-    float4 part[kMaxC];  // every CTA's (maximum, sum) off the list and on it
-    float2 warp_off[kNW], warp_on[kMaxList / 32];
-    float r, total;  // from the first CTA
-    double r64, log_sum;  // first CTA: r, and ln sum exp(a - largest a)
+    float z[2][kMaxList];  // the draft logits of the list
+    float warp_max[kNW];
+    float r[2], total[2];  // from the first CTA
     float list_max, list_sum;
-    uint32_t flags;  // bit 0: a listed token; above: 1 << code
-    uint64_t bar;
+    uint32_t listed;  // whether a token is
+    uint32_t flags;   // 1 << code
 };
 
-// 2^((z - m) c) times k for a vector's logits, in the logits' type
-template <int ES>
-__device__ __forceinline__ uint4 exp_scaled(const uint4& v, float m, float c, float k) {
+__device__ __forceinline__ void store_cluster(uint32_t addr, float x) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(x) : "memory");
+}
+
+__device__ __forceinline__ unsigned long long two(float x, float y) {
+    unsigned long long t;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(t) : "f"(x), "f"(y));
+    return t;
+}
+
+// 2^((z - m) c) of logits 2j and 2j + 1 of a vector, c = log2(e) / T in one float or (Fine) two: what
+// rounding leaves of c moves every weight the same way, by up to |(z - m) / T| 2^-25
+template <int ES, bool Fine>
+__device__ __forceinline__ unsigned long long exp_two(const uint4& v, int j, float m, unsigned long long ch,
+                                                      unsigned long long cl) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    float lo, hi;
+    if constexpr (ES == 2) {
+        asm("{\n\t.reg .b16 l, h;\n\t"
+            "mov.b32 {l, h}, %2;\n\t"
+            "add.rn.f32.bf16 %0, l, %3;\n\t"
+            "add.rn.f32.bf16 %1, h, %3;\n\t}"
+            : "=f"(lo), "=f"(hi)
+            : "r"(w[j]), "f"(-m));
+    } else {
+        lo = __uint_as_float(w[2 * j]) - m;
+        hi = __uint_as_float(w[2 * j + 1]) - m;
+    }
+    unsigned long long d = two(lo, hi), y;
+    if constexpr (Fine) {
+        // both parts are above 0: a difference of -inf gives -inf
+        asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(d), "l"(cl));
+        asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(y) : "l"(d), "l"(ch));
+    } else {
+        asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(d), "l"(ch));
+    }
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(y));
+    return two(ex2_approx(lo), ex2_approx(hi));
+}
+
+// their sum over a vector
+template <int ES>
+__device__ __forceinline__ float exp_vector_sum(const uint4& v, float m, unsigned long long ch, unsigned long long cl) {
+    unsigned long long s = exp_two<ES, true>(v, 0, m, ch, cl);
+#pragma unroll
+    for (int j = 1; j < 8 / ES; ++j)
+        asm("add.rn.f32x2 %0, %0, %1;" : "+l"(s) : "l"(exp_two<ES, true>(v, j, m, ch, cl)));
+    float lo, hi;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(s));
+    return lo + hi;
+}
+
+// times k, in the logits' type (bfloat16 rounds more away than the rest of c would add)
+template <int ES>
+__device__ __forceinline__ uint4 exp_scaled(const uint4& v, float m, unsigned long long ch, unsigned long long cl,
+                                            float k) {
     uint32_t out[4];
-    unsigned long long cc, kk;
-    asm("mov.b64 %0, {%1, %1};" : "=l"(cc) : "f"(c));
-    asm("mov.b64 %0, {%1, %1};" : "=l"(kk) : "f"(k));
+    const unsigned long long kk = two(k, k);
 #pragma unroll
     for (int j = 0; j < 8 / ES; ++j) {
+        unsigned long long t = exp_two<ES, ES == 4>(v, j, m, ch, cl);
         float lo, hi;
-        if constexpr (ES == 2) {
-            asm("{\n\t.reg .b16 l, h;\n\t"
-                "mov.b32 {l, h}, %2;\n\t"
-                "add.rn.f32.bf16 %0, l, %3;\n\t"
-                "add.rn.f32.bf16 %1, h, %3;\n\t}"
-                : "=f"(lo), "=f"(hi)
-                : "r"(w[j]), "f"(-m));
-        } else {
-            lo = __uint_as_float(w[2 * j]) - m;
-            hi = __uint_as_float(w[2 * j + 1]) - m;
-        }
-        unsigned long long t;
-        asm("{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\tmul.rn.f32x2 %0, d, %3;\n\t}" : "=l"(t) : "f"(lo), "f"(hi), "l"(cc));
-        asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(t));
-        asm("{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\tmul.rn.f32x2 %0, d, %3;\n\t}"
-            : "=l"(t)
-            : "f"(ex2_approx(lo)), "f"(ex2_approx(hi)), "l"(kk));
+        asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(t) : "l"(kk));
         asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(t));
         if constexpr (ES == 2) {
             asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(out[j]) : "f"(hi), "f"(lo));
@@ -141,163 +192,480 @@ struct Part {
     }
 };
 
-// Writes f(k, local vector) as the gradient's vectors of this part.
+// the largest of a warp's lanes; NaN if one is
+__device__ __forceinline__ float warp_max(float x) {
+    float m;
+    asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
+    return m;
+}
+// The largest logit of a slice's vectors that fall to this warp; NaN if one is.
+template <int ES>
+__device__ __forceinline__ float slice_max(const uint4* slice, uint32_t vectors) {
+    float m = -__int_as_float(0x7f800000);
+    if constexpr (ES == 2) {
+        uint32_t x = 0xff80ff80u;  // -inf, -inf
+        for (uint32_t k = threadIdx.x; k < vectors; k += kNT) {
+            const uint4 w = slice[k];
+            uint32_t y, z;
+            asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(w.x), "r"(w.y));
+            asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(z) : "r"(w.z), "r"(w.w));
+            asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(y), "r"(z));
+            asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(x) : "r"(x), "r"(y));
+        }
+        m = max_nan(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+    } else {
+        for (uint32_t k = threadIdx.x; k < vectors; k += kNT)
+            m = max_nan(m, vector_max_nan<ES>(slice[k]));
+    }
+    return warp_max(m);
+}
+
+// the sum over a warp's lanes
+__device__ __forceinline__ Two warp_sum(Two x) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        x = two_add(x, Two{__shfl_xor_sync(kAllLanes, x.h, o), __shfl_xor_sync(kAllLanes, x.l, o)});
+    return x;
+}
+// x + y, where a y beyond float is an infinity that stays (x and y are above -inf)
+__device__ __forceinline__ Two two_finite(Two x, Two y) {
+    const float inf = __int_as_float(0x7f800000);
+    return x.h < inf && y.h < inf ? two_add(x, y) : Two{inf, 0.0f};
+}
+// (x - y) / T; an infinity stays one
+__device__ __forceinline__ Two over(float x, float y, Two iT) {
+    const Two d = two_sum(x, -y);
+    return fabsf(d.h) <= 3.4028235e38f ? two_mul(d, iT) : Two{d.h, 0.0f};
+}
+
+// Writes f(local vector) as the gradient's vectors of this part.
 template <int ES, typename F>
 __device__ __forceinline__ void write_part(const Part<ES>& p, unsigned char* grad, F f) {
     constexpr int E = 16 / ES;
     const bool same = (uint32_t)(reinterpret_cast<uintptr_t>(grad) & 15u) / ES == p.off;
-    uint4* vectors = reinterpret_cast<uint4*>(grad - (size_t)p.off * ES);
-    for (uint32_t k = p.v0 + threadIdx.x; k < p.v1; k += kNT) {
+    // the row's ends, and rows whose gradient lies otherwise to 16 bytes than they do: entry by entry
+    const auto by_entry = [&](uint32_t k) {
         const uint4 w = f(k - p.v0);
-        if (same && p.whole(k)) {
-            vectors[k] = w;
-        } else {
-            // the row's ends, and rows whose gradient lies otherwise to 16 bytes than they do: entry by entry
-            const int64_t id = (int64_t)k * E - p.off;
+        const int64_t id = (int64_t)k * E - p.off;
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                if (id + e >= 0 && id + e < p.V)
-                    store_entry<ES>(grad, id + e, vector_entry<ES>(w, e));
-        }
+        for (int e = 0; e < E; ++e)
+            if (id + e >= 0 && id + e < p.V)
+                store_entry<ES>(grad, id + e, vector_entry<ES>(w, e));
+    };
+    if (same) {
+        uint4* vectors = reinterpret_cast<uint4*>(grad - (size_t)p.off * ES) + p.v0;
+        const uint32_t w0 = p.v0 < p.v1 && !p.whole(p.v0) ? 1u : 0u;
+        const uint32_t n = p.v1 - p.v0, w1 = n > w0 && !p.whole(p.v1 - 1) ? n - 1 : n;
+#pragma unroll 4
+        for (uint32_t i = w0 + threadIdx.x; i < w1; i += kNT)
+            vectors[i] = f(i);
+        if (threadIdx.x == 0 && w0)
+            by_entry(p.v0);
+        if (threadIdx.x == 32 && w1 < n)
+            by_entry(p.v1 - 1);
+    } else {
+        for (uint32_t k = p.v0 + threadIdx.x; k < p.v1; k += kNT)
+            by_entry(k);
     }
 }
 
+// the warps that walk the slice
+__device__ __forceinline__ void sync_walkers() {
+    asm volatile("barrier.cta.sync 1, %0;" ::"n"(kNT) : "memory");
+}
+
+// the whole vectors of a part: first, and bytes of all
 template <int ES>
-__global__ void __launch_bounds__(kNT, 3) sv_distill_kernel(const __grid_constant__ Args a) {
+__device__ __forceinline__ uint32_t whole_vectors(const Part<ES>& p, uint32_t& first) {
+    uint32_t w0 = p.v0, w1 = p.v1;
+    if (w0 < w1 && !p.whole(w0))
+        ++w0;
+    if (w0 < w1 && !p.whole(w1 - 1))
+        --w1;
+    first = w0;
+    return (w1 - w0) * 16u;
+}
+
+template <int ES>
+__global__ void __launch_bounds__(kNT + 64, kDistillCtas) sv_distill_kernel(const __grid_constant__ Args a) {
     extern __shared__ __align__(128) uint4 slice[];
     __shared__ Shared sh;
-    cg::cluster_group cluster = cg::this_cluster();
     constexpr int E = 16 / ES;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int C = a.C, rank = (int)cluster.block_rank(), n = a.n;
-    const int64_t row = blockIdx.x / C, seq = row / a.rows_per_seq;
-    const float inf = __int_as_float(0x7f800000), nan = __int_as_float(0x7fffffff);
-    const unsigned char* base = static_cast<const unsigned char*>(a.logits) + row * a.stride * ES;
-    unsigned char* grad = a.grad ? static_cast<unsigned char*>(a.grad) + row * a.grad_stride * ES : nullptr;
-    const Part<ES> p(base, a.V, a.vectors, rank);
+    const int C = a.C, n = a.n;
+    const uint32_t rank = blockIdx.x % C, clusters = gridDim.x / C;
+    const float inf = __int_as_float(0x7f800000);
+    const bool teacher = warp == kNW;     // the list, and what follows from the slices' sums
+    const bool scribe = warp == kNW + 1;  // of the first CTA: what the list leaves, and the loss
+    const unsigned long long ch = two(a.ch, a.ch), cl = two(a.cl, a.cl);
+    const auto row_base = [&](int64_t row) { return static_cast<const unsigned char*>(a.logits) + row * a.stride * ES; };
+    const auto is_live = [&](int64_t row) {
+        if (!a.accept_len)
+            return true;
+        const int64_t seq = row / a.rows_per_seq;
+        return row - seq * a.rows_per_seq < a.accept_len[seq];
+    };
 
-    // every way through the kernel passes both barriers of the cluster once: CTAs of a row that see
-    // different lists or lengths, which a program changes under the call, still end
-    cluster.barrier_arrive();
-    const bool live = !a.accept_len || row - seq * a.rows_per_seq < a.accept_len[seq];
-    bool answer = live;  // the row has a teacher
-    int code = SV_OK;
-    float M = 0.0f, S = 1.0f, mu = -inf, su = 0.0f, r = 0.0f, total = 1.0f;
-    float mine = -inf;  // listed logit of token number tid, where it is of this slice
-    bool own = false;
-    if (live) {
-        if (tid == 0) {
-            sh.flags = 0;
-            barrier_init(&sh.bar, 1);
-            barrier_init_fence();
-            uint32_t w0 = p.v0, w1 = p.v1;
-            if (w0 < w1 && !p.whole(w0))
-                ++w0;
-            if (w0 < w1 && !p.whole(w1 - 1))
-                --w1;
-            const uint32_t bytes = (w1 - w0) * 16u;
-            barrier_expect(&sh.bar, bytes);
-            const unsigned char* src = base - (size_t)p.off * ES + (size_t)w0 * 16;
-            unsigned char* dst = reinterpret_cast<unsigned char*>(slice + (w0 - p.v0));
-            for (uint32_t at = 0; at < bytes; at += kCopyPiece)
-                copy_bulk(dst + at, src + at, min(kCopyPiece, bytes - at), &sh.bar);
-        }
-        if (tid < 2 * E && p.v0 < p.v1) {  // the row's ends, where vectors are not whole
-            const uint32_t k = tid < E ? p.v0 : p.v1 - 1;
-            const int64_t id = (int64_t)k * E - p.off + tid % E;
-            if (!p.whole(k)) {
-                const float z = id >= 0 && id < a.V ? scalar_entry<ES>(base, id) : -inf;
-                store_entry<ES>(reinterpret_cast<unsigned char*>(slice + (k - p.v0)), tid % E, z);
-            }
-        }
-        // the list
-        int32_t x = -1;
-        uint32_t flags = 0;
-        if (tid < n) {
-            x = a.top_tokens[row * n + tid];
-            float lp = a.top_logprobs[row * n + tid];
-            if (x < -1 || x >= a.V) {
-                flags = 1u << SV_ERR_TOKEN_RANGE;
-                x = -1;
-            }
-            if (x >= 0) {
-                flags |= 1u;
-                if (!(lp < inf)) {
-                    flags |= 1u << SV_ERR_NONFINITE;
-                    lp = -inf;
-                }
-            } else {
-                lp = -inf;
-            }
-            sh.token[tid] = x;
-            sh.a[tid] = lp;
-        }
-        __syncthreads();
-        if (tid < n && x >= 0) {
-            bool twice = false;
-            for (int j = 0; j < tid; ++j)
-                twice |= sh.token[j] == x;
-            if (twice) {
-                flags |= 1u << SV_ERR_TOKEN_RANGE;
-                x = -1;
-            }
-        }
-        if (flags)
-            atomicOr(&sh.flags, flags);
-        if (warp == 0) {
-            float top = -inf;
-            for (int k = lane; k < n; k += 32)
-                top = fmaxf(top, sh.a[k]);
+    if (teacher && lane == 0) {
+        sh.listed = 0;
+        sh.flags = 0;
+        barrier_init(&sh.bar, 1);
+        for (int i = 0; i < 2; ++i)
+            barrier_init(&sh.exchange[i], (uint32_t)C + 1);  // every CTA's sums, and the first one's r
+        barrier_init_fence();
+    }
+    __syncwarp();
+    cluster_arrive();
+    int64_t row = blockIdx.x / C;
+    // What the next row needs, ahead of it: a walker's listed token, the others' tokens and log-probabilities.
+    int32_t tokens[kMaxList / 32];
+    float logprobs[kMaxList / 32];
+    bool next_live = is_live(row);
+    const auto fetch = [&](int64_t r) {
+        if (warp < kNW) {
+            tokens[0] = tid < n ? a.top_tokens[r * n + tid] : -1;
+        } else {
 #pragma unroll
-            for (int o = 16; o; o >>= 1)
-                top = fmaxf(top, __shfl_xor_sync(kAllLanes, top, o));
+            for (int j = 0; j < kMaxList / 32; ++j)
+                if (lane + 32 * j < n) {
+                    tokens[j] = a.top_tokens[r * n + lane + 32 * j];
+                    logprobs[j] = a.top_logprobs[r * n + lane + 32 * j];
+                }
+        }
+    };
+    fetch(row);
+    cluster_wait();  // every CTA of the cluster runs: its memory may be written
+
+    // The first CTA's scribe: a row's list in two floats, ahead of the row,
+    struct {
+        Two r, ts, t[kMaxList / 32];  // what the list leaves, its sum, its shares
+        float a[kMaxList / 32], shift;
+        uint32_t tokens;  // bit j: a token in place lane + 32 j
+    } list;
+    const auto read_list = [&] {
+        float top = -inf;
+        list.tokens = 0;
+#pragma unroll
+        for (int j = 0; j < kMaxList / 32; ++j) {
+            const bool there = lane + 32 * j < n && tokens[j] >= 0 && tokens[j] < a.V;
+            list.tokens |= (uint32_t)there << j;
+            list.a[j] = there && logprobs[j] < inf ? logprobs[j] : -inf;
+            top = fmaxf(top, list.a[j]);
+        }
+        top = warp_max(top);
+        list.shift = !a.tail && top > -inf ? top : 0.0f;
+        list.ts = Two{0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < kMaxList / 32; ++j) {
+            list.t[j] = Two{0.0f, 0.0f};
+            if (32 * j < n) {
+                list.t[j] = two_exp(two_sum(list.a[j], -list.shift));
+                list.ts = two_add(list.ts, list.t[j]);
+            }
+        }
+        list.ts = warp_sum(list.ts);
+        list.r = Two{0.0f, 0.0f};
+        if (a.tail) {
+            list.r = two_add(Two{1.0f, 0.0f}, two_neg(list.ts));
+            if (!(list.r.h > 0.0f))
+                list.r = Two{0.0f, 0.0f};
+        } else if (list.ts.h > 0.0f) {
+#pragma unroll
+            for (int j = 0; j < kMaxList / 32; ++j)
+                if (32 * j < n)
+                    list.t[j] = two_div(list.t[j], list.ts);
+        }
+    };
+    // and its loss from the parts' sums and the list's logits, while the walkers have the next row's sums to take.
+    struct {
+        int64_t row;
+        Two r, ts, t[kMaxList / 32];
+        CtaPart part;
+        float z[kMaxList / 32], a[kMaxList / 32], shift, mu, M, su;
+        int code;
+    } owed;
+    owed.row = -1;
+    if (scribe && rank == 0)
+        read_list();
+    const auto settle = [&] {
+        if (owed.row < 0)
+            return;
+        Two loss{0.0f, 0.0f};
+        if (owed.code == SV_OK && a.loss) {
+            const Two iT{a.iT, a.iTl};
+            Two off{0.0f, 0.0f}, on{0.0f, 0.0f};
+            if (owed.part.m > -inf) {
+                const Two s = two_sum(owed.part.hi * (1.0f / 64.0f), owed.part.lo * 3.6379788e-12f);
+                off = two_mul(two_mul(s, Two{1.0f, kPowerBias}), two_exp(over(owed.part.m, owed.M, iT)));
+            }
+            // sums of t (a - shift - z / T), and of the listed weights
+#pragma unroll
+            for (int j = 0; j < kMaxList / 32; ++j) {
+                if (32 * j >= n)
+                    break;
+                const Two y = over(owed.z[j], owed.M, iT);
+                on = two_add(on, two_exp(y));
+                if (owed.t[j].h > 0.0f) {
+                    const Two d = two_add(two_sum(owed.a[j], -owed.shift), two_neg(y));
+                    loss = two_finite(loss, two_mul(owed.t[j], d));
+                }
+            }
+            off = warp_sum(off);
+            on = warp_sum(on);
+            const bool infinite = __any_sync(kAllLanes, loss.h == inf);
+            loss = warp_sum(loss);
+            const Two ls = two_log(two_add(on, off));
+            if (a.tail)
+                loss = two_add(loss, two_mul(owed.ts, ls));
+            else
+                loss = two_add(loss, two_add(ls, two_neg(two_log(owed.ts))));
+            if (owed.r.h > 0.0f) {  // a tail too small beside M for its weight still has a logarithm
+                const Two lu = off.h > 1e-30f ? two_log(off)
+                               : owed.su > 0.0f ? two_add(over(owed.mu, owed.M, iT), two_log(Two{owed.su, 0.0f}))
+                                                : Two{-inf, 0.0f};
+                const Two d = two_add(two_log(owed.r), two_add(ls, two_neg(lu)));
+                loss = two_finite(loss, two_mul(owed.r, d));
+            }
+            if (infinite || !(loss.h < inf))
+                loss.h = inf, loss.l = 0.0f;
+        }
+        owed.code = owed.code < 0 ? SV_OK : owed.code;
+        if (lane == 0) {
+            if (a.loss)
+                a.loss[owed.row] = owed.code ? __int_as_float(0x7fffffff) : loss.h + loss.l;
+            if (a.status)
+                a.status[owed.row] = owed.code;
+            if (owed.code)
+                atomicOr(a.err_word, 1u << owed.code);
+        }
+        owed.row = -1;
+    };
+
+    // Every CTA of a row arrives at all the others and waits for them, whatever it sees of the row: CTAs that see
+    // different lists or lengths, which a program changes under the call, still end.  What others write has a place
+    // for even turns and one for odd ones: a CTA is at most one turn ahead of another.
+    uint32_t loads = 0;
+    for (uint32_t turn = 0; row < a.rows; ++turn, row += clusters) {
+        const uint32_t odd = turn & 1u, phase = (turn >> 1) & 1u;
+        const unsigned char* base = row_base(row);
+        unsigned char* grad = a.grad ? static_cast<unsigned char*>(a.grad) + row * a.grad_stride * ES : nullptr;
+        const Part<ES> p(base, a.V, a.vectors, (int)rank);
+        const bool more = row + clusters < a.rows;
+        const bool live = __syncthreads_and(next_live);  // one answer for the CTA, whose last row is done with
+        if (teacher) {
+            if (live && lane == 0) {
+                uint32_t first;
+                const uint32_t bytes = whole_vectors(p, first);
+                barrier_expect(&sh.bar, bytes);
+                const unsigned char* src = base - (size_t)p.off * ES + (size_t)first * 16;
+                unsigned char* dst = reinterpret_cast<unsigned char*>(slice + (first - p.v0));
+                for (uint32_t at = 0; at < bytes; at += kCopyPiece)
+                    copy_bulk(dst + at, src + at, min(kCopyPiece, bytes - at), &sh.bar);
+            }
+            __syncwarp();
             // shares against the largest (top) or as they are (tail)
-            const float shift = a.tail ? 0.0f : top > -inf ? top : 0.0f;
-            float sum = 0.0f;
-            for (int k = lane; k < n; k += 32)
-                sum += expf(sh.a[k] - shift);
+            uint32_t flags = 0;
+            float top = -inf;
 #pragma unroll
-            for (int o = 16; o; o >>= 1)
-                sum += __shfl_xor_sync(kAllLanes, sum, o);
-            if (lane == 0) {
-                sh.list_max = shift;
-                sh.list_sum = a.tail ? 1.0f : sum;
+            for (int j = 0; j < kMaxList / 32; ++j) {
+                const int k = lane + 32 * j;
+                if (k >= n)
+                    break;
+                const int32_t y = tokens[j];
+                float lp = logprobs[j];
+                if (y < 0 || y >= a.V)
+                    lp = -inf;
+                else if (!(lp < inf))
+                    flags |= 1u << SV_ERR_NONFINITE, lp = -inf;
+                sh.a[k] = lp;
+                sh.token[k] = y;
+                top = fmaxf(top, lp);
             }
-            if (rank == 0) {
-                double s = 0.0;
-                for (int k = lane; k < n; k += 32) {
-                    const double t = exp((double)sh.a[k] - (double)shift);
-                    sh.t[k] = t;
-                    s += t;
-                }
+            __syncwarp();
+            if (more) {
+                next_live = is_live(row + clusters);
+                fetch(row + clusters);
+            }
+            const float weight = grad && a.grad_loss ? a.grad_loss[row] : 1.0f;
+            float shift = 0.0f, sum = 1.0f;
+            if (!a.tail) {
+                top = warp_max(top);
+                shift = top > -inf ? top : 0.0f;
+                sum = 0.0f;
+#pragma unroll
+                for (int j = 0; j < kMaxList / 32; ++j)
+                    if (lane + 32 * j < n)
+                        sum += expf(sh.a[lane + 32 * j] - shift);
 #pragma unroll
                 for (int o = 16; o; o >>= 1)
-                    s += __shfl_xor_sync(kAllLanes, s, o);
-                const double rest = a.tail ? fmax(0.0, 1.0 - s) : 0.0;
-                if (lane == 0) {
-                    sh.r64 = rest;
-                    sh.log_sum = a.tail ? 0.0 : log(s);
-                }
-                const float r_ = (float)rest, total_ = a.tail ? (float)(s + rest) : 1.0f;
-                for (int k = lane; k < n; k += 32)
-                    if (!a.tail)
-                        sh.t[k] /= s;
-                cluster.barrier_wait();  // every CTA of the cluster runs: its memory may be written
-                if (lane < C) {
-                    *cluster.map_shared_rank(&sh.r, lane) = r_;
-                    *cluster.map_shared_rank(&sh.total, lane) = total_;
-                }
-            } else {
-                cluster.barrier_wait();
+                    sum += __shfl_xor_sync(kAllLanes, sum, o);
             }
-        } else {
-            cluster.barrier_wait();
+            sh.list_max = shift;
+            sh.list_sum = sum;
+            // a token listed twice
+            for (int k = lane; k < n; k += 32) {
+                const int32_t y = sh.token[k];
+                if (y >= 0)
+                    for (int j = 0; j < k; ++j)
+                        if (sh.token[j] == y)
+                            flags |= 1u << SV_ERR_TOKEN_RANGE;
+            }
+            if (flags)
+                atomicOr(&sh.flags, flags);
+            __syncwarp();
+            if (live && more && next_live && lane == 0) {  // the next row comes into L2 meanwhile
+                const unsigned char* after = row_base(row + clusters);
+                const Part<ES> q(after, a.V, a.vectors, (int)rank);
+                uint32_t first;
+                const uint32_t bytes = whole_vectors(q, first);
+                if (bytes)
+                    prefetch_bulk(after - (size_t)q.off * ES + (size_t)first * 16, bytes);
+            }
+            __syncwarp();
+            if (!barrier_try_cluster(&sh.exchange[odd], phase) &&
+                !barrier_wait_cluster(&sh.exchange[odd], phase, kWaitNs))
+                atomicOr(&sh.flags, 1u << SV_ERR_TIMEOUT);
+            __syncwarp();
+            if (!live) {
+                if (rank == 0 && lane == 0) {
+                    if (a.loss)
+                        a.loss[row] = 0.0f;
+                    if (a.status)
+                        a.status[row] = SV_OK;
+                }
+                if (lane == 0)
+                    sh.flags = 0;
+                continue;
+            }
+            const CtaPart part = sh.part[odd][lane % C];
+            float mu = part.m, M = -inf, z[kMaxList / 32];
+#pragma unroll
+            for (int j = 0; j < kMaxList / 32; ++j) {
+                const int k = lane + 32 * j;
+                z[j] = k < n && sh.token[k] >= 0 ? sh.z[odd][k] : -inf;
+                M = max_nan(M, z[j]);
+            }
+            mu = warp_max(mu);
+            M = max_nan(mu, warp_max(M));
+            const bool has = lane < C && part.m > -inf;
+            float su = has ? fmaf(part.hi, 1.0f / 64.0f, part.lo * 3.6379788e-12f) * expf((part.m - mu) * a.iT) : 0.0f;
+            float S = 0.0f;
+#pragma unroll
+            for (int j = 0; j < kMaxList / 32; ++j)
+                if (32 * j < n)
+                    S += z[j] > -inf ? expf((z[j] - M) * a.iT) : 0.0f;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) {
+                su += __shfl_xor_sync(kAllLanes, su, o);
+                S += __shfl_xor_sync(kAllLanes, S, o);
+            }
+            flags = sh.flags;
+            const bool answer = flags || sh.listed;
+            const int code = flags ? __ffs(flags) - 1
+                             : answer && (!(M > -inf && M < inf) || !(sum > 0.0f)) ? SV_ERR_NONFINITE : SV_OK;
+            const bool good = answer && code == SV_OK;
+            // the draft's mass off the list
+            const float wu = good && mu > -inf ? su * expf((mu - M) * a.iT) : 0.0f;
+            S += wu;
+            const float iS = __fdividef(1.0f, S), rest = wu * iS;
+            // what rounding leaves of a list that holds all the mass there is, is no outcome
+            float r = sh.r[odd], total = sh.total[odd];
+            const bool nothing = rest < 1.17549435e-38f && r <= 9.5367432e-7f;
+            if (nothing) {
+                total -= r;
+                r = 0.0f;
+            }
+            __syncwarp();
+            if (lane == 0) {
+                const float g = weight * a.iT;
+                sh.answer = Answer{mu > -inf ? mu : 0.0f, su > 0.0f ? __fdividef(g * (total * rest - r), su) : 0.0f, M, iS,
+                                   total, g, mu, su, answer ? code : -1, nothing};
+                sh.listed = 0;  // for the next row
+                sh.flags = 0;
+            }
+            __syncthreads();
+            continue;
         }
-        if (!barrier_wait(&sh.bar, 0, kCopyWaitNs))
+        if (scribe) {
+            if (rank == 0) {
+                if (lane < C) {
+                    store_cluster(cluster_addr(&sh.r[odd], lane), list.r.h);
+                    store_cluster(cluster_addr(&sh.total[odd], lane), a.tail ? two_add(list.ts, list.r).h : 1.0f);
+                    barrier_arrive_cluster(cluster_addr(&sh.exchange[odd], lane));
+                }
+                __syncwarp();
+                if (more)
+                    fetch(row + clusters);
+                settle();
+            }
+            if (more)
+                next_live = is_live(row + clusters);
+            if (live && rank == 0) {
+                if (!barrier_try_cluster(&sh.exchange[odd], phase))
+                    barrier_wait_cluster(&sh.exchange[odd], phase, kWaitNs);  // the teacher says if it ran out
+                __syncwarp();
+                owed.part = lane < C ? sh.part[odd][lane] : CtaPart{0.0f, 0.0f, -inf};
+                owed.r = list.r, owed.ts = list.ts, owed.shift = list.shift;
+#pragma unroll
+                for (int j = 0; j < kMaxList / 32; ++j) {
+                    owed.t[j] = list.t[j], owed.a[j] = list.a[j];
+                    owed.z[j] = (list.tokens >> j) & 1u ? sh.z[odd][lane + 32 * j] : -inf;
+                }
+            }
+            if (live) {
+                __syncthreads();  // what the teacher makes of the sums
+                if (rank == 0) {
+                    owed.row = row;
+                    owed.mu = sh.answer.mu, owed.M = sh.answer.M, owed.su = sh.answer.su;
+                    owed.code = sh.answer.kind;
+                    if (sh.answer.nothing)
+                        owed.r = Two{0.0f, 0.0f};
+                }
+            }
+            if (rank == 0 && more)
+                read_list();
+            continue;
+        }
+
+        // the walkers
+        int32_t x = tokens[0];  // listed token number tid
+        float mine = -inf;      // and its logit, where it is of this slice
+        bool own = false;
+        if (live) {
+            if (tid < 2 * E && p.v0 < p.v1) {  // the row's ends, where vectors are not whole
+                const uint32_t k = tid < E ? p.v0 : p.v1 - 1;
+                const int64_t id = (int64_t)k * E - p.off + tid % E;
+                if (!p.whole(k)) {
+                    const float z = id >= 0 && id < a.V ? scalar_entry<ES>(base, id) : -inf;
+                    store_entry<ES>(reinterpret_cast<unsigned char*>(slice + (k - p.v0)), tid % E, z);
+                }
+            }
+            if (x < -1 || x >= a.V) {
+                atomicOr(&sh.flags, 1u << SV_ERR_TOKEN_RANGE);
+                x = -1;
+            }
+            if (x >= 0)
+                sh.listed = 1;
+        }
+        if (more) {
+            next_live = is_live(row + clusters);
+            fetch(row + clusters);
+        }
+        if (!live) {
+            if (warp == 0 && lane < C)
+                barrier_arrive_cluster(cluster_addr(&sh.exchange[odd], lane));
+            __syncwarp();
+            if (grad)
+                write_part<ES>(p, grad, [](uint32_t) { return make_uint4(0, 0, 0, 0); });
+            continue;
+        }
+        if (!barrier_wait(&sh.bar, loads & 1u, kCopyWaitNs))
             atomicOr(&sh.flags, 1u << SV_ERR_TIMEOUT);
-        __syncthreads();
+        ++loads;
+        sync_walkers();  // also the row's ends are in
+        const uint32_t vectors = sh.listed ? p.v1 - p.v0 : 0;  // without a list there is nothing to sum
         // the listed entries leave the slice
-        if (tid < n && x >= 0) {
+        if (x >= 0) {
             const int64_t at = (int64_t)x + p.off;
             own = at >= (int64_t)p.v0 * E && at < (int64_t)p.v1 * E;
             if (own) {
@@ -305,124 +673,84 @@ __global__ void __launch_bounds__(kNT, 3) sv_distill_kernel(const __grid_constan
                 const int64_t i = at - (int64_t)p.v0 * E;
                 mine = scalar_entry<ES>(s8, i);
                 store_entry<ES>(s8, i, -inf);
-                *cluster.map_shared_rank(&sh.z[tid], 0) = mine;
+                for (int c = 0; c < C; ++c)
+                    store_cluster(cluster_addr(&sh.z[odd][tid], c), mine);
             }
         }
-        __syncthreads();
-        answer = sh.flags & 1u;
-        // sums off the list
-        float m = -inf, s = 0.0f;
-        if (sh.flags)  // without a list there is nothing to sum
-            for (uint32_t k = tid; k < p.v1 - p.v0; k += kNT) {
-                const uint4 w = slice[k];
-                const float top = vector_max_nan<ES>(w);
-                if (!(top <= m))
-                    join_sums(m, s, top, 0.0f, a.ch);
-                if (top > -inf)  // else m may be -inf too
-                    s += exp_sum<ES>(w, m, a.ch);
-            }
-        join_lanes<32>(m, s, a.ch);
-        if (lane == 0)
-            sh.warp_off[warp] = make_float2(m, s);
-        if (warp < kMaxList / 32) {
-            float mo = mine, so = own ? 1.0f : 0.0f;
-            join_lanes<32>(mo, so, a.ch);
+        sync_walkers();
+        // Sums off the list against the largest of one vector per thread: a thread's stays below 2^12 unless that
+        // misses the slice's largest by far (or there is a NaN), and then they are taken again against the largest
+        // of all.  A sum that follows a growing maximum would be multiplied by powers that are each off by 2^-22.
+        float m;
+        for (uint32_t span = kNT;; span = vectors) {
+            m = slice_max<ES>(slice, min(span, vectors));
             if (lane == 0)
-                sh.warp_on[warp] = make_float2(mo, so);
-        }
-        __syncthreads();
-        if (warp == 0) {
-            const float2 off = lane < kNW ? sh.warp_off[lane] : make_float2(-inf, 0.0f);
-            const float2 on = lane < kMaxList / 32 ? sh.warp_on[lane] : make_float2(-inf, 0.0f);
-            float m0 = off.x, s0 = off.y, m1 = on.x, s1 = on.y;
-            join_lanes<8>(m0, s0, a.ch);
-            join_lanes<8>(m1, s1, a.ch);
-            m0 = __shfl_sync(kAllLanes, m0, 0), s0 = __shfl_sync(kAllLanes, s0, 0);
-            m1 = __shfl_sync(kAllLanes, m1, 0), s1 = __shfl_sync(kAllLanes, s1, 0);
-            if (lane < C)
-                *cluster.map_shared_rank(&sh.part[rank], lane) = make_float4(m0, s0, m1, s1);
-        }
-    } else {
-        cluster.barrier_wait();
-    }
-    cluster.sync();
-
-    if (live && answer) {
-        float4 part = lane < C ? sh.part[lane] : make_float4(-inf, 0.0f, -inf, 0.0f);
-        join_lanes<16>(part.x, part.y, a.ch);
-        join_lanes<16>(part.z, part.w, a.ch);
-        mu = __shfl_sync(kAllLanes, part.x, 0), su = __shfl_sync(kAllLanes, part.y, 0);
-        M = __shfl_sync(kAllLanes, part.z, 0), S = __shfl_sync(kAllLanes, part.w, 0);
-        join_sums(M, S, mu, su, a.ch);
-        const uint32_t flags = sh.flags >> 1;
-        if (flags)
-            code = __ffs(flags);
-        else if (!(M > -inf && M < inf) || !(sh.list_sum > 0.0f))
-            code = SV_ERR_NONFINITE;
-        r = sh.r;
-        total = sh.total;
-    } else if (live && sh.flags) {
-        code = __ffs(sh.flags >> 1);  // a list of nothing but errors
-        answer = true;
-    }
-    const bool good = answer && code == SV_OK;
-    // the draft's mass off the list
-    const float wu = good && mu > -inf ? su * ex2_approx((mu - M) * a.ch) : 0.0f;
-    const float rest = wu / S;
-    // what rounding leaves of a list that holds all the mass there is, is no outcome
-    const bool nothing = rest < 1.17549435e-38f && r <= 9.5367432e-7f;
-    if (nothing) {
-        total -= r;
-        r = 0.0f;
-    }
-
-    if (grad) {
-        if (!answer) {
-            write_part<ES>(p, grad, [](uint32_t) { return make_uint4(0, 0, 0, 0); });
-        } else {
-            const float g = (a.grad_loss ? a.grad_loss[row] : 1.0f) / a.T;
-            const float k = !good ? nan : su > 0.0f ? g * ((total * rest - r) / su) : 0.0f;
-            const float m = good && mu > -inf ? mu : 0.0f;
-            if (good)
-                write_part<ES>(p, grad, [&](uint32_t i) { return exp_scaled<ES>(slice[i], m, a.ch, k); });
-            else
-                write_part<ES>(p, grad, [&](uint32_t) {
-                    const uint32_t w = ES == 4 ? 0x7fffffffu : 0x7fff7fffu;
-                    return make_uint4(w, w, w, w);
-                });
-            __syncthreads();  // the listed entries' gradients come after the others'
-            if (good && own) {
-                const float q = expf((mine - M) / a.T) / S, t = expf(sh.a[tid] - sh.list_max) / sh.list_sum;
-                store_entry<ES>(grad, sh.token[tid], g * (total * q - t));
-            }
-        }
-    }
-    if (rank == 0 && warp == 0) {
-        double loss = 0.0;
-        if (good && a.loss) {
-            const double iT = 1.0 / (double)a.T, ls = log((double)S);
-            for (int k = lane; k < n; k += 32) {
-                const double t = sh.t[k];
-                if (t > 0.0)
-                    loss += t * (((double)sh.a[k] - (double)sh.list_max - sh.log_sum) -
-                                 (((double)sh.z[k] - (double)M) * iT - ls));
-            }
+                sh.warp_max[warp] = m;
+            sync_walkers();
 #pragma unroll
-            for (int o = 16; o; o >>= 1)
-                loss += __shfl_xor_sync(kAllLanes, loss, o);
-            const double r64 = nothing ? 0.0 : sh.r64;
-            if (r64 > 0.0)
-                loss += r64 * (log(r64) - (((double)mu - (double)M) * iT + log((double)su) - ls));
+            for (int w = 0; w < kNW; ++w)
+                m = max_nan(m, sh.warp_max[w]);
+            float s = 0.0f;
+            if (m > -inf) {
+#pragma unroll 2
+                for (uint32_t k = tid; k < vectors; k += kNT)
+                    s += exp_vector_sum<ES>(slice[k], m, ch, cl);
+            }
+            // Threads' sums join as integers, 2^-38 a unit: in 12 and 26 bits behind the point, whose sums over a
+            // warp stay below 2^29 and 2^31
+            const bool fits = s < 4096.0f && (m > -inf || span >= vectors);
+            const uint32_t whole = (uint32_t)(s * 4096.0f);
+            const uint32_t part = (uint32_t)((s - (float)whole * (1.0f / 4096.0f)) * 274877906944.0f);
+            const uint32_t hi = __reduce_add_sync(kAllLanes, whole), lo = __reduce_add_sync(kAllLanes, part);
+            const bool all = __all_sync(kAllLanes, fits);
+            if (lane == 0)
+                sh.warp_sum[warp] = all ? ((unsigned long long)hi << 26) + lo : ~0ull;
+            sync_walkers();
+            if (span >= vectors)
+                break;
+            bool again = false;
+#pragma unroll
+            for (int w = 0; w < kNW; ++w)
+                again |= sh.warp_sum[w] == ~0ull;
+            if (!again)
+                break;
+            sync_walkers();  // before these are written again
         }
-        if (lane == 0) {
-            if (a.loss)
-                a.loss[row] = code ? nan : (float)loss;
-            if (a.status)
-                a.status[row] = code;
-            if (code)
-                atomicOr(a.err_word, 1u << code);
+        if (warp == 0 && lane < C) {
+            unsigned long long sum = 0;
+#pragma unroll
+            for (int w = 0; w < kNW; ++w)
+                sum += sh.warp_sum[w];
+            const uint32_t to = cluster_addr(&sh.part[odd][rank], lane);
+            store_cluster(to, (float)(uint32_t)(sum >> 32));
+            store_cluster(to + 4, (float)(uint32_t)sum);
+            store_cluster(to + 8, m);
+            barrier_arrive_cluster(cluster_addr(&sh.exchange[odd], lane));
         }
+        __syncthreads();  // what the teacher makes of the sums
+        if (grad) {
+            const Answer w = sh.answer;
+            if (w.kind == SV_OK) {
+                write_part<ES>(p, grad, [&](uint32_t i) { return exp_scaled<ES>(slice[i], w.m, ch, cl, w.k); });
+                sync_walkers();  // the listed entries' gradients come after the others'
+                if (own) {
+                    const float q = expf((mine - w.M) * a.iT) * w.iS, t = expf(sh.a[tid] - sh.list_max) / sh.list_sum;
+                    store_entry<ES>(grad, x, w.g * (w.total * q - t));
+                }
+            } else {  // zeros without a teacher, else NaN
+                const uint32_t v = w.kind < 0 ? 0u : ES == 4 ? 0x7fffffffu : 0x7fff7fffu;
+                write_part<ES>(p, grad, [&](uint32_t) { return make_uint4(v, v, v, v); });
+            }
+        }
+        // what was written into the slice comes before the copies that fill it next
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
+    if (scribe && rank == 0)
+        settle();
+    // no CTA leaves before the others have written into it for the last time
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
 }
 
 // Attributes of the kernels on a device, once.
@@ -440,6 +768,30 @@ bool setup(int device) {
     if (device < 64)
         done.fetch_or(bit, std::memory_order_release);
     return true;
+}
+
+// How many clusters of a shape run at once: asked once for each shape.
+int resident(const void* fn, int device, int es, const cudaLaunchConfig_t& like) {
+    struct Known {
+        int device, es, C, smem, clusters;
+    };
+    static std::mutex mutex;
+    static Known known[64];
+    static int count = 0;
+    const int C = (int)like.attrs[0].val.clusterDim.x, smem = (int)like.dynamicSmemBytes;
+    std::lock_guard<std::mutex> lock(mutex);
+    for (int i = 0; i < (count < 64 ? count : 64); ++i)
+        if (known[i].device == device && known[i].es == es && known[i].C == C && known[i].smem == smem)
+            return known[i].clusters;
+    cudaLaunchConfig_t cfg = like;
+    cfg.gridDim = dim3((unsigned)C, 1, 1);
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n < 1) {
+        (void)cudaGetLastError();
+        return 0;
+    }
+    known[count++ % 64] = Known{device, es, C, smem, n};
+    return n;
 }
 
 }  // namespace
@@ -500,17 +852,24 @@ int spec_distill_run(sv_ctx* ctx, const void* draft_logits, int logits_dtype, in
     a.status = status;
     a.err_word = ctx->d_err;
     a.V = V;
+    a.rows = rows;
     a.rows_per_seq = rows_per_seq;
     a.C = plan.cluster;
     a.n = n;
     a.tail = tail;
     a.vectors = (uint32_t)(plan.slice * es / 16);
-    a.T = temperature;
-    a.ch = (float)(1.4426950408889634074 / (double)temperature);
+    a.iT = (float)(1.0 / (double)temperature);
+    a.iTl = (float)(1.0 / (double)temperature - (double)a.iT);
+    const double c = 1.4426950408889634074 / (double)temperature;
+    a.ch = (float)c;
+    if ((double)a.ch > c)
+        a.ch = std::nextafterf(a.ch, 0.0f);
+    a.cl = (float)(c - (double)a.ch);
+    if (!(a.cl >= 1.17549435e-38f))  // a difference of -inf times it is -inf
+        a.cl = 1.17549435e-38f;
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof cfg);
-    cfg.gridDim = dim3((unsigned)plan.grid, 1, 1);
-    cfg.blockDim = dim3(kNT, 1, 1);
+    cfg.blockDim = dim3(kNT + 64, 1, 1);
     cfg.dynamicSmemBytes = (size_t)plan.smem_bytes;
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[1];
@@ -523,7 +882,16 @@ int spec_distill_run(sv_ctx* ctx, const void* draft_logits, int logits_dtype, in
     DeviceGuard guard(ctx->device);
     if (!setup(ctx->device))
         return SV_ERR_CUDA;
-    if (cudaLaunchKernelEx(&cfg, es == 2 ? sv_distill_kernel<2> : sv_distill_kernel<4>, a) != cudaSuccess) {
+    const auto kernel = es == 2 ? sv_distill_kernel<2> : sv_distill_kernel<4>;
+    int64_t clusters = rows;
+    if (plan.grid > ctx->num_sms) {  // as many as run at once, which take the rows in turn
+        const int most_clusters = resident((const void*)kernel, ctx->device, es, cfg);
+        if (most_clusters < 1)
+            return SV_ERR_CUDA;
+        clusters = rows < most_clusters ? rows : most_clusters;
+    }
+    cfg.gridDim = dim3((unsigned)(clusters * plan.cluster), 1, 1);
+    if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) {
         (void)cudaGetLastError();
         return SV_ERR_CUDA;
     }

@@ -6,7 +6,8 @@
 
 namespace sv {
 
-constexpr int kDistillThreads = 256;
+constexpr int kDistillThreads = 224;     // that walk a slice; two warps beside them have the list and the loss
+constexpr int kDistillCtas = 3;           // that fit an SM
 constexpr int kDistillMaxList = 128;
 constexpr int kDistillSmem = 221184;      // a CTA's slice at most (216 KB, beside the fixed state)
 constexpr int kDistillFullSmem = 73728;   // a slice of which three CTAs fit an SM

@@ -41,11 +41,8 @@ extern "C" int spec_distill_plan_for(int num_sms, int max_cluster, int B, int ro
     if (ovr_cluster) {
         C = ovr_cluster;
     } else {
-        for (int c = 1; c <= most; c *= 2) {  // the least whose slices leave an SM three CTAs, else the most
-            C = c;
-            if (ceil_div(vectors, c) * 16 <= kDistillFullSmem)
-                break;
-        }
+        for (C = 1; C < most && ceil_div(vectors, C) * 16 > kDistillFullSmem;)  // the least of which an SM takes three
+            ++C;
         // few rows: more CTAs for each, down to 512 vectors a slice
         while (2 * C <= most && rows * 2 * C <= num_sms && ceil_div(vectors, 2 * C) >= 512)
             C *= 2;
@@ -55,7 +52,7 @@ extern "C" int spec_distill_plan_for(int num_sms, int max_cluster, int B, int ro
         return SV_ERR_UNSUPPORTED;
     out->cluster = C;
     out->group = 1;
-    out->threads = kDistillThreads;
+    out->threads = kDistillThreads + 64;
     out->smem_bytes = (int)(per * 16);
     out->slice = per * entries;
     out->grid = rows * C;

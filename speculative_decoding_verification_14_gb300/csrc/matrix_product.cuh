@@ -33,25 +33,6 @@ struct MatrixBarriers {
     uint32_t tmem, failed;
 };
 
-__device__ __forceinline__ uint32_t first_cta(uint32_t addr) {  // the same place in the pair's first CTA
-    uint32_t r;
-    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
-    return r;
-}
-__device__ __forceinline__ void barrier_arrive_cluster(uint32_t addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
-}
-__device__ __forceinline__ bool barrier_try_cluster(uint64_t* bar, uint32_t parity) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(shared_addr(bar)), "r"(parity)
-        : "memory");
-    return done != 0;
-}
 // Waits for a phase, at most kWaitNs; whoever gives up says so to the CTA's other warps, which then give up too.
 static __device__ __noinline__ bool matrix_wait_slow(uint64_t* bar, uint32_t parity, volatile uint32_t* failed) {
     const unsigned long long t0 = global_ns();
@@ -206,7 +187,7 @@ __device__ __forceinline__ void run_tiles(const CUtensorMap* map_a, const CUtens
                         break;
                     }
                     // both CTAs' copies arrive on the first one's barrier
-                    const uint32_t bar = first_cta(shared_addr(&bars.full[stage]));
+                    const uint32_t bar = cluster_addr(&bars.full[stage], 0);
                     if (rank == 0)
                         barrier_expect(&bars.full[stage], 2 * kStageBytes);
                     const uint32_t at = stage0 + stage * kStageBytes, bt = at + kOperandBytes;
@@ -300,7 +281,7 @@ __device__ __forceinline__ void run_tiles(const CUtensorMap* map_a, const CUtens
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
             __syncwarp();
             if (lane == 0)
-                barrier_arrive_cluster(first_cta(shared_addr(&bars.tile_empty[t])));
+                barrier_arrive_cluster(cluster_addr(&bars.tile_empty[t], 0));
             if (++t == 2)
                 t = 0, tphase ^= 1u;
         }

@@ -292,3 +292,40 @@ def test_two_threads_on_streams_of_their_own():
     for t in ts:
         t.join()
     assert not failed, failed
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("cluster,V", [(0, 3001), (4, 9011), (3, 4003)])
+def test_more_rows_than_run_at_once(cluster, V, dtype):
+    """Clusters take row after row: live ones, ones behind the last, ones without a list and erroneous ones."""
+    torch = _torch()
+    v = gh.verifier()
+    B, rows = 260, 4
+    z, a, x, w = make(B, rows, V, 12, dtype, V)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    lens = torch.randint(0, rows + 1, (B,), device="cuda", generator=g, dtype=torch.int32)
+    lens[100:180] = 0  # many in turn that a CTA has nothing to do for
+    x[::7, 0] = -1
+    z[::11, 1, V - 1] = float("nan")
+    x[::13, 2, 3] = x[::13, 2, 9]
+    v.set_plan_override(cluster)
+    try:
+        for tail in (False, True):
+            out = v.distill(z, a, x, lens, tail=tail, grad_loss=w)
+            check(out, z, a, x, 1.0, tail, w, lens.cpu(), dtype)
+    finally:
+        v.set_plan_override(0)
+        v.error()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_entries_far_above_the_rest(dtype):
+    """Off the list, where no thread's first vector lies, and so far that a sum against those overflows."""
+    torch = _torch()
+    V = 40000
+    z, a, x, w = make(6, 1, V, 16, dtype, 53, spread=1.0)
+    for i, (at, top) in enumerate([(39999, 12.0), (39999, 40.0), (30011, 200.0), (17777, 3e4), (39990, 3e38)]):
+        z[i, 0, at] = top
+    z[5, 0, :20000] = -float("inf")  # a slice without a logit in its first vectors
+    for tail in (False, True):
+        check(gh.verifier().distill(z, a, x, tail=tail, grad_loss=w), z, a, x, 1.0, tail, w, dtype=dtype)

@@ -60,7 +60,7 @@ def test_distill_plans(sv, B, rows, V, dtype):
     rc, p = sv.spec_distill_plan_for(152, 16, B, rows, V, dtype)
     assert rc == sv.SV_OK
     C, s, E = p["cluster"], p["slice"], 8 if dtype else 4
-    assert C in (1, 2, 4, 8, 16) and p["grid"] == B * rows * C
+    assert 1 <= C <= 16 and p["grid"] == B * rows * C
     assert s % E == 0 and s * C >= V + E - 1 and p["smem_bytes"] == s // E * 16 <= 216 * 1024
     for c in (1, 3, 16):
         rc, p = sv.spec_distill_plan_for(152, 16, B, rows, V, dtype, c)
