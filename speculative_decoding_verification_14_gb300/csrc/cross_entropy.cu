@@ -87,6 +87,7 @@ __device__ __forceinline__ int row_kind(const Rows& a, int64_t row) {
 __global__ void __launch_bounds__(256) sv_ce_rows_kernel(const __grid_constant__ Rows a) {
     __shared__ int before;
     __shared__ int kinds[kRowsPerBlock];
+    launch_next();
     const int tid = threadIdx.x;
     const int64_t r0 = (int64_t)blockIdx.x * kRowsPerBlock, end = r0 < a.R ? r0 : a.R;
     if (tid == 0)
@@ -108,23 +109,27 @@ __global__ void __launch_bounds__(256) sv_ce_rows_kernel(const __grid_constant__
                 a.packed[at * a.depth + d] = __float2bfloat16_rn(0.0f);
         return;
     }
-    int64_t at = before;
-    for (int i = 0; i < kRowsPerBlock && r0 + i < a.R; ++i) {
-        const int64_t row = r0 + i;
-        const int kind = kinds[i];
+    // a row a warp
+    const int warp = tid >> 5, lane = tid & 31;
+    const int64_t row = r0 + warp;
+    if (row < a.R) {
+        int64_t at = before;
+        for (int i = 0; i < warp; ++i)
+            at += kinds[i] == 0;
+        const int kind = kinds[warp];
         if (kind == 0) {
             const __nv_bfloat16* src = a.hidden + row * a.stride;
             __nv_bfloat16* dst = a.packed + at * a.depth;
+            int64_t done = 0;
             if ((reinterpret_cast<uintptr_t>(src) & 15u) == 0) {
-                for (int64_t d = tid; d < a.D / 8; d += blockDim.x)
+                done = a.D / 8 * 8;
+#pragma unroll 4
+                for (int64_t d = lane; d < a.D / 8; d += 32)
                     reinterpret_cast<uint4*>(dst)[d] = reinterpret_cast<const uint4*>(src)[d];
-                for (int64_t d = a.D / 8 * 8 + tid; d < a.D; d += blockDim.x)
-                    dst[d] = src[d];
-            } else {
-                for (int64_t d = tid; d < a.D; d += blockDim.x)
-                    dst[d] = src[d];
             }
-            if (tid == 0) {
+            for (int64_t d = done + lane; d < a.D; d += 32)
+                dst[d] = src[d];
+            if (lane == 0) {
                 a.index[at] = (int32_t)row;
                 a.label[at] = a.labels[row];
                 if (a.packed_lse) {
@@ -134,26 +139,25 @@ __global__ void __launch_bounds__(256) sv_ce_rows_kernel(const __grid_constant__
                     a.scale[at] = a.grad_loss ? a.grad_loss[row] : 1.0f;
                 }
             }
-            ++at;
-            continue;
+        } else {
+            const float x = kind == 1 ? 0.0f : __int_as_float(0x7fffffff);
+            if (lane == 0) {
+                if (a.loss)
+                    a.loss[row] = x;
+                if (a.lse_out)
+                    a.lse_out[row] = x;
+                if (a.status)
+                    a.status[row] = kind == 1 ? SV_OK : kind;
+                if (kind != 1)
+                    atomicOr(a.err_word, 1u << kind);
+            }
+            if (a.grad_hidden)
+                for (int64_t d = lane; d < a.D; d += 32)
+                    a.grad_hidden[row * a.grad_stride + d] = __float2bfloat16_rn(x);
         }
-        const float nan = __int_as_float(0x7fffffff), x = kind == 1 ? 0.0f : nan;
-        if (tid == 0) {
-            if (a.loss)
-                a.loss[row] = x;
-            if (a.lse_out)
-                a.lse_out[row] = x;
-            if (a.status)
-                a.status[row] = kind == 1 ? SV_OK : kind;
-            if (kind != 1)
-                atomicOr(a.err_word, 1u << kind);
-        }
-        if (a.grad_hidden)
-            for (int64_t d = tid; d < a.D; d += blockDim.x)
-                a.grad_hidden[row * a.grad_stride + d] = __float2bfloat16_rn(x);
+        if (lane == 0 && row == a.R - 1)
+            *a.count = (int32_t)(at + (kind == 0));
     }
-    if (tid == 0 && r0 + kRowsPerBlock >= a.R)
-        *a.count = (int32_t)at;
 }
 
 // ---------------------------------------------------------------- tiles
@@ -182,6 +186,8 @@ struct Tiles {
     int out_vectors;  // rows of out lie on 16 bytes
 };
 
+// What a launch needs of the one before it is read behind wait_previous(), which run_tiles calls once its own
+// barriers and tensor memory are set up.
 __device__ __forceinline__ int64_t packed_rows(const Tiles& p) { return *p.count; }
 // the row of a tile that this thread has in tensor memory
 __device__ __forceinline__ int64_t tile_row(int64_t tile) {
@@ -193,8 +199,11 @@ __device__ __forceinline__ int64_t tile_row(int64_t tile) {
 // (maximum, sum of exponentials) of each row's logits in each tile of the vocabulary
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsMm, 1)
     sv_ce_stats_kernel(const __grid_constant__ Tiles p) {
-    const int64_t n = packed_rows(p);
-    const MatrixShape shape{(n + kTile - 1) / kTile, p.tiles, (p.D + kBlockK - 1) / kBlockK, 1};
+    int64_t n = 0;
+    const auto shape = [&] {
+        n = packed_rows(p);
+        return MatrixShape{(n + kTile - 1) / kTile, p.tiles, (p.D + kBlockK - 1) / kBlockK, 1};
+    };
     run_tiles<false, false>(&p.a, &p.b, shape, 0, 0, p.err_word, 1u << SV_ERR_TIMEOUT,
                             [&](int64_t rt, int64_t ct, int, auto load) {
         const int64_t row = tile_row(rt), c0 = ct * kTile;
@@ -242,8 +251,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsMm, 1)
 // d of a piece of the vocabulary, bfloat16; zeros in rows and columns that only fill up tiles
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsMm, 1)
     sv_ce_probs_kernel(const __grid_constant__ Tiles p) {
-    const int64_t n = packed_rows(p);
-    const MatrixShape shape{(n + kTile - 1) / kTile, p.tiles, (p.D + kBlockK - 1) / kBlockK, 1};
+    int64_t n = 0;
+    const auto shape = [&] {
+        n = packed_rows(p);
+        return MatrixShape{(n + kTile - 1) / kTile, p.tiles, (p.D + kBlockK - 1) / kBlockK, 1};
+    };
     run_tiles<false, false>(&p.a, &p.b, shape, p.first_tile * kTile, 0, p.err_word, 1u << SV_ERR_TIMEOUT,
                             [&](int64_t rt, int64_t ct, int, auto load) {
         const int64_t row = tile_row(rt), c0 = (p.first_tile + ct) * kTile;
@@ -278,8 +290,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsMm, 1)
 // a piece's part of the hidden states' gradient: float32 sums, those of a split apart
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsMm, 1)
     sv_ce_hidden_kernel(const __grid_constant__ Tiles p) {
-    const int64_t n = packed_rows(p);
-    const MatrixShape shape{(n + kTile - 1) / kTile, (p.D + kTile - 1) / kTile, p.tiles * (kTile / kBlockK), p.splits};
+    int64_t n = 0;
+    const auto shape = [&] {
+        n = packed_rows(p);
+        return MatrixShape{(n + kTile - 1) / kTile, (p.D + kTile - 1) / kTile, p.tiles * (kTile / kBlockK), p.splits};
+    };
     run_tiles<false, true>(&p.a, &p.b, shape, 0, p.first_tile * kTile, p.err_word, 1u << SV_ERR_TIMEOUT,
                            [&](int64_t rt, int64_t ct, int split, auto load) {
         const int64_t row = tile_row(rt), c0 = ct * kTile;
@@ -304,8 +319,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsMm, 1)
 // a piece's rows of the head's gradient
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsMm, 1)
     sv_ce_weight_kernel(const __grid_constant__ Tiles p) {
-    const int64_t n = packed_rows(p);
-    const MatrixShape shape{p.tiles, (p.D + kTile - 1) / kTile, (n + kBlockK - 1) / kBlockK, 1};
+    int64_t n = 0;
+    const auto shape = [&] {
+        n = packed_rows(p);
+        return MatrixShape{p.tiles, (p.D + kTile - 1) / kTile, (n + kBlockK - 1) / kBlockK, 1};
+    };
     run_tiles<true, true>(&p.a, &p.b, shape, 0, 0, p.err_word, 1u << SV_ERR_TIMEOUT,
                           [&](int64_t rt, int64_t ct, int, auto load) {
         const int64_t v_id = p.first_tile * kTile + tile_row(rt), c0 = ct * kTile;
@@ -354,35 +372,47 @@ struct Join {
     int64_t grad_stride;
 };
 
-// 32 rows a block, their tiles over 8 threads each
+// Eight rows a block, their tiles over 32 threads each: first the largest maximum, then the sums against it.
 __global__ void __launch_bounds__(256) sv_ce_join_kernel(const __grid_constant__ Join a) {
-    __shared__ float2 part[8][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t row = (int64_t)blockIdx.x * 32 + lane;
+    __shared__ float part[32][8];
+    launch_next();
+    wait_previous();
+    const int at = threadIdx.x & 7, share = threadIdx.x >> 3;
+    const int64_t row = (int64_t)blockIdx.x * 8 + at;
     const int64_t n = *a.count;
-    if ((int64_t)blockIdx.x * 32 >= n)
+    if ((int64_t)blockIdx.x * 8 >= n)
         return;
     const float inf = __int_as_float(0x7f800000);
+    const float2* stats = a.stats + row;
     float m = -inf, s = 0.0f;
-    const auto join = [&](float m1, float s1) {
-        float top = m;
-        asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(m1));
-        s = (m > -inf ? s * ex2((m - top) * kLog2e) : 0.0f) + (m1 > -inf ? s1 * ex2((m1 - top) * kLog2e) : 0.0f);
-        m = top;
-    };
-    if (row < n)
-        for (int64_t t = warp; t < a.tiles; t += 8) {
-            const float2 x = a.stats[t * a.rows + row];
-            join(x.x, x.y);
-        }
-    part[warp][lane] = make_float2(m, s);
+    if (row < n) {
+#pragma unroll 4
+        for (int64_t t = share; t < a.tiles; t += 32)
+            asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(stats[t * a.rows].x));
+    }
+    part[share][at] = m;
     __syncthreads();
-    if (warp || row >= n)
-        return;
-    for (int w = 1; w < 8; ++w)
-        join(part[w][lane].x, part[w][lane].y);
-    const int64_t to = a.index[row];
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(part[i][at]));
     const bool good = m > -inf && m < inf;
+    if (row < n && good) {
+#pragma unroll 4
+        for (int64_t t = share; t < a.tiles; t += 32) {
+            const float2 x = stats[t * a.rows];
+            s += x.y * expf(x.x - m);
+        }
+    }
+    __syncthreads();
+    part[share][at] = s;
+    __syncthreads();
+    if (share || row >= n)
+        return;
+    s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        s += part[i][at];
+    const int64_t to = a.index[row];
     const float ls = logf(s), nan = __int_as_float(0x7fffffff);
     a.loss[to] = good ? (m - a.label_logit[row]) + ls : nan;
     a.lse[to] = good ? m + ls : nan;
@@ -392,17 +422,33 @@ __global__ void __launch_bounds__(256) sv_ce_join_kernel(const __grid_constant__
         atomicOr(a.err_word, 1u << SV_ERR_NONFINITE);
 }
 
-// a row a block: the splits' sums, rounded once
+// Four columns a thread: the splits' sums, rounded once.
 __global__ void __launch_bounds__(256) sv_ce_hidden_join_kernel(const __grid_constant__ Join a) {
-    const int64_t row = blockIdx.x;
-    if (row >= *a.count)
+    launch_next();
+    wait_previous();
+    const int64_t row = blockIdx.x, d = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 4;
+    if (row >= *a.count || d >= a.D)
         return;
-    __nv_bfloat16* out = a.grad_hidden + (int64_t)a.index[row] * a.grad_stride;
-    for (int64_t d = threadIdx.x; d < a.D; d += blockDim.x) {
-        float x = 0.0f;
-        for (int s = 0; s < a.splits; ++s)
-            x += a.sums[((int64_t)s * a.rows + row) * a.depth + d];
-        out[d] = __float2bfloat16_rn(x);
+    const float4* from = reinterpret_cast<const float4*>(a.sums + row * a.depth + d);
+    const int64_t apart = a.rows * a.depth / 4;
+    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+    for (int s = 0; s < a.splits; ++s) {
+        const float4 y = from[s * apart];
+        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+    }
+    __nv_bfloat16* out = a.grad_hidden + (int64_t)a.index[row] * a.grad_stride + d;
+    if (d + 4 <= a.D && (reinterpret_cast<uintptr_t>(out) & 7u) == 0) {
+        uint2 w;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.x) : "f"(x.y), "f"(x.x));
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w.y) : "f"(x.w), "f"(x.z));
+        *reinterpret_cast<uint2*>(out) = w;
+    } else {
+        const float v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (d + e < a.D)
+                out[e] = __float2bfloat16_rn(v[e]);
     }
 }
 
@@ -472,10 +518,29 @@ int matrix_pairs(int device) {
     return least;
 }
 
+// A launch that may begin while the one before it, of the same call, ends: it waits for that one's results itself.
+template <typename Args>
+bool launch_after(void (*fn)(const Args), const Args& args, dim3 grid, int threads, int smem, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof cfg);
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, fn, args) == cudaSuccess)
+        return true;
+    (void)cudaGetLastError();
+    return false;
+}
+
 bool launch_tiles(TilesFn fn, const Tiles& p, int64_t most, int pairs, cudaStream_t stream) {
     const int64_t n = most < pairs ? most : pairs;
-    fn<<<dim3((unsigned)(2 * (n < 1 ? 1 : n))), kThreadsMm, kSmemMm, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess;
+    return launch_after(fn, p, dim3((unsigned)(2 * (n < 1 ? 1 : n)), 1, 1), kThreadsMm, kSmemMm, stream);
 }
 
 int check(const sv_ctx* ctx, const void* hidden, int dtype, int64_t hidden_stride, const void* weight,
@@ -583,8 +648,7 @@ int spec_cross_entropy_run(sv_ctx* ctx, const void* hidden, int dtype, int64_t h
     if (cudaGetLastError() != cudaSuccess ||
         !launch_tiles(sv_ce_stats_kernel, p, plan.rows / kTile * plan.vocab_tiles, pairs, st))
         return SV_ERR_CUDA;
-    sv_ce_join_kernel<<<(unsigned)((r.R + 31) / 32), 256, 0, st>>>(j);
-    return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+    return launch_after(sv_ce_join_kernel, j, dim3((unsigned)((r.R + 7) / 8), 1, 1), 256, 0, st) ? SV_OK : SV_ERR_CUDA;
 }
 
 int spec_cross_entropy_grad(sv_ctx* ctx, const void* hidden, int dtype, int64_t hidden_stride, const void* weight,
@@ -676,8 +740,7 @@ int spec_cross_entropy_grad(sv_ctx* ctx, const void* hidden, int dtype, int64_t 
         j.splits = plan.splits;
         j.grad_hidden = r.grad_hidden;
         j.grad_stride = grad_hidden_stride;
-        sv_ce_hidden_join_kernel<<<(unsigned)R, 256, 0, st>>>(j);
-        if (cudaGetLastError() != cudaSuccess)
+        if (!launch_after(sv_ce_hidden_join_kernel, j, dim3((unsigned)R, (unsigned)((D + 1023) / 1024), 1), 256, 0, st))
             return SV_ERR_CUDA;
     }
     return SV_OK;

@@ -95,6 +95,10 @@ __device__ __forceinline__ void copy_bulk(void* dst, const void* src, uint32_t b
                  : "memory");
 }
 
+// Of launches that may overlap: lets the next one begin, and waits until the one before has ended and its writes
+// are seen.
+__device__ __forceinline__ void launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // global to L2, the same alignment
 __device__ __forceinline__ void prefetch_bulk(const void* src, uint32_t bytes) {
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");

@@ -129,12 +129,12 @@ struct MatrixShape {
     }
 };
 
-// Runs the pair's tiles.  a0, b0: rows (columns for a turned operand) at which the operands begin in their maps,
-// ka, kb: depths likewise.  finish(row tile, column tile, split, load) is called by the four tile warps of each CTA
+// Runs the pair's tiles, of a shape that is asked for once the launch before has ended.  b0: row (column for a turned
+// operand) at which B begins in its map, kb: depth likewise.  finish(row tile, column tile, split, load) is called by the four tile warps of each CTA
 // for each tile; load(c, v) gives columns c .. c + 31 of the thread's row, and has to be called by whole warps;
 // without a single block of depth the tile is all zeros and load gives them.
-template <bool TurnedA, bool TurnedB, typename Finish>
-__device__ __forceinline__ void run_tiles(const CUtensorMap* map_a, const CUtensorMap* map_b, const MatrixShape& shape,
+template <bool TurnedA, bool TurnedB, typename Shape, typename Finish>
+__device__ __forceinline__ void run_tiles(const CUtensorMap* map_a, const CUtensorMap* map_b, Shape shape_of,
                                           int64_t b0, int64_t kb, uint32_t* err_word, uint32_t timeout_bit,
                                           Finish finish) {
     extern __shared__ unsigned char dynamic[];
@@ -169,6 +169,9 @@ __device__ __forceinline__ void run_tiles(const CUtensorMap* map_a, const CUtens
     asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = *(volatile uint32_t*)&bars.tmem;
+    launch_next();
+    wait_previous();
+    const MatrixShape shape = shape_of();
 
     if (warp == 0) {
         if (lane == 0) {
