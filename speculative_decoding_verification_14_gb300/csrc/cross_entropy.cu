@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(256) sv_ce_rows_kernel(const __grid_constant__
 // ---------------------------------------------------------------- tiles
 
 struct Tiles {
-    CUtensorMap a, b;
+    CUtensorMap a, b, c;  // c: what is written
     const int32_t* count;
     const int32_t* label;
     uint32_t* err_word;
@@ -176,14 +176,12 @@ struct Tiles {
     // gradients
     const float* lse;
     const float* scale;
-    __nv_bfloat16* probs;
-    int64_t probs_stride;
     float* sums;
     int64_t depth;
     int splits, add;
     __nv_bfloat16* out;
     int64_t out_stride;
-    int out_vectors;  // rows of out lie on 16 bytes
+    int out_vectors;  // rows of out lie on 16 bytes: written through c, else entry by entry
 };
 
 // What a launch needs of the one before it is read behind wait_previous(), which run_tiles calls once its own
@@ -251,6 +249,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsMm, 1)
 // d of a piece of the vocabulary, bfloat16; zeros in rows and columns that only fill up tiles
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsMm, 1)
     sv_ce_probs_kernel(const __grid_constant__ Tiles p) {
+    TileStore store;
     int64_t n = 0;
     const auto shape = [&] {
         n = packed_rows(p);
@@ -262,29 +261,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsMm, 1)
         const bool there = row < n;
         const int64_t y = there ? p.label[row] - c0 : -1;
         const float lse = there ? p.lse[row] : 0.0f, g = there ? p.scale[row] : 0.0f;
-        __nv_bfloat16* out = p.probs + row * p.probs_stride + ct * kTile;
-        for (int c = 0; c < kTile; c += 32) {
-            float v[32];
-            load(c, v);
-            const int left = there ? (int)(p.V - c0 - c < 32 ? p.V - c0 - c : 32) : 0;
+        // rows behind those that fill up the last block of depth are read by nobody
+        const int64_t warp_row = row - (threadIdx.x & 31);
+        if (warp_row >= (n + kBlockK - 1) / kBlockK * kBlockK)
+            return;
+        for (int c = 0; c < kTile; c += 64) {
+            float v[64];
+            load(c, *reinterpret_cast<float(*)[32]>(v));
+            load(c + 32, *reinterpret_cast<float(*)[32]>(v + 32));
+            const int left = there ? (int)(p.V - c0 - c < 64 ? p.V - c0 - c : 64) : 0;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
+            for (int e = 0; e < 64; ++e) {
                 float d = ex2((v[e] - lse) * kLog2e);
                 if (y == c + e)
                     d -= 1.0f;
                 v[e] = e < left ? d * g : 0.0f;
             }
-            uint4* to = reinterpret_cast<uint4*>(out + c);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                uint32_t w[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[e]) : "f"(v[q * 8 + 2 * e + 1]), "f"(v[q * 8 + 2 * e]));
-                to[q] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+            store.put(&p.c, (int)(ct * kTile + c), (int)warp_row, v);
         }
     });
+    if (threadIdx.x >= 128)
+        store.finish();
 }
 
 // a piece's part of the hidden states' gradient: float32 sums, those of a split apart
@@ -319,6 +316,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsMm, 1)
 // a piece's rows of the head's gradient
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsMm, 1)
     sv_ce_weight_kernel(const __grid_constant__ Tiles p) {
+    TileStore store;
     int64_t n = 0;
     const auto shape = [&] {
         n = packed_rows(p);
@@ -327,31 +325,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsMm, 1)
     run_tiles<true, true>(&p.a, &p.b, shape, 0, 0, p.err_word, 1u << SV_ERR_TIMEOUT,
                           [&](int64_t rt, int64_t ct, int, auto load) {
         const int64_t v_id = p.first_tile * kTile + tile_row(rt), c0 = ct * kTile;
+        if (p.out_vectors) {
+            for (int c = 0; c < kTile && c0 + c < p.D; c += 64) {
+                float v[64];
+                load(c, *reinterpret_cast<float(*)[32]>(v));
+                load(c + 32, *reinterpret_cast<float(*)[32]>(v + 32));
+                if (v_id - (threadIdx.x & 31) < p.V)  // what lies beyond the head is left out by the copy
+                    store.put(&p.c, (int)(c0 + c), (int)(v_id - (threadIdx.x & 31)), v);
+            }
+            return;
+        }
         __nv_bfloat16* out = p.out + v_id * p.out_stride + c0;
         for (int c = 0; c < kTile && c0 + c < p.D; c += 32) {
             float v[32];
             load(c, v);
-            if (v_id >= p.V)
-                continue;
+            if (v_id < p.V)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                if (p.out_vectors && c0 + c + 8 * q + 8 <= p.D) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
-                            : "=r"(w[e])
-                            : "f"(v[q * 8 + 2 * e + 1]), "f"(v[q * 8 + 2 * e]));
-                    reinterpret_cast<uint4*>(out + c)[q] = make_uint4(w[0], w[1], w[2], w[3]);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (c0 + c + 8 * q + e < p.D)
-                            out[c + 8 * q + e] = __float2bfloat16_rn(v[8 * q + e]);
-                }
-            }
+                for (int e = 0; e < 32; ++e)
+                    if (c0 + c + e < p.D)
+                        out[c + e] = __float2bfloat16_rn(v[e]);
         }
     });
+    if (threadIdx.x >= 128)
+        store.finish();
 }
 
 // ---------------------------------------------------------------- joins
@@ -695,8 +691,6 @@ int spec_cross_entropy_grad(sv_ctx* ctx, const void* hidden, int dtype, int64_t 
     logits.rows = plan.rows;
     logits.lse = r.packed_lse;
     logits.scale = r.scale;
-    logits.probs = probs;
-    logits.probs_stride = width;
     logits.sums = reinterpret_cast<float*>(ws + plan.sums);
     logits.depth = plan.depth;
     logits.splits = plan.splits;
@@ -709,7 +703,9 @@ int spec_cross_entropy_grad(sv_ctx* ctx, const void* hidden, int dtype, int64_t 
         !tensor_map(&hid.a, probs, plan.rows, width, width, kHalf) ||
         !tensor_map(&hid.b, weight, V, D, weight_stride, kBlockK) ||
         !tensor_map(&wgt.a, probs, plan.rows, width, width, kBlockK) ||
-        !tensor_map(&wgt.b, r.packed, plan.rows, D, plan.depth, kBlockK))
+        !tensor_map(&wgt.b, r.packed, plan.rows, D, plan.depth, kBlockK) ||
+        !tensor_map(&logits.c, probs, plan.rows, width, width, 32) ||
+        (grad_weight && logits.out_vectors && !tensor_map(&wgt.c, grad_weight, V, D, grad_weight_stride, 32)))
         return SV_ERR_CUDA;
     sv_ce_rows_kernel<<<(unsigned)((R + kRowsPerBlock - 1) / kRowsPerBlock + kBlockK), 256, 0, st>>>(r);
     if (cudaGetLastError() != cudaSuccess)

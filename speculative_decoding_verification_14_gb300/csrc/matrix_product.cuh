@@ -26,7 +26,9 @@ constexpr int kOperandBytes = kHalf * kBlockK * 2;  // one operand of one stage:
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kThreadsMm = 256;  // warps: copies, products, tensor memory, none, four for tiles
 constexpr int kTmemColumns = 512;
-constexpr int kSmemMm = kStagesMm * kStageBytes + 1024;  // and the distance to a multiple of 1024
+constexpr int kStoreBytes = 32 * 128;  // 32 rows of 64 bfloat16 columns on their way out
+constexpr int kSmemMm = kStagesMm * kStageBytes + 8 * kStoreBytes + 1024;  // two for each tile warp; and the
+                                                                           // distance to a multiple of 1024
 
 struct MatrixBarriers {
     uint64_t full[kStagesMm], empty[kStagesMm], tile_full[2], tile_empty[2];
@@ -107,6 +109,51 @@ __device__ __forceinline__ void load_columns(uint32_t addr, float (&v)[32]) {
     for (int i = 0; i < 32; ++i)
         v[i] = __uint_as_float(r[i]);
 }
+
+// 64 columns of a tile warp's 32 rows, rounded to bfloat16, out through shared memory: a thread has a row, whose
+// 16-byte parts go to places swizzled as the copy engine takes them (no two lanes of eight in a bank), and one lane
+// hands the box to it.  Lane 0 of each warp waits for its own copies alone; two boxes take turns.
+struct TileStore {
+    uint32_t at;  // this warp's two boxes
+    int turn = 0;
+    __device__ __forceinline__ TileStore() {
+        extern __shared__ unsigned char dynamic[];
+        at = ((shared_addr(dynamic) + 1023u) & ~1023u) + kStagesMm * kStageBytes +
+             ((threadIdx.x >> 5) & 3) * 2 * kStoreBytes;
+    }
+    __device__ __forceinline__ void put(const CUtensorMap* map, int x, int y, const float (&v)[64]) {
+        const int lane = threadIdx.x & 31;
+        if (lane == 0)
+            asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+        __syncwarp();
+        const uint32_t box = at + turn * kStoreBytes, row = box + lane * 128;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[e]) : "f"(v[8 * q + 2 * e + 1]), "f"(v[8 * q + 2 * e]));
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + ((q ^ (lane & 7)) << 4)), "r"(w[0]),
+                         "r"(w[1]), "r"(w[2]), "r"(w[3])
+                         : "memory");
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+            asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map),
+                         "r"(box), "r"(x), "r"(y)
+                         : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+        turn ^= 1;
+    }
+    // all of it is in memory
+    __device__ __forceinline__ void finish() {
+        if ((threadIdx.x & 31) == 0)
+            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        __syncwarp();
+    }
+};
 
 // What a pair computes: `rows` x `columns` tiles, each over blocks k0 .. k1 - 1 of its split of the depth.
 struct MatrixShape {
