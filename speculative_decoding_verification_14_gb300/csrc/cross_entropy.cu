@@ -170,6 +170,7 @@ struct Tiles {
     int64_t V, D;
     int64_t first_tile, tiles;  // vocabulary tiles of this launch
     int64_t rows;               // of the workspace
+    int a_rows;                 // the most that count, up to a tile's
     // loss
     float2* stats;
     float* label_logit;
@@ -202,7 +203,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsMm, 1)
         n = packed_rows(p);
         return MatrixShape{(n + kTile - 1) / kTile, p.tiles, (p.D + kBlockK - 1) / kBlockK, 1};
     };
-    run_tiles<false, false>(&p.a, &p.b, shape, 0, 0, p.err_word, 1u << SV_ERR_TIMEOUT,
+    run_tiles<false, false>(&p.a, &p.b, p.a_rows, shape, 0, 0, p.err_word, 1u << SV_ERR_TIMEOUT,
                             [&](int64_t rt, int64_t ct, int, auto load) {
         const int64_t row = tile_row(rt), c0 = ct * kTile;
         const bool there = row < n;
@@ -255,7 +256,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsMm, 1)
         n = packed_rows(p);
         return MatrixShape{(n + kTile - 1) / kTile, p.tiles, (p.D + kBlockK - 1) / kBlockK, 1};
     };
-    run_tiles<false, false>(&p.a, &p.b, shape, p.first_tile * kTile, 0, p.err_word, 1u << SV_ERR_TIMEOUT,
+    run_tiles<false, false>(&p.a, &p.b, p.a_rows, shape, p.first_tile * kTile, 0, p.err_word, 1u << SV_ERR_TIMEOUT,
                             [&](int64_t rt, int64_t ct, int, auto load) {
         const int64_t row = tile_row(rt), c0 = (p.first_tile + ct) * kTile;
         const bool there = row < n;
@@ -292,7 +293,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsMm, 1)
         n = packed_rows(p);
         return MatrixShape{(n + kTile - 1) / kTile, (p.D + kTile - 1) / kTile, p.tiles * (kTile / kBlockK), p.splits};
     };
-    run_tiles<false, true>(&p.a, &p.b, shape, 0, p.first_tile * kTile, p.err_word, 1u << SV_ERR_TIMEOUT,
+    run_tiles<false, true>(&p.a, &p.b, p.a_rows, shape, 0, p.first_tile * kTile, p.err_word, 1u << SV_ERR_TIMEOUT,
                            [&](int64_t rt, int64_t ct, int split, auto load) {
         const int64_t row = tile_row(rt), c0 = ct * kTile;
         float* out = p.sums + ((int64_t)split * p.rows + row) * p.depth + c0;
@@ -322,7 +323,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsMm, 1)
         n = packed_rows(p);
         return MatrixShape{p.tiles, (p.D + kTile - 1) / kTile, (n + kBlockK - 1) / kBlockK, 1};
     };
-    run_tiles<true, true>(&p.a, &p.b, shape, 0, 0, p.err_word, 1u << SV_ERR_TIMEOUT,
+    run_tiles<true, true>(&p.a, &p.b, p.a_rows, shape, 0, 0, p.err_word, 1u << SV_ERR_TIMEOUT,
                           [&](int64_t rt, int64_t ct, int, auto load) {
         const int64_t v_id = p.first_tile * kTile + tile_row(rt), c0 = ct * kTile;
         if (p.out_vectors) {
@@ -616,7 +617,7 @@ int spec_cross_entropy_run(sv_ctx* ctx, const void* hidden, int dtype, int64_t h
     r.status = status;
     Tiles p;
     std::memset(&p, 0, sizeof p);
-    if (!tensor_map(&p.a, r.packed, plan.rows, D, plan.depth, kHalf) ||
+    if (!tensor_map(&p.a, r.packed, plan.rows, D, plan.depth, box_rows(r.R)) ||
         !tensor_map(&p.b, weight, V, D, weight_stride, kHalf))
         return SV_ERR_CUDA;
     p.count = r.count;
@@ -626,6 +627,7 @@ int spec_cross_entropy_run(sv_ctx* ctx, const void* hidden, int dtype, int64_t h
     p.D = D;
     p.tiles = plan.vocab_tiles;
     p.rows = plan.rows;
+    p.a_rows = (int)(r.R < kTile ? r.R : kTile);
     p.stats = reinterpret_cast<float2*>(ws + plan.stats);
     p.label_logit = reinterpret_cast<float*>(ws + plan.label_logit);
     Join j;
@@ -689,6 +691,7 @@ int spec_cross_entropy_grad(sv_ctx* ctx, const void* hidden, int dtype, int64_t 
     logits.V = V;
     logits.D = D;
     logits.rows = plan.rows;
+    logits.a_rows = (int)(R < kTile ? R : kTile);
     logits.lse = r.packed_lse;
     logits.scale = r.scale;
     logits.sums = reinterpret_cast<float*>(ws + plan.sums);
@@ -698,9 +701,9 @@ int spec_cross_entropy_grad(sv_ctx* ctx, const void* hidden, int dtype, int64_t 
     logits.out_stride = grad_weight_stride;
     logits.out_vectors = aligned(grad_weight, 16) && grad_weight_stride % 8 == 0;
     hid = wgt = logits;
-    if (!tensor_map(&logits.a, r.packed, plan.rows, D, plan.depth, kHalf) ||
+    if (!tensor_map(&logits.a, r.packed, plan.rows, D, plan.depth, box_rows(R)) ||
         !tensor_map(&logits.b, weight, V, D, weight_stride, kHalf) ||
-        !tensor_map(&hid.a, probs, plan.rows, width, width, kHalf) ||
+        !tensor_map(&hid.a, probs, plan.rows, width, width, box_rows(R)) ||
         !tensor_map(&hid.b, weight, V, D, weight_stride, kBlockK) ||
         !tensor_map(&wgt.a, probs, plan.rows, width, width, kBlockK) ||
         !tensor_map(&wgt.b, r.packed, plan.rows, D, plan.depth, kBlockK) ||

@@ -13,6 +13,12 @@ constexpr int kBlockK = 64;            // depth of a stage: 128 bytes, one swizz
 constexpr int64_t kPieceBytes = (int64_t)1 << 28;  // draft of a piece's probabilities
 constexpr int kMaxSplits = 16;
 
+// rows of the box that A's copies have
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+constexpr int box_rows(int64_t rows) { return rows >= kHalf ? kHalf : (int)((rows + 7) / 8 * 8); }
+
 // What a call keeps in its workspace: offsets in bytes.
 struct CrossEntropyPlan {
     int64_t rows;        // R rounded up to a tile

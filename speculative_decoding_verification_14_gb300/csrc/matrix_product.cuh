@@ -176,13 +176,15 @@ struct MatrixShape {
     }
 };
 
-// Runs the pair's tiles, of a shape that is asked for once the launch before has ended.  b0: row (column for a turned
+// Runs the pair's tiles, of a shape that is asked for once the launch before has ended.  a_rows: the
+// most rows that A can have (its box has 128 of them, or as many as there are, rounded up to eight): where they fit one
+// CTA, what the other would copy is left out, and its rows of the tile mean nothing.  b0: row (column for a turned
 // operand) at which B begins in its map, kb: depth likewise.  finish(row tile, column tile, split, load) is called by the four tile warps of each CTA
 // for each tile; load(c, v) gives columns c .. c + 31 of the thread's row, and has to be called by whole warps;
 // without a single block of depth the tile is all zeros and load gives them.
 template <bool TurnedA, bool TurnedB, typename Shape, typename Finish>
-__device__ __forceinline__ void run_tiles(const CUtensorMap* map_a, const CUtensorMap* map_b, Shape shape_of,
-                                          int64_t b0, int64_t kb, uint32_t* err_word, uint32_t timeout_bit,
+__device__ __forceinline__ void run_tiles(const CUtensorMap* map_a, const CUtensorMap* map_b, int a_rows,
+                                          Shape shape_of, int64_t b0, int64_t kb, uint32_t* err_word, uint32_t timeout_bit,
                                           Finish finish) {
     extern __shared__ unsigned char dynamic[];
     __shared__ MatrixBarriers bars;
@@ -222,6 +224,8 @@ __device__ __forceinline__ void run_tiles(const CUtensorMap* map_a, const CUtens
 
     if (warp == 0) {
         if (lane == 0) {
+            const uint32_t stage_bytes = TurnedA || a_rows > kHalf ? 2 * kStageBytes
+                                                                   : 2 * kOperandBytes + box_rows(a_rows) * 128u;
             int stage = 0;
             uint32_t phase = 0;
             bool go = true;
@@ -239,13 +243,13 @@ __device__ __forceinline__ void run_tiles(const CUtensorMap* map_a, const CUtens
                     // both CTAs' copies arrive on the first one's barrier
                     const uint32_t bar = cluster_addr(&bars.full[stage], 0);
                     if (rank == 0)
-                        barrier_expect(&bars.full[stage], 2 * kStageBytes);
+                        barrier_expect(&bars.full[stage], stage_bytes);
                     const uint32_t at = stage0 + stage * kStageBytes, bt = at + kOperandBytes;
                     const int da = (int)(k * kBlockK), db = (int)(kb + k * kBlockK);
                     if constexpr (TurnedA) {
                         copy_tile(at, map_a, ra, da, bar);
                         copy_tile(at + kOperandBytes / 2, map_a, ra + 64, da, bar);
-                    } else {
+                    } else if (rank == 0 || a_rows > kHalf) {
                         copy_tile(at, map_a, da, ra, bar);
                     }
                     if constexpr (TurnedB) {
