@@ -699,7 +699,8 @@ int spec_cross_entropy_grad(sv_ctx* ctx, const void* hidden, int dtype, int64_t 
     logits.splits = plan.splits;
     logits.out = static_cast<__nv_bfloat16*>(grad_weight);
     logits.out_stride = grad_weight_stride;
-    logits.out_vectors = aligned(grad_weight, 16) && grad_weight_stride % 8 == 0;
+    // the copy engine writes whole 16 bytes: beyond D too, where that ends inside some
+    logits.out_vectors = aligned(grad_weight, 16) && grad_weight_stride % 8 == 0 && D % 8 == 0;
     hid = wgt = logits;
     if (!tensor_map(&logits.a, r.packed, plan.rows, D, plan.depth, box_rows(R)) ||
         !tensor_map(&logits.b, weight, V, D, weight_stride, kHalf) ||

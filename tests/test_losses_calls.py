@@ -138,3 +138,118 @@ def test_the_wrapper_refuses_what_the_library_cannot_see(sv):
         for bad in (dict(temperature=0.0), dict(loss=False, grad=False)):
             with pytest.raises(sv.SpecVerifyError):
                 v.distill(lg, a, x, **bad)
+
+
+def test_cross_entropy_worked_example():
+    import torch
+    from tests.losses_reference import cross_entropy_truth
+    # logits (0, ln 3): p = (1/4, 3/4)
+    h = torch.tensor([[1.0, 2.0]], dtype=torch.float64)
+    W = torch.tensor([[0.0, 0.0], [np.log(3.0), 0.0]], dtype=torch.float64)
+    t = cross_entropy_truth(h, W, torch.tensor([0]), torch.tensor([2.0]))
+    assert abs(t["loss"].item() - np.log(4.0)) < 1e-12 and abs(t["lse"].item() - np.log(4.0)) < 1e-12
+    np.testing.assert_allclose(t["grad_hidden"].numpy(), [[2 * .75 * np.log(3.0), 0.0]], atol=1e-12)
+    np.testing.assert_allclose(t["grad_weight"].numpy(), [[-1.5, -3.0], [1.5, 3.0]], atol=1e-12)
+
+
+def test_cross_entropy_reference_is_autograds():
+    import torch
+    from tests.losses_reference import cross_entropy_truth
+    g = torch.Generator().manual_seed(3)
+    h, W = (torch.randn(n, 6, dtype=torch.float64, generator=g, requires_grad=True) for n in (5, 9))
+    y, w = torch.randint(0, 9, (5,), generator=g), torch.rand(5, dtype=torch.float64, generator=g)
+    loss = torch.nn.functional.cross_entropy(h @ W.T, y, reduction="none")
+    (loss * w).sum().backward()
+    t = cross_entropy_truth(h.detach(), W.detach(), y, w)
+    torch.testing.assert_close(t["loss"], loss.detach())
+    torch.testing.assert_close(t["grad_hidden"], h.grad)
+    torch.testing.assert_close(t["grad_weight"], W.grad)
+
+
+@pytest.mark.parametrize("B,rows,V,D", list(itertools.product([1, 64, 1024, 200000], [1, 8, 33],
+                                                              [1, 257, 32000, 151936], [1, 64, 1000, 4096])))
+def test_cross_entropy_workspaces(sv, B, rows, V, D):
+    """Room for what a call keeps: packed rows, and a piece's probabilities and the gradient's sums, or a tile's
+    statistics; and never that of whole logits."""
+    R, pad = B * rows, -(-B * rows // 256) * 256
+    rc, loss = sv.spec_cross_entropy_workspace_for(152, B, rows, V, D, 0)
+    assert rc == sv.SV_OK
+    packed = 2 * pad * -(-D // 8) * 8
+    tiles = -(-V // 256)
+    assert packed + 8 * pad * tiles <= loss < packed + 8 * pad * tiles + 16 * pad + 4096
+    rc, both = sv.spec_cross_entropy_workspace_for(152, B, rows, V, D, 1)
+    assert rc == sv.SV_OK and both >= loss
+    piece = max(1 << 28, pad * 512)
+    sums = 4 * pad * -(-D // 8) * 8
+    assert both <= max(loss, packed + min(piece, 512 * pad * tiles) + 32 * sums + 32 * pad + 4096)
+    if R >= 76 * 256:  # enough tiles without splits
+        assert both <= max(loss, packed + piece + sums + 32 * pad + 4096)
+
+
+def test_cross_entropy_workspaces_refuse(sv):
+    for bad in ((0, 1, 1, 10, 8, 0), (152, 0, 1, 10, 8, 0), (152, 1, 0, 10, 8, 0), (152, 1, 34, 10, 8, 0), (152, 1, 1, 0, 8, 0),
+                (152, 1, 1, 1 << 31, 8, 0), (152, 1, 1, 10, 0, 0), (152, 1, 1, 10, (1 << 20) + 1, 0), (152, 1, 1, 10, 8, 2),
+                (152, 1 << 24, 2, 10, 8, 0)):
+        assert sv.spec_cross_entropy_workspace_for(*bad)[0] == sv.SV_ERR_INVALID_ARG, bad
+    assert sv.spec_cross_entropy_run(None, 16, 1, 8, 16, 8, 16, None, 1, 1, 10, 8, 16, 16, None, 256, 1 << 30) == \
+        sv.SV_ERR_INVALID_ARG
+    assert sv.spec_cross_entropy_grad(None, 16, 1, 8, 16, 8, 16, None, 16, None, 1, 1, 10, 8, 16, 8, 16, 8, None, 256,
+                                      1 << 30) == sv.SV_ERR_INVALID_ARG
+    with pytest.raises(sv.SpecVerifyError):
+        sv.spec_cross_entropy_workspace(None, 1, 1, 10, 8, 0)
+
+
+@pytest.mark.gpu
+def test_cross_entropy_refusals_launch_nothing(sv):
+    import torch
+    B, rows, V, D = 2, 3, 64, 16
+    h = torch.zeros(B, rows, D, device="cuda", dtype=torch.bfloat16)
+    W = torch.zeros(V, D, device="cuda", dtype=torch.bfloat16)
+    y = torch.zeros(B, rows, device="cuda", dtype=torch.int32)
+    fl = torch.full((2, B, rows), -7.0, device="cuda")
+    ints = torch.full((B, rows), -7, device="cuda", dtype=torch.int32)
+    gh, gw = torch.full_like(h, -7.0), torch.full_like(W, -7.0)
+    with sv.Verifier(4, 4, 100) as v:
+        ws = v.cross_entropy_workspace(B, rows, V, D)
+        ws.fill_(0x5a)
+        head = dict(ctx=v.ctx, hidden_ptr=h.data_ptr(), dtype=1, hidden_stride=D, weight_ptr=W.data_ptr(), weight_stride=D,
+                    labels_ptr=y.data_ptr(), accept_len_ptr=None, B=B, rows_per_seq=rows, V=V, D=D,
+                    status_ptr=ints.data_ptr(), workspace_ptr=ws.data_ptr(), workspace_bytes=ws.numel())
+        shared = [dict(hidden_ptr=None), dict(hidden_ptr=h.data_ptr() + 1), dict(dtype=2), dict(hidden_stride=D - 1),
+                  dict(hidden_stride=1 << 41), dict(weight_ptr=None), dict(weight_ptr=W.data_ptr() + 2),
+                  dict(weight_stride=D - 8), dict(weight_stride=D + 1), dict(weight_stride=(1 << 32) + 8),
+                  dict(labels_ptr=None), dict(labels_ptr=y.data_ptr() + 1), dict(accept_len_ptr=y.data_ptr() + 2),
+                  dict(B=0), dict(B=5), dict(rows_per_seq=0), dict(rows_per_seq=6), dict(V=0), dict(V=101), dict(D=0),
+                  dict(D=(1 << 20) + 1), dict(status_ptr=ints.data_ptr() + 1), dict(workspace_ptr=None),
+                  dict(workspace_ptr=ws.data_ptr() + 16), dict(workspace_bytes=100)]
+        run = dict(head, loss_ptr=fl[0].data_ptr(), lse_ptr=fl[1].data_ptr())
+        for bad in shared + [dict(loss_ptr=None), dict(lse_ptr=None), dict(loss_ptr=fl.data_ptr() + 2),
+                             dict(lse_ptr=fl.data_ptr() + 1)]:
+            assert sv.spec_cross_entropy_run(**{**run, **bad}) == sv.SV_ERR_INVALID_ARG, bad
+        assert sv.spec_cross_entropy_run(**{**run, "dtype": 0}) == sv.SV_ERR_UNSUPPORTED
+        grad = dict(head, lse_ptr=fl[0].data_ptr(), grad_loss_ptr=fl[1].data_ptr(), grad_hidden_ptr=gh.data_ptr(),
+                    grad_hidden_stride=D, grad_weight_ptr=gw.data_ptr(), grad_weight_stride=D)
+        for bad in shared + [dict(lse_ptr=None), dict(lse_ptr=fl.data_ptr() + 2), dict(grad_loss_ptr=fl.data_ptr() + 1),
+                             dict(grad_hidden_ptr=None, grad_weight_ptr=None), dict(grad_hidden_ptr=gh.data_ptr() + 1),
+                             dict(grad_weight_ptr=gw.data_ptr() + 1), dict(grad_hidden_stride=D - 1),
+                             dict(grad_weight_stride=D - 1), dict(grad_weight_stride=1 << 41)]:
+            assert sv.spec_cross_entropy_grad(**{**grad, **bad}) == sv.SV_ERR_INVALID_ARG, bad
+        assert sv.spec_cross_entropy_grad(**{**grad, "dtype": 0}) == sv.SV_ERR_UNSUPPORTED
+        torch.cuda.synchronize()
+        assert all((t == -7).all() for t in (fl, ints, gh, gw)) and (ws == 0x5a).all()
+        assert v.error() == (0, 0)
+        for bad in (lambda: v.cross_entropy(h.cpu(), W, y), lambda: v.cross_entropy(h, W.cpu(), y),
+                    lambda: v.cross_entropy(h, W, y.long()), lambda: v.cross_entropy(h, W[:, :8], y),
+                    lambda: v.cross_entropy(h, W.T, y), lambda: v.cross_entropy(h, W, y[:1]),
+                    lambda: v.cross_entropy(h.transpose(0, 1), W, y), lambda: v.cross_entropy(h.float(), W, y),
+                    lambda: v.cross_entropy(h, W.float(), y), lambda: v.cross_entropy(h[..., ::2], W[:, :8], y),
+                    lambda: v.cross_entropy(h, W, y, workspace=ws.cpu()), lambda: v.cross_entropy(h, W, y, workspace=fl),
+                    lambda: v.cross_entropy(h, W, y, y[0, :2].clone().long()),
+                    lambda: v.cross_entropy_grad(h, W, y, fl[0].double()),
+                    lambda: v.cross_entropy_grad(h, W, y, fl[0], out={"grad_hidden": gh.float()}),
+                    lambda: v.cross_entropy_grad(h, W, y, fl[0], out={"grad_weight": gw[:9]})):
+            with pytest.raises((ValueError, TypeError)):
+                bad()
+        for bad in (dict(hidden_grad=False, weight_grad=False), dict(workspace=ws[:64])):
+            with pytest.raises(sv.SpecVerifyError):
+                v.cross_entropy_grad(h, W, y, fl[0], **bad)
