@@ -326,3 +326,56 @@ def test_two_threads_on_streams_of_their_own():
     for t in ts:
         t.join()
     assert not failed, failed
+
+
+def test_offsets_beyond_32_bits():
+    """600 000 rows of 4096: the last ones against the definition; each row's probabilities are one tile wide."""
+    torch = _torch()
+    v = gh.verifier()
+    B, rows, V, D, tail = 20000, 30, 300, 4096, 3
+    h, W, y, w = make(tail, rows, V, D, 137)
+    big = torch.zeros(B, rows, D, device="cuda", dtype=torch.bfloat16)
+    big[-tail:] = h
+    yb = torch.full((B, rows), -1, device="cuda", dtype=torch.int32)
+    yb[:-tail, ::2] = 5  # packed in front of them
+    yb[-tail:] = y
+    wb = torch.zeros(B, rows, device="cuda")
+    wb[-tail:] = w
+    out, grads = both(v, big, W, yb, w=wb)
+    part = {k: t[-tail:] for k, t in out.items()}
+    check(part, {"grad_hidden": grads["grad_hidden"][-tail:], "grad_weight": grads["grad_weight"]}, h, W, y, w)
+    assert (out["lse"][0, ::2] - np.log(V)).abs().max() < 1e-5 and (grads["grad_hidden"][:-tail] == 0).all()
+    assert v.error() == (0, 0)
+
+
+def test_the_first_call_of_a_process_in_a_capture():
+    """Kernel attributes and limits are asked for while a stream is captured."""
+    import subprocess
+    import sys
+    code = """
+import torch
+import speculative_decoding_verification_14_gb300 as sv
+torch.cuda.set_device(0)
+g = torch.Generator(device="cuda").manual_seed(1)
+h = torch.randn(20, 4, 64, device="cuda", generator=g).bfloat16()
+W = torch.randn(600, 64, device="cuda", generator=g).bfloat16()
+y = torch.randint(0, 600, (20, 4), device="cuda", generator=g, dtype=torch.int32)
+z = torch.randn(400, 4, 600, device="cuda", generator=g)
+a = torch.randn(400, 4, 7, device="cuda", generator=g)
+x = torch.arange(7, device="cuda", dtype=torch.int32).expand(400, 4, 7).contiguous()
+v = sv.Verifier(400, 4, 1000)
+def step():
+    out = v.cross_entropy(h, W, y)
+    return [out["loss"], *v.cross_entropy_grad(h, W, y, out["lse"]).values(), *v.distill(z, a, x).values()]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = step()
+graph.replay()
+want = step()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, want)) and v.error() == (0, 0)
+print("equal")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "equal" in r.stdout, r.stderr

@@ -329,3 +329,23 @@ def test_entries_far_above_the_rest(dtype):
     z[5, 0, :20000] = -float("inf")  # a slice without a logit in its first vectors
     for tail in (False, True):
         check(gh.verifier().distill(z, a, x, tail=tail, grad_loss=w), z, a, x, 1.0, tail, w, dtype=dtype)
+
+
+def test_offsets_beyond_32_bits():
+    """17000 rows of 128256: their last rows, in place."""
+    torch = _torch()
+    v = gh.verifier()
+    B, V = 17000, 128256
+    z, a, x, w = make(2, 1, V, 20, "bf16", 59)
+    big = torch.zeros(B, 1, V, device="cuda", dtype=torch.bfloat16)
+    big[-2:] = z
+    ab, xb = a[:1].expand(B, 1, 20).contiguous(), x[:1].expand(B, 1, 20).contiguous()
+    ab[-2:], xb[-2:] = a, x
+    wb = torch.ones(B, 1, device="cuda")
+    wb[-2:] = w
+    out = {"loss": torch.empty(B, 1, device="cuda"), "grad_logits": big,
+           "status": torch.empty(B, 1, device="cuda", dtype=torch.int32)}
+    v.distill(big, ab, xb, tail=True, grad_loss=wb, out=out)
+    check({k: t[-2:] for k, t in out.items()}, z, a, x, 1.0, True, w, dtype="bf16")
+    check({k: t[:1] for k, t in out.items()}, torch.zeros_like(z[:1]), a[:1], x[:1], 1.0, True, None, dtype="bf16")
+    assert (out["status"] == 0).all() and torch.equal(out["loss"][:-2], out["loss"][:1].expand(B - 2, 1))
