@@ -537,7 +537,8 @@ int spec_distill_plan_for(int num_sms, int max_cluster, int B, int rows_per_seq,
  *            spec_cross_entropy_run; 1: for either call
  * Each d_v is rounded to bfloat16 before the products that sum it, and each
  * gradient once after.  A row's work is not done where it does not count.
- * 1 <= D <= 2^20, R <= 2^24.  No output may lie where an input or another output does.
+ * 1 <= D <= 2^20, R <= 2^20.  No output may lie where an input or another output
+ * does (rows of a gradient that meet those of its input are refused).
  * An erroneous row (a label outside [-1, V): SV_ERR_TOKEN_RANGE; logits with a
  * NaN or +inf or only -inf, in the gradients' call an lse that is not finite:
  * SV_ERR_NONFINITE) gets a NaN loss and lse and a NaN grad_hidden, adds nothing to

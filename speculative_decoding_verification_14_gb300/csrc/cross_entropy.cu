@@ -10,7 +10,18 @@
 // Gradients: piece by piece of the vocabulary, the logits once more, now written as bfloat16 d
 // (a piece's d stays within 256 MB); then d W into float32 sums of the hidden states' gradient, and
 // d^T h, which is that piece's rows of the head's gradient.  d is rounded to bfloat16 (2^-8 of itself at most) since the
-// tensor cores take it so; its errors are independent from entry to entry, and both gradients sum many.
+// tensor cores take it so; its errors are independent from entry to entry, and both gradients sum many (against 64 bits
+// they are off by 2.2e-3 to 3.0e-3 of their norm, 1.7e-3 of which is their own rounding).  A logit's sum is a float in
+// tensor memory, which the tensor cores cut and do not round: at D of 4096 lse is off by 2.0e-6 of itself, at 100 by 1e-7.
+// The launches of a call begin while the ones before them end.
+//
+// What bounds it (replayed): from some 300 rows on the tensor cores.  8192 rows of 128256 x 4096, loss and both gradients,
+// 20.7 to 21.5 ms: its products, 4 of 8.6 TFLOP, one of them the logits' second, take 95 % of the rate that a library
+// product reaches in a burst, and what the clock leaves of that under the power limit; 2048 rows, the loss, 1.22 ms (0.92).
+// 256 rows of 151936 x 2048, the hidden states' gradient, 360 us: three products of 83 us at that rate, each 8 rounds of 76
+// pairs and 10 us of beginning and end.  Few rows read the weight at 5.2 TB/s once it flows: 5 rows of 32000 x 1024, the
+// loss, 21 us (10 for 65 MB): 4 until the rows are packed, 4 until the first tile is there, 12 for the weight, 3 for
+// the last tile's statistics.  40 rows, both gradients, 93 us: four such passes, over the weight or its gradient.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -22,6 +33,7 @@
 
 #include "../../include/spec_verify.h"
 #include "cross_entropy.h"
+#include "distill_plan.h"
 #include "matrix_product.cuh"
 #include "sv_context.h"
 
@@ -547,7 +559,7 @@ int check(const sv_ctx* ctx, const void* hidden, int dtype, int64_t hidden_strid
         return SV_ERR_INVALID_ARG;
     const int64_t most = (int64_t)1 << 40;
     if (B < 1 || B > ctx->max_B || rows_per_seq < 1 || rows_per_seq > ctx->max_K + 1 || V < 1 || V > ctx->max_V ||
-        V > ((int64_t)1 << 31) - 1 || D < 1 || D > ((int64_t)1 << 20) || (int64_t)B * rows_per_seq > (1 << 24) ||
+        V > ((int64_t)1 << 31) - 1 || D < 1 || D > ((int64_t)1 << 20) || (int64_t)B * rows_per_seq > kMaxRowsCe ||
         hidden_stride < D || hidden_stride > most || weight_stride < D || weight_stride > ((int64_t)1 << 32) ||
         (double)B * rows_per_seq * (double)hidden_stride >= 1099511627776.0 ||  // 2^40
         (double)V * (double)weight_stride >= 1099511627776.0)
@@ -665,7 +677,9 @@ int spec_cross_entropy_grad(sv_ctx* ctx, const void* hidden, int dtype, int64_t 
         (grad_hidden && (grad_hidden_stride < D || grad_hidden_stride > most ||
                          (double)R * (double)grad_hidden_stride >= 1099511627776.0)) ||
         (grad_weight && (grad_weight_stride < D || grad_weight_stride > most ||
-                         (double)V * (double)grad_weight_stride >= 1099511627776.0)))
+                         (double)V * (double)grad_weight_stride >= 1099511627776.0)) ||
+        (grad_hidden && rows_meet(hidden, hidden_stride * 2, grad_hidden, grad_hidden_stride * 2, R, D * 2)) ||
+        (grad_weight && rows_meet(weight, weight_stride * 2, grad_weight, grad_weight_stride * 2, V, D * 2)))
         return SV_ERR_INVALID_ARG;
     DeviceGuard guard(ctx->device);
     const int pairs = matrix_pairs(ctx->device);

@@ -12,6 +12,7 @@ constexpr int kHalf = kTile / 2;       // of one CTA's operands
 constexpr int kBlockK = 64;            // depth of a stage: 128 bytes, one swizzle atom
 constexpr int64_t kPieceBytes = (int64_t)1 << 28;  // draft of a piece's probabilities
 constexpr int kMaxSplits = 16;
+constexpr int64_t kMaxRowsCe = (int64_t)1 << 20;  // each block of rows counts those before it
 
 // rows of the box that A's copies have
 #ifdef __CUDACC__

@@ -54,7 +54,7 @@ extern "C" int spec_cross_entropy_workspace_for(int num_sms, int B, int rows_per
     using namespace sv;
     if (!bytes || num_sms < 1 || B < 1 || rows_per_seq < 1 || rows_per_seq > kMaxRows || V < 1 ||
         V > ((int64_t)1 << 31) - 1 || D < 1 || D > ((int64_t)1 << 20) || (grad != 0 && grad != 1) ||
-        (int64_t)B * rows_per_seq > (1 << 24))
+        (int64_t)B * rows_per_seq > kMaxRowsCe)
         return SV_ERR_INVALID_ARG;
     const int64_t R = (int64_t)B * rows_per_seq;
     *bytes = cross_entropy_plan(num_sms, R, V, D, false).total;

@@ -7,6 +7,8 @@
 // turn.  One thread of each CTA issues the copies (cp.async.bulk.tensor, 128-byte swizzle) that fill its
 // ring of stages, one thread of the first CTA the products, and four warps of each CTA take the finished
 // tile out of tensor memory, where two tiles have room: the next one's products run meanwhile.
+// A CTA's operands of a stage come to 32 KB for 128 x 256 x 64 products, 64 bytes a cycle at the tensor cores' full rate;
+// one CTA by itself with 128 x 256 would need 96.  Six stages are in flight.
 // An operand lies in memory with its depth contiguous, or with its rows contiguous ("turned": the
 // probabilities as [v, r] and the weight as [d, v] are read from [r, v] and [v, d] as they lie).
 #pragma once

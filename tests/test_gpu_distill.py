@@ -331,6 +331,15 @@ def test_entries_far_above_the_rest(dtype):
         check(gh.verifier().distill(z, a, x, tail=tail, grad_loss=w), z, a, x, 1.0, tail, w, dtype=dtype)
 
 
+@pytest.mark.parametrize("T", [2.0 ** -100, 1e-3, 0.05, 50.0, 1e6, 2.0 ** 100])
+def test_temperatures(T):
+    for dtype in ("f32", "bf16"):
+        z, a, x, w = make(4, 2, 5001, 16, dtype, 61, T=max(T, 0.3))
+        for tail in (False, True):
+            out = gh.verifier().distill(z, a, x, temperature=T, tail=tail, grad_loss=w)
+            check(out, z, a, x, T, tail, w, dtype=dtype)
+
+
 def test_offsets_beyond_32_bits():
     """17000 rows of 128256: their last rows, in place."""
     torch = _torch()
