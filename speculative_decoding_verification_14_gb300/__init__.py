@@ -519,15 +519,15 @@ def _row_stride(t, name: str, rows: int, inner: int) -> int:
     """Elements from one row of ``t`` to the next, its rows taken in order.
     ``t`` is [B, ...] or [B, rows, ...] with ``inner`` (0: none) contiguous
     entries per row; rows must be evenly spaced."""
-    B = t.shape[0]
-    three = t.dim() == (3 if inner else 2)
-    if inner > 1 and t.stride(-1) != 1:
+    B, strides = t.shape[0], t.stride()
+    three = len(strides) == (3 if inner else 2)
+    if inner > 1 and strides[-1] != 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
     if rows == 1 or not three:
-        return t.stride(0) if B > 1 else max(inner, 1)
-    if B > 1 and t.stride(0) != rows * t.stride(1):
+        return strides[0] if B > 1 else max(inner, 1)
+    if B > 1 and strides[0] != rows * strides[1]:
         raise ValueError(f"{name}: rows must be evenly spaced in memory")
-    return t.stride(1)
+    return strides[1]
 
 
 class Verifier:
@@ -791,16 +791,15 @@ class Verifier:
 
     def _rows_of(self, logits):
         """(B, rows per sequence, V, dtype code, row stride) of logits [B, V] or [B, rows, V]."""
-        code = _dtype_code(logits)
-        if logits.dim() not in (2, 3):
+        code, shape = _dtype_code(logits), logits.shape
+        if len(shape) not in (2, 3):
             raise ValueError("logits must be [B, V] or [B, rows, V]")
         self._on_device(logits, "logits")
-        B, V = logits.shape[0], logits.shape[-1]
-        rows = logits.shape[1] if logits.dim() == 3 else 1
-        return B, rows, V, code, _row_stride(logits, "logits", rows, V)
+        rows = shape[1] if len(shape) == 3 else 1
+        return shape[0], rows, shape[-1], code, _row_stride(logits, "logits", rows, shape[-1])
 
     def _on_device(self, t, name):
-        if not t.is_cuda or t.device.index != self.device:
+        if t.get_device() != self.device:
             raise ValueError(f"{name} must be a tensor on CUDA device {self.device}")
 
     def _expect(self, t, name, shape, dtype):
@@ -808,13 +807,24 @@ class Verifier:
         if t.dtype != dtype or t.shape != shape:
             raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} of "
                              f"shape {tuple(t.shape)}")
-        self._on_device(t, name)
+        if t.get_device() != self.device:
+            self._on_device(t, name)
         return t
 
     def _dense(self, t, name, shape, dtype):
-        if not self._expect(t, name, shape, dtype).is_contiguous():
+        if t.dtype != dtype or t.shape != shape or t.get_device() != self.device:
+            self._expect(t, name, shape, dtype)
+        if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
         return t.data_ptr()
+
+    def _stream(self, stream):
+        """The stream given, or torch's current one on this device."""
+        if stream is not None:
+            return stream
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # a tenth of the time of the next line
+        return raw(self.device) if raw else torch.cuda.current_stream(self.device).cuda_stream
 
     def _settings(self, temperature, top_k, top_p, min_p, B) -> sv_sampling:
         import torch
@@ -969,6 +979,7 @@ class Verifier:
         if top_tokens.dim() != logits.dim():
             raise ValueError("top_tokens must be logits' shape with n in place of V")
         n = top_tokens.shape[-1]
+        lists = (*shape, n)
         if out is None:
             dev = logits.device
             out = {}
@@ -978,20 +989,19 @@ class Verifier:
                 out["grad_logits"] = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
             if status:
                 out["status"] = torch.empty(shape, dtype=torch.int32, device=dev)
-        ls, g, st = (out.get(k) for k in ("loss", "grad_logits", "status"))
-        rc = spec_distill_run(
-            self.ctx, logits.data_ptr(), code, stride,
-            self._dense(top_logprobs, "top_logprobs", (*shape, n), torch.float32),
-            self._dense(top_tokens, "top_tokens", (*shape, n), torch.int32), n,
-            None if accept_len is None else self._dense(accept_len, "accept_len", (B,), torch.int32),
-            B, rows, V, temperature, bool(tail),
-            None if grad_loss is None else self._dense(grad_loss, "grad_loss", shape, torch.float32),
-            None if ls is None else self._dense(ls, "loss", shape, torch.float32),
+        ls, g, st = out.get("loss"), out.get("grad_logits"), out.get("status")
+        dense, f32, i32 = self._dense, torch.float32, torch.int32
+        rc = library().spec_distill_run(
+            self.ctx, logits.data_ptr(), code, stride, dense(top_logprobs, "top_logprobs", lists, f32),
+            dense(top_tokens, "top_tokens", lists, i32), n,
+            None if accept_len is None else dense(accept_len, "accept_len", (B,), i32), B, rows, V,
+            temperature, bool(tail),
+            None if grad_loss is None else dense(grad_loss, "grad_loss", shape, f32),
+            None if ls is None else dense(ls, "loss", shape, f32),
             None if g is None else
             self._expect(g, "grad_logits", logits.shape, logits.dtype).data_ptr(),
             0 if g is None else _row_stride(g, "grad_logits", rows, V),
-            None if st is None else self._dense(st, "status", shape, torch.int32),
-            stream if stream is not None else torch.cuda.current_stream(self.device).cuda_stream)
+            None if st is None else dense(st, "status", shape, i32), self._stream(stream))
         if rc != SV_OK:
             raise SpecVerifyError(rc, "spec_distill_run")
         return out
@@ -1050,8 +1060,7 @@ class Verifier:
             self.ctx, *head, B, rows, V, D, self._dense(out["loss"], "loss", shape, torch.float32),
             self._dense(out["lse"], "lse", shape, torch.float32),
             None if st is None else self._dense(st, "status", shape, torch.int32), ws.data_ptr(),
-            ws.numel(),
-            stream if stream is not None else torch.cuda.current_stream(self.device).cuda_stream)
+            ws.numel(), self._stream(stream))
         if rc != SV_OK:
             raise SpecVerifyError(rc, "spec_cross_entropy_run")
         return out
@@ -1086,8 +1095,7 @@ class Verifier:
             self._expect(gw, "grad_weight", weight.shape, torch.bfloat16).data_ptr(),
             0 if gw is None else _row_stride(gw, "grad_weight", 1, D),
             None if st is None else self._dense(st, "status", shape, torch.int32), ws.data_ptr(),
-            ws.numel(),
-            stream if stream is not None else torch.cuda.current_stream(self.device).cuda_stream)
+            ws.numel(), self._stream(stream))
         if rc != SV_OK:
             raise SpecVerifyError(rc, "spec_cross_entropy_grad")
         return out
