@@ -502,7 +502,10 @@ int spec_distill_run(sv_ctx* ctx, const void* draft_logits, int logits_dtype,
                      float temperature, int tail, const float* grad_loss, float* loss,
                      void* grad_logits, int64_t grad_stride, int32_t* status, void* stream);
 
-/* Its launch plan, and its planner as a pure host function. */
+/* Its launch plan, and its planner as a pure host function: a cluster per row, its
+ * slices of the least number of CTAs that leaves an SM room for three (more where
+ * rows are few).  grid is the most: a call with more rows than run at once launches
+ * as many clusters as do, which take the rows in turn. */
 int spec_distill_get_plan(sv_ctx* ctx, int B, int rows_per_seq, int64_t V, int logits_dtype,
                           sv_plan* out);
 int spec_distill_plan_for(int num_sms, int max_cluster, int B, int rows_per_seq, int64_t V,
