@@ -9,6 +9,7 @@ raise.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -537,7 +538,9 @@ class Verifier:
     [B, K, V] float32, tokens [B, K] int32, uniforms [B, K+1] float32, and a
     temperature; it returns a dict of CUDA tensors accept_len [B], out_tokens
     [B, K+1], accept_mask [B, K] (uint8), and optionally row_stats [B, K+1, 2],
-    p_draft [B, K], status [B].  The launch goes on torch's current stream."""
+    p_draft [B, K], status [B].  The launch goes on torch's current stream, or on
+    ``stream``, a cudaStream_t as a number: what the call allocates then belongs to
+    that stream, as it would inside ``torch.cuda.stream`` of it."""
 
     def __init__(self, max_B: int, max_K: int, max_V: int, device: Optional[int] = None):
         import torch
@@ -617,16 +620,17 @@ class Verifier:
         K = K1 - 1
         dev = logits.device
         if out is None:
-            out = {
-                "accept_len": torch.empty(B, dtype=torch.int32, device=dev),
-                "out_tokens": torch.empty(B, K + 1, dtype=torch.int32, device=dev),
-                "accept_mask": torch.empty(B, max(K, 1), dtype=torch.uint8, device=dev)[:, :K],
-            }
-            if stats:
-                out["row_stats"] = torch.empty(B, K + 1, 2, dtype=torch.float32, device=dev)
-                out["p_draft"] = torch.empty(B, max(K, 1), dtype=torch.float32, device=dev)[:, :K]
-            if status:
-                out["status"] = torch.empty(B, dtype=torch.int32, device=dev)
+            with self._allocating(stream):
+                out = {
+                    "accept_len": torch.empty(B, dtype=torch.int32, device=dev),
+                    "out_tokens": torch.empty(B, K + 1, dtype=torch.int32, device=dev),
+                    "accept_mask": torch.empty(B, max(K, 1), dtype=torch.uint8, device=dev)[:, :K],
+                }
+                if stats:
+                    out["row_stats"] = torch.empty(B, K + 1, 2, dtype=torch.float32, device=dev)
+                    out["p_draft"] = torch.empty(B, max(K, 1), dtype=torch.float32, device=dev)[:, :K]
+                if status:
+                    out["status"] = torch.empty(B, dtype=torch.int32, device=dev)
         s = stream if stream is not None else torch.cuda.current_stream(dev).cuda_stream
 
         def ptr(name):
@@ -652,15 +656,16 @@ class Verifier:
         K = K1 - 1
         dev = logits.device
         if out is None:
-            out = {
-                "accept_len": torch.empty(B, dtype=torch.int32, device=dev),
-                "out_tokens": torch.empty(B, K + 1, dtype=torch.int32, device=dev),
-                "accept_mask": torch.empty(B, max(K, 1), dtype=torch.uint8, device=dev)[:, :K],
-            }
-            if argmax:
-                out["row_argmax"] = torch.empty(B, K + 1, dtype=torch.int32, device=dev)
-            if status:
-                out["status"] = torch.empty(B, dtype=torch.int32, device=dev)
+            with self._allocating(stream):
+                out = {
+                    "accept_len": torch.empty(B, dtype=torch.int32, device=dev),
+                    "out_tokens": torch.empty(B, K + 1, dtype=torch.int32, device=dev),
+                    "accept_mask": torch.empty(B, max(K, 1), dtype=torch.uint8, device=dev)[:, :K],
+                }
+                if argmax:
+                    out["row_argmax"] = torch.empty(B, K + 1, dtype=torch.int32, device=dev)
+                if status:
+                    out["status"] = torch.empty(B, dtype=torch.int32, device=dev)
         s = stream if stream is not None else torch.cuda.current_stream(dev).cuda_stream
 
         def ptr(name):
@@ -688,14 +693,15 @@ class Verifier:
         nd = R - B
         dev = logits.device
         if out is None:
-            out = {"accept_len": torch.empty(B, dtype=torch.int32, device=dev),
-                   "out_tokens": torch.empty(R, dtype=torch.int32, device=dev),
-                   "accept_mask": torch.empty(max(nd, 1), dtype=torch.uint8, device=dev)[:nd]}
-            if stats:
-                out["row_stats"] = torch.empty(R, 2, dtype=torch.float32, device=dev)
-                out["p_draft"] = torch.empty(max(nd, 1), dtype=torch.float32, device=dev)[:nd]
-            if status:
-                out["status"] = torch.empty(B, dtype=torch.int32, device=dev)
+            with self._allocating(stream):
+                out = {"accept_len": torch.empty(B, dtype=torch.int32, device=dev),
+                       "out_tokens": torch.empty(R, dtype=torch.int32, device=dev),
+                       "accept_mask": torch.empty(max(nd, 1), dtype=torch.uint8, device=dev)[:nd]}
+                if stats:
+                    out["row_stats"] = torch.empty(R, 2, dtype=torch.float32, device=dev)
+                    out["p_draft"] = torch.empty(max(nd, 1), dtype=torch.float32, device=dev)[:nd]
+                if status:
+                    out["status"] = torch.empty(B, dtype=torch.int32, device=dev)
         s = stream if stream is not None else torch.cuda.current_stream(dev).cuda_stream
 
         def ptr(name):
@@ -722,16 +728,17 @@ class Verifier:
         K = K1 - 1
         dev = logits.device
         if out is None:
-            out = {
-                "accept_len": torch.empty(B, dtype=torch.int32, device=dev),
-                "out_tokens": torch.empty(B, K + 1, dtype=torch.int32, device=dev),
-                "accept_mask": torch.empty(B, max(K, 1), dtype=torch.uint8, device=dev)[:, :K],
-            }
-            if stats:
-                out["row_stats"] = torch.empty(B, K + 1, 2, dtype=torch.float32, device=dev)
-                out["p_draft"] = torch.empty(B, max(K, 1), dtype=torch.float32, device=dev)[:, :K]
-            if status:
-                out["status"] = torch.empty(B, dtype=torch.int32, device=dev)
+            with self._allocating(stream):
+                out = {
+                    "accept_len": torch.empty(B, dtype=torch.int32, device=dev),
+                    "out_tokens": torch.empty(B, K + 1, dtype=torch.int32, device=dev),
+                    "accept_mask": torch.empty(B, max(K, 1), dtype=torch.uint8, device=dev)[:, :K],
+                }
+                if stats:
+                    out["row_stats"] = torch.empty(B, K + 1, 2, dtype=torch.float32, device=dev)
+                    out["p_draft"] = torch.empty(B, max(K, 1), dtype=torch.float32, device=dev)[:, :K]
+                if status:
+                    out["status"] = torch.empty(B, dtype=torch.int32, device=dev)
         s = stream if stream is not None else torch.cuda.current_stream(dev).cuda_stream
 
         def ptr(name):
@@ -762,16 +769,17 @@ class Verifier:
             raise ValueError("dlogits must be [B, K, V] in the target's dtype")
         dev = logits.device
         if out is None:
-            out = {
-                "accept_len": torch.empty(B, dtype=torch.int32, device=dev),
-                "out_tokens": torch.empty(B, K + 1, dtype=torch.int32, device=dev),
-                "accept_mask": torch.empty(B, max(K, 1), dtype=torch.uint8, device=dev)[:, :K],
-            }
-            if stats:
-                out["row_stats"] = torch.empty(B, K + 1, 2, dtype=torch.float32, device=dev)
-                out["p_draft"] = torch.empty(B, max(K, 1), dtype=torch.float32, device=dev)[:, :K]
-            if status:
-                out["status"] = torch.empty(B, dtype=torch.int32, device=dev)
+            with self._allocating(stream):
+                out = {
+                    "accept_len": torch.empty(B, dtype=torch.int32, device=dev),
+                    "out_tokens": torch.empty(B, K + 1, dtype=torch.int32, device=dev),
+                    "accept_mask": torch.empty(B, max(K, 1), dtype=torch.uint8, device=dev)[:, :K],
+                }
+                if stats:
+                    out["row_stats"] = torch.empty(B, K + 1, 2, dtype=torch.float32, device=dev)
+                    out["p_draft"] = torch.empty(B, max(K, 1), dtype=torch.float32, device=dev)[:, :K]
+                if status:
+                    out["status"] = torch.empty(B, dtype=torch.int32, device=dev)
         s = stream if stream is not None else torch.cuda.current_stream(dev).cuda_stream
 
         def ptr(name):
@@ -817,6 +825,16 @@ class Verifier:
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
         return t.data_ptr()
+
+    def _allocating(self, stream):
+        """Under it, tensors come from the memory that torch keeps for the stream given: what was freed
+        there was last used in that stream's order.  From another stream's memory a call could be handed
+        what that stream's kernels still work on."""
+        if stream is None:
+            return contextlib.nullcontext()
+        import torch
+        return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=self.device) if stream
+                                 else torch.cuda.default_stream(self.device))
 
     def _stream(self, stream):
         """The stream given, or torch's current one on this device."""
@@ -868,14 +886,15 @@ class Verifier:
         settings = self._settings(temperature, top_k, top_p, min_p, B)
         self._expect(uniforms, "uniforms", shape, torch.float32)
         if out is None:
-            dev = logits.device
-            out = {"tokens": torch.empty(shape, dtype=torch.int32, device=dev),
-                   "p_token": torch.empty(shape, dtype=torch.float32, device=dev),
-                   "kept": torch.empty(shape, dtype=torch.int32, device=dev)}
-            if probs:
-                out["probs"] = torch.empty(logits.shape, dtype=torch.float32, device=dev)
-            if status:
-                out["status"] = torch.empty(shape, dtype=torch.int32, device=dev)
+            with self._allocating(stream):
+                dev = logits.device
+                out = {"tokens": torch.empty(shape, dtype=torch.int32, device=dev),
+                       "p_token": torch.empty(shape, dtype=torch.float32, device=dev),
+                       "kept": torch.empty(shape, dtype=torch.int32, device=dev)}
+                if probs:
+                    out["probs"] = torch.empty(logits.shape, dtype=torch.float32, device=dev)
+                if status:
+                    out["status"] = torch.empty(shape, dtype=torch.int32, device=dev)
         tokens = self._expect(out["tokens"], "tokens", shape, torch.int32)
         q, p_token, kept, st = (out.get(k) for k in ("probs", "p_token", "kept", "status"))
         rc = spec_sample_run(
@@ -906,12 +925,13 @@ class Verifier:
         shape = logits.shape[:-1]
         settings = self._settings(temperature, top_k, top_p, min_p, B)
         if out is None:
-            dev = logits.device
-            out = {"logits": torch.empty(logits.shape, dtype=logits.dtype, device=dev),
-                   "kept": torch.empty(shape, dtype=torch.int32, device=dev),
-                   "mass": torch.empty(shape, dtype=torch.float32, device=dev)}
-            if status:
-                out["status"] = torch.empty(shape, dtype=torch.int32, device=dev)
+            with self._allocating(stream):
+                dev = logits.device
+                out = {"logits": torch.empty(logits.shape, dtype=logits.dtype, device=dev),
+                       "kept": torch.empty(shape, dtype=torch.int32, device=dev),
+                       "mass": torch.empty(shape, dtype=torch.float32, device=dev)}
+                if status:
+                    out["status"] = torch.empty(shape, dtype=torch.int32, device=dev)
         o = self._expect(out["logits"], "out logits", logits.shape, logits.dtype)
         kept, mass, st = (out.get(k) for k in ("kept", "mass", "status"))
         rc = spec_filter_run(
@@ -935,14 +955,15 @@ class Verifier:
         B, rows, V, code, stride = self._rows_of(logits)
         shape = logits.shape[:-1]
         if out is None:
-            dev = logits.device
-            out = {"logprob": torch.empty(shape, dtype=torch.float32, device=dev),
-                   "rank": torch.empty(shape, dtype=torch.int32, device=dev)}
-            if top_n > 0:
-                out["top_logprobs"] = torch.empty((*shape, top_n), dtype=torch.float32, device=dev)
-                out["top_tokens"] = torch.empty((*shape, top_n), dtype=torch.int32, device=dev)
-            if status:
-                out["status"] = torch.empty(shape, dtype=torch.int32, device=dev)
+            with self._allocating(stream):
+                dev = logits.device
+                out = {"logprob": torch.empty(shape, dtype=torch.float32, device=dev),
+                       "rank": torch.empty(shape, dtype=torch.int32, device=dev)}
+                if top_n > 0:
+                    out["top_logprobs"] = torch.empty((*shape, top_n), dtype=torch.float32, device=dev)
+                    out["top_tokens"] = torch.empty((*shape, top_n), dtype=torch.int32, device=dev)
+                if status:
+                    out["status"] = torch.empty(shape, dtype=torch.int32, device=dev)
         rank, st = out.get("rank"), out.get("status")
         top = top_n > 0
         rc = spec_logprobs_run(
@@ -981,14 +1002,15 @@ class Verifier:
         n = top_tokens.shape[-1]
         lists = (*shape, n)
         if out is None:
-            dev = logits.device
-            out = {}
-            if loss:
-                out["loss"] = torch.empty(shape, dtype=torch.float32, device=dev)
-            if grad:
-                out["grad_logits"] = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
-            if status:
-                out["status"] = torch.empty(shape, dtype=torch.int32, device=dev)
+            with self._allocating(stream):
+                dev = logits.device
+                out = {}
+                if loss:
+                    out["loss"] = torch.empty(shape, dtype=torch.float32, device=dev)
+                if grad:
+                    out["grad_logits"] = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+                if status:
+                    out["status"] = torch.empty(shape, dtype=torch.int32, device=dev)
         ls, g, st = out.get("loss"), out.get("grad_logits"), out.get("status")
         dense, f32, i32 = self._dense, torch.float32, torch.int32
         rc = library().spec_distill_run(
@@ -1026,9 +1048,8 @@ class Verifier:
         B, D, V = hidden.shape[0], hidden.shape[-1], weight.shape[0]
         rows = hidden.shape[1] if hidden.dim() == 3 else 1
         if workspace is None:
-            workspace = self.cross_entropy_workspace(B, rows, V, D, grad)
-            if stream is not None:  # torch may hand it on once that stream is through with it
-                workspace.record_stream(torch.cuda.ExternalStream(stream, device=workspace.device))
+            with self._allocating(stream):
+                workspace = self.cross_entropy_workspace(B, rows, V, D, grad)
         elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
             raise ValueError("the workspace must be a contiguous uint8 tensor")
         self._on_device(workspace, "workspace")
@@ -1050,11 +1071,12 @@ class Verifier:
         head, (B, rows, V, D), shape, ws = self._head_of(hidden, weight, labels, accept_len,
                                                          workspace, False, stream)
         if out is None:
-            dev = hidden.device
-            out = {"loss": torch.empty(shape, dtype=torch.float32, device=dev),
-                   "lse": torch.empty(shape, dtype=torch.float32, device=dev)}
-            if status:
-                out["status"] = torch.empty(shape, dtype=torch.int32, device=dev)
+            with self._allocating(stream):
+                dev = hidden.device
+                out = {"loss": torch.empty(shape, dtype=torch.float32, device=dev),
+                       "lse": torch.empty(shape, dtype=torch.float32, device=dev)}
+                if status:
+                    out["status"] = torch.empty(shape, dtype=torch.int32, device=dev)
         st = out.get("status")
         rc = spec_cross_entropy_run(
             self.ctx, *head, B, rows, V, D, self._dense(out["loss"], "loss", shape, torch.float32),
@@ -1075,14 +1097,15 @@ class Verifier:
         head, (B, rows, V, D), shape, ws = self._head_of(hidden, weight, labels, accept_len,
                                                          workspace, True, stream)
         if out is None:
-            dev = hidden.device
-            out = {}
-            if hidden_grad:
-                out["grad_hidden"] = torch.empty(hidden.shape, dtype=hidden.dtype, device=dev)
-            if weight_grad:
-                out["grad_weight"] = torch.empty(weight.shape, dtype=weight.dtype, device=dev)
-            if status:
-                out["status"] = torch.empty(shape, dtype=torch.int32, device=dev)
+            with self._allocating(stream):
+                dev = hidden.device
+                out = {}
+                if hidden_grad:
+                    out["grad_hidden"] = torch.empty(hidden.shape, dtype=hidden.dtype, device=dev)
+                if weight_grad:
+                    out["grad_weight"] = torch.empty(weight.shape, dtype=weight.dtype, device=dev)
+                if status:
+                    out["status"] = torch.empty(shape, dtype=torch.int32, device=dev)
         gh, gw, st = (out.get(k) for k in ("grad_hidden", "grad_weight", "status"))
         rc = spec_cross_entropy_grad(
             self.ctx, *head, self._dense(lse, "lse", shape, torch.float32),
