@@ -528,7 +528,8 @@ int spec_distill_plan_for(int num_sms, int max_cluster, int B, int rows_per_seq,
  *   labels, accept_len  [B, rows] int32 and [B] or NULL (every row): a verify's
  *            out_tokens and accept_len; rows from accept_len on and rows of label -1
  *            do not count, whatever their hidden states hold
- *   loss, lse  out float [B, rows]; 0 for rows that do not count
+ *   loss, lse  out float [B, rows]; 0 for rows that do not count.  A loss near 0 keeps
+ *            its digits
  *   status   optional out int32 [B, rows]
  *   grad_loss  [B, rows] float or NULL (1)
  *   grad_hidden, grad_weight  optional out (not both NULL), R and V rows of D at
@@ -538,13 +539,18 @@ int spec_distill_plan_for(int num_sms, int max_cluster, int B, int rows_per_seq,
  *            aligned, written as the call likes: calls that can overlap on the GPU need
  *            one each, and so do graphs that can.  grad 0: enough for
  *            spec_cross_entropy_run; 1: for either call
+ * spec_cross_entropy_grad_of_loss is given the losses that spec_cross_entropy_run
+ * wrote as well (NULL: as spec_cross_entropy_grad), and has the label's d_y from them,
+ * g (exp(-loss) - 1).  From lse alone it is the difference exp(z_y - lse) - 1, off by
+ * what half a unit in lse's last place is: 5e-7 g at an lse of 8 to 16, 2e-6 at 32 to
+ * 64, which is much of d_y where the row's loss is of that size.
  * Each d_v is rounded to bfloat16 before the products that sum it, and each
  * gradient once after.  A row's work is not done where it does not count.
  * 1 <= D <= 2^20, R <= 2^20.  No output may lie where an input or another output
  * does (rows of a gradient that meet those of its input are refused).
  * An erroneous row (a label outside [-1, V): SV_ERR_TOKEN_RANGE; logits with a
- * NaN or +inf or only -inf, in the gradients' call an lse that is not finite:
- * SV_ERR_NONFINITE) gets a NaN loss and lse and a NaN grad_hidden, adds nothing to
+ * NaN or +inf or only -inf, in the gradients' call an lse that is not finite or a
+ * loss that is NaN: SV_ERR_NONFINITE) gets a NaN loss and lse and a NaN grad_hidden, adds nothing to
  * grad_weight, and sets the context's error word; a wait inside the kernels that
  * runs out sets SV_ERR_TIMEOUT there.  Repeated calls give the same bits.
  * Asynchronous, no allocation; a few launches on `stream` (three per piece of the
@@ -564,6 +570,15 @@ int spec_cross_entropy_grad(sv_ctx* ctx, const void* hidden, int dtype, int64_t 
                             int64_t grad_hidden_stride, void* grad_weight,
                             int64_t grad_weight_stride, int32_t* status, void* workspace,
                             size_t workspace_bytes, void* stream);
+
+int spec_cross_entropy_grad_of_loss(sv_ctx* ctx, const void* hidden, int dtype, int64_t hidden_stride,
+                                    const void* weight, int64_t weight_stride,
+                                    const int32_t* labels, const int32_t* accept_len,
+                                    const float* lse, const float* loss, const float* grad_loss,
+                                    int B, int rows_per_seq, int64_t V, int64_t D,
+                                    void* grad_hidden, int64_t grad_hidden_stride,
+                                    void* grad_weight, int64_t grad_weight_stride, int32_t* status,
+                                    void* workspace, size_t workspace_bytes, void* stream);
 
 /* Bytes of workspace a call needs on the context's device, and the same as a pure host
  * function of the device's SMs. */

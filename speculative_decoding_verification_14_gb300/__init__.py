@@ -162,6 +162,12 @@ def library() -> ctypes.CDLL:
                                                        ctypes.c_int, ctypes.c_int64,
                                                        ctypes.c_int64, P, ctypes.c_int64, P,
                                                        ctypes.c_int64, P, P, ctypes.c_size_t, P]),
+            "spec_cross_entropy_grad_of_loss": (ctypes.c_int, [P, P, ctypes.c_int, ctypes.c_int64, P,
+                                                               ctypes.c_int64, P, P, P, P, P,
+                                                               ctypes.c_int, ctypes.c_int,
+                                                               ctypes.c_int64, ctypes.c_int64, P,
+                                                               ctypes.c_int64, P, ctypes.c_int64,
+                                                               P, P, ctypes.c_size_t, P]),
             "spec_cross_entropy_workspace": (ctypes.c_int, [P, ctypes.c_int, ctypes.c_int,
                                                             ctypes.c_int64, ctypes.c_int64,
                                                             ctypes.c_int,
@@ -440,6 +446,17 @@ def spec_cross_entropy_grad(ctx, hidden_ptr, dtype, hidden_stride, weight_ptr, w
                                              grad_hidden_ptr, grad_hidden_stride, grad_weight_ptr,
                                              grad_weight_stride, status_ptr, workspace_ptr,
                                              workspace_bytes, stream)
+
+
+def spec_cross_entropy_grad_of_loss(ctx, hidden_ptr, dtype, hidden_stride, weight_ptr, weight_stride,
+                                    labels_ptr, accept_len_ptr, lse_ptr, loss_ptr, grad_loss_ptr, B,
+                                    rows_per_seq, V, D, grad_hidden_ptr=None, grad_hidden_stride=0,
+                                    grad_weight_ptr=None, grad_weight_stride=0, status_ptr=None,
+                                    workspace_ptr=None, workspace_bytes=0, stream=None) -> int:
+    return library().spec_cross_entropy_grad_of_loss(
+        ctx, hidden_ptr, dtype, hidden_stride, weight_ptr, weight_stride, labels_ptr, accept_len_ptr,
+        lse_ptr, loss_ptr, grad_loss_ptr, B, rows_per_seq, V, D, grad_hidden_ptr, grad_hidden_stride,
+        grad_weight_ptr, grad_weight_stride, status_ptr, workspace_ptr, workspace_bytes, stream)
 
 
 def spec_cross_entropy_workspace(ctx, B, rows_per_seq, V, D, grad) -> int:
@@ -1089,10 +1106,13 @@ class Verifier:
 
     def cross_entropy_grad(self, hidden, weight, labels, lse, accept_len=None, grad_loss=None,
                            hidden_grad: bool = True, weight_grad: bool = True, workspace=None,
-                           out: Optional[dict] = None, status: bool = False, stream=None) -> dict:
+                           out: Optional[dict] = None, status: bool = False, stream=None,
+                           loss=None) -> dict:
         """The gradients of the sum of grad_loss (float32 [B, rows]; None: 1) times ``cross_entropy``'s
         losses, given its lse: grad_hidden and grad_weight in bfloat16, each only if it is asked for
-        (a head that is not trained costs neither its product nor its bytes)."""
+        (a head that is not trained costs neither its product nor its bytes).  loss: what ``cross_entropy``
+        returned as such, for rows that the head gets right but for 1e-4 of the mass and less: an lse alone
+        holds the label's share to some 1e-6 of the whole."""
         import torch
         head, (B, rows, V, D), shape, ws = self._head_of(hidden, weight, labels, accept_len,
                                                          workspace, True, stream)
@@ -1107,8 +1127,9 @@ class Verifier:
                 if status:
                     out["status"] = torch.empty(shape, dtype=torch.int32, device=dev)
         gh, gw, st = (out.get(k) for k in ("grad_hidden", "grad_weight", "status"))
-        rc = spec_cross_entropy_grad(
+        rc = spec_cross_entropy_grad_of_loss(
             self.ctx, *head, self._dense(lse, "lse", shape, torch.float32),
+            None if loss is None else self._dense(loss, "loss", shape, torch.float32),
             None if grad_loss is None else self._dense(grad_loss, "grad_loss", shape, torch.float32),
             B, rows, V, D,
             None if gh is None else
@@ -1120,7 +1141,7 @@ class Verifier:
             None if st is None else self._dense(st, "status", shape, torch.int32), ws.data_ptr(),
             ws.numel(), self._stream(stream))
         if rc != SV_OK:
-            raise SpecVerifyError(rc, "spec_cross_entropy_grad")
+            raise SpecVerifyError(rc, "spec_cross_entropy_grad_of_loss")
         return out
 
     def plan_distill(self, B, rows_per_seq, V, dtype=SV_BF16) -> dict:

@@ -59,6 +59,7 @@ struct Rows {
     const int32_t* labels;
     const int32_t* accept_len;  // or NULL
     const float* lse;           // backward: rows whose lse is not finite have no gradient
+    const float* loss_in;       // or NULL
     const float* grad_loss;     // or NULL
     int64_t R, V, D, depth;
     int rows_per_seq;
@@ -67,6 +68,7 @@ struct Rows {
     int32_t* count;
     int32_t* label;
     float* packed_lse;
+    float* packed_loss;
     float* scale;
     __nv_bfloat16* packed;
     // of rows that do not count
@@ -91,6 +93,8 @@ __device__ __forceinline__ int row_kind(const Rows& a, int64_t row) {
     if (y < 0 || y >= a.V)
         return SV_ERR_TOKEN_RANGE;
     if (a.lse && !(fabsf(a.lse[row]) <= 3.4028235e38f))
+        return SV_ERR_NONFINITE;
+    if (a.loss_in && !(a.loss_in[row] == a.loss_in[row]))
         return SV_ERR_NONFINITE;
     return 0;
 }
@@ -150,6 +154,8 @@ __global__ void __launch_bounds__(256) sv_ce_rows_kernel(const __grid_constant__
                     if (a.status)
                         a.status[row] = SV_OK;
                     a.packed_lse[at] = a.lse[row];
+                    if (a.loss_in)
+                        a.packed_loss[at] = a.loss_in[row];
                     a.scale[at] = a.grad_loss ? a.grad_loss[row] : 1.0f;
                 }
             }
@@ -190,6 +196,7 @@ struct Tiles {
     float* label_logit;
     // gradients
     const float* lse;
+    const float* loss;  // or NULL
     const float* scale;
     float* sums;
     int64_t depth;
@@ -264,7 +271,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsMm, 1)
     });
 }
 
-// d of a piece of the vocabulary, bfloat16; zeros in rows and columns that only fill up tiles
+// d of a piece of the vocabulary, bfloat16; zeros in rows and columns that only fill up tiles.  The label's is p - 1: of
+// an lse, whose last place is 1e-6 to 4e-6 of p, or, without that cancellation, exp(-loss) - 1.
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsMm, 1)
     sv_ce_probs_kernel(const __grid_constant__ Tiles p) {
     TileStore store;
@@ -279,6 +287,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsMm, 1)
         const bool there = row < n;
         const int64_t y = there ? p.label[row] - c0 : -1;
         const float lse = there ? p.lse[row] : 0.0f, g = there ? p.scale[row] : 0.0f;
+        const bool given = p.loss != nullptr;
+        const float dy = given && y >= 0 && y < kTile ? expm1f(-p.loss[row]) : 0.0f;
         // rows behind those that fill up the last block of depth are read by nobody
         const int64_t warp_row = row - (threadIdx.x & 31);
         if (warp_row >= (n + kBlockK - 1) / kBlockK * kBlockK)
@@ -289,12 +299,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsMm, 1)
             load(c + 32, *reinterpret_cast<float(*)[32]>(v + 32));
             const int left = there ? (int)(p.V - c0 - c < 64 ? p.V - c0 - c : 64) : 0;
 #pragma unroll
-            for (int e = 0; e < 64; ++e) {
-                float d = ex2((v[e] - lse) * kLog2e);
-                if (y == c + e)
-                    d -= 1.0f;
-                v[e] = e < left ? d * g : 0.0f;
+            for (int e = 0; e < 64; ++e)
+                v[e] = ex2((v[e] - lse) * kLog2e);
+            if (y >= c && y < c + 64) {
+#pragma unroll
+                for (int e = 0; e < 64; ++e)
+                    if (y == c + e)
+                        v[e] = given ? dy : v[e] - 1.0f;
             }
+#pragma unroll
+            for (int e = 0; e < 64; ++e)
+                v[e] = e < left ? v[e] * g : 0.0f;
             store.put(&p.c, (int)(ct * kTile + c), (int)warp_row, v);
         }
     });
@@ -683,18 +698,20 @@ int spec_cross_entropy_run(sv_ctx* ctx, const void* hidden, int dtype, int64_t h
     return launch_after(sv_ce_join_kernel, j, dim3((unsigned)((r.R + 7) / 8), 1, 1), 256, 0, st) ? SV_OK : SV_ERR_CUDA;
 }
 
-int spec_cross_entropy_grad(sv_ctx* ctx, const void* hidden, int dtype, int64_t hidden_stride, const void* weight,
-                            int64_t weight_stride, const int32_t* labels, const int32_t* accept_len, const float* lse,
-                            const float* grad_loss, int B, int rows_per_seq, int64_t V, int64_t D, void* grad_hidden,
-                            int64_t grad_hidden_stride, void* grad_weight, int64_t grad_weight_stride, int32_t* status,
-                            void* workspace, size_t workspace_bytes, void* stream) {
+int spec_cross_entropy_grad_of_loss(sv_ctx* ctx, const void* hidden, int dtype, int64_t hidden_stride,
+                                    const void* weight, int64_t weight_stride, const int32_t* labels,
+                                    const int32_t* accept_len, const float* lse, const float* loss,
+                                    const float* grad_loss, int B, int rows_per_seq, int64_t V, int64_t D,
+                                    void* grad_hidden, int64_t grad_hidden_stride, void* grad_weight,
+                                    int64_t grad_weight_stride, int32_t* status, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
     CrossEntropyPlan plan;
     const int rc = check(ctx, hidden, dtype, hidden_stride, weight, weight_stride, labels, accept_len, B, rows_per_seq,
                          V, D, workspace, workspace_bytes, true, &plan);
     if (rc != SV_OK)
         return rc;
     const int64_t R = (int64_t)B * rows_per_seq, most = (int64_t)1 << 40;
-    if (!lse || (!grad_hidden && !grad_weight) || !aligned(lse, 4) || !aligned(grad_loss, 4) ||
+    if (!lse || (!grad_hidden && !grad_weight) || !aligned(lse, 4) || !aligned(loss, 4) || !aligned(grad_loss, 4) ||
         !aligned(grad_hidden, 2) || !aligned(grad_weight, 2) || !aligned(status, 4) ||
         (grad_hidden && (grad_hidden_stride < D || grad_hidden_stride > most ||
                          (double)R * (double)grad_hidden_stride >= 1099511627776.0)) ||
@@ -711,8 +728,10 @@ int spec_cross_entropy_grad(sv_ctx* ctx, const void* hidden, int dtype, int64_t 
     unsigned char* ws = static_cast<unsigned char*>(workspace);
     Rows r = pack_args(plan, ws, hidden, hidden_stride, labels, accept_len, B, rows_per_seq, V, D, ctx->d_err);
     r.lse = lse;
+    r.loss_in = loss;
     r.grad_loss = grad_loss;
     r.packed_lse = reinterpret_cast<float*>(ws + plan.lse);
+    r.packed_loss = reinterpret_cast<float*>(ws + plan.loss);
     r.scale = reinterpret_cast<float*>(ws + plan.scale);
     r.status = status;
     r.grad_hidden = static_cast<__nv_bfloat16*>(grad_hidden);
@@ -729,6 +748,7 @@ int spec_cross_entropy_grad(sv_ctx* ctx, const void* hidden, int dtype, int64_t 
     logits.rows = plan.rows;
     logits.a_rows = (int)(R < kTile ? R : kTile);
     logits.lse = r.packed_lse;
+    logits.loss = loss ? r.packed_loss : nullptr;
     logits.scale = r.scale;
     logits.sums = reinterpret_cast<float*>(ws + plan.sums);
     logits.depth = plan.depth;
@@ -780,6 +800,17 @@ int spec_cross_entropy_grad(sv_ctx* ctx, const void* hidden, int dtype, int64_t 
             return SV_ERR_CUDA;
     }
     return SV_OK;
+}
+
+int spec_cross_entropy_grad(sv_ctx* ctx, const void* hidden, int dtype, int64_t hidden_stride, const void* weight,
+                            int64_t weight_stride, const int32_t* labels, const int32_t* accept_len, const float* lse,
+                            const float* grad_loss, int B, int rows_per_seq, int64_t V, int64_t D, void* grad_hidden,
+                            int64_t grad_hidden_stride, void* grad_weight, int64_t grad_weight_stride, int32_t* status,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+    return spec_cross_entropy_grad_of_loss(ctx, hidden, dtype, hidden_stride, weight, weight_stride, labels, accept_len,
+                                           lse, nullptr, grad_loss, B, rows_per_seq, V, D, grad_hidden,
+                                           grad_hidden_stride, grad_weight, grad_weight_stride, status, workspace,
+                                           workspace_bytes, stream);
 }
 
 }  // extern "C"

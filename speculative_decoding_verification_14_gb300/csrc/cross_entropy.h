@@ -28,7 +28,7 @@ struct CrossEntropyPlan {
     int64_t piece_tiles; // of one piece of the vocabulary
     int64_t pieces;
     int splits;          // of a piece's depth in the hidden states' gradient
-    size_t index, label, lse, scale;    // [rows]: source row, label, lse, grad_loss
+    size_t index, label, lse, loss, scale;  // [rows]: source row, label, lse, loss, grad_loss
     size_t hidden;                      // bf16 [rows, depth]
     size_t stats, label_logit;          // float2 [vocab_tiles, rows], float [rows]
     size_t probs;                       // bf16 [rows, piece_tiles * kTile]

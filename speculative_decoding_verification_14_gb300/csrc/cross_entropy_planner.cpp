@@ -36,6 +36,7 @@ CrossEntropyPlan cross_entropy_plan(int num_sms, int64_t R, int64_t V, int64_t D
     p.hidden = take(p.rows * p.depth * 2);
     if (grad) {
         p.lse = take(p.rows * 4);
+        p.loss = take(p.rows * 4);
         p.scale = take(p.rows * 4);
         p.probs = take(p.rows * p.piece_tiles * kTile * 2);
         p.sums = take((int64_t)p.splits * p.rows * p.depth * 4);
