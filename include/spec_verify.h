@@ -551,8 +551,10 @@ int spec_distill_plan_for(int num_sms, int max_cluster, int B, int rows_per_seq,
  * An erroneous row (a label outside [-1, V): SV_ERR_TOKEN_RANGE; logits with a
  * NaN or +inf or only -inf, in the gradients' call an lse that is not finite or a
  * loss that is NaN: SV_ERR_NONFINITE) gets a NaN loss and lse and a NaN grad_hidden, adds nothing to
- * grad_weight, and sets the context's error word; a wait inside the kernels that
- * runs out sets SV_ERR_TIMEOUT there.  Repeated calls give the same bits.
+ * grad_weight, and sets the context's error word.  Where a wait inside the kernels
+ * runs out, no row of the call has an answer: loss, lse and grad_hidden of the rows
+ * that count are NaN, grad_weight has NaN in it (as a whole or from the product that
+ * was left on), and their status and the error word say SV_ERR_TIMEOUT.  Repeated calls give the same bits.
  * Asynchronous, no allocation; a few launches on `stream` (three per piece of the
  * vocabulary for both gradients); safe to capture.  Returns SV_OK,
  * SV_ERR_INVALID_ARG (null or misaligned pointers, sizes beyond the context's
@@ -676,6 +678,24 @@ int spec_verify_run_noalloc(int device,
  * SV_ERR_INVALID_ARG (null outputs, limit_ns > 2e9) or SV_ERR_CUDA. */
 int spec_verify_selftest_wait(int device, unsigned long long limit_ns, int arrive,
                               int* completed, unsigned long long* elapsed_ns);
+
+/* Self-test of what the losses' kernels do behind a wait that ran out (the pages have
+ * no counterpart: a diagnostic of this library).  In later calls on this context one
+ * wait of the kernels named is taken, once it is over, for one that ran out: nothing
+ * is withheld and nothing waits longer than it would.  The call has the outputs that
+ * it documents for SV_ERR_TIMEOUT.  One context of a process at a time, the last one
+ * named; 0 turns it off, and has to before that context is destroyed.
+ *   LOGITS  spec_cross_entropy_run's product
+ *   PROBS, HIDDEN, WEIGHT  the gradients' products, each in its first tile
+ * Returns SV_OK or SV_ERR_INVALID_ARG. */
+enum {
+    SV_SELFTEST_OFF = 0,
+    SV_SELFTEST_LOGITS = 1,
+    SV_SELFTEST_PROBS = 2,
+    SV_SELFTEST_HIDDEN = 3,
+    SV_SELFTEST_WEIGHT = 4
+};
+int spec_losses_selftest(sv_ctx* ctx, int wait);
 
 /* Release the context and everything it owns. */
 int spec_verify_destroy(sv_ctx* ctx);

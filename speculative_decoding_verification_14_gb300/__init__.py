@@ -18,6 +18,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libspecverify.so")
 
 SV_F32, SV_BF16 = 0, 1
+(SV_SELFTEST_OFF, SV_SELFTEST_LOGITS, SV_SELFTEST_PROBS, SV_SELFTEST_HIDDEN, SV_SELFTEST_WEIGHT) = range(5)
 (SV_OK, SV_ERR_INVALID_ARG, SV_ERR_UNSUPPORTED, SV_ERR_CUDA, SV_ERR_TOKEN_RANGE, SV_ERR_NONFINITE,
  SV_ERR_TIMEOUT, SV_ERR_UNIFORM_RANGE, SV_ERR_BAD_OFFSETS) = range(9)
 
@@ -176,6 +177,7 @@ def library() -> ctypes.CDLL:
                                                                 ctypes.c_int, ctypes.c_int64,
                                                                 ctypes.c_int64, ctypes.c_int,
                                                                 ctypes.POINTER(ctypes.c_size_t)]),
+            "spec_losses_selftest": (ctypes.c_int, [P, ctypes.c_int]),
             "spec_verify_set_telemetry": (ctypes.c_int, [P, P, ctypes.c_int]),
             "spec_sample_set_telemetry": (ctypes.c_int, [P, P]),
             "spec_verify_selftest_wait": (ctypes.c_int, [ctypes.c_int, ctypes.c_ulonglong,
@@ -473,6 +475,10 @@ def spec_cross_entropy_workspace_for(num_sms, B, rows_per_seq, V, D, grad):
     rc = library().spec_cross_entropy_workspace_for(num_sms, B, rows_per_seq, V, D, int(grad),
                                                     ctypes.byref(n))
     return rc, n.value
+
+
+def spec_losses_selftest(ctx, wait: int) -> int:
+    return library().spec_losses_selftest(ctx, int(wait))
 
 
 def spec_verify_set_telemetry(ctx, hist_ptr, bins) -> int:

@@ -21,7 +21,7 @@ HOST_SOURCES = ("planner.cpp", "adapt.cpp", "sampling_planner.cpp", "distill_pla
                 "cross_entropy_planner.cpp")
 HEADERS = ("sv_internal.h", "sv_context.h", "sampling_common.cuh", "sampling_weights.cuh",
            "sampling_row.cuh", "sampling_general.cuh", "losses_common.cuh", "two_floats.cuh", "distill_plan.h",
-           "matrix_product.cuh", "cross_entropy.h")
+           "matrix_product.cuh", "cross_entropy.h", "losses_selftest.h")
 SOURCES = [os.path.join(CSRC, f) for f in (*CUDA_SOURCES, *HEADERS, *HOST_SOURCES)] + [
     os.path.join(INCLUDE, "spec_verify.h")]
 

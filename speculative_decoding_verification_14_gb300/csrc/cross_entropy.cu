@@ -35,6 +35,7 @@
 #include "../../include/spec_verify.h"
 #include "cross_entropy.h"
 #include "distill_plan.h"
+#include "losses_selftest.h"
 #include "matrix_product.cuh"
 #include "sv_context.h"
 #include "two_floats.cuh"
@@ -65,7 +66,7 @@ struct Rows {
     int rows_per_seq;
     // packed
     int32_t* index;
-    int32_t* count;
+    int32_t* state;  // the number of rows that count, and whether a wait of this call has run out
     int32_t* label;
     float* packed_lse;
     float* packed_loss;
@@ -110,6 +111,8 @@ __global__ void __launch_bounds__(256) sv_ce_rows_kernel(const __grid_constant__
     const int64_t r0 = (int64_t)blockIdx.x * kRowsPerBlock, end = r0 < a.R ? r0 : a.R;
     if (tid == 0)
         before = 0;
+    if (tid == 0 && blockIdx.x == 0)
+        a.state[1] = 0;
     __syncthreads();
     int n = 0;
     for (int64_t r = tid; r < end; r += blockDim.x)
@@ -176,7 +179,7 @@ __global__ void __launch_bounds__(256) sv_ce_rows_kernel(const __grid_constant__
                     a.grad_hidden[row * a.grad_stride + d] = __float2bfloat16_rn(x);
         }
         if (lane == 0 && row == a.R - 1)
-            *a.count = (int32_t)(at + (kind == 0));
+            a.state[0] = (int32_t)(at + (kind == 0));
     }
 }
 
@@ -184,9 +187,12 @@ __global__ void __launch_bounds__(256) sv_ce_rows_kernel(const __grid_constant__
 
 struct Tiles {
     CUtensorMap a, b, c;  // c: what is written
-    const int32_t* count;
+    int32_t* state;  // the rows that count, and whether a wait of this call has run out
     const int32_t* label;
+    const int32_t* index;
+    int32_t* status;  // of the gradients' call, or NULL
     uint32_t* err_word;
+    int64_t selftest;  // a tile's number, or -1
     int64_t V, D;
     int64_t first_tile, tiles;  // vocabulary tiles of this launch
     int64_t rows;               // of the workspace
@@ -208,7 +214,6 @@ struct Tiles {
 
 // What a launch needs of the one before it is read behind wait_previous(), which run_tiles calls once its own
 // barriers and tensor memory are set up.
-__device__ __forceinline__ int64_t packed_rows(const Tiles& p) { return *p.count; }
 // the row of a tile that this thread has in tensor memory
 __device__ __forceinline__ int64_t tile_row(int64_t tile) {
     uint32_t rank;
@@ -216,16 +221,23 @@ __device__ __forceinline__ int64_t tile_row(int64_t tile) {
     return tile * kTile + rank * kHalf + (threadIdx.x & 127);
 }
 
+// Behind a wait that ran out no row of the call has an answer.
+__device__ __noinline__ void timed_out(int32_t* status, const int32_t* index, const int32_t* state) {
+    if (status)
+        for (int64_t r = threadIdx.x; r < *state; r += blockDim.x)
+            status[index[r]] = SV_ERR_TIMEOUT;
+}
+
 // (maximum, sum of exponentials) of each row's logits in each tile of the vocabulary, the label's left out: a loss
 // near 0 is the others' sum beside the label's weight, which is lost in a sum that begins with that weight
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsMm, 1)
     sv_ce_stats_kernel(const __grid_constant__ Tiles p) {
     int64_t n = 0;
-    const auto shape = [&] {
-        n = packed_rows(p);
+    const auto shape = [&](int64_t count) {
+        n = count;
         return MatrixShape{(n + kTile - 1) / kTile, p.tiles, (p.D + kBlockK - 1) / kBlockK, 1};
     };
-    run_tiles<false, false>(&p.a, &p.b, p.a_rows, shape, 0, 0, p.err_word, 1u << SV_ERR_TIMEOUT,
+    run_tiles<false, false>(&p.a, &p.b, p.a_rows, shape, 0, 0, p.err_word, 1u << SV_ERR_TIMEOUT, p.state, p.selftest,
                             [&](int64_t rt, int64_t ct, int, auto load) {
         const int64_t row = tile_row(rt), c0 = ct * kTile;
         const bool there = row < n;
@@ -277,11 +289,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsMm, 1)
     sv_ce_probs_kernel(const __grid_constant__ Tiles p) {
     TileStore store;
     int64_t n = 0;
-    const auto shape = [&] {
-        n = packed_rows(p);
+    const auto shape = [&](int64_t count) {
+        n = count;
         return MatrixShape{(n + kTile - 1) / kTile, p.tiles, (p.D + kBlockK - 1) / kBlockK, 1};
     };
-    run_tiles<false, false>(&p.a, &p.b, p.a_rows, shape, p.first_tile * kTile, 0, p.err_word, 1u << SV_ERR_TIMEOUT,
+    const bool gave_up = run_tiles<false, false>(&p.a, &p.b, p.a_rows, shape, p.first_tile * kTile, 0, p.err_word, 1u << SV_ERR_TIMEOUT, p.state, p.selftest,
                             [&](int64_t rt, int64_t ct, int, auto load) {
         const int64_t row = tile_row(rt), c0 = (p.first_tile + ct) * kTile;
         const bool there = row < n;
@@ -315,17 +327,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsMm, 1)
     });
     if (threadIdx.x >= 128)
         store.finish();
+    if (__builtin_expect(gave_up, 0))
+        timed_out(p.status, p.index, p.state);
 }
 
 // a piece's part of the hidden states' gradient: float32 sums, those of a split apart
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsMm, 1)
     sv_ce_hidden_kernel(const __grid_constant__ Tiles p) {
     int64_t n = 0;
-    const auto shape = [&] {
-        n = packed_rows(p);
+    const auto shape = [&](int64_t count) {
+        n = count;
         return MatrixShape{(n + kTile - 1) / kTile, (p.D + kTile - 1) / kTile, p.tiles * (kTile / kBlockK), p.splits};
     };
-    run_tiles<false, true>(&p.a, &p.b, p.a_rows, shape, 0, p.first_tile * kTile, p.err_word, 1u << SV_ERR_TIMEOUT,
+    const bool gave_up = run_tiles<false, true>(&p.a, &p.b, p.a_rows, shape, 0, p.first_tile * kTile, p.err_word, 1u << SV_ERR_TIMEOUT, p.state, p.selftest,
                            [&](int64_t rt, int64_t ct, int split, auto load) {
         const int64_t row = tile_row(rt), c0 = ct * kTile;
         float* out = p.sums + ((int64_t)split * p.rows + row) * p.depth + c0;
@@ -344,6 +358,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsMm, 1)
                 }
         }
     });
+    if (__builtin_expect(gave_up, 0))
+        timed_out(p.status, p.index, p.state);
 }
 
 // a piece's rows of the head's gradient
@@ -351,11 +367,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsMm, 1)
     sv_ce_weight_kernel(const __grid_constant__ Tiles p) {
     TileStore store;
     int64_t n = 0;
-    const auto shape = [&] {
-        n = packed_rows(p);
+    const auto shape = [&](int64_t count) {
+        n = count;
         return MatrixShape{p.tiles, (p.D + kTile - 1) / kTile, (n + kBlockK - 1) / kBlockK, 1};
     };
-    run_tiles<true, true>(&p.a, &p.b, p.a_rows, shape, 0, 0, p.err_word, 1u << SV_ERR_TIMEOUT,
+    const bool gave_up = run_tiles<true, true>(&p.a, &p.b, p.a_rows, shape, 0, 0, p.err_word, 1u << SV_ERR_TIMEOUT, p.state, p.selftest,
                           [&](int64_t rt, int64_t ct, int, auto load) {
         const int64_t v_id = p.first_tile * kTile + tile_row(rt), c0 = ct * kTile;
         if (p.out_vectors) {
@@ -381,12 +397,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreadsMm, 1)
     });
     if (threadIdx.x >= 128)
         store.finish();
+    if (__builtin_expect(gave_up, 0))
+        timed_out(p.status, p.index, p.state);
 }
 
 // ---------------------------------------------------------------- joins
 
 struct Join {
-    const int32_t* count;
+    const int2* state;  // the rows that count, and whether a wait of this call has run out
     const int32_t* index;
     int64_t rows, tiles, D, depth;
     const float2* stats;
@@ -412,7 +430,8 @@ __global__ void __launch_bounds__(256) sv_ce_join_kernel(const __grid_constant__
     wait_previous();
     const int at = threadIdx.x & 7, share = threadIdx.x >> 3;
     const int64_t row = (int64_t)blockIdx.x * 8 + at;
-    const int64_t n = *a.count;
+    const int2 state = *a.state;
+    const int64_t n = state.x;
     if ((int64_t)blockIdx.x * 8 >= n)
         return;
     const float inf = __int_as_float(0x7f800000);
@@ -458,13 +477,13 @@ __global__ void __launch_bounds__(256) sv_ce_join_kernel(const __grid_constant__
     const float nan = __int_as_float(0x7fffffff);
     float most = m;
     asm("max.NaN.f32 %0, %0, %1;" : "+f"(most) : "f"(z));
-    const bool good = most > -inf && most < inf;
+    const bool lost = state.y != 0, good = !lost && most > -inf && most < inf;
     const float ls = z >= m ? log1pf(s.h * expf(m - z)) : logf(s.h + (s.l + expf(z - m)));
     a.loss[to] = good ? (z >= m ? ls : (m - z) + ls) : nan;
     a.lse[to] = good ? most + ls : nan;
     if (a.status)
-        a.status[to] = good ? SV_OK : SV_ERR_NONFINITE;
-    if (!good)
+        a.status[to] = good ? SV_OK : lost ? SV_ERR_TIMEOUT : SV_ERR_NONFINITE;
+    if (!good && !lost)
         atomicOr(a.err_word, 1u << SV_ERR_NONFINITE);
 }
 
@@ -473,7 +492,8 @@ __global__ void __launch_bounds__(256) sv_ce_hidden_join_kernel(const __grid_con
     launch_next();
     wait_previous();
     const int64_t row = blockIdx.x, d = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 4;
-    if (row >= *a.count || d >= a.D)
+    const int2 state = *a.state;
+    if (row >= state.x || d >= a.D)
         return;
     const float4* from = reinterpret_cast<const float4*>(a.sums + row * a.depth + d);
     const int64_t apart = a.rows * a.depth / 4;
@@ -483,6 +503,8 @@ __global__ void __launch_bounds__(256) sv_ce_hidden_join_kernel(const __grid_con
         const float4 y = from[s * apart];
         x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
     }
+    if (state.y)
+        x.x = x.y = x.z = x.w = __int_as_float(0x7fffffff);
     __nv_bfloat16* out = a.grad_hidden + (int64_t)a.index[row] * a.grad_stride + d;
     if (d + 4 <= a.D && (reinterpret_cast<uintptr_t>(out) & 7u) == 0) {
         uint2 w;
@@ -626,7 +648,7 @@ Rows pack_args(const CrossEntropyPlan& plan, unsigned char* ws, const void* hidd
     r.depth = plan.depth;
     r.rows_per_seq = rows_per_seq;
     r.index = reinterpret_cast<int32_t*>(ws + plan.index);
-    r.count = r.index + plan.rows;
+    r.state = r.index + plan.rows;
     r.label = reinterpret_cast<int32_t*>(ws + plan.label);
     r.packed = reinterpret_cast<__nv_bfloat16*>(ws + plan.hidden);
     r.err_word = err_word;
@@ -669,7 +691,8 @@ int spec_cross_entropy_run(sv_ctx* ctx, const void* hidden, int dtype, int64_t h
     if (!tensor_map(&p.a, r.packed, plan.rows, D, plan.depth, box_rows(r.R)) ||
         !tensor_map(&p.b, weight, V, D, weight_stride, kHalf))
         return SV_ERR_CUDA;
-    p.count = r.count;
+    p.state = r.state;
+    p.selftest = losses_selftest(ctx) == SV_SELFTEST_LOGITS ? 0 : -1;
     p.label = r.label;
     p.err_word = ctx->d_err;
     p.V = V;
@@ -681,7 +704,7 @@ int spec_cross_entropy_run(sv_ctx* ctx, const void* hidden, int dtype, int64_t h
     p.label_logit = reinterpret_cast<float*>(ws + plan.label_logit);
     Join j;
     std::memset(&j, 0, sizeof j);
-    j.count = r.count;
+    j.state = reinterpret_cast<const int2*>(r.state);
     j.index = r.index;
     j.rows = plan.rows;
     j.tiles = plan.vocab_tiles;
@@ -740,8 +763,10 @@ int spec_cross_entropy_grad_of_loss(sv_ctx* ctx, const void* hidden, int dtype, 
     const int64_t width = plan.piece_tiles * kTile;
     Tiles logits, hid, wgt;
     std::memset(&logits, 0, sizeof logits);
-    logits.count = r.count;
+    logits.state = r.state;
     logits.label = r.label;
+    logits.index = r.index;
+    logits.status = status;
     logits.err_word = ctx->d_err;
     logits.V = V;
     logits.D = D;
@@ -758,6 +783,10 @@ int spec_cross_entropy_grad_of_loss(sv_ctx* ctx, const void* hidden, int dtype, 
     // the copy engine writes whole 16 bytes: beyond D too, where that ends inside some
     logits.out_vectors = aligned(grad_weight, 16) && grad_weight_stride % 8 == 0 && D % 8 == 0;
     hid = wgt = logits;
+    const int selftest = losses_selftest(ctx);
+    logits.selftest = selftest == SV_SELFTEST_PROBS ? 0 : -1;
+    hid.selftest = selftest == SV_SELFTEST_HIDDEN ? 0 : -1;
+    wgt.selftest = selftest == SV_SELFTEST_WEIGHT ? 0 : -1;
     if (!tensor_map(&logits.a, r.packed, plan.rows, D, plan.depth, box_rows(R)) ||
         !tensor_map(&logits.b, weight, V, D, weight_stride, kHalf) ||
         !tensor_map(&hid.a, probs, plan.rows, width, width, box_rows(R)) ||
@@ -787,7 +816,7 @@ int spec_cross_entropy_grad_of_loss(sv_ctx* ctx, const void* hidden, int dtype, 
     if (grad_hidden) {
         Join j;
         std::memset(&j, 0, sizeof j);
-        j.count = r.count;
+        j.state = reinterpret_cast<const int2*>(r.state);
         j.index = r.index;
         j.rows = plan.rows;
         j.D = D;

@@ -1,11 +1,23 @@
 // cross_entropy_planner.cpp -- pieces of the vocabulary, splits and workspace of the cross-entropy
-// calls.
+// calls; the losses' self-test.
 #include "cross_entropy.h"
 
+#include <atomic>
+
 #include "../../include/spec_verify.h"
+#include "losses_selftest.h"
 #include "sv_internal.h"
 
 namespace sv {
+
+namespace {
+std::atomic<const sv_ctx*> tested{nullptr};
+std::atomic<int> tested_wait{0};
+}  // namespace
+
+int losses_selftest(const sv_ctx* ctx) {
+    return tested.load(std::memory_order_acquire) == ctx ? tested_wait.load(std::memory_order_relaxed) : SV_SELFTEST_OFF;
+}
 
 CrossEntropyPlan cross_entropy_plan(int num_sms, int64_t R, int64_t V, int64_t D, bool grad) {
     CrossEntropyPlan p{};
@@ -31,7 +43,7 @@ CrossEntropyPlan cross_entropy_plan(int num_sms, int64_t R, int64_t V, int64_t D
         at += (size_t)round_up(bytes, 256);
         return here;
     };
-    p.index = take(p.rows * 4 + 4);  // and the number of rows that count
+    p.index = take(p.rows * 4 + 8);  // and the number of rows that count, and whether a wait ran out
     p.label = take(p.rows * 4);
     p.hidden = take(p.rows * p.depth * 2);
     if (grad) {
@@ -49,6 +61,16 @@ CrossEntropyPlan cross_entropy_plan(int num_sms, int64_t R, int64_t V, int64_t D
 }
 
 }  // namespace sv
+
+extern "C" int spec_losses_selftest(sv_ctx* ctx, int wait) {
+    if (!ctx || wait < SV_SELFTEST_OFF || wait > SV_SELFTEST_WEIGHT)
+        return SV_ERR_INVALID_ARG;
+    sv::tested.store(nullptr, std::memory_order_release);
+    sv::tested_wait.store(wait, std::memory_order_relaxed);
+    if (wait != SV_SELFTEST_OFF)
+        sv::tested.store(ctx, std::memory_order_release);
+    return SV_OK;
+}
 
 extern "C" int spec_cross_entropy_workspace_for(int num_sms, int B, int rows_per_seq, int64_t V, int64_t D, int grad,
                                                 size_t* bytes) {

@@ -33,24 +33,79 @@ constexpr int kSmemMm = kStagesMm * kStageBytes + 8 * kStoreBytes + 1024;  // tw
                                                                            // distance to a multiple of 1024
 
 struct MatrixBarriers {
-    uint64_t full[kStagesMm], empty[kStagesMm], tile_full[2], tile_empty[2];
+    uint64_t full[kStagesMm], empty[kStagesMm], tile_full[2], tile_empty[2], done;
+    long long fills[2];  // stages that either CTA has issued its copies for
     uint32_t tmem, failed;
 };
 
-// Waits for a phase, at most kWaitNs; whoever gives up says so to the CTA's other warps, which then give up too.
-static __device__ __noinline__ bool matrix_wait_slow(uint64_t* bar, uint32_t parity, volatile uint32_t* failed) {
+// A wait for copies has their own limit, one for what follows from copies, or from products of them, that and kWaitNs.
+constexpr unsigned long long kProductWaitNs = kCopyWaitNs + kWaitNs;
+
+// Whoever gives up says so to all warps of the pair, which then give up at their next wait that is not over.
+__device__ __forceinline__ void give_up(volatile uint32_t* failed) {
+    uint32_t rank;
+    asm("mov.u32 %0, %cluster_ctarank;" : "=r"(rank));
+    *failed = 1;
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr(const_cast<uint32_t*>(failed), rank ^ 1u)), "r"(1u)
+                 : "memory");
+}
+// Waits for a phase, at most `limit` ns.
+static __device__ __noinline__ bool matrix_wait_slow(uint64_t* bar, uint32_t parity, unsigned long long limit,
+                                                     volatile uint32_t* failed) {
     const unsigned long long t0 = global_ns();
     while (!*failed) {
         for (int i = 0; i < 64; ++i)
             if (barrier_try_cluster(bar, parity))
                 return true;
-        if (global_ns() - t0 > kWaitNs)
-            *failed = 1;
+        if (global_ns() - t0 > limit)
+            give_up(failed);
     }
     return false;
 }
-__device__ __forceinline__ bool matrix_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* failed) {
-    return barrier_try_cluster(bar, parity) || matrix_wait_slow(bar, parity, failed);
+__device__ __forceinline__ bool matrix_wait(uint64_t* bar, uint32_t parity, unsigned long long limit,
+                                            volatile uint32_t* failed) {
+    return barrier_try_cluster(bar, parity) || matrix_wait_slow(bar, parity, limit, failed);
+}
+
+// After a pair has given up, and all its warps know and wait for one another: the copies issued have landed and the
+// products issued are done before either CTA leaves, as far as kCopyWaitNs and kWaitNs see.  One CTA may have issued
+// copies of a stage whose other half the other one then left out, up to a ring's worth: the first CTA, on whose
+// barriers both halves arrive, takes the half that never comes off what the barrier expects.
+static __device__ __noinline__ void matrix_drain(MatrixBarriers& bars, uint32_t second_bytes, int32_t* state,
+                                                 uint32_t* err_word, uint32_t timeout_bit) {
+    uint32_t rank;
+    asm("mov.u32 %0, %cluster_ctarank;" : "=r"(rank));
+    if (rank == 1 && threadIdx.x == 0)
+        asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(cluster_addr(&bars.fills[1], 0)), "l"(bars.fills[1]) : "memory");
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+    if (threadIdx.x == 0 && rank == 0) {
+        const long long own = bars.fills[0], other = bars.fills[1], most = own > other ? own : other;
+        for (long long j = own; j < other; ++j)
+            barrier_expect(&bars.full[j % kStagesMm], second_bytes);
+        for (long long j = other; j < own; ++j)
+            asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(
+                             shared_addr(&bars.full[j % kStagesMm])),
+                         "r"(second_bytes)
+                         : "memory");
+        for (long long j = most > kStagesMm ? most - kStagesMm : 0; j < most; ++j)
+            barrier_wait(&bars.full[j % kStagesMm], (uint32_t)(j / kStagesMm) & 1u, kCopyWaitNs);
+    }
+    if (threadIdx.x == 32) {  // of the first CTA: the thread that issued the products
+        if (rank == 0)
+            asm volatile(
+                "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                    shared_addr(&bars.done)),
+                "h"((uint16_t)3)
+                : "memory");
+        barrier_wait(&bars.done, 0, kWaitNs);
+    }
+    __syncthreads();
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+    if (threadIdx.x == 0) {
+        *(volatile int32_t*)(state + 1) = 1;
+        atomicOr(err_word, timeout_bit);
+    }
 }
 
 __device__ __forceinline__ void copy_tile(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
@@ -184,10 +239,15 @@ struct MatrixShape {
 // operand) at which B begins in its map, kb: depth likewise.  finish(row tile, column tile, split, load) is called by the four tile warps of each CTA
 // for each tile; load(c, v) gives columns c .. c + 31 of the thread's row, and has to be called by whole warps;
 // without a single block of depth the tile is all zeros and load gives them.
+// state: the rows that count, which the shape is asked with, and whether a wait has run out, kept in memory from launch to
+// launch and read in one load.  A pair whose wait ran out, and every pair of a
+// launch behind one where that happened, does no more products: load gives NaN for each tile that is left, so that none
+// keeps what an earlier call wrote.  Such a pair says so there and in the error word, and run_tiles returns true.
+// selftest: the number of a tile at which the tile warps do as if their wait for it had run out; -1 for none.
 template <bool TurnedA, bool TurnedB, typename Shape, typename Finish>
-__device__ __forceinline__ void run_tiles(const CUtensorMap* map_a, const CUtensorMap* map_b, int a_rows,
+__device__ __forceinline__ bool run_tiles(const CUtensorMap* map_a, const CUtensorMap* map_b, int a_rows,
                                           Shape shape_of, int64_t b0, int64_t kb, uint32_t* err_word, uint32_t timeout_bit,
-                                          Finish finish) {
+                                          int32_t* state, int64_t selftest, Finish finish) {
     extern __shared__ unsigned char dynamic[];
     __shared__ MatrixBarriers bars;
     const uint32_t stage0 = (shared_addr(dynamic) + 1023u) & ~1023u;
@@ -206,6 +266,7 @@ __device__ __forceinline__ void run_tiles(const CUtensorMap* map_a, const CUtens
             barrier_init(&bars.tile_full[t], 1);
             barrier_init(&bars.tile_empty[t], 8);  // four warps of two CTAs
         }
+        barrier_init(&bars.done, 1);
         bars.failed = 0;
         barrier_init_fence();
     }
@@ -222,15 +283,21 @@ __device__ __forceinline__ void run_tiles(const CUtensorMap* map_a, const CUtens
     const uint32_t tmem = *(volatile uint32_t*)&bars.tmem;
     launch_next();
     wait_previous();
-    const MatrixShape shape = shape_of();
+    int32_t count, lost;
+    asm volatile("ld.global.v2.s32 {%0, %1}, [%2];" : "=r"(count), "=r"(lost) : "l"(state) : "memory");
+    const MatrixShape shape = shape_of((int64_t)count);
+    const uint32_t second_bytes = TurnedA || a_rows > kHalf ? kStageBytes : kOperandBytes;  // the second CTA's copies
+    const uint32_t stage_bytes = second_bytes + (TurnedA || a_rows > kHalf ? kStageBytes : kOperandBytes + box_rows(a_rows) * 128u);
+    const bool late = lost != 0;
+    if (late && threadIdx.x == 0)
+        give_up(failed);
 
     if (warp == 0) {
         if (lane == 0) {
-            const uint32_t stage_bytes = TurnedA || a_rows > kHalf ? 2 * kStageBytes
-                                                                   : 2 * kOperandBytes + box_rows(a_rows) * 128u;
             int stage = 0;
             uint32_t phase = 0;
-            bool go = true;
+            bool go = !late;
+            long long fills = 0;
             for (int64_t i = pair; go && i < shape.tiles(); i += pairs) {
                 int64_t row, column, k0, k1;
                 int split;
@@ -238,10 +305,11 @@ __device__ __forceinline__ void run_tiles(const CUtensorMap* map_a, const CUtens
                 shape.depth(split, k0, k1);
                 const int ra = (int)(row * kTile + rank * kHalf), rb = (int)(b0 + column * kTile + rank * kHalf);
                 for (int64_t k = k0; k < k1; ++k) {
-                    if (!matrix_wait(&bars.empty[stage], phase ^ 1u, failed)) {
+                    if (!matrix_wait(&bars.empty[stage], phase ^ 1u, kProductWaitNs, failed)) {
                         go = false;
                         break;
                     }
+                    ++fills;
                     // both CTAs' copies arrive on the first one's barrier
                     const uint32_t bar = cluster_addr(&bars.full[stage], 0);
                     if (rank == 0)
@@ -266,17 +334,18 @@ __device__ __forceinline__ void run_tiles(const CUtensorMap* map_a, const CUtens
             }
             // until every stage was read: the last arrivals on this CTA's barriers are in
             for (int s = 0; go && s < kStagesMm; ++s) {
-                go = matrix_wait(&bars.empty[stage], phase ^ 1u, failed);
+                go = matrix_wait(&bars.empty[stage], phase ^ 1u, kProductWaitNs, failed);
                 if (++stage == kStagesMm)
                     stage = 0, phase ^= 1u;
             }
+            bars.fills[rank] = fills;
         }
         __syncwarp();
     } else if (warp == 1) {
         if (rank == 0 && lane == 0) {
             int stage = 0, t = 0;
             uint32_t phase = 0, tphase = 0;
-            bool go = true;
+            bool go = !late;
             for (int64_t i = pair; go && i < shape.tiles(); i += pairs) {
                 int64_t row, column, k0, k1;
                 int split;
@@ -284,12 +353,12 @@ __device__ __forceinline__ void run_tiles(const CUtensorMap* map_a, const CUtens
                 shape.depth(split, k0, k1);
                 if (k0 == k1)
                     continue;
-                if (!matrix_wait(&bars.tile_empty[t], tphase ^ 1u, failed))
+                if (!matrix_wait(&bars.tile_empty[t], tphase ^ 1u, kWaitNs, failed))
                     break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 const uint32_t d = tmem + t * kTile;
                 for (int64_t k = k0; k < k1; ++k) {
-                    if (!matrix_wait(&bars.full[stage], phase, failed)) {
+                    if (!matrix_wait(&bars.full[stage], phase, kCopyWaitNs, failed)) {
                         go = false;
                         break;
                     }
@@ -315,22 +384,28 @@ __device__ __forceinline__ void run_tiles(const CUtensorMap* map_a, const CUtens
     } else if (warp >= 4) {
         int t = 0;
         uint32_t tphase = 0;
+        bool there = !late;
         for (int64_t i = pair; i < shape.tiles(); i += pairs) {
             int64_t row, column, k0, k1;
             int split;
             shape.tile(i, row, column, split);
             shape.depth(split, k0, k1);
-            if (k0 == k1) {
-                finish(row, column, split, [](int, float(&v)[32]) {
+            if (there && k0 < k1) {
+                there = __all_sync(0xffffffffu, matrix_wait(&bars.tile_full[t], tphase, kProductWaitNs, failed));
+                if (i == selftest) {
+                    give_up(failed);
+                    there = false;
+                }
+            }
+            if (!there || k0 == k1) {
+                const float fill = there ? 0.0f : __int_as_float(0x7fffffff);
+                finish(row, column, split, [fill](int, float(&v)[32]) {
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
-                        v[e] = 0.0f;
+                        v[e] = fill;
                 });
                 continue;
             }
-            const bool there = matrix_wait(&bars.tile_full[t], tphase, failed);
-            if (!__all_sync(0xffffffffu, there))
-                break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t at = tmem + t * kTile + ((uint32_t)((warp & 3) * 32) << 16);
             finish(row, column, split, [at](int c, float(&v)[32]) { load_columns(at + c, v); });
@@ -342,16 +417,17 @@ __device__ __forceinline__ void run_tiles(const CUtensorMap* map_a, const CUtens
                 t = 0, tphase ^= 1u;
         }
     }
-    // neither CTA leaves while the other may still write into it; after a wait that ran out (seconds), copies have
-    // long landed
+    // neither CTA leaves while the other may still write into it
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     __syncthreads();
     asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    if (threadIdx.x == 0 && *failed)
-        atomicOr(err_word, timeout_bit);
+    const bool gave_up = *failed != 0;  // the same in both
+    if (__builtin_expect(gave_up, 0))
+        matrix_drain(bars, second_bytes, state, err_word, timeout_bit);
     if (warp == 2)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemColumns) : "memory");
+    return gave_up;
 }
 
 }  // namespace sv
