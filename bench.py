@@ -125,8 +125,8 @@ KERNEL_SOURCES = {
                  "sampling_weights.cuh", "sampling_planner.cpp", "sv_context.h"),
     "logprobs": ("logprobs.cu", "sampling_common.cuh", "sampling_weights.cuh", "sampling_planner.cpp",
                  "sv_context.h"),
-    "distill": ("distill.cu", "distill_plan.h", "distill_planner.cpp", "losses_common.cuh", "two_floats.cuh",
-                "sampling_common.cuh", "sampling_weights.cuh", "sv_internal.h", "sv_context.h"),
+    "distill": ("distill.cu", "distill_plan.h", "distill_planner.cpp", "losses_common.cuh", "losses_selftest.h",
+                "two_floats.cuh", "sampling_common.cuh", "sampling_weights.cuh", "sv_internal.h", "sv_context.h"),
     "cross_entropy": ("cross_entropy.cu", "cross_entropy.h", "cross_entropy_planner.cpp", "matrix_product.cuh",
                       "losses_common.cuh", "losses_selftest.h", "two_floats.cuh", "distill_plan.h", "sv_internal.h",
                       "sv_context.h"),

@@ -491,7 +491,9 @@ int spec_logprobs_plan_for(int num_sms, int max_cluster, int B, int rows_per_seq
  * [-1, V) or listed twice: SV_ERR_TOKEN_RANGE; a listed log-probability that is
  * NaN or +inf, or only -inf under tail 0; logits with a NaN or +inf or only -inf:
  * SV_ERR_NONFINITE) gets a NaN loss and NaN gradients, and sets the context's
- * error word.
+ * error word.  Where a wait inside the kernel runs out, so do the rows that its
+ * cluster has left, with SV_ERR_TIMEOUT (of the row itself, where it is the wait for
+ * what other CTAs have found, perhaps only the waiting CTA's part of the gradient).
  * Repeated calls give the same bits.  Asynchronous, no allocation, one launch on
  * `stream`; safe to capture.  Rows that 16 CTAs' shared memory holds (V up to
  * 884733 float, 1769465 bfloat16) are taken: SV_ERR_UNSUPPORTED beyond.  Otherwise
@@ -687,13 +689,16 @@ int spec_verify_selftest_wait(int device, unsigned long long limit_ns, int arriv
  * named; 0 turns it off, and has to before that context is destroyed.
  *   LOGITS  spec_cross_entropy_run's product
  *   PROBS, HIDDEN, WEIGHT  the gradients' products, each in its first tile
+ *   DISTILL_COPY, DISTILL_EXCHANGE  spec_distill_run's, in the last CTA of the middle row
  * Returns SV_OK or SV_ERR_INVALID_ARG. */
 enum {
     SV_SELFTEST_OFF = 0,
     SV_SELFTEST_LOGITS = 1,
     SV_SELFTEST_PROBS = 2,
     SV_SELFTEST_HIDDEN = 3,
-    SV_SELFTEST_WEIGHT = 4
+    SV_SELFTEST_WEIGHT = 4,
+    SV_SELFTEST_DISTILL_COPY = 5,
+    SV_SELFTEST_DISTILL_EXCHANGE = 6
 };
 int spec_losses_selftest(sv_ctx* ctx, int wait);
 

@@ -18,7 +18,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libspecverify.so")
 
 SV_F32, SV_BF16 = 0, 1
-(SV_SELFTEST_OFF, SV_SELFTEST_LOGITS, SV_SELFTEST_PROBS, SV_SELFTEST_HIDDEN, SV_SELFTEST_WEIGHT) = range(5)
+(SV_SELFTEST_OFF, SV_SELFTEST_LOGITS, SV_SELFTEST_PROBS, SV_SELFTEST_HIDDEN, SV_SELFTEST_WEIGHT,
+ SV_SELFTEST_DISTILL_COPY, SV_SELFTEST_DISTILL_EXCHANGE) = range(7)
 (SV_OK, SV_ERR_INVALID_ARG, SV_ERR_UNSUPPORTED, SV_ERR_CUDA, SV_ERR_TOKEN_RANGE, SV_ERR_NONFINITE,
  SV_ERR_TIMEOUT, SV_ERR_UNIFORM_RANGE, SV_ERR_BAD_OFFSETS) = range(9)
 

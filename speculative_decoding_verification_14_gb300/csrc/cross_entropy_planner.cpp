@@ -63,7 +63,7 @@ CrossEntropyPlan cross_entropy_plan(int num_sms, int64_t R, int64_t V, int64_t D
 }  // namespace sv
 
 extern "C" int spec_losses_selftest(sv_ctx* ctx, int wait) {
-    if (!ctx || wait < SV_SELFTEST_OFF || wait > SV_SELFTEST_WEIGHT)
+    if (!ctx || wait < SV_SELFTEST_OFF || wait > SV_SELFTEST_DISTILL_EXCHANGE)
         return SV_ERR_INVALID_ARG;
     sv::tested.store(nullptr, std::memory_order_release);
     sv::tested_wait.store(wait, std::memory_order_relaxed);

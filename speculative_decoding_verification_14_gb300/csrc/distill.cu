@@ -19,13 +19,18 @@
 // would lose what 1 - sum t_k or a small loss leaves (up to 5e-5 of it), and 64-bit arithmetic takes 140 cycles an
 // operation (with it, by the teacher, 256 x 8 rows of 128256 bfloat16 took 334 us).
 //
-// What bounds it: 256 x 8 rows of 128256, 20 entries, loss and gradient: bfloat16 223 us for 1.05 GB (4.7 TB/s, 0.70 of
-// a copy's rate), float32 416 us (0.75); 64 x 4 of 151936 bfloat16 44 us (0.52).  A CTA's turn of some 20 thousand
+// What bounds it: 256 x 8 rows of 128256, 20 entries, loss and gradient: bfloat16 224 us for 1.05 GB (4.7 TB/s, 0.69 of
+// a copy's rate), float32 416 us (0.75); 64 x 4 of 151936 bfloat16 46 us (0.50).  A CTA's turn of some 20 thousand
 // cycles is 2.5 waiting for the copy, 1.5 at the barriers before the sums, 4 summing, 6 between the sums and the
 // gradient (joins, the exchange, the teacher), 6 writing; three CTAs an SM (their slices fill its shared memory) hide
 // most of one another's, and no pipe is above 30 %.  Tried: rows one by one, a cluster each, 279 and 485 us; four CTAs
 // an SM with smaller slices 259 and 462, two with larger ones 234 and 410; 256 or 320 walkers an SM at fewer
 // registers 246 and 261.
+// Three CTAs of 288 threads leave 72 registers a thread; the scribe, who alone keeps two rows' lists, spills some 130
+// bytes of them (204 read back), once a row of the first CTA.
+//
+// A wait that runs out (2 s for other CTAs, 10 s for a copy) ends the cluster's work: the CTA that gave up says so with
+// its next sums, no CTA that hears of it waits or copies any more, and the rows left get NaN and SV_ERR_TIMEOUT.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -38,6 +43,7 @@
 #include "../../include/spec_verify.h"
 #include "distill_plan.h"
 #include "losses_common.cuh"
+#include "losses_selftest.h"
 #include "sampling_common.cuh"
 #include "sv_context.h"
 #include "two_floats.cuh"
@@ -69,11 +75,14 @@ struct Args {
     uint32_t* err_word;
     int64_t V, rows;
     int rows_per_seq, C, n, tail;
+    int selftest;          // SV_SELFTEST_DISTILL_COPY or _EXCHANGE: in the last CTA of this row; 0 for neither
+    int64_t selftest_row;
     uint32_t vectors;  // per CTA
     float iT, iTl, ch, cl;  // 1 / T and log2(e) / T in two parts each, the latter's both above 0
 };
 
-// what a CTA's slice gives off the list: a sum of weights, 2^-38 a unit in two halves, and what they are against
+// what a CTA's slice gives off the list: a sum of weights, 2^-38 a unit in two halves, and what they are against; hi is
+// -1 from a CTA that has given up
 struct CtaPart {
     float hi, lo, m;
 };
@@ -99,6 +108,9 @@ struct Shared {
     float list_max, list_sum;
     uint32_t listed;  // whether a token is
     uint32_t flags;   // 1 << code
+    // Whether a wait of this CTA, or of one that told it so, has run out before a turn: of even turns and of odd ones,
+    // each written in the turn before.  From then on it waits no more, copies nothing, and its rows have no answers.
+    uint32_t dead[2];
 };
 
 __device__ __forceinline__ void store_cluster(uint32_t addr, float x) {
@@ -318,6 +330,7 @@ __global__ void __launch_bounds__(kNT + 64, kDistillCtas) sv_distill_kernel(cons
     if (teacher && lane == 0) {
         sh.listed = 0;
         sh.flags = 0;
+        sh.dead[0] = sh.dead[1] = 0;
         barrier_init(&sh.bar, 1);
         for (int i = 0; i < 2; ++i)
             barrier_init(&sh.exchange[i], (uint32_t)C + 1);  // every CTA's sums, and the first one's r
@@ -461,8 +474,9 @@ __global__ void __launch_bounds__(kNT + 64, kDistillCtas) sv_distill_kernel(cons
         const Part<ES> p(base, a.V, a.vectors, (int)rank);
         const bool more = row + clusters < a.rows;
         const bool live = __syncthreads_and(next_live);  // one answer for the CTA, whose last row is done with
+        const bool dead = sh.dead[odd] != 0;
         if (teacher) {
-            if (live && lane == 0) {
+            if (live && !dead && lane == 0) {
                 uint32_t first;
                 const uint32_t bytes = whole_vectors(p, first);
                 barrier_expect(&sh.bar, bytes);
@@ -522,7 +536,7 @@ __global__ void __launch_bounds__(kNT + 64, kDistillCtas) sv_distill_kernel(cons
             if (flags)
                 atomicOr(&sh.flags, flags);
             __syncwarp();
-            if (live && more && next_live && lane == 0) {  // the next row comes into L2 meanwhile
+            if (live && more && next_live && !dead && lane == 0) {  // the next row comes into L2 meanwhile
                 const unsigned char* after = row_base(row + clusters);
                 const Part<ES> q(after, a.V, a.vectors, (int)rank);
                 uint32_t first;
@@ -531,9 +545,12 @@ __global__ void __launch_bounds__(kNT + 64, kDistillCtas) sv_distill_kernel(cons
                     prefetch_bulk(after - (size_t)q.off * ES + (size_t)first * 16, bytes);
             }
             __syncwarp();
-            if (!barrier_try_cluster(&sh.exchange[odd], phase) &&
-                !barrier_wait_cluster(&sh.exchange[odd], phase, kWaitNs))
+            if (dead || (!barrier_try_cluster(&sh.exchange[odd], phase) &&
+                         !barrier_wait_cluster(&sh.exchange[odd], phase, kWaitNs)) ||
+                (a.selftest == SV_SELFTEST_DISTILL_EXCHANGE && row == a.selftest_row && (int)rank == C - 1)) {
                 atomicOr(&sh.flags, 1u << SV_ERR_TIMEOUT);
+                sh.dead[odd ^ 1u] = 1;
+            }
             __syncwarp();
             if (!live) {
                 if (rank == 0 && lane == 0) {
@@ -568,6 +585,11 @@ __global__ void __launch_bounds__(kNT + 64, kDistillCtas) sv_distill_kernel(cons
                 su += __shfl_xor_sync(kAllLanes, su, o);
                 S += __shfl_xor_sync(kAllLanes, S, o);
             }
+            if (__any_sync(kAllLanes, part.hi < 0.0f) && lane == 0) {
+                atomicOr(&sh.flags, 1u << SV_ERR_TIMEOUT);
+                sh.dead[odd ^ 1u] = 1;
+            }
+            __syncwarp();
             flags = sh.flags;
             const bool answer = flags || sh.listed;
             const int code = flags ? __ffs(flags) - 1
@@ -610,7 +632,7 @@ __global__ void __launch_bounds__(kNT + 64, kDistillCtas) sv_distill_kernel(cons
             if (more)
                 next_live = is_live(row + clusters);
             if (live && rank == 0) {
-                if (!barrier_try_cluster(&sh.exchange[odd], phase))
+                if (!dead && !barrier_try_cluster(&sh.exchange[odd], phase))
                     barrier_wait_cluster(&sh.exchange[odd], phase, kWaitNs);  // the teacher says if it ran out
                 __syncwarp();
                 owed.part = lane < C ? sh.part[odd][lane] : CtaPart{0.0f, 0.0f, -inf};
@@ -640,7 +662,7 @@ __global__ void __launch_bounds__(kNT + 64, kDistillCtas) sv_distill_kernel(cons
         int32_t x = tokens[0];  // listed token number tid
         float mine = -inf;      // and its logit, where it is of this slice
         bool own = false;
-        if (live) {
+        if (live && !dead) {
             if (tid < 2 * E && p.v0 < p.v1) {  // the row's ends, where vectors are not whole
                 const uint32_t k = tid < E ? p.v0 : p.v1 - 1;
                 const int64_t id = (int64_t)k * E - p.off + tid % E;
@@ -660,16 +682,25 @@ __global__ void __launch_bounds__(kNT + 64, kDistillCtas) sv_distill_kernel(cons
             next_live = is_live(row + clusters);
             fetch(row + clusters);
         }
-        if (!live) {
-            if (warp == 0 && lane < C)
+        if (!live || dead) {
+            if (warp == 0 && lane < C) {
+                if (live)
+                    store_cluster(cluster_addr(&sh.part[odd][rank].hi, lane), -1.0f);
                 barrier_arrive_cluster(cluster_addr(&sh.exchange[odd], lane));
+            }
             __syncwarp();
+            if (live)
+                __syncthreads();  // the others' warps wait for the teacher's answer
+            const uint32_t v = !live ? 0u : ES == 4 ? 0x7fffffffu : 0x7fff7fffu;
             if (grad)
-                write_part<ES>(p, grad, [](uint32_t) { return make_uint4(0, 0, 0, 0); });
+                write_part<ES>(p, grad, [&](uint32_t) { return make_uint4(v, v, v, v); });
             continue;
         }
-        if (!barrier_wait(&sh.bar, loads & 1u, kCopyWaitNs))
+        if (!barrier_wait(&sh.bar, loads & 1u, kCopyWaitNs) ||
+            (a.selftest == SV_SELFTEST_DISTILL_COPY && row == a.selftest_row && (int)rank == C - 1)) {
             atomicOr(&sh.flags, 1u << SV_ERR_TIMEOUT);
+            sh.dead[odd ^ 1u] = 1;
+        }
         ++loads;
         sync_walkers();  // also the row's ends are in
         const uint32_t vectors = sh.listed ? p.v1 - p.v0 : 0;  // without a list there is nothing to sum
@@ -731,7 +762,7 @@ __global__ void __launch_bounds__(kNT + 64, kDistillCtas) sv_distill_kernel(cons
             for (int w = 0; w < kNW; ++w)
                 sum += sh.warp_sum[w];
             const uint32_t to = cluster_addr(&sh.part[odd][rank], lane);
-            store_cluster(to, (float)(uint32_t)(sum >> 32));
+            store_cluster(to, (sh.flags >> SV_ERR_TIMEOUT) & 1u ? -1.0f : (float)(uint32_t)(sum >> 32));
             store_cluster(to + 4, (float)(uint32_t)sum);
             store_cluster(to + 8, m);
             barrier_arrive_cluster(cluster_addr(&sh.exchange[odd], lane));
@@ -760,6 +791,11 @@ __global__ void __launch_bounds__(kNT + 64, kDistillCtas) sv_distill_kernel(cons
     __syncwarp();
     cluster_arrive();
     cluster_wait();
+    if (tid == 0 && (sh.dead[0] | sh.dead[1])) {
+        if (loads)
+            barrier_wait(&sh.bar, (loads - 1) & 1u, kCopyWaitNs);  // the last copy that was issued
+        atomicOr(a.err_word, 1u << SV_ERR_TIMEOUT);
+    }
 }
 
 // Attributes of the kernels on a device, once.
@@ -876,6 +912,8 @@ int spec_distill_run(sv_ctx* ctx, const void* draft_logits, int logits_dtype, in
     a.cl = (float)(c - (double)a.ch);
     if (!(a.cl >= 1.17549435e-38f))  // a difference of -inf times it is -inf
         a.cl = 1.17549435e-38f;
+    a.selftest = losses_selftest(ctx);
+    a.selftest_row = rows / 2;
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof cfg);
     cfg.blockDim = dim3(kNT + 64, 1, 1);

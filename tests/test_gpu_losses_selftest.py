@@ -87,6 +87,49 @@ def test_gradients(product, B, rows, V, D):
         check(None, {k: t.nan_to_num() for k, t in again.items()}, h, W, y, w, live)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("cluster,V", [(0, 2000), (3, 4003), (16, 5001)])
+@pytest.mark.parametrize("wait", ["COPY", "EXCHANGE"])
+def test_distillation(wait, cluster, V, dtype):
+    """The middle row's cluster loses that row and those it takes after it; every other row is as it was."""
+    import torch
+    import speculative_decoding_verification_14_gb300 as sv
+    from tests.test_gpu_distill import make as rows_of
+    B, rows = 1024, 4
+    z, a, x, w = rows_of(B, rows, V, 12, dtype, V)
+    lens = torch.randint(0, rows + 1, (B,), device="cuda", generator=torch.Generator(device="cuda").manual_seed(V),
+                         dtype=torch.int32)
+    lens[B // 2] = rows
+    live = (torch.arange(rows, device="cuda")[None] < lens[:, None]).view(-1)
+    mid = B * rows // 2
+    with sv.Verifier(B, rows, V) as v:
+        v.set_plan_override(cluster)
+        call = lambda: timed(lambda: v.distill(z, a, x, lens, tail=True, grad_loss=w))
+        call()
+        good = call()
+        assert v.error() == (0, 0)
+        assert sv.spec_losses_selftest(v.ctx, getattr(sv, "SV_SELFTEST_DISTILL_" + wait)) == 0
+        out = call()
+        assert v.error()[1] == 1 << TIMEOUT
+        assert sv.spec_losses_selftest(v.ctx, sv.SV_SELFTEST_OFF) == 0
+        again = call()
+        assert all(torch.equal(again[k], good[k]) for k in good) and v.error() == (0, 0)
+    loss, st, g = out["loss"].view(-1), out["status"].view(-1), out["grad_logits"].view(B * rows, V)
+    bad = st == TIMEOUT
+    lost = bad.nonzero()[:, 0].tolist()
+    # of the row itself an exchange's wait is lost in the last CTA alone
+    nan = torch.isnan(g).any(-1)
+    assert nan[mid] and (wait == "EXCHANGE" or lost[0] == mid) and lost[0] >= mid and len(lost) > 1
+    step = min(b - a for a, b in zip(lost, lost[1:]))
+    assert all((r - mid) % step == 0 for r in lost) and live[lost].all()
+    assert live[mid::step].sum() == len(lost) + (lost[0] != mid)
+    assert torch.isnan(loss[bad]).all() and torch.isnan(g[bad]).all()
+    rest = ~bad
+    rest[mid] = False
+    assert torch.equal(loss[rest], good["loss"].view(-1)[rest]) and (st[rest] == 0).all()
+    assert torch.equal(g[rest], good["grad_logits"].view(B * rows, V)[rest])
+
+
 def test_refusals():
     import speculative_decoding_verification_14_gb300 as sv
     assert sv.spec_losses_selftest(None, 0) == sv.SV_ERR_INVALID_ARG
