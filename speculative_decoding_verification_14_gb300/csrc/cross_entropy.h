@@ -12,7 +12,10 @@ constexpr int kHalf = kTile / 2;       // of one CTA's operands
 constexpr int kBlockK = 64;            // depth of a stage: 128 bytes, one swizzle atom
 constexpr int64_t kPieceBytes = (int64_t)1 << 28;  // draft of a piece's probabilities
 constexpr int kMaxSplits = 16;
-constexpr int64_t kMaxRowsCe = (int64_t)1 << 20;  // each block of rows counts those before it
+constexpr int64_t kMaxRowsCe = (int64_t)1 << 20;
+constexpr int64_t kCountRows = 1024;  // have a number of their own of those that count, in calls of more rows than
+constexpr int64_t kCountFrom = 8192;
+constexpr int64_t kCountFromLengths = 2048;  // where a look at a row divides by the rows of a sequence
 
 // rows of the box that A's copies have
 #ifdef __CUDACC__
@@ -28,6 +31,7 @@ struct CrossEntropyPlan {
     int64_t piece_tiles; // of one piece of the vocabulary
     int64_t pieces;
     int splits;          // of a piece's depth in the hidden states' gradient
+    size_t counts;                      // int32 of each kCountRows rows
     size_t index, label, lse, loss, scale;  // [rows]: source row, label, lse, loss, grad_loss
     size_t hidden;                      // bf16 [rows, depth]
     size_t stats, label_logit;          // float2 [vocab_tiles, rows], float [rows]

@@ -43,6 +43,7 @@ CrossEntropyPlan cross_entropy_plan(int num_sms, int64_t R, int64_t V, int64_t D
         at += (size_t)round_up(bytes, 256);
         return here;
     };
+    p.counts = R > kCountFromLengths ? take(ceil_div(R, kCountRows) * 4) : 0;
     p.index = take(p.rows * 4 + 8);  // and the number of rows that count, and whether a wait ran out
     p.label = take(p.rows * 4);
     p.hidden = take(p.rows * p.depth * 2);
