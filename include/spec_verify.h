@@ -523,8 +523,8 @@ int spec_distill_plan_for(int num_sms, int max_cluster, int B, int rows_per_seq,
  *
  *   hidden   R = B * rows_per_seq rows of D, row r at r * hidden_stride, in any
  *            alignment; row r belongs to sequence r / rows_per_seq
- *   weight   V rows of D, row v at v * weight_stride: 16-byte aligned, the stride a
- *            multiple of 8
+ *   weight   V rows of D, row v at v * weight_stride: 16-byte aligned, the stride of
+ *            more than one row a multiple of 8
  *   dtype    of hidden, weight and their gradients: SV_BF16 (SV_F32 returns
  *            SV_ERR_UNSUPPORTED); products are summed in float
  *   labels, accept_len  [B, rows] int32 and [B] or NULL (every row): a verify's

@@ -653,12 +653,15 @@ int check(const sv_ctx* ctx, const void* hidden, int dtype, int64_t hidden_strid
     if (dtype != SV_BF16)
         return SV_ERR_UNSUPPORTED;
     // the copy engine takes the weight's rows on 16 bytes
-    if (!aligned(hidden, 2) || !aligned(weight, 16) || weight_stride % 8 || !aligned(labels, 4) ||
+    if (!aligned(hidden, 2) || !aligned(weight, 16) || (V > 1 && weight_stride % 8) || !aligned(labels, 4) ||
         !aligned(accept_len, 4) || !aligned(workspace, 256))
         return SV_ERR_INVALID_ARG;
     *plan = cross_entropy_plan(ctx->num_sms, (int64_t)B * rows_per_seq, V, D, grad);
     return workspace_bytes < plan->total ? SV_ERR_INVALID_ARG : SV_OK;
 }
+
+// The stride the copy engine is given: a single row's is its length on 16 bytes, whatever the call's is.
+int64_t rows_apart(int64_t V, int64_t D, int64_t weight_stride) { return V > 1 ? weight_stride : round_up(D, 8); }
 
 Rows pack_args(const CrossEntropyPlan& plan, unsigned char* ws, const void* hidden, int64_t stride,
                const int32_t* labels, const int32_t* accept_len, int B, int rows_per_seq, int64_t V, int64_t D,
@@ -727,7 +730,7 @@ int spec_cross_entropy_run(sv_ctx* ctx, const void* hidden, int dtype, int64_t h
     Tiles p;
     std::memset(&p, 0, sizeof p);
     if (!tensor_map(&p.a, r.packed, plan.rows, D, plan.depth, box_rows(r.R)) ||
-        !tensor_map(&p.b, weight, V, D, weight_stride, kHalf))
+        !tensor_map(&p.b, weight, V, D, rows_apart(V, D, weight_stride), kHalf))
         return SV_ERR_CUDA;
     p.state = r.state;
     p.selftest = losses_selftest(ctx) == SV_SELFTEST_LOGITS ? 0 : -1;
@@ -817,17 +820,18 @@ int spec_cross_entropy_grad_of_loss(sv_ctx* ctx, const void* hidden, int dtype, 
     logits.splits = plan.splits;
     logits.out = static_cast<__nv_bfloat16*>(grad_weight);
     logits.out_stride = grad_weight_stride;
-    // the copy engine writes whole 16 bytes: beyond D too, where that ends inside some
-    logits.out_vectors = aligned(grad_weight, 16) && grad_weight_stride % 8 == 0 && D % 8 == 0;
+    // the copy engine writes whole 16 bytes: beyond D too, where that ends inside some; and its strides end at 2^40 bytes
+    logits.out_vectors = aligned(grad_weight, 16) && grad_weight_stride % 8 == 0 && D % 8 == 0 &&
+                         grad_weight_stride < ((int64_t)1 << 39);
     hid = wgt = logits;
     const int selftest = losses_selftest(ctx);
     logits.selftest = selftest == SV_SELFTEST_PROBS ? 0 : -1;
     hid.selftest = selftest == SV_SELFTEST_HIDDEN ? 0 : -1;
     wgt.selftest = selftest == SV_SELFTEST_WEIGHT ? 0 : -1;
     if (!tensor_map(&logits.a, r.packed, plan.rows, D, plan.depth, box_rows(R)) ||
-        !tensor_map(&logits.b, weight, V, D, weight_stride, kHalf) ||
+        !tensor_map(&logits.b, weight, V, D, rows_apart(V, D, weight_stride), kHalf) ||
         !tensor_map(&hid.a, probs, plan.rows, width, width, box_rows(R)) ||
-        !tensor_map(&hid.b, weight, V, D, weight_stride, kBlockK) ||
+        !tensor_map(&hid.b, weight, V, D, rows_apart(V, D, weight_stride), kBlockK) ||
         !tensor_map(&wgt.a, probs, plan.rows, width, width, kBlockK) ||
         !tensor_map(&wgt.b, r.packed, plan.rows, D, plan.depth, kBlockK) ||
         !tensor_map(&logits.c, probs, plan.rows, width, width, 32) ||
