@@ -1016,7 +1016,8 @@ class Verifier:
         list leaves as one more outcome (tail).  Rows from accept_len[b] on are not read (None:
         every row).  grad_loss [B, rows] float32: the objective's derivative by each row's loss
         (None: 1).  Returns loss and, for grad, grad_logits in the logits' type, and optionally
-        status; ``out={"grad_logits": logits, ...}`` writes in place.  A gradient asked for
+        status; ``out={"grad_logits": logits, ...}`` writes in place.  With ``out``, what it
+        holds says what is written, and loss, grad and status say nothing.  A gradient asked for
         later, once grad_loss is known, is a second call with loss=False."""
         import torch
         B, rows, V, code, stride = self._rows_of(logits)
@@ -1119,7 +1120,8 @@ class Verifier:
         losses, given its lse: grad_hidden and grad_weight in bfloat16, each only if it is asked for
         (a head that is not trained costs neither its product nor its bytes).  loss: what ``cross_entropy``
         returned as such, for rows that the head gets right but for 1e-4 of the mass and less: an lse alone
-        holds the label's share to some 1e-6 of the whole."""
+        holds the label's share to some 1e-6 of the whole.  With ``out``, what it holds says what is
+        written, and hidden_grad, weight_grad and status say nothing."""
         import torch
         head, (B, rows, V, D), shape, ws = self._head_of(hidden, weight, labels, accept_len,
                                                          workspace, True, stream)
