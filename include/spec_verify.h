@@ -494,6 +494,9 @@ int spec_logprobs_plan_for(int num_sms, int max_cluster, int B, int rows_per_seq
  * error word.  Where a wait inside the kernel runs out, so do the rows that its
  * cluster has left, with SV_ERR_TIMEOUT (of the row itself, where it is the wait for
  * what other CTAs have found, perhaps only the waiting CTA's part of the gradient).
+ * A loss is good to 2^-26 or 2^-21 of itself, whichever is more; an entry of a float
+ * gradient to some 2^-20 of the larger of its two terms (q_v's and the teacher's), not
+ * of their difference: it keeps fewer digits the nearer the draft is to its teacher.
  * Repeated calls give the same bits.  Asynchronous, no allocation, one launch on
  * `stream`; safe to capture.  Rows that 16 CTAs' shared memory holds (V up to
  * 884733 float, 1769465 bfloat16) are taken: SV_ERR_UNSUPPORTED beyond.  Otherwise
@@ -547,7 +550,8 @@ int spec_distill_plan_for(int num_sms, int max_cluster, int B, int rows_per_seq,
  * what half a unit in lse's last place is: 5e-7 g at an lse of 8 to 16, 2e-6 at 32 to
  * 64, which is much of d_y where the row's loss is of that size.
  * Each d_v is rounded to bfloat16 before the products that sum it, and each
- * gradient once after.  A row's work is not done where it does not count.
+ * gradient once after.  A logit is a float32 sum that the tensor cores cut: loss and
+ * lse are off by some 6e-10 D of a logit's size.  A row's work is not done where it does not count.
  * 1 <= D <= 2^20, R <= 2^20.  No output may lie where an input or another output
  * does (rows of a gradient that meet those of its input are refused).
  * An erroneous row (a label outside [-1, V): SV_ERR_TOKEN_RANGE; logits with a

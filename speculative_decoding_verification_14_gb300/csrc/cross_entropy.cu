@@ -2,27 +2,29 @@
 // without keeping the logits, and its gradients.
 //
 //   loss = lse - z_y,  lse = ln sum_v exp z_v
-//   d_v = g (exp(z_v - lse) - [v = y]),  grad_h = sum_v d_v W_v,  grad_W_v = sum over rows of d_v h
+//   d_v = g (exp(z_v - lse) - [v = y]), of the label g (exp(-loss) - 1) where the losses are given,  grad_h = sum_v d_v W_v,  grad_W_v = sum over rows of d_v h
 //
 // Rows that count are packed first (those below accept_len with a label), so that the products' work is
 // theirs alone and nothing that a padded row holds reaches the head's gradient.
 // Loss: one product whose tiles leave (maximum, sum) of each row's 256 logits without the label's, and a join of those
 // with it: small losses keep their digits (1e-5 relative beside what the logits are off; 0.8 us of a loss of 5 rows).
-// Gradients: piece by piece of the vocabulary, the logits once more, now written as bfloat16 d
-// (a piece's d stays within 256 MB); then d W into float32 sums of the hidden states' gradient, and
+// Gradients: piece by piece of the vocabulary, the logits once more, now written as bfloat16 d (how much a piece is:
+// kPieceBytes); then d W into float32 sums of the hidden states' gradient, and
 // d^T h, which is that piece's rows of the head's gradient.  d is rounded to bfloat16 (2^-8 of itself at most) since the
-// tensor cores take it so; its errors are independent from entry to entry, and both gradients sum many (against 64 bits
-// they are off by 2.2e-3 to 3.0e-3 of their norm, 1.7e-3 of which is their own rounding).  A logit's sum is a float in
-// tensor memory, which the tensor cores cut and do not round: at D of 4096 lse is off by 2.0e-6 of itself, at 100 by 1e-7.
+// tensor cores take it so: the rest of d as a second operand would be two more products beside four.  Its errors are
+// independent from entry to entry, but a row's label may be most of its gradient (against 64 bits both are off by 2.2e-3
+// to 2.6e-3 of their norm, 1.7e-3 of which is their own rounding).  A logit's sum is a float in tensor memory, which
+// the tensor cores cut and do not round, the same way in every row: at D of 4096 loss and lse are off by 2.3e-6 of
+// themselves, at 1024 by 6e-7, at 100 by 1e-7.
 // The launches of a call begin while the ones before them end.
 //
-// What bounds it (replayed): from some 300 rows on the tensor cores.  8192 rows of 128256 x 4096, loss and both gradients,
-// 20.7 to 21.5 ms: its products, 4 of 8.6 TFLOP, one of them the logits' second, take 95 % of the rate that a library
-// product reaches in a burst, and what the clock leaves of that under the power limit; 2048 rows, the loss, 1.22 ms (0.92).
-// 256 rows of 151936 x 2048, the hidden states' gradient, 360 us: three products of 83 us at that rate, each 8 rounds of 76
-// pairs and 10 us of beginning and end.  Few rows read the weight at 5.2 TB/s once it flows: 5 rows of 32000 x 1024, the
-// loss, 21 us (10 for 65 MB): 4 until the rows are packed, 4 until the first tile is there, 12 for the weight, 3 for
-// the last tile's statistics.  40 rows, both gradients, 93 us: four such passes, over the weight or its gradient.
+// What bounds it (replayed): with many rows the tensor cores.  8192 rows of 128256 x 4096, loss and both gradients,
+// 20.3 to 21.5 ms: its products, 4 of 8.6 TFLOP, one of them the logits' second, take 95 % of the rate that a library
+// product reaches in a burst, and what the clock leaves of that under the power limit; 2048 rows, the loss, 1.25 ms (0.90).
+// 256 rows of 151936 x 2048, the hidden states' gradient, 368 us: three products, each over all of the weight, whose 622 MB
+// no L2 holds from one to the next: 3 x 92 us at a copy's rate, where the products are 3 x 83.  Few rows read the weight at 5.2 TB/s once it flows: 5 rows of 32000 x 1024, the
+// loss, 22.5 us (10 for 65 MB): 4 until the rows are packed, 4 until the first tile is there, 12 for the weight, 3 for
+// the last tile's statistics.  40 rows, both gradients, 96 us: four such passes, over the weight or its gradient.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

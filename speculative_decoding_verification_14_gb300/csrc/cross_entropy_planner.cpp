@@ -24,7 +24,7 @@ CrossEntropyPlan cross_entropy_plan(int num_sms, int64_t R, int64_t V, int64_t D
     p.rows = round_up(R, kTile);
     p.depth = round_up(D, 8);
     p.vocab_tiles = ceil_div(V, kTile);
-    // the largest pieces whose probabilities stay within kPieceBytes, all of nearly the same size
+    // the largest pieces whose probabilities stay within kPieceBytes, or of one tile, all of nearly the same size
     const int64_t fit = kPieceBytes / (p.rows * kTile * 2);
     p.pieces = ceil_div(p.vocab_tiles, fit < 1 ? 1 : fit);
     p.piece_tiles = ceil_div(p.vocab_tiles, p.pieces);

@@ -26,8 +26,8 @@
 // most of one another's, and no pipe is above 30 %.  Tried: rows one by one, a cluster each, 279 and 485 us; four CTAs
 // an SM with smaller slices 259 and 462, two with larger ones 234 and 410; 256 or 320 walkers an SM at fewer
 // registers 246 and 261.
-// Three CTAs of 288 threads leave 72 registers a thread; the scribe, who alone keeps two rows' lists, spills some 130
-// bytes of them (204 read back), once a row of the first CTA.
+// Three CTAs of 288 threads leave 72 registers a thread, which is less than the scribe needs, who alone keeps two rows'
+// lists: the compiler reports 130 bytes of spills, 206 read back.
 //
 // A wait that runs out (2 s for other CTAs, 10 s for a copy) ends the cluster's work: the CTA that gave up says so with
 // its next sums, no CTA that hears of it waits or copies any more, and the rows left get NaN and SV_ERR_TIMEOUT.
