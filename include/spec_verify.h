@@ -494,9 +494,10 @@ int spec_logprobs_plan_for(int num_sms, int max_cluster, int B, int rows_per_seq
  * error word.  Where a wait inside the kernel runs out, so do the rows that its
  * cluster has left, with SV_ERR_TIMEOUT (of the row itself, where it is the wait for
  * what other CTAs have found, perhaps only the waiting CTA's part of the gradient).
- * A loss is good to 2^-26 or 2^-21 of itself, whichever is more; an entry of a float
- * gradient to some 2^-20 of the larger of its two terms (q_v's and the teacher's), not
- * of their difference: it keeps fewer digits the nearer the draft is to its teacher.
+ * A loss is good to 2^-26, 2^-21 of itself or 2^-21 of its square root, whichever is
+ * most; an entry of a float gradient to some 2^-20 of the larger of its two terms
+ * (q_v's and the teacher's), not of their difference: it keeps fewer digits the nearer
+ * the draft is to its teacher.
  * Repeated calls give the same bits.  Asynchronous, no allocation, one launch on
  * `stream`; safe to capture.  Rows that 16 CTAs' shared memory holds (V up to
  * 884733 float, 1769465 bfloat16) are taken: SV_ERR_UNSUPPORTED beyond.  Otherwise

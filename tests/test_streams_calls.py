@@ -88,3 +88,41 @@ def test_outputs_lie_in_the_streams_memory(name):
         owner = [g["stream"] for g in segments if g["address"] <= t.data_ptr() < g["address"] + g["total_size"]]
         assert owner == [s.cuda_stream], k
         assert k not in whole or torch.equal(t, want[k]) and torch.equal(default[k], want[k]), k
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("named", [False, True])
+@pytest.mark.parametrize("B,rows,lengths", [(6, 3, False), (9001, 1, False), (700, 4, True)])
+def test_captured_with_losses_and_without_a_workspace(B, rows, lengths, named):
+    """A training step of loss, gradients given the losses, and no memory of the caller's, captured on a stream that the
+    calls are told of or find current; replayed on other data, with the answers of calls on the default stream."""
+    import torch
+    from tests import gpu_helpers as gh
+    v = gh.verifier()
+    V, D = 300, 24
+
+    def data(seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        W = torch.randn(V, D, device="cuda", generator=g).bfloat16()
+        y = torch.randint(-1, V, (B, rows), device="cuda", generator=g, dtype=torch.int32)
+        h = (torch.randn(B, rows, D, device="cuda", generator=g) + 0.5 * W[y.clamp(min=0).long()].float()).bfloat16()
+        return [h, W, y, torch.randint(0, rows + 1, (B,), device="cuda", generator=g, dtype=torch.int32),
+                torch.rand(B, rows, device="cuda", generator=g)]
+
+    def step(x, **kw):
+        h, W, y, lens, w = x
+        lens = lens if lengths else None
+        out = v.cross_entropy(h, W, y, lens, **kw)
+        return {**out, **v.cross_entropy_grad(h, W, y, out["lse"], lens, grad_loss=w, loss=out["loss"], **kw)}
+    x = data(1)
+    torch.cuda.synchronize()
+    s, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        got = step(x, **({"stream": s.cuda_stream} if named else {}))
+    for seed in (2, 3):
+        for t, f in zip(x, data(seed)):
+            t.copy_(f)
+        graph.replay()
+        want = step(x)
+        torch.cuda.synchronize()
+        assert all(torch.equal(got[k], want[k]) for k in want) and (want["status"] == 0).all()
