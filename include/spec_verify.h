@@ -551,8 +551,9 @@ int spec_distill_plan_for(int num_sms, int max_cluster, int B, int rows_per_seq,
  * what half a unit in lse's last place is: 5e-7 g at an lse of 8 to 16, 2e-6 at 32 to
  * 64, which is much of d_y where the row's loss is of that size.
  * Each d_v is rounded to bfloat16 before the products that sum it, and each
- * gradient once after.  A logit is a float32 sum that the tensor cores cut: loss and
- * lse are off by some 6e-10 D of a logit's size.  A row's work is not done where it does not count.
+ * gradient once after.  A logit is a float32 sum that the tensor cores cut towards 0,
+ * short of itself by some 1e-9 D where products of either sign make it up, and by up to
+ * 4e-9 D where all have one sign (1.4e-5 at a D of 4096); loss and lse are as far off.  A row's work is not done where it does not count.
  * 1 <= D <= 2^20, R <= 2^20.  No output may lie where an input or another output
  * does (rows of a gradient that meet those of its input are refused).
  * An erroneous row (a label outside [-1, V): SV_ERR_TOKEN_RANGE; logits with a
